@@ -238,6 +238,43 @@ int kpool_expand(const int32_t *pool_ids, const int32_t *cu_seqlens_host,
 int kpool_topk(const float *scores, int64_t ld, const int32_t *n_valid, int64_t rows,
                int32_t budget, int32_t *pool_ids, void *stream);
 
+/* Layer norm of rows - the indexer's keys pass one with weight and bias before they are
+ * pooled (Atlas inference docs, glm5next_dsa/tp.rs: the indexer's k_norm among the shard
+ * plan's tensors).  For row r and column j < N:
+ *   mean = sum_j x[r,j] / N,   rstd = 1 / sqrt(sum_j (x[r,j] - mean)^2 / N + eps)
+ *   y[r,j] = (x[r,j] - mean) * rstd * weight[j] + bias[j]
+ * in fp32, rounded once to the output's type.
+ *   dtype    of x, y, dy and dx: KPOOL_DTYPE_BF16 or KPOOL_DTYPE_F32
+ *   x        [rows, N], row r at x + r * x_stride elements (x_stride >= N): a slice of a
+ *            wider projection needs no copy
+ *   weight   fp32 [N], NULL for ones;  bias fp32 [N], NULL for zeros
+ *   eps      finite, >= 0 (a constant row with eps = 0 gives the formula's NaN)
+ *   y        [rows, N] contiguous, not overlapping x
+ *   mean, rstd  NULLABLE fp32 [rows]: what the backward pass reads
+ * rows 0 is a no-op; N >= 1.  Any alignment of whole elements is taken; 16-byte aligned
+ * rows (pointers, x_stride and N) are read and written in 16-byte pieces. */
+#define KPOOL_DTYPE_BF16 0
+#define KPOOL_DTYPE_F32 1
+int kpool_layer_norm(const void *x, int64_t x_stride, const float *weight, const float *bias,
+                     int64_t rows, int32_t N, float eps, int32_t dtype, void *y, float *mean,
+                     float *rstd, void *stream);
+
+/* Its backward pass.  With xh = (x - mean) * rstd and g = dy * weight:
+ *   dx[r,j] = rstd * (g - sum_j(g) / N - xh * sum_j(g * xh) / N)
+ *   dweight[j] = sum_r dy * xh,   dbias[j] = sum_r dy            (fp32 sums)
+ *   dy       [rows, N] contiguous;  x, x_stride, weight as in the forward call
+ *   mean, rstd  fp32 [rows] from it
+ *   dx       NULLABLE [rows, N];  dweight, dbias  NULLABLE fp32 [N], overwritten
+ *   workspace  kpool_layer_norm_backward_workspace_bytes(rows, N) bytes where dweight or
+ *            dbias is given (NULL and 0 otherwise), 16-byte aligned; scratch on return
+ * The sums over rows run in a fixed order: the same inputs give the same bits.  rows 0
+ * writes zeros to dweight and dbias. */
+size_t kpool_layer_norm_backward_workspace_bytes(int64_t rows, int32_t N);
+int kpool_layer_norm_backward(const void *dy, const void *x, int64_t x_stride, const float *weight,
+                              const float *mean, const float *rstd, int64_t rows, int32_t N,
+                              int32_t dtype, void *workspace, size_t workspace_bytes, void *dx,
+                              float *dweight, float *dbias, void *stream);
+
 /* Optional per-kernel device timing, per host thread.  While enabled on a
  * thread, every launch that thread's calls make is bracketed by HIP events on
  * its stream.  kpool_profile_collect waits for the events the calling thread
@@ -246,7 +283,8 @@ int kpool_topk(const float *scores, int64_t ld, const int32_t *n_valid, int64_t 
  * Other threads' records and switches are untouched.  Event spans of
  * overlapped chunks (KPOOL_FLAG_OVERLAP) include whatever else the GPU runs
  * meanwhile; time kernels with flags = 0. */
-#define KPOOL_PROFILE_KINDS 5 /* 0 pool_keys, 1 score, 2 topk, 3 expand, 4 scores_out copy */
+#define KPOOL_PROFILE_KINDS 7 /* 0 pool_keys, 1 score, 2 topk, 3 expand, 4 scores_out copy,
+                                 5 layer norm, 6 attention (a call's launches as one) */
 int kpool_profile_enable(int on);
 int kpool_profile_collect(double *ms, int64_t *launches);
 

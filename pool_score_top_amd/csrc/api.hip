@@ -63,6 +63,15 @@ int check_cu(const int32_t *cu, int32_t nseq, const char *fn) {
   return KPOOL_OK;
 }
 
+int check_norm(const char *fn, int64_t rows, int32_t N, int64_t x_stride, int32_t dtype) {
+  if (dtype != KPOOL_DTYPE_BF16 && dtype != KPOOL_DTYPE_F32)
+    return fail(KPOOL_EINVAL, "%s: unknown dtype %d", fn, dtype);
+  if (rows < 0) return fail(KPOOL_EINVAL, "%s: rows must be >= 0", fn);
+  if (N < 1 || N > (1 << 30)) return fail(KPOOL_EINVAL, "%s: N must be in [1, 2^30] (got %d)", fn, N);
+  if (x_stride < N) return fail(KPOOL_EINVAL, "%s: x_stride must be >= N", fn);
+  return KPOOL_OK;
+}
+
 // ---------------------------------------------------------------------------
 // Optional per-kernel timing with HIP events on the launch stream.  The switch
 // and the records are per host thread, so one thread's profiling never sees or
@@ -562,6 +571,64 @@ int kpool_topk(const float *scores, int64_t ld, const int32_t *n_valid, int64_t 
   hipError_t e = timed(2, st, [&] {
     return kpool::launch_topk(scores, ld, rows, n_valid, nullptr, 0, 0, 1, false, budget, pool_ids,
                               nullptr, 0, st);
+  });
+  if (e != hipSuccess) return hip_fail(fn, e);
+  return ok();
+}
+
+int kpool_layer_norm(const void *x, int64_t x_stride, const float *weight, const float *bias,
+                     int64_t rows, int32_t N, float eps, int32_t dtype, void *y, float *mean,
+                     float *rstd, void *stream) {
+  const char *fn = "kpool_layer_norm";
+  int rc = check_norm(fn, rows, N, x_stride, dtype);
+  if (rc) return rc;
+  if (!(eps >= 0.0f) || !isfinite(eps)) return fail(KPOOL_EINVAL, "%s: eps must be finite and >= 0", fn);
+  if (rows == 0) return ok();
+  if (!x || !y) return fail(KPOOL_EINVAL, "%s: null pointer", fn);
+  const uintptr_t mask = dtype == KPOOL_DTYPE_F32 ? 3 : 1;
+  if ((((uintptr_t)x | (uintptr_t)y) & mask) ||
+      (((uintptr_t)weight | (uintptr_t)bias | (uintptr_t)mean | (uintptr_t)rstd) & 3))
+    return fail(KPOOL_EINVAL, "%s: a pointer is not aligned to its elements", fn);
+  hipStream_t st = (hipStream_t)stream;
+  hipError_t e = timed(5, st, [&] {
+    return kpool::launch_norm(dtype == KPOOL_DTYPE_F32, x, x_stride, weight, bias, rows, N, eps, y, mean,
+                              rstd, st);
+  });
+  if (e != hipSuccess) return hip_fail(fn, e);
+  return ok();
+}
+
+size_t kpool_layer_norm_backward_workspace_bytes(int64_t rows, int32_t N) {
+  if (rows < 0 || N < 1) return 0;
+  return (size_t)kpool::norm_bwd_blocks(std::max<int64_t>(rows, 1), N) * 2 * (size_t)N * sizeof(float);
+}
+
+int kpool_layer_norm_backward(const void *dy, const void *x, int64_t x_stride, const float *weight,
+                              const float *mean, const float *rstd, int64_t rows, int32_t N,
+                              int32_t dtype, void *workspace, size_t workspace_bytes, void *dx,
+                              float *dweight, float *dbias, void *stream) {
+  const char *fn = "kpool_layer_norm_backward";
+  int rc = check_norm(fn, rows, N, x_stride, dtype);
+  if (rc) return rc;
+  const bool sums = dweight || dbias;
+  if (!dx && !sums) return fail(KPOOL_EINVAL, "%s: no output given", fn);
+  if (rows == 0 && !sums) return ok();
+  if (rows > 0 && (!dy || !x || !mean || !rstd)) return fail(KPOOL_EINVAL, "%s: null pointer", fn);
+  const uintptr_t mask = dtype == KPOOL_DTYPE_F32 ? 3 : 1;
+  if ((((uintptr_t)x | (uintptr_t)dy | (uintptr_t)dx) & mask) ||
+      (((uintptr_t)weight | (uintptr_t)mean | (uintptr_t)rstd | (uintptr_t)dweight | (uintptr_t)dbias) & 3))
+    return fail(KPOOL_EINVAL, "%s: a pointer is not aligned to its elements", fn);
+  if (sums) {
+    const size_t need = kpool_layer_norm_backward_workspace_bytes(rows, N);
+    if (!workspace || workspace_bytes < need)
+      return fail(KPOOL_EWORKSPACE, "%s: needs %zu bytes of workspace, got %zu", fn, need,
+                  workspace ? workspace_bytes : (size_t)0);
+    if (!aligned16(workspace)) return fail(KPOOL_EINVAL, "%s: workspace must be 16-byte aligned", fn);
+  }
+  hipStream_t st = (hipStream_t)stream;
+  hipError_t e = timed(5, st, [&] {
+    return kpool::launch_norm_bwd(dtype == KPOOL_DTYPE_F32, dy, x, x_stride, weight, mean, rstd, rows, N,
+                                  dx, dweight, dbias, (float *)workspace, st);
   });
   if (e != hipSuccess) return hip_fail(fn, e);
   return ok();

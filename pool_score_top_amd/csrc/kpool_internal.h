@@ -74,6 +74,17 @@ hipError_t launch_expand(const int32_t *pool_ids, const int32_t *cu_seqlens, int
                          int32_t kpool, bool tail, int64_t q_lo, int64_t nrows, int32_t budget,
                          int32_t *token_ids, hipStream_t stream);
 
+// Layer norm of rows (norm.hip); f32: x, y, dy and dx are fp32, else bf16 bits.  Null
+// pointers among w, b, mean, rstd (forward), dx, dw, db stand for what is not there or not
+// wanted.  part: norm_bwd_blocks(rows, N) * 2 * N floats where dw or db is wanted.
+hipError_t launch_norm(bool f32, const void *x, int64_t x_stride, const float *w, const float *b,
+                       int64_t rows, int32_t N, float eps, void *y, float *mean, float *rstd,
+                       hipStream_t stream);
+int norm_bwd_blocks(int64_t rows, int32_t N);
+hipError_t launch_norm_bwd(bool f32, const void *dy, const void *x, int64_t x_stride, const float *w,
+                           const float *mean, const float *rstd, int64_t rows, int32_t N, void *dx,
+                           float *dw, float *db, float *part, hipStream_t stream);
+
 // ----------------------------------------------------------------------------
 // Device helpers
 // ----------------------------------------------------------------------------
@@ -84,6 +95,14 @@ hipError_t launch_expand(const int32_t *pool_ids, const int32_t *cu_seqlens, int
 __device__ inline int64_t visible_count(int64_t t, int64_t L, int kpool, bool tail) {
   const int64_t n = t / kpool + 1;
   return tail ? min(n, L / kpool) : n;
+}
+
+// Two fp32 values rounded to bf16 (to nearest, ties to even) as one word, lo in the low half.
+__device__ inline uint32_t pack_bf16(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const f32x2 f = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2));
 }
 
 // Index of the sequence holding global row `row`: the largest s < nseq with

@@ -19,7 +19,8 @@ LIB_PATH = os.path.join(HERE, "libkpool.so")
 KPOOL_OK, KPOOL_EINVAL, KPOOL_EUNSUPPORTED, KPOOL_EWORKSPACE, KPOOL_EHIP = 0, -1, -2, -3, -4
 KPOOL_FLAG_OVERLAP = 1
 KPOOL_FLAG_TAIL = 2
-PROFILE_KINDS = ("pool_keys", "score", "topk", "expand", "scores_copy")
+PROFILE_KINDS = ("pool_keys", "score", "topk", "expand", "scores_copy", "norm", "attend")
+KPOOL_DTYPE_BF16, KPOOL_DTYPE_F32 = 0, 1
 
 _lib = None
 
@@ -54,6 +55,10 @@ def lib():
                                                     i64, i64, i32, u32, vp, vp, vp]),
         "kpool_expand": (ctypes.c_int, [vp, vp, vp, i32, i32, i64, i64, i32, u32, vp, vp]),
         "kpool_topk": (ctypes.c_int, [vp, i64, vp, i64, i32, vp, vp]),
+        "kpool_layer_norm": (ctypes.c_int, [vp, i64, vp, vp, i64, i32, f32, i32, vp, vp, vp, vp]),
+        "kpool_layer_norm_backward_workspace_bytes": (sz, [i64, i32]),
+        "kpool_layer_norm_backward": (ctypes.c_int, [vp, vp, i64, vp, vp, vp, i64, i32, i32, vp, sz,
+                                                     vp, vp, vp, vp]),
         "kpool_profile_enable": (ctypes.c_int, [ctypes.c_int]),
         "kpool_profile_collect": (ctypes.c_int, [vp, vp]),
     }
@@ -277,14 +282,119 @@ def topk(scores, n_valid, budget: int, out=None, stream=None):
     return out
 
 
+def _on_device(t, stream):
+    """The stream for a call on t's device (the device's current one by default), with that
+    device made current for the launches: a context manager giving the stream's handle."""
+    import contextlib
+
+    import torch
+
+    @contextlib.contextmanager
+    def ctx():
+        with torch.cuda.device(t.device):
+            s = torch.cuda.current_stream() if stream is None else stream
+            if s.device != t.device:
+                raise ValueError(f"the stream is on {s.device}, the tensors on {t.device}")
+            with torch.cuda.stream(s):  # outputs and workspaces belong to the call's stream
+                yield ctypes.c_void_p(s.cuda_stream)
+    return ctx()
+
+
+def _like(t, name, shape, dtype, device):
+    """An output or parameter given by the caller: contiguous, of this shape, type and device."""
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}")
+
+
+def _norm_rows(x, name):
+    """x as rows: (rows, N, row stride, dtype code)."""
+    import torch
+    codes = {torch.bfloat16: KPOOL_DTYPE_BF16, torch.int16: KPOOL_DTYPE_BF16,
+             torch.float32: KPOOL_DTYPE_F32}
+    if not x.is_cuda or x.dim() != 2:
+        raise ValueError(f"{name} must be a device tensor of rows [rows, N]")
+    if x.dtype not in codes:
+        raise ValueError(f"{name} must be bfloat16 (or int16 bit patterns) or float32")
+    rows, N = x.shape
+    if N < 1 or (N > 1 and x.stride(1) != 1) or (rows > 1 and x.stride(0) < N):
+        raise ValueError(f"{name} must hold contiguous rows that do not overlap")
+    return rows, N, x.stride(0) if rows > 1 else N, codes[x.dtype]
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, want_stats: bool = False,
+               stream=None):
+    """Layer norm of the rows of x [rows, N] (bf16 or fp32, any row stride), with fp32 weight
+    and bias [N] (None: ones, zeros).  Returns (y, mean, rstd); mean and rstd, fp32 [rows],
+    are what layer_norm_backward reads, and None unless want_stats."""
+    import torch
+    rows, N, stride, code = _norm_rows(x, "x")
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _like(t, name, (N,), torch.float32, x.device)
+    if out is not None:
+        _like(out, "out", (rows, N), x.dtype, x.device)
+    with _on_device(x, stream) as s:
+        if out is None:
+            out = torch.empty((rows, N), dtype=x.dtype, device=x.device)
+        mean = rstd = None
+        if want_stats:
+            mean, rstd = (torch.empty(rows, dtype=torch.float32, device=x.device) for _ in range(2))
+        rc = lib().kpool_layer_norm(_p(x), stride, _p(weight), _p(bias), rows, N, ctypes.c_float(eps),
+                                    code, _p(out), _p(mean), _p(rstd), s)
+    _check(rc, "kpool_layer_norm")
+    return out, mean, rstd
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, want_dx: bool = True, want_dweight: bool = True,
+                        want_dbias: bool = True, workspace=None, stream=None):
+    """Gradients of layer_norm: (dx, dweight, dbias), each None where it is not wanted.  dy is
+    like y; x, weight as in the forward call; mean, rstd from it.  A workspace of
+    layer_norm_backward_workspace_bytes(rows, N) bytes may be passed in."""
+    import torch
+    rows, N, stride, code = _norm_rows(x, "x")
+    _like(dy, "dy", (rows, N), x.dtype, x.device)
+    if weight is not None:
+        _like(weight, "weight", (N,), torch.float32, x.device)
+    _like(mean, "mean", (rows,), torch.float32, x.device)
+    _like(rstd, "rstd", (rows,), torch.float32, x.device)
+    if not (want_dx or want_dweight or want_dbias):
+        raise ValueError("no output is wanted")
+    with _on_device(x, stream) as s:
+        f32 = dict(dtype=torch.float32, device=x.device)
+        dx = torch.empty((rows, N), dtype=x.dtype, device=x.device) if want_dx else None
+        dw = torch.empty(N, **f32) if want_dweight else None
+        db = torch.empty(N, **f32) if want_dbias else None
+        if workspace is None and (want_dweight or want_dbias):
+            workspace = torch.empty(layer_norm_backward_workspace_bytes(rows, N), dtype=torch.uint8,
+                                    device=x.device)
+        rc = lib().kpool_layer_norm_backward(_p(dy), _p(x), stride, _p(weight), _p(mean), _p(rstd), rows,
+                                             N, code, _p(workspace), _bytes(workspace, x.device), _p(dx),
+                                             _p(dw), _p(db), s)
+    _check(rc, "kpool_layer_norm_backward")
+    return dx, dw, db
+
+
+def layer_norm_backward_workspace_bytes(rows: int, N: int) -> int:
+    return int(lib().kpool_layer_norm_backward_workspace_bytes(rows, N))
+
+
+def _bytes(workspace, device):
+    """Size of a caller's workspace (0 for none)."""
+    if workspace is None:
+        return 0
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace.numel() * workspace.element_size()
+
+
 def profile_enable(on: bool = True):
     _check(lib().kpool_profile_enable(1 if on else 0), "kpool_profile_enable")
 
 
 def profile_collect():
     """{kind: (ms, launches)} accumulated since the last collect."""
-    ms = (ctypes.c_double * 5)()
-    n = (ctypes.c_int64 * 5)()
+    ms = (ctypes.c_double * len(PROFILE_KINDS))()
+    n = (ctypes.c_int64 * len(PROFILE_KINDS))()
     _check(lib().kpool_profile_collect(ms, n), "kpool_profile_collect")
     return {k: (ms[i], int(n[i])) for i, k in enumerate(PROFILE_KINDS)}
 

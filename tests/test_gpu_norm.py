@@ -1,0 +1,272 @@
+"""Layer norm, forward and backward, against the formulas in 64 bits.
+
+Tolerances (u = 2^-24 is fp32's half step, h the half step of the output's type): a sum of
+n terms in fp32, in any order that adds at most `depth` values one after the other, is off
+by at most depth * u * sum|terms|.  A thread adds its columns in turn and the lanes join in
+a tree, so depth <= N / 16 + 16 covers every layout of the kernels for rows, and the row
+sums of the weight's gradient add rows of one workgroup, then the workgroups' sums.
+  mean     depth u max|x|                                                  (and u |mean|)
+  xh       the mean's error times rstd, and rstd's relative (depth + 8) u
+  y        xh's error times |w|, 3 roundings, and h |y| for the output's type
+  dx       depth u on each of the two means, a few roundings, and h |dx|
+A constant of 2 on the fp32 part covers the products of these errors.
+"""
+import numpy as np
+import pytest
+import torch
+
+from pool_score_top_amd import kpool as K
+
+U = 2.0 ** -24
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+
+
+def forward64(x, w, b, eps):
+    mean = x.mean(1, keepdim=True)
+    xc = x - mean
+    rstd = 1.0 / ((xc * xc).mean(1, keepdim=True) + eps).sqrt()
+    return xc * rstd * w + b, mean, rstd
+
+
+def inputs(rows, N, dtype, seed, pad=0, offset=0.0):
+    g = torch.Generator().manual_seed(seed)
+    wide = (torch.randn(rows, N + pad, generator=g) + offset).to(dtype).cuda()
+    x = wide[:, :N]
+    w = (1.0 + 0.3 * torch.randn(N, generator=g)).cuda()
+    b = torch.randn(N, generator=g).cuda()
+    dy = torch.randn(rows, N, generator=g).to(dtype).cuda()
+    return x, w, b, dy
+
+
+def check_forward(x, w, b, eps, y, mean, rstd):
+    rows, N = x.shape
+    x64 = x.double()
+    w64 = torch.ones(N, dtype=torch.float64, device="cuda") if w is None else w.double()
+    b64 = torch.zeros(N, dtype=torch.float64, device="cuda") if b is None else b.double()
+    y64, m64, r64 = forward64(x64, w64, b64, eps)
+    depth = N / 16 + 16
+    top = x64.abs().amax(1, keepdim=True)
+    xh = (x64 - m64) * r64
+    tol32 = 2 * U * ((depth + 16) * (w64.abs() * (top * r64 + xh.abs())) + 3 * b64.abs())
+    tol = HALF[x.dtype] * (y64.abs() + tol32) + tol32
+    assert ((y.double() - y64).abs() <= tol).all()
+    if mean is not None:
+        assert ((mean.double() - m64[:, 0]).abs() <= 2 * (depth + 2) * U * top[:, 0]).all()
+        # the shift of the mean enters the variance squared, relative to it (top rstd depth u)^2
+        rel = 2 * ((depth + 8) * U + (depth * U * top * r64) ** 2)[:, 0]
+        assert ((rstd.double() - r64[:, 0]).abs() <= rel * r64[:, 0]).all()
+
+
+def check_backward(x, w, dy, mean, rstd, dx, dw, db):
+    """Against the formulas with the kernel's own mean and rstd as inputs."""
+    rows, N = x.shape
+    x64, g0 = x.double(), dy.double()
+    w64 = torch.ones(N, dtype=torch.float64, device="cuda") if w is None else w.double()
+    mu, rs = mean.double()[:, None], rstd.double()[:, None]
+    xh = (x64 - mu) * rs
+    g = g0 * w64
+    c1, c2 = (g * xh).mean(1, keepdim=True), g.mean(1, keepdim=True)
+    d64 = rs * (g - c2 - xh * c1)
+    depth = N / 16 + 16
+    a1, a2 = (g * xh).abs().mean(1, keepdim=True), g.abs().mean(1, keepdim=True)
+    tol32 = 2 * U * rs * (6 * g.abs() + (depth + 8) * (a2 + xh.abs() * a1))
+    tol = HALF[x.dtype] * (d64.abs() + tol32) + tol32
+    assert ((dx.double() - d64).abs() <= tol).all()
+    depth = 16 * 1024 if rows > 16 * 1024 else rows  # (far above the longest run of any split)
+    assert ((dw.double() - (g0 * xh).sum(0)).abs() <= 2 * (depth + 8) * U * (g0 * xh).abs().sum(0)).all()
+    assert ((db.double() - g0.sum(0)).abs() <= 2 * (depth + 8) * U * g0.abs().sum(0)).all()
+
+
+# one vector or less a row, each thread layout and its edges, rows past the registers
+WIDTHS = [1, 2, 7, 8, 16, 63, 64, 127, 128, 136, 256, 500, 512, 1000, 1024, 1237, 2048, 2056, 4096,
+          4100, 8192, 8200, 9001, 20480]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N", WIDTHS)
+def test_layer_norm_and_gradients(N, dtype):
+    for rows in (1, 5, 67):
+        x, w, b, dy = inputs(rows, N, dtype, 100 * N + rows)
+        y, mean, rstd = K.layer_norm(x, w, b, 1e-5, want_stats=True)
+        check_forward(x, w, b, 1e-5, y, mean, rstd)
+        check_backward(x, w, dy, mean, rstd, *K.layer_norm_backward(dy, x, w, mean, rstd))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,N,pad", [(70001, 128, 0), (70001, 128, 8), (3000, 100, 3), (5000, 640, 16)])
+def test_many_rows_and_row_strides(rows, N, pad, dtype):
+    """Slices of a wider projection, on the vector path (pad 8, 16) and off it (pad 3)."""
+    x, w, b, dy = inputs(rows, N, dtype, 7, pad, offset=2.0)
+    y, mean, rstd = K.layer_norm(x, w, b, 1e-6, want_stats=True)
+    check_forward(x, w, b, 1e-6, y, mean, rstd)
+    check_backward(x, w, dy, mean, rstd, *K.layer_norm_backward(dy, x, w, mean, rstd))
+
+
+@pytest.mark.gpu
+def test_without_weight_and_bias_and_wanted_outputs():
+    x, w, b, dy = inputs(37, 129, torch.float32, 3)
+    for weight, bias in ((None, None), (w, None), (None, b)):
+        y, mean, rstd = K.layer_norm(x, weight, bias, 0.0, want_stats=True)
+        check_forward(x, weight, bias, 0.0, y, mean, rstd)
+        dx, dw, db = K.layer_norm_backward(dy, x, weight, mean, rstd)
+        check_backward(x, weight, dy, mean, rstd, dx, dw, db)
+        only = K.layer_norm_backward(dy, x, weight, mean, rstd, want_dweight=False, want_dbias=False)
+        assert torch.equal(only[0], dx) and only[1] is None and only[2] is None
+        only = K.layer_norm_backward(dy, x, weight, mean, rstd, want_dx=False, want_dweight=False)
+        assert only[0] is None and only[1] is None and torch.equal(only[2], db)
+
+
+@pytest.mark.gpu
+def test_constant_and_large_rows():
+    """A constant row has variance 0: y is the bias; the formula's NaN only with eps 0.  A row
+    with NaN or an infinity spoils no other row."""
+    x = torch.full((3, 128), 5.0, device="cuda")
+    w, b = torch.full((128,), 2.0, device="cuda"), torch.arange(128.0, device="cuda")
+    y, mean, rstd = K.layer_norm(x, w, b, 1e-6, want_stats=True)
+    assert torch.equal(y, b.expand(3, 128)) and (mean == 5.0).all()
+    assert K.layer_norm(x, w, b, 0.0)[0].isnan().all()
+    x, w, b, _ = inputs(64, 128, torch.bfloat16, 5)
+    ref = K.layer_norm(x, w, b)[0]
+    x = x.clone()
+    x[3, 7], x[20, 0] = float("nan"), float("inf")
+    y = K.layer_norm(x, w, b)[0]
+    keep = torch.ones(64, dtype=torch.bool, device="cuda")
+    keep[3] = keep[20] = False
+    assert torch.equal(y[keep], ref[keep]) and y[3].isnan().all() and y[20].isnan().all()
+
+
+@pytest.mark.gpu
+def test_gradients_match_differences():
+    """dx, dw and db along a random direction against central differences of the 64-bit
+    forward: with a step of 1e-5 the cubic term is about 1e-10 and the kernel's fp32 gradients
+    are good to 1e-5 of the sums' magnitude."""
+    x, w, b, dy = inputs(6, 200, torch.float32, 11)
+    _, mean, rstd = K.layer_norm(x, w, b, 1e-5, want_stats=True)
+    grads = K.layer_norm_backward(dy, x, w, mean, rstd)
+    g = torch.Generator().manual_seed(1)
+    p = [x.double(), w.double(), b.double()]
+    for i in range(3):
+        d = torch.randn(p[i].shape, generator=g, dtype=torch.float64).cuda()
+        up, dn = list(p), list(p)
+        up[i], dn[i] = p[i] + 1e-5 * d, p[i] - 1e-5 * d
+        num = (dy.double() * (forward64(*up, 1e-5)[0] - forward64(*dn, 1e-5)[0])).sum() / 2e-5
+        terms = (grads[i].double() * d)
+        assert abs(num - terms.sum()) <= 1e-5 * terms.abs().sum()
+
+
+@pytest.mark.gpu
+def test_same_bits_every_time_and_rows_outside_untouched():
+    x, w, b, dy = inputs(40000, 128, torch.bfloat16, 9)
+    y, mean, rstd = K.layer_norm(x, w, b, want_stats=True)
+    a = K.layer_norm_backward(dy, x, w, mean, rstd)
+    for _ in range(3):
+        assert all(torch.equal(p, q) for p, q in zip(a, K.layer_norm_backward(dy, x, w, mean, rstd)))
+    big = torch.full((40010, 128), 9.0, dtype=torch.bfloat16, device="cuda")
+    K.layer_norm(x, w, b, out=big[:40000])
+    assert torch.equal(big[:40000], y) and (big[40000:] == 9.0).all()
+
+
+@pytest.mark.gpu
+def test_no_rows():
+    x, w, b, dy = inputs(0, 128, torch.bfloat16, 9)
+    y, mean, rstd = K.layer_norm(x, w, b, want_stats=True)
+    assert y.shape == (0, 128)
+    dx, dw, db = K.layer_norm_backward(dy, x, w, mean, rstd)
+    assert dx.shape == (0, 128) and (dw == 0).all() and (db == 0).all()
+
+
+@pytest.mark.gpu
+def test_captured_step_replays_equal_eager():
+    """Forward and backward in one graph, replayed over new inputs between eager calls, on a
+    stream of its own."""
+    x, w, b, dy = inputs(999, 640, torch.bfloat16, 21)
+    x = x.clone()
+    ws = torch.empty(K.layer_norm_backward_workspace_bytes(999, 640), dtype=torch.uint8, device="cuda")
+
+    def step():
+        y, mean, rstd = K.layer_norm(x, w, b, want_stats=True)
+        return (y, mean, rstd) + K.layer_norm_backward(dy, x, w, mean, rstd, workspace=ws)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for i in range(4):
+        x.copy_(inputs(999, 640, torch.bfloat16, 30 + i)[0])
+        for t in out:
+            t.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        assert all(torch.equal(p, q) for p, q in zip(got, step()))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y = K.layer_norm(x, w, b, stream=side)[0]
+    side.synchronize()
+    assert torch.equal(y, got[0])
+
+
+# ---------------------------------------------------------------------------
+# Refusals (no GPU: the checks come before any launch)
+# ---------------------------------------------------------------------------
+
+def _c(**kw):
+    a = dict(x=16, stride=128, w=16, b=16, rows=4, N=128, eps=1e-6, dtype=0, y=16, mean=16, rstd=16)
+    a.update(kw)
+    return K.lib().kpool_layer_norm(a["x"], a["stride"], a["w"], a["b"], a["rows"], a["N"], a["eps"],
+                                    a["dtype"], a["y"], a["mean"], a["rstd"], None)
+
+
+def _c_bwd(**kw):
+    a = dict(dy=16, x=16, stride=128, w=16, mean=16, rstd=16, rows=4, N=128, dtype=0, ws=16,
+             ws_bytes=1 << 20, dx=16, dw=16, db=16)
+    a.update(kw)
+    return K.lib().kpool_layer_norm_backward(a["dy"], a["x"], a["stride"], a["w"], a["mean"], a["rstd"],
+                                             a["rows"], a["N"], a["dtype"], a["ws"], a["ws_bytes"],
+                                             a["dx"], a["dw"], a["db"], None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(rows=-1), dict(N=0), dict(stride=127), dict(eps=-1.0), dict(eps=float("nan")),
+    dict(eps=float("inf")), dict(dtype=2), dict(x=None), dict(y=None), dict(x=17), dict(y=18, dtype=1),
+    dict(w=18), dict(mean=17)])
+def test_layer_norm_refuses(kw):
+    assert _c(**kw) == K.KPOOL_EINVAL
+    assert K.lib().kpool_last_error()
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=-1), K.KPOOL_EINVAL), (dict(N=0), K.KPOOL_EINVAL), (dict(stride=127), K.KPOOL_EINVAL),
+    (dict(dtype=-1), K.KPOOL_EINVAL), (dict(dy=None), K.KPOOL_EINVAL), (dict(mean=None), K.KPOOL_EINVAL),
+    (dict(dx=None, dw=None, db=None), K.KPOOL_EINVAL), (dict(dy=17), K.KPOOL_EINVAL),
+    (dict(ws=24), K.KPOOL_EINVAL), (dict(ws=None), K.KPOOL_EWORKSPACE),
+    (dict(ws_bytes=1023), K.KPOOL_EWORKSPACE), (dict(ws_bytes=0, dw=None), K.KPOOL_EWORKSPACE)])
+def test_layer_norm_backward_refuses(kw, code):
+    assert _c_bwd(**kw) == code
+    assert K.lib().kpool_last_error()
+
+
+def test_no_rows_need_no_pointers():
+    assert _c(rows=0, x=None, y=None) == K.KPOOL_OK
+    assert _c_bwd(rows=0, dy=None, x=None, mean=None, rstd=None, dw=None, db=None, ws=None) == K.KPOOL_OK
+
+
+def test_backward_workspace_bytes():
+    assert K.layer_norm_backward_workspace_bytes(4, 128) == 2 * 128 * 4
+    assert K.layer_norm_backward_workspace_bytes(0, 128) == 2 * 128 * 4
+    assert K.layer_norm_backward_workspace_bytes(1 << 30, 128) == 1024 * 2 * 128 * 4
+    assert K.layer_norm_backward_workspace_bytes(-1, 128) == 0
+    assert K.layer_norm_backward_workspace_bytes(4, 0) == 0
+
+
+@pytest.mark.parametrize("bad", [
+    lambda x: x.half(), lambda x: x[0], lambda x: x.t(), lambda x: x.cpu()])
+def test_binding_refuses_other_tensors(bad):
+    x = torch.zeros(4, 8, dtype=torch.bfloat16)
+    if torch.cuda.is_available():
+        x = x.cuda()
+    with pytest.raises(ValueError):
+        K.layer_norm(bad(x))
