@@ -238,6 +238,53 @@ int kpool_expand(const int32_t *pool_ids, const int32_t *cu_seqlens_host,
 int kpool_topk(const float *scores, int64_t ld, const int32_t *n_valid, int64_t rows,
                int32_t budget, int32_t *pool_ids, void *stream);
 
+/* Attention of query rows over keys and values - what the selection is made for
+ * (Megatron-LM PR #8299 "Mechanism": the selected tokens are what a row attends to).
+ * For token row i of sequence s, query head h and key head g = h / (Hq / Hkv):
+ *   o[i,h,:] = sum_j softmax_j(scale * <q[i,h,:], k[j,g,:]>) v[j,g,:]
+ *   lse[i,h] = log sum_j exp(scale * <q[i,h,:], k[j,g,:]>)
+ * over the tokens j that the row sees; kpool_attend: every j <= t(i).
+ *   q        bf16, token row i at q + i * q_stride elements, its heads [Hq, D] contiguous;
+ *            k, v likewise with [Hkv, D] (a slice of a fused projection needs no copy)
+ *   cu_q     sequence s has the query rows [cu_q[s], cu_q[s+1]) and the keys
+ *   cu_k     [cu_k[s], cu_k[s+1]); its queries are the LAST rows of its keys: with Lq
+ *            queries and Lk keys, query n sits at position t = Lk - Lq + n.  A whole prompt
+ *            has cu_q = cu_k; a chunk of a prompt, or one new token a sequence, fewer
+ *            queries than keys.  Any lengths, 0 included; Lq > Lk leaves the first rows
+ *            without keys.  Host and device copies hold the same values.
+ *   o        bf16 [Tq, Hq, D] contiguous, Tq = cu_q[nseq]; rows past Tq are not touched
+ *   lse      NULLABLE fp32 [Tq, Hq]
+ * A row that sees nothing gets o = 0 and lse = -inf.  Sums and statistics are fp32; the
+ * weights are rounded to bf16 for the product with v, and o once.  q, k and v must be finite
+ * in the rows of the sequences; nothing outside them is read.  Outputs must not overlap
+ * inputs.  The same call gives the same bits every time.
+ * Sizes: D a multiple of 8 up to 128; Hq a multiple of Hkv; strides multiples of 8 from
+ * H * D to 2^24; q, k, v, o and the workspace 16-byte aligned.
+ *   workspace  kpool_attend_workspace_bytes(the same sizes) bytes (may be 0: then it is
+ *            not read): the parts of the key axis where there are few query rows; scratch. */
+size_t kpool_attend_workspace_bytes(const int32_t *cu_q_host, const int32_t *cu_k_host, int32_t nseq,
+                                    int32_t Hq, int32_t Hkv, int32_t D);
+int kpool_attend(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                 const uint16_t *v, int64_t v_stride, const int32_t *cu_q_host,
+                 const int32_t *cu_q_dev, const int32_t *cu_k_host, const int32_t *cu_k_dev,
+                 int32_t nseq, int32_t Hq, int32_t Hkv, int32_t D, float scale, void *workspace,
+                 size_t workspace_bytes, uint16_t *o, float *lse, void *stream);
+
+/* The same over the tokens a row selected: row i sees the tokens token_ids[i, 0 .. width)
+ * that lie in 0 .. t(i) (kpool_expand's output; other entries, -1 among them, stand for
+ * nothing, wherever they are in the list).  A token that is listed twice counts twice.
+ *   token_ids  int32 [Tq, width], sequence-local token ids, any order
+ * The other arguments, the outputs and what holds for them are kpool_attend's; only the
+ * listed tokens' keys and values have to be finite, as no others are read. */
+size_t kpool_attend_selected_workspace_bytes(int64_t Tq, int32_t nseq, int32_t width, int32_t Hq,
+                                             int32_t Hkv, int32_t D);
+int kpool_attend_selected(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                          const uint16_t *v, int64_t v_stride, const int32_t *token_ids,
+                          int32_t width, const int32_t *cu_q_host, const int32_t *cu_q_dev,
+                          const int32_t *cu_k_host, const int32_t *cu_k_dev, int32_t nseq, int32_t Hq,
+                          int32_t Hkv, int32_t D, float scale, void *workspace,
+                          size_t workspace_bytes, uint16_t *o, float *lse, void *stream);
+
 /* Layer norm of rows - the indexer's keys pass one with weight and bias before they are
  * pooled (Atlas inference docs, glm5next_dsa/tp.rs: the indexer's k_norm among the shard
  * plan's tensors).  For row r and column j < N:

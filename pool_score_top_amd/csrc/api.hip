@@ -412,6 +412,63 @@ int score_topk_impl(const char *fn, const uint16_t *q, const uint16_t *kp, const
   return ok();
 }
 
+// Arguments that the attention entry points share.
+int check_heads(const char *fn, int32_t Hq, int32_t Hkv, int32_t D) {
+  if (Hq < 1 || Hkv < 1 || Hq % Hkv)
+    return fail(KPOOL_EINVAL, "%s: Hq must be a positive multiple of Hkv (Hq=%d Hkv=%d)", fn, Hq, Hkv);
+  if (Hq > 65536) return fail(KPOOL_EUNSUPPORTED, "%s: more than 65536 heads (got %d)", fn, Hq);
+  if (D < 8 || D % 8) return fail(KPOOL_EINVAL, "%s: D must be a positive multiple of 8 (got %d)", fn, D);
+  if (D > 128) return fail(KPOOL_EUNSUPPORTED, "%s: D up to 128 is compiled in (got %d)", fn, D);
+  return KPOOL_OK;
+}
+
+int check_lengths(const char *fn, const int32_t *cu_q, const int32_t *cu_k, int32_t nseq, int32_t G) {
+  int rc = check_cu(cu_q, nseq, fn);
+  if (!rc) rc = check_cu(cu_k, nseq, fn);
+  if (rc) return rc;
+  for (int32_t s = 0; s < nseq; ++s)  // (a tile's rows are numbered in 32 bits)
+    if ((int64_t)(cu_q[s + 1] - cu_q[s]) * G > 0x7FFFFF00)
+      return fail(KPOOL_EUNSUPPORTED, "%s: sequence %d has too many query rows", fn, s);
+  return KPOOL_OK;
+}
+
+// Fills in Tq and Tk.  Tq = 0 needs no pointers.
+int check_attend(const char *fn, kpool::AttendCall &c, const int32_t *cu_q_host, const int32_t *cu_k_host) {
+  int rc = check_heads(fn, c.Hq, c.Hkv, c.D);
+  if (!rc) rc = check_lengths(fn, cu_q_host, cu_k_host, c.nseq, c.Hq / c.Hkv);
+  if (rc) return rc;
+  if (!(c.scale > 0.0f) || !isfinite(c.scale)) return fail(KPOOL_EINVAL, "%s: scale must be finite and > 0", fn);
+  const struct { int64_t stride, least; } st[3] = {{c.q_stride, (int64_t)c.Hq * c.D},
+                                                   {c.k_stride, (int64_t)c.Hkv * c.D},
+                                                   {c.v_stride, (int64_t)c.Hkv * c.D}};
+  for (const auto &x : st)
+    if (x.stride < x.least || x.stride % 8 || x.stride > (1 << 24))
+      return fail(KPOOL_EINVAL, "%s: a token stride must be a multiple of 8 in [%lld, 2^24] (got %lld)", fn,
+                  (long long)x.least, (long long)x.stride);
+  c.Tq = cu_q_host[c.nseq];
+  c.Tk = cu_k_host[c.nseq];
+  if (c.Tq == 0) return ok();
+  if (!c.q || !c.o || !c.cu_q || !c.cu_k || (c.Tk > 0 && (!c.k || !c.v)))
+    return fail(KPOOL_EINVAL, "%s: null pointer", fn);
+  if (!aligned16(c.q) || !aligned16(c.k) || !aligned16(c.v) || !aligned16(c.o))
+    return fail(KPOOL_EINVAL, "%s: q, k, v and o must be 16-byte aligned", fn);
+  if ((uintptr_t)c.lse & 3) return fail(KPOOL_EINVAL, "%s: lse is not aligned to its elements", fn);
+  return KPOOL_OK;
+}
+
+int check_attend_plan(const char *fn, const kpool::AttendCall &c, const kpool::AttendPlan &p, int64_t per,
+                      const void *workspace, size_t workspace_bytes) {
+  // workgroups of up to 512 threads; a launch's threads stay below 2^32
+  if (p.ntiles * per * p.nsplit * c.Hkv >= (int64_t(1) << 23))
+    return fail(KPOOL_EUNSUPPORTED, "%s: too many query rows for one launch", fn);
+  const size_t need = kpool::attend_workspace(p, c.Tq * c.Hq, c.D);
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(KPOOL_EWORKSPACE, "%s: needs %zu bytes of workspace, got %zu", fn, need,
+                workspace ? workspace_bytes : (size_t)0);
+  if (need && !aligned16(workspace)) return fail(KPOOL_EINVAL, "%s: workspace must be 16-byte aligned", fn);
+  return KPOOL_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -571,6 +628,71 @@ int kpool_topk(const float *scores, int64_t ld, const int32_t *n_valid, int64_t 
   hipError_t e = timed(2, st, [&] {
     return kpool::launch_topk(scores, ld, rows, n_valid, nullptr, 0, 0, 1, false, budget, pool_ids,
                               nullptr, 0, st);
+  });
+  if (e != hipSuccess) return hip_fail(fn, e);
+  return ok();
+}
+
+size_t kpool_attend_workspace_bytes(const int32_t *cu_q_host, const int32_t *cu_k_host, int32_t nseq,
+                                    int32_t Hq, int32_t Hkv, int32_t D) {
+  const char *fn = "kpool_attend_workspace_bytes";
+  if (check_heads(fn, Hq, Hkv, D) || check_lengths(fn, cu_q_host, cu_k_host, nseq, Hq / Hkv)) return 0;
+  ok();
+  return kpool::attend_workspace(kpool::plan_attend(cu_q_host, cu_k_host, nseq, Hq, Hkv),
+                                 (int64_t)cu_q_host[nseq] * Hq, D);
+}
+
+int kpool_attend(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                 const uint16_t *v, int64_t v_stride, const int32_t *cu_q_host,
+                 const int32_t *cu_q_dev, const int32_t *cu_k_host, const int32_t *cu_k_dev,
+                 int32_t nseq, int32_t Hq, int32_t Hkv, int32_t D, float scale, void *workspace,
+                 size_t workspace_bytes, uint16_t *o, float *lse, void *stream) {
+  const char *fn = "kpool_attend";
+  kpool::AttendCall c{q, k, v, q_stride, k_stride, v_stride, cu_q_dev, cu_k_dev, nseq, Hq, Hkv, D,
+                      0, 0, scale, o, lse};
+  int rc = check_attend(fn, c, cu_q_host, cu_k_host);
+  if (rc || c.Tq == 0) return rc;
+  const kpool::AttendPlan p = kpool::plan_attend(cu_q_host, cu_k_host, nseq, Hq, Hkv);
+  rc = check_attend_plan(fn, c, p, 1, workspace, workspace_bytes);
+  if (rc) return rc;
+  hipStream_t st = (hipStream_t)stream;
+  hipError_t e = timed(6, st, [&] { return kpool::launch_attend(c, p, workspace, st); });
+  if (e != hipSuccess) return hip_fail(fn, e);
+  return ok();
+}
+
+size_t kpool_attend_selected_workspace_bytes(int64_t Tq, int32_t nseq, int32_t width, int32_t Hq,
+                                             int32_t Hkv, int32_t D) {
+  const char *fn = "kpool_attend_selected_workspace_bytes";
+  if (check_heads(fn, Hq, Hkv, D)) return 0;
+  if (Tq < 0 || nseq < 1 || width < 0) {
+    fail(KPOOL_EINVAL, "%s: need Tq >= 0, nseq >= 1, width >= 0", fn);
+    return 0;
+  }
+  ok();
+  return kpool::attend_workspace(kpool::plan_list(Tq, nseq, width, Hq, Hkv), Tq * Hq, D);
+}
+
+int kpool_attend_selected(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                          const uint16_t *v, int64_t v_stride, const int32_t *token_ids,
+                          int32_t width, const int32_t *cu_q_host, const int32_t *cu_q_dev,
+                          const int32_t *cu_k_host, const int32_t *cu_k_dev, int32_t nseq, int32_t Hq,
+                          int32_t Hkv, int32_t D, float scale, void *workspace,
+                          size_t workspace_bytes, uint16_t *o, float *lse, void *stream) {
+  const char *fn = "kpool_attend_selected";
+  if (width < 0 || width > (1 << 30)) return fail(KPOOL_EINVAL, "%s: width must be in [0, 2^30] (got %d)", fn, width);
+  kpool::AttendCall c{q, k, v, q_stride, k_stride, v_stride, cu_q_dev, cu_k_dev, nseq, Hq, Hkv, D,
+                      0, 0, scale, o, lse};
+  int rc = check_attend(fn, c, cu_q_host, cu_k_host);
+  if (rc || c.Tq == 0) return rc;
+  if (width > 0 && !token_ids) return fail(KPOOL_EINVAL, "%s: null pointer", fn);
+  if ((uintptr_t)token_ids & 3) return fail(KPOOL_EINVAL, "%s: token_ids is not aligned to its elements", fn);
+  const kpool::AttendPlan p = kpool::plan_list(c.Tq, nseq, width, Hq, Hkv);
+  rc = check_attend_plan(fn, c, p, (Hq / Hkv + 31) / 32, workspace, workspace_bytes);
+  if (rc) return rc;
+  hipStream_t st = (hipStream_t)stream;
+  hipError_t e = timed(6, st, [&] {
+    return kpool::launch_attend_list(c, p, token_ids, width, workspace, st);
   });
   if (e != hipSuccess) return hip_fail(fn, e);
   return ok();

@@ -1,0 +1,579 @@
+// Attention of query rows over the keys they see: o = softmax(scale q k^T) v per head, and
+// lse = log sum exp(scale q k^T), forward.
+//
+// Pages: Megatron-LM PR #8299 and SkyRL PR #2422 describe the selection as the step before
+// sparse attention: each row then attends to the tokens selected for it.  The rows kernel
+// below reads such lists of token ids; the tile kernel is the attention of the rows over
+// everything before them (dense layers, prompts no longer than the selection's width).
+//
+// One pass over the keys with the running maximum m and sum l of the softmax:
+//   m' = max(m, max_j s_j),  l' = l e^(m - m') + sum_j e^(s_j - m'),
+//   O' = O e^(m - m') + sum_j e^(s_j - m') v_j,   o = O / l,  lse = m + ln l
+// kept in fp32 in base 2 (s = q k^T scale log2 e).  e^(s - m) is rounded to bf16 for the
+// matrix product with v (relative 2^-9 on average, as the output's own rounding; it averages
+// over the keys); l sums the unrounded values.  m follows the maximum only when that rises by
+// more than 8 (a factor of 256 in base 2): the exact shift cancels in O / l, values up to
+// 2^8 lose nothing in bf16 or fp32, and most tiles then leave O alone.
+//
+// S^T = K Q^T and O^T = V^T P^T: a lane owns one query row, so the softmax needs one
+// exchange between the wave's halves and P feeds the second product from registers.
+#include <type_traits>
+
+#include "attend_tile.h"
+
+namespace kpool {
+namespace {
+
+struct AttendArgs {
+  const uint16_t *q, *k, *v;
+  int64_t qs, ks, vs;  // elements between tokens
+  const int32_t *cu_q, *cu_k;
+  int nseq, Hq, Hkv, D;
+  float scale_log2;
+  int64_t ntiles;
+  int nsplit;
+  int chunk;  // keys (or list entries) of a split, a multiple of 256
+  const int32_t *ids;
+  int width;
+  uint16_t *o;
+  float *lse;
+  float *part_o, *part_lse;  // [nsplit][Tq * Hq][D], [nsplit][Tq * Hq]
+  int64_t rows;              // Tq * Hq
+};
+
+// One wave's 32 query rows: fragments, running softmax and output.
+template <int DP>
+struct Rows {
+  using S = Keys<DP>;
+  bf16x8 q[S::KS];
+  f32x16 o[S::DT];
+  float m, l;  // base 2; l is this lane half's part
+
+  // row: this lane's query (l % 32), null for none
+  __device__ inline void init(const uint16_t *row, int D, int lane) {
+#pragma unroll
+    for (int ks = 0; ks < S::KS; ++ks) {
+      const int d = ks * 16 + (lane >> 5) * 8;
+      uint4 z = make_uint4(0, 0, 0, 0);
+      if (row && d < D) z = *reinterpret_cast<const uint4 *>(row + d);
+      q[ks] = __builtin_bit_cast(bf16x8, z);
+    }
+#pragma unroll
+    for (int dt = 0; dt < S::DT; ++dt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[dt][i] = 0.0f;
+    m = -__builtin_inff();
+    l = 0.0f;
+  }
+
+  // Adds the BK keys of a tile at LDS offsets sk and sv past the addresses of `f`.  Where
+  // `masked` (the same for the wave), key sub * 32 + r counts only if visible(sub, r).
+  template <int BK, class F>
+  __device__ inline void add(const Frag<DP> &f, uint32_t sk, uint32_t sv, float c, int lane, bool masked,
+                             F &&visible) {
+    constexpr int SUBS = BK / 32;
+    f32x16 s[SUBS];
+#pragma unroll
+    for (int sub = 0; sub < SUBS; ++sub) {
+      f32x16 t = {};
+#pragma unroll
+      for (int ks = 0; ks < S::KS; ++ks) t = mfma(f.rows(sk + sub * 32 * S::ROWB, ks), q[ks], t);
+      s[sub] = t;
+    }
+    if (masked) {
+#pragma unroll
+      for (int sub = 0; sub < SUBS; ++sub)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (!visible(sub, 8 * (i / 4) + 4 * (lane >> 5) + i % 4)) s[sub][i] = -__builtin_inff();
+    }
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int sub = 0; sub < SUBS; ++sub)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[sub][i]);
+    top = fmaxf(top, other_half(top)) * c;
+    if (__any(top > m + 8.0f)) {  // (m = -inf: any visible key)
+      const float up = fmaxf(top, m);
+      const float a = up > m ? exp2f_fast(m - up) : 1.0f;  // m = -inf gives 0
+      m = up;
+      l *= a;
+#pragma unroll
+      for (int dt = 0; dt < S::DT; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[dt][i] *= a;
+    }
+    const float shift = m > -__builtin_inff() ? m : 0.0f;
+#pragma unroll
+    for (int sub = 0; sub < SUBS; ++sub) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[sub][i] = exp2f_fast(fmaf(s[sub][i], c, -shift));
+        l += s[sub][i];
+      }
+#pragma unroll
+      for (int kc = 0; kc < 2; ++kc) {
+        const bf16x8 p = as_operand(s[sub], kc);
+#pragma unroll
+        for (int dt = 0; dt < S::DT; ++dt)
+          o[dt] = mfma(f.cols(sv + (sub * 32 + kc * 16) * S::ROWB, dt), p, o[dt]);
+      }
+    }
+  }
+};
+
+// Writes a row's output: the final one, or a split's part (in fp32, normalised by its own l).
+template <int DP>
+__device__ inline void write_row(const AttendArgs &a, int64_t row, int split, const f32x16 (&o)[DP / 32],
+                                 float m, float l, int lane) {
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float lse = l > 0.0f ? (m + log2f(l)) * kLn2 : -__builtin_inff();
+  const int h = lane >> 5;
+  if (a.nsplit > 1) {
+    float *dst = a.part_o + ((int64_t)split * a.rows + row) * a.D;
+#pragma unroll
+    for (int dt = 0; dt < DP / 32; ++dt)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const int d = dt * 32 + 2 * i + 4 * h;
+        if (d < a.D)
+          *reinterpret_cast<float4 *>(dst + d) = make_float4(o[dt][i] * inv, o[dt][i + 1] * inv,
+                                                             o[dt][i + 2] * inv, o[dt][i + 3] * inv);
+      }
+    if (h == 0) a.part_lse[(int64_t)split * a.rows + row] = lse;
+    return;
+  }
+  uint16_t *dst = a.o + row * a.D;
+#pragma unroll
+  for (int dt = 0; dt < DP / 32; ++dt)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const int d = dt * 32 + 2 * i + 4 * h;
+      if (d < a.D)
+        *reinterpret_cast<uint2 *>(dst + d) =
+            make_uint2(pack_bf16(o[dt][i] * inv, o[dt][i + 1] * inv),
+                       pack_bf16(o[dt][i + 2] * inv, o[dt][i + 3] * inv));
+    }
+  if (h == 0 && a.lse) a.lse[row] = lse;
+}
+
+// Many rows: NW waves of 32 virtual rows each share key tiles of 64.
+template <int DP, int NW>
+__global__ __launch_bounds__(NW * 64) void attend_tile_kernel(AttendArgs a) {
+  using S = Keys<DP>;
+  constexpr int BK = 64, BQ = NW * 32, TILE = BK * S::ROWB;
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int G = a.Hq / a.Hkv;
+  int64_t idx = blockIdx.x;
+  const int kvh = (int)(idx % a.Hkv);
+  idx /= a.Hkv;
+  const int split = (int)(idx % a.nsplit);
+  // (the last tiles of a sequence see the most keys and go first)
+  const TileAt at = find_tile(a.cu_q, a.cu_k, a.nseq, G, BQ, a.ntiles - 1 - idx / a.nsplit, lane);
+  if (at.seq < 0) return;
+  const int nrows = min(BQ, at.Lq * G - at.n0);
+  const int t1 = (at.n0 + nrows - 1) / G + at.Lk - at.Lq;  // the last row's position
+  const int k_lo = split * a.chunk, k_hi = (int)min<int64_t>(t1 + 1, (int64_t)k_lo + a.chunk);
+  const uint16_t *kb = (const uint16_t *)uniform_ptr(a.k + (int64_t)at.k_start * a.ks + (int64_t)kvh * a.D);
+  const uint16_t *vb = (const uint16_t *)uniform_ptr(a.v + (int64_t)at.k_start * a.vs + (int64_t)kvh * a.D);
+
+  const int n = at.n0 + wave * 32 + (lane & 31);
+  const bool live = wave * 32 + (lane & 31) < nrows;
+  const int tok = n / G;
+  const int head = kvh * G + (n - tok * G);
+  const int t = tok + at.Lk - at.Lq;
+  // this wave's first and last position
+  const int wave_rows = min(32, nrows - wave * 32);
+  const int w0 = (at.n0 + wave * 32) / G + at.Lk - at.Lq;
+  const int w1 = wave_rows > 0 ? (at.n0 + wave * 32 + wave_rows - 1) / G + at.Lk - at.Lq : -1;
+  Rows<DP> r;
+  r.init(live ? a.q + ((int64_t)at.q_start + tok) * a.qs + (int64_t)head * a.D : nullptr, a.D, lane);
+  
+  Frag<DP> f;
+  f.init(lds_offset(lds), lane);
+  KeyLoader<DP, BK, NW> keys;
+  keys.init(wave, lane, a.D);
+  const int ntile = k_hi > k_lo ? (k_hi - k_lo + BK - 1) / BK : 0;
+  auto load = [&](int tile, int buf) {
+    const int k0 = k_lo + tile * BK;
+    keys.load(kb + (int64_t)k0 * a.ks, a.ks, at.Lk - 1 - k0, lds + buf * 2 * TILE);
+    keys.load(vb + (int64_t)k0 * a.vs, a.vs, at.Lk - 1 - k0, lds + buf * 2 * TILE + TILE);
+  };
+  auto step = [&](int j, auto buf_c) {
+    constexpr int BUF = decltype(buf_c)::value;
+    // this wave's part of tile j has landed; behind the barrier everyone's has, and everyone
+    // is done with the buffer that tile j + 1 goes to
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+    __syncthreads();
+    if (j + 1 < ntile) load(j + 1, BUF ^ 1);
+    const int k0 = k_lo + j * BK;
+    if (k0 <= w1)  // (the whole wave; not where it sees none of the tile, or has no rows)
+      r.template add<BK>(f, BUF * 2 * TILE, BUF * 2 * TILE + TILE, a.scale_log2, lane, k0 + BK - 1 > w0,
+                         [&](int sub, int i) { return k0 + sub * 32 + i <= t; });
+  };
+  if (ntile > 0) load(0, 0);
+  for (int j = 0; j < ntile; j += 2) {
+    step(j, std::integral_constant<int, 0>{});
+    if (j + 1 < ntile) step(j + 1, std::integral_constant<int, 1>{});
+  }
+  const float l = r.l + other_half(r.l);
+  if (live) write_row<DP>(a, ((int64_t)at.q_start + tok) * a.Hq + head, split, r.o, r.m, l, lane);
+}
+
+// Few rows, or rows with lists: a workgroup's 4 waves share 32 virtual rows and take key
+// tiles of 32 in turn, each through its own double-buffered LDS, and join at the end.
+// LIST: the tile's rows are heads of one token and the keys are the token's ids; an entry
+// outside 0 .. t is not there.
+template <int DP, bool LIST>
+__global__ __launch_bounds__(256) void attend_rows_kernel(AttendArgs a) {
+  using S = Keys<DP>;
+  constexpr int BK = 32, NW = 4, TILE = BK * S::ROWB;
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int G = a.Hq / a.Hkv;
+  int64_t idx = blockIdx.x;
+  const int kvh = (int)(idx % a.Hkv);
+  idx /= a.Hkv;
+  const int split = (int)(idx % a.nsplit);
+  idx /= a.nsplit;
+  TileAt at;
+  int first = 0;  // LIST: the tile's first head of the group
+  if (LIST) {
+    const int per = (G + 31) / 32;
+    const int64_t token = idx / per;
+    first = (int)(idx - token * per) * 32;
+    at = find_tile(a.cu_q, a.cu_k, a.nseq, 1, 1, token, lane);
+    (void)token;
+  } else {
+    at = find_tile(a.cu_q, a.cu_k, a.nseq, G, 32, a.ntiles - 1 - idx, lane);
+  }
+  if (at.seq < 0) return;
+  int tok, head, nrows;
+  if (LIST) {
+    tok = at.n0;
+    head = first + (lane & 31);
+    nrows = min(32, G - first);
+  } else {
+    const int n = at.n0 + (lane & 31);
+    tok = n / G;
+    head = n - tok * G;
+    nrows = min(32, at.Lq * G - at.n0);
+  }
+  const bool live = (lane & 31) < nrows;
+  head += kvh * G;
+  const int t = tok + at.Lk - at.Lq;
+  Rows<DP> r;
+  r.init(live ? a.q + ((int64_t)at.q_start + tok) * a.qs + (int64_t)head * a.D : nullptr, a.D, lane);
+
+  const uint16_t *kb = (const uint16_t *)uniform_ptr(a.k + (int64_t)at.k_start * a.ks + (int64_t)kvh * a.D);
+  const uint16_t *vb = (const uint16_t *)uniform_ptr(a.v + (int64_t)at.k_start * a.vs + (int64_t)kvh * a.D);
+  unsigned char *mine = lds + wave * 4 * TILE;
+  Frag<DP> f;
+  f.init(lds_offset(mine), lane);
+  KeyLoader<DP, BK, 1> keys;
+  keys.init(0, lane, a.D);
+  // the last key (or list entry) of any row of the tile, and of every row
+  const int t1 = LIST ? 0 : (at.n0 + nrows - 1) / G + at.Lk - at.Lq;
+  const int t0 = LIST ? 0 : at.n0 / G + at.Lk - at.Lq;
+  const int end = LIST ? a.width : t1 + 1;
+  const int k_lo = split * a.chunk, k_hi = (int)min<int64_t>(end, (int64_t)k_lo + a.chunk);
+  const int32_t *ids = LIST ? a.ids + ((int64_t)at.q_start + tok) * a.width : nullptr;
+
+  // entry `lane` (of 32) of list tile k0: the id, and which of the tile are there
+  auto entries = [&](int k0, uint32_t &there) {
+    const int e = k0 + (lane & 31);
+    const int id = e < k_hi ? ids[e] : -1;
+    const bool ok = id >= 0 && id <= t;
+    there = (uint32_t)__ballot(ok);
+    // absent entries read the tile's first present one, so that only keys of the list are read
+    const int any = there ? __builtin_ctz(there) : 0;
+    const int stand_in = __builtin_amdgcn_readlane(id, any);
+    return ok ? id : stand_in;
+  };
+  // 2 * BK / REGION_ROWS loads of 1 KiB a tile
+  constexpr int REGIONS = BK / S::REGION_ROWS;
+  auto load_list = [&](int id, int buf) {
+#if defined(__HIP_DEVICE_COMPILE__)
+#pragma unroll
+    for (int i = 0; i < REGIONS; ++i) {
+      const int row = i * S::REGION_ROWS + lane * 16 / S::ROWB;
+      const int chunk = min((lane & (DP / 8 - 1)) ^ S::swz(row), a.D / 8 - 1);
+      const int64_t key = __shfl(id, row);
+      __builtin_amdgcn_global_load_lds(
+          (const __attribute__((address_space(1))) void *)(kb + key * a.ks + chunk * 8),
+          (KPOOL_LDS void *)(mine + buf * 2 * TILE + i * 1024), 16, 0, 0);
+      __builtin_amdgcn_global_load_lds(
+          (const __attribute__((address_space(1))) void *)(vb + key * a.vs + chunk * 8),
+          (KPOOL_LDS void *)(mine + buf * 2 * TILE + TILE + i * 1024), 16, 0, 0);
+    }
+#endif
+  };
+  auto load = [&](int k0, int buf) {
+    keys.load(kb + (int64_t)k0 * a.ks, a.ks, at.Lk - 1 - k0, mine + buf * 2 * TILE);
+    keys.load(vb + (int64_t)k0 * a.vs, a.vs, at.Lk - 1 - k0, mine + buf * 2 * TILE + TILE);
+  };
+  uint32_t there = 0, there_next = 0;
+  int k0 = k_lo + wave * BK, buf = 0;
+  if (k0 < k_hi) {
+    if (LIST) {
+      const int id = entries(k0, there);
+      if (there) load_list(id, 0);
+    } else {
+      load(k0, 0);
+    }
+  }
+  for (; k0 < k_hi; k0 += NW * BK, buf ^= 1) {
+    const int kn = k0 + NW * BK;
+    bool more = kn < k_hi;
+    if (LIST) {
+      there_next = 0;
+      if (more) {
+        const int id = entries(kn, there_next);
+        more = there_next != 0;
+        if (more) load_list(id, buf ^ 1);
+      }
+    } else if (more) {
+      load(kn, buf ^ 1);
+    }
+    // the tile's own loads are the older ones: wait until only the next tile's are out
+    static_assert(2 * REGIONS == 16 || 2 * REGIONS == 8, "loads of a tile");
+    if (!more) __builtin_amdgcn_s_waitcnt(0x0F70);                        // vmcnt(0)
+    else if (2 * REGIONS == 16) __builtin_amdgcn_s_waitcnt(0x4F70);       // vmcnt(16)
+    else __builtin_amdgcn_s_waitcnt(0x0F78);                              // vmcnt(8)
+    asm volatile("" ::: "memory");
+    const uint32_t sk = buf * 2 * TILE, sv = sk + TILE;
+    if (LIST) {
+      if (there)
+        r.template add<BK>(f, sk, sv, a.scale_log2, lane, there != 0xFFFFFFFFu,
+                           [&](int, int i) { return (there >> i) & 1; });
+      there = there_next;
+    } else {
+      r.template add<BK>(f, sk, sv, a.scale_log2, lane, k0 + BK - 1 > t0,
+                         [&](int, int i) { return k0 + i <= t; });
+    }
+    asm volatile("" ::: "memory");
+  }
+  // The waves join: m and l of every row, then O scaled to the common m, summed in wave order.
+  float l = r.l + other_half(r.l);
+  __syncthreads();  // (all waves are done with their tiles)
+  float *stat = reinterpret_cast<float *>(lds);                 // [NW][2][32]
+  float *acc = stat + NW * 64;                                  // [NW][DP][33]
+  if (lane < 32) stat[wave * 64 + lane] = r.m, stat[wave * 64 + 32 + lane] = l;
+  __syncthreads();
+  float m = -__builtin_inff();
+#pragma unroll
+  for (int w = 0; w < NW; ++w) m = fmaxf(m, stat[w * 64 + (lane & 31)]);
+  const float shift = m > -__builtin_inff() ? m : 0.0f;
+  l = 0.0f;
+#pragma unroll
+  for (int w = 0; w < NW; ++w)
+    l += stat[w * 64 + 32 + (lane & 31)] * exp2f_fast(stat[w * 64 + (lane & 31)] - shift);
+  const float mul = exp2f_fast(r.m - shift);
+#pragma unroll
+  for (int dt = 0; dt < S::DT; ++dt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      acc[(wave * DP + dt * 32 + 8 * (i / 4) + 4 * (lane >> 5) + i % 4) * 33 + (lane & 31)] =
+          r.o[dt][i] * mul;
+  __syncthreads();
+  // thread: row (tid / 8), columns 16 (tid % 8) .. + DP / 8
+  {
+    const int row = threadIdx.x >> 3, d0 = (threadIdx.x & 7) * (DP / 8);
+    float rm = -__builtin_inff(), rl = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) rm = fmaxf(rm, stat[w * 64 + row]);
+    const float sh = rm > -__builtin_inff() ? rm : 0.0f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) rl += stat[w * 64 + 32 + row] * exp2f_fast(stat[w * 64 + row] - sh);
+    if (row >= nrows) return;
+    int tk, hd;
+    if (LIST) {
+      tk = at.n0;
+      hd = first + row;
+    } else {
+      const int n = at.n0 + row;
+      tk = n / G;
+      hd = n - tk * G;
+    }
+    const int64_t out_row = ((int64_t)at.q_start + tk) * a.Hq + kvh * G + hd;
+    const float inv = rl > 0.0f ? 1.0f / rl : 0.0f;
+    const float lse = rl > 0.0f ? (rm + log2f(rl)) * kLn2 : -__builtin_inff();
+    float out[DP / 8];
+#pragma unroll
+    for (int d = 0; d < DP / 8; ++d) {
+      float t4 = 0.0f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) t4 += acc[(w * DP + d0 + d) * 33 + row];
+      out[d] = t4 * inv;
+    }
+#pragma unroll
+    for (int d = 0; d < DP / 8; d += 8) {
+      if (d0 + d >= a.D) break;  // (D is a multiple of 8)
+      if (a.nsplit > 1) {
+        float *dst = a.part_o + ((int64_t)split * a.rows + out_row) * a.D + d0 + d;
+        *reinterpret_cast<float4 *>(dst) = make_float4(out[d], out[d + 1], out[d + 2], out[d + 3]);
+        *reinterpret_cast<float4 *>(dst + 4) = make_float4(out[d + 4], out[d + 5], out[d + 6], out[d + 7]);
+      } else {
+        *reinterpret_cast<uint4 *>(a.o + out_row * a.D + d0 + d) =
+            make_uint4(pack_bf16(out[d], out[d + 1]), pack_bf16(out[d + 2], out[d + 3]),
+                       pack_bf16(out[d + 4], out[d + 5]), pack_bf16(out[d + 6], out[d + 7]));
+      }
+    }
+    if ((threadIdx.x & 7) == 0) {
+      if (a.nsplit > 1) a.part_lse[(int64_t)split * a.rows + out_row] = lse;
+      else if (a.lse) a.lse[out_row] = lse;
+    }
+  }
+}
+
+// Joins the splits of a row: o = sum_s 2^(lse_s - lse) o_s.  A wave per row; a split that
+// saw nothing has lse -inf and was not written, so it is not read.
+__global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (row >= a.rows) return;
+  float m = -__builtin_inff();
+  for (int s = lane; s < a.nsplit; s += 64) m = fmaxf(m, a.part_lse[(int64_t)s * a.rows + row]);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+  const float shift = m > -__builtin_inff() ? m : 0.0f;
+  float total = 0.0f, o0 = 0.0f, o1 = 0.0f;
+  const int d = lane * 2;
+  for (int s = 0; s < a.nsplit; ++s) {
+    const float part = a.part_lse[(int64_t)s * a.rows + row];
+    if (!(part > -__builtin_inff())) continue;
+    const float w = exp2f_fast((part - shift) * kLog2e);
+    total += w;
+    if (d < a.D) {
+      const float2 v = *reinterpret_cast<const float2 *>(a.part_o + ((int64_t)s * a.rows + row) * a.D + d);
+      o0 = fmaf(w, v.x, o0);
+      o1 = fmaf(w, v.y, o1);
+    }
+  }
+  const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+  if (d < a.D) *reinterpret_cast<uint32_t *>(a.o + row * a.D + d) = pack_bf16(o0 * inv, o1 * inv);
+  if (lane == 0 && a.lse) a.lse[row] = total > 0.0f ? shift + log2f(total) * kLn2 : -__builtin_inff();
+}
+
+
+hipError_t launch_join(const AttendArgs &a, hipStream_t st) {
+  hipLaunchKernelGGL(attend_join_kernel, dim3((unsigned)((a.rows + 3) / 4)), dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
+template <class F>
+hipError_t with_lds(F *kernel, size_t bytes) {
+  // (a launch may use more than 64 KiB of LDS only where the kernel was told so)
+  return bytes > 65536 ? hipFuncSetAttribute((const void *)kernel,
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)
+                       : hipSuccess;
+}
+
+template <int DP>
+hipError_t launch_attend_t(const AttendPlan &p, const AttendArgs &a, hipStream_t st) {
+  const unsigned grid = (unsigned)(a.ntiles * a.nsplit * a.Hkv);
+  hipError_t e;
+  if (p.form == AttendPlan::kRows) {
+    const size_t lds = 4 * 4 * 32 * DP * 2;
+    e = with_lds(attend_rows_kernel<DP, false>, lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((attend_rows_kernel<DP, false>), dim3(grid), dim3(256), lds, st, a);
+  } else {
+    const size_t lds = 4 * 64 * DP * 2;
+    e = with_lds(attend_tile_kernel<DP, 8>, lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((attend_tile_kernel<DP, 8>), dim3(grid), dim3(512), lds, st, a);
+  }
+  e = hipGetLastError();
+  if (e == hipSuccess && a.nsplit > 1) e = launch_join(a, st);
+  return e;
+}
+
+template <int DP>
+hipError_t launch_list_t(const AttendArgs &a, hipStream_t st) {
+  const int G = a.Hq / a.Hkv;
+  const size_t lds = 4 * 4 * 32 * DP * 2;
+  hipError_t e = with_lds(attend_rows_kernel<DP, true>, lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((attend_rows_kernel<DP, true>),
+                     dim3((unsigned)(a.ntiles * ((G + 31) / 32) * a.nsplit * a.Hkv)), dim3(256), lds, st, a);
+  e = hipGetLastError();
+  if (e == hipSuccess && a.nsplit > 1) e = launch_join(a, st);
+  return e;
+}
+
+AttendArgs make_args(const AttendCall &c, const AttendPlan &p, void *workspace) {
+  AttendArgs a{};
+  a.q = c.q, a.k = c.k, a.v = c.v;
+  a.qs = c.q_stride, a.ks = c.k_stride, a.vs = c.v_stride;
+  a.cu_q = c.cu_q, a.cu_k = c.cu_k;
+  a.nseq = c.nseq, a.Hq = c.Hq, a.Hkv = c.Hkv, a.D = c.D;
+  a.scale_log2 = c.scale * kLog2e;
+  a.ntiles = p.ntiles, a.nsplit = p.nsplit, a.chunk = p.chunk;
+  a.o = c.o, a.lse = c.lse;
+  a.rows = c.Tq * c.Hq;
+  a.part_o = (float *)workspace;
+  a.part_lse = a.part_o + (int64_t)p.nsplit * a.rows * c.D;
+  return a;
+}
+
+int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+
+}  // namespace
+
+size_t attend_workspace(const AttendPlan &p, int64_t rows, int D) {
+  return p.nsplit > 1 ? (size_t)p.nsplit * rows * (D + 1) * sizeof(float) : 0;
+}
+
+AttendPlan plan_attend(const int32_t *cu_q, const int32_t *cu_k, int nseq, int Hq, int Hkv) {
+  const int64_t G = Hq / Hkv;
+  int64_t most_rows = 0, most_keys = 0;
+  for (int s = 0; s < nseq; ++s) {
+    const int64_t lq = cu_q[s + 1] - cu_q[s], lk = cu_k[s + 1] - cu_k[s];
+    if (lq > 0) most_rows = most_rows > lq * G ? most_rows : lq * G, most_keys = most_keys > lk ? most_keys : lk;
+  }
+  AttendPlan p;
+  p.form = most_rows <= 64 ? AttendPlan::kRows : AttendPlan::kTiles;
+  const int BQ = p.form == AttendPlan::kRows ? 32 : 256;
+  p.ntiles = tile_start(cu_q[nseq], nseq, (int)G, BQ);
+  // keys that all workgroups walk, without a split
+  int64_t walked = 0;
+  for (int s = 0; s < nseq; ++s) {
+    const int64_t lq = cu_q[s + 1] - cu_q[s], lk = cu_k[s + 1] - cu_k[s];
+    walked += (lq * G + BQ - 1) / BQ * lk * Hkv;
+  }
+  p.chunk = (int)round_up(walked / 512 > 1024 ? walked / 512 : 1024, 256);
+  p.nsplit = (int)((most_keys + p.chunk - 1) / p.chunk);
+  if (p.nsplit < 1) p.nsplit = 1;
+  if (p.nsplit == 1 || p.ntiles * Hkv >= 1024) p.nsplit = 1, p.chunk = 0x7FFFFF00;
+  return p;
+}
+
+AttendPlan plan_list(int64_t Tq, int nseq, int width, int Hq, int Hkv) {
+  AttendPlan p;
+  p.form = AttendPlan::kList;
+  p.ntiles = tile_start(Tq, nseq, 1, 1);
+  const int64_t wgs = Tq * Hkv * ((Hq / Hkv + 31) / 32);
+  const int64_t want = wgs > 0 ? (256 + wgs - 1) / wgs : 1;
+  p.chunk = width > 0 ? (int)round_up((width + want - 1) / want, 256) : 256;
+  p.nsplit = (int)((width + p.chunk - 1) / p.chunk);
+  if (p.nsplit <= 1) p.nsplit = 1, p.chunk = 0x7FFFFF00;
+  return p;
+}
+
+hipError_t launch_attend(const AttendCall &c, const AttendPlan &p, void *workspace, hipStream_t st) {
+  const AttendArgs a = make_args(c, p, workspace);
+  return c.D <= 64 ? launch_attend_t<64>(p, a, st) : launch_attend_t<128>(p, a, st);
+}
+
+hipError_t launch_attend_list(const AttendCall &c, const AttendPlan &p, const int32_t *ids, int width,
+                              void *workspace, hipStream_t st) {
+  AttendArgs a = make_args(c, p, workspace);
+  a.ids = ids, a.width = width;
+  return c.D <= 64 ? launch_list_t<64>(a, st) : launch_list_t<128>(a, st);
+}
+
+}  // namespace kpool

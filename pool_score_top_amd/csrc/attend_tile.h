@@ -1,0 +1,209 @@
+// Device pieces shared by the attention kernels (attend.hip, attend_bwd.hip): key tiles in
+// LDS, their loads and fragments, and where a workgroup's query rows sit.
+//
+// Query rows.  The G = Hq / Hkv query heads of one key head see the same keys, so the G
+// heads of the Lq tokens of a sequence form one axis of Lq * G "virtual" rows, row n being
+// head n % G of token n / G.  A tile of virtual rows then shares every key it reads among
+// the heads as well as the tokens, and one new token of a serving step fills G rows.
+//
+// Matrix products are v_mfma_f32_32x32x16_bf16.  Lane l holds of A row l % 32 and of B
+// column l % 32, each the 8 values k = 8 (l / 32) + j; of the result column l % 32 and rows
+// 8 (i / 4) + 4 (l / 32) + i % 4, i < 16.  A product whose result is the next one's B
+// operand (S^T = K Q^T, then O^T = V^T P^T) needs no exchange between lanes: registers
+// 8c .. 8c + 7 of the result are B for 16 of the contracted indexes, in the order
+// 4 h + {0..3}, 8 + 4 h + {0..3} of lane half h, and the A operand is read in that order.
+//
+// Key tiles in LDS.  A row of DP bf16 values is DP / 8 slots of 16 bytes; slot s holds chunk
+// s ^ swz(row).  Two kinds of reads have to be free of bank conflicts (64 banks, 256 bytes a
+// phase): 16-byte reads of one chunk of 32 rows, whose phases hold rows {0-3, 12-15, 20-27}
+// and {4-11, 16-19, 28-31}, and transposing 8-byte reads of 4 consecutive rows by 64 bytes.
+// The first needs swz to differ over a phase's rows (row % 16 does), the second needs the 4
+// rows' 64-byte blocks to differ, so the row's lowest bits go to the chunk's highest ones.
+#pragma once
+
+#include "kpool_internal.h"
+
+namespace kpool {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+
+#define KPOOL_LDS __attribute__((address_space(3)))
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int DP>
+struct Keys {
+  static_assert(DP == 64 || DP == 128, "padded head dims");
+  static constexpr int ROWB = DP * 2;            // bytes of a row
+  static constexpr int KS = DP / 16;             // contraction steps over the head dim
+  static constexpr int DT = DP / 32;             // 32-wide blocks of the head dim
+  static constexpr int REGION_ROWS = 1024 / ROWB;  // rows of one wave-wide 1 KiB load
+
+  static __device__ inline int swz(int row) {
+    const int r = DP == 128 ? row : row >> 1;
+    return DP == 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : ((r & 1) << 2) | ((r >> 1) & 3);
+  }
+  // byte of chunk 0's fragment for row l % 32, half l / 32; chunk step ks is ^ (ks << 5)
+  static __device__ inline uint32_t row_base(int lane) {
+    const int row = lane & 31;
+    return row * ROWB + (((lane >> 5) ^ swz(row)) << 4);
+  }
+  // byte of the transposing read of rows 4 h + {0..3} (+ 8 where second), columns 0..31;
+  // column block dt is ^ (dt << 6), 16 rows further down + 16 * ROWB
+  static __device__ inline uint32_t col_base(int lane, int second) {
+    const int i = lane & 15, g = lane >> 4;
+    const int row = 8 * second + 4 * (g >> 1) + (i >> 2);
+    const int chunk = (g & 1) * 2 + ((i & 3) >> 1);
+    return row * ROWB + ((chunk ^ swz(row)) << 4) + (i & 1) * 8;
+  }
+};
+
+__device__ inline uint32_t lds_offset(const void *p) {
+  return (uint32_t)(uintptr_t)(KPOOL_LDS const char *)p;
+}
+__device__ inline bf16x8 lds_read(uint32_t at) { return *(KPOOL_LDS const bf16x8 *)(uintptr_t)at; }
+
+// A operand for 16 contracted rows, transposed out of LDS: two reads of 4 rows each half
+__device__ inline bf16x8 lds_read_cols(uint32_t first, uint32_t second) {
+  typedef short i16x8 __attribute__((ext_vector_type(8)));
+  const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((KPOOL_LDS i16x4 *)(uintptr_t)first);
+  const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((KPOOL_LDS i16x4 *)(uintptr_t)second);
+  const i16x8 v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  return __builtin_bit_cast(bf16x8, v);
+}
+
+// A lane's addresses of the fragments of a key tile
+template <int DP>
+struct Frag {
+  using S = Keys<DP>;
+  uint32_t row[S::KS], col0[S::DT], col1[S::DT];
+  __device__ inline void init(uint32_t lds0, int lane) {
+    const uint32_t rb = S::row_base(lane), c0 = S::col_base(lane, 0), c1 = S::col_base(lane, 1);
+#pragma unroll
+    for (int ks = 0; ks < S::KS; ++ks) row[ks] = lds0 + (rb ^ (ks << 5));
+#pragma unroll
+    for (int dt = 0; dt < S::DT; ++dt) col0[dt] = lds0 + (c0 ^ (dt << 6)), col1[dt] = lds0 + (c1 ^ (dt << 6));
+  }
+  // rows l % 32 from `off` on, contraction step ks over the head dim
+  __device__ inline bf16x8 rows(uint32_t off, int ks) const { return lds_read(row[ks] + off); }
+  // columns 32 dt + l % 32, contraction over the 16 rows from `off` on
+  __device__ inline bf16x8 cols(uint32_t off, int dt) const {
+    return lds_read_cols(col0[dt] + off, col1[dt] + off);
+  }
+};
+
+__device__ inline f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// registers 8c .. 8c + 7 of a result as a B operand, each value rounded to bf16
+__device__ inline bf16x8 as_operand(const f32x16 &p, int c) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  const u32x4 v = {pack_bf16(p[8 * c], p[8 * c + 1]), pack_bf16(p[8 * c + 2], p[8 * c + 3]),
+                   pack_bf16(p[8 * c + 4], p[8 * c + 5]), pack_bf16(p[8 * c + 6], p[8 * c + 7])};
+  return __builtin_bit_cast(bf16x8, v);
+}
+
+// the same value from the other half of the wave (lane ^ 32)
+__device__ inline float other_half(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  // r[0] = [lo, lo], r[1] = [hi, hi]
+  return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+}
+
+// 2^x by the hardware's instruction (relative error about 2^-23; -inf gives 0)
+__device__ inline float exp2f_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+__device__ inline const void *uniform_ptr(const void *p) {
+  const uint64_t a = (uint64_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+  return (const void *)(((uint64_t)hi << 32) | lo);
+}
+
+// Reads key tiles of BK rows from memory straight into LDS, by NWAVES waves of which this is
+// `wave`.  Row r of a tile comes from its base + min(r, last) * stride, so a tile that ends
+// inside takes its last row again and every byte of LDS is a key's.  Chunks past D (head dims
+// below DP) take the row's last chunk: they meet zeros of the query.  A wave's load covers
+// REGION_ROWS rows; the rows' swizzles repeat every 16 rows, so loads 16 rows apart share
+// their lane offsets and the rest of the address is a scalar.
+template <int DP, int BK, int NWAVES>
+struct KeyLoader {
+  using S = Keys<DP>;
+  static constexpr int REGIONS = BK / S::REGION_ROWS;
+  static constexpr int PER = REGIONS / NWAVES;  // loads a wave
+  static constexpr int CYCLE = 16 / S::REGION_ROWS;  // regions after which the swizzle repeats
+  static constexpr int NOFF = PER < CYCLE ? PER : CYCLE;
+  // (with several waves, a wave's regions are NWAVES apart, and those share one swizzle)
+  static_assert(REGIONS % NWAVES == 0 && (NWAVES == 1 || NWAVES % CYCLE == 0), "regions of a wave");
+  static constexpr int NCOL = NWAVES == 1 ? NOFF : 1;
+  uint32_t col[NCOL];  // byte of the lane's chunk
+  int wave, lane;
+
+  __device__ inline void init(int wave_, int lane_, int D) {
+    wave = wave_, lane = lane_;
+#pragma unroll
+    for (int i = 0; i < NCOL; ++i) {
+      const int row = (wave + i) * S::REGION_ROWS + lane * 16 / S::ROWB;
+      col[i] = min((lane & (DP / 8 - 1)) ^ S::swz(row), D / 8 - 1) * 16;
+    }
+  }
+  // base and at are the same in every lane
+  __device__ inline void load(const uint16_t *base, int64_t stride, int last, unsigned char *at) const {
+#if defined(__HIP_DEVICE_COMPILE__)
+    const uint32_t pitch = (uint32_t)stride * 2;
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)uniform_ptr(base), 0, -1, 0x00020000);
+    const int sub = lane * 16 / S::ROWB;  // the lane's row of a region
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int region = wave + i * NWAVES;
+      const int row = min(region * S::REGION_ROWS + sub, last);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (KPOOL_LDS void *)(at + region * 1024), 16,
+                                               row * pitch + col[i % NCOL], 0, 0, 0);
+    }
+#endif
+  }
+};
+
+// Where a tile of virtual rows sits.  Tiles of BQ rows are numbered through the batch with
+// sequence s starting at tile cu_q[s] * G / BQ + s: that leaves room for ceil(Lq * G / BQ)
+// tiles each and needs no table (a sequence may leave its last number unused).
+struct TileAt {
+  int seq;           // -1: no such tile
+  int n0;            // its first virtual row
+  int q_start, k_start;
+  int Lq, Lk;
+};
+
+__host__ __device__ inline int64_t tile_start(int64_t cu, int s, int G, int BQ) {
+  return cu * G / BQ + s;
+}
+
+// All 64 lanes call it; the search probes 64 sequences at a time.
+__device__ inline TileAt find_tile(const int32_t *__restrict__ cu_q, const int32_t *__restrict__ cu_k,
+                                   int nseq, int G, int BQ, int64_t tile, int lane) {
+  int lo = 0, n = nseq;  // the answer is in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 63) / 64;
+    const int s = lo + lane * step;
+    const bool below = s < lo + n && tile_start(cu_q[min(s, nseq)], s, G, BQ) <= tile;
+    const int hits = __popcll(__ballot(below));
+    const int at = lo + (hits > 0 ? hits - 1 : 0) * step;
+    n = min(step, lo + n - at);
+    lo = at;
+  }
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  TileAt r;
+  const int q0 = cu_q[lo], q1 = cu_q[lo + 1], k0 = cu_k[lo], k1 = cu_k[lo + 1];
+  r.q_start = q0, r.k_start = k0, r.Lq = q1 - q0, r.Lk = k1 - k0;
+  const int64_t n0 = (tile - tile_start(q0, lo, G, BQ)) * BQ;
+  r.n0 = (int)n0;
+  r.seq = n0 < (int64_t)r.Lq * G ? lo : -1;  // (Lq * G fits 32 bits, checked by the host)
+  return r;
+}
+
+}  // namespace kpool

@@ -85,6 +85,30 @@ hipError_t launch_norm_bwd(bool f32, const void *dy, const void *x, int64_t x_st
                            const float *mean, const float *rstd, int64_t rows, int32_t N, void *dx,
                            float *dw, float *db, float *part, hipStream_t stream);
 
+// Attention (attend.hip).  A call's operands, its plan by the sizes alone, its workspace.
+struct AttendCall {
+  const uint16_t *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;  // elements between tokens
+  const int32_t *cu_q, *cu_k;            // device
+  int32_t nseq, Hq, Hkv, D;
+  int64_t Tq, Tk;
+  float scale;
+  uint16_t *o;
+  float *lse;
+};
+struct AttendPlan {
+  enum Form { kRows, kTiles, kList } form;
+  int64_t ntiles;  // tiles of query rows
+  int nsplit;      // parts of the key axis, joined by a second kernel where there are more than one
+  int chunk;       // keys of a part
+};
+AttendPlan plan_attend(const int32_t *cu_q, const int32_t *cu_k, int nseq, int Hq, int Hkv);
+AttendPlan plan_list(int64_t Tq, int nseq, int width, int Hq, int Hkv);
+size_t attend_workspace(const AttendPlan &p, int64_t rows, int D);
+hipError_t launch_attend(const AttendCall &c, const AttendPlan &p, void *workspace, hipStream_t st);
+hipError_t launch_attend_list(const AttendCall &c, const AttendPlan &p, const int32_t *ids, int width,
+                              void *workspace, hipStream_t st);
+
 // ----------------------------------------------------------------------------
 // Device helpers
 // ----------------------------------------------------------------------------

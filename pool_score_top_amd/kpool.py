@@ -55,6 +55,12 @@ def lib():
                                                     i64, i64, i32, u32, vp, vp, vp]),
         "kpool_expand": (ctypes.c_int, [vp, vp, vp, i32, i32, i64, i64, i32, u32, vp, vp]),
         "kpool_topk": (ctypes.c_int, [vp, i64, vp, i64, i32, vp, vp]),
+        "kpool_attend_workspace_bytes": (sz, [vp, vp, i32, i32, i32, i32]),
+        "kpool_attend": (ctypes.c_int, [vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i32, i32, i32, i32,
+                                        f32, vp, sz, vp, vp, vp]),
+        "kpool_attend_selected_workspace_bytes": (sz, [i64, i32, i32, i32, i32, i32]),
+        "kpool_attend_selected": (ctypes.c_int, [vp, i64, vp, i64, vp, i64, vp, i32, vp, vp, vp, vp, i32,
+                                                 i32, i32, i32, f32, vp, sz, vp, vp, vp]),
         "kpool_layer_norm": (ctypes.c_int, [vp, i64, vp, vp, i64, i32, f32, i32, vp, vp, vp, vp]),
         "kpool_layer_norm_backward_workspace_bytes": (sz, [i64, i32]),
         "kpool_layer_norm_backward": (ctypes.c_int, [vp, vp, i64, vp, vp, vp, i64, i32, i32, vp, sz,
@@ -282,28 +288,168 @@ def topk(scores, n_valid, budget: int, out=None, stream=None):
     return out
 
 
-def _on_device(t, stream):
-    """The stream for a call on t's device (the device's current one by default), with that
-    device made current for the launches: a context manager giving the stream's handle."""
-    import contextlib
+class _OnDevice:
+    """The call's stream (by default the current one of t's device) made current along with
+    t's device, so that outputs and workspaces allocated inside belong to that stream; gives
+    its handle."""
 
-    import torch
+    def __init__(self, t, stream):
+        self.device, self.stream = t.device, stream
+        self.contexts = []
 
-    @contextlib.contextmanager
-    def ctx():
-        with torch.cuda.device(t.device):
-            s = torch.cuda.current_stream() if stream is None else stream
-            if s.device != t.device:
-                raise ValueError(f"the stream is on {s.device}, the tensors on {t.device}")
-            with torch.cuda.stream(s):  # outputs and workspaces belong to the call's stream
-                yield ctypes.c_void_p(s.cuda_stream)
-    return ctx()
+    def __enter__(self):
+        import torch
+        if self.stream is None and torch.cuda.current_device() == self.device.index:
+            return torch.cuda.current_stream().cuda_stream
+        if self.stream is not None and self.stream.device != self.device:
+            raise ValueError(f"the stream is on {self.stream.device}, the tensors on {self.device}")
+        self.contexts = [torch.cuda.device(self.device)]
+        if self.stream is not None:
+            self.contexts.append(torch.cuda.stream(self.stream))
+        for c in self.contexts:
+            c.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
 
 
 def _like(t, name, shape, dtype, device):
     """An output or parameter given by the caller: contiguous, of this shape, type and device."""
     if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}")
+
+
+def _heads(t, name, device):
+    """t as packed tokens [T, H, D] of bf16 with any token stride: (T, H, D, stride)."""
+    import torch
+    if not t.is_cuda or t.dim() != 3 or t.device != device:
+        raise ValueError(f"{name} must be a device tensor [T, heads, D] on {device}")
+    if t.dtype not in (torch.bfloat16, torch.int16):
+        raise ValueError(f"{name} must be bfloat16 (or int16 bit patterns)")
+    T, H, D = t.shape
+    s = t.stride()
+    if (D > 1 and s[2] != 1) or (H > 1 and s[1] != D):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return T, H, D, s[0] if T > 1 else H * D
+
+
+def _cu_pair(cu_q, cu_q_dev, cu_k, cu_k_dev, device):
+    """Host arrays (and their pointers) and device copies of both lengths; no keys' lengths
+    given: the queries'."""
+    import torch
+    if (cu_k is None) != (cu_k_dev is None):
+        raise ValueError("give both cu_k and cu_k_dev, or neither")
+    cu_q, q_ptr = _host_i32(cu_q)
+    cu_k, k_ptr = (cu_q, q_ptr) if cu_k is None else _host_i32(cu_k)
+    cu_k_dev = cu_q_dev if cu_k_dev is None else cu_k_dev
+    if cu_q.ndim != 1 or len(cu_q) < 2 or cu_k.shape != cu_q.shape:
+        raise ValueError("cu_q and cu_k must be 1-dimensional with nseq + 1 entries each")
+    for t, name in ((cu_q_dev, "cu_q_dev"), (cu_k_dev, "cu_k_dev")):
+        _like(t, name, cu_q.shape, torch.int32, device)
+    return cu_q, q_ptr, cu_q_dev, cu_k, k_ptr, cu_k_dev
+
+
+class _Attend:
+    """The arguments that the attention calls share, checked."""
+
+    def __init__(self, q, k, v, cu_q, cu_q_dev, cu_k, cu_k_dev, scale):
+        self.device = q.device
+        tq, self.Hq, self.D, qs = _heads(q, "q", q.device)
+        tk, self.Hkv, d, ks = _heads(k, "k", q.device)
+        tv, hv, dv, vs = _heads(v, "v", q.device)
+        if (hv, dv) != (self.Hkv, self.D) or d != self.D:
+            raise ValueError("q, k and v must agree in D, and k and v in their heads")
+        self.cu_q, q_ptr, q_dev, self.cu_k, k_ptr, k_dev = _cu_pair(cu_q, cu_q_dev, cu_k, cu_k_dev, q.device)
+        self.nseq = len(self.cu_q) - 1
+        self.Tq, self.Tk = int(self.cu_q[-1]), int(self.cu_k[-1])
+        if tq < self.Tq or min(tk, tv) < self.Tk:
+            raise ValueError("q, k or v has fewer tokens than its cumulative lengths say")
+        self.scale = float(np.float32(1.0) / np.sqrt(np.float32(self.D))) if scale is None else scale
+        self.lens = (q_ptr, k_ptr, self.nseq, self.Hq, self.Hkv, self.D)
+        self.rows = (_p(q), qs, _p(k), ks, _p(v), vs)
+        self.cu = (q_ptr, _p(q_dev), k_ptr, _p(k_dev), self.nseq, self.Hq, self.Hkv, self.D, self.scale)
+
+    def outputs(self, q, out, lse, want_lse):
+        import torch
+        if out is None:
+            out = torch.empty((self.Tq, self.Hq, self.D), dtype=q.dtype, device=self.device)
+        else:
+            _like(out, "out", (self.Tq, self.Hq, self.D), q.dtype, self.device)
+        if lse is not None:
+            _like(lse, "lse", (self.Tq, self.Hq), torch.float32, self.device)
+        elif want_lse:
+            lse = torch.empty((self.Tq, self.Hq), dtype=torch.float32, device=self.device)
+        return out, lse
+
+    def scratch(self, workspace, nbytes):
+        import torch
+        if workspace is None and nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        return workspace
+
+
+def attend_workspace_bytes(cu_q, cu_k, Hq: int, Hkv: int, D: int) -> int:
+    """Workspace of attend for these sequences (0 where it needs none)."""
+    cu_q, qp = _host_i32(cu_q)
+    cu_k, kp = _host_i32(cu_k)
+    if cu_q.ndim != 1 or cu_k.shape != cu_q.shape:
+        raise ValueError("cu_q and cu_k must be 1-dimensional with nseq + 1 entries each")
+    nb = int(lib().kpool_attend_workspace_bytes(qp, kp, len(cu_q) - 1, Hq, Hkv, D))
+    msg = lib().kpool_last_error().decode()
+    if msg:
+        raise KpoolError("kpool_attend_workspace_bytes", KPOOL_EINVAL, msg)
+    return nb
+
+
+def attend(q, k, v, cu_q, cu_q_dev, cu_k=None, cu_k_dev=None, scale: float | None = None, out=None,
+           want_lse: bool = False, lse=None, workspace=None, stream=None):
+    """Causal attention of packed query rows over all the keys they see: (o, lse or None).
+
+    q bf16 [Tq, Hq, D], k and v bf16 [Tk, Hkv, D] (any token stride; each key head serves
+    Hq / Hkv query heads); cu_q, cu_k host arrays of nseq + 1 cumulative lengths and their
+    device copies, the keys' being the queries' where they are left out.  A sequence's queries
+    are the last rows of its keys.  scale is 1 / sqrt(D) by default."""
+    a = _Attend(q, k, v, cu_q, cu_q_dev, cu_k, cu_k_dev, scale)
+    with _OnDevice(q, stream) as s:
+        out, lse = a.outputs(q, out, lse, want_lse)
+        ws = a.scratch(workspace, int(lib().kpool_attend_workspace_bytes(*a.lens)))
+        rc = lib().kpool_attend(*a.rows, *a.cu, _p(ws), _bytes(ws, q.device), _p(out), _p(lse), s)
+    _check(rc, "kpool_attend")
+    return out, lse
+
+
+def attend_selected_workspace_bytes(Tq: int, nseq: int, width: int, Hq: int, Hkv: int, D: int) -> int:
+    """Workspace of attend_selected for these sizes (0 where it needs none)."""
+    nb = int(lib().kpool_attend_selected_workspace_bytes(Tq, nseq, width, Hq, Hkv, D))
+    msg = lib().kpool_last_error().decode()
+    if msg:
+        raise KpoolError("kpool_attend_selected_workspace_bytes", KPOOL_EINVAL, msg)
+    return nb
+
+
+def attend_selected(q, k, v, token_ids, cu_q, cu_q_dev, cu_k=None, cu_k_dev=None,
+                    scale: float | None = None, out=None, want_lse: bool = False, lse=None,
+                    workspace=None, stream=None):
+    """Attention of packed query rows over the tokens each selected: (o, lse or None).
+
+    token_ids int32 [Tq, width]: sequence-local token ids as expand gives them; entries that
+    are negative or past the row stand for nothing.  The rest is attend's."""
+    import torch
+    a = _Attend(q, k, v, cu_q, cu_q_dev, cu_k, cu_k_dev, scale)
+    if token_ids.dim() != 2:
+        raise ValueError("token_ids must be [Tq, width]")
+    width = token_ids.shape[1]
+    _like(token_ids, "token_ids", (a.Tq, width), torch.int32, q.device)
+    with _OnDevice(q, stream) as s:
+        out, lse = a.outputs(q, out, lse, want_lse)
+        ws = a.scratch(workspace, int(lib().kpool_attend_selected_workspace_bytes(
+            a.Tq, a.nseq, width, a.Hq, a.Hkv, a.D)))
+        rc = lib().kpool_attend_selected(*a.rows, _p(token_ids), width, *a.cu, _p(ws),
+                                         _bytes(ws, q.device), _p(out), _p(lse), s)
+    _check(rc, "kpool_attend_selected")
+    return out, lse
 
 
 def _norm_rows(x, name):
@@ -333,7 +479,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, want_stat
             _like(t, name, (N,), torch.float32, x.device)
     if out is not None:
         _like(out, "out", (rows, N), x.dtype, x.device)
-    with _on_device(x, stream) as s:
+    with _OnDevice(x, stream) as s:
         if out is None:
             out = torch.empty((rows, N), dtype=x.dtype, device=x.device)
         mean = rstd = None
@@ -359,7 +505,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, want_dx: bool = True, want_dw
     _like(rstd, "rstd", (rows,), torch.float32, x.device)
     if not (want_dx or want_dweight or want_dbias):
         raise ValueError("no output is wanted")
-    with _on_device(x, stream) as s:
+    with _OnDevice(x, stream) as s:
         f32 = dict(dtype=torch.float32, device=x.device)
         dx = torch.empty((rows, N), dtype=x.dtype, device=x.device) if want_dx else None
         dw = torch.empty(N, **f32) if want_dweight else None
