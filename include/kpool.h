@@ -270,7 +270,28 @@ int kpool_attend(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t
                  int32_t nseq, int32_t Hq, int32_t Hkv, int32_t D, float scale, void *workspace,
                  size_t workspace_bytes, uint16_t *o, float *lse, void *stream);
 
-/* The same over the tokens a row selected: row i sees the tokens token_ids[i, 0 .. width)
+/* Gradients of kpool_attend.  With P = exp(scale * q k^T - lse) over what a row sees and
+ * delta[i,h] = <d_o[i,h,:], o[i,h,:]>:
+ *   dv[j] = sum_i P[i,j] d_o[i]        dS[i,j] = P[i,j] (<d_o[i], v[j]> - delta[i])
+ *   dk[j] = scale sum_i dS[i,j] q[i]   dq[i] = scale sum_j dS[i,j] k[j]
+ * where dk and dv of a key head sum over its Hq / Hkv query heads.
+ *   d_o, o   bf16 [Tq, Hq, D] contiguous; o and lse (fp32 [Tq, Hq]) from kpool_attend
+ *   dq       bf16 [Tq, Hq, D];  dk, dv  bf16 [Tk, Hkv, D], contiguous, overwritten (0 for a
+ *            row that sees nothing and a key that no row sees)
+ *   workspace  kpool_attend_backward_workspace_bytes bytes, 16-byte aligned; scratch
+ * The other arguments are the forward call's, and d_o must be finite as well.  Sums are fp32
+ * in a fixed order (no atomics): the same call gives the same bits. */
+size_t kpool_attend_backward_workspace_bytes(const int32_t *cu_q_host, const int32_t *cu_k_host,
+                                             int32_t nseq, int32_t Hq, int32_t Hkv, int32_t D);
+int kpool_attend_backward(const uint16_t *d_o, const uint16_t *q, int64_t q_stride, const uint16_t *k,
+                          int64_t k_stride, const uint16_t *v, int64_t v_stride, const uint16_t *o,
+                          const float *lse, const int32_t *cu_q_host, const int32_t *cu_q_dev,
+                          const int32_t *cu_k_host, const int32_t *cu_k_dev, int32_t nseq, int32_t Hq,
+                          int32_t Hkv, int32_t D, float scale, void *workspace,
+                          size_t workspace_bytes, uint16_t *dq, uint16_t *dk, uint16_t *dv,
+                          void *stream);
+
+/* kpool_attend over the tokens a row selected: row i sees the tokens token_ids[i, 0 .. width)
  * that lie in 0 .. t(i) (kpool_expand's output; other entries, -1 among them, stand for
  * nothing, wherever they are in the list).  A token that is listed twice counts twice.
  *   token_ids  int32 [Tq, width], sequence-local token ids, any order

@@ -661,6 +661,50 @@ int kpool_attend(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t
   return ok();
 }
 
+size_t kpool_attend_backward_workspace_bytes(const int32_t *cu_q_host, const int32_t *cu_k_host,
+                                             int32_t nseq, int32_t Hq, int32_t Hkv, int32_t D) {
+  const char *fn = "kpool_attend_backward_workspace_bytes";
+  if (check_heads(fn, Hq, Hkv, D) || check_lengths(fn, cu_q_host, cu_k_host, nseq, Hq / Hkv)) return 0;
+  ok();
+  return kpool::attend_bwd_workspace(kpool::plan_attend_bwd(cu_q_host, cu_k_host, nseq, Hq, Hkv),
+                                     cu_q_host[nseq], cu_k_host[nseq], Hq, Hkv, D);
+}
+
+int kpool_attend_backward(const uint16_t *d_o, const uint16_t *q, int64_t q_stride, const uint16_t *k,
+                          int64_t k_stride, const uint16_t *v, int64_t v_stride, const uint16_t *o,
+                          const float *lse, const int32_t *cu_q_host, const int32_t *cu_q_dev,
+                          const int32_t *cu_k_host, const int32_t *cu_k_dev, int32_t nseq, int32_t Hq,
+                          int32_t Hkv, int32_t D, float scale, void *workspace,
+                          size_t workspace_bytes, uint16_t *dq, uint16_t *dk, uint16_t *dv,
+                          void *stream) {
+  const char *fn = "kpool_attend_backward";
+  kpool::AttendCall c{q, k, v, q_stride, k_stride, v_stride, cu_q_dev, cu_k_dev, nseq, Hq, Hkv, D,
+                      0, 0, scale, const_cast<uint16_t *>(o), const_cast<float *>(lse)};
+  int rc = check_attend(fn, c, cu_q_host, cu_k_host);
+  if (rc) return rc;
+  if (c.Tq == 0 && c.Tk == 0) return ok();
+  if (!cu_q_dev || !cu_k_dev || (c.Tq > 0 && (!d_o || !lse || !dq)) || (c.Tk > 0 && (!dk || !dv)))
+    return fail(KPOOL_EINVAL, "%s: null pointer", fn);
+  if (!aligned16(d_o) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
+    return fail(KPOOL_EINVAL, "%s: d_o, dq, dk and dv must be 16-byte aligned", fn);
+  const kpool::BwdPlan p = kpool::plan_attend_bwd(cu_q_host, cu_k_host, nseq, Hq, Hkv);
+  const int64_t most = int64_t(1) << 23, sums = std::max(c.Tq * Hq, c.Tk * Hkv) * D / 1024;
+  if (p.ktiles * p.ksplit * Hkv >= most || p.qtiles * p.qsplit * Hkv >= most || c.Tq * Hq / 16 >= most ||
+      sums >= most)
+    return fail(KPOOL_EUNSUPPORTED, "%s: too many rows for one launch", fn);
+  const size_t need = kpool::attend_bwd_workspace(p, c.Tq, c.Tk, Hq, Hkv, D);
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(KPOOL_EWORKSPACE, "%s: needs %zu bytes of workspace, got %zu", fn, need,
+                workspace ? workspace_bytes : (size_t)0);
+  if (!aligned16(workspace)) return fail(KPOOL_EINVAL, "%s: workspace must be 16-byte aligned", fn);
+  hipStream_t st = (hipStream_t)stream;
+  hipError_t e = timed(6, st, [&] {
+    return kpool::launch_attend_bwd(c, d_o, p, workspace, dq, dk, dv, st);
+  });
+  if (e != hipSuccess) return hip_fail(fn, e);
+  return ok();
+}
+
 size_t kpool_attend_selected_workspace_bytes(int64_t Tq, int32_t nseq, int32_t width, int32_t Hq,
                                              int32_t Hkv, int32_t D) {
   const char *fn = "kpool_attend_selected_workspace_bytes";

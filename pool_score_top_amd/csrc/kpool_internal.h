@@ -109,6 +109,17 @@ hipError_t launch_attend(const AttendCall &c, const AttendPlan &p, void *workspa
 hipError_t launch_attend_list(const AttendCall &c, const AttendPlan &p, const int32_t *ids, int width,
                               void *workspace, hipStream_t st);
 
+// Its gradients (attend_bwd.hip); c.o and c.lse are the forward pass's.
+struct BwdPlan {
+  int64_t ktiles, qtiles;  // tiles of keys, of query rows
+  int ksplit, qsplit;      // parts of the rows (dK, dV) and of the keys (dQ)
+  int kchunk, qchunk;
+};
+BwdPlan plan_attend_bwd(const int32_t *cu_q, const int32_t *cu_k, int nseq, int Hq, int Hkv);
+size_t attend_bwd_workspace(const BwdPlan &p, int64_t Tq, int64_t Tk, int Hq, int Hkv, int D);
+hipError_t launch_attend_bwd(const AttendCall &c, const uint16_t *d_o, const BwdPlan &p, void *workspace,
+                             uint16_t *dq, uint16_t *dk, uint16_t *dv, hipStream_t st);
+
 // ----------------------------------------------------------------------------
 // Device helpers
 // ----------------------------------------------------------------------------

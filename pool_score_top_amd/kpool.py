@@ -58,6 +58,9 @@ def lib():
         "kpool_attend_workspace_bytes": (sz, [vp, vp, i32, i32, i32, i32]),
         "kpool_attend": (ctypes.c_int, [vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i32, i32, i32, i32,
                                         f32, vp, sz, vp, vp, vp]),
+        "kpool_attend_backward_workspace_bytes": (sz, [vp, vp, i32, i32, i32, i32]),
+        "kpool_attend_backward": (ctypes.c_int, [vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp,
+                                                 i32, i32, i32, i32, f32, vp, sz, vp, vp, vp, vp]),
         "kpool_attend_selected_workspace_bytes": (sz, [i64, i32, i32, i32, i32, i32]),
         "kpool_attend_selected": (ctypes.c_int, [vp, i64, vp, i64, vp, i64, vp, i32, vp, vp, vp, vp, i32,
                                                  i32, i32, i32, f32, vp, sz, vp, vp, vp]),
@@ -390,17 +393,21 @@ class _Attend:
         return workspace
 
 
-def attend_workspace_bytes(cu_q, cu_k, Hq: int, Hkv: int, D: int) -> int:
-    """Workspace of attend for these sequences (0 where it needs none)."""
+def _attend_bytes(fn, cu_q, cu_k, Hq, Hkv, D):
     cu_q, qp = _host_i32(cu_q)
     cu_k, kp = _host_i32(cu_k)
     if cu_q.ndim != 1 or cu_k.shape != cu_q.shape:
         raise ValueError("cu_q and cu_k must be 1-dimensional with nseq + 1 entries each")
-    nb = int(lib().kpool_attend_workspace_bytes(qp, kp, len(cu_q) - 1, Hq, Hkv, D))
+    nb = int(getattr(lib(), fn)(qp, kp, len(cu_q) - 1, Hq, Hkv, D))
     msg = lib().kpool_last_error().decode()
     if msg:
-        raise KpoolError("kpool_attend_workspace_bytes", KPOOL_EINVAL, msg)
+        raise KpoolError(fn, KPOOL_EINVAL, msg)
     return nb
+
+
+def attend_workspace_bytes(cu_q, cu_k, Hq: int, Hkv: int, D: int) -> int:
+    """Workspace of attend for these sequences (0 where it needs none)."""
+    return _attend_bytes("kpool_attend_workspace_bytes", cu_q, cu_k, Hq, Hkv, D)
 
 
 def attend(q, k, v, cu_q, cu_q_dev, cu_k=None, cu_k_dev=None, scale: float | None = None, out=None,
@@ -418,6 +425,37 @@ def attend(q, k, v, cu_q, cu_q_dev, cu_k=None, cu_k_dev=None, scale: float | Non
         rc = lib().kpool_attend(*a.rows, *a.cu, _p(ws), _bytes(ws, q.device), _p(out), _p(lse), s)
     _check(rc, "kpool_attend")
     return out, lse
+
+
+def attend_backward_workspace_bytes(cu_q, cu_k, Hq: int, Hkv: int, D: int) -> int:
+    """Workspace of attend_backward for these sequences."""
+    return _attend_bytes("kpool_attend_backward_workspace_bytes", cu_q, cu_k, Hq, Hkv, D)
+
+
+def attend_backward(d_o, q, k, v, o, lse, cu_q, cu_q_dev, cu_k=None, cu_k_dev=None,
+                    scale: float | None = None, workspace=None, dq=None, dk=None, dv=None, stream=None):
+    """Gradients (dq, dk, dv) of attend: d_o is the gradient of o [Tq, Hq, D]; o and lse are what
+    attend returned (want_lse=True); the rest are its arguments.  dq is [Tq, Hq, D], dk and dv
+    [Tk, Hkv, D], in bf16."""
+    import torch
+    a = _Attend(q, k, v, cu_q, cu_q_dev, cu_k, cu_k_dev, scale)
+    rows = (a.Tq, a.Hq, a.D)
+    _like(d_o, "d_o", rows, q.dtype, q.device)
+    _like(o, "o", rows, q.dtype, q.device)
+    _like(lse, "lse", rows[:2], torch.float32, q.device)
+    with _OnDevice(q, stream) as s:
+        out = []
+        for t, name, shape in ((dq, "dq", rows), (dk, "dk", (a.Tk, a.Hkv, a.D)), (dv, "dv", (a.Tk, a.Hkv, a.D))):
+            if t is None:
+                t = torch.empty(shape, dtype=q.dtype, device=q.device)
+            else:
+                _like(t, name, shape, q.dtype, q.device)
+            out.append(t)
+        ws = a.scratch(workspace, int(lib().kpool_attend_backward_workspace_bytes(*a.lens)))
+        rc = lib().kpool_attend_backward(_p(d_o), *a.rows, _p(o), _p(lse), *a.cu, _p(ws),
+                                         _bytes(ws, q.device), *(_p(t) for t in out), s)
+    _check(rc, "kpool_attend_backward")
+    return tuple(out)
 
 
 def attend_selected_workspace_bytes(Tq: int, nseq: int, width: int, Hq: int, Hkv: int, D: int) -> int:

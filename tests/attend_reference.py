@@ -97,3 +97,48 @@ def cu_of(lens):
     import numpy as np
     cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
     return cu, torch.from_numpy(cu).cuda()
+
+
+def check_backward(q, k, v, d_o, o, lse, cu_q, cu_k, scale, dq, dk, dv):
+    """The gradients of every sequence and key head against the formulas in 64 bits with the
+    given o and lse (as the backward pass has them).
+
+    P = exp(s - lse) has the relative error ep = 4 e + 16 u (1 + |lse|); dP and delta are sums
+    of D products (D + 8) u; dS = P (dP - delta) carries both and is rounded to bf16 (h) for
+    its products, as P is; sums over n rows or keys add n u, the outputs' rounding h.
+
+    Below 2^-126, the smallest normal number of fp32 and bf16, the hardware's 2^x and the
+    matrix products give 0 (no subnormals), whatever the relative bounds say: P, dS and each
+    output are off by up to that much on top, P's part reaching dS through |dP - delta|."""
+    G = q.shape[1] // k.shape[1]
+    D = q.shape[2]
+    for a, b, c, d in sequences(cu_q, cu_k):
+        lq, lk = b - a, d - c
+        if lk == 0:
+            assert (dq[a:b] == 0).all()
+            continue
+        seen = (causal_counts(lq, lk) > 0).repeat_interleave(G, 0)
+        for g in range(k.shape[1]):
+            hs = slice(g * G, g * G + G)
+            rows = lambda t: t[a:b, hs].double().reshape(lq * G, D)
+            qq, oo, ee = rows(q), rows(o), rows(d_o)
+            kk, vv = k[c:d, g].double(), v[c:d, g].double()
+            l64 = lse[a:b, hs].double().reshape(-1, 1)
+            p = torch.where(seen, (scale * (qq @ kk.t()) - l64.clamp(min=-1e30)).exp(), 0.0)
+            e = torch.where(seen, scale * (qq.abs() @ kk.abs().t()) * (D + 8) * U, 0.0).amax(1, keepdim=True) \
+                if lq else p.sum(1, keepdim=True)
+            ep = 4 * e + 16 * U * (1 + l64.abs().clamp(max=1e30) * (l64 > -math.inf))
+            dp, delta = ee @ vv.t(), (ee * oo).sum(1, keepdim=True)
+            ds = p * (dp - delta)
+            e2 = (D + 8) * U * (ee.abs() @ vv.abs().t() + (ee * oo).abs().sum(1, keepdim=True))
+            n = (lq * G + lk + 64) * U
+            tiny = 2.0 ** -126
+            bp = p * (H + ep + 2 * n) + tiny * seen
+            bs = ds.abs() * (H + ep + 2 * n) + 2 * p * e2 + tiny * (1 + (dp - delta).abs()) * seen
+            for got, ref, bound in (
+                    (dv[c:d, g].double(), p.t() @ ee, bp.t() @ ee.abs()),
+                    (dk[c:d, g].double(), scale * ds.t() @ qq, scale * bs.t() @ qq.abs()),
+                    (rows(dq), scale * ds @ kk, scale * bs @ kk.abs())):
+                tol = bound + H * (ref.abs() + bound) + tiny
+                err = (got - ref).abs()
+                assert (err <= tol).all(), (a, g, float((err - tol).max()))
