@@ -648,7 +648,8 @@ int kpool_attend(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t
                  int32_t nseq, int32_t Hq, int32_t Hkv, int32_t D, float scale, void *workspace,
                  size_t workspace_bytes, uint16_t *o, float *lse, void *stream) {
   const char *fn = "kpool_attend";
-  kpool::AttendCall c{q, k, v, q_stride, k_stride, v_stride, cu_q_dev, cu_k_dev, nseq, Hq, Hkv, D,
+  kpool::AttendCall c{q, k, v, q_stride, k_stride, v_stride, cu_q_dev, cu_k_dev, cu_q_host,
+                      cu_k_host, nseq, Hq, Hkv, D,
                       0, 0, scale, o, lse};
   int rc = check_attend(fn, c, cu_q_host, cu_k_host);
   if (rc || c.Tq == 0) return rc;
@@ -678,7 +679,8 @@ int kpool_attend_backward(const uint16_t *d_o, const uint16_t *q, int64_t q_stri
                           size_t workspace_bytes, uint16_t *dq, uint16_t *dk, uint16_t *dv,
                           void *stream) {
   const char *fn = "kpool_attend_backward";
-  kpool::AttendCall c{q, k, v, q_stride, k_stride, v_stride, cu_q_dev, cu_k_dev, nseq, Hq, Hkv, D,
+  kpool::AttendCall c{q, k, v, q_stride, k_stride, v_stride, cu_q_dev, cu_k_dev, cu_q_host,
+                      cu_k_host, nseq, Hq, Hkv, D,
                       0, 0, scale, const_cast<uint16_t *>(o), const_cast<float *>(lse)};
   int rc = check_attend(fn, c, cu_q_host, cu_k_host);
   if (rc) return rc;
@@ -725,7 +727,8 @@ int kpool_attend_selected(const uint16_t *q, int64_t q_stride, const uint16_t *k
                           size_t workspace_bytes, uint16_t *o, float *lse, void *stream) {
   const char *fn = "kpool_attend_selected";
   if (width < 0 || width > (1 << 30)) return fail(KPOOL_EINVAL, "%s: width must be in [0, 2^30] (got %d)", fn, width);
-  kpool::AttendCall c{q, k, v, q_stride, k_stride, v_stride, cu_q_dev, cu_k_dev, nseq, Hq, Hkv, D,
+  kpool::AttendCall c{q, k, v, q_stride, k_stride, v_stride, cu_q_dev, cu_k_dev, cu_q_host,
+                      cu_k_host, nseq, Hq, Hkv, D,
                       0, 0, scale, o, lse};
   int rc = check_attend(fn, c, cu_q_host, cu_k_host);
   if (rc || c.Tq == 0) return rc;

@@ -24,6 +24,11 @@
 namespace kpool {
 namespace {
 
+#ifndef KPOOL_TW
+#define KPOOL_TW 8
+#endif
+constexpr int kTileWaves = KPOOL_TW;
+
 struct AttendArgs {
   const uint16_t *q, *k, *v;
   int64_t qs, ks, vs;  // elements between tokens
@@ -39,6 +44,7 @@ struct AttendArgs {
   float *lse;
   float *part_o, *part_lse;  // [nsplit][Tq * Hq][D], [nsplit][Tq * Hq]
   int64_t rows;              // Tq * Hq
+  TileTable table;
 };
 
 // One wave's 32 query rows: fragments, running softmax and output.
@@ -73,11 +79,17 @@ struct Rows {
                              F &&visible) {
     constexpr int SUBS = BK / 32;
     f32x16 s[SUBS];
+    bf16x8 kr[SUBS][S::KS];
+#pragma unroll
+    for (int sub = 0; sub < SUBS; ++sub)
+#pragma unroll
+      for (int ks = 0; ks < S::KS; ++ks) kr[sub][ks] = f.rows(sk + sub * 32 * S::ROWB, ks);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int sub = 0; sub < SUBS; ++sub) {
       f32x16 t = {};
 #pragma unroll
-      for (int ks = 0; ks < S::KS; ++ks) t = mfma(f.rows(sk + sub * 32 * S::ROWB, ks), q[ks], t);
+      for (int ks = 0; ks < S::KS; ++ks) t = mfma(kr[sub][ks], q[ks], t);
       s[sub] = t;
     }
     if (masked) {
@@ -170,8 +182,7 @@ __global__ __launch_bounds__(NW * 64) void attend_tile_kernel(AttendArgs a) {
   const int kvh = (int)(idx % a.Hkv);
   idx /= a.Hkv;
   const int split = (int)(idx % a.nsplit);
-  // (the last tiles of a sequence see the most keys and go first)
-  const TileAt at = find_tile(a.cu_q, a.cu_k, a.nseq, G, BQ, a.ntiles - 1 - idx / a.nsplit, lane);
+  const TileAt at = find_tile(a.table, a.cu_q, a.cu_k, a.nseq, G, BQ, idx / a.nsplit, a.ntiles, lane);
   if (at.seq < 0) return;
   const int nrows = min(BQ, at.Lq * G - at.n0);
   const int t1 = (at.n0 + nrows - 1) / G + at.Lk - at.Lq;  // the last row's position
@@ -191,28 +202,30 @@ __global__ __launch_bounds__(NW * 64) void attend_tile_kernel(AttendArgs a) {
   Rows<DP> r;
   r.init(live ? a.q + ((int64_t)at.q_start + tok) * a.qs + (int64_t)head * a.D : nullptr, a.D, lane);
   
+  const uint32_t lds0 = lds_offset(lds);
   Frag<DP> f;
-  f.init(lds_offset(lds), lane);
+  f.init(lds0, lane);
   KeyLoader<DP, BK, NW> keys;
   keys.init(wave, lane, a.D);
   const int ntile = k_hi > k_lo ? (k_hi - k_lo + BK - 1) / BK : 0;
   auto load = [&](int tile, int buf) {
     const int k0 = k_lo + tile * BK;
-    keys.load(kb + (int64_t)k0 * a.ks, a.ks, at.Lk - 1 - k0, lds + buf * 2 * TILE);
-    keys.load(vb + (int64_t)k0 * a.vs, a.vs, at.Lk - 1 - k0, lds + buf * 2 * TILE + TILE);
+    keys.load(kb + (int64_t)k0 * a.ks, a.ks, at.Lk - 1 - k0, lds0 + buf * 2 * TILE);
+    keys.load(vb + (int64_t)k0 * a.vs, a.vs, at.Lk - 1 - k0, lds0 + buf * 2 * TILE + TILE);
   };
   auto step = [&](int j, auto buf_c) {
     constexpr int BUF = decltype(buf_c)::value;
     // this wave's part of tile j has landed; behind the barrier everyone's has, and everyone
     // is done with the buffer that tile j + 1 goes to
     __builtin_amdgcn_s_waitcnt(0x0F70);
-    __syncthreads();
+    barrier_only();
     if (j + 1 < ntile) load(j + 1, BUF ^ 1);
     const int k0 = k_lo + j * BK;
     if (k0 <= w1)  // (the whole wave; not where it sees none of the tile, or has no rows)
       r.template add<BK>(f, BUF * 2 * TILE, BUF * 2 * TILE + TILE, a.scale_log2, lane, k0 + BK - 1 > w0,
                          [&](int sub, int i) { return k0 + sub * 32 + i <= t; });
   };
+  wait_loads();
   if (ntile > 0) load(0, 0);
   for (int j = 0; j < ntile; j += 2) {
     step(j, std::integral_constant<int, 0>{});
@@ -245,10 +258,9 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendArgs a) {
     const int per = (G + 31) / 32;
     const int64_t token = idx / per;
     first = (int)(idx - token * per) * 32;
-    at = find_tile(a.cu_q, a.cu_k, a.nseq, 1, 1, token, lane);
-    (void)token;
+    at = find_tile(a.table, a.cu_q, a.cu_k, a.nseq, 1, 1, token, a.ntiles, lane);
   } else {
-    at = find_tile(a.cu_q, a.cu_k, a.nseq, G, 32, a.ntiles - 1 - idx, lane);
+    at = find_tile(a.table, a.cu_q, a.cu_k, a.nseq, G, 32, idx, a.ntiles, lane);
   }
   if (at.seq < 0) return;
   int tok, head, nrows;
@@ -270,9 +282,9 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendArgs a) {
 
   const uint16_t *kb = (const uint16_t *)uniform_ptr(a.k + (int64_t)at.k_start * a.ks + (int64_t)kvh * a.D);
   const uint16_t *vb = (const uint16_t *)uniform_ptr(a.v + (int64_t)at.k_start * a.vs + (int64_t)kvh * a.D);
-  unsigned char *mine = lds + wave * 4 * TILE;
+  const uint32_t mine = lds_offset(lds) + wave * 4 * TILE;
   Frag<DP> f;
-  f.init(lds_offset(mine), lane);
+  f.init(mine, lane);
   KeyLoader<DP, BK, 1> keys;
   keys.init(0, lane, a.D);
   // the last key (or list entry) of any row of the tile, and of every row
@@ -296,20 +308,14 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendArgs a) {
   // 2 * BK / REGION_ROWS loads of 1 KiB a tile
   constexpr int REGIONS = BK / S::REGION_ROWS;
   auto load_list = [&](int id, int buf) {
-#if defined(__HIP_DEVICE_COMPILE__)
 #pragma unroll
     for (int i = 0; i < REGIONS; ++i) {
       const int row = i * S::REGION_ROWS + lane * 16 / S::ROWB;
       const int chunk = min((lane & (DP / 8 - 1)) ^ S::swz(row), a.D / 8 - 1);
       const int64_t key = __shfl(id, row);
-      __builtin_amdgcn_global_load_lds(
-          (const __attribute__((address_space(1))) void *)(kb + key * a.ks + chunk * 8),
-          (KPOOL_LDS void *)(mine + buf * 2 * TILE + i * 1024), 16, 0, 0);
-      __builtin_amdgcn_global_load_lds(
-          (const __attribute__((address_space(1))) void *)(vb + key * a.vs + chunk * 8),
-          (KPOOL_LDS void *)(mine + buf * 2 * TILE + TILE + i * 1024), 16, 0, 0);
+      load_lds_16(kb + key * a.ks + chunk * 8, mine + buf * 2 * TILE + i * 1024);
+      load_lds_16(vb + key * a.vs + chunk * 8, mine + buf * 2 * TILE + TILE + i * 1024);
     }
-#endif
   };
   auto load = [&](int k0, int buf) {
     keys.load(kb + (int64_t)k0 * a.ks, a.ks, at.Lk - 1 - k0, mine + buf * 2 * TILE);
@@ -317,6 +323,7 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendArgs a) {
   };
   uint32_t there = 0, there_next = 0;
   int k0 = k_lo + wave * BK, buf = 0;
+  wait_loads();
   if (k0 < k_hi) {
     if (LIST) {
       const int id = entries(k0, there);
@@ -429,47 +436,50 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendArgs a) {
   }
 }
 
-// Joins the splits of a row: o = sum_s 2^(lse_s - lse) o_s.  A wave per row; a split that
-// saw nothing has lse -inf and was not written, so it is not read.
+// Joins the splits of a row: o = sum_s 2^(lse_s - lse) o_s.  A wave per row; 16 splits at a
+// time, whose loads go out together.  A split that saw nothing has lse -inf and was not
+// written: its weight is 0 and it is not read.
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   if (row >= a.rows) return;
-  float m = -__builtin_inff();
+  const float none = -__builtin_inff();
+  float m = none;
   for (int s = lane; s < a.nsplit; s += 64) m = fmaxf(m, a.part_lse[(int64_t)s * a.rows + row]);
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-  const float shift = m > -__builtin_inff() ? m : 0.0f;
+  const float shift = m > none ? m : 0.0f;
   float total = 0.0f, o0 = 0.0f, o1 = 0.0f;
-  const int d = lane * 2;
-  for (int s = 0; s < a.nsplit; ++s) {
-    const float part = a.part_lse[(int64_t)s * a.rows + row];
-    if (!(part > -__builtin_inff())) continue;
-    const float w = exp2f_fast((part - shift) * kLog2e);
-    total += w;
-    if (d < a.D) {
-      const float2 v = *reinterpret_cast<const float2 *>(a.part_o + ((int64_t)s * a.rows + row) * a.D + d);
-      o0 = fmaf(w, v.x, o0);
-      o1 = fmaf(w, v.y, o1);
+  const int d = min(lane * 2, a.D - 2);
+  for (int s0 = 0; s0 < a.nsplit; s0 += 16) {
+    // lane s: the weight of split s0 + s
+    const int mine = s0 + (lane & 15);
+    float w = mine < a.nsplit ? a.part_lse[(int64_t)mine * a.rows + row] : none;
+    w = w > none ? exp2f_fast((w - shift) * kLog2e) : 0.0f;
+    float2 v[16];
+#pragma unroll
+    for (int s = 0; s < 16; ++s) {
+      v[s] = make_float2(0.0f, 0.0f);
+      if (__builtin_amdgcn_readlane(__float_as_uint(w), s) != 0)  // (the same for the wave)
+        v[s] = *reinterpret_cast<const float2 *>(a.part_o + ((int64_t)(s0 + s) * a.rows + row) * a.D + d);
+    }
+#pragma unroll
+    for (int s = 0; s < 16; ++s) {
+      const float ws = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), s));
+      total += ws;
+      o0 = fmaf(ws, v[s].x, o0);
+      o1 = fmaf(ws, v[s].y, o1);
     }
   }
   const float inv = total > 0.0f ? 1.0f / total : 0.0f;
-  if (d < a.D) *reinterpret_cast<uint32_t *>(a.o + row * a.D + d) = pack_bf16(o0 * inv, o1 * inv);
-  if (lane == 0 && a.lse) a.lse[row] = total > 0.0f ? shift + log2f(total) * kLn2 : -__builtin_inff();
+  if (lane * 2 < a.D)
+    *reinterpret_cast<uint32_t *>(a.o + row * a.D + d) = pack_bf16(o0 * inv, o1 * inv);
+  if (lane == 0 && a.lse) a.lse[row] = total > 0.0f ? shift + log2f(total) * kLn2 : none;
 }
-
 
 hipError_t launch_join(const AttendArgs &a, hipStream_t st) {
   hipLaunchKernelGGL(attend_join_kernel, dim3((unsigned)((a.rows + 3) / 4)), dim3(256), 0, st, a);
   return hipGetLastError();
-}
-
-template <class F>
-hipError_t with_lds(F *kernel, size_t bytes) {
-  // (a launch may use more than 64 KiB of LDS only where the kernel was told so)
-  return bytes > 65536 ? hipFuncSetAttribute((const void *)kernel,
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)
-                       : hipSuccess;
 }
 
 template <int DP>
@@ -483,9 +493,9 @@ hipError_t launch_attend_t(const AttendPlan &p, const AttendArgs &a, hipStream_t
     hipLaunchKernelGGL((attend_rows_kernel<DP, false>), dim3(grid), dim3(256), lds, st, a);
   } else {
     const size_t lds = 4 * 64 * DP * 2;
-    e = with_lds(attend_tile_kernel<DP, 8>, lds);
+    e = with_lds(attend_tile_kernel<DP, kTileWaves>, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((attend_tile_kernel<DP, 8>), dim3(grid), dim3(512), lds, st, a);
+    hipLaunchKernelGGL((attend_tile_kernel<DP, kTileWaves>), dim3(grid), dim3(kTileWaves * 64), lds, st, a);
   }
   e = hipGetLastError();
   if (e == hipSuccess && a.nsplit > 1) e = launch_join(a, st);
@@ -512,7 +522,10 @@ AttendArgs make_args(const AttendCall &c, const AttendPlan &p, void *workspace) 
   a.cu_q = c.cu_q, a.cu_k = c.cu_k;
   a.nseq = c.nseq, a.Hq = c.Hq, a.Hkv = c.Hkv, a.D = c.D;
   a.scale_log2 = c.scale * kLog2e;
-  a.ntiles = p.ntiles, a.nsplit = p.nsplit, a.chunk = p.chunk;
+  const int BQ = p.form == AttendPlan::kList ? 1 : p.form == AttendPlan::kRows ? 32 : kTileWaves * 32;
+  a.ntiles = make_table(a.table, c.cu_q_host, c.cu_k_host, c.nseq, p.form == AttendPlan::kList ? 1 : c.Hq / c.Hkv,
+                        BQ, true);
+  a.nsplit = p.nsplit, a.chunk = p.chunk;
   a.o = c.o, a.lse = c.lse;
   a.rows = c.Tq * c.Hq;
   a.part_o = (float *)workspace;
@@ -537,18 +550,19 @@ AttendPlan plan_attend(const int32_t *cu_q, const int32_t *cu_k, int nseq, int H
   }
   AttendPlan p;
   p.form = most_rows <= 64 ? AttendPlan::kRows : AttendPlan::kTiles;
-  const int BQ = p.form == AttendPlan::kRows ? 32 : 256;
+  const int BQ = p.form == AttendPlan::kRows ? 32 : kTileWaves * 32;
   p.ntiles = tile_start(cu_q[nseq], nseq, (int)G, BQ);
-  // keys that all workgroups walk, without a split
-  int64_t walked = 0;
+  // workgroups, and the keys that all of them walk, without a split
+  int64_t wgs = 0, walked = 0;
   for (int s = 0; s < nseq; ++s) {
     const int64_t lq = cu_q[s + 1] - cu_q[s], lk = cu_k[s + 1] - cu_k[s];
+    wgs += (lq * G + BQ - 1) / BQ * Hkv;
     walked += (lq * G + BQ - 1) / BQ * lk * Hkv;
   }
-  p.chunk = (int)round_up(walked / 512 > 1024 ? walked / 512 : 1024, 256);
-  p.nsplit = (int)((most_keys + p.chunk - 1) / p.chunk);
-  if (p.nsplit < 1) p.nsplit = 1;
-  if (p.nsplit == 1 || p.ntiles * Hkv >= 1024) p.nsplit = 1, p.chunk = 0x7FFFFF00;
+  p.nsplit = 1, p.chunk = 0x7FFFFF00;
+  if (wgs >= 256) return p;
+  const int64_t chunk = round_up(walked / 512 > 1024 ? walked / 512 : 1024, 256);
+  if (most_keys > chunk) p.nsplit = (int)((most_keys + chunk - 1) / chunk), p.chunk = (int)chunk;
   return p;
 }
 

@@ -38,6 +38,7 @@ struct BwdArgs {
   int kchunk, qchunk;   // their sizes: virtual rows (multiple of 32), keys (multiple of 64)
   uint16_t *dq, *dk, *dv;
   float *part;          // fp32 parts, used by one kernel and its sum at a time
+  TileTable table;      // of keys, or of query rows
 };
 
 // One (row, head) per 16 lanes.
@@ -102,144 +103,270 @@ __device__ inline void load_frag(bf16x8 (&f)[DP / 16], const uint16_t *row, int 
   }
 }
 
-// dK and dV: 4 waves of 32 keys; tiles of 32 virtual rows (q, do and their statistics) pass
-// through LDS.
+// dK and dV: a workgroup's 128 keys in 4 groups of 32, two waves a group on one SIMD: the
+// first computes S and P and sums dV, the second computes dP and dS one tile behind it and
+// sums dK.  P passes from one to the other through LDS in fp32, lane for lane.  One wave for
+// both would need over 256 registers (128 of sums, 64 of keys and values) and have the SIMD to
+// itself, with nothing to fill its waits; in this form each needs under 256 and one's vector
+// work runs beside the other's matrix instructions (16 a tile each).
+// Tiles of 32 virtual rows (q, do, lse, delta) pass through four LDS buffers: the first
+// wave's tile, the second's, and two on their way.  The steps are unrolled by four so that
+// every LDS address is a register computed once plus a constant.
 template <int DP>
-__global__ __launch_bounds__(256, 1) void bwd_keys_kernel(BwdArgs a) {
+struct BwdKeys {
+  static constexpr int BR = 32, NG = 4, KEYS = NG * 32;
+  static constexpr int TILE = BR * Keys<DP>::ROWB, BUFB = 2 * TILE;
+  static constexpr int AHEAD = 2, NBUF = 4;
+  static constexpr int STAT = NBUF * BUFB, STATB = 256;   // lse and delta of the buffers
+  static constexpr int PBUF = 32 * 32 * 4, P = STAT + NBUF * STATB;
+  static constexpr int LDS = P + 2 * NG * PBUF;
+};
+
+template <int DP>
+__global__ __launch_bounds__(512) void bwd_keys_kernel(BwdArgs a) {
   using S = Keys<DP>;
-  constexpr int BR = 32, NW = 4, TILE = BR * S::ROWB, BUFB = 2 * TILE + 256;
-  constexpr int PER = BR / S::REGION_ROWS / NW > 0 ? BR / S::REGION_ROWS / NW : 1;
+  using C = BwdKeys<DP>;
+  constexpr int BR = C::BR, TILE = C::TILE, BUFB = C::BUFB, NW = 8;
+  constexpr int REGIONS = 2 * BR / S::REGION_ROWS;  // q's, then do's
+  constexpr int PER = REGIONS / NW;                 // loads a wave
+  static_assert(REGIONS % NW == 0, "whole loads a wave");
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = wave & 3;
+  const bool second = wave >= 4;
   const int G = a.Hq / a.Hkv;
   int64_t idx = blockIdx.x;
   const int kvh = (int)(idx % a.Hkv);
   idx /= a.Hkv;
   const int split = (int)(idx % a.ksplit);
   // (tiles of keys: the roles of the two length arrays are exchanged)
-  const TileAt at = find_tile(a.cu_k, a.cu_q, a.nseq, 1, NW * 32, idx / a.ksplit, lane);
+  const TileAt at = find_tile(a.table, a.cu_k, a.cu_q, a.nseq, 1, C::KEYS, idx / a.ksplit, a.ktiles, lane);
   if (at.seq < 0) return;
   const int k_start = at.q_start, Lk = at.Lq, q_start = at.k_start, Lq = at.Lk;
-  const int key = at.n0 + wave * 32 + (lane & 31);  // this lane's key, of the sequence
+  const int key = at.n0 + group * 32 + (lane & 31);  // this lane's key, of the sequence
   const bool live = key < Lk;
-  bf16x8 kf[S::KS], vf[S::KS];
-  load_frag<DP>(kf, live ? a.k + ((int64_t)k_start + key) * a.ks + (int64_t)kvh * a.D : nullptr, a.D, lane);
-  load_frag<DP>(vf, live ? a.v + ((int64_t)k_start + key) * a.vs + (int64_t)kvh * a.D : nullptr, a.D, lane);
-  f32x16 dk[S::DT], dv[S::DT];
-#pragma unroll
-  for (int dt = 0; dt < S::DT; ++dt)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) dk[dt][i] = dv[dt][i] = 0.0f;
 
   // virtual rows that see the first key of the workgroup, cut to this part
   const int nvirt = Lq * G, off = Lk - Lq;
-  const int first = (int)min<int64_t>(nvirt, (int64_t)max(0, at.n0 - off) * G);
-  const int n_lo = max(first / 32 * 32, split * a.kchunk);
+  auto seen_from = [&](int k) {
+    return k < Lk ? (int)min<int64_t>(nvirt, (int64_t)max(0, k - off) * G) : nvirt;
+  };
+  const int n_lo = max(seen_from(at.n0) / 32 * 32, split * a.kchunk);
   const int n_hi = (int)min<int64_t>(nvirt, (int64_t)split * a.kchunk + a.kchunk);
   const int ntile = n_hi > n_lo ? (n_hi - n_lo + BR - 1) / BR : 0;
-  // this lane's key is seen from virtual row `from` on; every key of the wave from `all` on
-  const int from = live ? (int)min<int64_t>(nvirt, (int64_t)max(0, key - off) * G) : nvirt;
-  const int wave_first = at.n0 + wave * 32;
-  const int none = wave_first < Lk ? (int)min<int64_t>(nvirt, (int64_t)max(0, wave_first - off) * G) : nvirt;
-  const int all = wave_first + 31 < Lk ? (int)min<int64_t>(nvirt, (int64_t)max(0, wave_first + 31 - off) * G)
-                                       : nvirt;
+  if (a.ksplit > 1 && ntile == 0) return;  // (the sum does not read this part)
+  // this lane's key is seen from virtual row `from` on, the group's first key from `some` on
+  // and all of them from `all` on
+  const int from = live ? seen_from(key) : nvirt;
+  const int some = seen_from(at.n0 + group * 32), all = seen_from(at.n0 + group * 32 + 31);
 
-  const uint16_t *qb = a.q + (int64_t)q_start * a.qs + (int64_t)kvh * G * a.D;
-  const int64_t dos = (int64_t)a.Hq * a.D;
-  const uint16_t *dob = a.d_o + (int64_t)q_start * dos + (int64_t)kvh * G * a.D;
-  const float *stat = (lane < 32 ? a.lse2 : a.delta) + (int64_t)kvh * a.Tq * G + (int64_t)q_start * G;
-  // rows of this lane's loads: token and head of the group, moved on by 32 virtual rows a tile
-  int tok[PER], g[PER];
+  bf16x8 kv[S::KS];  // the first wave's keys, the second's values
+  {
+    const uint16_t *row = second ? a.v + ((int64_t)k_start + key) * a.vs : a.k + ((int64_t)k_start + key) * a.ks;
+    load_frag<DP>(kv, live ? row + (int64_t)kvh * a.D : nullptr, a.D, lane);
+  }
+  f32x16 sum[S::DT];  // dV^T of the first, dK^T of the second
+#pragma unroll
+  for (int dt = 0; dt < S::DT; ++dt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum[dt][i] = 0.0f;
+
+  // Loads: regions wave, wave + 8, ..; for each the address of the lane's row and its head of
+  // the group, moved on by 32 virtual rows a tile.
   const int sub = lane * 16 / S::ROWB;
+  int g[PER];
+  const uint16_t *src[PER];
+  const int step_tok = BR / G, step_g = BR - step_tok * G;
+  auto row_of = [&](int i) { return (wave + i * NW) % (REGIONS / 2) * S::REGION_ROWS + sub; };
+  auto pitch_of = [&](int i) { return wave + i * NW >= REGIONS / 2 ? (int64_t)a.Hq * a.D : a.qs; };
+  int64_t move[PER], move_over[PER];  // 32 virtual rows on, without and with a new token
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int n = n_lo + (wave + i * NW) * S::REGION_ROWS + sub;
-    tok[i] = n / G;
-    g[i] = n - tok[i] * G;
+    move[i] = step_tok * pitch_of(i) + step_g * a.D;
+    move_over[i] = move[i] + pitch_of(i) - (int64_t)G * a.D;
   }
-  const int step_tok = BR / G, step_g = BR - step_tok * G;
-  auto load = [&](int tile, int buf) {
-#if defined(__HIP_DEVICE_COMPILE__)
-    unsigned char *at_lds = lds + buf * BUFB;
+  auto address = [&](int i, int n) {  // of the lane's 16 bytes of virtual row n
+    const int row = row_of(i);
+    const int chunk = min((lane & (DP / 8 - 1)) ^ S::swz(row), a.D / 8 - 1);
+    const uint16_t *p = wave + i * NW >= REGIONS / 2 ? a.d_o : a.q;
+    const int tok = n / G;
+    return p + (q_start + tok) * pitch_of(i) + (int64_t)(kvh * G + n - tok * G) * a.D + chunk * 8;
+  };
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int region = wave + i * NW;
-      const int row = region * S::REGION_ROWS + sub;
-      const int chunk = min((lane & (DP / 8 - 1)) ^ S::swz(row), a.D / 8 - 1);
-      // (rows past the last one take it again; they count for nothing)
-      const bool in = tok[i] < Lq;
-      const int64_t t = in ? tok[i] : Lq - 1, hd = (in ? g[i] : G - 1) * a.D + chunk * 8;
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(qb + t * a.qs + hd),
-                                       (KPOOL_LDS void *)(at_lds + region * 1024), 16, 0, 0);
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(dob + t * dos + hd),
-                                       (KPOOL_LDS void *)(at_lds + TILE + region * 1024), 16, 0, 0);
-      tok[i] += step_tok, g[i] += step_g;
-      if (g[i] >= G) g[i] -= G, ++tok[i];
+  for (int i = 0; i < PER; ++i) {
+    const int n = min(n_lo + row_of(i), max(nvirt - 1, 0));
+    src[i] = address(i, n);
+    g[i] = n - n / G * G;
+  }
+  const float *stat = (lane < 32 ? a.lse2 : a.delta) + (int64_t)kvh * a.Tq * G + (int64_t)q_start * G;
+  const uint32_t lds0 = lds_offset(lds);
+  auto load = [&](int tile, int buf) {
+    const uint32_t to = lds0 + buf * BUFB + wave * 1024;
+    const int n0 = n_lo + tile * BR;
+    if (n0 + BR <= nvirt) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        load_lds_16(src[i], to + i * NW * 1024);
+        g[i] += step_g;
+        const bool over = g[i] >= G;
+        g[i] -= over ? G : 0;
+        src[i] += over ? move_over[i] : move[i];
+      }
+    } else {  // the last rows: those past the end are the last one again and count for nothing
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        load_lds_16(address(i, min(n0 + row_of(i), nvirt - 1)), to + i * NW * 1024);
     }
-    if (wave == 0) {
-      const int n = min(n_lo + tile * BR + (lane & 31), nvirt - 1);
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(stat + n),
-                                       (KPOOL_LDS void *)(at_lds + 2 * TILE), 4, 0, 0);
-    }
-#endif
+    // (every wave loads the statistics, the same to the same place: its loads then count alike)
+    load_lds_4(stat + min(n0 + (lane & 31), nvirt - 1), lds0 + C::STAT + buf * C::STATB);
   };
   Frag<DP> f;
-  f.init(lds_offset(lds), lane);
-  const uint32_t st0 = lds_offset(lds) + 2 * TILE + (lane >> 5) * 16;
-  auto step = [&](int j, auto buf_c) {
-    constexpr int BUF = decltype(buf_c)::value;
-    constexpr uint32_t SQ = BUF * BUFB, SO = SQ + TILE;
-    __builtin_amdgcn_s_waitcnt(0x0F70);
-    __syncthreads();
-    if (j + 1 < ntile) load(j + 1, BUF ^ 1);
+  f.init(lds0, lane);
+  typedef float f32x4 __attribute__((ext_vector_type(4)));
+  uint32_t st0 = lds0 + C::STAT + (lane >> 5) * 16 + (second ? 128 : 0);
+  uint32_t pb = lds0 + C::P + group * C::PBUF + lane * 16;
+  opaque(st0), opaque(pb);
+  // The reads of a phase go out together ahead of the matrix instructions that need them; the
+  // compiler left to itself reads one fragment and waits for it, eight times over.
+  auto product = [&](uint32_t buf, f32x4 (&st)[4], uint32_t st_at) {  // rows of the tile with kv
+    bf16x8 r[S::KS];
+#pragma unroll
+    for (int ks = 0; ks < S::KS; ++ks) r[ks] = f.rows(buf, ks);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) st[b] = *(KPOOL_LDS const f32x4 *)(uintptr_t)(st_at + b * 32);
+    __builtin_amdgcn_sched_barrier(0);
+    f32x16 t = {};
+#pragma unroll
+    for (int ks = 0; ks < S::KS; ++ks) t = mfma(r[ks], kv[ks], t);
+    return t;
+  };
+  auto columns = [&](uint32_t buf, int c, bf16x8 (&w)[S::DT]) {
+#pragma unroll
+    for (int dt = 0; dt < S::DT; ++dt) w[dt] = f.cols(buf + c * 16 * S::ROWB, dt);
+  };
+  auto gather = [&](const bf16x8 (&w)[S::DT], const bf16x8 &x) {
+#pragma unroll
+    for (int dt = 0; dt < S::DT; ++dt) sum[dt] = mfma(w[dt], x, sum[dt]);
+  };
+  wait_loads();
+#pragma unroll
+  for (int i = 0; i < C::AHEAD; ++i)
+    if (i < ntile) load(i, i);
+  auto enter = [&](int j) {
+    // tile j has landed and P of tile j - 1 is written (everyone's, behind the barrier), and
+    // nobody reads the buffer of tile j - 2 any more, where tile j + 2 goes
+    static_assert(C::AHEAD == 2 && C::NBUF == 4 && (PER == 1 || PER == 2), "one tile's loads stay out");
+    if (j + 1 >= ntile) __builtin_amdgcn_s_waitcnt(0x0070);    // vmcnt(0), lgkmcnt(0)
+    else if (PER == 2) __builtin_amdgcn_s_waitcnt(0x0073);     // vmcnt(3)
+    else __builtin_amdgcn_s_waitcnt(0x0072);                   // vmcnt(2)
+    barrier_only();
+    if (j + C::AHEAD < ntile) load(j + C::AHEAD, (j + C::AHEAD) & 3);
+  };
+  // Both waves pass ntile + 1 barriers: the first works on tiles 0 .. ntile - 1, the second
+  // one step later; neither on the tiles before `skip`, which see no key of the group.
+  const int skip = min(ntile, max(0, some - n_lo) / BR);
+  auto first_wave = [&](int j, auto buf) {
+    constexpr int BUF = decltype(buf)::value;
+    enter(j);
     const int n0 = n_lo + j * BR;
-    if (n0 + BR <= none) return;  // (the whole wave) no row of the tile sees a key of the wave
-    f32x16 s = {}, dp = {};
+    f32x4 lse[4];
+    f32x16 p = product(BUF * BUFB, lse, st0 + BUF * C::STATB);
+    bf16x8 w0[S::DT], w1[S::DT];
+    columns(BUF * BUFB + TILE, 0, w0);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int ks = 0; ks < S::KS; ++ks) s = mfma(f.rows(SQ, ks), kf[ks], s);
-#pragma unroll
-    for (int ks = 0; ks < S::KS; ++ks) dp = mfma(f.rows(SO, ks), vf[ks], dp);
-    float lse[16], delta[16];
-    typedef float f32x4 __attribute__((ext_vector_type(4)));
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const f32x4 x = *(KPOOL_LDS const f32x4 *)(uintptr_t)(st0 + SQ + b * 32);
-      const f32x4 y = *(KPOOL_LDS const f32x4 *)(uintptr_t)(st0 + SQ + 128 + b * 32);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) lse[4 * b + i] = x[i], delta[4 * b + i] = y[i];
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) s[i] = exp2f_fast(fmaf(s[i], a.scale_log2, -lse[i]));
+    for (int i = 0; i < 16; ++i) p[i] = exp2f_fast(fmaf(p[i], a.scale_log2, -lse[i / 4][i % 4]));
     if (n0 < all || n0 + BR > n_hi) {
       const int lo = from - n0 - 4 * (lane >> 5), hi = n_hi - n0 - 4 * (lane >> 5);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int r = 8 * (i / 4) + i % 4;
-        if (r < lo || r >= hi) s[i] = 0.0f;
+        if (r < lo || r >= hi) p[i] = 0.0f;
       }
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) dp[i] = s[i] * (dp[i] - delta[i]);
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const bf16x8 p = as_operand(s, c), ds = as_operand(dp, c);
-#pragma unroll
-      for (int dt = 0; dt < S::DT; ++dt) dv[dt] = mfma(f.cols(SO + c * 16 * S::ROWB, dt), p, dv[dt]);
-#pragma unroll
-      for (int dt = 0; dt < S::DT; ++dt) dk[dt] = mfma(f.cols(SQ + c * 16 * S::ROWB, dt), ds, dk[dt]);
-    }
+    for (int b = 0; b < 4; ++b)
+      *(KPOOL_LDS f32x4 *)(uintptr_t)(pb + (BUF & 1) * C::NG * C::PBUF + b * 1024) =
+          f32x4{p[4 * b], p[4 * b + 1], p[4 * b + 2], p[4 * b + 3]};
+    columns(BUF * BUFB + TILE, 1, w1);
+    gather(w0, as_operand(p, 0));
+    gather(w1, as_operand(p, 1));
   };
-  if (ntile > 0) load(0, 0);
-  for (int j = 0; j < ntile; j += 2) {
-    step(j, std::integral_constant<int, 0>{});
-    if (j + 1 < ntile) step(j + 1, std::integral_constant<int, 1>{});
+  auto second_wave = [&](int j, auto buf) {  // tile j - 1
+    constexpr int BUF = (decltype(buf)::value + 3) & 3;
+    enter(j);
+    f32x4 delta[4], p[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      p[b] = *(KPOOL_LDS const f32x4 *)(uintptr_t)(pb + (BUF & 1) * C::NG * C::PBUF + b * 1024);
+    f32x16 ds = product(BUF * BUFB + TILE, delta, st0 + BUF * C::STATB);
+    bf16x8 w0[S::DT], w1[S::DT];
+    columns(BUF * BUFB, 0, w0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) ds[i] = p[i / 4][i % 4] * (ds[i] - delta[i / 4][i % 4]);
+    columns(BUF * BUFB, 1, w1);
+    gather(w0, as_operand(ds, 0));
+    gather(w1, as_operand(ds, 1));
+  };
+  // steps [j, end), in rounds of four from a multiple of four on
+  auto steps = [&](int j, int end, auto &&step) {
+    using B0 = std::integral_constant<int, 0>;
+    using B1 = std::integral_constant<int, 1>;
+    using B2 = std::integral_constant<int, 2>;
+    using B3 = std::integral_constant<int, 3>;
+    if (j < end && (j & 3) == 1) step(j++, B1{});
+    if (j < end && (j & 3) == 2) step(j++, B2{});
+    if (j < end && (j & 3) == 3) step(j++, B3{});
+    for (; j + 4 <= end; j += 4) step(j, B0{}), step(j + 1, B1{}), step(j + 2, B2{}), step(j + 3, B3{});
+    if (j < end) step(j++, B0{});
+    if (j < end) step(j++, B1{});
+    if (j < end) step(j++, B2{});
+  };
+  if (!second) {
+    for (int j = 0; j < skip; ++j) enter(j);
+    steps(skip, ntile, first_wave);
+    enter(ntile);
+  } else {
+    for (int j = 0; j <= skip; ++j) enter(j);
+    steps(skip + 1, ntile + 1, second_wave);
   }
   if (!live) return;
   const int64_t row = ((int64_t)k_start + key) * a.Hkv + kvh, rows = a.Tk * a.Hkv;
-  float *part = a.ksplit > 1 ? a.part + (int64_t)split * 2 * rows * a.D : nullptr;
-  write_cols<DP>(dk, a.scale, a.dk, part, row, a.D, lane);
-  write_cols<DP>(dv, 1.0f, a.dv, part ? part + rows * a.D : nullptr, row, a.D, lane);
+  float *part = a.ksplit > 1 ? a.part + ((int64_t)split * 2 + second) * rows * a.D : nullptr;
+  write_cols<DP>(sum, second ? a.scale : 1.0f, second ? a.dk : a.dv, part, row, a.D, lane);
+}
+
+// Sums the parts of dK and dV in order; a workgroup per 8 keys of a key head, which reads the
+// parts whose rows see its keys.
+__global__ __launch_bounds__(256) void bwd_keys_sum_kernel(BwdArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int kvh = (int)(blockIdx.x % a.Hkv);
+  const int G = a.Hq / a.Hkv;
+  const int64_t tile = blockIdx.x / a.Hkv;
+  const TileAt at = find_tile(a.table, a.cu_k, a.cu_q, a.nseq, 1, 128, tile >> 4, a.ktiles, lane);
+  const int key0 = at.n0 + (int)(tile & 15) * 8;
+  if (at.seq < 0 || key0 >= at.Lq) return;
+  const int Lk = at.Lq, Lq = at.Lk, nvirt = Lq * G;
+  // (the first virtual row of the keys' workgroup, as there)
+  const int first = (int)min<int64_t>(nvirt, (int64_t)max(0, at.n0 - (Lk - Lq)) * G) / 32 * 32;
+  const int s0 = first / a.kchunk, s1 = nvirt > first ? (nvirt - 1) / a.kchunk + 1 : s0;
+  const int64_t pitch = a.Tk * a.Hkv * a.D;
+  const int per = a.D / 4;
+  for (int e = threadIdx.x; e < 2 * 8 * per; e += 256) {
+    const int which = e >= 8 * per, r = (e - which * 8 * per) / per, d = (e - (which * 8 + r) * per) * 4;
+    if (key0 + r >= Lk) continue;
+    const int64_t to = (((int64_t)at.q_start + key0 + r) * a.Hkv + kvh) * a.D + d;
+    float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int s = s0; s < s1; ++s) {
+      const float4 x = *reinterpret_cast<const float4 *>(a.part + ((int64_t)s * 2 + which) * pitch + to);
+      t.x += x.x, t.y += x.y, t.z += x.z, t.w += x.w;
+    }
+    *reinterpret_cast<uint2 *>((which ? a.dk : a.dv) + to) =
+        make_uint2(pack_bf16(t.x, t.y), pack_bf16(t.z, t.w));
+  }
 }
 
 // dQ: NW waves of 32 virtual rows; key tiles of 64 pass through LDS, as in the forward pass.
@@ -255,7 +382,7 @@ __global__ __launch_bounds__(NW * 64) void bwd_rows_kernel(BwdArgs a) {
   const int kvh = (int)(idx % a.Hkv);
   idx /= a.Hkv;
   const int split = (int)(idx % a.qsplit);
-  const TileAt at = find_tile(a.cu_q, a.cu_k, a.nseq, G, BQ, a.qtiles - 1 - idx / a.qsplit, lane);
+  const TileAt at = find_tile(a.table, a.cu_q, a.cu_k, a.nseq, G, BQ, idx / a.qsplit, a.qtiles, lane);
   if (at.seq < 0) return;
   const int nrows = min(BQ, at.Lq * G - at.n0);
   const int t1 = (at.n0 + nrows - 1) / G + at.Lk - at.Lq;
@@ -281,20 +408,21 @@ __global__ __launch_bounds__(NW * 64) void bwd_rows_kernel(BwdArgs a) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) dq[dt][i] = 0.0f;
 
+  const uint32_t lds0 = lds_offset(lds);
   Frag<DP> f;
-  f.init(lds_offset(lds), lane);
+  f.init(lds0, lane);
   KeyLoader<DP, BK, NW> keys;
   keys.init(wave, lane, a.D);
   const int ntile = k_hi > k_lo ? (k_hi - k_lo + BK - 1) / BK : 0;
   auto load = [&](int tile, int buf) {
     const int k0 = k_lo + tile * BK;
-    keys.load(kb + (int64_t)k0 * a.ks, a.ks, at.Lk - 1 - k0, lds + buf * 2 * TILE);
-    keys.load(vb + (int64_t)k0 * a.vs, a.vs, at.Lk - 1 - k0, lds + buf * 2 * TILE + TILE);
+    keys.load(kb + (int64_t)k0 * a.ks, a.ks, at.Lk - 1 - k0, lds0 + buf * 2 * TILE);
+    keys.load(vb + (int64_t)k0 * a.vs, a.vs, at.Lk - 1 - k0, lds0 + buf * 2 * TILE + TILE);
   };
   auto step = [&](int j, auto buf_c) {
     constexpr int BUF = decltype(buf_c)::value;
     __builtin_amdgcn_s_waitcnt(0x0F70);
-    __syncthreads();
+    barrier_only();
     if (j + 1 < ntile) load(j + 1, BUF ^ 1);
     const int k0 = k_lo + j * BK;
     if (k0 > w1) return;
@@ -303,11 +431,22 @@ __global__ __launch_bounds__(NW * 64) void bwd_rows_kernel(BwdArgs a) {
     for (int half = 0; half < 2; ++half) {
       constexpr uint32_t SK = BUF * 2 * TILE, SV = SK + TILE;
       const uint32_t down = half * 32 * S::ROWB;
+      // (the reads of a phase go out together, ahead of what needs them)
+      bf16x8 kr[S::KS], vr[S::KS];
+#pragma unroll
+      for (int ks = 0; ks < S::KS; ++ks) kr[ks] = f.rows(SK + down, ks), vr[ks] = f.rows(SV + down, ks);
+      __builtin_amdgcn_sched_barrier(0);
       f32x16 s = {}, dp = {};
 #pragma unroll
-      for (int ks = 0; ks < S::KS; ++ks) s = mfma(f.rows(SK + down, ks), qf[ks], s);
+      for (int ks = 0; ks < S::KS; ++ks) s = mfma(kr[ks], qf[ks], s);
 #pragma unroll
-      for (int ks = 0; ks < S::KS; ++ks) dp = mfma(f.rows(SV + down, ks), dof[ks], dp);
+      for (int ks = 0; ks < S::KS; ++ks) dp = mfma(vr[ks], dof[ks], dp);
+      bf16x8 w[2][S::DT];
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int dt = 0; dt < S::DT; ++dt) w[c][dt] = f.cols(SK + down + c * 16 * S::ROWB, dt);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[i] = exp2f_fast(fmaf(s[i], a.scale_log2, -lse));
       if (masked) {
@@ -322,10 +461,11 @@ __global__ __launch_bounds__(NW * 64) void bwd_rows_kernel(BwdArgs a) {
       for (int c = 0; c < 2; ++c) {
         const bf16x8 ds = as_operand(s, c);
 #pragma unroll
-        for (int dt = 0; dt < S::DT; ++dt) dq[dt] = mfma(f.cols(SK + down + c * 16 * S::ROWB, dt), ds, dq[dt]);
+        for (int dt = 0; dt < S::DT; ++dt) dq[dt] = mfma(w[c][dt], ds, dq[dt]);
       }
     }
   };
+  wait_loads();
   if (ntile > 0) load(0, 0);
   for (int j = 0; j < ntile; j += 2) {
     step(j, std::integral_constant<int, 0>{});
@@ -361,7 +501,7 @@ hipError_t launch_sum(const float *part, int64_t pitch, int nsplit, int64_t coun
 constexpr int kBwdWaves = 8;
 
 template <int DP>
-hipError_t launch_bwd_t(const BwdArgs &a, hipStream_t st) {
+hipError_t launch_bwd_t(const AttendCall &c, BwdArgs a, hipStream_t st) {
   hipError_t e = hipSuccess;
   if (a.Tq > 0) {
     hipLaunchKernelGGL(bwd_stat_kernel, dim3((unsigned)((a.Tq * a.Hq + 15) / 16)), dim3(256), 0, st, a);
@@ -369,15 +509,20 @@ hipError_t launch_bwd_t(const BwdArgs &a, hipStream_t st) {
     if (e != hipSuccess) return e;
   }
   if (a.Tk > 0) {
-    hipLaunchKernelGGL(bwd_keys_kernel<DP>, dim3((unsigned)(a.ktiles * a.ksplit * a.Hkv)), dim3(256),
-                       2 * (2 * 32 * DP * 2 + 256), st, a);
+    a.ktiles = make_table(a.table, c.cu_k_host, c.cu_q_host, a.nseq, 1, BwdKeys<DP>::KEYS, false);
+    e = with_lds(bwd_keys_kernel<DP>, BwdKeys<DP>::LDS);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(bwd_keys_kernel<DP>, dim3((unsigned)(a.ktiles * a.ksplit * a.Hkv)), dim3(512),
+                       BwdKeys<DP>::LDS, st, a);
     e = hipGetLastError();
-    const int64_t count = a.Tk * a.Hkv * a.D;
-    if (e == hipSuccess && a.ksplit > 1) e = launch_sum(a.part, 2 * count, a.ksplit, count, a.dk, st);
-    if (e == hipSuccess && a.ksplit > 1) e = launch_sum(a.part + count, 2 * count, a.ksplit, count, a.dv, st);
+    if (e == hipSuccess && a.ksplit > 1) {
+      hipLaunchKernelGGL(bwd_keys_sum_kernel, dim3((unsigned)(a.ktiles * 16 * a.Hkv)), dim3(256), 0, st, a);
+      e = hipGetLastError();
+    }
     if (e != hipSuccess) return e;
   }
   if (a.Tq > 0) {
+    a.qtiles = make_table(a.table, c.cu_q_host, c.cu_k_host, a.nseq, a.Hq / a.Hkv, kBwdWaves * 32, true);
     const size_t lds = 4 * 64 * DP * 2;
     hipLaunchKernelGGL((bwd_rows_kernel<DP, kBwdWaves>), dim3((unsigned)(a.qtiles * a.qsplit * a.Hkv)),
                        dim3(kBwdWaves * 64), lds, st, a);
@@ -390,10 +535,12 @@ hipError_t launch_bwd_t(const BwdArgs &a, hipStream_t st) {
 
 int64_t up_to(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
-// Parts of a walked axis of at most `longest`, for tiles that walk `walked` in all: enough
-// for two workgroups a CU, each part `least` long or more.
+// Parts of a walked axis, the longest `longest`, for tiles that walk about `walked` / 2 in
+// all (causal): no part longer than what a CU gets on average, in multiples of 128,
+// and no shorter than `least`.
 void split_walk(int64_t walked, int64_t longest, int64_t least, int *split, int *chunk) {
-  const int64_t c = up_to(walked / 512 > least ? walked / 512 : least, 64);
+  const int64_t share = walked / (2 * 256);
+  const int64_t c = up_to(share > least ? share : least, 128);
   const int64_t n = (longest + c - 1) / c;
   *split = n > 1 ? (int)n : 1;
   *chunk = n > 1 ? (int)c : 0x7FFFFF00;
@@ -406,18 +553,19 @@ BwdPlan plan_attend_bwd(const int32_t *cu_q, const int32_t *cu_k, int nseq, int 
   BwdPlan p;
   p.ktiles = tile_start(cu_k[nseq], nseq, 1, 128);
   p.qtiles = tile_start(cu_q[nseq], nseq, G, kBwdWaves * 32);
-  int64_t rows = 0, keys = 0, most_rows = 0, most_keys = 0, kt = 0, qt = 0;
+  int64_t rows = 0, keys = 0, most_rows = 0, most_keys = 0, qt = 0;
   for (int s = 0; s < nseq; ++s) {
     const int64_t lq = (int64_t)(cu_q[s + 1] - cu_q[s]) * G, lk = cu_k[s + 1] - cu_k[s];
     const int64_t nk = (lk + 127) / 128, nq = (lq + kBwdWaves * 32 - 1) / (kBwdWaves * 32);
-    rows += nk * lq, keys += nq * lk, kt += nk, qt += nq;
+    rows += nk * lq, keys += nq * lk, qt += nq;
     if (lk > 0 && most_rows < lq) most_rows = lq;
     if (lq > 0 && most_keys < lk) most_keys = lk;
   }
-  p.ksplit = p.qsplit = 1;
-  p.kchunk = p.qchunk = 0x7FFFFF00;
-  if (kt * Hkv < 256) split_walk(rows * Hkv, most_rows, 512, &p.ksplit, &p.kchunk);
-  if (qt * Hkv < 256) split_walk(keys * Hkv, most_keys, 512, &p.qsplit, &p.qchunk);
+  split_walk(rows * Hkv, most_rows, 1024, &p.ksplit, &p.kchunk);
+  if (qt * Hkv < 256)  // (with more, the heaviest tiles start first and the rest fills in behind them)
+    split_walk(keys * Hkv, most_keys, 512, &p.qsplit, &p.qchunk);
+  else
+    p.qsplit = 1, p.qchunk = 0x7FFFFF00;
   return p;
 }
 
@@ -439,10 +587,10 @@ hipError_t launch_attend_bwd(const AttendCall &c, const uint16_t *d_o, const Bwd
   a.lse2 = (float *)workspace;
   a.delta = a.lse2 + c.Tq * c.Hq;
   a.part = (float *)((char *)workspace + up_to(c.Tq * c.Hq * 8, 16));
-  a.ktiles = p.ktiles, a.qtiles = p.qtiles, a.ksplit = p.ksplit, a.qsplit = p.qsplit;
+  a.ksplit = p.ksplit, a.qsplit = p.qsplit;
   a.kchunk = p.kchunk, a.qchunk = p.qchunk;
   a.dq = dq, a.dk = dk, a.dv = dv;
-  return c.D <= 64 ? launch_bwd_t<64>(a, st) : launch_bwd_t<128>(a, st);
+  return c.D <= 64 ? launch_bwd_t<64>(c, a, st) : launch_bwd_t<128>(c, a, st);
 }
 
 }  // namespace kpool

@@ -75,6 +75,9 @@ __device__ inline bf16x8 lds_read_cols(uint32_t first, uint32_t second) {
   return __builtin_bit_cast(bf16x8, v);
 }
 
+// Keeps the compiler from looking through a value.
+__device__ inline void opaque(uint32_t &x) { asm volatile("" : "+v"(x)); }
+
 // A lane's addresses of the fragments of a key tile
 template <int DP>
 struct Frag {
@@ -86,6 +89,11 @@ struct Frag {
     for (int ks = 0; ks < S::KS; ++ks) row[ks] = lds0 + (rb ^ (ks << 5));
 #pragma unroll
     for (int dt = 0; dt < S::DT; ++dt) col0[dt] = lds0 + (c0 ^ (dt << 6)), col1[dt] = lds0 + (c1 ^ (dt << 6));
+    // (opaque, so that a tile's constant offset stays apart and goes into the read itself)
+#pragma unroll
+    for (int ks = 0; ks < S::KS; ++ks) opaque(row[ks]);
+#pragma unroll
+    for (int dt = 0; dt < S::DT; ++dt) opaque(col0[dt]), opaque(col1[dt]);
   }
   // rows l % 32 from `off` on, contraction step ks over the head dim
   __device__ inline bf16x8 rows(uint32_t off, int ks) const { return lds_read(row[ks] + off); }
@@ -114,6 +122,19 @@ __device__ inline float other_half(float v) {
   return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
 }
 
+// A workgroup barrier alone.  __syncthreads() also waits for all of the wave's loads, those
+// that are meant to stay out among them; here the wave waits for what it needs beforehand.
+// The compiler keeps LDS accesses on their side of it.
+__device__ inline void barrier_only() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Waits for all of the wave's loads.  Before a loop it keeps the compiler, which would wait at
+// the first use, from doing so in every round, for that round's loads as well.
+__device__ inline void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+
 // 2^x by the hardware's instruction (relative error about 2^-23; -inf gives 0)
 __device__ inline float exp2f_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -122,6 +143,23 @@ __device__ inline const void *uniform_ptr(const void *p) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
   const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
   return (const void *)(((uint64_t)hi << 32) | lo);
+}
+
+// Loads from memory straight into LDS: lane i's 16 (or 4) bytes go to LDS byte `to` + 16 i
+// (4 i).  Written as asm because the compiler, which knows the builtins' loads to write LDS,
+// waits for all of them before each transposing LDS read and so for the tile that was just
+// asked for.  The loads have no result registers; the kernels wait for them by count before
+// the barrier behind which the tile is read, and the compiler's own waits, which do not count
+// them, can only wait longer.  (One wait state between writing M0 and its use.)
+__device__ inline void load_lds_16(const void *src, uint32_t to) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"{m0}"(to), "v"(src) : "memory");
+#endif
+}
+__device__ inline void load_lds_4(const void *src, uint32_t to) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, off" ::"{m0}"(to), "v"(src) : "memory");
+#endif
 }
 
 // Reads key tiles of BK rows from memory straight into LDS, by NWAVES waves of which this is
@@ -151,42 +189,97 @@ struct KeyLoader {
       col[i] = min((lane & (DP / 8 - 1)) ^ S::swz(row), D / 8 - 1) * 16;
     }
   }
-  // base and at are the same in every lane
-  __device__ inline void load(const uint16_t *base, int64_t stride, int last, unsigned char *at) const {
+  // base and to (an LDS offset) are the same in every lane
+  __device__ inline void load(const uint16_t *base, int64_t stride, int last, uint32_t to) const {
 #if defined(__HIP_DEVICE_COMPILE__)
     const uint32_t pitch = (uint32_t)stride * 2;
-    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-        (void *)uniform_ptr(base), 0, -1, 0x00020000);
+    const uint64_t b = (uint64_t)uniform_ptr(base);
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    const u32x4 rs = {(uint32_t)b, (uint32_t)(b >> 32) & 0xFFFFu, 0xFFFFFFFFu, 0x00020000u};
     const int sub = lane * 16 / S::ROWB;  // the lane's row of a region
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int region = wave + i * NWAVES;
       const int row = min(region * S::REGION_ROWS + sub, last);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (KPOOL_LDS void *)(at + region * 1024), 16,
-                                               row * pitch + col[i % NCOL], 0, 0, 0);
+      // (load_lds_16 through a buffer resource: the lane holds a 32-bit offset)
+      asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"{m0}"(to + region * 1024),
+                   "v"(row * pitch + col[i % NCOL]), "s"(rs)
+                   : "memory");
     }
 #endif
   }
 };
 
-// Where a tile of virtual rows sits.  Tiles of BQ rows are numbered through the batch with
-// sequence s starting at tile cu_q[s] * G / BQ + s: that leaves room for ceil(Lq * G / BQ)
-// tiles each and needs no table (a sequence may leave its last number unused).
+// Where a tile sits: BQ virtual rows of a sequence's queries, or 128 keys (cu_q and cu_k
+// exchanged, G = 1).
 struct TileAt {
-  int seq;           // -1: no such tile
-  int n0;            // its first virtual row
+  int seq;     // -1: no such tile
+  int n0;      // its first virtual row
   int q_start, k_start;
   int Lq, Lk;
 };
 
+// Tiles of up to kTableSeqs sequences are found in a table that travels with the arguments,
+// longest sequence first: workgroups start in this order, and what starts last should be
+// short.  (A packed batch of 4096, 2048, .. 1 tokens takes 13% longer in the order of its
+// tiles' numbers with the shortest first.)  `last_first` walks a sequence from its end, where
+// causal rows see the most keys.
+constexpr int kTableSeqs = 32;
+struct TileTable {
+  int32_t n;  // 0: more sequences than that; find_tile searches cu_q
+  int32_t last_first;
+  int32_t tile0[kTableSeqs + 1];
+  int32_t q_start[kTableSeqs], k_start[kTableSeqs], Lq[kTableSeqs], Lk[kTableSeqs];
+};
+
+// Without a table, tiles are numbered through the batch with sequence s starting at tile
+// cu_q[s] * G / BQ + s: that leaves room for ceil(Lq * G / BQ) tiles each (a sequence may leave
+// its last number unused).
 __host__ __device__ inline int64_t tile_start(int64_t cu, int s, int G, int BQ) {
   return cu * G / BQ + s;
 }
 
-// All 64 lanes call it; the search probes 64 sequences at a time.
-__device__ inline TileAt find_tile(const int32_t *__restrict__ cu_q, const int32_t *__restrict__ cu_k,
-                                   int nseq, int G, int BQ, int64_t tile, int lane) {
-  int lo = 0, n = nseq;  // the answer is in [lo, lo + n)
+// Fills in the table and returns the number of tiles.
+inline int64_t make_table(TileTable &t, const int32_t *cu_q, const int32_t *cu_k, int nseq, int G, int BQ,
+                          bool last_first) {
+  t.n = 0;
+  t.last_first = last_first;
+  int64_t tiles = 0;
+  if (nseq > kTableSeqs) return tile_start(cu_q[nseq], nseq, G, BQ);
+  for (int s = 0; s < nseq; ++s) {
+    const int32_t lq = cu_q[s + 1] - cu_q[s], lk = cu_k[s + 1] - cu_k[s];
+    if (lq == 0) continue;
+    int i = t.n++;  // insertion by the walked length, longest first
+    for (; i > 0 && t.Lk[i - 1] < lk; --i)
+      t.q_start[i] = t.q_start[i - 1], t.k_start[i] = t.k_start[i - 1], t.Lq[i] = t.Lq[i - 1],
+      t.Lk[i] = t.Lk[i - 1];
+    t.q_start[i] = cu_q[s], t.k_start[i] = cu_k[s], t.Lq[i] = lq, t.Lk[i] = lk;
+  }
+  for (int i = 0; i < t.n; ++i) {
+    t.tile0[i] = (int32_t)tiles;
+    tiles += ((int64_t)t.Lq[i] * G + BQ - 1) / BQ;
+  }
+  for (int i = t.n; i <= kTableSeqs; ++i) t.tile0[i] = 0x7FFFFFFF;
+  return tiles;
+}
+
+// All 64 lanes call it.  Tiles past the last one (their number is below the grid's) give seq -1.
+__device__ inline TileAt find_tile(const TileTable &tab, const int32_t *__restrict__ cu_q,
+                                   const int32_t *__restrict__ cu_k, int nseq, int G, int BQ, int64_t tile,
+                                   int64_t ntiles, int lane) {
+  TileAt r;
+  if (tab.n > 0) {
+    const int hits = __popcll(__ballot(lane < kTableSeqs && tab.tile0[lane & (kTableSeqs - 1)] <= (int)tile));
+    const int i = __builtin_amdgcn_readfirstlane(hits - 1);
+    r.seq = i;
+    r.q_start = tab.q_start[i], r.k_start = tab.k_start[i], r.Lq = tab.Lq[i], r.Lk = tab.Lk[i];
+    int local = (int)tile - tab.tile0[i];
+    if (tab.last_first) local = (int)(((int64_t)r.Lq * G + BQ - 1) / BQ) - 1 - local;
+    r.n0 = local * BQ;
+    return r;
+  }
+  if (tab.last_first) tile = ntiles - 1 - tile;
+  int lo = 0, n = nseq;  // the answer is in [lo, lo + n); 64 sequences are probed at a time
   while (n > 1) {
     const int step = (n + 63) / 64;
     const int s = lo + lane * step;
@@ -197,13 +290,20 @@ __device__ inline TileAt find_tile(const int32_t *__restrict__ cu_q, const int32
     lo = at;
   }
   lo = __builtin_amdgcn_readfirstlane(lo);
-  TileAt r;
   const int q0 = cu_q[lo], q1 = cu_q[lo + 1], k0 = cu_k[lo], k1 = cu_k[lo + 1];
   r.q_start = q0, r.k_start = k0, r.Lq = q1 - q0, r.Lk = k1 - k0;
   const int64_t n0 = (tile - tile_start(q0, lo, G, BQ)) * BQ;
   r.n0 = (int)n0;
   r.seq = n0 < (int64_t)r.Lq * G ? lo : -1;  // (Lq * G fits 32 bits, checked by the host)
   return r;
+}
+
+template <class F>
+inline hipError_t with_lds(F *kernel, size_t bytes) {
+  // (a launch may use more than 64 KiB of LDS only where the kernel was told so)
+  return bytes > 65536 ? hipFuncSetAttribute((const void *)kernel,
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)
+                       : hipSuccess;
 }
 
 }  // namespace kpool

@@ -90,6 +90,7 @@ struct AttendCall {
   const uint16_t *q, *k, *v;
   int64_t q_stride, k_stride, v_stride;  // elements between tokens
   const int32_t *cu_q, *cu_k;            // device
+  const int32_t *cu_q_host, *cu_k_host;
   int32_t nseq, Hq, Hkv, D;
   int64_t Tq, Tk;
   float scale;
@@ -98,7 +99,7 @@ struct AttendCall {
 };
 struct AttendPlan {
   enum Form { kRows, kTiles, kList } form;
-  int64_t ntiles;  // tiles of query rows
+  int64_t ntiles;  // tiles of query rows, or more
   int nsplit;      // parts of the key axis, joined by a second kernel where there are more than one
   int chunk;       // keys of a part
 };
@@ -111,7 +112,7 @@ hipError_t launch_attend_list(const AttendCall &c, const AttendPlan &p, const in
 
 // Its gradients (attend_bwd.hip); c.o and c.lse are the forward pass's.
 struct BwdPlan {
-  int64_t ktiles, qtiles;  // tiles of keys, of query rows
+  int64_t ktiles, qtiles;  // tiles of keys, of query rows, or more
   int ksplit, qsplit;      // parts of the rows (dK, dV) and of the keys (dQ)
   int kchunk, qchunk;
 };
