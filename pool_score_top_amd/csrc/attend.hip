@@ -24,10 +24,9 @@
 namespace kpool {
 namespace {
 
-#ifndef KPOOL_TW
-#define KPOOL_TW 8
-#endif
-constexpr int kTileWaves = KPOOL_TW;
+// Waves of the tile kernel, 32 rows each.  With 4, two workgroups fit a CU, but each loads its
+// own key tiles: a 16384-token prompt then takes 1345 us instead of 1028.
+constexpr int kTileWaves = 8;
 
 struct AttendArgs {
   const uint16_t *q, *k, *v;
@@ -72,26 +71,29 @@ struct Rows {
     l = 0.0f;
   }
 
-  // Adds the BK keys of a tile at LDS offsets sk and sv past the addresses of `f`.  Where
-  // `masked` (the same for the wave), key sub * 32 + r counts only if visible(sub, r).
-  template <int BK, class F>
-  __device__ inline void add(const Frag<DP> &f, uint32_t sk, uint32_t sv, float c, int lane, bool masked,
-                             F &&visible) {
-    constexpr int SUBS = BK / 32;
-    f32x16 s[SUBS];
-    bf16x8 kr[SUBS][S::KS];
+  // S of the BK keys of a tile at LDS offset sk past the addresses of `f`
+  template <int BK>
+  __device__ inline void scores(const Frag<DP> &f, uint32_t sk, f32x16 (&s)[BK / 32]) const {
+    // (the reads go out together, ahead of what needs them)
+    bf16x8 kr[BK / 32][S::KS];
 #pragma unroll
-    for (int sub = 0; sub < SUBS; ++sub)
+    for (int sub = 0; sub < BK / 32; ++sub)
 #pragma unroll
       for (int ks = 0; ks < S::KS; ++ks) kr[sub][ks] = f.rows(sk + sub * 32 * S::ROWB, ks);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int sub = 0; sub < SUBS; ++sub) {
+    for (int sub = 0; sub < BK / 32; ++sub) {
       f32x16 t = {};
 #pragma unroll
       for (int ks = 0; ks < S::KS; ++ks) t = mfma(kr[sub][ks], q[ks], t);
       s[sub] = t;
     }
+  }
+
+  // S to P, with the running maximum and sum.  Where `masked` (the same for the wave), key
+  // sub * 32 + r counts only if visible(sub, r).
+  template <int SUBS, class F>
+  __device__ inline void weights(f32x16 (&s)[SUBS], float c, int lane, bool masked, F &&visible) {
     if (masked) {
 #pragma unroll
       for (int sub = 0; sub < SUBS; ++sub)
@@ -117,20 +119,35 @@ struct Rows {
     }
     const float shift = m > -__builtin_inff() ? m : 0.0f;
 #pragma unroll
-    for (int sub = 0; sub < SUBS; ++sub) {
+    for (int sub = 0; sub < SUBS; ++sub)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         s[sub][i] = exp2f_fast(fmaf(s[sub][i], c, -shift));
         l += s[sub][i];
       }
+  }
+
+  // O of the tile whose values lie at LDS offset sv
+  template <int SUBS>
+  __device__ inline void values(const Frag<DP> &f, uint32_t sv, const f32x16 (&p)[SUBS]) {
+#pragma unroll
+    for (int sub = 0; sub < SUBS; ++sub)
 #pragma unroll
       for (int kc = 0; kc < 2; ++kc) {
-        const bf16x8 p = as_operand(s[sub], kc);
+        const bf16x8 w = as_operand(p[sub], kc);
 #pragma unroll
         for (int dt = 0; dt < S::DT; ++dt)
-          o[dt] = mfma(f.cols(sv + (sub * 32 + kc * 16) * S::ROWB, dt), p, o[dt]);
+          o[dt] = mfma(f.cols(sv + (sub * 32 + kc * 16) * S::ROWB, dt), w, o[dt]);
       }
-    }
+  }
+
+  template <int BK, class F>
+  __device__ inline void add(const Frag<DP> &f, uint32_t sk, uint32_t sv, float c, int lane, bool masked,
+                             F &&visible) {
+    f32x16 s[BK / 32];
+    scores<BK>(f, sk, s);
+    weights(s, c, lane, masked, visible);
+    values(f, sv, s);
   }
 };
 
@@ -186,7 +203,7 @@ __global__ __launch_bounds__(NW * 64) void attend_tile_kernel(AttendArgs a) {
   if (at.seq < 0) return;
   const int nrows = min(BQ, at.Lq * G - at.n0);
   const int t1 = (at.n0 + nrows - 1) / G + at.Lk - at.Lq;  // the last row's position
-  const int k_lo = split * a.chunk, k_hi = (int)min<int64_t>(t1 + 1, (int64_t)k_lo + a.chunk);
+  const int k_lo = split * a.chunk, k_hi = (int)min64(t1 + 1, (int64_t)k_lo + a.chunk);
   const uint16_t *kb = (const uint16_t *)uniform_ptr(a.k + (int64_t)at.k_start * a.ks + (int64_t)kvh * a.D);
   const uint16_t *vb = (const uint16_t *)uniform_ptr(a.v + (int64_t)at.k_start * a.vs + (int64_t)kvh * a.D);
 
@@ -217,7 +234,7 @@ __global__ __launch_bounds__(NW * 64) void attend_tile_kernel(AttendArgs a) {
     constexpr int BUF = decltype(buf_c)::value;
     // this wave's part of tile j has landed; behind the barrier everyone's has, and everyone
     // is done with the buffer that tile j + 1 goes to
-    __builtin_amdgcn_s_waitcnt(0x0F70);
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0), lgkmcnt(0)
     barrier_only();
     if (j + 1 < ntile) load(j + 1, BUF ^ 1);
     const int k0 = k_lo + j * BK;
@@ -235,14 +252,81 @@ __global__ __launch_bounds__(NW * 64) void attend_tile_kernel(AttendArgs a) {
   if (live) write_row<DP>(a, ((int64_t)at.q_start + tok) * a.Hq + head, split, r.o, r.m, l, lane);
 }
 
-// Few rows, or rows with lists: a workgroup's 4 waves share 32 virtual rows and take key
-// tiles of 32 in turn, each through its own double-buffered LDS, and join at the end.
-// LIST: the tile's rows are heads of one token and the keys are the token's ids; an entry
-// outside 0 .. t is not there.
-template <int DP, bool LIST>
+// The NW waves of a workgroup, each with its keys' part of the same 32 rows, join: O of every
+// wave scaled to the common maximum, summed in wave order.  `lds` is free for it.  Row r of the
+// workgroup is row out_row(r) of the output, r < nrows.
+template <int DP, int NW>
+struct Join {
+  static constexpr int STAT = NW * 64;                  // m and l, [NW][2][32]
+  static constexpr int LDS = (STAT + NW * DP * 33) * 4;  // and O^T, [NW][DP][33]
+};
+template <int DP, int NW, class F>
+__device__ inline void join_waves(const AttendArgs &a, const Rows<DP> &r, unsigned char *lds, int wave,
+                                  int lane, int split, int nrows, F &&out_row) {
+  using S = Keys<DP>;
+  const float l = r.l + other_half(r.l);
+  __syncthreads();  // (all waves are done with their tiles)
+  float *stat = reinterpret_cast<float *>(lds);
+  float *acc = stat + Join<DP, NW>::STAT;
+  if (lane < 32) stat[wave * 64 + lane] = r.m, stat[wave * 64 + 32 + lane] = l;
+  __syncthreads();
+  float m = -__builtin_inff();
+#pragma unroll
+  for (int w = 0; w < NW; ++w) m = fmaxf(m, stat[w * 64 + (lane & 31)]);
+  const float shift = m > -__builtin_inff() ? m : 0.0f;
+  const float mul = exp2f_fast(r.m - shift);
+#pragma unroll
+  for (int dt = 0; dt < S::DT; ++dt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      acc[(wave * DP + dt * 32 + 8 * (i / 4) + 4 * (lane >> 5) + i % 4) * 33 + (lane & 31)] = r.o[dt][i] * mul;
+  __syncthreads();
+  // 8 columns of a row a thread at a time
+  for (int e = threadIdx.x; e < 32 * (DP / 8); e += NW * 64) {
+    const int row = e / (DP / 8), d0 = e % (DP / 8) * 8;
+    if (row >= nrows || d0 >= a.D) continue;
+    float rm = -__builtin_inff(), rl = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) rm = fmaxf(rm, stat[w * 64 + row]);
+    const float sh = rm > -__builtin_inff() ? rm : 0.0f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) rl += stat[w * 64 + 32 + row] * exp2f_fast(stat[w * 64 + row] - sh);
+    const int64_t to = out_row(row);
+    const float inv = rl > 0.0f ? 1.0f / rl : 0.0f;
+    const float lse = rl > 0.0f ? (rm + log2f(rl)) * kLn2 : -__builtin_inff();
+    float out[8];
+#pragma unroll
+    for (int d = 0; d < 8; ++d) {
+      float t = 0.0f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) t += acc[(w * DP + d0 + d) * 33 + row];
+      out[d] = t * inv;
+    }
+    if (a.nsplit > 1) {
+      float *dst = a.part_o + ((int64_t)split * a.rows + to) * a.D + d0;
+      *reinterpret_cast<float4 *>(dst) = make_float4(out[0], out[1], out[2], out[3]);
+      *reinterpret_cast<float4 *>(dst + 4) = make_float4(out[4], out[5], out[6], out[7]);
+      if (d0 == 0) a.part_lse[(int64_t)split * a.rows + to] = lse;
+    } else {
+      *reinterpret_cast<uint4 *>(a.o + to * a.D + d0) =
+          make_uint4(pack_bf16(out[0], out[1]), pack_bf16(out[2], out[3]), pack_bf16(out[4], out[5]),
+                     pack_bf16(out[6], out[7]));
+      if (d0 == 0 && a.lse) a.lse[to] = lse;
+    }
+  }
+}
+
+// Few rows: a workgroup's 4 waves share 32 virtual rows and take key tiles of 32 in turn,
+// each through its own double-buffered LDS without a barrier, and join at the end.
+template <int DP>
+struct FewRows {
+  static constexpr int NW = 4, BK = 32, TILE = BK * Keys<DP>::ROWB;
+  static constexpr int LDS = NW * 4 * TILE > Join<DP, NW>::LDS ? NW * 4 * TILE : Join<DP, NW>::LDS;
+};
+template <int DP>
 __global__ __launch_bounds__(256) void attend_rows_kernel(AttendArgs a) {
   using S = Keys<DP>;
-  constexpr int BK = 32, NW = 4, TILE = BK * S::ROWB;
+  constexpr int BK = FewRows<DP>::BK, NW = FewRows<DP>::NW, TILE = FewRows<DP>::TILE;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -251,35 +335,14 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendArgs a) {
   const int kvh = (int)(idx % a.Hkv);
   idx /= a.Hkv;
   const int split = (int)(idx % a.nsplit);
-  idx /= a.nsplit;
-  TileAt at;
-  int first = 0;  // LIST: the tile's first head of the group
-  if (LIST) {
-    const int per = (G + 31) / 32;
-    const int64_t token = idx / per;
-    first = (int)(idx - token * per) * 32;
-    at = find_tile(a.table, a.cu_q, a.cu_k, a.nseq, 1, 1, token, a.ntiles, lane);
-  } else {
-    at = find_tile(a.table, a.cu_q, a.cu_k, a.nseq, G, 32, idx, a.ntiles, lane);
-  }
+  const TileAt at = find_tile(a.table, a.cu_q, a.cu_k, a.nseq, G, 32, idx / a.nsplit, a.ntiles, lane);
   if (at.seq < 0) return;
-  int tok, head, nrows;
-  if (LIST) {
-    tok = at.n0;
-    head = first + (lane & 31);
-    nrows = min(32, G - first);
-  } else {
-    const int n = at.n0 + (lane & 31);
-    tok = n / G;
-    head = n - tok * G;
-    nrows = min(32, at.Lq * G - at.n0);
-  }
-  const bool live = (lane & 31) < nrows;
-  head += kvh * G;
+  const int n = at.n0 + (lane & 31), tok = n / G, head = kvh * G + n - tok * G;
+  const int nrows = min(32, at.Lq * G - at.n0);
   const int t = tok + at.Lk - at.Lq;
   Rows<DP> r;
-  r.init(live ? a.q + ((int64_t)at.q_start + tok) * a.qs + (int64_t)head * a.D : nullptr, a.D, lane);
-
+  r.init((lane & 31) < nrows ? a.q + ((int64_t)at.q_start + tok) * a.qs + (int64_t)head * a.D : nullptr, a.D,
+         lane);
   const uint16_t *kb = (const uint16_t *)uniform_ptr(a.k + (int64_t)at.k_start * a.ks + (int64_t)kvh * a.D);
   const uint16_t *vb = (const uint16_t *)uniform_ptr(a.v + (int64_t)at.k_start * a.vs + (int64_t)kvh * a.D);
   const uint32_t mine = lds_offset(lds) + wave * 4 * TILE;
@@ -287,153 +350,166 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendArgs a) {
   f.init(mine, lane);
   KeyLoader<DP, BK, 1> keys;
   keys.init(0, lane, a.D);
-  // the last key (or list entry) of any row of the tile, and of every row
-  const int t1 = LIST ? 0 : (at.n0 + nrows - 1) / G + at.Lk - at.Lq;
-  const int t0 = LIST ? 0 : at.n0 / G + at.Lk - at.Lq;
-  const int end = LIST ? a.width : t1 + 1;
-  const int k_lo = split * a.chunk, k_hi = (int)min<int64_t>(end, (int64_t)k_lo + a.chunk);
-  const int32_t *ids = LIST ? a.ids + ((int64_t)at.q_start + tok) * a.width : nullptr;
-
-  // entry `lane` (of 32) of list tile k0: the id, and which of the tile are there
-  auto entries = [&](int k0, uint32_t &there) {
-    const int e = k0 + (lane & 31);
-    const int id = e < k_hi ? ids[e] : -1;
-    const bool ok = id >= 0 && id <= t;
-    there = (uint32_t)__ballot(ok);
-    // absent entries read the tile's first present one, so that only keys of the list are read
-    const int any = there ? __builtin_ctz(there) : 0;
-    const int stand_in = __builtin_amdgcn_readlane(id, any);
-    return ok ? id : stand_in;
-  };
-  // 2 * BK / REGION_ROWS loads of 1 KiB a tile
-  constexpr int REGIONS = BK / S::REGION_ROWS;
-  auto load_list = [&](int id, int buf) {
-#pragma unroll
-    for (int i = 0; i < REGIONS; ++i) {
-      const int row = i * S::REGION_ROWS + lane * 16 / S::ROWB;
-      const int chunk = min((lane & (DP / 8 - 1)) ^ S::swz(row), a.D / 8 - 1);
-      const int64_t key = __shfl(id, row);
-      load_lds_16(kb + key * a.ks + chunk * 8, mine + buf * 2 * TILE + i * 1024);
-      load_lds_16(vb + key * a.vs + chunk * 8, mine + buf * 2 * TILE + TILE + i * 1024);
-    }
-  };
+  // the first row's position and the last one's
+  const int t0 = at.n0 / G + at.Lk - at.Lq, t1 = (at.n0 + nrows - 1) / G + at.Lk - at.Lq;
+  const int k_lo = split * a.chunk, k_hi = (int)min64(t1 + 1, (int64_t)k_lo + a.chunk);
   auto load = [&](int k0, int buf) {
     keys.load(kb + (int64_t)k0 * a.ks, a.ks, at.Lk - 1 - k0, mine + buf * 2 * TILE);
     keys.load(vb + (int64_t)k0 * a.vs, a.vs, at.Lk - 1 - k0, mine + buf * 2 * TILE + TILE);
   };
-  uint32_t there = 0, there_next = 0;
-  int k0 = k_lo + wave * BK, buf = 0;
   wait_loads();
-  if (k0 < k_hi) {
-    if (LIST) {
-      const int id = entries(k0, there);
-      if (there) load_list(id, 0);
-    } else {
-      load(k0, 0);
-    }
-  }
+  int k0 = k_lo + wave * BK, buf = 0;
+  if (k0 < k_hi) load(k0, 0);
   for (; k0 < k_hi; k0 += NW * BK, buf ^= 1) {
-    const int kn = k0 + NW * BK;
-    bool more = kn < k_hi;
-    if (LIST) {
-      there_next = 0;
-      if (more) {
-        const int id = entries(kn, there_next);
-        more = there_next != 0;
-        if (more) load_list(id, buf ^ 1);
-      }
-    } else if (more) {
-      load(kn, buf ^ 1);
-    }
+    const bool more = k0 + NW * BK < k_hi;
+    wait_reads();
+    if (more) load(k0 + NW * BK, buf ^ 1);
     // the tile's own loads are the older ones: wait until only the next tile's are out
-    static_assert(2 * REGIONS == 16 || 2 * REGIONS == 8, "loads of a tile");
-    if (!more) __builtin_amdgcn_s_waitcnt(0x0F70);                        // vmcnt(0)
-    else if (2 * REGIONS == 16) __builtin_amdgcn_s_waitcnt(0x4F70);       // vmcnt(16)
-    else __builtin_amdgcn_s_waitcnt(0x0F78);                              // vmcnt(8)
+    constexpr int LOADS = 2 * BK / S::REGION_ROWS;
+    static_assert(LOADS == 16 || LOADS == 8, "loads of a tile");
+    if (!more) wait_loads();
+    else if (LOADS == 16) __builtin_amdgcn_s_waitcnt(0x4F70);  // vmcnt(16)
+    else __builtin_amdgcn_s_waitcnt(0x0F78);                   // vmcnt(8)
     asm volatile("" ::: "memory");
-    const uint32_t sk = buf * 2 * TILE, sv = sk + TILE;
-    if (LIST) {
-      if (there)
-        r.template add<BK>(f, sk, sv, a.scale_log2, lane, there != 0xFFFFFFFFu,
-                           [&](int, int i) { return (there >> i) & 1; });
-      there = there_next;
-    } else {
-      r.template add<BK>(f, sk, sv, a.scale_log2, lane, k0 + BK - 1 > t0,
-                         [&](int, int i) { return k0 + i <= t; });
-    }
+    r.template add<BK>(f, buf * 2 * TILE, buf * 2 * TILE + TILE, a.scale_log2, lane, k0 + BK - 1 > t0,
+                       [&](int, int i) { return k0 + i <= t; });
     asm volatile("" ::: "memory");
   }
-  // The waves join: m and l of every row, then O scaled to the common m, summed in wave order.
-  float l = r.l + other_half(r.l);
-  __syncthreads();  // (all waves are done with their tiles)
-  float *stat = reinterpret_cast<float *>(lds);                 // [NW][2][32]
-  float *acc = stat + NW * 64;                                  // [NW][DP][33]
-  if (lane < 32) stat[wave * 64 + lane] = r.m, stat[wave * 64 + 32 + lane] = l;
-  __syncthreads();
-  float m = -__builtin_inff();
+  join_waves<DP, NW>(a, r, lds, wave, lane, split, nrows, [&](int row) {
+    const int m = at.n0 + row, tk = m / G;
+    return ((int64_t)at.q_start + tk) * a.Hq + kvh * G + (m - tk * G);
+  });
+}
+
+// Rows with lists of tokens: a workgroup takes up to 32 heads of one token and key head; its
+// 8 waves take list tiles of 32 in turn and join at the end.  The keys come from all over
+// memory, so what counts is how many bytes are on their way: each wave has one LDS buffer for
+// keys and one for values, asks for the next tile's keys as soon as S is computed and for its
+// values after the product with P, and 8 waves do so independently (2 waves a SIMD).
+// The ids of 8 tiles at a time pass through LDS too, a block ahead, so that no wait for ids
+// holds up the keys' loads.  An entry outside 0 .. t is not there; it reads the tile's first
+// one that is, so that no other key is read, and counts for nothing.
+// Workgroups of one XCD (every 8th) take consecutive tokens of one key head: what neighbouring
+// rows both selected is then in that XCD's L2.
+template <int DP>
+struct Lists {
+  static constexpr int NW = 8, BK = 32, TILE = BK * Keys<DP>::ROWB;
+  static constexpr int BLOCK = 8;                           // tiles whose ids are fetched at once
+  static constexpr int IDS = NW * 2 * TILE, IDB = BLOCK * BK * 4;
+  static constexpr int USE = IDS + NW * 2 * IDB;
+  static constexpr int LDS = USE > Join<DP, NW>::LDS ? USE : Join<DP, NW>::LDS;
+};
+template <int DP>
+__global__ __launch_bounds__(512) void attend_list_kernel(AttendArgs a) {
+  using S = Keys<DP>;
+  using C = Lists<DP>;
+  constexpr int BK = C::BK, NW = C::NW, TILE = C::TILE;
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int G = a.Hq / a.Hkv, per = (G + 31) / 32;
+  const int64_t each = a.ntiles * per * a.nsplit, total = each * a.Hkv;  // workgroups: of a key head, all
+  int64_t idx = (blockIdx.x & 7) * ((total + 7) / 8) + (blockIdx.x >> 3);
+  if (idx >= total || (int64_t)(blockIdx.x >> 3) >= (total + 7) / 8) return;
+  const int kvh = (int)(idx / each);
+  idx -= kvh * each;
+  const int split = (int)(idx % a.nsplit);
+  idx /= a.nsplit;
+  const int first = (int)(idx % per) * 32;  // the workgroup's first head of the group
+  const TileAt at = find_tile(a.table, a.cu_q, a.cu_k, a.nseq, 1, 1, idx / per, a.ntiles, lane);
+  if (at.seq < 0) return;
+  const int tok = at.n0, t = tok + at.Lk - at.Lq;
+  const int nrows = min(32, G - first), head = kvh * G + first;
+  const int64_t token = (int64_t)at.q_start + tok;
+  Rows<DP> r;
+  r.init((lane & 31) < nrows ? a.q + token * a.qs + (int64_t)(head + (lane & 31)) * a.D : nullptr, a.D, lane);
+  const uint16_t *kb = (const uint16_t *)uniform_ptr(a.k + (int64_t)at.k_start * a.ks + (int64_t)kvh * a.D);
+  const uint16_t *vb = (const uint16_t *)uniform_ptr(a.v + (int64_t)at.k_start * a.vs + (int64_t)kvh * a.D);
+  const int32_t *ids = a.ids + token * a.width;
+  const uint32_t lds0 = lds_offset(lds), mine = lds0 + wave * 2 * TILE;
+  const uint32_t my_ids = lds0 + C::IDS + wave * 2 * C::IDB;
+  Frag<DP> f;
+  f.init(mine, lane);
+  const int e_lo = split * a.chunk + wave * BK;  // this wave's first entry; its tiles are NW * BK apart
+  const int e_hi = (int)min64(a.width, (int64_t)split * a.chunk + a.chunk);
+  const int ntile = e_lo < e_hi ? (e_hi - e_lo + NW * BK - 1) / (NW * BK) : 0;
+
+  auto load_ids = [&](int block) {  // two tiles a load
 #pragma unroll
-  for (int w = 0; w < NW; ++w) m = fmaxf(m, stat[w * 64 + (lane & 31)]);
-  const float shift = m > -__builtin_inff() ? m : 0.0f;
-  l = 0.0f;
-#pragma unroll
-  for (int w = 0; w < NW; ++w)
-    l += stat[w * 64 + 32 + (lane & 31)] * exp2f_fast(stat[w * 64 + (lane & 31)] - shift);
-  const float mul = exp2f_fast(r.m - shift);
-#pragma unroll
-  for (int dt = 0; dt < S::DT; ++dt)
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      acc[(wave * DP + dt * 32 + 8 * (i / 4) + 4 * (lane >> 5) + i % 4) * 33 + (lane & 31)] =
-          r.o[dt][i] * mul;
-  __syncthreads();
-  // thread: row (tid / 8), columns 16 (tid % 8) .. + DP / 8
-  {
-    const int row = threadIdx.x >> 3, d0 = (threadIdx.x & 7) * (DP / 8);
-    float rm = -__builtin_inff(), rl = 0.0f;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) rm = fmaxf(rm, stat[w * 64 + row]);
-    const float sh = rm > -__builtin_inff() ? rm : 0.0f;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) rl += stat[w * 64 + 32 + row] * exp2f_fast(stat[w * 64 + row] - sh);
-    if (row >= nrows) return;
-    int tk, hd;
-    if (LIST) {
-      tk = at.n0;
-      hd = first + row;
-    } else {
-      const int n = at.n0 + row;
-      tk = n / G;
-      hd = n - tk * G;
+    for (int i = 0; i < C::BLOCK; i += 2) {
+      const int64_t e = e_lo + ((int64_t)block * C::BLOCK + i + (lane >> 5)) * (NW * BK) + (lane & 31);
+      load_lds_4(ids + min64(e, a.width - 1), my_ids + (block & 1) * C::IDB + i * BK * 4);
     }
-    const int64_t out_row = ((int64_t)at.q_start + tk) * a.Hq + kvh * G + hd;
-    const float inv = rl > 0.0f ? 1.0f / rl : 0.0f;
-    const float lse = rl > 0.0f ? (rm + log2f(rl)) * kLn2 : -__builtin_inff();
-    float out[DP / 8];
+  };
+  // a tile's ids, entry l % 32 in lane l, and which of them are there
+  auto entries = [&](int tile, uint32_t &there) {
+    const int e = e_lo + tile * NW * BK + (lane & 31);
+    const int id = *(KPOOL_LDS const int *)(uintptr_t)(my_ids + (tile / C::BLOCK & 1) * C::IDB +
+                                                       (tile % C::BLOCK * BK + (lane & 31)) * 4);
+    const bool ok = e < e_hi && id >= 0 && id <= t;
+    there = (uint32_t)__ballot(ok);
+    const int stand_in = __builtin_amdgcn_readlane(id, there ? __builtin_ctz(there) : 0);
+    return ok ? id : stand_in;
+  };
+  constexpr int REGIONS = BK / S::REGION_ROWS;  // loads of a tile's keys, and of its values
+  constexpr int PATTERNS = 16 / S::REGION_ROWS;  // regions after which the swizzle repeats
+  int col[PATTERNS];
 #pragma unroll
-    for (int d = 0; d < DP / 8; ++d) {
-      float t4 = 0.0f;
+  for (int i = 0; i < PATTERNS; ++i)
+    col[i] = min((lane & (DP / 8 - 1)) ^ S::swz(i * S::REGION_ROWS + lane * 16 / S::ROWB), a.D / 8 - 1) * 8;
+  auto load = [&](const uint16_t *base, int64_t stride, int id, uint32_t to) {
 #pragma unroll
-      for (int w = 0; w < NW; ++w) t4 += acc[(w * DP + d0 + d) * 33 + row];
-      out[d] = t4 * inv;
+    for (int i = 0; i < REGIONS; ++i) {
+      const int64_t key = __shfl(id, i * S::REGION_ROWS + lane * 16 / S::ROWB);
+      load_lds_16(base + key * stride + col[i % PATTERNS], to + i * 1024);
     }
-#pragma unroll
-    for (int d = 0; d < DP / 8; d += 8) {
-      if (d0 + d >= a.D) break;  // (D is a multiple of 8)
-      if (a.nsplit > 1) {
-        float *dst = a.part_o + ((int64_t)split * a.rows + out_row) * a.D + d0 + d;
-        *reinterpret_cast<float4 *>(dst) = make_float4(out[d], out[d + 1], out[d + 2], out[d + 3]);
-        *reinterpret_cast<float4 *>(dst + 4) = make_float4(out[d + 4], out[d + 5], out[d + 6], out[d + 7]);
+  };
+  // waits until at most the loads of one side (keys or values) of a tile are out
+  auto wait_side = [&](bool out) {
+    static_assert(REGIONS == 8 || REGIONS == 4, "loads of a side");
+    if (!out) wait_loads();
+    else if (REGIONS == 8) __builtin_amdgcn_s_waitcnt(0x0F78);  // vmcnt(8)
+    else __builtin_amdgcn_s_waitcnt(0x0F74);                    // vmcnt(4)
+    asm volatile("" ::: "memory");
+  };
+  if (ntile > 0) {
+    uint32_t there, there_next = 0;
+    load_ids(0);
+    wait_loads();
+    asm volatile("" ::: "memory");
+    int id = entries(0, there), id_next = 0;
+    if (there) load(kb, a.ks, id, mine), load(vb, a.vs, id, mine + TILE);
+    for (int j = 0; j < ntile; ++j) {
+      if (j % C::BLOCK == 0 && (j / C::BLOCK + 1) * C::BLOCK < ntile) load_ids(j / C::BLOCK + 1);
+      if (j + 1 < ntile) {
+        if ((j + 1) % C::BLOCK == 0) {  // the next block's ids, asked for 7 tiles ago
+          wait_loads();
+          asm volatile("" ::: "memory");
+        }
+        id_next = entries(j + 1, there_next);
       } else {
-        *reinterpret_cast<uint4 *>(a.o + out_row * a.D + d0 + d) =
-            make_uint4(pack_bf16(out[d], out[d + 1]), pack_bf16(out[d + 2], out[d + 3]),
-                       pack_bf16(out[d + 4], out[d + 5]), pack_bf16(out[d + 6], out[d + 7]));
+        there_next = 0;
       }
+      f32x16 s[1];
+      if (there) {
+        wait_side(true);  // the keys; the values may still be out
+        r.template scores<BK>(f, 0, s);
+        wait_reads();
+      }
+      if (there_next) load(kb, a.ks, id_next, mine);
+      if (there) {
+        r.weights(s, a.scale_log2, lane, there != 0xFFFFFFFFu, [&](int, int i) { return (there >> i) & 1; });
+        wait_side(there_next != 0);  // the values; the next keys may still be out
+        r.values(f, TILE, s);
+        wait_reads();
+      }
+      if (there_next) load(vb, a.vs, id_next, mine + TILE);
+      there = there_next, id = id_next;
     }
-    if ((threadIdx.x & 7) == 0) {
-      if (a.nsplit > 1) a.part_lse[(int64_t)split * a.rows + out_row] = lse;
-      else if (a.lse) a.lse[out_row] = lse;
-    }
+    wait_loads();
   }
+  join_waves<DP, NW>(a, r, lds, wave, lane, split, nrows,
+                     [&](int row) { return token * a.Hq + head + row; });
 }
 
 // Joins the splits of a row: o = sum_s 2^(lse_s - lse) o_s.  A wave per row; 16 splits at a
@@ -487,12 +563,12 @@ hipError_t launch_attend_t(const AttendPlan &p, const AttendArgs &a, hipStream_t
   const unsigned grid = (unsigned)(a.ntiles * a.nsplit * a.Hkv);
   hipError_t e;
   if (p.form == AttendPlan::kRows) {
-    const size_t lds = 4 * 4 * 32 * DP * 2;
-    e = with_lds(attend_rows_kernel<DP, false>, lds);
+    constexpr size_t lds = FewRows<DP>::LDS;
+    e = with_lds(attend_rows_kernel<DP>, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((attend_rows_kernel<DP, false>), dim3(grid), dim3(256), lds, st, a);
+    hipLaunchKernelGGL(attend_rows_kernel<DP>, dim3(grid), dim3(256), lds, st, a);
   } else {
-    const size_t lds = 4 * 64 * DP * 2;
+    constexpr size_t lds = 4 * 64 * DP * 2;
     e = with_lds(attend_tile_kernel<DP, kTileWaves>, lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((attend_tile_kernel<DP, kTileWaves>), dim3(grid), dim3(kTileWaves * 64), lds, st, a);
@@ -504,12 +580,11 @@ hipError_t launch_attend_t(const AttendPlan &p, const AttendArgs &a, hipStream_t
 
 template <int DP>
 hipError_t launch_list_t(const AttendArgs &a, hipStream_t st) {
-  const int G = a.Hq / a.Hkv;
-  const size_t lds = 4 * 4 * 32 * DP * 2;
-  hipError_t e = with_lds(attend_rows_kernel<DP, true>, lds);
+  const int64_t total = a.ntiles * ((a.Hq / a.Hkv + 31) / 32) * a.nsplit * a.Hkv;
+  hipError_t e = with_lds(attend_list_kernel<DP>, Lists<DP>::LDS);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attend_rows_kernel<DP, true>),
-                     dim3((unsigned)(a.ntiles * ((G + 31) / 32) * a.nsplit * a.Hkv)), dim3(256), lds, st, a);
+  hipLaunchKernelGGL(attend_list_kernel<DP>, dim3((unsigned)((total + 7) / 8 * 8)), dim3(512), Lists<DP>::LDS,
+                     st, a);
   e = hipGetLastError();
   if (e == hipSuccess && a.nsplit > 1) e = launch_join(a, st);
   return e;

@@ -150,10 +150,10 @@ __global__ __launch_bounds__(512) void bwd_keys_kernel(BwdArgs a) {
   // virtual rows that see the first key of the workgroup, cut to this part
   const int nvirt = Lq * G, off = Lk - Lq;
   auto seen_from = [&](int k) {
-    return k < Lk ? (int)min<int64_t>(nvirt, (int64_t)max(0, k - off) * G) : nvirt;
+    return k < Lk ? (int)min64(nvirt, (int64_t)max(0, k - off) * G) : nvirt;
   };
   const int n_lo = max(seen_from(at.n0) / 32 * 32, split * a.kchunk);
-  const int n_hi = (int)min<int64_t>(nvirt, (int64_t)split * a.kchunk + a.kchunk);
+  const int n_hi = (int)min64(nvirt, (int64_t)split * a.kchunk + a.kchunk);
   const int ntile = n_hi > n_lo ? (n_hi - n_lo + BR - 1) / BR : 0;
   if (a.ksplit > 1 && ntile == 0) return;  // (the sum does not read this part)
   // this lane's key is seen from virtual row `from` on, the group's first key from `some` on
@@ -350,7 +350,7 @@ __global__ __launch_bounds__(256) void bwd_keys_sum_kernel(BwdArgs a) {
   if (at.seq < 0 || key0 >= at.Lq) return;
   const int Lk = at.Lq, Lq = at.Lk, nvirt = Lq * G;
   // (the first virtual row of the keys' workgroup, as there)
-  const int first = (int)min<int64_t>(nvirt, (int64_t)max(0, at.n0 - (Lk - Lq)) * G) / 32 * 32;
+  const int first = (int)min64(nvirt, (int64_t)max(0, at.n0 - (Lk - Lq)) * G) / 32 * 32;
   const int s0 = first / a.kchunk, s1 = nvirt > first ? (nvirt - 1) / a.kchunk + 1 : s0;
   const int64_t pitch = a.Tk * a.Hkv * a.D;
   const int per = a.D / 4;
@@ -386,7 +386,7 @@ __global__ __launch_bounds__(NW * 64) void bwd_rows_kernel(BwdArgs a) {
   if (at.seq < 0) return;
   const int nrows = min(BQ, at.Lq * G - at.n0);
   const int t1 = (at.n0 + nrows - 1) / G + at.Lk - at.Lq;
-  const int k_lo = split * a.qchunk, k_hi = (int)min<int64_t>(t1 + 1, (int64_t)k_lo + a.qchunk);
+  const int k_lo = split * a.qchunk, k_hi = (int)min64(t1 + 1, (int64_t)k_lo + a.qchunk);
   const uint16_t *kb = (const uint16_t *)uniform_ptr(a.k + (int64_t)at.k_start * a.ks + (int64_t)kvh * a.D);
   const uint16_t *vb = (const uint16_t *)uniform_ptr(a.v + (int64_t)at.k_start * a.vs + (int64_t)kvh * a.D);
   const int n = at.n0 + wave * 32 + (lane & 31);
@@ -421,7 +421,7 @@ __global__ __launch_bounds__(NW * 64) void bwd_rows_kernel(BwdArgs a) {
   };
   auto step = [&](int j, auto buf_c) {
     constexpr int BUF = decltype(buf_c)::value;
-    __builtin_amdgcn_s_waitcnt(0x0F70);
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0), lgkmcnt(0)
     barrier_only();
     if (j + 1 < ntile) load(j + 1, BUF ^ 1);
     const int k0 = k_lo + j * BK;

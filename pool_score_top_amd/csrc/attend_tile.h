@@ -34,6 +34,9 @@ typedef short i16x4 __attribute__((ext_vector_type(4)));
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// (HIP's min of two integer types goes through double)
+__host__ __device__ inline int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
+
 template <int DP>
 struct Keys {
   static_assert(DP == 64 || DP == 128, "padded head dims");
@@ -134,6 +137,14 @@ __device__ inline void barrier_only() {
 // Waits for all of the wave's loads.  Before a loop it keeps the compiler, which would wait at
 // the first use, from doing so in every round, for that round's loads as well.
 __device__ inline void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+
+// Waits for the wave's LDS reads: what it read may then be overwritten, by its own loads or, past
+// a barrier, by others'.  (The values are long in use where this stands; it costs nothing and
+// does not leave to the instructions' order what has to hold.)
+__device__ inline void wait_reads() {
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  asm volatile("" ::: "memory");
+}
 
 // 2^x by the hardware's instruction (relative error about 2^-23; -inf gives 0)
 __device__ inline float exp2f_fast(float x) { return __builtin_amdgcn_exp2f(x); }
