@@ -510,8 +510,6 @@ hipError_t launch_bwd_t(const AttendCall &c, BwdArgs a, hipStream_t st) {
   }
   if (a.Tk > 0) {
     a.ktiles = make_table(a.table, c.cu_k_host, c.cu_q_host, a.nseq, 1, BwdKeys<DP>::KEYS, false);
-    e = with_lds(bwd_keys_kernel<DP>, BwdKeys<DP>::LDS);
-    if (e != hipSuccess) return e;
     hipLaunchKernelGGL(bwd_keys_kernel<DP>, dim3((unsigned)(a.ktiles * a.ksplit * a.Hkv)), dim3(512),
                        BwdKeys<DP>::LDS, st, a);
     e = hipGetLastError();

@@ -309,12 +309,4 @@ __device__ inline TileAt find_tile(const TileTable &tab, const int32_t *__restri
   return r;
 }
 
-template <class F>
-inline hipError_t with_lds(F *kernel, size_t bytes) {
-  // (a launch may use more than 64 KiB of LDS only where the kernel was told so)
-  return bytes > 65536 ? hipFuncSetAttribute((const void *)kernel,
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)
-                       : hipSuccess;
-}
-
 }  // namespace kpool

@@ -102,6 +102,7 @@ struct AttendPlan {
   int64_t ntiles;  // tiles of query rows, or more
   int nsplit;      // parts of the key axis, joined by a second kernel where there are more than one
   int chunk;       // keys of a part
+  bool by_place;   // lists: ordered by place in the sequence first
 };
 AttendPlan plan_attend(const int32_t *cu_q, const int32_t *cu_k, int nseq, int Hq, int Hkv);
 AttendPlan plan_list(int64_t Tq, int nseq, int width, int Hq, int Hkv);

@@ -296,26 +296,34 @@ class _OnDevice:
     t's device, so that outputs and workspaces allocated inside belong to that stream; gives
     its handle."""
 
+    __slots__ = ("device", "stream", "contexts")
+
     def __init__(self, t, stream):
-        self.device, self.stream = t.device, stream
-        self.contexts = []
+        self.device, self.stream, self.contexts = t.device, stream, ()
 
     def __enter__(self):
         import torch
-        if self.stream is None and torch.cuda.current_device() == self.device.index:
-            return torch.cuda.current_stream().cuda_stream
+        index = self.device.index
+        if self.stream is None and torch.cuda.current_device() == index:
+            return torch._C._cuda_getCurrentRawStream(index)
         if self.stream is not None and self.stream.device != self.device:
             raise ValueError(f"the stream is on {self.stream.device}, the tensors on {self.device}")
-        self.contexts = [torch.cuda.device(self.device)]
+        contexts = [torch.cuda.device(self.device)]
         if self.stream is not None:
-            self.contexts.append(torch.cuda.stream(self.stream))
-        for c in self.contexts:
+            contexts.append(torch.cuda.stream(self.stream))
+        for c in contexts:
             c.__enter__()
-        return torch.cuda.current_stream().cuda_stream
+        self.contexts = contexts
+        return torch._C._cuda_getCurrentRawStream(index)
 
     def __exit__(self, *exc):
         for c in reversed(self.contexts):
             c.__exit__(*exc)
+
+
+def _at(t):
+    """A tensor's address for a call (None for none)."""
+    return None if t is None else t.data_ptr()
 
 
 def _like(t, name, shape, dtype, device):
@@ -324,66 +332,71 @@ def _like(t, name, shape, dtype, device):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}")
 
 
-def _heads(t, name, device):
+def _heads(t, name, device, codes):
     """t as packed tokens [T, H, D] of bf16 with any token stride: (T, H, D, stride)."""
-    import torch
-    if not t.is_cuda or t.dim() != 3 or t.device != device:
+    shape = t.shape
+    if len(shape) != 3 or not t.is_cuda or t.device != device:
         raise ValueError(f"{name} must be a device tensor [T, heads, D] on {device}")
-    if t.dtype not in (torch.bfloat16, torch.int16):
+    if t.dtype not in codes:
         raise ValueError(f"{name} must be bfloat16 (or int16 bit patterns)")
-    T, H, D = t.shape
-    s = t.stride()
-    if (D > 1 and s[2] != 1) or (H > 1 and s[1] != D):
+    T, H, D = shape
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and D > 1) or (s1 != D and H > 1):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return T, H, D, s[0] if T > 1 else H * D
+    return T, H, D, s0 if T > 1 else H * D
 
 
 def _cu_pair(cu_q, cu_q_dev, cu_k, cu_k_dev, device):
-    """Host arrays (and their pointers) and device copies of both lengths; no keys' lengths
-    given: the queries'."""
+    """Host arrays and device copies of both lengths; no keys' lengths given: the queries'."""
     import torch
     if (cu_k is None) != (cu_k_dev is None):
         raise ValueError("give both cu_k and cu_k_dev, or neither")
-    cu_q, q_ptr = _host_i32(cu_q)
-    cu_k, k_ptr = (cu_q, q_ptr) if cu_k is None else _host_i32(cu_k)
-    cu_k_dev = cu_q_dev if cu_k_dev is None else cu_k_dev
+    cu_q = np.ascontiguousarray(cu_q, dtype=np.int32)
+    cu_k = cu_q if cu_k is None else np.ascontiguousarray(cu_k, dtype=np.int32)
     if cu_q.ndim != 1 or len(cu_q) < 2 or cu_k.shape != cu_q.shape:
         raise ValueError("cu_q and cu_k must be 1-dimensional with nseq + 1 entries each")
-    for t, name in ((cu_q_dev, "cu_q_dev"), (cu_k_dev, "cu_k_dev")):
-        _like(t, name, cu_q.shape, torch.int32, device)
-    return cu_q, q_ptr, cu_q_dev, cu_k, k_ptr, cu_k_dev
+    _like(cu_q_dev, "cu_q_dev", cu_q.shape, torch.int32, device)
+    if cu_k_dev is None:
+        cu_k_dev = cu_q_dev
+    else:
+        _like(cu_k_dev, "cu_k_dev", cu_q.shape, torch.int32, device)
+    return cu_q, cu_q_dev, cu_k, cu_k_dev
 
 
 class _Attend:
     """The arguments that the attention calls share, checked."""
 
     def __init__(self, q, k, v, cu_q, cu_q_dev, cu_k, cu_k_dev, scale):
-        self.device = q.device
-        tq, self.Hq, self.D, qs = _heads(q, "q", q.device)
-        tk, self.Hkv, d, ks = _heads(k, "k", q.device)
-        tv, hv, dv, vs = _heads(v, "v", q.device)
-        if (hv, dv) != (self.Hkv, self.D) or d != self.D:
+        import torch
+        codes = (torch.bfloat16, torch.int16)
+        self.device = device = q.device
+        tq, self.Hq, self.D, qs = _heads(q, "q", device, codes)
+        tk, self.Hkv, d, ks = _heads(k, "k", device, codes)
+        tv, hv, dv, vs = _heads(v, "v", device, codes)
+        if hv != self.Hkv or dv != d or d != self.D:
             raise ValueError("q, k and v must agree in D, and k and v in their heads")
-        self.cu_q, q_ptr, q_dev, self.cu_k, k_ptr, k_dev = _cu_pair(cu_q, cu_q_dev, cu_k, cu_k_dev, q.device)
+        self.cu_q, q_dev, self.cu_k, k_dev = _cu_pair(cu_q, cu_q_dev, cu_k, cu_k_dev, device)
+        q_ptr = self.cu_q.__array_interface__["data"][0]
+        k_ptr = q_ptr if self.cu_k is self.cu_q else self.cu_k.__array_interface__["data"][0]
         self.nseq = len(self.cu_q) - 1
         self.Tq, self.Tk = int(self.cu_q[-1]), int(self.cu_k[-1])
         if tq < self.Tq or min(tk, tv) < self.Tk:
             raise ValueError("q, k or v has fewer tokens than its cumulative lengths say")
         self.scale = float(np.float32(1.0) / np.sqrt(np.float32(self.D))) if scale is None else scale
         self.lens = (q_ptr, k_ptr, self.nseq, self.Hq, self.Hkv, self.D)
-        self.rows = (_p(q), qs, _p(k), ks, _p(v), vs)
-        self.cu = (q_ptr, _p(q_dev), k_ptr, _p(k_dev), self.nseq, self.Hq, self.Hkv, self.D, self.scale)
+        self.rows = (q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs)
+        self.cu = (q_ptr, q_dev.data_ptr(), k_ptr, k_dev.data_ptr(), self.nseq, self.Hq, self.Hkv, self.D, self.scale)
 
     def outputs(self, q, out, lse, want_lse):
         import torch
         if out is None:
-            out = torch.empty((self.Tq, self.Hq, self.D), dtype=q.dtype, device=self.device)
+            out = q.new_empty((self.Tq, self.Hq, self.D))
         else:
             _like(out, "out", (self.Tq, self.Hq, self.D), q.dtype, self.device)
         if lse is not None:
             _like(lse, "lse", (self.Tq, self.Hq), torch.float32, self.device)
         elif want_lse:
-            lse = torch.empty((self.Tq, self.Hq), dtype=torch.float32, device=self.device)
+            lse = q.new_empty((self.Tq, self.Hq), dtype=torch.float32)
         return out, lse
 
     def scratch(self, workspace, nbytes):
@@ -422,7 +435,7 @@ def attend(q, k, v, cu_q, cu_q_dev, cu_k=None, cu_k_dev=None, scale: float | Non
     with _OnDevice(q, stream) as s:
         out, lse = a.outputs(q, out, lse, want_lse)
         ws = a.scratch(workspace, int(lib().kpool_attend_workspace_bytes(*a.lens)))
-        rc = lib().kpool_attend(*a.rows, *a.cu, _p(ws), _bytes(ws, q.device), _p(out), _p(lse), s)
+        rc = lib().kpool_attend(*a.rows, *a.cu, _at(ws), _bytes(ws, q.device), _at(out), _at(lse), s)
     _check(rc, "kpool_attend")
     return out, lse
 
@@ -452,8 +465,8 @@ def attend_backward(d_o, q, k, v, o, lse, cu_q, cu_q_dev, cu_k=None, cu_k_dev=No
                 _like(t, name, shape, q.dtype, q.device)
             out.append(t)
         ws = a.scratch(workspace, int(lib().kpool_attend_backward_workspace_bytes(*a.lens)))
-        rc = lib().kpool_attend_backward(_p(d_o), *a.rows, _p(o), _p(lse), *a.cu, _p(ws),
-                                         _bytes(ws, q.device), *(_p(t) for t in out), s)
+        rc = lib().kpool_attend_backward(_at(d_o), *a.rows, _at(o), _at(lse), *a.cu, _at(ws),
+                                         _bytes(ws, q.device), *(_at(t) for t in out), s)
     _check(rc, "kpool_attend_backward")
     return tuple(out)
 
@@ -484,8 +497,8 @@ def attend_selected(q, k, v, token_ids, cu_q, cu_q_dev, cu_k=None, cu_k_dev=None
         out, lse = a.outputs(q, out, lse, want_lse)
         ws = a.scratch(workspace, int(lib().kpool_attend_selected_workspace_bytes(
             a.Tq, a.nseq, width, a.Hq, a.Hkv, a.D)))
-        rc = lib().kpool_attend_selected(*a.rows, _p(token_ids), width, *a.cu, _p(ws),
-                                         _bytes(ws, q.device), _p(out), _p(lse), s)
+        rc = lib().kpool_attend_selected(*a.rows, _at(token_ids), width, *a.cu, _at(ws),
+                                         _bytes(ws, q.device), _at(out), _at(lse), s)
     _check(rc, "kpool_attend_selected")
     return out, lse
 
@@ -523,8 +536,8 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, want_stat
         mean = rstd = None
         if want_stats:
             mean, rstd = (torch.empty(rows, dtype=torch.float32, device=x.device) for _ in range(2))
-        rc = lib().kpool_layer_norm(_p(x), stride, _p(weight), _p(bias), rows, N, ctypes.c_float(eps),
-                                    code, _p(out), _p(mean), _p(rstd), s)
+        rc = lib().kpool_layer_norm(_at(x), stride, _at(weight), _at(bias), rows, N, eps,
+                                    code, _at(out), _at(mean), _at(rstd), s)
     _check(rc, "kpool_layer_norm")
     return out, mean, rstd
 
@@ -551,9 +564,9 @@ def layer_norm_backward(dy, x, weight, mean, rstd, want_dx: bool = True, want_dw
         if workspace is None and (want_dweight or want_dbias):
             workspace = torch.empty(layer_norm_backward_workspace_bytes(rows, N), dtype=torch.uint8,
                                     device=x.device)
-        rc = lib().kpool_layer_norm_backward(_p(dy), _p(x), stride, _p(weight), _p(mean), _p(rstd), rows,
-                                             N, code, _p(workspace), _bytes(workspace, x.device), _p(dx),
-                                             _p(dw), _p(db), s)
+        rc = lib().kpool_layer_norm_backward(_at(dy), _at(x), stride, _at(weight), _at(mean), _at(rstd), rows,
+                                             N, code, _at(workspace), _bytes(workspace, x.device), _at(dx),
+                                             _at(dw), _at(db), s)
     _check(rc, "kpool_layer_norm_backward")
     return dx, dw, db
 
