@@ -16,9 +16,13 @@
 //   TPR 16 for rows of up to 16 vectors (a head dim of 128 in bf16): a wave holds 4 rows,
 //          so no lane idles, and sums take 4 lane exchanges.
 //   TPR 64 up to 256 vectors: a wave per row, no barrier.
-//   TPR 256 up to 2048 vectors: a workgroup per row.
+//   TPR 256 up to 1024 vectors, 2048 of one or four elements: a workgroup per row.
 //   Longer rows are read again for each pass (the second and third reads hit the caches).
 // VEC is 16 bytes where pointers and pitches allow it, one element otherwise.
+// Measured (the card copies at 4.75 TB/s, reads and writes counted): 524288 x 128 in bf16,
+// forward, 46 us (5.8 TB/s); 8192 x 4096 in bf16, forward 24 us (5.6 TB/s), backward 45 us (4.5
+// TB/s) and 4 us to join the sums; 5003 x 1237 in fp32 at a pitch of 1328, by single elements,
+// forward 12.5 us (4.0 TB/s), backward 16 us (4.6 TB/s).
 //
 // The weight's gradient sums over rows in a fixed order: every workgroup takes a
 // contiguous run of rows and keeps its columns' sums in registers, the workgroups'
@@ -33,51 +37,52 @@ namespace {
 
 constexpr int kNormThreads = 256;
 
+// VEC elements as they lie in memory, and as floats.
 template <class T, int VEC>
-struct Io;
-template <int VEC>
-struct Io<float, VEC> {
-  static __device__ inline void load(const float *p, float (&v)[VEC]) {
-    if constexpr (VEC == 4) {
-      const float4 a = *reinterpret_cast<const float4 *>(p);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    } else {
-      v[0] = p[0];
-    }
+struct Io {
+  static_assert(VEC == 1, "one element");
+  typedef T Raw;
+  static __device__ inline Raw fetch(const T *p) { return *p; }
+  static __device__ inline void unpack(Raw a, float (&v)[1]) {
+    v[0] = sizeof(T) == 4 ? (float)a : __uint_as_float((uint32_t)a << 16);
   }
-  static __device__ inline void store(float *p, const float (&v)[VEC]) {
-    if constexpr (VEC == 4)
-      *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    else
-      p[0] = v[0];
+  static __device__ inline void store(T *p, const float (&v)[1]) {
+    if constexpr (sizeof(T) == 4) *p = v[0];
+    else *p = (T)pack_bf16(v[0], 0.0f);
   }
 };
-template <int VEC>
-struct Io<uint16_t, VEC> {
-  static __device__ inline void load(const uint16_t *p, float (&v)[VEC]) {
-    if constexpr (VEC == 8) {
-      const uint4 a = *reinterpret_cast<const uint4 *>(p);
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      }
-    } else {
-      v[0] = __uint_as_float((uint32_t)p[0] << 16);
-    }
+template <>
+struct Io<float, 4> {
+  typedef float4 Raw;
+  static __device__ inline Raw fetch(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+  static __device__ inline void unpack(const Raw &a, float (&v)[4]) {
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
   }
-  static __device__ inline void store(uint16_t *p, const float (&v)[VEC]) {
-    if constexpr (VEC == 8) {
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-      *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-      p[0] = (uint16_t)pack_bf16(v[0], 0.0f);
-    }
+  static __device__ inline void store(float *p, const float (&v)[4]) {
+    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
   }
 };
+template <>
+struct Io<uint16_t, 8> {
+  typedef uint4 Raw;
+  static __device__ inline Raw fetch(const uint16_t *p) { return *reinterpret_cast<const uint4 *>(p); }
+  static __device__ inline void unpack(const Raw &a, float (&v)[8]) {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+  static __device__ inline void store(uint16_t *p, const float (&v)[8]) {
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                               pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+  }
+};
+template <class T, int VEC>
+__device__ inline void load(const T *p, float (&v)[VEC]) {
+  Io<T, VEC>::unpack(Io<T, VEC>::fetch(p), v);
+}
 
 template <int VEC>
 __device__ inline void load_f32(const float *p, float (&v)[VEC]) {
@@ -131,7 +136,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(
     for (int r = 0; r < R; ++r) {
       const int c = col + r * TPR * VEC;
       if (row0 + i < rows && c < N) {
-        Io<T, VEC>::load(x + (row0 + i) * x_stride + c, v[i][r]);
+        load<T, VEC>(x + (row0 + i) * x_stride + c, v[i][r]);
       } else {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) v[i][r][e] = 0.0f;
@@ -199,7 +204,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_long_kernel(
   const T *xr = x + row * x_stride;
   float v[VEC], wv[VEC], bv[VEC], s[1] = {0.0f};
   for (int c = threadIdx.x * VEC; c < N; c += kNormThreads * VEC) {
-    Io<T, VEC>::load(xr + c, v);
+    load<T, VEC>(xr + c, v);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) s[0] += v[e];
   }
@@ -207,14 +212,14 @@ __global__ __launch_bounds__(kNormThreads) void norm_long_kernel(
   const float inv_n = 1.0f / (float)N, mean = s[0] * inv_n;
   s[0] = 0.0f;
   for (int c = threadIdx.x * VEC; c < N; c += kNormThreads * VEC) {
-    Io<T, VEC>::load(xr + c, v);
+    load<T, VEC>(xr + c, v);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) s[0] = fmaf(v[e] - mean, v[e] - mean, s[0]);
   }
   row_sum<256, 1>(s, red, phase);
   const float rstd = 1.0f / sqrtf(fmaf(s[0], inv_n, eps));
   for (int c = threadIdx.x * VEC; c < N; c += kNormThreads * VEC) {
-    Io<T, VEC>::load(xr + c, v);
+    load<T, VEC>(xr + c, v);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) wv[e] = 1.0f, bv[e] = 0.0f;
     if (w) load_f32<VEC>(w + c, wv);
@@ -249,22 +254,34 @@ __global__ __launch_bounds__(kNormThreads) void norm_bwd_kernel(
     for (int e = 0; e < VEC; ++e) wv[r][e] = 1.0f, dw[r][e] = db[r][e] = 0.0f;
     if (w && col + r * TPR * VEC < N) load_f32<VEC>(w + col + r * TPR * VEC, wv[r]);
   }
-  for (int64_t base = lo; base < hi; base += GROUPS) {  // the same trips for all groups
-    const int64_t row = base + group;
-    const bool ok = row < hi;
-    const float mu = ok ? mean[row] : 0.0f, rs = ok ? rstd[row] : 0.0f;
-    float xh[R][VEC], g[R][VEC], s[2] = {0.0f, 0.0f};
+  // The next row is fetched before this one's sums: a row's loads and the last row's exchanges
+  // and barrier then run side by side.
+  typename Io<T, VEC>::Raw xn[R] = {}, gn[R] = {};
+  float mun = 0.0f, rsn = 0.0f;
+  auto fetch = [&](int64_t row) {
+    if (row >= hi) return;
+    mun = mean[row], rsn = rstd[row];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int c = col + r * TPR * VEC;
-      const bool in = ok && c < N;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) xh[r][e] = mu, g[r][e] = 0.0f;
-      if (in) {
-        Io<T, VEC>::load(x + row * x_stride + c, xh[r]);
-        Io<T, VEC>::load(dy + row * N + c, g[r]);
-      }
+      if (c < N) xn[r] = Io<T, VEC>::fetch(x + row * x_stride + c), gn[r] = Io<T, VEC>::fetch(dy + row * N + c);
     }
+  };
+  fetch(lo + group);
+  for (int64_t base = lo; base < hi; base += GROUPS) {  // the same trips for all groups
+    const int64_t row = base + group;
+    const bool ok = row < hi;
+    const float mu = mun, rs = rsn;
+    float xh[R][VEC], g[R][VEC], s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      Io<T, VEC>::unpack(xn[r], xh[r]);
+      Io<T, VEC>::unpack(gn[r], g[r]);
+      if (!ok || col + r * TPR * VEC >= N)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) xh[r][e] = mu, g[r][e] = 0.0f;
+    }
+    fetch(row + GROUPS);
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -336,8 +353,8 @@ __global__ __launch_bounds__(kNormThreads) void norm_bwd_long_kernel(
 #pragma unroll
   for (int e = 0; e < VEC; ++e) wv[e] = 1.0f;
   for (int c = threadIdx.x * VEC; c < N; c += kNormThreads * VEC) {
-    Io<T, VEC>::load(x + row * x_stride + c, xv);
-    Io<T, VEC>::load(dy + row * N + c, g);
+    load<T, VEC>(x + row * x_stride + c, xv);
+    load<T, VEC>(dy + row * N + c, g);
     if (w) load_f32<VEC>(w + c, wv);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
@@ -348,8 +365,8 @@ __global__ __launch_bounds__(kNormThreads) void norm_bwd_long_kernel(
   row_sum<256, 2>(s, red, phase);
   const float c2 = s[0] * inv_n, c1 = s[1] * inv_n;
   for (int c = threadIdx.x * VEC; c < N; c += kNormThreads * VEC) {
-    Io<T, VEC>::load(x + row * x_stride + c, xv);
-    Io<T, VEC>::load(dy + row * N + c, g);
+    load<T, VEC>(x + row * x_stride + c, xv);
+    load<T, VEC>(dy + row * N + c, g);
     if (w) load_f32<VEC>(w + c, wv);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) g[e] = rs * (g[e] * wv[e] - c2 - (xv[e] - mu) * rs * c1);
@@ -369,8 +386,8 @@ __global__ __launch_bounds__(kNormThreads) void norm_cols_kernel(
   float dw = 0.0f, db = 0.0f;
   for (int64_t r = lo; r < hi; ++r) {
     float g[1], xv[1];
-    Io<T, 1>::load(dy + r * N + c, g);
-    Io<T, 1>::load(x + r * x_stride + c, xv);
+    load<T, 1>(dy + r * N + c, g);
+    load<T, 1>(x + r * x_stride + c, xv);
     db += g[0];
     dw = fmaf(g[0], (xv[0] - mean[r]) * rstd[r], dw);
   }
@@ -411,6 +428,11 @@ constexpr int64_t kNormLaunchRows = int64_t(1) << 23;
 template <class T>
 constexpr int kVec = 16 / sizeof(T);
 
+// whether 6 and 8 vectors of a row fit a thread's registers beside the sums (with 8 bf16 a
+// vector they would take over 256 and leave a wave a SIMD)
+template <int VEC>
+constexpr bool kWide = VEC <= 4;
+
 // (the pitch counts only where there is a second row)
 template <class T>
 bool vector_ok(const void *x, int64_t x_stride, int N, const void *w, const void *b, const void *y,
@@ -440,8 +462,10 @@ void norm_pick(const void *x, int64_t xs, const float *w, const float *b, int64_
   else if (nv <= 128) KPOOL_NORM(64, 2, 1);
   else if (nv <= 256) KPOOL_NORM(64, 4, 1);
   else if (nv <= 512) KPOOL_NORM(256, 2, 1);
+  else if (nv <= 768) KPOOL_NORM(256, 3, 1);
   else if (nv <= 1024) KPOOL_NORM(256, 4, 1);
-  else if (nv <= 2048 && VEC <= 4) KPOOL_NORM(256, 8, 1);
+  else if (kWide<VEC> && nv <= 1536) KPOOL_NORM(256, kWide<VEC> ? 6 : 1, 1);
+  else if (kWide<VEC> && nv <= 2048) KPOOL_NORM(256, kWide<VEC> ? 8 : 1, 1);
   else
     hipLaunchKernelGGL((norm_long_kernel<T, VEC>), dim3((unsigned)rows), dim3(kNormThreads), 0, st,
                        (const T *)x, xs, w, b, N, eps, (T *)y, mean, rstd);
@@ -462,8 +486,10 @@ void norm_bwd_pick(const void *dy, const void *x, int64_t xs, const float *w, co
   else if (nv <= 128) KPOOL_NORM(64, 2);
   else if (nv <= 256) KPOOL_NORM(256, 1);
   else if (nv <= 512) KPOOL_NORM(256, 2);
+  else if (nv <= 768) KPOOL_NORM(256, 3);
   else if (nv <= 1024) KPOOL_NORM(256, 4);
-  else if (nv <= 2048 && VEC <= 4) KPOOL_NORM(256, 8);
+  else if (kWide<VEC> && nv <= 1536) KPOOL_NORM(256, kWide<VEC> ? 6 : 1);
+  else if (kWide<VEC> && nv <= 2048) KPOOL_NORM(256, kWide<VEC> ? 8 : 1);
   else {
     for (int64_t r = 0; dx && r < rows; r += kNormLaunchRows) {
       const int64_t n = rows - r < kNormLaunchRows ? rows - r : kNormLaunchRows;
@@ -502,14 +528,14 @@ hipError_t launch_norm(bool f32, const void *x, int64_t x_stride, const float *w
   return hipSuccess;
 }
 
-// Row runs of the backward pass, by the sizes alone: at most 1024 workgroups, runs of 16
-// rows or more, and partial sums of at most 8 MiB (an eighth of what 64 MiB of rows move)
-// unless that leaves fewer than 128 workgroups.
+// Row runs of the backward pass, by the sizes alone: at most 1024 workgroups, runs of 8 rows
+// or more, and partial sums of at most 8 MiB, unless that leaves fewer than 128 workgroups
+// (8192 x 4096 in bf16: 256 workgroups 80 us a step, 512 the same, 1024 95 us).
 int norm_bwd_blocks(int64_t rows, int32_t N) {
   int64_t most = (int64_t(1) << 20) / N;
   if (most > 1024) most = 1024;
   if (most < 128) most = 128;
-  const int64_t want = rows > 16 ? (rows + 15) / 16 : 1;
+  const int64_t want = rows > 8 ? (rows + 7) / 8 : 1;
   return (int)(want < most ? want : most);
 }
 

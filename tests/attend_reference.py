@@ -101,11 +101,13 @@ def cu_of(lens):
 
 def check_backward(q, k, v, d_o, o, lse, cu_q, cu_k, scale, dq, dk, dv):
     """The gradients of every sequence and key head against the formulas in 64 bits with the
-    given o and lse (as the backward pass has them).
+    given lse (as the backward pass has it).
 
-    P = exp(s - lse) has the relative error ep = 4 e + 16 u (1 + |lse|); dP and delta are sums
-    of D products (D + 8) u; dS = P (dP - delta) carries both and is rounded to bf16 (h) for
-    its products, as P is; sums over n rows or keys add n u, the outputs' rounding h.
+    P = exp(s - lse) has the relative error ep = 4 e + 16 u (1 + |lse|); dP is a sum of D
+    products (D + 8) u; delta = sum P dP may be taken as sum do o with the forward pass's o,
+    which is off by (h + 4 e + 3 n u) sum p |v| and h |o| (see above); dS = P (dP - delta)
+    carries these and is rounded to bf16 (h) for its products, as P is; sums over n rows or
+    keys add n u, the outputs' rounding h.
 
     Below 2^-126, the smallest normal number of fp32 and bf16, the hardware's 2^x and the
     matrix products give 0 (no subnormals), whatever the relative bounds say: P, dS and each
@@ -128,10 +130,14 @@ def check_backward(q, k, v, d_o, o, lse, cu_q, cu_k, scale, dq, dk, dv):
             e = torch.where(seen, scale * (qq.abs() @ kk.abs().t()) * (D + 8) * U, 0.0).amax(1, keepdim=True) \
                 if lq else p.sum(1, keepdim=True)
             ep = 4 * e + 16 * U * (1 + l64.abs().clamp(max=1e30) * (l64 > -math.inf))
-            dp, delta = ee @ vv.t(), (ee * oo).sum(1, keepdim=True)
+            dp = ee @ vv.t()
+            delta = (p * dp).sum(1, keepdim=True)
             ds = p * (dp - delta)
-            e2 = (D + 8) * U * (ee.abs() @ vv.abs().t() + (ee * oo).abs().sum(1, keepdim=True))
             n = (lq * G + lk + 64) * U
+            o_off = (H + 4 * e + 3 * n) * (p @ vv.abs())
+            o_off = o_off + H * ((p @ vv).abs() + o_off)
+            e2 = (D + 8) * U * (ee.abs() @ vv.abs().t() + (ee * oo).abs().sum(1, keepdim=True))
+            e2 = e2 + (ee.abs() * o_off).sum(1, keepdim=True)
             tiny = 2.0 ** -126
             bp = p * (H + ep + 2 * n) + tiny * seen
             bs = ds.abs() * (H + ep + 2 * n) + 2 * p * e2 + tiny * (1 + (dp - delta).abs()) * seen
