@@ -541,49 +541,50 @@ __global__ __launch_bounds__(Lists<DP>::NW * 64, 2) void attend_list_kernel(Atte
                      [&](int row) { return token * a.Hq + head + row; });
 }
 
-// Joins the splits of a row: o = sum_s 2^(lse_s - lse) o_s.  A wave per row; 16 splits at a
-// time, whose loads go out together.  A split that saw nothing has lse -inf and was not
-// written: its weight is 0 and it is not read.
+// Joins the splits of a row: o = sum_s 2^(lse_s - lse) o_s, 4 columns a lane, 64 / (D / 4) rows
+// a workgroup, whose 4 waves take every fourth split each.  A split that saw nothing has lse
+// -inf: its weight is 0 and its o is not read.  The loads do not wait for one another.
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (row >= a.rows) return;
+  __shared__ float part[4][64][5];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int per = a.D / 4, rows = 64 / per;  // (lanes past rows * per repeat the last row's)
+  const int r = min(lane / per, rows - 1), d = min(lane - r * per, per - 1) * 4;
+  const int64_t row = min64((int64_t)blockIdx.x * rows + r, a.rows - 1);
   const float none = -__builtin_inff();
+  const float *lse = a.part_lse + row;
   float m = none;
-  for (int s = lane; s < a.nsplit; s += 64) m = fmaxf(m, a.part_lse[(int64_t)s * a.rows + row]);
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+#pragma unroll 8
+  for (int s = 0; s < a.nsplit; ++s) m = fmaxf(m, lse[(int64_t)s * a.rows]);
   const float shift = m > none ? m : 0.0f;
-  float total = 0.0f, o0 = 0.0f, o1 = 0.0f;
-  const int d = min(lane * 2, a.D - 2);
-  for (int s0 = 0; s0 < a.nsplit; s0 += 16) {
-    // lane s: the weight of split s0 + s
-    const int mine = s0 + (lane & 15);
-    float w = mine < a.nsplit ? a.part_lse[(int64_t)mine * a.rows + row] : none;
-    w = w > none ? exp2f_fast((w - shift) * kLog2e) : 0.0f;
-    float2 v[16];
+  float total = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int s = wave; s < a.nsplit; s += 4) {
+    const float x = lse[(int64_t)s * a.rows];
+    const float w = exp2f_fast((x - shift) * kLog2e);
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (x > none) v = *reinterpret_cast<const float4 *>(a.part_o + ((int64_t)s * a.rows + row) * a.D + d);
+    total += w;
+    o[0] = fmaf(w, v.x, o[0]), o[1] = fmaf(w, v.y, o[1]), o[2] = fmaf(w, v.z, o[2]), o[3] = fmaf(w, v.w, o[3]);
+  }
 #pragma unroll
-    for (int s = 0; s < 16; ++s) {
-      v[s] = make_float2(0.0f, 0.0f);
-      if (__builtin_amdgcn_readlane(__float_as_uint(w), s) != 0)  // (the same for the wave)
-        v[s] = *reinterpret_cast<const float2 *>(a.part_o + ((int64_t)(s0 + s) * a.rows + row) * a.D + d);
-    }
+  for (int i = 0; i < 4; ++i) part[wave][lane][i] = o[i];
+  part[wave][lane][4] = total;
+  __syncthreads();
+  if (wave != 0 || lane >= rows * per || (int64_t)blockIdx.x * rows + r >= a.rows) return;
 #pragma unroll
-    for (int s = 0; s < 16; ++s) {
-      const float ws = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), s));
-      total += ws;
-      o0 = fmaf(ws, v[s].x, o0);
-      o1 = fmaf(ws, v[s].y, o1);
-    }
+  for (int w = 1; w < 4; ++w) {
+    total += part[w][lane][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] += part[w][lane][i];
   }
   const float inv = total > 0.0f ? 1.0f / total : 0.0f;
-  if (lane * 2 < a.D)
-    *reinterpret_cast<uint32_t *>(a.o + row * a.D + d) = pack_bf16(o0 * inv, o1 * inv);
-  if (lane == 0 && a.lse) a.lse[row] = total > 0.0f ? shift + log2f(total) * kLn2 : none;
+  *reinterpret_cast<uint2 *>(a.o + row * a.D + d) =
+      make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+  if (d == 0 && a.lse) a.lse[row] = total > 0.0f ? shift + log2f(total) * kLn2 : none;
 }
 
 hipError_t launch_join(const AttendArgs &a, hipStream_t st) {
-  hipLaunchKernelGGL(attend_join_kernel, dim3((unsigned)((a.rows + 3) / 4)), dim3(256), 0, st, a);
+  hipLaunchKernelGGL(attend_join_kernel, dim3((unsigned)((a.rows + 256 / a.D - 1) / (256 / a.D))), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
@@ -659,7 +660,8 @@ AttendPlan plan_attend(const int32_t *cu_q, const int32_t *cu_k, int nseq, int H
   }
   p.nsplit = 1, p.chunk = 0x7FFFFF00;
   if (wgs >= 256) return p;
-  const int64_t chunk = round_up(walked / 512 > 1024 ? walked / 512 : 1024, 256);
+  const int64_t least = p.form == AttendPlan::kRows ? 1024 : 512;
+  const int64_t chunk = round_up(walked / 512 > least ? walked / 512 : least, 256);
   if (most_keys > chunk) p.nsplit = (int)((most_keys + chunk - 1) / chunk), p.chunk = (int)chunk;
   return p;
 }
