@@ -1,0 +1,118 @@
+"""The layer as it is used: index keys normalised, pooled, scored, selected, expanded, and the
+attention over what was selected, through Selector.run(k_norm=) and Selector.attend.
+
+Each step is checked against its own reference on the step's actual inputs: the normalised keys
+against the library's own layer_norm (which test_gpu_norm.py checks), the selection by its
+oracle on those keys, the attention against 64 bits over the token ids that the selection gave
+(tolerances: attend_reference.py)."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from attend_reference import check, make, sequences
+from gpu_helpers import check_selection_vs_oracle
+from pool_score_top_amd import kpool as K
+from pool_score_top_amd import synth
+
+BF16 = torch.bfloat16
+
+
+def layer(cu, kpool, budget, seed, Hq=8, Hkv=2, D=64, tail=False, q_lo=0, q_hi=None):
+    wl = synth.workload("sq4096", T=int(cu[-1]), kpool=kpool, budget=budget)
+    r = synth.host_inputs(wl, seed)
+    dev = {n: torch.from_numpy(r[n].view(np.int16) if r[n].dtype == np.uint16 else r[n]).cuda()
+           for n in ("q", "k", "w")}
+    g = torch.Generator().manual_seed(seed)
+    norm = ((1 + 0.2 * torch.randn(128, generator=g)).cuda(), torch.randn(128, generator=g).cuda(), 1e-6)
+    sel = K.Selector(cu, kpool, budget, 32, 128, tail=tail, q_lo=q_lo, q_hi=q_hi)
+    out = sel.run(dev["q"], dev["k"], dev["w"], k_norm=norm)
+    cu = np.asarray(cu)
+    qkv = [t[:int(cu[-1])] for t in make(cu, cu, Hq, Hkv, D, seed + 1)]
+    o, lse = sel.attend(*qkv, want_lse=True)
+    return sel, r, dev, norm, out, qkv, o, lse
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cu,kpool,budget,tail", [
+    ([0, 700, 701, 701, 1500], 4, 64, False), ([0, 700, 701, 701, 1500], 4, 64, True),
+    ([0, 1003], 1, 200, False), ([0, 300, 1200], 5, 7, False), ([0, 90, 400], 4, 128, False),
+    ([0, 90, 401], 4, 128, True)])
+def test_the_layer(cu, kpool, budget, tail):
+    sel, r, dev, norm, out, (q, k, v), o, lse = layer(cu, kpool, budget, 3, tail=tail)
+    k_n = K.layer_norm(dev["k"], *norm)[0]
+    bits = k_n.cpu().numpy().view(np.uint16)
+    ref = oracle.select(r["q"], bits, r["w"], np.asarray(cu, np.int32), kpool, budget, tail=tail)
+    np.testing.assert_array_equal(out["kp"].cpu().numpy().view(np.uint16), ref["kp"])
+    cu_pools, _ = oracle.count_pools(cu, kpool, tail=tail)
+    seq, t = oracle.row_positions(np.arange(cu[-1]), cu)
+    nvis = oracle.visible_pools(t, kpool, cu_pools[seq + 1] - cu_pools[seq])
+    check_selection_vs_oracle(out["pool_ids"].cpu().numpy(), ref["scores"], nvis, budget, "layer")
+    check(q, k, v, np.asarray(cu), np.asarray(cu), 1.0 / 8, o, lse, out["token_ids"])
+
+
+@pytest.mark.gpu
+def test_whole_attention_where_everything_is_selected():
+    """budget pools cover every sequence: the lists name every visible token, and both ways of
+    the attention agree with 64 bits over them."""
+    cu = [0, 90, 400]
+    sel, _, _, _, out, (q, k, v), o, lse = layer(cu, 4, 128, 5)
+    assert sel.max_pools <= sel.budget
+    for a, b, _, _ in sequences(cu, cu):
+        ids = out["token_ids"][a:b].long().sort(1).values
+        want = torch.arange(b - a, device="cuda")
+        assert torch.equal((ids[:, :, None] == want).any(1), want <= want[:, None])
+    (cu_q, cu_k), (cqd, ckd) = sel.attend_cu, sel.attend_cu_dev
+    by_list = K.attend_selected(q, k, v, out["token_ids"], cu_q, cqd, cu_k, ckd, want_lse=True)
+    for got in ((o, lse), by_list):
+        check(q, k, v, np.asarray(cu), np.asarray(cu), 1.0 / 8, *got, out["token_ids"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("budget", [32, 400])
+def test_row_ranges_equal_the_whole(budget):
+    """Ranges that cut sequences: their rows' tokens are the whole batch's, bit for bit, and the
+    attention of them (whose sums run in another order) obeys the same bounds."""
+    cu = [0, 300, 1000, 1500]
+    sel, _, _, _, out, qkv, o, lse = layer(cu, 4, budget, 7)
+    for lo, hi in ((0, 200), (200, 1100), (1100, 1500), (650, 651), (1500, 1500)):
+        part = layer(cu, 4, budget, 7, q_lo=lo, q_hi=hi)
+        assert torch.equal(part[4]["token_ids"], out["token_ids"][lo:hi])
+        assert part[6].shape == (hi - lo, 8, 64)
+        cu_q, cu_k = part[0].attend_cu
+        check(qkv[0][lo:hi], qkv[1], qkv[2], cu_q, cu_k, 1.0 / 8, part[6], part[7], part[4]["token_ids"])
+
+
+@pytest.mark.gpu
+def test_captured_layer_replays_equal_eager():
+    cu = [0, 500, 900]
+    sel, _, dev, norm, out, (q, k, v), o, lse = layer(cu, 4, 32, 9)
+
+    def step():
+        out = sel.run(dev["q"], dev["k"], dev["w"], k_norm=norm)
+        return (out["token_ids"],) + sel.attend(q, k, v, want_lse=True)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for i in range(4):
+        dev["k"].copy_(torch.from_numpy(synth.host_inputs(synth.workload("sq4096", T=900), 40 + i)["k"]
+                                        .view(np.int16)))
+        for t in got:
+            t.fill_(3)
+        graph.replay()
+        torch.cuda.synchronize()
+        first = [t.clone() for t in got]
+        assert all(torch.equal(a, b) for a, b in zip(first, step()))
+
+
+def test_row_range():
+    cu_q, cu_k = K.row_range([0, 300, 1000, 1500], 200, 1100)
+    assert cu_q.tolist() == [0, 100, 800, 900] and cu_k.tolist() == [0, 300, 1000, 1100]
+    cu_q, cu_k = K.row_range([0, 300, 1000], 300, 300)
+    assert cu_q.tolist() == [0, 0, 0] and cu_k.tolist() == [0, 300, 300]
+    for lo, hi in ((-1, 3), (4, 3), (0, 1001)):
+        with pytest.raises(ValueError):
+            K.row_range([0, 300, 1000], lo, hi)
