@@ -427,8 +427,8 @@ int check_lengths(const char *fn, const int32_t *cu_q, const int32_t *cu_k, int3
   if (!rc) rc = check_cu(cu_k, nseq, fn);
   if (rc) return rc;
   for (int32_t s = 0; s < nseq; ++s)  // (a tile's rows are numbered in 32 bits)
-    if ((int64_t)(cu_q[s + 1] - cu_q[s]) * G > 0x7FFFFF00)
-      return fail(KPOOL_EUNSUPPORTED, "%s: sequence %d has too many query rows", fn, s);
+    if ((int64_t)(cu_q[s + 1] - cu_q[s]) * G > 0x7FFFFF00 || cu_k[s + 1] - cu_k[s] > 0x7FFFFF00)
+      return fail(KPOOL_EUNSUPPORTED, "%s: sequence %d has too many query rows or keys", fn, s);
   return KPOOL_OK;
 }
 
@@ -458,8 +458,8 @@ int check_attend(const char *fn, kpool::AttendCall &c, const int32_t *cu_q_host,
 
 int check_attend_plan(const char *fn, const kpool::AttendCall &c, const kpool::AttendPlan &p, int64_t per,
                       const void *workspace, size_t workspace_bytes) {
-  // workgroups of up to 512 threads; a launch's threads stay below 2^32
-  if (p.ntiles * per * p.nsplit * c.Hkv >= (int64_t(1) << 23))
+  // a launch's threads stay below 2^32: workgroups of 512 for tiles, of 256 else
+  if (p.ntiles * per * p.nsplit * c.Hkv >= (int64_t(1) << (p.form == kpool::AttendPlan::kTiles ? 23 : 24)) - 8)
     return fail(KPOOL_EUNSUPPORTED, "%s: too many query rows for one launch", fn);
   const size_t need = kpool::attend_workspace(p, c.Tq * c.Hq, c.D);
   if (need && (!workspace || workspace_bytes < need))
@@ -692,7 +692,7 @@ int kpool_attend_backward(const uint16_t *d_o, const uint16_t *q, int64_t q_stri
   const kpool::BwdPlan p = kpool::plan_attend_bwd(cu_q_host, cu_k_host, nseq, Hq, Hkv);
   const int64_t most = int64_t(1) << 23, sums = std::max(c.Tq * Hq, c.Tk * Hkv) * D / 1024;
   if (p.ktiles * p.ksplit * Hkv >= most || p.qtiles * p.qsplit * Hkv >= most || c.Tq * Hq / 16 >= most ||
-      sums >= most)
+      sums >= most || (p.ksplit > 1 && p.ktiles * Hkv >= most / 16))
     return fail(KPOOL_EUNSUPPORTED, "%s: too many rows for one launch", fn);
   const size_t need = kpool::attend_bwd_workspace(p, c.Tq, c.Tk, Hq, Hkv, D);
   if (need && (!workspace || workspace_bytes < need))

@@ -304,7 +304,7 @@ class _OnDevice:
     def __enter__(self):
         import torch
         index = self.device.index
-        if self.stream is None and torch.cuda.current_device() == index:
+        if self.stream is None and torch._C._cuda_getDevice() == index:  # (t has initialised HIP)
             return torch._C._cuda_getCurrentRawStream(index)
         if self.stream is not None and self.stream.device != self.device:
             raise ValueError(f"the stream is on {self.stream.device}, the tensors on {self.device}")
@@ -328,7 +328,7 @@ def _at(t):
 
 def _like(t, name, shape, dtype, device):
     """An output or parameter given by the caller: contiguous, of this shape, type and device."""
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}")
 
 
@@ -506,16 +506,20 @@ def attend_selected(q, k, v, token_ids, cu_q, cu_q_dev, cu_k=None, cu_k_dev=None
 def _norm_rows(x, name):
     """x as rows: (rows, N, row stride, dtype code)."""
     import torch
-    codes = {torch.bfloat16: KPOOL_DTYPE_BF16, torch.int16: KPOOL_DTYPE_BF16,
-             torch.float32: KPOOL_DTYPE_F32}
-    if not x.is_cuda or x.dim() != 2:
+    shape, dtype = x.shape, x.dtype
+    if len(shape) != 2 or not x.is_cuda:
         raise ValueError(f"{name} must be a device tensor of rows [rows, N]")
-    if x.dtype not in codes:
+    if dtype == torch.float32:
+        code = KPOOL_DTYPE_F32
+    elif dtype == torch.bfloat16 or dtype == torch.int16:
+        code = KPOOL_DTYPE_BF16
+    else:
         raise ValueError(f"{name} must be bfloat16 (or int16 bit patterns) or float32")
-    rows, N = x.shape
-    if N < 1 or (N > 1 and x.stride(1) != 1) or (rows > 1 and x.stride(0) < N):
+    rows, N = shape
+    s0, s1 = x.stride()
+    if N < 1 or (N > 1 and s1 != 1) or (rows > 1 and s0 < N):
         raise ValueError(f"{name} must hold contiguous rows that do not overlap")
-    return rows, N, x.stride(0) if rows > 1 else N, codes[x.dtype]
+    return rows, N, s0 if rows > 1 else N, code
 
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, want_stats: bool = False,
@@ -525,19 +529,21 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, want_stat
     are what layer_norm_backward reads, and None unless want_stats."""
     import torch
     rows, N, stride, code = _norm_rows(x, "x")
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        if t is not None:
-            _like(t, name, (N,), torch.float32, x.device)
+    device = x.device
+    if weight is not None:
+        _like(weight, "weight", (N,), torch.float32, device)
+    if bias is not None:
+        _like(bias, "bias", (N,), torch.float32, device)
     if out is not None:
-        _like(out, "out", (rows, N), x.dtype, x.device)
+        _like(out, "out", (rows, N), x.dtype, device)
     with _OnDevice(x, stream) as s:
         if out is None:
-            out = torch.empty((rows, N), dtype=x.dtype, device=x.device)
+            out = x.new_empty((rows, N))
         mean = rstd = None
         if want_stats:
-            mean, rstd = (torch.empty(rows, dtype=torch.float32, device=x.device) for _ in range(2))
-        rc = lib().kpool_layer_norm(_at(x), stride, _at(weight), _at(bias), rows, N, eps,
-                                    code, _at(out), _at(mean), _at(rstd), s)
+            mean, rstd = x.new_empty((2, rows), dtype=torch.float32).unbind()
+        rc = lib().kpool_layer_norm(x.data_ptr(), stride, _at(weight), _at(bias), rows, N, eps, code,
+                                    out.data_ptr(), _at(mean), _at(rstd), s)
     _check(rc, "kpool_layer_norm")
     return out, mean, rstd
 
@@ -557,10 +563,9 @@ def layer_norm_backward(dy, x, weight, mean, rstd, want_dx: bool = True, want_dw
     if not (want_dx or want_dweight or want_dbias):
         raise ValueError("no output is wanted")
     with _OnDevice(x, stream) as s:
-        f32 = dict(dtype=torch.float32, device=x.device)
-        dx = torch.empty((rows, N), dtype=x.dtype, device=x.device) if want_dx else None
-        dw = torch.empty(N, **f32) if want_dweight else None
-        db = torch.empty(N, **f32) if want_dbias else None
+        dx = x.new_empty((rows, N)) if want_dx else None
+        dw = x.new_empty(N, dtype=torch.float32) if want_dweight else None
+        db = x.new_empty(N, dtype=torch.float32) if want_dbias else None
         if workspace is None and (want_dweight or want_dbias):
             workspace = torch.empty(layer_norm_backward_workspace_bytes(rows, N), dtype=torch.uint8,
                                     device=x.device)
