@@ -198,9 +198,9 @@ __global__ __launch_bounds__(NW * 64) void attend_tile_kernel(AttendArgs a) {
   const int G = a.Hq / a.Hkv;
   int64_t idx = blockIdx.x;
   const int kvh = (int)(idx % a.Hkv);
-  idx /= a.Hkv;
-  const int split = (int)(idx % a.nsplit);
-  const TileAt at = find_tile(a.table, a.cu_q, a.cu_k, a.nseq, G, BQ, idx / a.nsplit, a.ntiles, lane);
+  idx = spread(idx / a.Hkv, a.ntiles * a.nsplit);
+  const int split = (int)(idx / a.ntiles);
+  const TileAt at = find_tile(a.table, a.cu_q, a.cu_k, a.nseq, G, BQ, idx - split * a.ntiles, a.ntiles, lane);
   if (at.seq < 0) return;
   const int nrows = min(BQ, at.Lq * G - at.n0);
   const int t1 = (at.n0 + nrows - 1) / G + at.Lk - at.Lq;  // the last row's position
@@ -334,9 +334,9 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendArgs a) {
   const int G = a.Hq / a.Hkv;
   int64_t idx = blockIdx.x;
   const int kvh = (int)(idx % a.Hkv);
-  idx /= a.Hkv;
-  const int split = (int)(idx % a.nsplit);
-  const TileAt at = find_tile(a.table, a.cu_q, a.cu_k, a.nseq, G, 32, idx / a.nsplit, a.ntiles, lane);
+  idx = spread(idx / a.Hkv, a.ntiles * a.nsplit);
+  const int split = (int)(idx / a.ntiles);
+  const TileAt at = find_tile(a.table, a.cu_q, a.cu_k, a.nseq, G, 32, idx - split * a.ntiles, a.ntiles, lane);
   if (at.seq < 0) return;
   const int n = at.n0 + (lane & 31), tok = n / G, head = kvh * G + n - tok * G;
   const int nrows = min(32, at.Lq * G - at.n0);

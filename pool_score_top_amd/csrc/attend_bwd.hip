@@ -138,10 +138,10 @@ __global__ __launch_bounds__(512) void bwd_keys_kernel(BwdArgs a) {
   const int G = a.Hq / a.Hkv;
   int64_t idx = blockIdx.x;
   const int kvh = (int)(idx % a.Hkv);
-  idx /= a.Hkv;
-  const int split = (int)(idx % a.ksplit);
+  idx = spread(idx / a.Hkv, a.ktiles * a.ksplit);
+  const int split = (int)(idx / a.ktiles);
   // (tiles of keys: the roles of the two length arrays are exchanged)
-  const TileAt at = find_tile(a.table, a.cu_k, a.cu_q, a.nseq, 1, C::KEYS, idx / a.ksplit, a.ktiles, lane);
+  const TileAt at = find_tile(a.table, a.cu_k, a.cu_q, a.nseq, 1, C::KEYS, idx - split * a.ktiles, a.ktiles, lane);
   if (at.seq < 0) return;
   const int k_start = at.q_start, Lk = at.Lq, q_start = at.k_start, Lq = at.Lk;
   const int key = at.n0 + group * 32 + (lane & 31);  // this lane's key, of the sequence
@@ -386,9 +386,9 @@ __global__ __launch_bounds__(NW * 64) void bwd_rows_kernel(BwdArgs a) {
   const int G = a.Hq / a.Hkv;
   int64_t idx = blockIdx.x;
   const int kvh = (int)(idx % a.Hkv);
-  idx /= a.Hkv;
-  const int split = (int)(idx % a.qsplit);
-  const TileAt at = find_tile(a.table, a.cu_q, a.cu_k, a.nseq, G, BQ, idx / a.qsplit, a.qtiles, lane);
+  idx = spread(idx / a.Hkv, a.qtiles * a.qsplit);
+  const int split = (int)(idx / a.qtiles);
+  const TileAt at = find_tile(a.table, a.cu_q, a.cu_k, a.nseq, G, BQ, idx - split * a.qtiles, a.qtiles, lane);
   if (at.seq < 0) return;
   const int nrows = min(BQ, at.Lq * G - at.n0);
   const int t1 = (at.n0 + nrows - 1) / G + at.Lk - at.Lq;
