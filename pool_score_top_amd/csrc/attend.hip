@@ -382,40 +382,50 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendArgs a) {
   });
 }
 
-// Rows with lists of tokens: a workgroup takes up to 32 heads of one token and key head; its
-// 4 waves take list tiles of 32 in turn and join at the end.  The keys come from all over
-// memory, so what counts is how many bytes are on their way, and how many of them from the L2.
+// Rows with lists of tokens.  A unit of work is up to 32 heads of one token and key head (and
+// one part of its list); WR waves share it, each taking list tiles of 32 in turn, and join at
+// the end.  The keys come from all over memory, so what counts is how many bytes are on their
+// way, and how many of them from the L2.
 //   Each wave has one LDS buffer for keys and one for values, asks for the next tile's keys as
-//   soon as S is computed and for its values after the product with P.  Two workgroups fit a
-//   CU, so that one's start and end run beside the other's loads (with 8 waves and one
-//   workgroup a CU, 2048 rows of 2048 tokens take 502 us instead of 410).
-//   The list is taken in blocks of 2048 entries, which first drop the entries outside 0 .. t
-//   and, where a.by_place, are put into 16 groups by their place in the sequence (a counting
-//   sort, stable, so the sums' order is the same every time).  Workgroups of one XCD (every
-//   8th) take consecutive tokens of one key head and walk the sequence in the same direction
-//   at about the same time, so what several of them selected is read from memory once: with
-//   rows that each pick 2048 of 65536 tokens at random the L2 serves 30% of the loads
-//   instead of 12% (549 us without it, 502 with it, at 8 waves).
+//   soon as S is computed and for its values after the product with P.  Two workgroups of 4
+//   waves fit a CU (with 8 waves and one workgroup, 2048 rows of 2048 tokens take 502 us
+//   instead of 410).
+//   The list is taken in blocks, which first drop the entries outside 0 .. t and, where
+//   a.by_place, are put into 16 groups by their place in the sequence (a counting sort, stable,
+//   so the sums' order is the same every time).  Workgroups of one XCD (every 8th) take
+//   consecutive tokens of one key head and walk the sequence in the same direction at about
+//   the same time, so what several of them selected is read from memory once.
+//   WR = 1, where there are rows enough: the 256 rows that an XCD then works on at a time
+//   pass a sixteenth of the sequence together and share more of it than 64 rows that each go
+//   by four times as fast, and no waves have to join.
+// L2 hits and time, 2048 rows that each pick 2048 of 65536 tokens at random, 32 heads over 2:
+//   by place, WR = 1: 47%, 355 us;  WR = 4: 30%, 410 us;  in the list's order: 12%, 549 us (at 8
+//   waves a workgroup).
 // The last tile of a block may be short: its absent entries read the tile's first key, so that
 // no other key is read, and count for nothing.
-template <int DP>
+template <int DP, int WR>
 struct Lists {
   static constexpr int NW = 4, BK = 32, TILE = BK * Keys<DP>::ROWB;
-  static constexpr int BLOCK = 2048, EACH = BLOCK / (NW * 64), GROUPS = 16;
-  static constexpr int IDS = NW * 2 * TILE, COUNT = IDS + BLOCK * 4, USE = COUNT + (GROUPS * NW + 1) * 4;
-  static constexpr int LDS = USE > Join<DP, NW>::LDS ? USE : Join<DP, NW>::LDS;
+  static constexpr int UNITS = NW / WR;                           // of a workgroup
+  static constexpr int BLOCK = WR == 1 ? 1024 : 2048, EACH = BLOCK / (WR * 64), GROUPS = 16;
+  static constexpr int IDS = NW * 2 * TILE, USE = IDS + UNITS * BLOCK * 4;
+  // (a unit's counts, [GROUPS][WR] and their total, lie in its first wave's tile buffer: a
+  // block is sorted when no tile is in use or on its way)
+  static_assert((GROUPS * WR + 1) * 4 <= 2 * TILE, "counts in a tile buffer");
+  static constexpr int LDS = WR > 1 && Join<DP, NW>::LDS > USE ? Join<DP, NW>::LDS : USE;
 };
-template <int DP>
-__global__ __launch_bounds__(Lists<DP>::NW * 64, 2) void attend_list_kernel(AttendArgs a) {
+template <int DP, int WR>
+__global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendArgs a) {
   using S = Keys<DP>;
-  using C = Lists<DP>;
+  using C = Lists<DP, WR>;
   constexpr int BK = C::BK, NW = C::NW, TILE = C::TILE;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int G = a.Hq / a.Hkv, per = (G + 31) / 32;
-  const int64_t each = a.ntiles * per * a.nsplit, total = each * a.Hkv;  // workgroups: of a key head, all
-  int64_t idx = (blockIdx.x & 7) * ((total + 7) / 8) + (blockIdx.x >> 3);
+  const int64_t each = a.ntiles * per * a.nsplit, total = each * a.Hkv;  // units: of a key head, all
+  const int64_t wgs = (total + C::UNITS - 1) / C::UNITS;
+  int64_t idx = ((blockIdx.x & 7) * ((wgs + 7) / 8) + (blockIdx.x >> 3)) * C::UNITS + wave / WR;
   if (idx >= total) return;
   const int kvh = (int)(idx / each);
   idx -= kvh * each;
@@ -435,8 +445,13 @@ __global__ __launch_bounds__(Lists<DP>::NW * 64, 2) void attend_list_kernel(Atte
   const uint32_t mine = lds_offset(lds) + wave * 2 * TILE;
   Frag<DP> f;
   f.init(mine, lane);
-  int *ids = reinterpret_cast<int *>(lds + C::IDS);
-  int *count = reinterpret_cast<int *>(lds + C::COUNT);  // [GROUPS][NW], then the total
+  const int part = wave % WR;  // of the unit's waves
+  int *ids = reinterpret_cast<int *>(lds + C::IDS) + wave / WR * C::BLOCK;
+  int *count = reinterpret_cast<int *>(lds + (wave - part) * 2 * TILE);  // [GROUPS][WR], then the total
+  auto sync = [&] {  // of the unit's waves
+    if (WR > 1) __syncthreads();
+    else wait_reads();  // (a wave's own LDS accesses go in order)
+  };
   const int e_lo = split * a.chunk, e_hi = (int)min64(a.width, (int64_t)e_lo + a.chunk);
   // group of an id: by_place the top 4 bits of the sequence's positions, else one for all
   const int shift = a.by_place ? max(0, 28 - __clz(max(at.Lk - 1, 1))) : 31;
@@ -467,7 +482,7 @@ __global__ __launch_bounds__(Lists<DP>::NW * 64, 2) void attend_list_kernel(Atte
     int id[C::EACH], group[C::EACH], rank[C::EACH];
 #pragma unroll
     for (int i = 0; i < C::EACH; ++i) {
-      const int e = block + i * NW * 64 + threadIdx.x;
+      const int e = block + i * WR * 64 + part * 64 + lane;
       id[i] = e < e_hi ? list[e] : -1;
       group[i] = id[i] >= 0 && id[i] <= t ? id[i] >> shift : -1;
     }
@@ -482,47 +497,43 @@ __global__ __launch_bounds__(Lists<DP>::NW * 64, 2) void attend_list_kernel(Atte
         if (group[i] == g) rank[i] = n + before;
         n += __popcll(m);
       }
-      if (lane == 0) count[g * NW + wave] = n;
+      if (lane == 0) count[g * WR + part] = n;
     }
-    __syncthreads();
-    if (wave == 0) {  // counts to starts
-      constexpr int PER = C::GROUPS * NW / 64;  // counts a lane
-      static_assert(PER * 64 == C::GROUPS * NW, "whole lanes");
-      int c[PER], sum = 0;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) c[i] = lane * PER + i < ngroups * NW ? count[lane * PER + i] : 0, sum += c[i];
-      const int own = sum;
+    sync();
+    if (part == 0) {  // counts to starts
+      static_assert(C::GROUPS * WR <= 64, "a count a lane");
+      const int c = lane < ngroups * WR ? count[lane] : 0;
+      int sum = c;
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {
         const int up = __shfl_up(sum, d);
         if (lane >= d) sum += up;
       }
-      int start = sum - own;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) count[lane * PER + i] = start, start += c[i];
-      if (lane == 63) count[C::GROUPS * NW] = sum;
+      if (lane < C::GROUPS * WR) count[lane] = sum - c;
+      if (lane == 63) count[C::GROUPS * WR] = sum;
     }
-    __syncthreads();
+    sync();
 #pragma unroll
     for (int i = 0; i < C::EACH; ++i)
-      if (group[i] >= 0) ids[count[group[i] * NW + wave] + rank[i]] = id[i];
-    const int present = count[C::GROUPS * NW];
-    __syncthreads();
+      if (group[i] >= 0) ids[count[group[i] * WR + part] + rank[i]] = id[i];
+    const int present = count[C::GROUPS * WR];
+    wait_reads();  // (the tiles' loads overwrite the counts)
+    sync();
 
-    // this wave's tiles: wave, wave + NW, ..
+    // this wave's tiles: part, part + WR, ..
     const int ntile = (present + BK - 1) / BK;
     auto entry = [&](int tile) {
       const int e = tile * BK + (lane & 31);
       return ids[e < present ? e : tile * BK];
     };
-    int j = wave;
+    int j = part;
     if (j < ntile) {
       const int e = entry(j);
       load(kb, a.ks, e, mine), load(vb, a.vs, e, mine + TILE);
     }
-    for (; j < ntile; j += NW) {
-      const bool more = j + NW < ntile;
-      const int next = more ? entry(j + NW) : 0;
+    for (; j < ntile; j += WR) {
+      const bool more = j + WR < ntile;
+      const int next = more ? entry(j + WR) : 0;
       f32x16 s[1];
       wait_side(true);  // the keys; the values may still be out
       r.template scores<BK>(f, 0, s);
@@ -535,10 +546,15 @@ __global__ __launch_bounds__(Lists<DP>::NW * 64, 2) void attend_list_kernel(Atte
       wait_reads();
       if (more) load(vb, a.vs, next, mine + TILE);
     }
-    __syncthreads();  // (the next block's ids go where these were)
+    sync();  // (the next block's ids go where these were)
   }
-  join_waves<DP, NW>(a, r, lds, wave, lane, split, nrows,
-                     [&](int row) { return token * a.Hq + head + row; });
+  if constexpr (WR > 1) {
+    join_waves<DP, NW>(a, r, lds, wave, lane, split, nrows,
+                       [&](int row) { return token * a.Hq + head + row; });
+  } else {
+    const float l = r.l + other_half(r.l);
+    if ((lane & 31) < nrows) write_row<DP>(a, token * a.Hq + head + (lane & 31), split, r.o, r.m, l, lane);
+  }
 }
 
 // Joins the splits of a row: o = sum_s 2^(lse_s - lse) o_s, 4 columns a lane, 64 / (D / 4) rows
@@ -604,10 +620,12 @@ hipError_t launch_attend_t(const AttendPlan &p, const AttendArgs &a, hipStream_t
   return e;
 }
 
-template <int DP>
+template <int DP, int WR>
 hipError_t launch_list_t(const AttendArgs &a, hipStream_t st) {
-  const int64_t total = a.ntiles * ((a.Hq / a.Hkv + 31) / 32) * a.nsplit * a.Hkv;
-  hipLaunchKernelGGL(attend_list_kernel<DP>, dim3((unsigned)((total + 7) / 8 * 8)), dim3(Lists<DP>::NW * 64), Lists<DP>::LDS,
+  using C = Lists<DP, WR>;
+  const int64_t units = a.ntiles * ((a.Hq / a.Hkv + 31) / 32) * a.nsplit * a.Hkv;
+  const int64_t wgs = (units + C::UNITS - 1) / C::UNITS;
+  hipLaunchKernelGGL((attend_list_kernel<DP, WR>), dim3((unsigned)((wgs + 7) / 8 * 8)), dim3(C::NW * 64), C::LDS,
                      st, a);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && a.nsplit > 1) e = launch_join(a, st);
@@ -677,6 +695,10 @@ AttendPlan plan_list(int64_t Tq, int nseq, int width, int Hq, int Hkv) {
   if (p.nsplit <= 1) p.nsplit = 1, p.chunk = 0x7FFFFF00;
   // sharing takes several workgroups an XCD at a time
   p.by_place = wgs >= 256;
+  // a wave per row where that fills the 256 CUs' 8 waves (lists of 2048, units and us by four
+  // waves and by one: 1024 110 113, 1536 159 174, 2048 208 179, 4096 409 349, 8192
+  // 791 708)
+  p.wave_rows = wgs >= 2048;
   return p;
 }
 
@@ -690,7 +712,8 @@ hipError_t launch_attend_list(const AttendCall &c, const AttendPlan &p, const in
   AttendArgs a = make_args(c, p, workspace);
   a.ids = ids, a.width = width;
   a.by_place = p.by_place;
-  return c.D <= 64 ? launch_list_t<64>(a, st) : launch_list_t<128>(a, st);
+  if (p.wave_rows) return c.D <= 64 ? launch_list_t<64, 1>(a, st) : launch_list_t<128, 1>(a, st);
+  return c.D <= 64 ? launch_list_t<64, 4>(a, st) : launch_list_t<128, 4>(a, st);
 }
 
 }  // namespace kpool

@@ -103,6 +103,7 @@ struct AttendPlan {
   int nsplit;      // parts of the key axis, joined by a second kernel where there are more than one
   int chunk;       // keys of a part
   bool by_place;   // lists: ordered by place in the sequence first
+  bool wave_rows;  // lists: a wave a row instead of four
 };
 AttendPlan plan_attend(const int32_t *cu_q, const int32_t *cu_k, int nseq, int Hq, int Hkv);
 AttendPlan plan_list(int64_t Tq, int nseq, int width, int Hq, int Hkv);

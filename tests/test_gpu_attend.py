@@ -307,3 +307,30 @@ def test_binding_refuses():
             f()
     with pytest.raises(K.KpoolError):
         K.attend(q, k, k, cu, cud, scale=-1.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 8, 64), (40, 4, 128), (3, 1, 16)])
+def test_selected_many_rows(Hq, Hkv, D):
+    """Enough rows for a wave each; lists of several blocks of 1024 entries."""
+    q_lens, k_lens = [1500, 0, 700], [1500, 3, 4000]
+    cu_q, cqd = cu_of(q_lens)
+    cu_k, ckd = cu_of(k_lens)
+    q, k, v = make(cu_q, cu_k, Hq, Hkv, D, 31)
+    for width, kind in ((130, "ragged"), (2100, "full")):
+        ids = lists(cu_q, cu_k, width, 3, kind)
+        o, lse = K.attend_selected(q, k, v, ids, cu_q, cqd, cu_k, ckd, want_lse=True)
+        check(q, k, v, cu_q, cu_k, 1.0 / D ** 0.5, o, lse, ids)
+        assert torch.equal(o, K.attend_selected(q, k, v, ids, cu_q, cqd, cu_k, ckd)[0])
+
+
+@pytest.mark.gpu
+def test_more_sequences_than_the_table():
+    """Tokens, chunks and lists of 70 sequences, some empty (found by search on the device)."""
+    rng = np.random.default_rng(4)
+    k_lens = [int(x) for x in rng.integers(0, 300, 70)]
+    for q_lens in ([min(1, n) for n in k_lens], [int(rng.integers(0, n + 1)) for n in k_lens]):
+        q, k, v, cu, o, lse = run(q_lens, k_lens, 4, 2, 64, 8)
+        ids = lists(cu[0], cu[2], 40, 5, "ragged")
+        o, lse = K.attend_selected(q, k, v, ids, *cu, want_lse=True)
+        check(q, k, v, cu[0], cu[2], 0.125, o, lse, ids)

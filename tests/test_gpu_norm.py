@@ -270,3 +270,13 @@ def test_binding_refuses_other_tensors(bad):
         x = x.cuda()
     with pytest.raises(ValueError):
         K.layer_norm(bad(x))
+
+
+@pytest.mark.gpu
+def test_more_rows_than_a_launch():
+    """2^23 + 9 rows of 3: two launches."""
+    rows = (1 << 23) + 9
+    x = torch.randn(rows, 3, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    y, mean, rstd = K.layer_norm(x, eps=1e-3, want_stats=True)
+    for part in (slice(0, 1000), slice((1 << 23) - 500, rows)):
+        check_forward(x[part], None, None, 1e-3, y[part], mean[part], rstd[part])
