@@ -67,7 +67,7 @@ int check_norm(const char *fn, int64_t rows, int32_t N, int64_t x_stride, int32_
   if (dtype != KPOOL_DTYPE_BF16 && dtype != KPOOL_DTYPE_F32)
     return fail(KPOOL_EINVAL, "%s: unknown dtype %d", fn, dtype);
   if (rows < 0) return fail(KPOOL_EINVAL, "%s: rows must be >= 0", fn);
-  if (N < 1 || N > (1 << 30)) return fail(KPOOL_EINVAL, "%s: N must be in [1, 2^30] (got %d)", fn, N);
+  if (N < 1 || N > (1 << 26)) return fail(KPOOL_EINVAL, "%s: N must be in [1, 2^26] (got %d)", fn, N);
   if (x_stride < N) return fail(KPOOL_EINVAL, "%s: x_stride must be >= N", fn);
   return KPOOL_OK;
 }
@@ -754,6 +754,7 @@ int kpool_layer_norm(const void *x, int64_t x_stride, const float *weight, const
   if (!(eps >= 0.0f) || !isfinite(eps)) return fail(KPOOL_EINVAL, "%s: eps must be finite and >= 0", fn);
   if (rows == 0) return ok();
   if (!x || !y) return fail(KPOOL_EINVAL, "%s: null pointer", fn);
+  if (x == y) return fail(KPOOL_EINVAL, "%s: y must not be x", fn);
   const uintptr_t mask = dtype == KPOOL_DTYPE_F32 ? 3 : 1;
   if ((((uintptr_t)x | (uintptr_t)y) & mask) ||
       (((uintptr_t)weight | (uintptr_t)bias | (uintptr_t)mean | (uintptr_t)rstd) & 3))

@@ -666,7 +666,10 @@ AttendPlan plan_attend(const int32_t *cu_q, const int32_t *cu_k, int nseq, int H
     if (lq > 0) most_rows = most_rows > lq * G ? most_rows : lq * G, most_keys = most_keys > lk ? most_keys : lk;
   }
   AttendPlan p;
-  p.form = most_rows <= 64 ? AttendPlan::kRows : AttendPlan::kTiles;
+  // 32 virtual rows fill one wave's tile; from there on sharing key tiles among waves is as good
+  // (us by the rows kernel and the tile kernel, D = 128, 4 key heads: 8 sequences of 8192 keys, 32
+  // rows 27 35, 64 rows 43 38, 128 rows 56 48; one of 16384 keys, 32 rows 24 24, 64 rows 26 25)
+  p.form = most_rows <= 32 ? AttendPlan::kRows : AttendPlan::kTiles;
   const int BQ = p.form == AttendPlan::kRows ? 32 : kTileWaves * 32;
   p.ntiles = tile_start(cu_q[nseq], nseq, (int)G, BQ);
   // workgroups, and the keys that all of them walk, without a split

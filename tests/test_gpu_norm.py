@@ -214,7 +214,7 @@ def test_captured_step_replays_equal_eager():
 # ---------------------------------------------------------------------------
 
 def _c(**kw):
-    a = dict(x=16, stride=128, w=16, b=16, rows=4, N=128, eps=1e-6, dtype=0, y=16, mean=16, rstd=16)
+    a = dict(x=16, stride=128, w=16, b=16, rows=4, N=128, eps=1e-6, dtype=0, y=32, mean=16, rstd=16)
     a.update(kw)
     return K.lib().kpool_layer_norm(a["x"], a["stride"], a["w"], a["b"], a["rows"], a["N"], a["eps"],
                                     a["dtype"], a["y"], a["mean"], a["rstd"], None)
@@ -232,7 +232,7 @@ def _c_bwd(**kw):
 @pytest.mark.parametrize("kw", [
     dict(rows=-1), dict(N=0), dict(stride=127), dict(eps=-1.0), dict(eps=float("nan")),
     dict(eps=float("inf")), dict(dtype=2), dict(x=None), dict(y=None), dict(x=17), dict(y=18, dtype=1),
-    dict(w=18), dict(mean=17)])
+    dict(w=18), dict(mean=17), dict(y=16), dict(N=(1 << 26) + 1, stride=1 << 30)])
 def test_layer_norm_refuses(kw):
     assert _c(**kw) == K.KPOOL_EINVAL
     assert K.lib().kpool_last_error()
