@@ -678,10 +678,13 @@ class Selector:
         overlap = self.overlap if overlap is None else overlap
         if k_norm is not None:
             weight, bias, eps = k_norm
-            with _on(stream):
-                if self.k_normed is None or self.k_normed.dtype != k.dtype:
-                    self.k_normed = k.new_empty(k.shape)
-            k = layer_norm(k, weight, bias, eps, out=self.k_normed, stream=stream)[0]
+            if k.dim() != 2 or k.shape[0] < self.T or k.element_size() != 2:
+                raise ValueError(f"k must be bfloat16 (or int16 bit patterns) with {self.T} rows")
+            if self.k_normed is None:  # (for good: a captured run keeps writing there)
+                with _on(stream):
+                    self.k_normed = k.new_empty((self.T, self.D))
+            g = None if g is None else g[:self.T]
+            k = layer_norm(k[:self.T], weight, bias, eps, out=self.k_normed.view(k.dtype), stream=stream)[0]
         if g is not None:
             pool_keys_gated(k, g, ape, self.cu, self.cu_dev, self.cu_pools_dev, self.kpool,
                             out=self.kp, stream=stream, tail=self.tail)

@@ -108,6 +108,23 @@ def test_captured_layer_replays_equal_eager():
         assert all(torch.equal(a, b) for a, b in zip(first, step()))
 
 
+@pytest.mark.gpu
+def test_normed_keys_have_one_place():
+    """Rows behind the batch are left out, types of the same bits share the buffer, and other
+    keys are refused."""
+    cu = [0, 100, 333]
+    sel, _, dev, norm, out, _, _, _ = layer(cu, 4, 32, 11)
+    ids, place = out["token_ids"].clone(), sel.k_normed.data_ptr()
+    k = dev["k"]
+    wide = torch.cat([k, torch.full((5, 128), float("nan"), device="cuda").to(BF16).view(k.dtype)])
+    for keys in (wide, k.view(BF16), torch.cat([wide, wide], 1)[:, :128]):
+        got = sel.run(dev["q"], keys, dev["w"], k_norm=norm)
+        assert torch.equal(got["token_ids"], ids) and sel.k_normed.data_ptr() == place
+    for bad in (k[:332], k.view(BF16).float(), k[:, :64], k[None]):
+        with pytest.raises(ValueError):
+            sel.run(dev["q"], bad, dev["w"], k_norm=norm)
+
+
 def test_row_range():
     cu_q, cu_k = K.row_range([0, 300, 1000, 1500], 200, 1100)
     assert cu_q.tolist() == [0, 100, 800, 900] and cu_k.tolist() == [0, 300, 1000, 1100]
