@@ -280,7 +280,8 @@ int kpool_attend(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t
  *   dq       bf16 [Tq, Hq, D];  dk, dv  bf16 [Tk, Hkv, D], contiguous, overwritten (0 for a
  *            row that sees nothing and a key that no row sees)
  *   workspace  kpool_attend_backward_workspace_bytes bytes, 16-byte aligned; scratch
- * The other arguments are the forward call's, and d_o must be finite as well.  Sums are fp32
+ * The other arguments are the forward call's, and d_o must be finite as well; the outputs
+ * overlap neither inputs nor one another.  Sums are fp32
  * in a fixed order (no atomics): the same call gives the same bits. */
 size_t kpool_attend_backward_workspace_bytes(const int32_t *cu_q_host, const int32_t *cu_k_host,
                                              int32_t nseq, int32_t Hq, int32_t Hkv, int32_t D);
@@ -333,7 +334,8 @@ int kpool_layer_norm(const void *x, int64_t x_stride, const float *weight, const
  *   dweight[j] = sum_r dy * xh,   dbias[j] = sum_r dy            (fp32 sums)
  *   dy       [rows, N] contiguous;  x, x_stride, weight as in the forward call
  *   mean, rstd  fp32 [rows] from it
- *   dx       NULLABLE [rows, N];  dweight, dbias  NULLABLE fp32 [N], overwritten
+ *   dx       NULLABLE [rows, N] contiguous, not overlapping x or dy
+ *   dweight, dbias  NULLABLE fp32 [N], overwritten
  *   workspace  kpool_layer_norm_backward_workspace_bytes(rows, N) bytes where dweight or
  *            dbias is given (NULL and 0 otherwise), 16-byte aligned; scratch on return
  * The sums over rows run in a fixed order: the same inputs give the same bits.  rows 0

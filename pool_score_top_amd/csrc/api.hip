@@ -63,6 +63,17 @@ int check_cu(const int32_t *cu, int32_t nseq, const char *fn) {
   return KPOOL_OK;
 }
 
+// Whether the n bytes at `out` meet one of `rows` rows of `len` bytes, `pitch` bytes apart from
+// `in` on (pitch >= len).
+bool meets(const void *out, int64_t n, const void *in, int64_t rows, int64_t len, int64_t pitch) {
+  if (!out || !in || n <= 0 || rows <= 0 || len <= 0) return false;
+  // the first row that ends behind `out`'s start, if that one starts before its end
+  const int64_t from = (int64_t)((uintptr_t)out - (uintptr_t)in);
+  const int64_t r = from < len ? 0 : (from - len) / pitch + 1;
+  return r < rows && r * pitch < from + n;
+}
+bool meets(const void *out, int64_t n, const void *in, int64_t len) { return meets(out, n, in, 1, len, len); }
+
 int check_norm(const char *fn, int64_t rows, int32_t N, int64_t x_stride, int32_t dtype) {
   if (dtype != KPOOL_DTYPE_BF16 && dtype != KPOOL_DTYPE_F32)
     return fail(KPOOL_EINVAL, "%s: unknown dtype %d", fn, dtype);
@@ -456,6 +467,24 @@ int check_attend(const char *fn, kpool::AttendCall &c, const int32_t *cu_q_host,
   return KPOOL_OK;
 }
 
+// n bytes of an output apart from q, k and v
+int check_apart(const char *fn, const kpool::AttendCall &c, const char *name, const void *out, int64_t n) {
+  if (meets(out, n, c.q, c.Tq, c.Hq * c.D * 2, c.q_stride * 2) ||
+      meets(out, n, c.k, c.Tk, c.Hkv * c.D * 2, c.k_stride * 2) ||
+      meets(out, n, c.v, c.Tk, c.Hkv * c.D * 2, c.v_stride * 2))
+    return fail(KPOOL_EINVAL, "%s: %s overlaps q, k or v", fn, name);
+  return KPOOL_OK;
+}
+
+int check_outputs(const char *fn, const kpool::AttendCall &c) {
+  const int64_t rows = c.Tq * c.Hq;
+  int rc = check_apart(fn, c, "o", c.o, rows * c.D * 2);
+  if (!rc && c.lse) rc = check_apart(fn, c, "lse", c.lse, rows * 4);
+  if (!rc && meets(c.lse, rows * 4, c.o, rows * c.D * 2))
+    return fail(KPOOL_EINVAL, "%s: lse overlaps o", fn);
+  return rc;
+}
+
 int check_attend_plan(const char *fn, const kpool::AttendCall &c, const kpool::AttendPlan &p, int64_t per,
                       const void *workspace, size_t workspace_bytes) {
   // a launch's threads stay below 2^32: workgroups of 512 for tiles, of 256 else
@@ -655,6 +684,7 @@ int kpool_attend(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t
   if (rc || c.Tq == 0) return rc;
   const kpool::AttendPlan p = kpool::plan_attend(cu_q_host, cu_k_host, nseq, Hq, Hkv);
   rc = check_attend_plan(fn, c, p, 1, workspace, workspace_bytes);
+  if (!rc) rc = check_outputs(fn, c);
   if (rc) return rc;
   hipStream_t st = (hipStream_t)stream;
   hipError_t e = timed(6, st, [&] { return kpool::launch_attend(c, p, workspace, st); });
@@ -685,10 +715,10 @@ int kpool_attend_backward(const uint16_t *d_o, const uint16_t *q, int64_t q_stri
   int rc = check_attend(fn, c, cu_q_host, cu_k_host);
   if (rc) return rc;
   if (c.Tq == 0 && c.Tk == 0) return ok();
-  if (!cu_q_dev || !cu_k_dev || (c.Tq > 0 && (!d_o || !lse || !dq)) || (c.Tk > 0 && (!dk || !dv)))
+  if (!cu_q_dev || !cu_k_dev || (c.Tq > 0 && (!d_o || !lse || !dq)) || (c.Tk > 0 && (!k || !v || !dk || !dv)))
     return fail(KPOOL_EINVAL, "%s: null pointer", fn);
-  if (!aligned16(d_o) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
-    return fail(KPOOL_EINVAL, "%s: d_o, dq, dk and dv must be 16-byte aligned", fn);
+  if (!aligned16(k) || !aligned16(v) || !aligned16(d_o) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
+    return fail(KPOOL_EINVAL, "%s: k, v, d_o, dq, dk and dv must be 16-byte aligned", fn);
   const kpool::BwdPlan p = kpool::plan_attend_bwd(cu_q_host, cu_k_host, nseq, Hq, Hkv);
   const int64_t most = int64_t(1) << 23, sums = std::max(c.Tq * Hq, c.Tk * Hkv) * D / 1024;
   if (p.ktiles * p.ksplit * Hkv >= most || p.qtiles * p.qsplit * Hkv >= most || c.Tq * Hq / 16 >= most ||
@@ -699,6 +729,17 @@ int kpool_attend_backward(const uint16_t *d_o, const uint16_t *q, int64_t q_stri
     return fail(KPOOL_EWORKSPACE, "%s: needs %zu bytes of workspace, got %zu", fn, need,
                 workspace ? workspace_bytes : (size_t)0);
   if (!aligned16(workspace)) return fail(KPOOL_EINVAL, "%s: workspace must be 16-byte aligned", fn);
+  const int64_t qbytes = c.Tq * Hq * D * 2, kbytes = c.Tk * Hkv * D * 2, lbytes = c.Tq * Hq * 4;
+  const struct { const char *name; const void *p; int64_t n; } outs[3] = {{"dq", dq, qbytes}, {"dk", dk, kbytes},
+                                                                           {"dv", dv, kbytes}};
+  for (int i = 0; i < 3; ++i) {
+    if ((rc = check_apart(fn, c, outs[i].name, outs[i].p, outs[i].n))) return rc;
+    const auto &next = outs[(i + 1) % 3];
+    if (meets(outs[i].p, outs[i].n, d_o, qbytes) || meets(outs[i].p, outs[i].n, o, qbytes) ||
+        meets(outs[i].p, outs[i].n, lse, lbytes) ||
+        meets(outs[i].p, outs[i].n, next.p, next.n))
+      return fail(KPOOL_EINVAL, "%s: %s overlaps d_o, o, lse or another output", fn, outs[i].name);
+  }
   hipStream_t st = (hipStream_t)stream;
   hipError_t e = timed(6, st, [&] {
     return kpool::launch_attend_bwd(c, d_o, p, workspace, dq, dk, dv, st);
@@ -736,7 +777,11 @@ int kpool_attend_selected(const uint16_t *q, int64_t q_stride, const uint16_t *k
   if ((uintptr_t)token_ids & 3) return fail(KPOOL_EINVAL, "%s: token_ids is not aligned to its elements", fn);
   const kpool::AttendPlan p = kpool::plan_list(c.Tq, nseq, width, Hq, Hkv);
   rc = check_attend_plan(fn, c, p, (Hq / Hkv + 31) / 32, workspace, workspace_bytes);
+  if (!rc) rc = check_outputs(fn, c);
   if (rc) return rc;
+  const int64_t ids = c.Tq * width * 4;
+  if (meets(o, c.Tq * Hq * D * 2, token_ids, ids) || meets(lse, c.Tq * Hq * 4, token_ids, ids))
+    return fail(KPOOL_EINVAL, "%s: o or lse overlaps token_ids", fn);
   hipStream_t st = (hipStream_t)stream;
   hipError_t e = timed(6, st, [&] {
     return kpool::launch_attend_list(c, p, token_ids, width, workspace, st);
@@ -754,11 +799,13 @@ int kpool_layer_norm(const void *x, int64_t x_stride, const float *weight, const
   if (!(eps >= 0.0f) || !isfinite(eps)) return fail(KPOOL_EINVAL, "%s: eps must be finite and >= 0", fn);
   if (rows == 0) return ok();
   if (!x || !y) return fail(KPOOL_EINVAL, "%s: null pointer", fn);
-  if (x == y) return fail(KPOOL_EINVAL, "%s: y must not be x", fn);
-  const uintptr_t mask = dtype == KPOOL_DTYPE_F32 ? 3 : 1;
+  const int64_t size = dtype == KPOOL_DTYPE_F32 ? 4 : 2;
+  const uintptr_t mask = size - 1;
   if ((((uintptr_t)x | (uintptr_t)y) & mask) ||
       (((uintptr_t)weight | (uintptr_t)bias | (uintptr_t)mean | (uintptr_t)rstd) & 3))
     return fail(KPOOL_EINVAL, "%s: a pointer is not aligned to its elements", fn);
+  if (meets(y, rows * N * size, x, rows, N * size, x_stride * size))
+    return fail(KPOOL_EINVAL, "%s: y overlaps x", fn);
   hipStream_t st = (hipStream_t)stream;
   hipError_t e = timed(5, st, [&] {
     return kpool::launch_norm(dtype == KPOOL_DTYPE_F32, x, x_stride, weight, bias, rows, N, eps, y, mean,
@@ -784,7 +831,8 @@ int kpool_layer_norm_backward(const void *dy, const void *x, int64_t x_stride, c
   if (!dx && !sums) return fail(KPOOL_EINVAL, "%s: no output given", fn);
   if (rows == 0 && !sums) return ok();
   if (rows > 0 && (!dy || !x || !mean || !rstd)) return fail(KPOOL_EINVAL, "%s: null pointer", fn);
-  const uintptr_t mask = dtype == KPOOL_DTYPE_F32 ? 3 : 1;
+  const int64_t size = dtype == KPOOL_DTYPE_F32 ? 4 : 2, row_bytes = N * size;
+  const uintptr_t mask = size - 1;
   if ((((uintptr_t)x | (uintptr_t)dy | (uintptr_t)dx) & mask) ||
       (((uintptr_t)weight | (uintptr_t)mean | (uintptr_t)rstd | (uintptr_t)dweight | (uintptr_t)dbias) & 3))
     return fail(KPOOL_EINVAL, "%s: a pointer is not aligned to its elements", fn);
@@ -795,6 +843,9 @@ int kpool_layer_norm_backward(const void *dy, const void *x, int64_t x_stride, c
                   workspace ? workspace_bytes : (size_t)0);
     if (!aligned16(workspace)) return fail(KPOOL_EINVAL, "%s: workspace must be 16-byte aligned", fn);
   }
+  if (meets(dx, rows * row_bytes, x, rows, row_bytes, x_stride * size) ||
+      meets(dx, rows * row_bytes, dy, rows * row_bytes))
+    return fail(KPOOL_EINVAL, "%s: dx overlaps x or dy", fn);
   hipStream_t st = (hipStream_t)stream;
   hipError_t e = timed(5, st, [&] {
     return kpool::launch_norm_bwd(dtype == KPOOL_DTYPE_F32, dy, x, x_stride, weight, mean, rstd, rows, N,

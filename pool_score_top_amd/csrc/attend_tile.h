@@ -178,7 +178,7 @@ __device__ inline void load_lds_4(const void *src, uint32_t to) {
 // inside takes its last row again and every byte of LDS is a key's.  Chunks past D (head dims
 // below DP) take the row's last chunk: they meet zeros of the query.  A wave's load covers
 // REGION_ROWS rows; the rows' swizzles repeat every 16 rows, so loads 16 rows apart share
-// their lane offsets and the rest of the address is a scalar.
+// their chunks' offsets.
 template <int DP, int BK, int NWAVES>
 struct KeyLoader {
   using S = Keys<DP>;

@@ -334,3 +334,53 @@ def test_more_sequences_than_the_table():
         ids = lists(cu[0], cu[2], 40, 5, "ragged")
         o, lse = K.attend_selected(q, k, v, ids, *cu, want_lse=True)
         check(q, k, v, cu[0], cu[2], 0.125, o, lse, ids)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("keys", [[300], [9000]])
+def test_nan_in_a_query_stays_in_its_row(keys):
+    """Inputs have to be finite; a row that is not still gives NaN, with and without a split,
+    and spoils no other row."""
+    cu_q, cqd = cu_of([2])
+    cu_k, ckd = cu_of(keys)
+    q, k, v = make(cu_q, cu_k, 4, 1, 64, 3)
+    ref, ref_lse = K.attend(q, k, v, cu_q, cqd, cu_k, ckd, want_lse=True)
+    q = q.clone()
+    q[1, 2, 5] = float("nan")
+    o, lse = K.attend(q, k, v, cu_q, cqd, cu_k, ckd, want_lse=True)
+    assert o[1, 2].isnan().all() and lse[1, 2].isnan()
+    keep = torch.ones(2, 4, dtype=torch.bool, device="cuda")
+    keep[1, 2] = False
+    assert torch.equal(o[keep], ref[keep]) and torch.equal(lse[keep], ref_lse[keep])
+
+
+APART = dict(q=1 << 20, k=2 << 20, v=3 << 20, ids=4 << 20, ws=5 << 20, o=6 << 20, lse=7 << 20)
+
+
+@pytest.mark.parametrize("selected", [False, True])
+@pytest.mark.parametrize("kw", [
+    *[{out: APART[n]} for out in ("o", "lse") for n in ("q", "k", "v")], dict(lse=APART["o"]),
+    dict(o=APART["k"] + 199 * 256), dict(o=APART["q"] - 16), dict(o=APART["q"] + 6 * 1024 - 16)])
+def test_refuses_outputs_over_inputs(selected, kw):
+    assert _call(selected, **{**APART, **kw}) == K.KPOOL_EINVAL
+    assert b"overlaps" in K.lib().kpool_last_error()
+
+
+@pytest.mark.parametrize("out", ["o", "lse"])
+def test_refuses_outputs_over_lists(out):
+    assert _call(True, **{**APART, out: APART["ids"]}) == K.KPOOL_EINVAL
+    assert b"overlaps" in K.lib().kpool_last_error()
+
+
+@pytest.mark.gpu
+def test_outputs_in_the_gaps_of_strided_inputs():
+    """What lies between the rows of a strided input is not the input's."""
+    cu, dev = cu_of([1])
+    ck, ckd = cu_of([40])
+    q, k, v = make(cu, ck, 2, 1, 64, 4)
+    ref, _ = K.attend(q, k, v, cu, dev, ck, ckd)
+    buf = torch.zeros(40, 256, dtype=torch.bfloat16, device="cuda")
+    buf[:, :64], buf[:, 64:128] = k[:40, 0], v[:40, 0]
+    out = buf[7, 128:].view(1, 2, 64)
+    K.attend(q, buf[:, None, :64], buf[:, None, 64:128], cu, dev, ck, ckd, out=out)
+    assert torch.equal(out, ref)

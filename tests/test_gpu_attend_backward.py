@@ -179,3 +179,22 @@ def test_workspace_bytes():
     assert K.attend_backward_workspace_bytes([0, 0], [0, 5], 4, 1, 128) == 0
     with pytest.raises(K.KpoolError):
         K.attend_backward_workspace_bytes([0, 4], [0, 4], 4, 3, 128)
+
+
+APART = dict(d_o=1 << 20, q=2 << 20, k=3 << 20, v=4 << 20, o=5 << 20, lse=6 << 20, ws=7 << 20, dq=8 << 20,
+             dk=9 << 20, dv=10 << 20)
+
+
+@pytest.mark.parametrize("kw", [
+    *[{out: APART[n]} for out in ("dq", "dk", "dv") for n in ("d_o", "q", "k", "v", "o", "lse")],
+    dict(dk=APART["dv"]), dict(dq=APART["dk"]), dict(dv=APART["dq"] + 16),
+    dict(dk=APART["k"] + 199 * 256), dict(dq=APART["d_o"] - 16)])
+def test_refuses_outputs_over_inputs(kw):
+    assert _call(**{**APART, **kw}) == K.KPOOL_EINVAL
+    assert b"overlaps" in K.lib().kpool_last_error()
+
+
+@pytest.mark.parametrize("kw", [dict(k=None), dict(v=None), dict(k=24), dict(v=24)])
+def test_keys_without_rows_need_their_pointers(kw):
+    """The keys' kernel loads its keys even where no row sees them."""
+    assert _call(**{**APART, "cu_q": [0, 0, 0], **kw}) == K.KPOOL_EINVAL

@@ -280,3 +280,15 @@ def test_more_rows_than_a_launch():
     y, mean, rstd = K.layer_norm(x, eps=1e-3, want_stats=True)
     for part in (slice(0, 1000), slice((1 << 23) - 500, rows)):
         check_forward(x[part], None, None, 1e-3, y[part], mean[part], rstd[part])
+
+
+@pytest.mark.parametrize("kw", [dict(y=1 << 20), dict(y=(1 << 20) + 3 * 400 + 254), dict(y=(1 << 20) - 1022)])
+def test_layer_norm_refuses_y_over_x(kw):
+    assert _c(**{**dict(x=1 << 20, stride=200, y=2 << 20), **kw}) == K.KPOOL_EINVAL
+    assert b"overlaps" in K.lib().kpool_last_error()
+
+
+@pytest.mark.parametrize("dx", [1 << 20, 2 << 20, (1 << 20) + 1022, (2 << 20) + 3 * 400 + 254])
+def test_layer_norm_backward_refuses_dx_over_inputs(dx):
+    assert _c_bwd(dy=1 << 20, x=2 << 20, stride=200, ws=3 << 20, dx=dx, dw=4 << 20, db=5 << 20) == K.KPOOL_EINVAL
+    assert b"overlaps" in K.lib().kpool_last_error()
