@@ -271,7 +271,7 @@ int kpool_attend(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t
                  size_t workspace_bytes, uint16_t *o, float *lse, void *stream);
 
 /* Gradients of kpool_attend.  With P = exp(scale * q k^T - lse) over what a row sees and
- * delta[i,h] = <d_o[i,h,:], o[i,h,:]> (rows that see few keys, up to 1024, where o's rounding
+ * delta[i,h] = <d_o[i,h,:], o[i,h,:]> (rows that see few keys, up to 512, where o's rounding
  * would show, take it as sum_j P[i,j] <d_o[i], v[j]>, which is the same):
  *   dv[j] = sum_i P[i,j] d_o[i]        dS[i,j] = P[i,j] (<d_o[i], v[j]> - delta[i])
  *   dk[j] = scale sum_i dS[i,j] q[i]   dq[i] = scale sum_j dS[i,j] k[j]

@@ -191,7 +191,7 @@ __device__ inline void write_row(const AttendArgs &a, int64_t row, int split, co
 
 // Many rows: NW waves of 32 virtual rows each share key tiles of 64.  8 waves and 64 KiB of
 // tiles: one workgroup a CU, two waves a SIMD, so that one's softmax runs beside the other's
-// matrix instructions.  Bound by the matrix pipe: a prompt of 16384 tokens, 32 heads over 2 of
+// matrix instructions.  Bound by the matrix pipe: a prompt of 16384 tokens, 16 heads over 2 of
 // 128, 1.1 TFLOP, takes 983 us (1.12 PFLOP/s; a 16384 library product reaches 1.3); with the
 // softmax and the LDS reads left out it still takes 915 us.
 template <int DP, int NW>

@@ -21,6 +21,8 @@
 // rows' 64-byte blocks to differ, so the row's lowest bits go to the chunk's highest ones.
 #pragma once
 
+#include <algorithm>
+
 #include "kpool_internal.h"
 
 namespace kpool {
@@ -316,6 +318,111 @@ __device__ inline TileAt find_tile(const TileTable &tab, const int32_t *__restri
   r.n0 = (int)n0;
   r.seq = n0 < (int64_t)r.Lq * G ? lo : -1;  // (Lq * G fits 32 bits, checked by the host)
   return r;
+}
+
+// Equal shares of a kernel's work.  Units (tile, key head) lie one behind the other, each as
+// long as the steps that it walks and a fixed cost; workgroup w takes the steps from
+// (unit[w], step[w]) to (unit[w + 1], step[w + 1]).  So all CUs end together, whatever the
+// lengths, and a unit that lies across workgroups leaves at most two parts a workgroup to join:
+// slot 2 w for the unit that w does not begin, slot 2 w + 1 for one that it begins and does not
+// end.  n = 0: a workgroup per unit.
+constexpr int kMostShares = 256;  // one a CU
+struct Shares {
+  int32_t n;
+  int32_t unit[kMostShares + 1], step[kMostShares + 1];
+};
+
+// How many shares: `least` steps or more each, but as many as there are units for the CUs.  None
+// where units by themselves end about as early: where no unit is longer than a share (and the
+// steps of a join), and either they all run at once or there are so many that the last of them
+// end close together.
+inline int share_count(const TotalCost &c, int64_t least) {
+  const int64_t n = std::min<int64_t>(kMostShares, std::max<int64_t>(c.units, c.total / least));
+  if (n <= 1) return 0;
+  const bool even = c.longest <= std::max(c.total / n, least) + 4;
+  return even && (c.units <= kMostShares || c.units >= 4 * kMostShares) ? 0 : (int)n;
+}
+
+// Parts of the walked keys (64 a step) where there are fewer tiles than CUs: no tile walks more
+// than the average of the CUs, or `least` steps, in one part.  All tiles start at their first key,
+// so what runs at a time reads much the same keys; equal shares, which do not, find 48% of them in
+// the L2 instead of 84% (dQ of 8192 packed tokens, 516 tiles: 235 us by equal shares, 200 by
+// tiles, 200 and 6 to join with the longest tiles cut to the CUs' average).
+inline void plan_parts(const TotalCost &c, int64_t least, int *nsplit, int *chunk) {
+  const int64_t steps = std::max(c.total / kMostShares + 1, least);
+  *nsplit = 1, *chunk = 0x7FFFFF00;
+  if (c.units < kMostShares && c.most_steps > steps)
+    *nsplit = (int)((c.most_steps + steps - 1) / steps), *chunk = (int)steps * 64;
+}
+
+// Calls f(tile, Lq, Lk, n0) for the tiles in the order of their numbers.
+template <class F>
+void for_tiles(const TileTable &t, const int32_t *cu_q, const int32_t *cu_k, int nseq, int G, int BQ,
+               int64_t ntiles, F &&f) {
+  const int seqs = t.n > 0 ? t.n : nseq;
+  for (int i = 0; i < seqs; ++i) {
+    const int s = t.n > 0 || !t.last_first ? i : nseq - 1 - i;
+    const int64_t lq = t.n > 0 ? t.Lq[s] : cu_q[s + 1] - cu_q[s], lk = t.n > 0 ? t.Lk[s] : cu_k[s + 1] - cu_k[s];
+    const int64_t n = (lq * G + BQ - 1) / BQ;
+    for (int64_t j = 0; j < n; ++j) {
+      const int64_t local = t.last_first ? n - 1 - j : j;
+      const int64_t number = t.n > 0 ? t.tile0[s] + j : tile_start(cu_q[s], s, G, BQ) + local;
+      f(t.n > 0 || !t.last_first ? number : ntiles - 1 - number, lq, lk, local * BQ);
+    }
+  }
+}
+
+// Fills in n shares; cost(Lq, Lk, n0) is a tile's, c their sum.  Parts of fewer than 4 steps are
+// left to the neighbour.  Returns whether any unit lies across shares.
+template <class F>
+bool make_shares(Shares &sh, int n, const TotalCost &c, int Hkv, const TileTable &t, const int32_t *cu_q,
+                 const int32_t *cu_k, int nseq, int G, int BQ, int64_t ntiles, F &&cost) {
+  sh.n = n;
+  if (n == 0) return false;
+  sh.unit[0] = sh.step[0] = 0;
+  bool cut = false;
+  int w = 1;
+  int64_t at = 0, next = c.total / n;
+  for_tiles(t, cu_q, cu_k, nseq, G, BQ, ntiles, [&](int64_t tile, int64_t lq, int64_t lk, int64_t n0) {
+    const UnitCost u = cost(lq, lk, n0);
+    for (int h = 0; h < Hkv; ++h) {
+      for (; w < n && next < at + u.fixed + u.steps; ++w, next = c.total * w / n) {
+        int64_t step = next - at - u.fixed, unit = tile * Hkv + h;
+        if (step < 4) step = 0;
+        else if (step > u.steps - 4) step = 0, ++unit;
+        sh.unit[w] = (int32_t)unit, sh.step[w] = (int32_t)step;
+        cut |= step > 0;
+      }
+      at += u.fixed + u.steps;
+    }
+  });
+  for (; w <= n; ++w) sh.unit[w] = (int32_t)(Hkv * ntiles), sh.step[w] = 0;
+  return cut;
+}
+
+// A workgroup's steps: the units u0 .. u1, from step s0 of the first to s1 of the last.
+struct Span {
+  int share, u0, s0, u1, s1;
+};
+__device__ inline Span span_of(const Shares &sh, int block) {
+  if (sh.n == 0) return {0, block, 0, block + 1, 0};
+  return {block, sh.unit[block], sh.step[block], sh.unit[block + 1], sh.step[block + 1]};
+}
+
+// The shares [share, end) of the unit that `share` begins and does not end, or false.  All 64
+// lanes call it.
+__device__ inline bool begins_cut(const Shares &sh, int share, int lane, int &unit, int &end) {
+  unit = sh.unit[share + 1];
+  if (sh.step[share + 1] == 0 || (sh.unit[share] == unit && sh.step[share] > 0)) return false;
+  uint64_t others;
+  end = share + 1 - 64;
+  do {  // (the last step is 0)
+    end += 64;
+    const int i = min(end + lane, sh.n);
+    others = __ballot(sh.unit[i] != unit || sh.step[i] == 0);
+  } while (others == 0);
+  end += __builtin_ctzll(others);
+  return true;
 }
 
 }  // namespace kpool

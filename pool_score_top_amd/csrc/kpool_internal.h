@@ -97,6 +97,18 @@ struct AttendCall {
   uint16_t *o;
   float *lse;
 };
+// What a unit costs, in steps: `fixed` for each part of it, then its steps.
+struct UnitCost {
+  int64_t fixed, steps;
+};
+struct TotalCost {
+  int64_t units = 0, total = 0, longest = 0, most_steps = 0;
+  void add(const UnitCost &c, int64_t times) {
+    units += times, total += (c.fixed + c.steps) * times;
+    if (longest < c.fixed + c.steps) longest = c.fixed + c.steps;
+    if (most_steps < c.steps) most_steps = c.steps;
+  }
+};
 struct AttendPlan {
   enum Form { kRows, kTiles, kList } form;
   int64_t ntiles;  // tiles of query rows, or more
@@ -115,8 +127,9 @@ hipError_t launch_attend_list(const AttendCall &c, const AttendPlan &p, const in
 // Its gradients (attend_bwd.hip); c.o and c.lse are the forward pass's.
 struct BwdPlan {
   int64_t ktiles, qtiles;  // tiles of keys, of query rows, or more
-  int ksplit, qsplit;      // parts of the rows (dK, dV) and of the keys (dQ)
-  int kchunk, qchunk;
+  TotalCost kcost;         // dK's and dV's work
+  int kshares;             // its equal shares (0: a workgroup per tile and key head)
+  int qsplit, qchunk;      // parts of the keys (dQ)
 };
 BwdPlan plan_attend_bwd(const int32_t *cu_q, const int32_t *cu_k, int nseq, int Hq, int Hkv);
 size_t attend_bwd_workspace(const BwdPlan &p, int64_t Tq, int64_t Tk, int Hq, int Hkv, int D);

@@ -70,6 +70,15 @@ def test_many_sequences_strided_tokens_large_scores():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("seqs", [5, 45])
+@pytest.mark.parametrize("Hq,Hkv,D", [(12, 3, 64), (16, 1, 128)])
+def test_tiles_that_lie_across_workgroups(seqs, Hq, Hkv, D):
+    """Long and short sequences, few enough to fit the table of sequences and more than that."""
+    lens = [int(x) for x in np.random.default_rng(seqs).choice([0, 1, 100, 129, 700, 1300], seqs - 1)] + [1111]
+    gradients(lens, [n + 7 * (n > 100) for n in lens], Hq, Hkv, D, seqs)
+
+
+@pytest.mark.gpu
 def test_same_bits_workspace_outputs_and_stream():
     q, k, v, d_o, o, lse, cu, ref = gradients([600, 100], [600, 700], 4, 1, 64, 9)
     nb = K.attend_backward_workspace_bytes(cu[0], cu[2], 4, 1, 64)
