@@ -415,11 +415,16 @@ template <int DP, int WR>
 struct Lists {
   static constexpr int NW = 4, BK = 32, TILE = BK * Keys<DP>::ROWB;
   static constexpr int UNITS = NW / WR;                           // of a workgroup
-  static constexpr int BLOCK = WR == 1 ? 1024 : 2048, EACH = BLOCK / (WR * 64), GROUPS = 16;
-  static constexpr int IDS = NW * 2 * TILE, USE = IDS + UNITS * BLOCK * 4;
-  // (a unit's counts, [GROUPS][WR] and their total, lie in its first wave's tile buffer: a
-  // block is sorted when no tile is in use or on its way)
-  static_assert((GROUPS * WR + 1) * 4 <= 2 * TILE, "counts in a tile buffer");
+  static constexpr int BLOCK = 2048, EACH = BLOCK / (WR * 64), GROUPS = 16;
+  // A wave a row and 128 wide: the LDS that the tiles leave holds a block's ids in 16 bits, or
+  // half a block's (which then walks the sequence once more) where sequences are longer
+  static constexpr bool HALF = WR == 1 && DP == 128;
+  static constexpr int IDS = NW * 2 * TILE, USE = IDS + UNITS * BLOCK * (HALF ? 2 : 4);
+  // (a wave's counts, [GROUPS][64], and behind them, at a unit's first wave, the unit's,
+  // [GROUPS][WR] and their total, lie in its tile buffers: a block is sorted when no tile is in use
+  // or on its way)
+  static constexpr int COUNTS = GROUPS * 64 * 4;
+  static_assert(COUNTS + (GROUPS * WR + 1) * 4 <= 2 * TILE, "counts in a tile buffer");
   static constexpr int LDS = WR > 1 && Join<DP, NW>::LDS > USE ? Join<DP, NW>::LDS : USE;
 };
 template <int DP, int WR>
@@ -454,8 +459,12 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendArgs a) {
   Frag<DP> f;
   f.init(mine, lane);
   const int part = wave % WR;  // of the unit's waves
-  int *ids = reinterpret_cast<int *>(lds + C::IDS) + wave / WR * C::BLOCK;
-  int *count = reinterpret_cast<int *>(lds + (wave - part) * 2 * TILE);  // [GROUPS][WR], then the total
+  const bool narrow = C::HALF && at.Lk <= 65536;
+  const int block_ids = C::HALF && !narrow ? C::BLOCK / 2 : C::BLOCK;
+  int *ids = reinterpret_cast<int *>(lds + C::IDS + wave / WR * C::BLOCK * (C::HALF ? 2 : 4));
+  uint16_t *ids16 = reinterpret_cast<uint16_t *>(ids);
+  KPOOL_LDS int *mine_count = (KPOOL_LDS int *)(uintptr_t)mine + lane;                 // [GROUPS][64]
+  int *count = reinterpret_cast<int *>(lds + (wave - part) * 2 * TILE + C::COUNTS);  // [GROUPS][WR], the total
   auto sync = [&] {  // of the unit's waves
     if (WR > 1) __syncthreads();
     else wait_reads();  // (a wave's own LDS accesses go in order)
@@ -485,27 +494,34 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendArgs a) {
     else __builtin_amdgcn_s_waitcnt(0x0F74);                    // vmcnt(4)
     asm volatile("" ::: "memory");
   };
-  for (int block = e_lo; block < e_hi; block += C::BLOCK) {
-    // the block's ids, EACH a thread, by group: rank within the wave's entries of the group
-    int id[C::EACH], group[C::EACH], rank[C::EACH];
+  const int ngroups = a.by_place ? C::GROUPS : 1;
+  for (int block = e_lo; block < e_hi; block += block_ids) {
+    // the block's ids, up to EACH a lane, by group, lane and place in the list: each lane counts
+    // its own, the counts are summed, and each lane takes places from its starts on
+    int id[C::EACH];
+    const int end = min(e_hi, block + block_ids);
 #pragma unroll
     for (int i = 0; i < C::EACH; ++i) {
       const int e = block + i * WR * 64 + part * 64 + lane;
-      id[i] = e < e_hi ? list[e] : -1;
-      group[i] = id[i] >= 0 && id[i] <= t ? id[i] >> shift : -1;
+      id[i] = e < end ? list[e] : -1;
     }
-    const int ngroups = a.by_place ? C::GROUPS : 1;
-    for (int g = 0; g < ngroups; ++g) {
-      int n = 0;
+    for (int g = 0; g < ngroups + 1; ++g) mine_count[(g & (C::GROUPS - 1)) * 64] = 0;  // (pairs are summed)
 #pragma unroll
-      for (int i = 0; i < C::EACH; ++i) {
-        const uint64_t m = __ballot(group[i] == g);
-        const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32),
-                                                     __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
-        if (group[i] == g) rank[i] = n + before;
-        n += __popcll(m);
+    for (int i = 0; i < C::EACH; ++i) {
+      if (id[i] > t) id[i] = -1;
+      if (id[i] >= 0)
+        __hip_atomic_fetch_add(mine_count + (id[i] >> shift) * 64, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
+    }
+    for (int g = 0; g < ngroups; g += 2) {  // two groups' counts of 16 bits at a time
+      const uint32_t c = mine_count[g * 64] | mine_count[g * 64 + 64] << 16;
+      uint32_t sum = c;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t up = __shfl_up(sum, d);
+        if (lane >= d) sum += up;
       }
-      if (lane == 0) count[g * WR + part] = n;
+      mine_count[g * 64] = (sum - c) & 0xFFFF, mine_count[g * 64 + 64] = (sum - c) >> 16;
+      if (lane == 63) count[g * WR + part] = sum & 0xFFFF, count[(g + 1) * WR + part] = sum >> 16;
     }
     sync();
     if (part == 0) {  // counts to starts
@@ -521,9 +537,15 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendArgs a) {
       if (lane == 63) count[C::GROUPS * WR] = sum;
     }
     sync();
+    for (int g = 0; g < ngroups; ++g) mine_count[g * 64] += count[g * WR + part];
 #pragma unroll
     for (int i = 0; i < C::EACH; ++i)
-      if (group[i] >= 0) ids[count[group[i] * WR + part] + rank[i]] = id[i];
+      if (id[i] >= 0) {
+        const int at = __hip_atomic_fetch_add(mine_count + (id[i] >> shift) * 64, 1, __ATOMIC_RELAXED,
+                                              __HIP_MEMORY_SCOPE_WAVEFRONT);
+        if (narrow) ids16[at] = (uint16_t)id[i];
+        else ids[at] = id[i];
+      }
     const int present = count[C::GROUPS * WR];
     wait_reads();  // (the tiles' loads overwrite the counts)
     sync();
@@ -531,8 +553,9 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendArgs a) {
     // this wave's tiles: part, part + WR, ..
     const int ntile = (present + BK - 1) / BK;
     auto entry = [&](int tile) {
-      const int e = tile * BK + (lane & 31);
-      return ids[e < present ? e : tile * BK];
+      int e = tile * BK + (lane & 31);
+      e = e < present ? e : tile * BK;
+      return narrow ? (int)ids16[e] : ids[e];
     };
     int j = part;
     if (j < ntile) {
@@ -706,10 +729,9 @@ AttendPlan plan_list(int64_t Tq, int nseq, int width, int Hq, int Hkv) {
   if (p.nsplit <= 1) p.nsplit = 1, p.chunk = 0x7FFFFF00;
   // sharing takes several workgroups an XCD at a time
   p.by_place = wgs >= 256;
-  // a wave per row where that fills the 256 CUs' 8 waves (lists of 2048, units and us by four
-  // waves and by one: 1024 110 113, 1536 159 174, 2048 208 179, 4096 409 349, 8192
-  // 791 708)
-  p.wave_rows = wgs >= 2048;
+  // a wave per row where that puts one on each SIMD (lists of 2048, units and us by four waves and
+  // by one: 512 55 97, 1024 108 103, 1536 158 149, 2048 202 150, 4096 396 291, 8192 770 572)
+  p.wave_rows = wgs >= 1024;
   return p;
 }
 
