@@ -296,29 +296,41 @@ class _OnDevice:
     t's device, so that outputs and workspaces allocated inside belong to that stream; gives
     its handle."""
 
-    __slots__ = ("device", "stream", "contexts")
+    __slots__ = ("handle", "contexts")
 
     def __init__(self, t, stream):
-        self.device, self.stream, self.contexts = t.device, stream, ()
+        import torch
+        index = t.get_device()
+        if stream is None and torch._C._cuda_getDevice() == index:  # (t has initialised HIP)
+            self.contexts = None
+            self.handle = torch._C._cuda_getCurrentRawStream(index)
+            return
+        if stream is not None and stream.device != t.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+        self.contexts = [torch.cuda.device(index)]
+        if stream is not None:
+            self.contexts.append(torch.cuda.stream(stream))
 
     def __enter__(self):
+        if self.contexts is None:
+            return self.handle
         import torch
-        index = self.device.index
-        if self.stream is None and torch._C._cuda_getDevice() == index:  # (t has initialised HIP)
-            return torch._C._cuda_getCurrentRawStream(index)
-        if self.stream is not None and self.stream.device != self.device:
-            raise ValueError(f"the stream is on {self.stream.device}, the tensors on {self.device}")
-        contexts = [torch.cuda.device(self.device)]
-        if self.stream is not None:
-            contexts.append(torch.cuda.stream(self.stream))
-        for c in contexts:
+        for c in self.contexts:
             c.__enter__()
-        self.contexts = contexts
-        return torch._C._cuda_getCurrentRawStream(index)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
     def __exit__(self, *exc):
-        for c in reversed(self.contexts):
-            c.__exit__(*exc)
+        if self.contexts is not None:
+            for c in reversed(self.contexts):
+                c.__exit__(*exc)
+
+
+def _host_address(a):
+    """A host array's address (the quick way needs a writable one)."""
+    try:
+        return ctypes.addressof(ctypes.c_char.from_buffer(a))
+    except TypeError:
+        return a.__array_interface__["data"][0]
 
 
 def _at(t):
@@ -334,12 +346,11 @@ def _like(t, name, shape, dtype, device):
 
 def _heads(t, name, device, codes):
     """t as packed tokens [T, H, D] of bf16 with any token stride: (T, H, D, stride)."""
-    shape = t.shape
-    if len(shape) != 3 or not t.is_cuda or t.device != device:
+    if t.dim() != 3 or not t.is_cuda or t.device != device:
         raise ValueError(f"{name} must be a device tensor [T, heads, D] on {device}")
     if t.dtype not in codes:
         raise ValueError(f"{name} must be bfloat16 (or int16 bit patterns)")
-    T, H, D = shape
+    T, H, D = t.shape
     s0, s1, s2 = t.stride()
     if (s2 != 1 and D > 1) or (s1 != D and H > 1):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
@@ -376,8 +387,8 @@ class _Attend:
         if hv != self.Hkv or dv != d or d != self.D:
             raise ValueError("q, k and v must agree in D, and k and v in their heads")
         self.cu_q, q_dev, self.cu_k, k_dev = _cu_pair(cu_q, cu_q_dev, cu_k, cu_k_dev, device)
-        q_ptr = self.cu_q.__array_interface__["data"][0]
-        k_ptr = q_ptr if self.cu_k is self.cu_q else self.cu_k.__array_interface__["data"][0]
+        q_ptr = _host_address(self.cu_q)
+        k_ptr = q_ptr if self.cu_k is self.cu_q else _host_address(self.cu_k)
         self.nseq = len(self.cu_q) - 1
         self.Tq, self.Tk = int(self.cu_q[-1]), int(self.cu_k[-1])
         if tq < self.Tq or min(tk, tv) < self.Tk:
@@ -390,13 +401,14 @@ class _Attend:
     def outputs(self, q, out, lse, want_lse):
         import torch
         if out is None:
-            out = q.new_empty((self.Tq, self.Hq, self.D))
+            rows, width = self.Hq * self.D, self.D
+            out = torch.empty_strided((self.Tq, self.Hq, width), (rows, width, 1), dtype=q.dtype, device=self.device)
         else:
             _like(out, "out", (self.Tq, self.Hq, self.D), q.dtype, self.device)
         if lse is not None:
             _like(lse, "lse", (self.Tq, self.Hq), torch.float32, self.device)
         elif want_lse:
-            lse = q.new_empty((self.Tq, self.Hq), dtype=torch.float32)
+            lse = torch.empty_strided((self.Tq, self.Hq), (self.Hq, 1), dtype=torch.float32, device=self.device)
         return out, lse
 
     def scratch(self, workspace, nbytes):
@@ -538,7 +550,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, want_stat
         _like(out, "out", (rows, N), x.dtype, device)
     with _OnDevice(x, stream) as s:
         if out is None:
-            out = x.new_empty((rows, N))
+            out = torch.empty_strided((rows, N), (N, 1), dtype=x.dtype, device=device)
         mean = rstd = None
         if want_stats:
             mean, rstd = x.new_empty((2, rows), dtype=torch.float32).unbind()
