@@ -720,8 +720,8 @@ int kpool_attend_backward(const uint16_t *d_o, const uint16_t *q, int64_t q_stri
   if (!aligned16(k) || !aligned16(v) || !aligned16(d_o) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
     return fail(KPOOL_EINVAL, "%s: k, v, d_o, dq, dk and dv must be 16-byte aligned", fn);
   const kpool::BwdPlan p = kpool::plan_attend_bwd(cu_q_host, cu_k_host, nseq, Hq, Hkv);
-  const int64_t most = int64_t(1) << 23, sums = std::max(c.Tq * Hq, c.Tk * Hkv) * D / 1024;
-  if (p.ktiles * Hkv >= most || p.qtiles * p.qsplit * Hkv >= most || c.Tq * Hq / 16 >= most || sums >= most)
+  const int64_t most = int64_t(1) << 23;  // (workgroups of 512 threads)
+  if (p.ktiles * Hkv >= most || p.qtiles * p.qsplit * Hkv >= most)
     return fail(KPOOL_EUNSUPPORTED, "%s: too many rows for one launch", fn);
   const size_t need = kpool::attend_bwd_workspace(p, c.Tq, c.Tk, Hq, Hkv, D);
   if (need && (!workspace || workspace_bytes < need))

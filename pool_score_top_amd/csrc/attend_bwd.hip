@@ -3,9 +3,9 @@
 //   dV_j = sum_i P_ij do_i          dP_ij = do_i v_j      dS_ij = P_ij (dP_ij - delta_i)
 //   dK_j = scale sum_i dS_ij q_i    dQ_i = scale sum_j dS_ij k_j
 //
-// Three kernels: the rows' lse (base 2) and delta laid out along the virtual rows; dQ with the
-// rows in registers and the keys walked; dK and dV with the keys in registers and the rows
-// walked.  S and dP are thus computed twice (7 matrix products instead of 5), and in return
+// Two kernels: dQ with the rows in registers and the keys walked, which also lays the rows' lse
+// (base 2) and delta out along the virtual rows; dK and dV with the keys in registers and the
+// rows walked.  S and dP are thus computed twice (7 matrix products instead of 5), and in return
 // no sum crosses workgroups through atomics: the same call gives the same bits, and the
 // gradients of shared key heads add up over their G query heads in registers, because the
 // walked axis is the virtual rows.  P and dS are rounded to bf16 for their products (as the
@@ -40,35 +40,6 @@ struct BwdArgs {
   float *part;          // fp32 parts, used by one kernel and its sum at a time
   TileTable table;      // of keys, or of query rows
 };
-
-// One (row, head) per 16 lanes.
-__global__ __launch_bounds__(256) void bwd_stat_kernel(BwdArgs a) {
-  const int64_t at = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-  if (at >= a.Tq * a.Hq) return;  // (16 lanes together)
-  const int c = (threadIdx.x & 15) * 8;
-  float s = 0.0f;
-  if (c < a.D) {
-    const uint4 x = *reinterpret_cast<const uint4 *>(a.o + at * a.D + c);
-    const uint4 y = *reinterpret_cast<const uint4 *>(a.d_o + at * a.D + c);
-    const uint32_t u[4] = {x.x, x.y, x.z, x.w}, w[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s = fmaf(__uint_as_float(u[i] << 16), __uint_as_float(w[i] << 16), s);
-      s = fmaf(__uint_as_float(u[i] & 0xFFFF0000u), __uint_as_float(w[i] & 0xFFFF0000u), s);
-    }
-  }
-#pragma unroll
-  for (int d = 1; d < 16; d <<= 1) s += __shfl_xor(s, d);
-  if ((threadIdx.x & 15) == 0) {
-    const int G = a.Hq / a.Hkv;
-    const int64_t row = at / a.Hq;
-    const int head = (int)(at - row * a.Hq);
-    const int64_t to = (int64_t)(head / G) * a.Tq * G + row * G + head % G;
-    const float l = a.lse[at];
-    a.lse2[to] = l > -__builtin_inff() ? l * kLog2e : __builtin_inff();
-    a.delta[to] = s;
-  }
-}
 
 // Writes a lane's column of a transposed result x^T [DP, 32]: row `row` of out (bf16, D
 // wide), or of a part (fp32).
@@ -422,9 +393,20 @@ __global__ __launch_bounds__(NW * 64) void bwd_rows_kernel(BwdArgs a) {
   bf16x8 qf[S::KS], dof[S::KS];
   load_frag<DP>(qf, live ? a.q + ((int64_t)at.q_start + tok) * a.qs + (int64_t)head * a.D : nullptr, a.D, lane);
   load_frag<DP>(dof, live ? a.d_o + row * a.D : nullptr, a.D, lane);
+  // the rows' lse and delta, which dK's and dV's kernel reads
   const int64_t stat = (int64_t)kvh * a.Tq * G + (int64_t)at.q_start * G + n;
-  const float lse = live ? a.lse2[stat] : __builtin_inff();
-  float delta = live ? a.delta[stat] : 0.0f;
+  const float none = -__builtin_inff(), given = live ? a.lse[row] : none;
+  const float lse = given != none ? given * kLog2e : -none;
+  float delta = 0.0f;
+  if (t1 >= kFewKeys) {
+    bf16x8 of[S::KS];
+    load_frag<DP>(of, live ? a.o + row * a.D : nullptr, a.D, lane);
+#pragma unroll
+    for (int ks = 0; ks < S::KS; ++ks)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) delta = fmaf((float)of[ks][i], (float)dof[ks][i], delta);
+    delta += other_half(delta);
+  }
   f32x16 dq[S::DT];
 #pragma unroll
   for (int dt = 0; dt < S::DT; ++dt)
@@ -491,10 +473,10 @@ __global__ __launch_bounds__(NW * 64) void bwd_rows_kernel(BwdArgs a) {
       }
     }
     delta = sum + other_half(sum);
-    if (split == 0 && live && lane < 32) a.delta[stat] = delta;  // (for dK)
     __builtin_amdgcn_s_waitcnt(0x0070);
     barrier_only();
   }
+  if (split == 0 && live && lane < 32) a.lse2[stat] = lse, a.delta[stat] = delta;
   auto step = [&](int j, auto buf_c) {
     constexpr int BUF = decltype(buf_c)::value;
     enter(j, ntile, k_lo, BUF);
@@ -578,11 +560,6 @@ hipError_t launch_bwd_t(const AttendCall &c, const BwdPlan &p, BwdArgs a, hipStr
   hipError_t e = hipSuccess;
   const int G = a.Hq / a.Hkv;
   if (a.Tq > 0) {
-    hipLaunchKernelGGL(bwd_stat_kernel, dim3((unsigned)((a.Tq * a.Hq + 15) / 16)), dim3(256), 0, st, a);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  if (a.Tq > 0) {
     a.qtiles = make_table(a.table, c.cu_q_host, c.cu_k_host, a.nseq, a.Hq / a.Hkv, kBwdWaves * 32, true);
     const size_t lds = 4 * 64 * DP * 2;
     hipLaunchKernelGGL((bwd_rows_kernel<DP, kBwdWaves>), dim3((unsigned)(a.qtiles * a.qsplit * a.Hkv)),
@@ -594,7 +571,7 @@ hipError_t launch_bwd_t(const AttendCall &c, const BwdPlan &p, BwdArgs a, hipStr
     }
     if (e != hipSuccess) return e;
   }
-  // (behind dQ's kernel, which corrects delta)
+  // (behind dQ's kernel, which lays lse and delta out for it)
   if (a.Tk > 0) {
     a.ktiles = make_table(a.table, c.cu_k_host, c.cu_q_host, a.nseq, 1, BwdKeys<DP>::KEYS, false);
     Shares shares;
