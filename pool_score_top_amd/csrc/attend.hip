@@ -153,6 +153,93 @@ struct Rows {
   }
 };
 
+// The same for up to 16 query rows, by products of 16 rows: 32 rows would be half empty.  o and
+// S have a column l % 16 a lane, the keys of S and the head dim of o go over its four groups.
+template <int DP>
+struct Rows16 {
+  using S = Keys16<DP>;
+  bf16x8 q[S::KS];
+  f32x4 o[S::DT];
+  float m, l;
+
+  __device__ inline void init(const uint16_t *row, int D, int lane) {
+#pragma unroll
+    for (int ks = 0; ks < S::KS; ++ks) {
+      const int d = ks * 32 + (lane >> 4) * 8;
+      uint4 z = make_uint4(0, 0, 0, 0);
+      if (row && d < D) z = *reinterpret_cast<const uint4 *>(row + d);
+      q[ks] = __builtin_bit_cast(bf16x8, z);
+    }
+#pragma unroll
+    for (int dt = 0; dt < S::DT; ++dt) o[dt] = f32x4{};
+    m = -__builtin_inff();
+    l = 0.0f;
+  }
+  template <int BK>
+  __device__ inline void scores(const Frag16<DP> &f, uint32_t sk, f32x4 (&s)[2]) const {
+    static_assert(BK == 32, "one contraction of the second product");
+    bf16x8 kr[2][S::KS];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int ks = 0; ks < S::KS; ++ks) kr[b][ks] = f.rows(sk + b * 16 * S::ROWB, ks);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      s[b] = f32x4{};
+#pragma unroll
+      for (int ks = 0; ks < S::KS; ++ks) s[b] = mfma(kr[b][ks], q[ks], s[b]);
+    }
+  }
+  template <class F>
+  __device__ inline void weights(f32x4 (&s)[2], float c, int lane, bool masked, F &&visible) {
+    if (masked) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (!visible(0, b * 16 + 4 * (lane >> 4) + i)) s[b][i] = -__builtin_inff();
+    }
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, s[b][i]);
+    const Pair t = row_pair(top);
+    top = fmaxf(t.a, t.b);
+    top = fmaxf(top, other_half(top)) * c;
+    if (__any(top > m + 8.0f)) {
+      const float up = fmaxf(top, m);
+      const float a = up > m ? exp2f_fast(m - up) : 1.0f;
+      m = up;
+      l *= a;
+#pragma unroll
+      for (int dt = 0; dt < S::DT; ++dt) o[dt] *= a;
+    }
+    const float shift = m > -__builtin_inff() ? m : 0.0f;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[b][i] = exp2f_fast(fmaf(s[b][i], c, -shift));
+        l += s[b][i];
+      }
+  }
+  __device__ inline void values(const Frag16<DP> &f, uint32_t sv, const f32x4 (&p)[2]) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    const u32x4 w = {pack_bf16(p[0][0], p[0][1]), pack_bf16(p[0][2], p[0][3]), pack_bf16(p[1][0], p[1][1]),
+                     pack_bf16(p[1][2], p[1][3])};
+#pragma unroll
+    for (int dt = 0; dt < S::DT; ++dt) o[dt] = mfma(f.cols(sv, dt), __builtin_bit_cast(bf16x8, w), o[dt]);
+  }
+  // the row's sum over its lanes
+  __device__ inline float sum() const {
+    const Pair t = row_pair(l);
+    const float x = t.a + t.b;
+    return x + other_half(x);
+  }
+};
+
 // Writes a row's output: the final one, or a split's part (in fp32, normalised by its own l).
 template <int DP>
 __device__ inline void write_row(const AttendArgs &a, int64_t row, int split, const f32x16 (&o)[DP / 32],
@@ -187,6 +274,20 @@ __device__ inline void write_row(const AttendArgs &a, int64_t row, int split, co
                        pack_bf16(o[dt][i + 2] * inv, o[dt][i + 3] * inv));
     }
   if (h == 0 && a.lse) a.lse[row] = lse;
+}
+
+template <int DP>
+__device__ inline void write_row16(const AttendArgs &a, int64_t row, const Rows16<DP> &r, float l, int lane) {
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  uint16_t *dst = a.o + row * a.D;
+#pragma unroll
+  for (int dt = 0; dt < DP / 16; ++dt) {
+    const int d = dt * 16 + 4 * (lane >> 4);
+    if (d < a.D)
+      *reinterpret_cast<uint2 *>(dst + d) = make_uint2(pack_bf16(r.o[dt][0] * inv, r.o[dt][1] * inv),
+                                                       pack_bf16(r.o[dt][2] * inv, r.o[dt][3] * inv));
+  }
+  if (lane < 16 && a.lse) a.lse[row] = l == 0.0f ? -__builtin_inff() : (r.m + log2f(l)) * kLn2;
 }
 
 // Many rows: NW waves of 32 virtual rows each share key tiles of 64.  8 waves and 64 KiB of
@@ -427,9 +528,9 @@ struct Lists {
   static_assert(COUNTS + (GROUPS * WR + 1) * 4 <= 2 * TILE, "counts in a tile buffer");
   static constexpr int LDS = WR > 1 && Join<DP, NW>::LDS > USE ? Join<DP, NW>::LDS : USE;
 };
-template <int DP, int WR>
+template <int DP, int WR, int ROWS>
 __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendArgs a) {
-  using S = Keys<DP>;
+  using S = std::conditional_t<ROWS == 16, Keys16<DP>, Keys<DP>>;
   using C = Lists<DP, WR>;
   constexpr int BK = C::BK, NW = C::NW, TILE = C::TILE;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
@@ -450,13 +551,14 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendArgs a) {
   const int tok = at.n0, t = tok + at.Lk - at.Lq;
   const int nrows = min(32, G - first), head = kvh * G + first;
   const int64_t token = (int64_t)at.q_start + tok;
-  Rows<DP> r;
-  r.init((lane & 31) < nrows ? a.q + token * a.qs + (int64_t)(head + (lane & 31)) * a.D : nullptr, a.D, lane);
+  const int col_row = lane & (ROWS - 1);  // the lane's row
+  std::conditional_t<ROWS == 16, Rows16<DP>, Rows<DP>> r;
+  r.init(col_row < nrows ? a.q + token * a.qs + (int64_t)(head + col_row) * a.D : nullptr, a.D, lane);
   const uint16_t *kb = (const uint16_t *)uniform_ptr(a.k + (int64_t)at.k_start * a.ks + (int64_t)kvh * a.D);
   const uint16_t *vb = (const uint16_t *)uniform_ptr(a.v + (int64_t)at.k_start * a.vs + (int64_t)kvh * a.D);
   const int32_t *list = a.ids + token * a.width;
   const uint32_t mine = lds_offset(lds) + wave * 2 * TILE;
-  Frag<DP> f;
+  std::conditional_t<ROWS == 16, Frag16<DP>, Frag<DP>> f;
   f.init(mine, lane);
   const int part = wave % WR;  // of the unit's waves
   const bool narrow = C::HALF && at.Lk <= 65536;
@@ -565,7 +667,7 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendArgs a) {
     for (; j < ntile; j += WR) {
       const bool more = j + WR < ntile;
       const int next = more ? entry(j + WR) : 0;
-      f32x16 s[1];
+      std::conditional_t<ROWS == 16, f32x4[2], f32x16[1]> s;
       wait_side(true);  // the keys; the values may still be out
       r.template scores<BK>(f, 0, s);
       wait_reads();
@@ -579,12 +681,15 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendArgs a) {
     }
     sync();  // (the next block's ids go where these were)
   }
-  if constexpr (WR > 1) {
+  if constexpr (ROWS == 16) {
+    const float l = r.sum();
+    if (col_row < nrows) write_row16<DP>(a, token * a.Hq + head + col_row, r, l, lane);
+  } else if constexpr (WR > 1) {
     join_waves<DP, NW>(a, r, lds, wave, lane, split, nrows,
                        [&](int row) { return token * a.Hq + head + row; });
   } else {
     const float l = r.l + other_half(r.l);
-    if ((lane & 31) < nrows) write_row<DP>(a, token * a.Hq + head + (lane & 31), split, r.o, r.m, l, lane);
+    if (col_row < nrows) write_row<DP>(a, token * a.Hq + head + col_row, split, r.o, r.m, l, lane);
   }
 }
 
@@ -651,12 +756,12 @@ hipError_t launch_attend_t(const AttendPlan &p, const AttendArgs &a, hipStream_t
   return e;
 }
 
-template <int DP, int WR>
+template <int DP, int WR, int ROWS>
 hipError_t launch_list_t(const AttendArgs &a, hipStream_t st) {
   using C = Lists<DP, WR>;
   const int64_t units = a.ntiles * ((a.Hq / a.Hkv + 31) / 32) * a.nsplit * a.Hkv;
   const int64_t wgs = (units + C::UNITS - 1) / C::UNITS;
-  hipLaunchKernelGGL((attend_list_kernel<DP, WR>), dim3((unsigned)((wgs + 7) / 8 * 8)), dim3(C::NW * 64), C::LDS,
+  hipLaunchKernelGGL((attend_list_kernel<DP, WR, ROWS>), dim3((unsigned)((wgs + 7) / 8 * 8)), dim3(C::NW * 64), C::LDS,
                      st, a);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && a.nsplit > 1) e = launch_join(a, st);
@@ -745,8 +850,10 @@ hipError_t launch_attend_list(const AttendCall &c, const AttendPlan &p, const in
   AttendArgs a = make_args(c, p, workspace);
   a.ids = ids, a.width = width;
   a.by_place = p.by_place;
-  if (p.wave_rows) return c.D <= 64 ? launch_list_t<64, 1>(a, st) : launch_list_t<128, 1>(a, st);
-  return c.D <= 64 ? launch_list_t<64, 4>(a, st) : launch_list_t<128, 4>(a, st);
+  if (!p.wave_rows) return c.D <= 64 ? launch_list_t<64, 4, 32>(a, st) : launch_list_t<128, 4, 32>(a, st);
+  if (c.Hq / c.Hkv <= 16)
+    return c.D <= 64 ? launch_list_t<64, 1, 16>(a, st) : launch_list_t<128, 1, 16>(a, st);
+  return c.D <= 64 ? launch_list_t<64, 1, 32>(a, st) : launch_list_t<128, 1, 32>(a, st);
 }
 
 }  // namespace kpool

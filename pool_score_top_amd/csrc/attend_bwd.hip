@@ -119,7 +119,6 @@ __global__ __launch_bounds__(512) void bwd_keys_kernel(BwdArgs a, Shares shares)
   const uint32_t lds0 = lds_offset(lds);
   Frag<DP> f;
   f.init(lds0, lane);
-  typedef float f32x4 __attribute__((ext_vector_type(4)));
   uint32_t st0 = lds0 + C::STAT + (lane >> 5) * 16 + (second ? 128 : 0);
   uint32_t pb = lds0 + C::P + group * C::PBUF + lane * 16;
   opaque(st0), opaque(pb);

@@ -29,6 +29,7 @@ namespace kpool {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 
 #define KPOOL_LDS __attribute__((address_space(3)))
@@ -108,6 +109,44 @@ struct Frag {
   }
 };
 
+// The same for v_mfma_f32_16x16x32_bf16, whose operands are 16 rows of 32 values (lane l: row
+// l % 16, values 8 (l / 16) + j) and whose result has column l % 16 and rows 4 (l / 16) + i,
+// i < 4: results of 32 keys, 16 at a time, are the next product's B operand in the order
+// 4 g + {0..3}, 16 + 4 g + {0..3} of lane group g = l / 16.  A phase of the 16-byte reads holds 8
+// rows' chunk c and 8 other rows' chunk c ^ 1, one of the transposing reads 8 rows by 32 bytes.
+template <int DP>
+struct Keys16 : Keys<DP> {
+  static constexpr int KS = DP / 32, DT = DP / 16;
+  static __device__ inline int swz(int row) {
+    if (DP == 64) return ((row >> 1) & 3) << 1;
+    const int quad = (row >> 2) & 3, gray = quad ^ (quad >> 1);
+    return (row & 3) << 2 | (gray & 1) << 1 | gray >> 1;
+  }
+};
+template <int DP>
+struct Frag16 {
+  using S = Keys16<DP>;
+  uint32_t row[S::KS], col[S::DT];
+  __device__ inline void init(uint32_t lds0, int lane) {
+    const int r = lane & 15, g = lane >> 4, c = 4 * g + (r >> 2);  // (the transposing read's row)
+    const uint32_t rb = r * S::ROWB + ((g ^ S::swz(r)) << 4);
+    const uint32_t cb = c * S::ROWB + ((((r & 3) >> 1) ^ S::swz(c)) << 4) + (r & 1) * 8;
+#pragma unroll
+    for (int ks = 0; ks < S::KS; ++ks) row[ks] = lds0 + (rb ^ (ks << 6)), opaque(row[ks]);
+#pragma unroll
+    for (int dt = 0; dt < S::DT; ++dt) col[dt] = lds0 + (cb ^ (dt << 5)), opaque(col[dt]);
+  }
+  // rows l % 16 from `off` on, contraction step ks over the head dim
+  __device__ inline bf16x8 rows(uint32_t off, int ks) const { return lds_read(row[ks] + off); }
+  // columns 16 dt + l % 16, contraction over the 32 rows from `off` on
+  __device__ inline bf16x8 cols(uint32_t off, int dt) const {
+    return lds_read_cols(col[dt] + off, col[dt] + off + 16 * S::ROWB);
+  }
+};
+
+__device__ inline f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
 __device__ inline f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
@@ -125,6 +164,15 @@ __device__ inline float other_half(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   // r[0] = [lo, lo], r[1] = [hi, hi]
   return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+}
+
+// the values of the lane and of lane ^ 16, in the same order in both
+struct Pair {
+  float a, b;
+};
+__device__ inline Pair row_pair(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return {__uint_as_float(r[0]), __uint_as_float(r[1])};
 }
 
 // A workgroup barrier alone.  __syncthreads() also waits for all of the wave's loads, those
