@@ -75,14 +75,16 @@ struct Rows {
 
   // S of the BK keys of a tile at LDS offset sk past the addresses of `f`
   template <int BK>
-  __device__ inline void scores(const Frag<DP> &f, uint32_t sk, f32x16 (&s)[BK / 32]) const {
-    // (the reads go out together, ahead of what needs them)
-    bf16x8 kr[BK / 32][S::KS];
+  using KeyFrag = bf16x8[BK / 32][S::KS];
+  template <int BK>
+  static __device__ inline void read_keys(const Frag<DP> &f, uint32_t sk, KeyFrag<BK> &kr) {
 #pragma unroll
     for (int sub = 0; sub < BK / 32; ++sub)
 #pragma unroll
       for (int ks = 0; ks < S::KS; ++ks) kr[sub][ks] = f.rows(sk + sub * 32 * S::ROWB, ks);
-    __builtin_amdgcn_sched_barrier(0);
+  }
+  template <int BK>
+  __device__ inline void scores(const KeyFrag<BK> &kr, f32x16 (&s)[BK / 32]) const {
 #pragma unroll
     for (int sub = 0; sub < BK / 32; ++sub) {
       f32x16 t = {};
@@ -142,12 +144,31 @@ struct Rows {
           o[dt] = mfma(f.cols(sv + (sub * 32 + kc * 16) * S::ROWB, dt), w, o[dt]);
       }
   }
+  // and of 32 keys whose values have been read
+  using ValueFrag = bf16x8[2][S::DT];
+  static __device__ inline void read_values(const Frag<DP> &f, uint32_t sv, ValueFrag &vr) {
+#pragma unroll
+    for (int kc = 0; kc < 2; ++kc)
+#pragma unroll
+      for (int dt = 0; dt < S::DT; ++dt) vr[kc][dt] = f.cols(sv + kc * 16 * S::ROWB, dt);
+  }
+  __device__ inline void values(const ValueFrag &vr, const f32x16 (&p)[1]) {
+#pragma unroll
+    for (int kc = 0; kc < 2; ++kc) {
+      const bf16x8 w = as_operand(p[0], kc);
+#pragma unroll
+      for (int dt = 0; dt < S::DT; ++dt) o[dt] = mfma(vr[kc][dt], w, o[dt]);
+    }
+  }
 
   template <int BK, class F>
   __device__ inline void add(const Frag<DP> &f, uint32_t sk, uint32_t sv, float c, int lane, bool masked,
                              F &&visible) {
     f32x16 s[BK / 32];
-    scores<BK>(f, sk, s);
+    KeyFrag<BK> kr;
+    read_keys<BK>(f, sk, kr);
+    __builtin_amdgcn_sched_barrier(0);  // (the reads go out together, ahead of what needs them)
+    scores<BK>(kr, s);
     weights(s, c, lane, masked, visible);
     values(f, sv, s);
   }
@@ -176,14 +197,17 @@ struct Rows16 {
     l = 0.0f;
   }
   template <int BK>
-  __device__ inline void scores(const Frag16<DP> &f, uint32_t sk, f32x4 (&s)[2]) const {
+  using KeyFrag = bf16x8[2][S::KS];
+  template <int BK>
+  static __device__ inline void read_keys(const Frag16<DP> &f, uint32_t sk, KeyFrag<BK> &kr) {
     static_assert(BK == 32, "one contraction of the second product");
-    bf16x8 kr[2][S::KS];
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int ks = 0; ks < S::KS; ++ks) kr[b][ks] = f.rows(sk + b * 16 * S::ROWB, ks);
-    __builtin_amdgcn_sched_barrier(0);
+  }
+  template <int BK>
+  __device__ inline void scores(const KeyFrag<BK> &kr, f32x4 (&s)[2]) const {
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       s[b] = f32x4{};
@@ -225,12 +249,17 @@ struct Rows16 {
         l += s[b][i];
       }
   }
-  __device__ inline void values(const Frag16<DP> &f, uint32_t sv, const f32x4 (&p)[2]) {
+  using ValueFrag = bf16x8[S::DT];
+  static __device__ inline void read_values(const Frag16<DP> &f, uint32_t sv, ValueFrag &vr) {
+#pragma unroll
+    for (int dt = 0; dt < S::DT; ++dt) vr[dt] = f.cols(sv, dt);
+  }
+  __device__ inline void values(const ValueFrag &vr, const f32x4 (&p)[2]) {
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
     const u32x4 w = {pack_bf16(p[0][0], p[0][1]), pack_bf16(p[0][2], p[0][3]), pack_bf16(p[1][0], p[1][1]),
                      pack_bf16(p[1][2], p[1][3])};
 #pragma unroll
-    for (int dt = 0; dt < S::DT; ++dt) o[dt] = mfma(f.cols(sv, dt), __builtin_bit_cast(bf16x8, w), o[dt]);
+    for (int dt = 0; dt < S::DT; ++dt) o[dt] = mfma(vr[dt], __builtin_bit_cast(bf16x8, w), o[dt]);
   }
   // the row's sum over its lanes
   __device__ inline float sum() const {
@@ -495,21 +524,20 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendArgs a) {
 // one part of its list); WR waves share it, each taking list tiles of 32 in turn, and join at
 // the end.  The keys come from all over memory, so what counts is how many bytes are on their
 // way, and how many of them from the L2.
-//   Each wave has one LDS buffer for keys and one for values, asks for the next tile's keys as
-//   soon as S is computed and for its values after the product with P.  Two workgroups of 4
-//   waves fit a CU (with 8 waves and one workgroup, 2048 rows of 2048 tokens take 502 us
-//   instead of 410).
+//   Each wave has one LDS buffer for keys and one for values and asks for the next tile's as
+//   soon as this one's are in registers.  Two workgroups of 4 waves fit a CU.
 //   The list is taken in blocks, which first drop the entries outside 0 .. t and, where
-//   a.by_place, are put into 16 groups by their place in the sequence (a counting sort, stable,
-//   so the sums' order is the same every time).  Workgroups of one XCD (every 8th) take
+//   a.by_place, are put into 16 groups by their place in the sequence (a counting sort whose
+//   order is the same every time, and so the sums').  Workgroups of one XCD (every 8th) take
 //   consecutive tokens of one key head and walk the sequence in the same direction at about
 //   the same time, so what several of them selected is read from memory once.
 //   WR = 1, where there are rows enough: the 256 rows that an XCD then works on at a time
 //   pass a sixteenth of the sequence together and share more of it than 64 rows that each go
 //   by four times as fast, and no waves have to join.
-// L2 hits and time, 2048 rows that each pick 2048 of 65536 tokens at random, 32 heads over 2:
-//   by place, WR = 1: 47%, 355 us;  WR = 4: 30%, 410 us;  in the list's order: 12%, 549 us (at 8
-//   waves a workgroup).
+//   ROWS = 16 for up to 16 heads a key head: half the matrix and vector work of 32.
+// 2048 rows of 2048 of 65536 tokens, 32 heads over 2: 273 us, 65% of the keys from the L2 (WR = 4:
+// 396 us; lists in their own order: 549 us, 12%).  Bound by the loads into the LDS: with all
+// keys in the L2 it takes 219 us, and without any of the products and the softmax 212.
 // The last tile of a block may be short: its absent entries read the tile's first key, so that
 // no other key is read, and count for nothing.
 template <int DP, int WR>
@@ -552,7 +580,8 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendArgs a) {
   const int nrows = min(32, G - first), head = kvh * G + first;
   const int64_t token = (int64_t)at.q_start + tok;
   const int col_row = lane & (ROWS - 1);  // the lane's row
-  std::conditional_t<ROWS == 16, Rows16<DP>, Rows<DP>> r;
+  using R = std::conditional_t<ROWS == 16, Rows16<DP>, Rows<DP>>;
+  R r;
   r.init(col_row < nrows ? a.q + token * a.qs + (int64_t)(head + col_row) * a.D : nullptr, a.D, lane);
   const uint16_t *kb = (const uint16_t *)uniform_ptr(a.k + (int64_t)at.k_start * a.ks + (int64_t)kvh * a.D);
   const uint16_t *vb = (const uint16_t *)uniform_ptr(a.v + (int64_t)at.k_start * a.vs + (int64_t)kvh * a.D);
@@ -668,16 +697,23 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendArgs a) {
       const bool more = j + WR < ntile;
       const int next = more ? entry(j + WR) : 0;
       std::conditional_t<ROWS == 16, f32x4[2], f32x16[1]> s;
+      // (a side's next tile is asked for once this one's fragments are in registers)
       wait_side(true);  // the keys; the values may still be out
-      r.template scores<BK>(f, 0, s);
+      typename R::template KeyFrag<BK> kr;
+      R::template read_keys<BK>(f, 0, kr);
       wait_reads();
       if (more) load(kb, a.ks, next, mine);
+      __builtin_amdgcn_sched_barrier(0);
+      r.template scores<BK>(kr, s);
       r.weights(s, a.scale_log2, lane, j * BK + BK > present,
                 [&](int, int i) { return j * BK + i < present; });
       wait_side(more);  // the values; the next keys may still be out
-      r.values(f, TILE, s);
+      typename R::ValueFrag vr;
+      R::read_values(f, TILE, vr);
       wait_reads();
       if (more) load(vb, a.vs, next, mine + TILE);
+      __builtin_amdgcn_sched_barrier(0);
+      r.values(vr, s);
     }
     sync();  // (the next block's ids go where these were)
   }
