@@ -52,9 +52,17 @@ struct AttendArgs {
 template <int DP>
 struct Rows {
   using S = Keys<DP>;
+  static constexpr int ROWS = 32, VALUES = 16;  // of a fragment of o: its rows, a lane's values
   bf16x8 q[S::KS];
   f32x16 o[S::DT];
   float m, l;  // base 2; l is this lane half's part
+
+  // where value i of o[dt] lies in the head dim
+  static __device__ inline int place(int dt, int i, int lane) {
+    return dt * 32 + 8 * (i / 4) + 4 * (lane >> 5) + i % 4;
+  }
+  // the row's sum over its lanes
+  __device__ inline float sum() const { return l + other_half(l); }
 
   // row: this lane's query (l % 32), null for none
   __device__ inline void init(const uint16_t *row, int D, int lane) {
@@ -179,10 +187,17 @@ struct Rows {
 template <int DP>
 struct Rows16 {
   using S = Keys16<DP>;
+  static constexpr int ROWS = 16, VALUES = 4;
   bf16x8 q[S::KS];
   f32x4 o[S::DT];
   float m, l;
 
+  static __device__ inline int place(int dt, int i, int lane) { return dt * 16 + 4 * (lane >> 4) + i; }
+  __device__ inline float sum() const {
+    const Pair t = row_pair(l);
+    const float x = t.a + t.b;
+    return x + other_half(x);
+  }
   __device__ inline void init(const uint16_t *row, int D, int lane) {
 #pragma unroll
     for (int ks = 0; ks < S::KS; ++ks) {
@@ -261,62 +276,31 @@ struct Rows16 {
 #pragma unroll
     for (int dt = 0; dt < S::DT; ++dt) o[dt] = mfma(vr[dt], __builtin_bit_cast(bf16x8, w), o[dt]);
   }
-  // the row's sum over its lanes
-  __device__ inline float sum() const {
-    const Pair t = row_pair(l);
-    const float x = t.a + t.b;
-    return x + other_half(x);
-  }
 };
 
 // Writes a row's output: the final one, or a split's part (in fp32, normalised by its own l).
-template <int DP>
-__device__ inline void write_row(const AttendArgs &a, int64_t row, int split, const f32x16 (&o)[DP / 32],
-                                 float m, float l, int lane) {
+template <class R>
+__device__ inline void write_row(const AttendArgs &a, bool live, int64_t row, int split, const R &r, int lane) {
+  const float l = r.sum();  // (all lanes)
+  if (!live) return;
   // (l is 0 where the row saw nothing; NaN goes through)
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const float lse = l == 0.0f ? -__builtin_inff() : (m + log2f(l)) * kLn2;
-  const int h = lane >> 5;
-  if (a.nsplit > 1) {
-    float *dst = a.part_o + ((int64_t)split * a.rows + row) * a.D;
+  const float lse = l == 0.0f ? -__builtin_inff() : (r.m + log2f(l)) * kLn2;
+  float *part = a.part_o + ((int64_t)split * a.rows + row) * a.D;
+  uint16_t *out = a.o + row * a.D;
 #pragma unroll
-    for (int dt = 0; dt < DP / 32; ++dt)
+  for (int dt = 0; dt < R::S::DT; ++dt)
 #pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        const int d = dt * 32 + 2 * i + 4 * h;
-        if (d < a.D)
-          *reinterpret_cast<float4 *>(dst + d) = make_float4(o[dt][i] * inv, o[dt][i + 1] * inv,
-                                                             o[dt][i + 2] * inv, o[dt][i + 3] * inv);
-      }
-    if (h == 0) a.part_lse[(int64_t)split * a.rows + row] = lse;
-    return;
-  }
-  uint16_t *dst = a.o + row * a.D;
-#pragma unroll
-  for (int dt = 0; dt < DP / 32; ++dt)
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const int d = dt * 32 + 2 * i + 4 * h;
-      if (d < a.D)
-        *reinterpret_cast<uint2 *>(dst + d) =
-            make_uint2(pack_bf16(o[dt][i] * inv, o[dt][i + 1] * inv),
-                       pack_bf16(o[dt][i + 2] * inv, o[dt][i + 3] * inv));
+    for (int i = 0; i < R::VALUES; i += 4) {
+      const int d = R::place(dt, i, lane);
+      if (d >= a.D) continue;
+      const float x[4] = {r.o[dt][i] * inv, r.o[dt][i + 1] * inv, r.o[dt][i + 2] * inv, r.o[dt][i + 3] * inv};
+      if (a.nsplit > 1) *reinterpret_cast<float4 *>(part + d) = make_float4(x[0], x[1], x[2], x[3]);
+      else *reinterpret_cast<uint2 *>(out + d) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
     }
-  if (h == 0 && a.lse) a.lse[row] = lse;
-}
-
-template <int DP>
-__device__ inline void write_row16(const AttendArgs &a, int64_t row, const Rows16<DP> &r, float l, int lane) {
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  uint16_t *dst = a.o + row * a.D;
-#pragma unroll
-  for (int dt = 0; dt < DP / 16; ++dt) {
-    const int d = dt * 16 + 4 * (lane >> 4);
-    if (d < a.D)
-      *reinterpret_cast<uint2 *>(dst + d) = make_uint2(pack_bf16(r.o[dt][0] * inv, r.o[dt][1] * inv),
-                                                       pack_bf16(r.o[dt][2] * inv, r.o[dt][3] * inv));
-  }
-  if (lane < 16 && a.lse) a.lse[row] = l == 0.0f ? -__builtin_inff() : (r.m + log2f(l)) * kLn2;
+  if (lane >= R::ROWS) return;
+  if (a.nsplit > 1) a.part_lse[(int64_t)split * a.rows + row] = lse;
+  else if (a.lse) a.lse[row] = lse;
 }
 
 // Many rows: NW waves of 32 virtual rows each share key tiles of 64.  8 waves and 64 KiB of
@@ -385,8 +369,7 @@ __global__ __launch_bounds__(NW * 64) void attend_tile_kernel(AttendArgs a) {
     step(j, std::integral_constant<int, 0>{});
     if (j + 1 < ntile) step(j + 1, std::integral_constant<int, 1>{});
   }
-  const float l = r.l + other_half(r.l);
-  if (live) write_row<DP>(a, ((int64_t)at.q_start + tok) * a.Hq + head, split, r.o, r.m, l, lane);
+  write_row(a, live, ((int64_t)at.q_start + tok) * a.Hq + head, split, r, lane);
 }
 
 // The NW waves of a workgroup, each with its keys' part of the same 32 rows, join: O of every
@@ -397,29 +380,28 @@ struct Join {
   static constexpr int STAT = NW * 64;                  // m and l, [NW][2][32]
   static constexpr int LDS = (STAT + NW * DP * 33) * 4;  // and O^T, [NW][DP][33]
 };
-template <int DP, int NW, class F>
-__device__ inline void join_waves(const AttendArgs &a, const Rows<DP> &r, unsigned char *lds, int wave,
-                                  int lane, int split, int nrows, F &&out_row) {
-  using S = Keys<DP>;
-  const float l = r.l + other_half(r.l);
+template <int DP, int NW, class R, class F>
+__device__ inline void join_waves(const AttendArgs &a, const R &r, unsigned char *lds, int wave, int lane,
+                                  int split, int nrows, F &&out_row) {
+  const int mine = lane & (R::ROWS - 1);
+  const float l = r.sum();
   __syncthreads();  // (all waves are done with their tiles)
   float *stat = reinterpret_cast<float *>(lds);
   float *acc = stat + Join<DP, NW>::STAT;
-  if (lane < 32) stat[wave * 64 + lane] = r.m, stat[wave * 64 + 32 + lane] = l;
+  if (lane < R::ROWS) stat[wave * 64 + lane] = r.m, stat[wave * 64 + 32 + lane] = l;
   __syncthreads();
   float m = -__builtin_inff();
 #pragma unroll
-  for (int w = 0; w < NW; ++w) m = fmaxf(m, stat[w * 64 + (lane & 31)]);
+  for (int w = 0; w < NW; ++w) m = fmaxf(m, stat[w * 64 + mine]);
   const float shift = m > -__builtin_inff() ? m : 0.0f;
   const float mul = exp2f_fast(r.m - shift);
 #pragma unroll
-  for (int dt = 0; dt < S::DT; ++dt)
+  for (int dt = 0; dt < R::S::DT; ++dt)
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      acc[(wave * DP + dt * 32 + 8 * (i / 4) + 4 * (lane >> 5) + i % 4) * 33 + (lane & 31)] = r.o[dt][i] * mul;
+    for (int i = 0; i < R::VALUES; ++i) acc[(wave * DP + R::place(dt, i, lane)) * 33 + mine] = r.o[dt][i] * mul;
   __syncthreads();
   // 8 columns of a row a thread at a time
-  for (int e = threadIdx.x; e < 32 * (DP / 8); e += NW * 64) {
+  for (int e = threadIdx.x; e < R::ROWS * (DP / 8); e += NW * 64) {
     const int row = e / (DP / 8), d0 = e % (DP / 8) * 8;
     if (row >= nrows || d0 >= a.D) continue;
     float rm = -__builtin_inff(), rl = 0.0f;
@@ -717,16 +699,11 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendArgs a) {
     }
     sync();  // (the next block's ids go where these were)
   }
-  if constexpr (ROWS == 16) {
-    const float l = r.sum();
-    if (col_row < nrows) write_row16<DP>(a, token * a.Hq + head + col_row, r, l, lane);
-  } else if constexpr (WR > 1) {
+  if constexpr (WR > 1)
     join_waves<DP, NW>(a, r, lds, wave, lane, split, nrows,
                        [&](int row) { return token * a.Hq + head + row; });
-  } else {
-    const float l = r.l + other_half(r.l);
-    if (col_row < nrows) write_row<DP>(a, token * a.Hq + head + col_row, split, r.o, r.m, l, lane);
-  }
+  else
+    write_row(a, col_row < nrows, token * a.Hq + head + col_row, split, r, lane);
 }
 
 // Joins the splits of a row: o = sum_s 2^(lse_s - lse) o_s, 4 columns a lane, 64 / (D / 4) rows
@@ -793,12 +770,16 @@ hipError_t launch_attend_t(const AttendPlan &p, const AttendArgs &a, hipStream_t
 }
 
 template <int DP, int WR, int ROWS>
-hipError_t launch_list_t(const AttendArgs &a, hipStream_t st) {
+void launch_list_dp(const AttendArgs &a, hipStream_t st) {
   using C = Lists<DP, WR>;
   const int64_t units = a.ntiles * ((a.Hq / a.Hkv + 31) / 32) * a.nsplit * a.Hkv;
   const int64_t wgs = (units + C::UNITS - 1) / C::UNITS;
-  hipLaunchKernelGGL((attend_list_kernel<DP, WR, ROWS>), dim3((unsigned)((wgs + 7) / 8 * 8)), dim3(C::NW * 64), C::LDS,
-                     st, a);
+  hipLaunchKernelGGL((attend_list_kernel<DP, WR, ROWS>), dim3((unsigned)((wgs + 7) / 8 * 8)), dim3(C::NW * 64),
+                     C::LDS, st, a);
+}
+template <int WR, int ROWS>
+hipError_t launch_list_t(const AttendArgs &a, hipStream_t st) {
+  a.D <= 64 ? launch_list_dp<64, WR, ROWS>(a, st) : launch_list_dp<128, WR, ROWS>(a, st);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && a.nsplit > 1) e = launch_join(a, st);
   return e;
@@ -871,7 +852,7 @@ AttendPlan plan_list(int64_t Tq, int nseq, int width, int Hq, int Hkv) {
   // sharing takes several workgroups an XCD at a time
   p.by_place = wgs >= 256;
   // a wave per row where that puts one on each SIMD (lists of 2048, units and us by four waves and
-  // by one: 512 55 97, 1024 108 103, 1536 158 149, 2048 202 150, 4096 396 291, 8192 770 572)
+  // by one: 512 54 90, 1024 107 93, 1536 157 141, 2048 205 129, 4096 398 265, 8192 796 530)
   p.wave_rows = wgs >= 1024;
   return p;
 }
@@ -886,10 +867,9 @@ hipError_t launch_attend_list(const AttendCall &c, const AttendPlan &p, const in
   AttendArgs a = make_args(c, p, workspace);
   a.ids = ids, a.width = width;
   a.by_place = p.by_place;
-  if (!p.wave_rows) return c.D <= 64 ? launch_list_t<64, 4, 32>(a, st) : launch_list_t<128, 4, 32>(a, st);
-  if (c.Hq / c.Hkv <= 16)
-    return c.D <= 64 ? launch_list_t<64, 1, 16>(a, st) : launch_list_t<128, 1, 16>(a, st);
-  return c.D <= 64 ? launch_list_t<64, 1, 32>(a, st) : launch_list_t<128, 1, 32>(a, st);
+  // (with four waves a row the loads bound it, and products of 16 rows take the same time)
+  if (!p.wave_rows) return launch_list_t<4, 32>(a, st);
+  return c.Hq / c.Hkv <= 16 ? launch_list_t<1, 16>(a, st) : launch_list_t<1, 32>(a, st);
 }
 
 }  // namespace kpool

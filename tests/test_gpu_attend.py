@@ -325,6 +325,48 @@ def test_selected_many_rows(Hq, Hkv, D):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,D", [(17, 1, 128), (64, 2, 64), (32, 2, 120)])
+def test_selected_many_rows_of_many_heads(Hq, Hkv, D):
+    """A wave a row with more than 16 heads a key head, and with exactly 16."""
+    cu_q, cqd = cu_of([100, 950])
+    cu_k, ckd = cu_of([131, 3000])
+    q, k, v = make(cu_q, cu_k, Hq, Hkv, D, 33)
+    for width, kind in ((97, "ragged"), (2049, "full")):
+        ids = lists(cu_q, cu_k, width, 5, kind)
+        o, lse = K.attend_selected(q, k, v, ids, cu_q, cqd, cu_k, ckd, want_lse=True)
+        check(q, k, v, cu_q, cu_k, 1.0 / D ** 0.5, o, lse, ids)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("keys", [65536, 65537, 70001])
+def test_selected_around_the_16_bit_ids(keys, D):
+    """Sequences whose ids just fit 16 bits and just do not; the last ids are in every list."""
+    cu_q, cqd = cu_of([1030])
+    cu_k, ckd = cu_of([keys])
+    q, k, v = make(cu_q, cu_k, 2, 1, D, 35)
+    ids = lists(cu_q, cu_k, 1500, 7, "full")
+    t = torch.arange(keys - 1030, keys, device="cuda", dtype=torch.int32)
+    ids[:, 3], ids[:, 1400], ids[:, 1025] = t, t - 1, 0
+    o, lse = K.attend_selected(q, k, v, ids, cu_q, cqd, cu_k, ckd, want_lse=True)
+    check(q, k, v, cu_q, cu_k, 1.0 / D ** 0.5, o, lse, ids)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [1, 1100])
+def test_selected_one_token_over_and_over(rows):
+    """All of a list in one place; and all its tokens but one there."""
+    cu_q, cqd = cu_of([rows])
+    cu_k, ckd = cu_of([5000])
+    q, k, v = make(cu_q, cu_k, 4, 1, 128, 37)
+    for last in (7, 3000):
+        ids = torch.full((rows, 4100), 7, dtype=torch.int32, device="cuda")
+        ids[:, 4099] = last
+        o, lse = K.attend_selected(q, k, v, ids, cu_q, cqd, cu_k, ckd, want_lse=True)
+        check(q, k, v, cu_q, cu_k, 1.0 / 128 ** 0.5, o, lse, ids)
+
+
+@pytest.mark.gpu
 def test_more_sequences_than_the_table():
     """Tokens, chunks and lists of 70 sequences, some empty (found by search on the device)."""
     rng = np.random.default_rng(4)
