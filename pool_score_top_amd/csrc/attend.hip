@@ -280,7 +280,8 @@ struct Rows16 {
 
 // Writes a row's output: the final one, or a split's part (in fp32, normalised by its own l).
 template <class R>
-__device__ inline void write_row(const AttendArgs &a, bool live, int64_t row, int split, const R &r, int lane) {
+__device__ inline void write_row(const AttendArgs &a, bool live, int64_t row, bool whole, int split, const R &r,
+                                 int lane) {
   const float l = r.sum();  // (all lanes)
   if (!live) return;
   // (l is 0 where the row saw nothing; NaN goes through)
@@ -295,11 +296,11 @@ __device__ inline void write_row(const AttendArgs &a, bool live, int64_t row, in
       const int d = R::place(dt, i, lane);
       if (d >= a.D) continue;
       const float x[4] = {r.o[dt][i] * inv, r.o[dt][i + 1] * inv, r.o[dt][i + 2] * inv, r.o[dt][i + 3] * inv};
-      if (a.nsplit > 1) *reinterpret_cast<float4 *>(part + d) = make_float4(x[0], x[1], x[2], x[3]);
+      if (!whole) *reinterpret_cast<float4 *>(part + d) = make_float4(x[0], x[1], x[2], x[3]);
       else *reinterpret_cast<uint2 *>(out + d) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
     }
   if (lane >= R::ROWS) return;
-  if (a.nsplit > 1) a.part_lse[(int64_t)split * a.rows + row] = lse;
+  if (!whole) a.part_lse[(int64_t)split * a.rows + row] = lse;
   else if (a.lse) a.lse[row] = lse;
 }
 
@@ -325,6 +326,7 @@ __global__ __launch_bounds__(NW * 64) void attend_tile_kernel(AttendArgs a) {
   const int nrows = min(BQ, at.Lq * G - at.n0);
   const int t1 = (at.n0 + nrows - 1) / G + at.Lk - at.Lq;  // the last row's position
   const int k_lo = split * a.chunk, k_hi = (int)min64(t1 + 1, (int64_t)k_lo + a.chunk);
+  if (split > 0 && k_lo >= k_hi) return;  // (the join does not read this part)
   const uint16_t *kb = (const uint16_t *)uniform_ptr(a.k + (int64_t)at.k_start * a.ks + (int64_t)kvh * a.D);
   const uint16_t *vb = (const uint16_t *)uniform_ptr(a.v + (int64_t)at.k_start * a.vs + (int64_t)kvh * a.D);
 
@@ -369,7 +371,8 @@ __global__ __launch_bounds__(NW * 64) void attend_tile_kernel(AttendArgs a) {
     step(j, std::integral_constant<int, 0>{});
     if (j + 1 < ntile) step(j + 1, std::integral_constant<int, 1>{});
   }
-  write_row(a, live, ((int64_t)at.q_start + tok) * a.Hq + head, split, r, lane);
+  // (a tile with one part writes the outputs themselves)
+  write_row(a, live, ((int64_t)at.q_start + tok) * a.Hq + head, t1 < a.chunk, split, r, lane);
 }
 
 // The NW waves of a workgroup, each with its keys' part of the same 32 rows, join: O of every
@@ -703,7 +706,7 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendArgs a) {
     join_waves<DP, NW>(a, r, lds, wave, lane, split, nrows,
                        [&](int row) { return token * a.Hq + head + row; });
   else
-    write_row(a, col_row < nrows, token * a.Hq + head + col_row, split, r, lane);
+    write_row(a, col_row < nrows, token * a.Hq + head + col_row, a.nsplit == 1, split, r, lane);
 }
 
 // Joins the splits of a row: o = sum_s 2^(lse_s - lse) o_s, 4 columns a lane, 64 / (D / 4) rows
@@ -748,6 +751,40 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
   if (d == 0 && a.lse) a.lse[row] = total == 0.0f ? none : shift + log2f(total) * kLn2;
 }
 
+// The same for the tiles of the tile kernel that have more than one part; 8 workgroups a tile.
+__global__ __launch_bounds__(256) void attend_tile_join_kernel(AttendArgs a) {
+  constexpr int BQ = kTileWaves * 32, ROWS = BQ / 8;
+  const int row0 = (blockIdx.x & 7) * ROWS, lane = threadIdx.x & 63, G = a.Hq / a.Hkv;
+  const int unit = blockIdx.x >> 3, kvh = unit % a.Hkv;
+  const TileAt at = find_tile(a.table, a.cu_q, a.cu_k, a.nseq, G, BQ, unit / a.Hkv, a.ntiles, lane);
+  if (at.seq < 0) return;
+  const int nrows = min(BQ, at.Lq * G - at.n0);
+  const int parts = ((at.n0 + nrows - 1) / G + at.Lk - at.Lq) / a.chunk + 1;
+  if (parts <= 1) return;
+  const int per = a.D / 4;
+  const float none = -__builtin_inff();
+  for (int e = threadIdx.x; e < ROWS * per; e += 256) {
+    const int n = at.n0 + row0 + e / per, d = e % per * 4;
+    if (n >= at.Lq * G) break;
+    const int64_t row = ((int64_t)at.q_start + n / G) * a.Hq + kvh * G + n % G;
+    float m = none, total = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int s = 0; s < parts; ++s) m = fmaxf(m, a.part_lse[(int64_t)s * a.rows + row]);
+    const float shift = m > none ? m : 0.0f;
+#pragma unroll 4
+    for (int s = 0; s < parts; ++s) {
+      const float w = exp2f_fast((a.part_lse[(int64_t)s * a.rows + row] - shift) * kLog2e);
+      const float4 v = *reinterpret_cast<const float4 *>(a.part_o + ((int64_t)s * a.rows + row) * a.D + d);
+      total += w;
+      o[0] = fmaf(w, v.x, o[0]), o[1] = fmaf(w, v.y, o[1]), o[2] = fmaf(w, v.z, o[2]), o[3] = fmaf(w, v.w, o[3]);
+    }
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    *reinterpret_cast<uint2 *>(a.o + row * a.D + d) =
+        make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+    if (d == 0 && a.lse) a.lse[row] = total == 0.0f ? none : shift + log2f(total) * kLn2;
+  }
+}
+
 hipError_t launch_join(const AttendArgs &a, hipStream_t st) {
   hipLaunchKernelGGL(attend_join_kernel, dim3((unsigned)((a.rows + 256 / a.D - 1) / (256 / a.D))), dim3(256), 0, st, a);
   return hipGetLastError();
@@ -756,17 +793,19 @@ hipError_t launch_join(const AttendArgs &a, hipStream_t st) {
 template <int DP>
 hipError_t launch_attend_t(const AttendPlan &p, const AttendArgs &a, hipStream_t st) {
   const unsigned grid = (unsigned)(a.ntiles * a.nsplit * a.Hkv);
-  hipError_t e;
-  if (p.form == AttendPlan::kRows) {
+  const bool few = p.form == AttendPlan::kRows;
+  if (few) {
     constexpr size_t lds = FewRows<DP>::LDS;
     hipLaunchKernelGGL(attend_rows_kernel<DP>, dim3(grid), dim3(256), lds, st, a);
   } else {
     constexpr size_t lds = 4 * 64 * DP * 2;
     hipLaunchKernelGGL((attend_tile_kernel<DP, kTileWaves>), dim3(grid), dim3(kTileWaves * 64), lds, st, a);
   }
-  e = hipGetLastError();
-  if (e == hipSuccess && a.nsplit > 1) e = launch_join(a, st);
-  return e;
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.nsplit == 1) return e;
+  if (few) return launch_join(a, st);
+  hipLaunchKernelGGL(attend_tile_join_kernel, dim3((unsigned)(a.ntiles * a.Hkv * 8)), dim3(256), 0, st, a);
+  return hipGetLastError();
 }
 
 template <int DP, int WR, int ROWS>
