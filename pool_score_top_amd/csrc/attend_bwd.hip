@@ -544,7 +544,7 @@ __global__ __launch_bounds__(256) void bwd_rows_sum_kernel(BwdArgs a) {
 
 // Costs of a tile of keys and of a tile of rows (which may have to find delta first, two of its
 // three products), and the steps that a share has at least.
-constexpr int kKeysShare = 16, kRowsShare = 8;
+constexpr int kKeysShare = 16, kRowsShare = 6;
 UnitCost keys_cost(int64_t lk, int64_t lq, int64_t n0, int64_t G) {
   return {4, (lq * G - first_row(lq * G, lk, lq, n0, G) + 31) / 32};
 }
