@@ -9,7 +9,8 @@
 // no sum crosses workgroups through atomics: the same call gives the same bits, and the
 // gradients of shared key heads add up over their G query heads in registers, because the
 // walked axis is the virtual rows.  P and dS are rounded to bf16 for their products (as the
-// outputs are); P, dP, dS and all sums are fp32.
+// outputs are; where few keys are seen, dS to two bf16 numbers for dQ); P, dP, dS and all sums are
+// fp32.
 //
 // Each kernel orients S so that its result registers are the next product's B operand: S^T
 // [keys, rows] where rows stay (dQ^T = K^T dS^T), S [rows, keys] where keys stay (dV^T =
@@ -349,12 +350,19 @@ __global__ __launch_bounds__(256) void bwd_keys_sum_kernel(BwdArgs a, Shares sha
   }
 }
 
-// Tiles of rows that see no more keys than this take delta from the keys instead of from o.
-// The error of dQ against 64 bits, in units of what rounding the exact dQ to bf16 gives, and
-// the time of a step, for 8192 packed tokens and for 2048 tokens with 8 heads over 1 of 64: 256:
-// 1.50, 572 us, 1.57, 86 us; 512: 1.48, 572, 1.54, 93; 1024: 1.46, 590, 1.50, 100; without: 1.60
-// and more.  (The rounding of dS alone gives 1.41.)
-constexpr int kFewKeys = 512;
+// Rows that see few keys have the largest gradients, and their roundings show in the whole's.
+// Tiles whose rows see no more than kFewKeys take delta from the keys instead of from o; up to
+// kFineKeys dS is held in two bf16 numbers for dQ (a fourth product, of operands that are there).
+// The errors against 64 bits, in units of what rounding the exact gradient to bf16 gives (one
+// rounding of dS beside it gives 1.41), for 2048 tokens, 8 heads over 1 of 64, and the time of a
+// step there and of 8192 packed tokens with 16 heads over 4 of 128:
+//   few, fine      dQ    dK    us
+//   1024, none     1.49  1.43  94.5  574
+//   512, none      1.53  1.45  87    561
+//   512, 512       1.36  1.45  89    565
+//   512, 1024      1.26  1.45  89    566
+//   512, 2048      1.12  1.45  89    576
+constexpr int kFewKeys = 512, kFineKeys = 1024;
 
 // dQ: NW waves of 32 virtual rows; key tiles of 64 pass through LDS, as in the forward pass.
 // 8192 packed tokens (4096, 2777, 1000, 319), 16 heads over 4 of 128: 157 GFLOP in 200 us, 0.79
@@ -501,6 +509,10 @@ __global__ __launch_bounds__(NW * 64) void bwd_rows_kernel(BwdArgs a) {
         const bf16x8 ds = as_operand(s, c);
 #pragma unroll
         for (int dt = 0; dt < S::DT; ++dt) dq[dt] = mfma(w[c][dt], ds, dq[dt]);
+        if (t1 >= kFineKeys) continue;
+        const bf16x8 rest = as_operand_rest(s, c, ds);
+#pragma unroll
+        for (int dt = 0; dt < S::DT; ++dt) dq[dt] = mfma(w[c][dt], rest, dq[dt]);
       }
     }
   };

@@ -159,6 +159,18 @@ __device__ inline bf16x8 as_operand(const f32x16 &p, int c) {
   return __builtin_bit_cast(bf16x8, v);
 }
 
+// and what that rounding took from them, rounded to bf16 in turn
+__device__ inline bf16x8 as_operand_rest(const f32x16 &p, int c, bf16x8 rounded) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  const u32x4 r = __builtin_bit_cast(u32x4, rounded);
+  u32x4 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = pack_bf16(p[8 * c + 2 * i] - __uint_as_float(r[i] << 16),
+                     p[8 * c + 2 * i + 1] - __uint_as_float(r[i] & 0xFFFF0000u));
+  return __builtin_bit_cast(bf16x8, v);
+}
+
 // the same value from the other half of the wave (lane ^ 32)
 __device__ inline float other_half(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
