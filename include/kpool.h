@@ -321,8 +321,8 @@ int kpool_attend_selected(const uint16_t *q, int64_t q_stride, const uint16_t *k
  *   eps      finite, >= 0 (a constant row with eps = 0 gives the formula's NaN)
  *   y        [rows, N] contiguous, not overlapping x
  *   mean, rstd  NULLABLE fp32 [rows]: what the backward pass reads
- * rows 0 is a no-op; N in [1, 2^26].  Any alignment of whole elements is taken; 16-byte aligned
- * rows (pointers, x_stride and N) are read and written in 16-byte pieces. */
+ * rows 0 is a no-op; N in [1, 2^26].  Any alignment of whole elements is taken; rows that start
+ * at 16-byte bounds and hold whole 16-byte pieces are the fastest. */
 #define KPOOL_DTYPE_BF16 0
 #define KPOOL_DTYPE_F32 1
 int kpool_layer_norm(const void *x, int64_t x_stride, const float *weight, const float *bias,

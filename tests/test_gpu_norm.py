@@ -95,6 +95,24 @@ def test_layer_norm_and_gradients(N, dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N,pad", [(1, 1), (3, 2), (5, 0), (7, 1), (8, 1), (9, 0), (64, 3), (127, 0), (129, 5), (257, 0),
+                                   (513, 1), (1023, 0), (1030, 0), (2049, 0), (4099, 2), (6150, 1), (8192, 1),
+                                   (8193, 0), (12289, 0), (16391, 3)])
+def test_rows_that_start_and_end_anywhere(N, pad, dtype):
+    """Rows at every alignment, whose last vector shares elements with the one before."""
+    for rows in (1, 37):
+        x, w, b, dy = inputs(rows, N, dtype, 10 * N + rows, pad, offset=1.0)
+        y, mean, rstd = K.layer_norm(x, w, b, 1e-5, want_stats=True)
+        check_forward(x, w, b, 1e-5, y, mean, rstd)
+        grads = K.layer_norm_backward(dy, x, w, mean, rstd)
+        check_backward(x, w, dy, mean, rstd, *grads)
+        assert all(torch.equal(p, q) for p, q in zip(grads, K.layer_norm_backward(dy, x, w, mean, rstd)))
+        again = K.layer_norm(x, w, b, 1e-5)[0]
+        assert torch.equal(again, y)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("rows,N,pad", [(70001, 128, 0), (70001, 128, 8), (3000, 100, 3), (5000, 640, 16)])
 def test_many_rows_and_row_strides(rows, N, pad, dtype):
     """Slices of a wider projection, on the vector path (pad 8, 16) and off it (pad 3)."""
