@@ -14,7 +14,8 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libkpool.so")
-SOURCES = ["api.hip", "pool_keys.hip", "score.hip", "topk.hip", "expand.hip", "norm.hip",
+# (layer.hip includes api.hip: one translation unit with the C ABI's shared state)
+SOURCES = ["layer.hip", "pool_keys.hip", "score.hip", "topk.hip", "expand.hip", "norm.hip",
            "attend.hip", "attend_bwd.hip"]
 # Per-file flags.  The score kernel runs with the IEEE mode bit off so that the
 # ReLU is one v_max_f32 (no NaN-quieting canonicalize before it); its inputs are
