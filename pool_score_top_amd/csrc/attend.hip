@@ -37,7 +37,7 @@ struct AttendArgs {
   float scale_log2;
   int64_t ntiles;
   int nsplit;
-  int chunk;  // keys (or list entries) of a split, a multiple of 256
+  int chunk;  // keys (or list entries) of a split, a multiple of 128
   const int32_t *ids;
   int width;
   bool by_place;
@@ -885,7 +885,8 @@ AttendPlan plan_list(int64_t Tq, int nseq, int width, int Hq, int Hkv) {
   p.ntiles = tile_start(Tq, nseq, 1, 1);
   const int64_t wgs = Tq * Hkv * ((Hq / Hkv + 31) / 32);
   const int64_t want = wgs > 0 ? (256 + wgs - 1) / wgs : 1;
-  p.chunk = width > 0 ? (int)round_up((width + want - 1) / want, 256) : 256;
+  // (128: 32 entries a wave; 8 tokens of 2048 entries 13.0 us captured, 13.3 with parts of 256)
+  p.chunk = width > 0 ? (int)round_up((width + want - 1) / want, 128) : 128;
   p.nsplit = (int)((width + p.chunk - 1) / p.chunk);
   if (p.nsplit <= 1) p.nsplit = 1, p.chunk = 0x7FFFFF00;
   // sharing takes several workgroups an XCD at a time
