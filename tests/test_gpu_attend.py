@@ -426,3 +426,32 @@ def test_outputs_in_the_gaps_of_strided_inputs():
     out = buf[7, 128:].view(1, 2, 64)
     K.attend(q, buf[:, None, :64], buf[:, None, 64:128], cu, dev, ck, ckd, out=out)
     assert torch.equal(out, ref)
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """Tokens 2^24 elements apart (the widest stride), 10 GB of them: the same bits as from tokens
+    side by side, by every kernel; the layer norm's rows likewise."""
+    T, wide = 300, 1 << 24
+    cu, dev = cu_of([T])
+    one, one_dev = cu_of([1])
+    q, k, v = (t[:T] for t in make(cu, cu, 4, 2, 64, 41))
+    far = torch.empty(T * wide, dtype=BF16, device="cuda").view(T, wide)
+    fq, fk, fv = (far[:, at:at + t[0].numel()].unflatten(1, t.shape[1:]) for at, t in ((0, q), (256, k), (wide - 128, v)))
+    for f, t in ((fq, q), (fk, k), (fv, v)):
+        f.copy_(t)
+    q, k, v = (t.contiguous() for t in (q, k, v))
+    ids = lists(cu, cu, 70, 3, "ragged")
+    many = torch.arange(T, dtype=torch.int32, device="cuda").repeat(T, 4)
+    d_o = torch.randn(T, 4, 64, device="cuda").to(BF16)
+
+    def calls(q, k, v):
+        o, lse = K.attend(q, k, v, cu, dev, want_lse=True)
+        out = [o, lse, *K.attend_backward(d_o, q, k, v, o, lse, cu, dev)]
+        out += K.attend(q[T - 1:], k, v, one, one_dev, cu, dev, want_lse=True)
+        for lists_of in (ids, many):
+            out += K.attend_selected(q, k, v, lists_of, cu, dev, want_lse=True)
+        return out + [K.layer_norm(x.flatten(1))[0] for x in (k, v)]
+
+    for near, there in zip(calls(q, k, v), calls(fq, fk, fv)):
+        assert torch.equal(near, there)

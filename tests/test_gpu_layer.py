@@ -133,3 +133,47 @@ def test_row_range():
     for lo, hi in ((-1, 3), (4, 3), (0, 1001)):
         with pytest.raises(ValueError):
             K.row_range([0, 300, 1000], lo, hi)
+
+
+@pytest.mark.gpu
+def test_calls_of_two_threads_at_once():
+    """Each on its own stream, with other sizes: the same bits as alone."""
+    import threading
+    from attend_reference import cu_of
+
+    def work(n, Hq, seed):
+        cu, dev = cu_of([n, n // 3])
+        q, k, v = make(cu, cu, Hq, 2, 64, seed)
+        g = torch.Generator().manual_seed(seed)
+        T = int(cu[-1])
+        ids = torch.randint(-1, n, (T, 150), generator=g, dtype=torch.int32).cuda()
+        d_o = torch.randn(T, Hq, 64, generator=g).to(BF16).cuda()
+        x = torch.randn(T, 301, generator=g).to(BF16).cuda()
+
+        def call(stream=None):
+            kw = dict(stream=stream)
+            o, lse = K.attend(q, k, v, cu, dev, want_lse=True, **kw)
+            y, mean, rstd = K.layer_norm(x, want_stats=True, **kw)
+            return [o, lse, *K.attend_backward(d_o, q, k, v, o, lse, cu, dev, **kw),
+                    *K.attend_selected(q, k, v, ids, cu, dev, want_lse=True, **kw),
+                    *K.layer_norm_backward(y, x, None, mean, rstd, **kw)]
+        return call
+
+    jobs = [work(700, 4, 1), work(1500, 8, 2)]
+    alone = [job() for job in jobs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run(job, want):
+        stream = torch.cuda.Stream()
+        for _ in range(10):
+            got = job(stream)
+            stream.synchronize()
+            wrong.extend(i for i, (a, b) in enumerate(zip(got, want)) if not torch.equal(a, b))
+
+    threads = [threading.Thread(target=run, args=pair) for pair in zip(jobs, alone)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
