@@ -11,15 +11,19 @@
 //
 // HBM-bound: about 8 (forward) and 21 (step) flops an element against 4 to 16 bytes.  So
 // each element is read once: a row lives in the registers of TPR threads (R vectors of VEC
-// elements each) between the statistics and the output.  Everything between load and store
-// is fp32; the one rounding is the output's to its type.
+// elements each) between the statistics and the output.  Between load and store everything but
+// the mean is fp32; the one rounding below that is the output's to its type.
+//   The mean's error counts against the row's spread, which may be far below the mean itself: in
+//   fp32 a row of 41 times 1000 gets 999.99994, off by more than its spread.  So the sum over a
+//   row and the mean are in 64 bits, and x - mean is taken as (x - high) - low of the mean's two
+//   fp32 parts: a constant row gives 0 exactly.
 //   TPR 16 for rows of up to 16 vectors (a head dim of 128 in bf16): a wave holds 4 rows,
 //          so no lane idles, and sums take 4 lane exchanges.
 //   TPR 64 up to 256 vectors (backward 128): a wave per row, no barrier.
 //   TPR 256 and 512 up to 2048 vectors (backward in bf16 1536): a workgroup per row.
 //   Longer rows are read again for each pass (the second and third reads hit the caches).
 // Measured (the card copies at 4.75 TB/s, reads and writes counted): 524288 x 128 in bf16,
-// forward, 46 us (5.8 TB/s); 8192 x 4096 in bf16, forward 24 us (5.6 TB/s), backward 45 us (4.5
+// forward, 47 us (5.7 TB/s); 8192 x 4096 in bf16, forward 24 us (5.6 TB/s), backward 45 us (4.5
 // TB/s) and 4 us to join the sums; 5003 x 1237 in fp32 at a pitch of 1328, forward 12.5 us (4.0
 // TB/s), backward 16 us (4.6 TB/s).
 //
@@ -159,8 +163,8 @@ __device__ inline void load_f32(const float *w, int c, int N, float (&v)[VEC]) {
 // Sums of K values over the TPR threads of a row, the same bits in every one of them.
 // TPR 256 and 512 go through `red` (two sets, used in turn, so that one barrier a sum is enough:
 // a set is written again only behind the barrier of the sum between).
-template <int TPR, int K>
-__device__ inline void row_sum(float (&s)[K], float (*red)[8][K], int &phase) {
+template <int TPR, int K, class S>
+__device__ inline void row_sum(S (&s)[K], S (*red)[8][K], int &phase) {
 #pragma unroll
   for (int d = 1; d < (TPR < 64 ? TPR : 64); d <<= 1)
 #pragma unroll
@@ -172,6 +176,14 @@ __device__ inline void row_sum(float (&s)[K], float (*red)[8][K], int &phase) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < K; ++i) {
+      if constexpr (sizeof(S) == 8) {
+        // (a wave's sum a lane: all 8 in every lane take the registers of a third workgroup a CU,
+        // 8187 x 4098 in fp32 forward 55 us, so 48)
+        s[i] = red[phase][threadIdx.x & (TPR / 64 - 1)][i];
+#pragma unroll
+        for (int d = 1; d < TPR / 64; d <<= 1) s[i] += __shfl_xor(s[i], d);
+        continue;
+      }
       s[i] = (red[phase][0][i] + red[phase][1][i]) + (red[phase][2][i] + red[phase][3][i]);
       if constexpr (TPR == 512)
         s[i] += (red[phase][4][i] + red[phase][5][i]) + (red[phase][6][i] + red[phase][7][i]);
@@ -180,16 +192,33 @@ __device__ inline void row_sum(float (&s)[K], float (*red)[8][K], int &phase) {
   }
 }
 
+// A row's mean as high + low in fp32.  sum / n, rounded once: where the quotient is a number (a
+// constant row's), that number.
+struct Mean {
+  float high, low;
+  __device__ inline Mean(double sum, double n, double inv_n) {
+    double m = sum * inv_n;
+    m = __builtin_fma(__builtin_fma(-m, n, sum), inv_n, m);
+    high = (float)m, low = (float)(m - high);
+  }
+  __device__ inline float below(float x) const { return (x - high) - low; }
+};
+// What a thread adds up of a row: in bf16 at most 32 values of 8 bits each, which fp32 holds (those
+// of one size exactly; beside larger ones, what it loses of a small one is far below their spread).
+template <class T>
+using Acc = std::conditional_t<sizeof(T) == 4, double, float>;
+
 // Rows in registers.  ROWS rows of a thread group are loaded before the first is worked on.
 template <int TPR>
 constexpr int kThreads = TPR > kNormThreads ? TPR : kNormThreads;
 template <class T, int VEC, bool ALIGNED, int TPR, int R, int ROWS>
 __global__ __launch_bounds__(kThreads<TPR>) void norm_kernel(
     const T *__restrict__ x, int64_t x_stride, const float *__restrict__ w,
-    const float *__restrict__ b, int64_t rows, int N, float eps, T *__restrict__ y,
+    const float *__restrict__ b, int64_t rows, int N, double inv, float eps, T *__restrict__ y,
     float *__restrict__ mean_out, float *__restrict__ rstd_out) {
   __shared__ float red[2][8][1];
-  int phase = 0;
+  __shared__ double red_sum[2][8][1];
+  int phase = 0, phase_sum = 0;
   constexpr int GROUPS = kThreads<TPR> / TPR;
   const int col = (threadIdx.x % TPR) * VEC;
   const int64_t row0 = ((int64_t)blockIdx.x * GROUPS + threadIdx.x / TPR) * ROWS;
@@ -216,27 +245,28 @@ __global__ __launch_bounds__(kThreads<TPR>) void norm_kernel(
       if (b) load_f32<ALIGNED>(b, c, N, bv[r]);
     }
   }
-  const float inv_n = 1.0f / (float)N;
+  const float inv_n = (float)inv;
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
     // (a group past the last row still takes part in the workgroup's barriers)
-    float s[1] = {0.0f};
+    Acc<T> own_sum = 0;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const Part<ALIGNED, VEC> own(col + r * TPR * VEC, N);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) s[0] += own.has(e) ? v[i][r][e] : 0.0f;
+      for (int e = 0; e < VEC; ++e) own_sum += own.has(e) ? v[i][r][e] : 0.0f;
     }
-    row_sum<TPR, 1>(s, red, phase);
-    const float mean = s[0] * inv_n;
-    s[0] = 0.0f;
+    double sum[1] = {own_sum};
+    row_sum<TPR, 1>(sum, red_sum, phase_sum);
+    const Mean mean(sum[0], N, inv);
+    float s[1] = {0.0f};
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const Part<ALIGNED, VEC> own(col + r * TPR * VEC, N);
       if (col + r * TPR * VEC < N)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          v[i][r][e] -= mean;
+          v[i][r][e] = mean.below(v[i][r][e]);
           s[0] = own.has(e) ? fmaf(v[i][r][e], v[i][r][e], s[0]) : s[0];
         }
     }
@@ -254,7 +284,7 @@ __global__ __launch_bounds__(kThreads<TPR>) void norm_kernel(
       }
     }
     if (threadIdx.x % TPR == 0) {
-      if (mean_out) mean_out[row0 + i] = mean;
+      if (mean_out) mean_out[row0 + i] = mean.high;
       if (rstd_out) rstd_out[row0 + i] = rstd;
     }
   }
@@ -264,29 +294,31 @@ __global__ __launch_bounds__(kThreads<TPR>) void norm_kernel(
 template <class T, bool ALIGNED>
 __global__ __launch_bounds__(kNormThreads) void norm_long_kernel(
     const T *__restrict__ x, int64_t x_stride, const float *__restrict__ w,
-    const float *__restrict__ b, int N, float eps, T *__restrict__ y,
+    const float *__restrict__ b, int N, double inv, float eps, T *__restrict__ y,
     float *__restrict__ mean_out, float *__restrict__ rstd_out) {
   __shared__ float red[2][8][1];
-  int phase = 0;
+  __shared__ double red_sum[2][8][1];
+  int phase = 0, phase_sum = 0;
   constexpr int VEC = kVec<T>;
   const int64_t row = blockIdx.x;
   const T *xr = x + row * x_stride;
   float v[VEC], wv[VEC], bv[VEC], s[1] = {0.0f};
+  double sum[1] = {0.0};
   for (int c = threadIdx.x * VEC; c < N; c += kNormThreads * VEC) {
     const Part<ALIGNED, VEC> own(c, N);
     load<T, ALIGNED>(xr, c, N, v);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) s[0] += own.has(e) ? v[e] : 0.0f;
+    for (int e = 0; e < VEC; ++e) sum[0] += own.has(e) ? v[e] : 0.0f;
   }
-  row_sum<256, 1>(s, red, phase);
-  const float inv_n = 1.0f / (float)N, mean = s[0] * inv_n;
-  s[0] = 0.0f;
+  row_sum<256, 1>(sum, red_sum, phase_sum);
+  const float inv_n = (float)inv;
+  const Mean mean(sum[0], N, inv);
   for (int c = threadIdx.x * VEC; c < N; c += kNormThreads * VEC) {
     const Part<ALIGNED, VEC> own(c, N);
     load<T, ALIGNED>(xr, c, N, v);
 #pragma unroll
     for (int e = 0; e < VEC; ++e)
-      if (own.has(e)) s[0] = fmaf(v[e] - mean, v[e] - mean, s[0]);
+      if (own.has(e)) s[0] = fmaf(mean.below(v[e]), mean.below(v[e]), s[0]);
   }
   row_sum<256, 1>(s, red, phase);
   const float rstd = 1.0f / sqrtf(fmaf(s[0], inv_n, eps));
@@ -297,11 +329,11 @@ __global__ __launch_bounds__(kNormThreads) void norm_long_kernel(
     if (w) load_f32<ALIGNED>(w, c, N, wv);
     if (b) load_f32<ALIGNED>(b, c, N, bv);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) v[e] = fmaf((v[e] - mean) * rstd, wv[e], bv[e]);
+    for (int e = 0; e < VEC; ++e) v[e] = fmaf(mean.below(v[e]) * rstd, wv[e], bv[e]);
     Io<T, VEC, ALIGNED>::store(y + row * N, c, N, v);
   }
   if (threadIdx.x == 0) {
-    if (mean_out) mean_out[row] = mean;
+    if (mean_out) mean_out[row] = mean.high;
     if (rstd_out) rstd_out[row] = rstd;
   }
 }
@@ -523,8 +555,8 @@ __global__ __launch_bounds__(kNormThreads) void norm_join_kernel(const float *__
 constexpr int64_t kNormLaunchRows = int64_t(1) << 22;
 
 // Unaligned rows of fp32 up to these go by single elements, forward and backward (us for 32 Mi
-// elements, single and by vectors: forward N = 65 98 128, 127 58 72, 501 62 42, 1237 42 45, 4098 85
-// 46; backward 65 115 196, 501 90 124, 1237 99 189, 2047 89 119, 4098 174 137; in bf16 vectors
+// elements, single and by vectors: forward N = 65 139 159, 127 72 82, 253 47 48, 501 83 42, 1237 78
+// 50; backward 65 115 196, 501 90 124, 1237 99 189, 2047 89 119, 4098 174 137; in bf16 vectors
 // always win: forward 65 120 35, 1237 57 35, 8191 70 31).
 constexpr int kSingle = 256, kSingleBwd = 2048;
 
@@ -541,7 +573,7 @@ void norm_go(const void *x, int64_t xs, const float *w, const float *b, int64_t 
              float eps, void *y, float *mean, float *rstd, hipStream_t st) {
   const int64_t per = (int64_t)(kThreads<TPR> / TPR) * ROWS;
   hipLaunchKernelGGL((norm_kernel<T, VEC, ALIGNED, TPR, R, ROWS>), dim3((unsigned)((rows + per - 1) / per)),
-                     dim3(kThreads<TPR>), 0, st, (const T *)x, xs, w, b, rows, N, eps, (T *)y, mean,
+                     dim3(kThreads<TPR>), 0, st, (const T *)x, xs, w, b, rows, N, 1.0 / N, eps, (T *)y, mean,
                      rstd);
 }
 
@@ -562,7 +594,7 @@ void norm_pick(const void *x, int64_t xs, const float *w, const float *b, int64_
   else if (nv <= 2048) KPOOL_NORM(512, 4, 1);
   else if constexpr (VEC > 1)
     hipLaunchKernelGGL((norm_long_kernel<T, ALIGNED>), dim3((unsigned)rows), dim3(kNormThreads), 0, st,
-                       (const T *)x, xs, w, b, N, eps, (T *)y, mean, rstd);
+                       (const T *)x, xs, w, b, N, 1.0 / N, eps, (T *)y, mean, rstd);
 #undef KPOOL_NORM
 }
 

@@ -310,3 +310,48 @@ def test_layer_norm_refuses_y_over_x(kw):
 def test_layer_norm_backward_refuses_dx_over_inputs(dx):
     assert _c_bwd(dy=1 << 20, x=2 << 20, stride=200, ws=3 << 20, dx=dx, dw=4 << 20, db=5 << 20) == K.KPOOL_EINVAL
     assert b"overlaps" in K.lib().kpool_last_error()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N,pad", [(3, 0), (41, 0), (61, 3), (82, 0), (336, 0), (1237, 1), (1240, 0), (4100, 0), (9001, 0),
+                                   (16404, 0), (20001, 0)])
+def test_constant_rows_of_every_width(N, pad, dtype):
+    """The mean of N equal numbers is that number, whatever N and 1 / N: y is the bias, rstd
+    1 / sqrt(eps), and with eps 0 the formula's NaN and infinity."""
+    values = torch.tensor([1000.0, 10001.0, 0.1, -77.7, 3e30, 1.0], device="cuda").to(dtype)
+    x = values[:, None].expand(-1, N + pad).contiguous()[:, :N]
+    _, w, b, _ = inputs(1, N, dtype, N)
+    y, mean, rstd = K.layer_norm(x, w, b, 1e-6, want_stats=True)
+    assert torch.equal(mean, values.float())
+    assert torch.equal(y, b.to(dtype).expand_as(y))
+    # (the root and the division: half a step each, eps itself is given in fp32)
+    want = 1.0 / torch.tensor(1e-6, dtype=torch.float32).double().sqrt().item()
+    assert ((rstd.double() - want).abs() <= 3 * U * want).all()
+    y, _, rstd = K.layer_norm(x, w, b, 0.0, want_stats=True)
+    assert y.isnan().all() and (rstd == float("inf")).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N,pad", [(100, 0), (123, 1), (1237, 0), (4096, 0), (9000, 3), (20480, 0)])
+def test_small_spread_around_a_large_mean(N, pad, dtype):
+    """Rows whose mean is thousands of times their spread.  x - mean takes three roundings of its
+    own size (x minus the mean's fp32 part, less the rest, and that rest's 2^-24 of 2^-24 of the
+    mean), the mean in 64 bits none that counts; rstd is a sum of N squares of those.  The mean
+    that is returned is rounded once."""
+    x, w, b, _ = inputs(37, N, torch.float32, N)
+    x = 10000.0 + x * torch.logspace(-2, 1.5, 37, device="cuda")[:, None]
+    wide = torch.zeros(37, N + pad, dtype=dtype, device="cuda")
+    wide[:, :N] = x.to(dtype)
+    x = wide[:, :N]
+    eps = 1e-6
+    y, mean, rstd = K.layer_norm(x, w, b, eps, want_stats=True)
+    y64, m64, r64 = forward64(x.double(), w.double(), b.double(), eps)
+    assert ((mean.double() - m64[:, 0]).abs() <= 1.001 * U * m64[:, 0].abs()).all()
+    depth = N / 16 + 16
+    assert ((rstd.double() - r64[:, 0]).abs() <= (depth + 8) * U * r64[:, 0]).all()
+    xc = (x.double() - m64).abs()
+    tol32 = w.double().abs() * r64 * ((depth + 16) * U * xc + 4 * U * U * m64.abs()) + 3 * U * b.double().abs()
+    tol = tol32 + HALF[dtype] * (y64.abs() + tol32)
+    assert ((y.double() - y64).abs() <= tol).all()
