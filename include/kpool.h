@@ -354,10 +354,14 @@ int kpool_layer_norm_backward(const void *dy, const void *x, int64_t x_stride, c
  * Other threads' records and switches are untouched.  Event spans of
  * overlapped chunks (KPOOL_FLAG_OVERLAP) include whatever else the GPU runs
  * meanwhile; time kernels with flags = 0. */
-#define KPOOL_PROFILE_KINDS 7 /* 0 pool_keys, 1 score, 2 topk, 3 expand, 4 scores_out copy,
-                                 5 layer norm, 6 attention (a call's launches as one) */
+#define KPOOL_PROFILE_KINDS 5 /* 0 pool_keys, 1 score, 2 topk, 3 expand, 4 scores_out copy */
 int kpool_profile_enable(int on);
 int kpool_profile_collect(double *ms, int64_t *launches);
+/* The same for the calls around the selection (a call's launches as one), which
+ * kpool_profile_collect neither reports nor forgets: arrays of
+ * KPOOL_LAYER_PROFILE_KINDS. */
+#define KPOOL_LAYER_PROFILE_KINDS 2 /* 0 layer norm, 1 attention */
+int kpool_layer_profile_collect(double *ms, int64_t *launches);
 
 #ifdef __cplusplus
 }

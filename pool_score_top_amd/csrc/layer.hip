@@ -7,6 +7,22 @@
 
 namespace {
 
+// The timing records of these entry points, apart from the selection's: a caller that knows only the
+// selection's kinds collects into arrays of that many.
+enum { kNorm, kAttend };
+thread_local std::vector<ProfRec> g_layer_prof;
+
+template <class F>
+hipError_t timed_layer(int kind, hipStream_t stream, F &&launch) {
+  const size_t before = g_prof.size();
+  const hipError_t e = timed(kind, stream, launch);
+  if (g_prof.size() > before) {
+    g_layer_prof.push_back(g_prof.back());
+    g_prof.pop_back();
+  }
+  return e;
+}
+
 // Whether the n bytes at `out` meet one of `rows` rows of `len` bytes, `pitch` bytes apart from
 // `in` on (pitch >= len).
 bool meets(const void *out, int64_t n, const void *in, int64_t rows, int64_t len, int64_t pitch) {
@@ -131,7 +147,7 @@ int kpool_attend(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t
   if (!rc) rc = check_outputs(fn, c);
   if (rc) return rc;
   hipStream_t st = (hipStream_t)stream;
-  hipError_t e = timed(6, st, [&] { return kpool::launch_attend(c, p, workspace, st); });
+  hipError_t e = timed_layer(kAttend, st, [&] { return kpool::launch_attend(c, p, workspace, st); });
   if (e != hipSuccess) return hip_fail(fn, e);
   return ok();
 }
@@ -184,7 +200,7 @@ int kpool_attend_backward(const uint16_t *d_o, const uint16_t *q, int64_t q_stri
       return fail(KPOOL_EINVAL, "%s: %s overlaps d_o, o, lse or another output", fn, outs[i].name);
   }
   hipStream_t st = (hipStream_t)stream;
-  hipError_t e = timed(6, st, [&] {
+  hipError_t e = timed_layer(kAttend, st, [&] {
     return kpool::launch_attend_bwd(c, d_o, p, workspace, dq, dk, dv, st);
   });
   if (e != hipSuccess) return hip_fail(fn, e);
@@ -226,7 +242,7 @@ int kpool_attend_selected(const uint16_t *q, int64_t q_stride, const uint16_t *k
   if (meets(o, c.Tq * Hq * D * 2, token_ids, ids) || meets(lse, c.Tq * Hq * 4, token_ids, ids))
     return fail(KPOOL_EINVAL, "%s: o or lse overlaps token_ids", fn);
   hipStream_t st = (hipStream_t)stream;
-  hipError_t e = timed(6, st, [&] {
+  hipError_t e = timed_layer(kAttend, st, [&] {
     return kpool::launch_attend_list(c, p, token_ids, width, workspace, st);
   });
   if (e != hipSuccess) return hip_fail(fn, e);
@@ -250,7 +266,7 @@ int kpool_layer_norm(const void *x, int64_t x_stride, const float *weight, const
   if (meets(y, rows * N * size, x, rows, N * size, x_stride * size))
     return fail(KPOOL_EINVAL, "%s: y overlaps x", fn);
   hipStream_t st = (hipStream_t)stream;
-  hipError_t e = timed(5, st, [&] {
+  hipError_t e = timed_layer(kNorm, st, [&] {
     return kpool::launch_norm(dtype == KPOOL_DTYPE_F32, x, x_stride, weight, bias, rows, N, eps, y, mean,
                               rstd, st);
   });
@@ -290,12 +306,19 @@ int kpool_layer_norm_backward(const void *dy, const void *x, int64_t x_stride, c
       meets(dx, rows * row_bytes, dy, rows * row_bytes))
     return fail(KPOOL_EINVAL, "%s: dx overlaps x or dy", fn);
   hipStream_t st = (hipStream_t)stream;
-  hipError_t e = timed(5, st, [&] {
+  hipError_t e = timed_layer(kNorm, st, [&] {
     return kpool::launch_norm_bwd(dtype == KPOOL_DTYPE_F32, dy, x, x_stride, weight, mean, rstd, rows, N,
                                   dx, dweight, dbias, (float *)workspace, st);
   });
   if (e != hipSuccess) return hip_fail(fn, e);
   return ok();
+}
+
+int kpool_layer_profile_collect(double *ms, int64_t *launches) {
+  std::swap(g_prof, g_layer_prof);
+  const int rc = kpool_profile_collect(ms, launches);
+  std::swap(g_prof, g_layer_prof);
+  return rc;
 }
 
 }  // extern "C"

@@ -19,7 +19,8 @@ LIB_PATH = os.path.join(HERE, "libkpool.so")
 KPOOL_OK, KPOOL_EINVAL, KPOOL_EUNSUPPORTED, KPOOL_EWORKSPACE, KPOOL_EHIP = 0, -1, -2, -3, -4
 KPOOL_FLAG_OVERLAP = 1
 KPOOL_FLAG_TAIL = 2
-PROFILE_KINDS = ("pool_keys", "score", "topk", "expand", "scores_copy", "norm", "attend")
+PROFILE_KINDS = ("pool_keys", "score", "topk", "expand", "scores_copy")
+LAYER_PROFILE_KINDS = ("norm", "attend")
 KPOOL_DTYPE_BF16, KPOOL_DTYPE_F32 = 0, 1
 
 _lib = None
@@ -70,6 +71,7 @@ def lib():
                                                      vp, vp, vp, vp]),
         "kpool_profile_enable": (ctypes.c_int, [ctypes.c_int]),
         "kpool_profile_collect": (ctypes.c_int, [vp, vp]),
+        "kpool_layer_profile_collect": (ctypes.c_int, [vp, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -607,10 +609,14 @@ def profile_enable(on: bool = True):
 
 def profile_collect():
     """{kind: (ms, launches)} accumulated since the last collect."""
-    ms = (ctypes.c_double * len(PROFILE_KINDS))()
-    n = (ctypes.c_int64 * len(PROFILE_KINDS))()
-    _check(lib().kpool_profile_collect(ms, n), "kpool_profile_collect")
-    return {k: (ms[i], int(n[i])) for i, k in enumerate(PROFILE_KINDS)}
+    out = {}
+    for kinds, fn in ((PROFILE_KINDS, "kpool_profile_collect"),
+                      (LAYER_PROFILE_KINDS, "kpool_layer_profile_collect")):
+        ms = (ctypes.c_double * len(kinds))()
+        n = (ctypes.c_int64 * len(kinds))()
+        _check(getattr(lib(), fn)(ms, n), fn)
+        out.update((k, (ms[i], int(n[i]))) for i, k in enumerate(kinds))
+    return out
 
 
 def row_range(cu, q_lo: int, q_hi: int):

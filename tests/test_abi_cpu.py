@@ -250,3 +250,12 @@ def test_c_example_is_built_and_rejects_bad_usage(tmp_path):
     p = subprocess.run([B.EXAMPLE, str(short), str(tmp_path / "out.bin")], capture_output=True, text=True,
                        timeout=60)
     assert p.returncode == 2 and "short input" in p.stderr
+
+
+def test_profile_kinds_of_the_header_and_the_binding():
+    """The selection's array keeps its five entries within an ABI version."""
+    text = open(os.path.join(ROOT, "include", "kpool.h")).read()
+    assert "#define KPOOL_PROFILE_KINDS 5 " in text and len(K.PROFILE_KINDS) == 5
+    assert "#define KPOOL_LAYER_PROFILE_KINDS 2 " in text and len(K.LAYER_PROFILE_KINDS) == 2
+    assert K.lib().kpool_layer_profile_collect(None, None) == K.KPOOL_OK
+    assert list(K.profile_collect()) == list(K.PROFILE_KINDS + K.LAYER_PROFILE_KINDS)

@@ -177,3 +177,32 @@ def test_calls_of_two_threads_at_once():
     for t in threads:
         t.join()
     assert not wrong
+
+
+@pytest.mark.gpu
+def test_profiles_of_the_layer_and_of_the_selection_are_apart():
+    """A program that knows the selection's five kinds collects into five entries, whatever else ran
+    on its thread; the layer's calls have two entries of their own."""
+    import ctypes
+    cu = [0, 300, 500]
+    sel, _, dev, norm, _, (q, k, v), _, _ = layer(cu, 4, 32, 13)
+    K.profile_collect()
+    K.profile_enable(True)
+    try:
+        for _ in range(3):
+            sel.run(dev["q"], dev["k"], dev["w"], k_norm=norm)
+            sel.attend(q, k, v)
+    finally:
+        K.profile_enable(False)
+
+    def collect(fn):
+        ms, n = (ctypes.c_double * 16)(*[7.0] * 16), (ctypes.c_int64 * 16)(*[7] * 16)
+        assert getattr(K.lib(), fn)(ms, n) == K.KPOOL_OK
+        return list(ms), list(n)
+
+    ms, n = collect("kpool_profile_collect")
+    assert n == [10, 10, 10, 10, 7] + [7] * 11 and ms[4:] == [7.0] * 12
+    assert all(t > 7.0 for t in ms[:4])
+    ms, n = collect("kpool_layer_profile_collect")
+    assert n == [10, 10] + [7] * 14 and all(t > 7.0 for t in ms[:2]) and ms[2:] == [7.0] * 14
+    assert set(x[1] for x in K.profile_collect().values()) == {0}
