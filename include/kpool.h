@@ -256,8 +256,8 @@ int kpool_topk(const float *scores, int64_t ld, const int32_t *n_valid, int64_t 
  *   lse      NULLABLE fp32 [Tq, Hq]
  * A row that sees nothing gets o = 0 and lse = -inf.  Sums and statistics are fp32; the
  * weights are rounded to bf16 for the product with v, and o once.  q, k and v must be finite
- * in the rows of the sequences; nothing outside them is read.  Outputs must not overlap
- * inputs.  The same call gives the same bits every time.
+ * in the rows of the sequences; nothing outside them is read.  Outputs and the workspace
+ * overlap neither inputs nor one another.  The same call gives the same bits every time.
  * Sizes: D a multiple of 8 up to 128; Hq a multiple of Hkv; strides multiples of 8 from
  * H * D to 2^24; q, k, v, o and the workspace 16-byte aligned.
  *   workspace  kpool_attend_workspace_bytes(the same sizes) bytes (may be 0: then it is
@@ -280,9 +280,9 @@ int kpool_attend(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t
  *   dq       bf16 [Tq, Hq, D];  dk, dv  bf16 [Tk, Hkv, D], contiguous, overwritten (0 for a
  *            row that sees nothing and a key that no row sees)
  *   workspace  kpool_attend_backward_workspace_bytes bytes, 16-byte aligned; scratch
- * The other arguments are the forward call's, and d_o must be finite as well; the outputs
- * overlap neither inputs nor one another.  Sums are fp32
- * in a fixed order (no atomics): the same call gives the same bits. */
+ * The other arguments are the forward call's, and d_o must be finite as well; the outputs and
+ * the workspace overlap neither inputs nor one another.  Sums are fp32 in a fixed order (no
+ * atomics): the same call gives the same bits. */
 size_t kpool_attend_backward_workspace_bytes(const int32_t *cu_q_host, const int32_t *cu_k_host,
                                              int32_t nseq, int32_t Hq, int32_t Hkv, int32_t D);
 int kpool_attend_backward(const uint16_t *d_o, const uint16_t *q, int64_t q_stride, const uint16_t *k,
@@ -319,8 +319,9 @@ int kpool_attend_selected(const uint16_t *q, int64_t q_stride, const uint16_t *k
  *            wider projection needs no copy
  *   weight   fp32 [N], NULL for ones;  bias fp32 [N], NULL for zeros
  *   eps      finite, >= 0 (a constant row with eps = 0 gives the formula's NaN)
- *   y        [rows, N] contiguous, not overlapping x
+ *   y        [rows, N] contiguous
  *   mean, rstd  NULLABLE fp32 [rows]: what the backward pass reads
+ * The outputs overlap neither inputs nor one another.
  * rows 0 is a no-op; N in [1, 2^26].  Any alignment of whole elements is taken; rows that start
  * at 16-byte bounds and hold whole 16-byte pieces are the fastest. */
 #define KPOOL_DTYPE_BF16 0
@@ -334,12 +335,13 @@ int kpool_layer_norm(const void *x, int64_t x_stride, const float *weight, const
  *   dweight[j] = sum_r dy * xh,   dbias[j] = sum_r dy            (fp32 sums)
  *   dy       [rows, N] contiguous;  x, x_stride, weight as in the forward call
  *   mean, rstd  fp32 [rows] from it
- *   dx       NULLABLE [rows, N] contiguous, not overlapping x or dy
+ *   dx       NULLABLE [rows, N] contiguous
  *   dweight, dbias  NULLABLE fp32 [N], overwritten
  *   workspace  kpool_layer_norm_backward_workspace_bytes(rows, N) bytes where dweight or
  *            dbias is given (NULL and 0 otherwise), 16-byte aligned; scratch on return
- * The sums over rows run in a fixed order: the same inputs give the same bits.  rows 0
- * writes zeros to dweight and dbias. */
+ * The outputs and the workspace overlap neither inputs nor one another.  The sums over rows
+ * run in a fixed order: the same inputs give the same bits.  rows 0 writes zeros to dweight
+ * and dbias. */
 size_t kpool_layer_norm_backward_workspace_bytes(int64_t rows, int32_t N);
 int kpool_layer_norm_backward(const void *dy, const void *x, int64_t x_stride, const float *weight,
                               const float *mean, const float *rstd, int64_t rows, int32_t N,

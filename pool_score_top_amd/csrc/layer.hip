@@ -3,6 +3,8 @@
 //
 // One translation unit with api.hip, whose error text, checks and profile records these entry
 // points share and which keep to that file.
+#include <initializer_list>
+
 #include "api.hip"
 
 namespace {
@@ -23,16 +25,34 @@ hipError_t timed_layer(int kind, hipStream_t stream, F &&launch) {
   return e;
 }
 
-// Whether the n bytes at `out` meet one of `rows` rows of `len` bytes, `pitch` bytes apart from
-// `in` on (pitch >= len).
-bool meets(const void *out, int64_t n, const void *in, int64_t rows, int64_t len, int64_t pitch) {
-  if (!out || !in || n <= 0 || rows <= 0 || len <= 0) return false;
+// What a call reads or writes at p: `rows` rows of `len` bytes, `pitch` bytes apart (pitch >= len);
+// one row for what is contiguous.
+struct Operand {
+  const char *name;
+  const void *p;
+  int64_t len, rows = 1, pitch = 0;
+};
+
+// Whether a contiguous operand meets one of the other's rows.
+bool meets(const Operand &out, const Operand &in) {
+  if (!out.p || !in.p || out.len <= 0 || in.rows <= 0 || in.len <= 0) return false;
+  const int64_t from = (int64_t)((uintptr_t)out.p - (uintptr_t)in.p);
+  if (from + out.len <= 0 || from >= (in.rows - 1) * in.pitch + in.len) return false;
   // the first row that ends behind `out`'s start, if that one starts before its end
-  const int64_t from = (int64_t)((uintptr_t)out - (uintptr_t)in);
-  const int64_t r = from < len ? 0 : (from - len) / pitch + 1;
-  return r < rows && r * pitch < from + n;
+  const int64_t r = from < in.len ? 0 : (from - in.len) / in.pitch + 1;
+  return r < in.rows && r * in.pitch < from + out.len;
 }
-bool meets(const void *out, int64_t n, const void *in, int64_t len) { return meets(out, n, in, 1, len, len); }
+
+// What is written (contiguous, the workspace among it) apart from what is read and from one another.
+int check_apart(const char *fn, std::initializer_list<Operand> written, std::initializer_list<Operand> read) {
+  for (const Operand *w = written.begin(); w != written.end(); ++w) {
+    for (const Operand &r : read)
+      if (meets(*w, r)) return fail(KPOOL_EINVAL, "%s: %s overlaps %s", fn, w->name, r.name);
+    for (const Operand *x = w + 1; x != written.end(); ++x)
+      if (meets(*w, *x)) return fail(KPOOL_EINVAL, "%s: %s overlaps %s", fn, w->name, x->name);
+  }
+  return KPOOL_OK;
+}
 
 int check_norm(const char *fn, int64_t rows, int32_t N, int64_t x_stride, int32_t dtype) {
   if (dtype != KPOOL_DTYPE_BF16 && dtype != KPOOL_DTYPE_F32)
@@ -87,26 +107,15 @@ int check_attend(const char *fn, kpool::AttendCall &c, const int32_t *cu_q_host,
   return KPOOL_OK;
 }
 
-// n bytes of an output apart from q, k and v
-int check_apart(const char *fn, const kpool::AttendCall &c, const char *name, const void *out, int64_t n) {
-  if (meets(out, n, c.q, c.Tq, c.Hq * c.D * 2, c.q_stride * 2) ||
-      meets(out, n, c.k, c.Tk, c.Hkv * c.D * 2, c.k_stride * 2) ||
-      meets(out, n, c.v, c.Tk, c.Hkv * c.D * 2, c.v_stride * 2))
-    return fail(KPOOL_EINVAL, "%s: %s overlaps q, k or v", fn, name);
-  return KPOOL_OK;
-}
+Operand q_of(const kpool::AttendCall &c) { return {"q", c.q, (int64_t)c.Hq * c.D * 2, c.Tq, c.q_stride * 2}; }
+Operand k_of(const kpool::AttendCall &c) { return {"k", c.k, (int64_t)c.Hkv * c.D * 2, c.Tk, c.k_stride * 2}; }
+Operand v_of(const kpool::AttendCall &c) { return {"v", c.v, (int64_t)c.Hkv * c.D * 2, c.Tk, c.v_stride * 2}; }
+Operand cu_q_of(const kpool::AttendCall &c) { return {"cu_q", c.cu_q, ((int64_t)c.nseq + 1) * 4}; }
+Operand cu_k_of(const kpool::AttendCall &c) { return {"cu_k", c.cu_k, ((int64_t)c.nseq + 1) * 4}; }
 
-int check_outputs(const char *fn, const kpool::AttendCall &c) {
-  const int64_t rows = c.Tq * c.Hq;
-  int rc = check_apart(fn, c, "o", c.o, rows * c.D * 2);
-  if (!rc && c.lse) rc = check_apart(fn, c, "lse", c.lse, rows * 4);
-  if (!rc && meets(c.lse, rows * 4, c.o, rows * c.D * 2))
-    return fail(KPOOL_EINVAL, "%s: lse overlaps o", fn);
-  return rc;
-}
-
+// The forward calls' plan, workspace and outputs; ids: the lists, if there are any.
 int check_attend_plan(const char *fn, const kpool::AttendCall &c, const kpool::AttendPlan &p, int64_t per,
-                      const void *workspace, size_t workspace_bytes) {
+                      const void *workspace, size_t workspace_bytes, const Operand &ids) {
   // a launch's threads stay below 2^32: workgroups of 512 for tiles, of 256 else
   if (p.ntiles * per * p.nsplit * c.Hkv >= (int64_t(1) << (p.form == kpool::AttendPlan::kTiles ? 23 : 24)) - 8)
     return fail(KPOOL_EUNSUPPORTED, "%s: too many query rows for one launch", fn);
@@ -115,7 +124,9 @@ int check_attend_plan(const char *fn, const kpool::AttendCall &c, const kpool::A
     return fail(KPOOL_EWORKSPACE, "%s: needs %zu bytes of workspace, got %zu", fn, need,
                 workspace ? workspace_bytes : (size_t)0);
   if (need && !aligned16(workspace)) return fail(KPOOL_EINVAL, "%s: workspace must be 16-byte aligned", fn);
-  return KPOOL_OK;
+  const int64_t rows = c.Tq * c.Hq;
+  return check_apart(fn, {{"o", c.o, rows * c.D * 2}, {"lse", c.lse, rows * 4}, {"workspace", workspace, (int64_t)need}},
+                     {q_of(c), k_of(c), v_of(c), cu_q_of(c), cu_k_of(c), ids});
 }
 
 }  // namespace
@@ -143,8 +154,7 @@ int kpool_attend(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t
   int rc = check_attend(fn, c, cu_q_host, cu_k_host);
   if (rc || c.Tq == 0) return rc;
   const kpool::AttendPlan p = kpool::plan_attend(cu_q_host, cu_k_host, nseq, Hq, Hkv);
-  rc = check_attend_plan(fn, c, p, 1, workspace, workspace_bytes);
-  if (!rc) rc = check_outputs(fn, c);
+  rc = check_attend_plan(fn, c, p, 1, workspace, workspace_bytes, {});
   if (rc) return rc;
   hipStream_t st = (hipStream_t)stream;
   hipError_t e = timed_layer(kAttend, st, [&] { return kpool::launch_attend(c, p, workspace, st); });
@@ -189,16 +199,10 @@ int kpool_attend_backward(const uint16_t *d_o, const uint16_t *q, int64_t q_stri
                 workspace ? workspace_bytes : (size_t)0);
   if (!aligned16(workspace)) return fail(KPOOL_EINVAL, "%s: workspace must be 16-byte aligned", fn);
   const int64_t qbytes = c.Tq * Hq * D * 2, kbytes = c.Tk * Hkv * D * 2, lbytes = c.Tq * Hq * 4;
-  const struct { const char *name; const void *p; int64_t n; } outs[3] = {{"dq", dq, qbytes}, {"dk", dk, kbytes},
-                                                                           {"dv", dv, kbytes}};
-  for (int i = 0; i < 3; ++i) {
-    if ((rc = check_apart(fn, c, outs[i].name, outs[i].p, outs[i].n))) return rc;
-    const auto &next = outs[(i + 1) % 3];
-    if (meets(outs[i].p, outs[i].n, d_o, qbytes) || meets(outs[i].p, outs[i].n, o, qbytes) ||
-        meets(outs[i].p, outs[i].n, lse, lbytes) ||
-        meets(outs[i].p, outs[i].n, next.p, next.n))
-      return fail(KPOOL_EINVAL, "%s: %s overlaps d_o, o, lse or another output", fn, outs[i].name);
-  }
+  rc = check_apart(fn, {{"dq", dq, qbytes}, {"dk", dk, kbytes}, {"dv", dv, kbytes}, {"workspace", workspace, (int64_t)need}},
+                   {q_of(c), k_of(c), v_of(c), cu_q_of(c), cu_k_of(c), {"d_o", d_o, qbytes}, {"o", o, qbytes},
+                    {"lse", lse, lbytes}});
+  if (rc) return rc;
   hipStream_t st = (hipStream_t)stream;
   hipError_t e = timed_layer(kAttend, st, [&] {
     return kpool::launch_attend_bwd(c, d_o, p, workspace, dq, dk, dv, st);
@@ -235,12 +239,9 @@ int kpool_attend_selected(const uint16_t *q, int64_t q_stride, const uint16_t *k
   if (width > 0 && !token_ids) return fail(KPOOL_EINVAL, "%s: null pointer", fn);
   if ((uintptr_t)token_ids & 3) return fail(KPOOL_EINVAL, "%s: token_ids is not aligned to its elements", fn);
   const kpool::AttendPlan p = kpool::plan_list(c.Tq, nseq, width, Hq, Hkv);
-  rc = check_attend_plan(fn, c, p, (Hq / Hkv + 31) / 32, workspace, workspace_bytes);
-  if (!rc) rc = check_outputs(fn, c);
+  rc = check_attend_plan(fn, c, p, (Hq / Hkv + 31) / 32, workspace, workspace_bytes,
+                         {"token_ids", token_ids, c.Tq * width * 4});
   if (rc) return rc;
-  const int64_t ids = c.Tq * width * 4;
-  if (meets(o, c.Tq * Hq * D * 2, token_ids, ids) || meets(lse, c.Tq * Hq * 4, token_ids, ids))
-    return fail(KPOOL_EINVAL, "%s: o or lse overlaps token_ids", fn);
   hipStream_t st = (hipStream_t)stream;
   hipError_t e = timed_layer(kAttend, st, [&] {
     return kpool::launch_attend_list(c, p, token_ids, width, workspace, st);
@@ -263,8 +264,9 @@ int kpool_layer_norm(const void *x, int64_t x_stride, const float *weight, const
   if ((((uintptr_t)x | (uintptr_t)y) & mask) ||
       (((uintptr_t)weight | (uintptr_t)bias | (uintptr_t)mean | (uintptr_t)rstd) & 3))
     return fail(KPOOL_EINVAL, "%s: a pointer is not aligned to its elements", fn);
-  if (meets(y, rows * N * size, x, rows, N * size, x_stride * size))
-    return fail(KPOOL_EINVAL, "%s: y overlaps x", fn);
+  rc = check_apart(fn, {{"y", y, rows * N * size}, {"mean", mean, rows * 4}, {"rstd", rstd, rows * 4}},
+                   {{"x", x, N * size, rows, x_stride * size}, {"weight", weight, N * 4LL}, {"bias", bias, N * 4LL}});
+  if (rc) return rc;
   hipStream_t st = (hipStream_t)stream;
   hipError_t e = timed_layer(kNorm, st, [&] {
     return kpool::launch_norm(dtype == KPOOL_DTYPE_F32, x, x_stride, weight, bias, rows, N, eps, y, mean,
@@ -295,16 +297,20 @@ int kpool_layer_norm_backward(const void *dy, const void *x, int64_t x_stride, c
   if ((((uintptr_t)x | (uintptr_t)dy | (uintptr_t)dx) & mask) ||
       (((uintptr_t)weight | (uintptr_t)mean | (uintptr_t)rstd | (uintptr_t)dweight | (uintptr_t)dbias) & 3))
     return fail(KPOOL_EINVAL, "%s: a pointer is not aligned to its elements", fn);
+  size_t need = 0;
   if (sums) {
-    const size_t need = kpool_layer_norm_backward_workspace_bytes(rows, N);
+    need = kpool_layer_norm_backward_workspace_bytes(rows, N);
     if (!workspace || workspace_bytes < need)
       return fail(KPOOL_EWORKSPACE, "%s: needs %zu bytes of workspace, got %zu", fn, need,
                   workspace ? workspace_bytes : (size_t)0);
     if (!aligned16(workspace)) return fail(KPOOL_EINVAL, "%s: workspace must be 16-byte aligned", fn);
   }
-  if (meets(dx, rows * row_bytes, x, rows, row_bytes, x_stride * size) ||
-      meets(dx, rows * row_bytes, dy, rows * row_bytes))
-    return fail(KPOOL_EINVAL, "%s: dx overlaps x or dy", fn);
+  rc = check_apart(fn,
+                   {{"dx", dx, rows * row_bytes}, {"dweight", dweight, N * 4LL}, {"dbias", dbias, N * 4LL},
+                    {"workspace", workspace, (int64_t)need}},
+                   {{"dy", dy, rows * row_bytes}, {"x", x, row_bytes, rows, x_stride * size},
+                    {"weight", weight, N * 4LL}, {"mean", mean, rows * 4}, {"rstd", rstd, rows * 4}});
+  if (rc) return rc;
   hipStream_t st = (hipStream_t)stream;
   hipError_t e = timed_layer(kNorm, st, [&] {
     return kpool::launch_norm_bwd(dtype == KPOOL_DTYPE_F32, dy, x, x_stride, weight, mean, rstd, rows, N,

@@ -455,3 +455,26 @@ def test_offsets_past_32_bits():
 
     for near, there in zip(calls(q, k, v), calls(fq, fk, fv)):
         assert torch.equal(near, there)
+
+
+@pytest.mark.parametrize("selected", [False, True])
+@pytest.mark.parametrize("name", ["q", "k", "v", "o", "lse", "cqd", "ckd", "ids"])
+def test_refuses_a_workspace_over_operands(selected, name):
+    """Single tokens over long keys, whose parts take a workspace."""
+    if name == "ids" and not selected:
+        return
+    at = dict(q=1 << 32, k=2 << 32, v=3 << 32, ids=4 << 32, ws=5 << 32, o=6 << 32, lse=7 << 32, cqd=8 << 32,
+              ckd=9 << 32)
+    at["ws"] = at[name] if name in ("cqd", "ckd") else at[name] + 16
+    assert _call(selected, **at, cu_q=[0, 1, 2], cu_k=[0, 50000, 100000], width=2048) == K.KPOOL_EINVAL
+    assert b"overlaps" in K.lib().kpool_last_error()
+
+
+@pytest.mark.parametrize("selected", [False, True])
+@pytest.mark.parametrize("out", ["o", "lse"])
+@pytest.mark.parametrize("name", ["cqd", "ckd"])
+def test_refuses_outputs_over_lengths(selected, out, name):
+    at = dict(APART, cqd=8 << 20, ckd=9 << 20)
+    at[out] = at[name]
+    assert _call(selected, **at) == K.KPOOL_EINVAL
+    assert b"overlaps" in K.lib().kpool_last_error()

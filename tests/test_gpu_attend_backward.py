@@ -207,3 +207,11 @@ def test_refuses_outputs_over_inputs(kw):
 def test_keys_without_rows_need_their_pointers(kw):
     """The keys' kernel loads its keys even where no row sees them."""
     assert _call(**{**APART, "cu_q": [0, 0, 0], **kw}) == K.KPOOL_EINVAL
+
+
+@pytest.mark.parametrize("kw", [
+    *[dict(ws=APART[n]) for n in ("d_o", "q", "k", "v", "o", "lse", "dq", "dk", "dv")],
+    *[{out: 11 << 20, n: 11 << 20} for out in ("ws", "dq", "dk", "dv") for n in ("cqd", "ckd")]])
+def test_refuses_a_workspace_over_operands_and_outputs_over_lengths(kw):
+    assert _call(**{**APART, "cqd": 12 << 20, "ckd": 13 << 20, **kw}) == K.KPOOL_EINVAL
+    assert b"overlaps" in K.lib().kpool_last_error()

@@ -355,3 +355,42 @@ def test_small_spread_around_a_large_mean(N, pad, dtype):
     tol32 = w.double().abs() * r64 * ((depth + 16) * U * xc + 4 * U * U * m64.abs()) + 3 * U * b.double().abs()
     tol = tol32 + HALF[dtype] * (y64.abs() + tol32)
     assert ((y.double() - y64).abs() <= tol).all()
+
+
+# (addresses 1 MiB apart; the refusals come before any launch)
+APART = dict(x=1 << 20, w=2 << 20, b=3 << 20, y=4 << 20, mean=5 << 20, rstd=6 << 20)
+BWD_APART = dict(dy=1 << 20, x=2 << 20, w=3 << 20, mean=4 << 20, rstd=5 << 20, ws=6 << 20, dx=7 << 20, dw=8 << 20,
+                 db=9 << 20)
+
+
+@pytest.mark.parametrize("kw", [
+    *[{out: APART[n] + 4} for out in ("mean", "rstd") for n in ("x", "w", "b", "y")],
+    *[dict(y=APART[n]) for n in ("w", "b")], dict(mean=APART["rstd"]), dict(rstd=APART["mean"] + 12),
+    dict(mean=APART["x"] + 3 * 512 + 252, stride=256), dict(y=APART["w"] - 1022), dict(b=APART["y"] + 1020)])
+def test_layer_norm_refuses_outputs_over_inputs_and_one_another(kw):
+    assert _c(**{**APART, **kw}) == K.KPOOL_EINVAL
+    assert b"overlaps" in K.lib().kpool_last_error()
+
+
+@pytest.mark.parametrize("kw", [
+    *[{out: BWD_APART[n]} for out in ("dw", "db", "ws") for n in ("dy", "x", "w", "mean", "rstd", "dx")],
+    *[dict(dx=BWD_APART[n]) for n in ("w", "mean", "rstd")], dict(dw=BWD_APART["db"]),
+    dict(db=BWD_APART["dw"] + 508), dict(dw=BWD_APART["ws"] + 1020), dict(ws=BWD_APART["db"] - 1008),
+    dict(rows=0, dw=BWD_APART["w"])])
+def test_layer_norm_backward_refuses_outputs_over_inputs_and_one_another(kw):
+    assert _c_bwd(**{**BWD_APART, **kw}) == K.KPOOL_EINVAL
+    assert b"overlaps" in K.lib().kpool_last_error()
+
+
+@pytest.mark.gpu
+def test_statistics_in_the_gaps_of_strided_rows():
+    """What lies between the rows of a strided input is not the input's."""
+    x, w, b, dy = inputs(1, 128, torch.float32, 3)
+    wide = torch.zeros(1, 160, device="cuda")
+    wide[:, :128] = x
+    y, mean, rstd = K.layer_norm(x, w, b, want_stats=True)
+    rc = K.lib().kpool_layer_norm(wide.data_ptr(), 160, w.data_ptr(), b.data_ptr(), 1, 128, 1e-6, K.KPOOL_DTYPE_F32,
+                                  y.data_ptr(), wide.data_ptr() + 4 * 128, wide.data_ptr() + 4 * 159,
+                                  torch.cuda.current_stream().cuda_stream)
+    assert rc == K.KPOOL_OK
+    assert torch.equal(wide[0, 128], mean[0]) and torch.equal(wide[0, 159], rstd[0]) and torch.equal(wide[:, :128], x)
