@@ -850,6 +850,17 @@ size_t attend_workspace(const AttendPlan &p, int64_t rows, int D) {
   return p.nsplit > 1 ? (size_t)p.nsplit * rows * (D + 1) * sizeof(float) : 0;
 }
 
+int64_t attend_threads(const AttendPlan &p, int Hq, int Hkv) {
+  const int64_t units = p.ntiles * p.nsplit * Hkv;
+  if (p.form == AttendPlan::kRows) return units * 256;
+  if (p.form == AttendPlan::kList) {
+    const int64_t n = units * ((Hq / Hkv + 31) / 32);  // (workgroups by eights, one for each XCD)
+    return round_up(p.wave_rows ? round_up(n, 4) / 4 : n, 8) * 256;
+  }
+  const int64_t join = p.nsplit > 1 ? p.ntiles * Hkv * 8 * 256 : 0;
+  return std::max(units * kTileWaves * 64, join);
+}
+
 AttendPlan plan_attend(const int32_t *cu_q, const int32_t *cu_k, int nseq, int Hq, int Hkv) {
   const int64_t G = Hq / Hkv;
   int64_t most_rows = 0, most_keys = 0;

@@ -628,6 +628,11 @@ size_t attend_bwd_workspace(const BwdPlan &p, int64_t Tq, int64_t Tk, int Hq, in
   return (size_t)(stat + (kpart > qpart ? kpart : qpart));
 }
 
+int64_t attend_bwd_threads(const BwdPlan &p, int Hkv) {
+  const int64_t sum = p.qsplit > 1 ? p.qtiles * Hkv * 8 * 256 : 0;
+  return std::max({p.ktiles * Hkv * 512, p.qtiles * p.qsplit * Hkv * kBwdWaves * 64, sum});
+}
+
 hipError_t launch_attend_bwd(const AttendCall &c, const uint16_t *d_o, const BwdPlan &p, void *workspace,
                              uint16_t *dq, uint16_t *dk, uint16_t *dv, hipStream_t st) {
   BwdArgs a{};

@@ -120,6 +120,7 @@ struct AttendPlan {
 AttendPlan plan_attend(const int32_t *cu_q, const int32_t *cu_k, int nseq, int Hq, int Hkv);
 AttendPlan plan_list(int64_t Tq, int nseq, int width, int Hq, int Hkv);
 size_t attend_workspace(const AttendPlan &p, int64_t rows, int D);
+int64_t attend_threads(const AttendPlan &p, int Hq, int Hkv);  // of its largest launch, or more
 hipError_t launch_attend(const AttendCall &c, const AttendPlan &p, void *workspace, hipStream_t st);
 hipError_t launch_attend_list(const AttendCall &c, const AttendPlan &p, const int32_t *ids, int width,
                               void *workspace, hipStream_t st);
@@ -133,6 +134,7 @@ struct BwdPlan {
 };
 BwdPlan plan_attend_bwd(const int32_t *cu_q, const int32_t *cu_k, int nseq, int Hq, int Hkv);
 size_t attend_bwd_workspace(const BwdPlan &p, int64_t Tq, int64_t Tk, int Hq, int Hkv, int D);
+int64_t attend_bwd_threads(const BwdPlan &p, int Hkv);  // of its largest launch, or more
 hipError_t launch_attend_bwd(const AttendCall &c, const uint16_t *d_o, const BwdPlan &p, void *workspace,
                              uint16_t *dq, uint16_t *dk, uint16_t *dv, hipStream_t st);
 

@@ -63,6 +63,9 @@ int check_norm(const char *fn, int64_t rows, int32_t N, int64_t x_stride, int32_
   return KPOOL_OK;
 }
 
+// A launch's threads are counted in 32 bits.
+constexpr int64_t kLaunchThreads = int64_t(1) << 32;
+
 // Arguments that the attention entry points share.
 int check_heads(const char *fn, int32_t Hq, int32_t Hkv, int32_t D) {
   if (Hq < 1 || Hkv < 1 || Hq % Hkv)
@@ -114,11 +117,10 @@ Operand cu_q_of(const kpool::AttendCall &c) { return {"cu_q", c.cu_q, ((int64_t)
 Operand cu_k_of(const kpool::AttendCall &c) { return {"cu_k", c.cu_k, ((int64_t)c.nseq + 1) * 4}; }
 
 // The forward calls' plan, workspace and outputs; ids: the lists, if there are any.
-int check_attend_plan(const char *fn, const kpool::AttendCall &c, const kpool::AttendPlan &p, int64_t per,
-                      const void *workspace, size_t workspace_bytes, const Operand &ids) {
-  // a launch's threads stay below 2^32: workgroups of 512 for tiles, of 256 else
-  if (p.ntiles * per * p.nsplit * c.Hkv >= (int64_t(1) << (p.form == kpool::AttendPlan::kTiles ? 23 : 24)) - 8)
-    return fail(KPOOL_EUNSUPPORTED, "%s: too many query rows for one launch", fn);
+int check_attend_plan(const char *fn, const kpool::AttendCall &c, const kpool::AttendPlan &p, const void *workspace,
+                      size_t workspace_bytes, const Operand &ids) {
+  if (kpool::attend_threads(p, c.Hq, c.Hkv) >= kLaunchThreads)
+    return fail(KPOOL_EUNSUPPORTED, "%s: too many query rows or sequences for one launch", fn);
   const size_t need = kpool::attend_workspace(p, c.Tq * c.Hq, c.D);
   if (need && (!workspace || workspace_bytes < need))
     return fail(KPOOL_EWORKSPACE, "%s: needs %zu bytes of workspace, got %zu", fn, need,
@@ -154,7 +156,7 @@ int kpool_attend(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t
   int rc = check_attend(fn, c, cu_q_host, cu_k_host);
   if (rc || c.Tq == 0) return rc;
   const kpool::AttendPlan p = kpool::plan_attend(cu_q_host, cu_k_host, nseq, Hq, Hkv);
-  rc = check_attend_plan(fn, c, p, 1, workspace, workspace_bytes, {});
+  rc = check_attend_plan(fn, c, p, workspace, workspace_bytes, {});
   if (rc) return rc;
   hipStream_t st = (hipStream_t)stream;
   hipError_t e = timed_layer(kAttend, st, [&] { return kpool::launch_attend(c, p, workspace, st); });
@@ -190,9 +192,8 @@ int kpool_attend_backward(const uint16_t *d_o, const uint16_t *q, int64_t q_stri
   if (!aligned16(k) || !aligned16(v) || !aligned16(d_o) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
     return fail(KPOOL_EINVAL, "%s: k, v, d_o, dq, dk and dv must be 16-byte aligned", fn);
   const kpool::BwdPlan p = kpool::plan_attend_bwd(cu_q_host, cu_k_host, nseq, Hq, Hkv);
-  const int64_t most = int64_t(1) << 23;  // (workgroups of 512 threads)
-  if (p.ktiles * Hkv >= most || p.qtiles * p.qsplit * Hkv >= most)
-    return fail(KPOOL_EUNSUPPORTED, "%s: too many rows for one launch", fn);
+  if (kpool::attend_bwd_threads(p, Hkv) >= kLaunchThreads)
+    return fail(KPOOL_EUNSUPPORTED, "%s: too many rows or sequences for one launch", fn);
   const size_t need = kpool::attend_bwd_workspace(p, c.Tq, c.Tk, Hq, Hkv, D);
   if (need && (!workspace || workspace_bytes < need))
     return fail(KPOOL_EWORKSPACE, "%s: needs %zu bytes of workspace, got %zu", fn, need,
@@ -239,8 +240,7 @@ int kpool_attend_selected(const uint16_t *q, int64_t q_stride, const uint16_t *k
   if (width > 0 && !token_ids) return fail(KPOOL_EINVAL, "%s: null pointer", fn);
   if ((uintptr_t)token_ids & 3) return fail(KPOOL_EINVAL, "%s: token_ids is not aligned to its elements", fn);
   const kpool::AttendPlan p = kpool::plan_list(c.Tq, nseq, width, Hq, Hkv);
-  rc = check_attend_plan(fn, c, p, (Hq / Hkv + 31) / 32, workspace, workspace_bytes,
-                         {"token_ids", token_ids, c.Tq * width * 4});
+  rc = check_attend_plan(fn, c, p, workspace, workspace_bytes, {"token_ids", token_ids, c.Tq * width * 4});
   if (rc) return rc;
   hipStream_t st = (hipStream_t)stream;
   hipError_t e = timed_layer(kAttend, st, [&] {

@@ -478,3 +478,48 @@ def test_refuses_outputs_over_lengths(selected, out, name):
     at[out] = at[name]
     assert _call(selected, **at) == K.KPOOL_EINVAL
     assert b"overlaps" in K.lib().kpool_last_error()
+
+
+def _codes(selected, lens_q, lens_k, **kw):
+    """What a call answers whose outputs overlap its inputs: that refusal comes last."""
+    cu = lambda lens: np.concatenate([[0], np.cumsum(lens)])
+    at = dict(q=1 << 40, k=2 << 40, v=3 << 40, ids=4 << 40, ws=5 << 40, o=1 << 40, lse=None, cqd=8 << 40, ckd=9 << 40)
+    return _call(selected, **{**at, "nb": 1 << 60, "cu_q": cu(lens_q), "cu_k": cu(lens_k), "nseq": len(lens_q), **kw})
+
+
+def test_takes_as_many_rows_as_a_launch_holds():
+    """Lists of many rows go four to a workgroup: 524288 rows of 32 key heads are 2^22 workgroups."""
+    kw = dict(Hkv=32, ks=4096, vs=4096, width=64)
+    assert _codes(True, [524288], [524288], Hq=32, qs=4096, **kw) == K.KPOOL_EINVAL
+    assert b"overlaps" in K.lib().kpool_last_error()
+    assert _codes(True, [1 << 21], [1 << 21], Hq=32, qs=4096, **kw) == K.KPOOL_EUNSUPPORTED
+    assert _codes(True, [(1 << 21) - 33], [1 << 21], Hq=32, qs=4096, **kw) == K.KPOOL_EINVAL
+    # (and 65 heads a key head are three units)
+    assert _codes(True, [1 << 20], [1 << 20], Hq=32 * 65, qs=32 * 65 * 128, **kw) == K.KPOOL_EUNSUPPORTED
+
+
+@pytest.mark.parametrize("nseq,code", [(1 << 17, K.KPOOL_EINVAL), (1 << 18, K.KPOOL_EUNSUPPORTED)])
+def test_refuses_more_sequences_than_the_join_of_parts_takes(nseq, code):
+    """Few rows among very many empty sequences: eight workgroups a tile join the parts."""
+    lens_q, lens_k = np.zeros((2, nseq), dtype=np.int64)
+    lens_q[5], lens_k[5] = 64, 1000
+    assert _codes(False, lens_q, lens_k, Hq=8, Hkv=8, qs=1024, ks=1024, vs=1024) == code
+
+
+@pytest.mark.gpu
+def test_selected_rows_of_half_a_million_tokens_and_32_key_heads():
+    """2^24 units of work, four to a workgroup."""
+    T, H, D = 524288, 32, 8
+    cu, dev = cu_of([T])
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q, k, v = (torch.randn(T, H, D, generator=g, device="cuda").to(BF16) for _ in range(3))
+    t = torch.arange(T, device="cuda")
+    ids = (torch.rand(T, 3, generator=g, device="cuda") * (t[:, None] + 1)).to(torch.int32)
+    o, lse = K.attend_selected(q, k, v, ids, cu, dev, want_lse=True)
+    rows = torch.cat([t[:50], t[T - 50:], t[::1021]])
+    # one sequence a row, its keys the three that it lists
+    at = ids[rows].long().flatten()
+    n = len(rows)
+    cu_q, cu_k = np.arange(n + 1), 3 * np.arange(n + 1)
+    three = torch.tensor([[0, 1, 2]], dtype=torch.int32, device="cuda").expand(n, 3)
+    check(q[rows], k[at], v[at], cu_q[:201], cu_k[:201], D ** -0.5, o[rows], lse[rows], three)

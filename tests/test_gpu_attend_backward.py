@@ -215,3 +215,13 @@ def test_keys_without_rows_need_their_pointers(kw):
 def test_refuses_a_workspace_over_operands_and_outputs_over_lengths(kw):
     assert _call(**{**APART, "cqd": 12 << 20, "ckd": 13 << 20, **kw}) == K.KPOOL_EINVAL
     assert b"overlaps" in K.lib().kpool_last_error()
+
+
+@pytest.mark.parametrize("nseq,code", [(1 << 17, K.KPOOL_EINVAL), (1 << 18, K.KPOOL_EUNSUPPORTED)])
+def test_refuses_more_sequences_than_the_sum_of_parts_takes(nseq, code):
+    """Few rows among very many empty sequences: eight workgroups a tile add dQ's parts."""
+    cu_q, cu_k = np.zeros((2, nseq + 1), dtype=np.int32)
+    cu_q[6:], cu_k[6:] = 64, 500
+    at = dict(d_o=1 << 40, q=2 << 40, k=3 << 40, v=4 << 40, o=5 << 40, lse=6 << 40, ws=7 << 40, dq=2 << 40,
+              dk=9 << 40, dv=10 << 40, cqd=11 << 40, ckd=12 << 40)
+    assert _call(**at, cu_q=cu_q, cu_k=cu_k, nseq=nseq, Hq=8, Hkv=8, qs=1024, ks=1024, vs=1024, nb=1 << 60) == code
