@@ -346,6 +346,15 @@ def _like(t, name, shape, dtype, device):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}")
 
 
+def _refuse_graph(fn, *tensors):
+    """Results are plain tensors: where autograd would record the call, its gradients would be lost
+    without a word."""
+    import torch
+    if any(t is not None and t.requires_grad for t in tensors) and torch.is_grad_enabled():
+        raise ValueError(f"{fn} records no autograd graph: call it under torch.no_grad() or from the forward of a "
+                         f"torch.autograd.Function, on detached tensors otherwise")
+
+
 def _heads(t, name, device, codes):
     """t as packed tokens [T, H, D] of bf16 with any token stride: (T, H, D, stride)."""
     if t.dim() != 3 or not t.is_cuda or t.device != device:
@@ -444,7 +453,10 @@ def attend(q, k, v, cu_q, cu_q_dev, cu_k=None, cu_k_dev=None, scale: float | Non
     q bf16 [Tq, Hq, D], k and v bf16 [Tk, Hkv, D] (any token stride; each key head serves
     Hq / Hkv query heads); cu_q, cu_k host arrays of nseq + 1 cumulative lengths and their
     device copies, the keys' being the queries' where they are left out.  A sequence's queries
-    are the last rows of its keys.  scale is 1 / sqrt(D) by default."""
+    are the last rows of its keys.  scale is 1 / sqrt(D) by default.  Autograd does not record the
+    call (tensors that require gradients are refused where it would); attend_backward has its
+    gradients."""
+    _refuse_graph("attend", q, k, v)
     a = _Attend(q, k, v, cu_q, cu_q_dev, cu_k, cu_k_dev, scale)
     with _OnDevice(q, stream) as s:
         out, lse = a.outputs(q, out, lse, want_lse)
@@ -500,8 +512,10 @@ def attend_selected(q, k, v, token_ids, cu_q, cu_q_dev, cu_k=None, cu_k_dev=None
     """Attention of packed query rows over the tokens each selected: (o, lse or None).
 
     token_ids int32 [Tq, width]: sequence-local token ids as expand gives them; entries that
-    are negative or past the row stand for nothing.  The rest is attend's."""
+    are negative or past the row stand for nothing.  The rest is attend's, but for a backward
+    pass, which there is none of."""
     import torch
+    _refuse_graph("attend_selected", q, k, v)
     a = _Attend(q, k, v, cu_q, cu_q_dev, cu_k, cu_k_dev, scale)
     if token_ids.dim() != 2:
         raise ValueError("token_ids must be [Tq, width]")
@@ -540,8 +554,10 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, want_stat
                stream=None):
     """Layer norm of the rows of x [rows, N] (bf16 or fp32, any row stride), with fp32 weight
     and bias [N] (None: ones, zeros).  Returns (y, mean, rstd); mean and rstd, fp32 [rows],
-    are what layer_norm_backward reads, and None unless want_stats."""
+    are what layer_norm_backward reads, and None unless want_stats.  Autograd does not record the
+    call (tensors that require gradients are refused where it would)."""
     import torch
+    _refuse_graph("layer_norm", x, weight, bias)
     rows, N, stride, code = _norm_rows(x, "x")
     device = x.device
     if weight is not None:
@@ -693,6 +709,7 @@ class Selector:
         pooled by the gated compression, otherwise by the mean.  With k_norm = (weight, bias,
         eps), k is the key projection's output and passes that layer norm first (its rows may
         then be a slice of a wider projection)."""
+        import torch
         overlap = self.overlap if overlap is None else overlap
         if k_norm is not None:
             weight, bias, eps = k_norm
@@ -702,7 +719,8 @@ class Selector:
                 with _on(stream):
                     self.k_normed = k.new_empty((self.T, self.D))
             g = None if g is None else g[:self.T]
-            k = layer_norm(k[:self.T], weight, bias, eps, out=self.k_normed.view(k.dtype), stream=stream)[0]
+            with torch.no_grad():  # (ids have no gradients)
+                k = layer_norm(k[:self.T], weight, bias, eps, out=self.k_normed.view(k.dtype), stream=stream)[0]
         if g is not None:
             pool_keys_gated(k, g, ape, self.cu, self.cu_dev, self.cu_pools_dev, self.kpool,
                             out=self.kp, stream=stream, tail=self.tail)

@@ -206,3 +206,53 @@ def test_profiles_of_the_layer_and_of_the_selection_are_apart():
     ms, n = collect("kpool_layer_profile_collect")
     assert n == [10, 10] + [7] * 14 and all(t > 7.0 for t in ms[:2]) and ms[2:] == [7.0] * 14
     assert set(x[1] for x in K.profile_collect().values()) == {0}
+
+
+@pytest.mark.parametrize("which", range(3))
+def test_refuses_to_lose_gradients(which):
+    """Autograd records none of the calls: with tensors that require gradients they raise, on any
+    device, before anything else."""
+    x = [torch.zeros(2, 1, 8), torch.zeros(2, 1, 8), torch.zeros(2, 1, 8)]
+    x[which].requires_grad_()
+    cu, cud = np.array([0, 2]), torch.zeros(2, dtype=torch.int32)
+    rows = [torch.zeros(2, 8), torch.zeros(8), torch.zeros(8)]
+    rows[which].requires_grad_()
+    for call in (lambda: K.attend(*x, cu, cud), lambda: K.layer_norm(*rows),
+                 lambda: K.attend_selected(*x, torch.zeros(2, 1, dtype=torch.int32), cu, cud)):
+        with pytest.raises(ValueError, match="autograd"):
+            call()
+
+
+@pytest.mark.gpu
+def test_parameters_without_autograd():
+    """The same tensors under no_grad, and in the forward of an autograd function whose backward is
+    attend_backward; the selection's key norm, whose ids have no gradients, takes parameters anywhere."""
+    from attend_reference import cu_of
+    cu, dev = cu_of([70, 5])
+    q, k, v = (t[:75].clone() for t in make(cu, cu, 4, 2, 64, 19))
+    ref, lse = K.attend(q, k, v, cu, dev, want_lse=True)
+    d_o = torch.randn(75, 4, 64, generator=torch.Generator().manual_seed(1)).to(BF16).cuda()
+    grads = K.attend_backward(d_o, q, k, v, ref, lse, cu, dev)
+
+    class Attend(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, v):
+            o, lse = K.attend(q, k, v, cu, dev, want_lse=True)
+            ctx.save_for_backward(q, k, v, o, lse)
+            return o
+
+        @staticmethod
+        def backward(ctx, d_o):
+            return K.attend_backward(d_o.contiguous(), *ctx.saved_tensors, cu, dev)
+
+    x = [t.clone().requires_grad_() for t in (q, k, v)]
+    with torch.no_grad():
+        assert torch.equal(K.attend(*x, cu, dev)[0], ref)
+    o = Attend.apply(*x)
+    o.backward(d_o)
+    assert torch.equal(o, ref) and all(torch.equal(t.grad, g) for t, g in zip(x, grads))
+    sel, _, dev_in, norm, out, _, _, _ = layer([0, 100, 333], 4, 32, 11)
+    ids = out["token_ids"].clone()
+    params = tuple(torch.nn.Parameter(t) for t in norm[:2]) + norm[2:]
+    got = sel.run(dev_in["q"], dev_in["k"], dev_in["w"], k_norm=params)
+    assert torch.equal(got["token_ids"], ids) and not got["kp"].requires_grad
