@@ -837,8 +837,10 @@ AttendArgs make_args(const AttendCall &c, const AttendPlan &p, void *workspace) 
   a.nsplit = p.nsplit, a.chunk = p.chunk;
   a.o = c.o, a.lse = c.lse;
   a.rows = c.Tq * c.Hq;
-  a.part_o = (float *)workspace;
-  a.part_lse = a.part_o + (int64_t)p.nsplit * a.rows * c.D;
+  if (p.nsplit > 1) {
+    a.part_o = (float *)workspace;
+    a.part_lse = a.part_o + (int64_t)p.nsplit * a.rows * c.D;
+  }
   return a;
 }
 
