@@ -559,13 +559,14 @@ constexpr int64_t kNormLaunchRows = int64_t(1) << 22;
 // 50; backward 65 115 196, 501 90 124, 1237 99 189, 2047 89 119, 4098 174 137; in bf16 vectors
 // always win: forward 65 120 35, 1237 57 35, 8191 70 31).
 constexpr int kSingle = 256, kSingleBwd = 2048;
+static_assert(kSingle <= 256 && kSingleBwd <= 2048, "what the kernels of single elements take");
 
 // (the pitch counts only where there is a second row)
 template <class T>
-bool aligned_rows(const void *x, int64_t x_stride, int N, const void *w, const void *b, const void *y,
-               const void *dy) {
+bool aligned_rows(const void *x, int64_t x_stride, int64_t rows, int N, const void *w, const void *b,
+                  const void *y, const void *dy) {
   const uintptr_t bits = (uintptr_t)x | (uintptr_t)w | (uintptr_t)b | (uintptr_t)y | (uintptr_t)dy;
-  return bits % 16 == 0 && N % kVec<T> == 0 && (x_stride * sizeof(T)) % 16 == 0;
+  return bits % 16 == 0 && N % kVec<T> == 0 && (rows <= 1 || (x_stride * sizeof(T)) % 16 == 0);
 }
 
 template <class T, int VEC, bool ALIGNED, int TPR, int R, int ROWS>
@@ -587,14 +588,16 @@ void norm_pick(const void *x, int64_t xs, const float *w, const float *b, int64_
   }
   else if (nv <= 64) KPOOL_NORM(64, 1, 1);
   else if (nv <= 128) KPOOL_NORM(64, 2, 1);
-  else if (nv <= 256) KPOOL_NORM(64, 4, 1);
-  else if (nv <= 512) KPOOL_NORM(256, 2, 1);
-  else if (nv <= 768) KPOOL_NORM(256, 3, 1);
-  else if (nv <= 1024) KPOOL_NORM(256, 4, 1);
-  else if (nv <= 2048) KPOOL_NORM(512, 4, 1);
-  else if constexpr (VEC > 1)
-    hipLaunchKernelGGL((norm_long_kernel<T, ALIGNED>), dim3((unsigned)rows), dim3(kNormThreads), 0, st,
-                       (const T *)x, xs, w, b, N, 1.0 / N, eps, (T *)y, mean, rstd);
+  else if (VEC == 1 || nv <= 256) KPOOL_NORM(64, 4, 1);  // (single elements: up to kSingle of them)
+  else if constexpr (VEC > 1) {
+    if (nv <= 512) KPOOL_NORM(256, 2, 1);
+    else if (nv <= 768) KPOOL_NORM(256, 3, 1);
+    else if (nv <= 1024) KPOOL_NORM(256, 4, 1);
+    else if (nv <= 2048) KPOOL_NORM(512, 4, 1);
+    else
+      hipLaunchKernelGGL((norm_long_kernel<T, ALIGNED>), dim3((unsigned)rows), dim3(kNormThreads), 0, st,
+                         (const T *)x, xs, w, b, N, 1.0 / N, eps, (T *)y, mean, rstd);
+  }
 #undef KPOOL_NORM
 }
 
@@ -642,8 +645,8 @@ hipError_t launch_norm(bool f32, const void *x, int64_t x_stride, const float *w
                        int64_t rows, int32_t N, float eps, void *y, float *mean, float *rstd,
                        hipStream_t st) {
   const int64_t size = f32 ? 4 : 2;
-  const bool vec = f32 ? aligned_rows<float>(x, x_stride, N, w, b, y, nullptr)
-                       : aligned_rows<uint16_t>(x, x_stride, N, w, b, y, nullptr);
+  const bool vec = f32 ? aligned_rows<float>(x, x_stride, rows, N, w, b, y, nullptr)
+                       : aligned_rows<uint16_t>(x, x_stride, rows, N, w, b, y, nullptr);
   for (int64_t r = 0; r < rows; r += kNormLaunchRows) {
     const int64_t n = rows - r < kNormLaunchRows ? rows - r : kNormLaunchRows;
     const char *xr = (const char *)x + r * x_stride * size;
@@ -661,8 +664,8 @@ hipError_t launch_norm(bool f32, const void *x, int64_t x_stride, const float *w
 }
 
 // Row runs of the backward pass, by the sizes alone: at most 1024 workgroups, runs of 8 rows
-// or more, and partial sums of at most 8 MiB, unless that leaves fewer than 128 workgroups
-// (8192 x 4096 in bf16: 256 workgroups 80 us a step, 512 the same, 1024 95 us).
+// or more, and partial sums of at most 8 MiB, unless that leaves fewer than 256 workgroups, one a
+// CU (8192 x 4096 in bf16: 256 workgroups 80 us a step, 512 the same, 1024 95 us).
 int norm_bwd_blocks(int64_t rows, int32_t N) {
   int64_t most = (int64_t(1) << 20) / N;
   if (most > 1024) most = 1024;
@@ -677,8 +680,8 @@ hipError_t launch_norm_bwd(bool f32, const void *dy, const void *x, int64_t x_st
   const int nblk = norm_bwd_blocks(rows, N);
   const int64_t rows_per = (rows + nblk - 1) / nblk;
   if (!dw && !db) part = nullptr;
-  const bool vec = f32 ? aligned_rows<float>(x, x_stride, N, w, nullptr, dx, dy)
-                       : aligned_rows<uint16_t>(x, x_stride, N, w, nullptr, dx, dy);
+  const bool vec = f32 ? aligned_rows<float>(x, x_stride, rows, N, w, nullptr, dx, dy)
+                       : aligned_rows<uint16_t>(x, x_stride, rows, N, w, nullptr, dx, dy);
 #define KPOOL_NORM(T, VEC, ALIGNED) \
   norm_bwd_pick<T, VEC, ALIGNED>(dy, x, x_stride, w, mean, rstd, rows, N, dx, part, nblk, rows_per, st)
   if (f32 && vec) KPOOL_NORM(float, 4, true);

@@ -394,3 +394,19 @@ def test_statistics_in_the_gaps_of_strided_rows():
                                   torch.cuda.current_stream().cuda_stream)
     assert rc == K.KPOOL_OK
     assert torch.equal(wide[0, 128], mean[0]) and torch.equal(wide[0, 159], rstd[0]) and torch.equal(wide[:, :128], x)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,code", [(torch.bfloat16, 0), (torch.float32, 1)])
+def test_one_row_has_no_pitch(dtype, code):
+    """Any row pitch of a single row gives the bits of the contiguous one."""
+    x, w, b, dy = inputs(1, 1240, dtype, 4)
+    y, mean, rstd = K.layer_norm(x, w, b, 1e-6, want_stats=True)
+    dx, _, _ = K.layer_norm_backward(dy, x, w, mean, rstd)
+    s = torch.cuda.current_stream().cuda_stream
+    y2, dx2, p = torch.empty_like(y), torch.empty_like(dx), lambda t: t.data_ptr()
+    for pitch in (1241, 1243, 5000):
+        assert K.lib().kpool_layer_norm(p(x), pitch, p(w), p(b), 1, 1240, 1e-6, code, p(y2), None, None, s) == 0
+        assert K.lib().kpool_layer_norm_backward(p(dy), p(x), pitch, p(w), p(mean), p(rstd), 1, 1240, code, None, 0,
+                                                 p(dx2), None, None, s) == 0
+        assert torch.equal(y, y2) and torch.equal(dx, dx2)
