@@ -180,7 +180,7 @@ def probe_peaks(reps: int = 10):
                     f"torch.matmul bf16 [{n},{n}] x [{n},{n}]; HIP events")}
 
 
-COUNTER_SOURCES = ("score.hip", "topk.hip", "api.hip")
+COUNTER_SOURCES = ("score.hip", "topk.hip", "api.hip", "kpool_internal.h")
 
 
 def committed_counters(workload: str):
@@ -189,9 +189,9 @@ def committed_counters(workload: str):
     The summary holds, per kernel, the FETCH_SIZE / WRITE_SIZE bytes per launch
     (scaled by a plain-copy calibration) and the score kernel's MFMA-busy share,
     from rocprofv3 --pmc runs of this script, together with the sha256 of the
-    sources they were measured on (score.hip, topk.hip and api.hip, which plans
-    the launches; the score kernel's cache policy also decides what the top-k
-    finds in the caches).  Any changed source makes the figures stale: None.
+    sources they were measured on (score.hip, topk.hip, their kpool_internal.h and
+    api.hip, which plans the launches; the score kernel's cache policy also decides
+    what the top-k finds in the caches).  Any changed source makes the figures stale: None.
     """
     import hashlib
     prof = os.path.join(ROOT, "profiles", f"counters_{workload}.md")

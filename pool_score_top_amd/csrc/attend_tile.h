@@ -23,7 +23,7 @@
 
 #include <algorithm>
 
-#include "kpool_internal.h"
+#include "layer_internal.h"
 
 namespace kpool {
 

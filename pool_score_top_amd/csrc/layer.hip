@@ -6,6 +6,7 @@
 #include <initializer_list>
 
 #include "api.hip"
+#include "layer_internal.h"
 
 namespace {
 

@@ -33,7 +33,7 @@
 // result does not change from run to run; the split depends on the sizes alone.
 #include <type_traits>
 
-#include "kpool_internal.h"
+#include "layer_internal.h"
 
 // (an element that two threads hold comes out the same in both: fused operations are written out)
 #pragma clang fp contract(off)
