@@ -100,6 +100,8 @@ int check_attend(const char *fn, kpool::AttendCall &c, const int32_t *cu_q_host,
     if (x.stride < x.least || x.stride % 8 || x.stride > (1 << 24))
       return fail(KPOOL_EINVAL, "%s: a token stride must be a multiple of 8 in [%lld, 2^24] (got %lld)", fn,
                   (long long)x.least, (long long)x.stride);
+  if (((uintptr_t)c.cu_q | (uintptr_t)c.cu_k) & 3)
+    return fail(KPOOL_EINVAL, "%s: cu_q or cu_k is not aligned to its elements", fn);
   c.Tq = cu_q_host[c.nseq];
   c.Tk = cu_k_host[c.nseq];
   if (c.Tq == 0) return ok();

@@ -523,3 +523,11 @@ def test_selected_rows_of_half_a_million_tokens_and_32_key_heads():
     cu_q, cu_k = np.arange(n + 1), 3 * np.arange(n + 1)
     three = torch.tensor([[0, 1, 2]], dtype=torch.int32, device="cuda").expand(n, 3)
     check(q[rows], k[at], v[at], cu_q[:201], cu_k[:201], D ** -0.5, o[rows], lse[rows], three)
+
+
+@pytest.mark.parametrize("selected", [False, True])
+@pytest.mark.parametrize("name", ["cqd", "ckd"])
+def test_refuses_lengths_off_their_elements(selected, name):
+    """Scalar loads would read the word below."""
+    assert _call(selected, **{**APART, "cqd": 8 << 20, "ckd": 9 << 20, name: (9 << 20) + 2}) == K.KPOOL_EINVAL
+    assert b"aligned" in K.lib().kpool_last_error()

@@ -225,3 +225,9 @@ def test_refuses_more_sequences_than_the_sum_of_parts_takes(nseq, code):
     at = dict(d_o=1 << 40, q=2 << 40, k=3 << 40, v=4 << 40, o=5 << 40, lse=6 << 40, ws=7 << 40, dq=2 << 40,
               dk=9 << 40, dv=10 << 40, cqd=11 << 40, ckd=12 << 40)
     assert _call(**at, cu_q=cu_q, cu_k=cu_k, nseq=nseq, Hq=8, Hkv=8, qs=1024, ks=1024, vs=1024, nb=1 << 60) == code
+
+
+@pytest.mark.parametrize("name", ["cqd", "ckd"])
+def test_refuses_lengths_off_their_elements(name):
+    assert _call(**{**APART, "cqd": 12 << 20, "ckd": 13 << 20, name: (13 << 20) + 1}) == K.KPOOL_EINVAL
+    assert b"aligned" in K.lib().kpool_last_error()
