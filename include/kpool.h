@@ -251,7 +251,9 @@ int kpool_topk(const float *scores, int64_t ld, const int32_t *n_valid, int64_t 
  *            queries and Lk keys, query n sits at position t = Lk - Lq + n.  A whole prompt
  *            has cu_q = cu_k; a chunk of a prompt, or one new token a sequence, fewer
  *            queries than keys.  Any lengths, 0 included; Lq > Lk leaves the first rows
- *            without keys.  Host and device copies hold the same values.
+ *            without keys.  Host and device copies hold the same values.  The launch is planned
+ *            from the host's, so a captured call replays with the lengths it was captured with:
+ *            new lengths (a decoding step) take a new call or a new capture.
  *   o        bf16 [Tq, Hq, D] contiguous, Tq = cu_q[nseq]; rows past Tq are not touched
  *   lse      NULLABLE fp32 [Tq, Hq]
  * A row that sees nothing gets o = 0 and lse = -inf.  Sums and statistics are fp32; the
@@ -261,7 +263,8 @@ int kpool_topk(const float *scores, int64_t ld, const int32_t *n_valid, int64_t 
  * Sizes: D a multiple of 8 up to 128; Hq a multiple of Hkv; strides multiples of 8 from
  * H * D to 2^24; q, k, v, o and the workspace 16-byte aligned.
  *   workspace  kpool_attend_workspace_bytes(the same sizes) bytes (may be 0: then it is
- *            not read): the parts of the key axis where there are few query rows; scratch. */
+ *            not read): the parts of the key axis where there are few query rows, as many for
+ *            every row as the longest sequence has; scratch. */
 size_t kpool_attend_workspace_bytes(const int32_t *cu_q_host, const int32_t *cu_k_host, int32_t nseq,
                                     int32_t Hq, int32_t Hkv, int32_t D);
 int kpool_attend(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,

@@ -306,9 +306,14 @@ __device__ inline void write_row(const AttendArgs &a, bool live, int64_t row, bo
 
 // Many rows: NW waves of 32 virtual rows each share key tiles of 64.  8 waves and 64 KiB of
 // tiles: one workgroup a CU, two waves a SIMD, so that one's softmax runs beside the other's
-// matrix instructions.  Bound by the matrix pipe: a prompt of 16384 tokens, 16 heads over 2 of
-// 128, 1.1 TFLOP, takes 983 us (1.12 PFLOP/s; a 16384 library product reaches 1.3); with the
-// softmax and the LDS reads left out it still takes 915 us.
+// matrix instructions.  A prompt of 16384 tokens, 16 heads over 2 of 128, 1.1 TFLOP, takes 983 to
+// 1035 us (1.06 to 1.12 PFLOP/s; a 16384 library product reaches 1.3): bound by the matrix
+// instructions at the clock that the card's power leaves, since with the softmax and the LDS reads
+// left out it still takes 915 us (CUs busy 91% of the time, the pipe 58% of that).  A packed batch
+// of 4097 to 1 tokens, 32 heads over 4: CUs 84%, the pipe 49%: shorter tiles, so a larger share goes
+// to their starts and ends, beside which a CU has nothing else to run.
+// Head dims above 64 run as 128: the blocks past D multiply zeros (8192 tokens, 16 heads over 2: D
+// = 64 192 us, 80 258, 96 263, 128 272).
 template <int DP, int NW>
 __global__ __launch_bounds__(NW * 64) void attend_tile_kernel(AttendArgs a) {
   using S = Keys<DP>;
@@ -520,7 +525,7 @@ __global__ __launch_bounds__(256) void attend_rows_kernel(AttendArgs a) {
 //   pass a sixteenth of the sequence together and share more of it than 64 rows that each go
 //   by four times as fast, and no waves have to join.
 //   ROWS = 16 for up to 16 heads a key head: half the matrix and vector work of 32.
-// 2048 rows of 2048 of 65536 tokens, 32 heads over 2: 273 us, 65% of the keys from the L2 (WR = 4:
+// 2048 rows of 2048 of 65536 tokens, 32 heads over 2: 274 us, 65% of the keys from the L2 (WR = 4:
 // 396 us; lists in their own order: 549 us, 12%).  Bound by the loads into the LDS: with all
 // keys in the L2 it takes 219 us, and without any of the products and the softmax 212.
 // The last tile of a block may be short: its absent entries read the tile's first key, so that
@@ -885,6 +890,11 @@ AttendPlan plan_attend(const int32_t *cu_q, const int32_t *cu_k, int nseq, int H
     walked += (lq * G + BQ - 1) / BQ * lk * Hkv;
   }
   p.nsplit = 1, p.chunk = 0x7FFFFF00;
+  // From 256 workgroups on, one a CU, no parts: right for sequences of like lengths (requests of
+  // 8192 keys, 32 heads over 4: 63 of them, 252 workgroups, 233 us with parts, 64 270 without).
+  // It does not look at the lengths: where one sequence is far longer than the others, one
+  // workgroup a key head walks all of it (one request of 60000 keys, the others of 500: 63 of them
+  // 244 us, 64 439 us).
   if (wgs >= 256) return p;
   const int64_t least = p.form == AttendPlan::kRows ? 1024 : 512;
   const int64_t chunk = round_up(walked / 512 > least ? walked / 512 : least, 256);

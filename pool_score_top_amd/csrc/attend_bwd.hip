@@ -86,7 +86,8 @@ __device__ inline void load_frag(bf16x8 (&f)[DP / 16], const uint16_t *row, int 
 // every LDS address is a register computed once plus a constant.
 // Work goes by equal shares: the first key's rows are all the rows, the last one's few, and with
 // parts of at most the CUs' average the CUs had work 66% of the time (the same tokens as at dQ's
-// kernel: 330 us; by shares 257 and 13 to join, 210 GFLOP at 0.82 PFLOP/s).
+// kernel: 330 us; by shares 254 and 13 to join, 210 GFLOP at 0.83 PFLOP/s; CUs busy 85% of the
+// time, the matrix pipe 45% of that).
 template <int DP>
 struct BwdKeys {
   static constexpr int BR = 32, NG = 4, KEYS = NG * 32;
@@ -353,6 +354,7 @@ __global__ __launch_bounds__(256) void bwd_keys_sum_kernel(BwdArgs a, Shares sha
 // Rows that see few keys have the largest gradients, and their roundings show in the whole's.
 // Tiles whose rows see no more than kFewKeys take delta from the keys instead of from o; up to
 // kFineKeys dS is held in two bf16 numbers for dQ (a fourth product, of operands that are there).
+// (Both limits were set at the shape below; others differ with their lengths and head counts.)
 // The errors against 64 bits, in units of what rounding the exact gradient to bf16 gives (one
 // rounding of dS beside it gives 1.41), for 2048 tokens, 8 heads over 1 of 64, and the time of a
 // step there and of 8192 packed tokens with 16 heads over 4 of 128:
@@ -365,9 +367,11 @@ __global__ __launch_bounds__(256) void bwd_keys_sum_kernel(BwdArgs a, Shares sha
 constexpr int kFewKeys = 512, kFineKeys = 1024;
 
 // dQ: NW waves of 32 virtual rows; key tiles of 64 pass through LDS, as in the forward pass.
-// 8192 packed tokens (4096, 2777, 1000, 319), 16 heads over 4 of 128: 157 GFLOP in 200 us, 0.79
-// PFLOP/s; bound by the matrix pipe (cutting the longest tiles to the CUs' average leaves the
-// time as it is).
+// 8192 packed tokens (4096, 2777, 1000, 319), 16 heads over 4 of 128: 157 GFLOP in 193 us, 0.81
+// PFLOP/s.  CUs are busy 75% of the time, the matrix pipe 54% of that: within a wave a half tile's
+// exponentials wait for its products and the next half's products for them (the scheduling
+// barriers keep the phases apart), and all waves wait for a whole tile's loads together.  Cutting
+// the longest tiles to the CUs' average leaves the time as it is.
 template <int DP, int NW>
 __global__ __launch_bounds__(NW * 64) void bwd_rows_kernel(BwdArgs a) {
   using S = Keys<DP>;

@@ -23,9 +23,11 @@
 //   TPR 256 and 512 up to 2048 vectors (backward in bf16 1536): a workgroup per row.
 //   Longer rows are read again for each pass (the second and third reads hit the caches).
 // Measured (the card copies at 4.75 TB/s, reads and writes counted): 524288 x 128 in bf16,
-// forward, 47 us (5.7 TB/s); 8192 x 4096 in bf16, forward 24 us (5.6 TB/s), backward 45 us (4.5
-// TB/s) and 4 us to join the sums; 5003 x 1237 in fp32 at a pitch of 1328, forward 12.5 us (4.0
-// TB/s), backward 16 us (4.6 TB/s).
+// forward, 46 us (5.8 TB/s); 8192 x 4096 in bf16, forward 25 us (5.4 TB/s), backward 44 us (4.6
+// TB/s) and 4 us to join the sums; 5003 x 1237 in fp32 at a pitch of 1328, forward 13.7 us (3.6
+// TB/s), backward 16.5 us (4.5 TB/s) and 6 to join, which is latency, not bytes.  Long rows in bf16:
+// 4096 x 16384 (forward in registers) 55 us, backward, which reads x and dy three times, once of
+// them by single elements, 199 us; 3277 x 20480 forward 76, backward 204.
 //
 // The weight's gradient sums over rows in a fixed order: every workgroup takes a
 // contiguous run of rows and keeps its columns' sums in registers, the workgroups'
