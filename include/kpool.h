@@ -316,7 +316,8 @@ int kpool_attend_selected(const uint16_t *q, int64_t q_stride, const uint16_t *k
  * plan's tensors).  For row r and column j < N:
  *   mean = sum_j x[r,j] / N,   rstd = 1 / sqrt(sum_j (x[r,j] - mean)^2 / N + eps)
  *   y[r,j] = (x[r,j] - mean) * rstd * weight[j] + bias[j]
- * in fp32, rounded once to the output's type.
+ * the mean in 64 bits, the rest in fp32, rounded once to the output's type (a constant row's
+ * x - mean is 0 exactly; the mean that is returned is rounded to fp32).
  *   dtype    of x, y, dy and dx: KPOOL_DTYPE_BF16 or KPOOL_DTYPE_F32
  *   x        [rows, N], row r at x + r * x_stride elements (x_stride >= N): a slice of a
  *            wider projection needs no copy
