@@ -352,6 +352,31 @@ int kpool_layer_norm_backward(const void *dy, const void *x, int64_t x_stride, c
                               int32_t dtype, void *workspace, size_t workspace_bytes, void *dx,
                               float *dweight, float *dbias, void *stream);
 
+/* Rotary positions of rows of heads - what the indexer's and the attention's queries and keys
+ * pass before they meet (Atlas inference docs, glm5next_dsa/tp.rs: the shard plan's q_b_proj and
+ * kv_a_proj_with_mqa carry the positional part).  With theta = positions[r] * freqs[j], pair j of
+ * each head of row r becomes
+ *   (a, b) -> factor * (a cos(theta) - b sin(theta), a sin(theta) + b cos(theta))
+ * and the head's other values are copied.
+ *   pairs    1 .. (D - begin) / 2.  Without KPOOL_ROTARY_INTERLEAVED pair j is the elements
+ *            begin + j and begin + pairs + j of a head, with it begin + 2 j and begin + 2 j + 1
+ *   KPOOL_ROTARY_INVERSE  turns by -theta: the backward pass (dx from dy; freqs, positions and factor
+ *            as in the forward call)
+ *   x        [rows, heads, D], row r at x + r * x_stride elements, its heads contiguous
+ *   positions  int32 [rows] device, any value;  freqs  fp64 [pairs] device, radians a token, finite:
+ *            scaled for long contexts as the model has it;  factor finite (1, or the scaling's)
+ *   dtype    of x and y
+ *   y        like x at its own stride; or x itself (the same pointer and stride): in place.  Rows of
+ *            x and y may share a wider row side by side; they do not overlap otherwise, nor does y
+ *            overlap positions or freqs.
+ * Angles are 64-bit turns, sines and cosines fp32, as the products; one rounding to the output's type.
+ * D up to 1024.  rows 0 is a no-op.  Any alignment of whole elements; 16-byte bounds are the fastest. */
+#define KPOOL_ROTARY_INTERLEAVED 1u
+#define KPOOL_ROTARY_INVERSE 2u
+int kpool_rotary(const void *x, int64_t x_stride, const int32_t *positions, const double *freqs,
+                 int64_t rows, int32_t heads, int32_t D, int32_t begin, int32_t pairs, float factor,
+                 int32_t dtype, uint32_t flags, void *y, int64_t y_stride, void *stream);
+
 /* Optional per-kernel device timing, per host thread.  While enabled on a
  * thread, every launch that thread's calls make is bracketed by HIP events on
  * its stream.  kpool_profile_collect waits for the events the calling thread
@@ -366,7 +391,7 @@ int kpool_profile_collect(double *ms, int64_t *launches);
 /* The same for the calls around the selection (a call's launches as one), which
  * kpool_profile_collect neither reports nor forgets: arrays of
  * KPOOL_LAYER_PROFILE_KINDS. */
-#define KPOOL_LAYER_PROFILE_KINDS 2 /* 0 layer norm, 1 attention */
+#define KPOOL_LAYER_PROFILE_KINDS 2 /* 0 layer norm and rotary positions, 1 attention */
 int kpool_layer_profile_collect(double *ms, int64_t *launches);
 
 #ifdef __cplusplus

@@ -1,5 +1,5 @@
 // C ABI of libkpool, the layer around the selection: argument validation and launches of the layer
-// norm and the attention.
+// norm, the rotary positions and the attention.
 //
 // One translation unit with api.hip, whose error text, checks and profile records these entry
 // points share and which keep to that file.
@@ -42,6 +42,18 @@ bool meets(const Operand &out, const Operand &in) {
   // the first row that ends behind `out`'s start, if that one starts before its end
   const int64_t r = from < in.len ? 0 : (from - in.len) / in.pitch + 1;
   return r < in.rows && r * in.pitch < from + out.len;
+}
+
+// Whether rows of two operands meet: exactly where they are as far apart in both, by their extents
+// otherwise (which may refuse what only interleaves).
+bool rows_meet(const Operand &a, const Operand &b) {
+  if (a.rows <= 1) return meets({a.name, a.p, a.len}, b);
+  if (b.rows <= 1) return meets({b.name, b.p, b.len}, a);
+  const int64_t from = (int64_t)((uintptr_t)b.p - (uintptr_t)a.p);
+  if (from >= (a.rows - 1) * a.pitch + a.len || -from >= (b.rows - 1) * b.pitch + b.len) return false;
+  if (a.pitch != b.pitch) return true;
+  const int64_t apart = ((from % a.pitch) + a.pitch) % a.pitch;  // b's row behind the start of a's
+  return apart < a.len || apart + b.len > a.pitch;
 }
 
 // What is written (contiguous, the workspace among it) apart from what is read and from one another.
@@ -319,6 +331,47 @@ int kpool_layer_norm_backward(const void *dy, const void *x, int64_t x_stride, c
     return kpool::launch_norm_bwd(dtype == KPOOL_DTYPE_F32, dy, x, x_stride, weight, mean, rstd, rows, N,
                                   dx, dweight, dbias, (float *)workspace, st);
   });
+  if (e != hipSuccess) return hip_fail(fn, e);
+  return ok();
+}
+
+int kpool_rotary(const void *x, int64_t x_stride, const int32_t *positions, const double *freqs,
+                 int64_t rows, int32_t heads, int32_t D, int32_t begin, int32_t pairs, float factor,
+                 int32_t dtype, uint32_t flags, void *y, int64_t y_stride, void *stream) {
+  const char *fn = "kpool_rotary";
+  if (dtype != KPOOL_DTYPE_BF16 && dtype != KPOOL_DTYPE_F32)
+    return fail(KPOOL_EINVAL, "%s: unknown dtype %d", fn, dtype);
+  if (flags & ~(KPOOL_ROTARY_INTERLEAVED | KPOOL_ROTARY_INVERSE))
+    return fail(KPOOL_EINVAL, "%s: unknown flags 0x%x", fn, flags);
+  if (rows < 0) return fail(KPOOL_EINVAL, "%s: rows must be >= 0", fn);
+  if (heads < 1 || heads > 65536) return fail(KPOOL_EINVAL, "%s: heads must be in [1, 65536] (got %d)", fn, heads);
+  if (D < 2 || D > 1024) return fail(KPOOL_EINVAL, "%s: D must be in [2, 1024] (got %d)", fn, D);
+  if (begin < 0 || begin > D || pairs < 1 || pairs > (D - begin) / 2)
+    return fail(KPOOL_EINVAL, "%s: need begin >= 0 and 1 <= pairs <= (D - begin) / 2 (begin=%d pairs=%d D=%d)", fn, begin,
+                pairs, D);
+  if (!isfinite(factor)) return fail(KPOOL_EINVAL, "%s: factor must be finite", fn);
+  const int64_t width = (int64_t)heads * D, most = int64_t(1) << 40;
+  if (x_stride < width || y_stride < width || x_stride > most || y_stride > most)
+    return fail(KPOOL_EINVAL, "%s: a stride must be in [heads * D, 2^40]", fn);
+  if (rows == 0) return ok();
+  if (!x || !y || !positions || !freqs) return fail(KPOOL_EINVAL, "%s: null pointer", fn);
+  const int64_t size = dtype == KPOOL_DTYPE_F32 ? 4 : 2;
+  const uintptr_t mask = size - 1;
+  if ((((uintptr_t)x | (uintptr_t)y) & mask) || ((uintptr_t)positions & 3) || ((uintptr_t)freqs & 7))
+    return fail(KPOOL_EINVAL, "%s: a pointer is not aligned to its elements", fn);
+  kpool::RotaryCall c{x, y, positions, freqs, x_stride, y_stride, rows, heads, D, begin, pairs, factor,
+                      dtype == KPOOL_DTYPE_F32, (flags & KPOOL_ROTARY_INTERLEAVED) != 0,
+                      (flags & KPOOL_ROTARY_INVERSE) != 0};
+  if (rows > (int64_t(1) << 31) || kpool::rotary_threads(c) >= kLaunchThreads)
+    return fail(KPOOL_EUNSUPPORTED, "%s: too many rows for one launch", fn);
+  const Operand to{"y", y, width * size, rows, y_stride * size};
+  const Operand in[3] = {{"x", x, width * size, rows, x_stride * size}, {"positions", positions, rows * 4},
+                         {"freqs", freqs, (int64_t)pairs * 8}};
+  const bool in_place = x == y && (x_stride == y_stride || rows == 1);
+  for (const Operand &r : in)
+    if (!(in_place && r.p == x) && rows_meet(to, r)) return fail(KPOOL_EINVAL, "%s: y overlaps %s", fn, r.name);
+  hipStream_t st = (hipStream_t)stream;
+  hipError_t e = timed_layer(kNorm, st, [&] { return kpool::launch_rotary(c, st); });
   if (e != hipSuccess) return hip_fail(fn, e);
   return ok();
 }

@@ -1,5 +1,5 @@
-// Declarations of the layer around the selection (norm.hip, attend.hip, attend_bwd.hip), apart from
-// the selection's in kpool_internal.h.
+// Declarations of the layer around the selection (norm.hip, rotary.hip, attend.hip, attend_bwd.hip), apart
+// from the selection's in kpool_internal.h.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -18,6 +18,20 @@ int norm_bwd_blocks(int64_t rows, int32_t N);
 hipError_t launch_norm_bwd(bool f32, const void *dy, const void *x, int64_t x_stride, const float *w,
                            const float *mean, const float *rstd, int64_t rows, int32_t N, void *dx,
                            float *dw, float *db, float *part, hipStream_t stream);
+
+// Rotary positions (rotary.hip); f32: x and y are fp32, else bf16 bits.  y may be x, at x's stride.
+struct RotaryCall {
+  const void *x;
+  void *y;
+  const int32_t *positions;
+  const double *freqs;
+  int64_t x_stride, y_stride, rows;  // strides in elements
+  int32_t heads, D, begin, pairs;
+  float factor;
+  bool f32, interleaved, inverse;
+};
+int64_t rotary_threads(const RotaryCall &c);  // of its launch
+hipError_t launch_rotary(const RotaryCall &c, hipStream_t st);
 
 // Attention (attend.hip).  A call's operands, its plan by the sizes alone, its workspace.
 struct AttendCall {

@@ -22,6 +22,7 @@ KPOOL_FLAG_TAIL = 2
 PROFILE_KINDS = ("pool_keys", "score", "topk", "expand", "scores_copy")
 LAYER_PROFILE_KINDS = ("norm", "attend")
 KPOOL_DTYPE_BF16, KPOOL_DTYPE_F32 = 0, 1
+KPOOL_ROTARY_INTERLEAVED, KPOOL_ROTARY_INVERSE = 1, 2
 
 _lib = None
 
@@ -69,6 +70,7 @@ def lib():
         "kpool_layer_norm_backward_workspace_bytes": (sz, [i64, i32]),
         "kpool_layer_norm_backward": (ctypes.c_int, [vp, vp, i64, vp, vp, vp, i64, i32, i32, vp, sz,
                                                      vp, vp, vp, vp]),
+        "kpool_rotary": (ctypes.c_int, [vp, i64, vp, vp, i64, i32, i32, i32, i32, f32, i32, u32, vp, i64, vp]),
         "kpool_profile_enable": (ctypes.c_int, [ctypes.c_int]),
         "kpool_profile_collect": (ctypes.c_int, [vp, vp]),
         "kpool_layer_profile_collect": (ctypes.c_int, [vp, vp]),
@@ -610,6 +612,94 @@ def layer_norm_backward_workspace_bytes(rows: int, N: int) -> int:
     return int(lib().kpool_layer_norm_backward_workspace_bytes(rows, N))
 
 
+def rotary_frequencies(pairs: int, base: float = 10000.0, scale: float = 1.0, trained: int | None = None,
+                       fast: float = 32.0, slow: float = 1.0, device="cuda"):
+    """Frequencies of rotary positions, fp64 [pairs] in radians a token, and the factor on the
+    rotated values: (freqs, factor).
+
+    Pair j of n turns by base^(-j / n) a token.  For contexts `scale` times as long as the
+    `trained` length (YaRN, Peng et al. 2023, section 3): pairs that make more than `fast` turns
+    within the trained length keep their frequency, those that make less than `slow` turns are
+    slowed by `scale`, and those between are mixed linearly; factor is 0.1 ln(scale) + 1.  With
+    trained=None every pair is slowed alike (linear interpolation), and factor is 1."""
+    import torch
+    if pairs < 1 or not base > 0 or not scale >= 1 or not fast > slow or (trained is not None and trained < 1):
+        raise ValueError("need pairs >= 1, base > 0, scale >= 1, fast > slow and trained >= 1")
+    freqs = base ** (-np.arange(pairs, dtype=np.float64) / pairs)
+    factor = 1.0
+    if scale > 1 and trained is None:
+        freqs = freqs / scale
+    elif scale > 1:
+        turns = trained * freqs / (2 * np.pi)
+        keep = np.clip((turns - slow) / (fast - slow), 0.0, 1.0)
+        freqs = freqs * (keep + (1.0 - keep) / scale)
+        factor = 0.1 * float(np.log(scale)) + 1.0
+    return torch.from_numpy(freqs).to(device), factor
+
+
+def _rotary(fn, x, positions, freqs, begin, interleaved, factor, out, stream, inverse):
+    import torch
+    dtype, device = x.dtype, x.device
+    shape = x.shape
+    if len(shape) == 2:
+        rows, D = shape
+        heads, (s0, s2) = 1, x.stride()
+        s1 = D
+    elif len(shape) == 3:
+        rows, heads, D = shape
+        s0, s1, s2 = x.stride()
+    else:
+        raise ValueError("x must be [rows, heads, D] or [rows, D]")
+    if not x.is_cuda or heads < 1 or (s2 != 1 and D > 1) or (s1 != D and heads > 1):
+        raise ValueError("x must be a device tensor with the heads of a row contiguous")
+    if dtype == torch.float32:
+        code = KPOOL_DTYPE_F32
+    elif dtype == torch.bfloat16 or dtype == torch.int16:
+        code = KPOOL_DTYPE_BF16
+    else:
+        raise ValueError("x must be bfloat16 (or int16 bit patterns) or float32")
+    if rows > 1 and s0 < heads * D:
+        raise ValueError("x must hold rows that do not overlap")
+    _like(positions, "positions", (rows,), torch.int32, device)
+    if freqs.dim() != 1:
+        raise ValueError("freqs must be [pairs]")
+    pairs = freqs.shape[0]
+    _like(freqs, "freqs", (pairs,), torch.float64, device)
+    y0 = heads * D
+    if out is not None:
+        if out.shape != shape or out.dtype != dtype or out.device != device or (D > 1 and out.stride(-1) != 1) or (
+                heads > 1 and out.stride(1) != D):
+            raise ValueError(f"out must be like x: {dtype} {tuple(shape)} on {device}, the heads of a row contiguous")
+        if rows > 1:
+            y0 = out.stride(0)
+    flags = (KPOOL_ROTARY_INTERLEAVED if interleaved else 0) | (KPOOL_ROTARY_INVERSE if inverse else 0)
+    with _OnDevice(x, stream) as s:
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=device)
+        rc = lib().kpool_rotary(x.data_ptr(), s0 if rows > 1 else heads * D, positions.data_ptr(), freqs.data_ptr(),
+                                rows, heads, D, begin, pairs, factor, code, flags, out.data_ptr(), y0, s)
+    _check(rc, "kpool_rotary")
+    return out
+
+
+def rotary(x, positions, freqs, begin: int = 0, interleaved: bool = False, factor: float = 1.0, out=None, stream=None):
+    """Rotary positions: pairs of each head's values of x [rows, heads, D] or [rows, D] (bf16 or fp32, any
+    row stride) turned by positions[r] * freqs[j], times factor; the head's other values copied.
+
+    positions int32 [rows], freqs fp64 [pairs] (rotary_frequencies makes them).  Pair j is the values
+    begin + j and begin + pairs + j of a head, or, interleaved, begin + 2 j and begin + 2 j + 1.
+    out may be x itself (in place) or a slice of wider rows.  Autograd does not record the call (tensors
+    that require gradients are refused where it would); rotary_backward has its gradient."""
+    _refuse_graph("rotary", x)
+    return _rotary("rotary", x, positions, freqs, begin, interleaved, factor, out, stream, False)
+
+
+def rotary_backward(dy, positions, freqs, begin: int = 0, interleaved: bool = False, factor: float = 1.0, out=None,
+                    stream=None):
+    """Gradient of rotary: dx, the values of dy turned back.  The other arguments are the forward call's."""
+    return _rotary("rotary_backward", dy, positions, freqs, begin, interleaved, factor, out, stream, True)
+
+
 def _bytes(workspace, device):
     """Size of a caller's workspace (0 for none)."""
     if workspace is None:
@@ -657,13 +747,14 @@ class Selector:
     within the 2 GiB cap; overlap=True sizes it for two chunk buffers and runs the
     chunk loop with KPOOL_FLAG_OVERLAP (two chunks in flight on two streams);
     workspace_cap caps the workspace (smaller chunks); tail=True runs every step in
-    tail mode (KPOOL_FLAG_TAIL).  `attend` is the attention of the same rows over what the
-    last run selected.
+    tail mode (KPOOL_FLAG_TAIL).  rotary=(freqs, begin, interleaved, factor) gives `run`'s queries and
+    keys rotary positions, counted from each sequence's start, before they meet.  `attend` is the
+    attention of the same rows over what the last run selected.
     """
 
     def __init__(self, cu_seqlens, kpool: int, budget: int, H: int, D: int, device="cuda",
                  q_lo: int = 0, q_hi: int | None = None, workspace_cap: int | None = None,
-                 scale: float | None = None, overlap: bool = False, tail: bool = False):
+                 scale: float | None = None, overlap: bool = False, tail: bool = False, rotary=None):
         import torch
         self.cu = np.ascontiguousarray(np.asarray(cu_seqlens, dtype=np.int32))
         self.T = int(self.cu[-1])
@@ -689,6 +780,12 @@ class Selector:
         # the rows' sequences for the attention: their queries and the keys up to the last row
         self.attend_cu = row_range(self.cu, self.q_lo, self.q_hi)
         self.attend_cu_dev = tuple(torch.from_numpy(c).to(device) for c in self.attend_cu)
+        self.rotary = rotary
+        if rotary is not None:
+            local = np.arange(self.T, dtype=np.int32) - np.repeat(self.cu[:-1], np.diff(self.cu))
+            self.positions = torch.from_numpy(local.astype(np.int32)).to(device)
+            self.q_turned = torch.empty((self.T, H, D), dtype=torch.int16, device=device)
+            self.k_turned = torch.empty((self.T, D), dtype=torch.int16, device=device)
 
     @property
     def workspace_bytes(self) -> int:
@@ -708,7 +805,8 @@ class Selector:
         """One pass of the path; with gate scores g and slot embeddings ape the keys are
         pooled by the gated compression, otherwise by the mean.  With k_norm = (weight, bias,
         eps), k is the key projection's output and passes that layer norm first (its rows may
-        then be a slice of a wider projection)."""
+        then be a slice of a wider projection).  A selector with rotary positions turns q and the
+        (normalised) keys next, into buffers of its own; gate scores are left as they are."""
         import torch
         overlap = self.overlap if overlap is None else overlap
         if k_norm is not None:
@@ -721,6 +819,9 @@ class Selector:
             g = None if g is None else g[:self.T]
             with torch.no_grad():  # (ids have no gradients)
                 k = layer_norm(k[:self.T], weight, bias, eps, out=self.k_normed.view(k.dtype), stream=stream)[0]
+        if self.rotary is not None:
+            q, k = self._turn(q, k, stream)
+            g = None if g is None else g[:self.T]
         if g is not None:
             pool_keys_gated(k, g, ape, self.cu, self.cu_dev, self.cu_pools_dev, self.kpool,
                             out=self.kp, stream=stream, tail=self.tail)
@@ -733,6 +834,19 @@ class Selector:
         expand(self.pool_ids, self.cu, self.cu_dev, self.kpool, self.budget, self.q_lo, self.q_hi,
                out=self.token_ids, stream=stream, tail=self.tail)
         return {"kp": self.kp, "pool_ids": self.pool_ids, "token_ids": self.token_ids}
+
+    def _turn(self, q, k, stream):
+        """Index queries (the rows' own) and keys at their positions, in the selector's buffers."""
+        import torch
+        if q.shape != self.q_turned.shape or q.element_size() != 2 or k.dim() != 2 or k.shape[0] < self.T:
+            raise ValueError(f"need q [{self.T}, {self.H}, {self.D}] and k with {self.T} rows in bfloat16 (or int16)")
+        freqs, begin, interleaved, factor = self.rotary
+        how = dict(begin=begin, interleaved=interleaved, factor=factor, stream=stream)
+        rows = slice(self.q_lo, self.q_hi)
+        with torch.no_grad():  # (ids have no gradients)
+            rotary(q[rows], self.positions[rows], freqs, out=self.q_turned[rows].view(q.dtype), **how)
+            rotary(k[:self.T], self.positions, freqs, out=self.k_turned.view(k.dtype), **how)
+        return self.q_turned, self.k_turned
 
     def attend(self, q, k, v, scale: float | None = None, out=None, want_lse: bool = False, stream=None):
         """Attention of the selector's rows over the tokens the last run selected for them:
