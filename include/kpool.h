@@ -311,6 +311,59 @@ int kpool_attend_selected(const uint16_t *q, int64_t q_stride, const uint16_t *k
                           int32_t Hkv, int32_t D, float scale, void *workspace,
                           size_t workspace_bytes, uint16_t *o, float *lse, void *stream);
 
+/* Latent attention over a cache - the absorbed form (Atlas inference docs, glm5next_dsa/tp.rs: the
+ * shard plan's kv_a_proj_with_mqa and kv_b_proj): one row of R + P values a token is the key of every
+ * head, its first R values are the value.  For token row i of sequence s and head h
+ *   o[i,h,:] = sum_j softmax_j(scale * <q[i,h,:], c[j,:]>) c[j,:R]
+ *   lse[i,h] = log sum_j exp(scale * <q[i,h,:], c[j,:]>)
+ * over the tokens j <= t(i), or, kpool_attend_latent_selected, over the tokens token_ids[i, 0 .. width)
+ * that lie in 0 .. t(i) (as for kpool_attend_selected: other entries stand for nothing, a token that is
+ * listed twice counts twice).
+ *   q        bf16, token row i at q + i * q_stride elements, its heads [H, R + P] contiguous (the latent
+ *            part, absorbed, then the positional part)
+ *   cache    bf16, row r at cache + r * cache_stride elements, cache_rows of them
+ *   page_table  int32 [nseq, pages_per_seq] device: token j of sequence s is the cache's row
+ *            page_table[s, j / page_size] * page_size + j % page_size; or NULL:
+ *   k_starts int32 [nseq] device: token j is row k_starts[s] + j (not read with a page table)
+ *   k_lens   int32 [nseq] device: the sequence's tokens, those of its queries among them; its queries
+ *            are the LAST of them: with Lq queries, query n sits at position t = k_lens[s] - Lq + n.
+ *            Lengths, page table and starts are read when the call runs on the device: a captured
+ *            call replays with what they hold then.  Lengths are taken as at most max_len (and what
+ *            pages_per_seq pages hold) and at least 0.  Tokens whose page or row the cache does not
+ *            have stand for nothing; entries of the page table past a sequence's tokens are not read.
+ *   cu_q     sequence s has the query rows [cu_q[s], cu_q[s+1]), any numbers, 0 among them; host and device
+ *            copies hold the same values
+ *   o        bf16 [Tq, H, R] contiguous, Tq = cu_q[nseq]; rows past Tq are not touched
+ *   lse      NULLABLE fp32 [Tq, H]
+ * A row that sees nothing gets o = 0 and lse = -inf.  Sums and statistics are fp32; the weights are
+ * rounded to bf16 for the product with the values, and o once.  q and the cache rows of the tokens that
+ * some row sees must be finite; no other rows are read.  Outputs and the workspace overlap neither inputs
+ * nor one another.  The same call gives the same bits every time.
+ * Sizes: R a multiple of 8 up to 512; P a multiple of 8 up to 64, or 0; strides multiples of 8 (q's from
+ * H * (R + P) to 2^24, the cache's from R + P to 2^24); q, cache, o and the workspace 16-byte aligned; at
+ * most 2^31 - 1 cache rows and tokens in pages_per_seq pages, max_len at most 2^31 - 256; tiles (16
+ * to 64 rows of a sequence by 64 tokens) of all sequences below 2^31.
+ *   workspace  kpool_attend_latent(_selected)_workspace_bytes(the same sizes) bytes (may be 0: then it is
+ *            not read); scratch.  It does not depend on what k_lens holds. */
+size_t kpool_attend_latent_workspace_bytes(const int32_t *cu_q_host, int32_t nseq, int32_t max_len,
+                                           int32_t H, int32_t R, int32_t P);
+int kpool_attend_latent(const uint16_t *q, int64_t q_stride, const uint16_t *cache,
+                        int64_t cache_stride, int64_t cache_rows, const int32_t *page_table,
+                        int32_t pages_per_seq, int32_t page_size, const int32_t *k_starts,
+                        const int32_t *k_lens, int32_t max_len, const int32_t *cu_q_host,
+                        const int32_t *cu_q_dev, int32_t nseq, int32_t H, int32_t R, int32_t P,
+                        float scale, void *workspace, size_t workspace_bytes, uint16_t *o, float *lse,
+                        void *stream);
+size_t kpool_attend_latent_selected_workspace_bytes(int64_t Tq, int32_t width, int32_t H, int32_t R,
+                                                    int32_t P);
+int kpool_attend_latent_selected(const uint16_t *q, int64_t q_stride, const uint16_t *cache,
+                                 int64_t cache_stride, int64_t cache_rows, const int32_t *page_table,
+                                 int32_t pages_per_seq, int32_t page_size, const int32_t *k_starts,
+                                 const int32_t *k_lens, const int32_t *token_ids, int32_t width,
+                                 const int32_t *cu_q_host, const int32_t *cu_q_dev, int32_t nseq,
+                                 int32_t H, int32_t R, int32_t P, float scale, void *workspace,
+                                 size_t workspace_bytes, uint16_t *o, float *lse, void *stream);
+
 /* Layer norm of rows - the indexer's keys pass one with weight and bias before they are
  * pooled (Atlas inference docs, glm5next_dsa/tp.rs: the indexer's k_norm among the shard
  * plan's tensors).  For row r and column j < N:

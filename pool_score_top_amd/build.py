@@ -16,13 +16,17 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libkpool.so")
 # (layer.hip includes api.hip: one translation unit with the C ABI's shared state)
 SOURCES = ["layer.hip", "pool_keys.hip", "score.hip", "topk.hip", "expand.hip", "norm.hip",
-           "rotary.hip", "attend.hip", "attend_bwd.hip"]
+           "rotary.hip", "attend.hip", "attend_bwd.hip", "latent.hip"]
 # Per-file flags.  The score kernel runs with the IEEE mode bit off so that the
 # ReLU is one v_max_f32 (no NaN-quieting canonicalize before it); its inputs are
 # finite bf16 / fp32 values, and NaN propagation is the only behaviour this changes.
 # (Its instruction order is pinned in the source with scheduling-group barriers; the
 # max-ILP machine scheduler measured ~2% slower with them than the default one.)
-FILE_FLAGS = {"score.hip": ["-mno-amdgpu-ieee", "-fno-honor-nans"]}
+# The latent attention's kernels hold up to 500 registers: results of matrix instructions stay in
+# ordinary registers (vector instructions cannot take accumulation registers, and copies to and fro
+# would double them), the queries' fragments in accumulation registers.
+FILE_FLAGS = {"score.hip": ["-mno-amdgpu-ieee", "-fno-honor-nans"],
+              "latent.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

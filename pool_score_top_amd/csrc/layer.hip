@@ -146,6 +146,74 @@ int check_attend_plan(const char *fn, const kpool::AttendCall &c, const kpool::A
                      {q_of(c), k_of(c), v_of(c), cu_q_of(c), cu_k_of(c), ids});
 }
 
+int check_latent_sizes(const char *fn, int32_t H, int32_t R, int32_t P) {
+  if (H < 1) return fail(KPOOL_EINVAL, "%s: H must be positive (got %d)", fn, H);
+  if (H > 65536) return fail(KPOOL_EUNSUPPORTED, "%s: more than 65536 heads (got %d)", fn, H);
+  if (R < 8 || R % 8 || P < 0 || P % 8)
+    return fail(KPOOL_EINVAL, "%s: R must be a positive multiple of 8, P a multiple of 8 (R=%d P=%d)", fn, R, P);
+  if (R > 512 || P > 64) return fail(KPOOL_EUNSUPPORTED, "%s: R up to 512 and P up to 64 are compiled in (R=%d P=%d)", fn, R, P);
+  return KPOOL_OK;
+}
+
+int check_latent_rows(const char *fn, const int32_t *cu_q, int32_t nseq, int32_t H) {
+  const int rc = check_cu(cu_q, nseq, fn);
+  if (rc) return rc;
+  for (int32_t s = 0; s < nseq; ++s)  // (a tile's rows are numbered in 32 bits)
+    if ((int64_t)(cu_q[s + 1] - cu_q[s]) * H > 0x7FFFFF00)
+      return fail(KPOOL_EUNSUPPORTED, "%s: sequence %d has too many query rows", fn, s);
+  return KPOOL_OK;
+}
+
+int check_max_len(const char *fn, int32_t max_len) {
+  if (max_len < 0 || max_len > 0x7FFFFF00)
+    return fail(KPOOL_EINVAL, "%s: max_len must be in [0, 2^31 - 256] (got %d)", fn, max_len);
+  return KPOOL_OK;
+}
+
+// Both forms' call; c.ids, c.width and c.max_len are set, the plan is made.
+int run_latent(const char *fn, kpool::LatentCall &c, const kpool::LatentPlan &p, int64_t Tq, void *workspace,
+               size_t workspace_bytes, void *stream) {
+  if (!(c.scale > 0.0f) || !isfinite(c.scale)) return fail(KPOOL_EINVAL, "%s: scale must be finite and > 0", fn);
+  const int32_t width = c.R + c.P;
+  if (c.q_stride < (int64_t)c.H * width || c.q_stride % 8 || c.q_stride > (1 << 24))
+    return fail(KPOOL_EINVAL, "%s: q_stride must be a multiple of 8 in [%lld, 2^24] (got %lld)", fn,
+                (long long)c.H * width, (long long)c.q_stride);
+  if (c.cache_stride < width || c.cache_stride % 8 || c.cache_stride > (1 << 24))
+    return fail(KPOOL_EINVAL, "%s: cache_stride must be a multiple of 8 in [%d, 2^24] (got %lld)", fn, width,
+                (long long)c.cache_stride);
+  if (c.cache_rows < 0 || c.cache_rows > 0x7FFFFFFF)
+    return fail(KPOOL_EINVAL, "%s: cache_rows must be in [0, 2^31) (got %lld)", fn, (long long)c.cache_rows);
+  if (c.page_table && (c.page_size < 1 || c.pages_per_seq < 0 || (int64_t)c.pages_per_seq * c.page_size > 0x7FFFFFFF))
+    return fail(KPOOL_EINVAL, "%s: need page_size >= 1, pages_per_seq >= 0 and fewer than 2^31 tokens of both (%d, %d)", fn,
+                c.page_size, c.pages_per_seq);
+  if (Tq == 0) return ok();
+  if (p.tiles > 0x7FFFFFFF || p.units > 0x7FFFFFFF) return fail(KPOOL_EUNSUPPORTED, "%s: too many query rows for one launch", fn);
+  if (!c.q || !c.o || !c.cu_q || !c.k_lens || (!c.page_table && !c.k_starts) || (c.cache_rows > 0 && !c.cache))
+    return fail(KPOOL_EINVAL, "%s: null pointer", fn);
+  if (!aligned16(c.q) || !aligned16(c.cache) || !aligned16(c.o))
+    return fail(KPOOL_EINVAL, "%s: q, cache and o must be 16-byte aligned", fn);
+  if (((uintptr_t)c.cu_q | (uintptr_t)c.k_lens | (uintptr_t)c.page_table | (uintptr_t)c.k_starts | (uintptr_t)c.ids |
+       (uintptr_t)c.lse) & 3)
+    return fail(KPOOL_EINVAL, "%s: a pointer is not aligned to its elements", fn);
+  const size_t need = kpool::latent_workspace(p, c.R);
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(KPOOL_EWORKSPACE, "%s: needs %zu bytes of workspace, got %zu", fn, need,
+                workspace ? workspace_bytes : (size_t)0);
+  if (need && !aligned16(workspace)) return fail(KPOOL_EINVAL, "%s: workspace must be 16-byte aligned", fn);
+  const int64_t rows = Tq * c.H;
+  const int rc = check_apart(
+      fn, {{"o", c.o, rows * c.R * 2}, {"lse", c.lse, rows * 4}, {"workspace", workspace, (int64_t)need}},
+      {{"q", c.q, (int64_t)c.H * width * 2, Tq, c.q_stride * 2}, {"cache", c.cache, width * 2, c.cache_rows, c.cache_stride * 2},
+       {"page_table", c.page_table, (int64_t)c.nseq * c.pages_per_seq * 4},
+       {"k_starts", c.page_table ? nullptr : c.k_starts, c.nseq * 4LL}, {"k_lens", c.k_lens, c.nseq * 4LL},
+       {"cu_q", c.cu_q, ((int64_t)c.nseq + 1) * 4}, {"token_ids", c.ids, Tq * c.width * 4}});
+  if (rc) return rc;
+  hipStream_t st = (hipStream_t)stream;
+  hipError_t e = timed_layer(kAttend, st, [&] { return kpool::launch_latent(c, p, workspace, st); });
+  if (e != hipSuccess) return hip_fail(fn, e);
+  return ok();
+}
+
 }  // namespace
 
 extern "C" {
@@ -263,6 +331,67 @@ int kpool_attend_selected(const uint16_t *q, int64_t q_stride, const uint16_t *k
   });
   if (e != hipSuccess) return hip_fail(fn, e);
   return ok();
+}
+
+size_t kpool_attend_latent_workspace_bytes(const int32_t *cu_q_host, int32_t nseq, int32_t max_len,
+                                           int32_t H, int32_t R, int32_t P) {
+  const char *fn = "kpool_attend_latent_workspace_bytes";
+  if (check_latent_sizes(fn, H, R, P) || check_latent_rows(fn, cu_q_host, nseq, H)) return 0;
+  if (check_max_len(fn, max_len)) return 0;
+  ok();
+  return kpool::latent_workspace(kpool::plan_latent(cu_q_host, nseq, H, max_len), R);
+}
+
+int kpool_attend_latent(const uint16_t *q, int64_t q_stride, const uint16_t *cache,
+                        int64_t cache_stride, int64_t cache_rows, const int32_t *page_table,
+                        int32_t pages_per_seq, int32_t page_size, const int32_t *k_starts,
+                        const int32_t *k_lens, int32_t max_len, const int32_t *cu_q_host,
+                        const int32_t *cu_q_dev, int32_t nseq, int32_t H, int32_t R, int32_t P,
+                        float scale, void *workspace, size_t workspace_bytes, uint16_t *o, float *lse,
+                        void *stream) {
+  const char *fn = "kpool_attend_latent";
+  int rc = check_latent_sizes(fn, H, R, P);
+  if (!rc) rc = check_latent_rows(fn, cu_q_host, nseq, H);
+  if (!rc) rc = check_max_len(fn, max_len);
+  if (rc) return rc;
+  kpool::LatentCall c{q, cache, q_stride, cache_stride, cache_rows, page_table, k_starts, k_lens,
+                      pages_per_seq, page_size, max_len, cu_q_dev, nullptr, 0, nseq, H, R, P, scale, o, lse};
+  return run_latent(fn, c, kpool::plan_latent(cu_q_host, nseq, H, max_len), cu_q_host[nseq], workspace,
+                    workspace_bytes, stream);
+}
+
+size_t kpool_attend_latent_selected_workspace_bytes(int64_t Tq, int32_t width, int32_t H, int32_t R,
+                                                    int32_t P) {
+  const char *fn = "kpool_attend_latent_selected_workspace_bytes";
+  if (check_latent_sizes(fn, H, R, P)) return 0;
+  if (Tq < 0 || Tq > 0x7FFFFFFF || width < 0) {
+    fail(KPOOL_EINVAL, "%s: need Tq in [0, 2^31) and width >= 0", fn);
+    return 0;
+  }
+  ok();
+  return kpool::latent_workspace(kpool::plan_latent_list(Tq, H, width), R);
+}
+
+int kpool_attend_latent_selected(const uint16_t *q, int64_t q_stride, const uint16_t *cache,
+                                 int64_t cache_stride, int64_t cache_rows, const int32_t *page_table,
+                                 int32_t pages_per_seq, int32_t page_size, const int32_t *k_starts,
+                                 const int32_t *k_lens, const int32_t *token_ids, int32_t width,
+                                 const int32_t *cu_q_host, const int32_t *cu_q_dev, int32_t nseq,
+                                 int32_t H, int32_t R, int32_t P, float scale, void *workspace,
+                                 size_t workspace_bytes, uint16_t *o, float *lse, void *stream) {
+  const char *fn = "kpool_attend_latent_selected";
+  int rc = check_latent_sizes(fn, H, R, P);
+  if (!rc) rc = check_latent_rows(fn, cu_q_host, nseq, H);
+  if (rc) return rc;
+  if (width < 0 || width > (1 << 30)) return fail(KPOOL_EINVAL, "%s: width must be in [0, 2^30] (got %d)", fn, width);
+  const int64_t Tq = cu_q_host[nseq];
+  if (Tq > 0 && width > 0 && !token_ids) return fail(KPOOL_EINVAL, "%s: null pointer", fn);
+  // (a list of no entries is the same as no tokens)
+  kpool::LatentCall c{q, cache, q_stride, cache_stride, cache_rows, page_table, k_starts, k_lens, pages_per_seq,
+                      page_size, width ? 0x7FFFFFFF : 0, cu_q_dev, width ? token_ids : nullptr, width, nseq, H, R, P, scale,
+                      o, lse};
+  return run_latent(fn, c, width ? kpool::plan_latent_list(Tq, H, width) : kpool::plan_latent(cu_q_host, nseq, H, 0), Tq,
+                    workspace, workspace_bytes, stream);
 }
 
 int kpool_layer_norm(const void *x, int64_t x_stride, const float *weight, const float *bias,

@@ -1,5 +1,5 @@
-// Declarations of the layer around the selection (norm.hip, rotary.hip, attend.hip, attend_bwd.hip), apart
-// from the selection's in kpool_internal.h.
+// Declarations of the layer around the selection (norm.hip, rotary.hip, attend.hip, attend_bwd.hip,
+// latent.hip), apart from the selection's in kpool_internal.h.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -85,6 +85,29 @@ size_t attend_bwd_workspace(const BwdPlan &p, int64_t Tq, int64_t Tk, int Hq, in
 int64_t attend_bwd_threads(const BwdPlan &p, int Hkv);  // of its largest launch, or more
 hipError_t launch_attend_bwd(const AttendCall &c, const uint16_t *d_o, const BwdPlan &p, void *workspace,
                              uint16_t *dq, uint16_t *dk, uint16_t *dv, hipStream_t st);
+
+// Latent attention over a cache of one row a token (latent.hip).  ids: [Tq, width] lists, or null.
+struct LatentCall {
+  const uint16_t *q, *cache;
+  int64_t q_stride, cache_stride, cache_rows;        // strides in elements
+  const int32_t *page_table, *k_starts, *k_lens;     // device; one of the first two
+  int32_t pages_per_seq, page_size, max_len;
+  const int32_t *cu_q, *ids;                         // device
+  int32_t width, nseq, H, R, P;
+  float scale;
+  uint16_t *o;
+  float *lse;
+};
+struct LatentPlan {
+  int rb;         // rows of a workgroup, by 16
+  int shares;     // equal shares of the work, or fewer
+  int64_t units;  // tiles of rows
+  int64_t tiles;  // of rows and keys, or more
+};
+LatentPlan plan_latent(const int32_t *cu_q, int nseq, int H, int64_t max_len);
+LatentPlan plan_latent_list(int64_t Tq, int H, int width);
+size_t latent_workspace(const LatentPlan &p, int R);
+hipError_t launch_latent(const LatentCall &c, const LatentPlan &p, void *workspace, hipStream_t st);
 
 #if defined(__HIPCC__)
 

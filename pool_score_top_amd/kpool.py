@@ -70,6 +70,12 @@ def lib():
         "kpool_layer_norm_backward_workspace_bytes": (sz, [i64, i32]),
         "kpool_layer_norm_backward": (ctypes.c_int, [vp, vp, i64, vp, vp, vp, i64, i32, i32, vp, sz,
                                                      vp, vp, vp, vp]),
+        "kpool_attend_latent_workspace_bytes": (sz, [vp, i32, i32, i32, i32, i32]),
+        "kpool_attend_latent": (ctypes.c_int, [vp, i64, vp, i64, i64, vp, i32, i32, vp, vp, i32, vp, vp, i32, i32, i32,
+                                               i32, f32, vp, sz, vp, vp, vp]),
+        "kpool_attend_latent_selected_workspace_bytes": (sz, [i64, i32, i32, i32, i32]),
+        "kpool_attend_latent_selected": (ctypes.c_int, [vp, i64, vp, i64, i64, vp, i32, i32, vp, vp, vp, i32, vp, vp, i32,
+                                                        i32, i32, i32, f32, vp, sz, vp, vp, vp]),
         "kpool_rotary": (ctypes.c_int, [vp, i64, vp, vp, i64, i32, i32, i32, i32, f32, i32, u32, vp, i64, vp]),
         "kpool_profile_enable": (ctypes.c_int, [ctypes.c_int]),
         "kpool_profile_collect": (ctypes.c_int, [vp, vp]),
@@ -530,6 +536,132 @@ def attend_selected(q, k, v, token_ids, cu_q, cu_q_dev, cu_k=None, cu_k_dev=None
         rc = lib().kpool_attend_selected(*a.rows, _at(token_ids), width, *a.cu, _at(ws),
                                          _bytes(ws, q.device), _at(out), _at(lse), s)
     _check(rc, "kpool_attend_selected")
+    return out, lse
+
+
+class _Latent:
+    """The arguments that both forms of the latent attention share, checked."""
+
+    def __init__(self, q, cache, rank, cu_q, cu_q_dev, k_lens, scale, page_table, k_starts):
+        import torch
+        codes = (torch.bfloat16, torch.int16)
+        self.device = device = q.device
+        tq, self.H, width, qs = _heads(q, "q", device, codes)
+        self.R, self.P = rank, width - rank
+        if not 0 < rank <= width:
+            raise ValueError(f"rank must be in 1 .. {width}, the values of a head of q")
+        if cache.dtype not in codes or cache.device != device or cache.shape[-1:] != (width,):
+            raise ValueError(f"cache must be a bfloat16 (or int16) tensor with rows of {width} values on {device}")
+        if (page_table is None) == (k_starts is None):
+            raise ValueError("give one of page_table and k_starts")
+        self.cu_q = cu = np.ascontiguousarray(cu_q, dtype=np.int32)
+        if cu.ndim != 1 or len(cu) < 2:
+            raise ValueError("cu_q must be 1-dimensional with nseq + 1 entries")
+        self.nseq, self.Tq = len(cu) - 1, int(cu[-1])
+        _like(cu_q_dev, "cu_q_dev", cu.shape, torch.int32, device)
+        _like(k_lens, "k_lens", (self.nseq,), torch.int32, device)
+        if tq < self.Tq:
+            raise ValueError("q has fewer tokens than its cumulative lengths say")
+        rows, per_seq, page = cache.shape[0], 0, 1
+        stride = cache.stride()
+        if page_table is not None:
+            if cache.dim() != 3 or page_table.dim() != 2:
+                raise ValueError("with a page table the cache is [pages, page_size, R + P], the table [nseq, pages]")
+            page, per_seq = cache.shape[1], page_table.shape[1]
+            _like(page_table, "page_table", (self.nseq, per_seq), torch.int32, device)
+            if rows > 1 and page > 0 and stride[0] != page * stride[1] and page > 1:
+                raise ValueError("the pages of the cache must follow one another")
+            row_stride = stride[1] if page > 1 else stride[0] if rows > 1 else width
+            rows *= page
+        else:
+            if cache.dim() != 2:
+                raise ValueError("with k_starts the cache is [rows, R + P]")
+            _like(k_starts, "k_starts", (self.nseq,), torch.int32, device)
+            row_stride = stride[0] if rows > 1 else width
+        if stride[-1] != 1 and width > 1:
+            raise ValueError("the values of a row of the cache must be contiguous")
+        self.cu_ptr = _host_address(cu)
+        self.keys = (q.data_ptr(), qs, cache.data_ptr() if rows else None, row_stride, rows, _at(page_table), per_seq, page,
+                     _at(k_starts), k_lens.data_ptr())
+        self.cu = (self.cu_ptr, cu_q_dev.data_ptr(), self.nseq, self.H, self.R, self.P, scale)
+
+    def outputs(self, q, out, lse, want_lse):
+        import torch
+        shape = (self.Tq, self.H, self.R)
+        if out is None:
+            out = torch.empty(shape, dtype=q.dtype, device=self.device)
+        else:
+            _like(out, "out", shape, q.dtype, self.device)
+        if lse is not None:
+            _like(lse, "lse", shape[:2], torch.float32, self.device)
+        elif want_lse:
+            lse = torch.empty(shape[:2], dtype=torch.float32, device=self.device)
+        return out, lse
+
+
+def _latent_bytes(fn, *args):
+    nb = int(getattr(lib(), fn)(*args))
+    msg = lib().kpool_last_error().decode()
+    if msg:
+        raise KpoolError(fn, KPOOL_EINVAL, msg)
+    return nb
+
+
+def attend_latent_workspace_bytes(cu_q, max_len: int, H: int, R: int, P: int) -> int:
+    """Workspace of attend_latent for these sizes (0 where it needs none)."""
+    cu_q, qp = _host_i32(cu_q)
+    return _latent_bytes("kpool_attend_latent_workspace_bytes", qp, len(cu_q) - 1, max_len, H, R, P)
+
+
+def attend_latent(q, cache, rank: int, cu_q, cu_q_dev, k_lens, max_len: int, scale: float, page_table=None,
+                  k_starts=None, out=None, want_lse: bool = False, lse=None, workspace=None, stream=None):
+    """Latent attention, absorbed: query rows over the cached tokens they see: (o, lse or None).
+
+    q bf16 [Tq, H, R + P] (any token stride), R being rank; the cache holds one row of R + P values a
+    token, which is every head's key and whose first R are the value: [pages, page_size, R + P] with
+    page_table int32 [nseq, pages], or [rows, R + P] with k_starts int32 [nseq], the sequences' first
+    rows.  k_lens int32 [nseq], on the device: each sequence's tokens, of which its queries (cu_q,
+    host and device) are the last, at most max_len.  A captured call reads lengths, pages and starts
+    anew at each replay.  o is bf16 [Tq, H, R].  Serving only: there is no backward pass, and tensors
+    that require gradients are refused where autograd would record the call."""
+    _refuse_graph("attend_latent", q, cache)
+    a = _Latent(q, cache, rank, cu_q, cu_q_dev, k_lens, scale, page_table, k_starts)
+    with _OnDevice(q, stream) as s:
+        out, lse = a.outputs(q, out, lse, want_lse)
+        if workspace is None:
+            import torch
+            nb = int(lib().kpool_attend_latent_workspace_bytes(a.cu_ptr, a.nseq, max_len, a.H, a.R, a.P))
+            workspace = torch.empty(nb, dtype=torch.uint8, device=a.device) if nb else None
+        rc = lib().kpool_attend_latent(*a.keys, max_len, *a.cu, _at(workspace), _bytes(workspace, a.device), _at(out),
+                                       _at(lse), s)
+    _check(rc, "kpool_attend_latent")
+    return out, lse
+
+
+def attend_latent_selected_workspace_bytes(Tq: int, width: int, H: int, R: int, P: int) -> int:
+    """Workspace of attend_latent_selected for these sizes (0 where it needs none)."""
+    return _latent_bytes("kpool_attend_latent_selected_workspace_bytes", Tq, width, H, R, P)
+
+
+def attend_latent_selected(q, cache, rank: int, token_ids, cu_q, cu_q_dev, k_lens, scale: float, page_table=None,
+                           k_starts=None, out=None, want_lse: bool = False, lse=None, workspace=None, stream=None):
+    """attend_latent over the tokens each row selected: token_ids int32 [Tq, width], sequence-local
+    ids as expand gives them; entries that are negative or past the row stand for nothing."""
+    _refuse_graph("attend_latent_selected", q, cache)
+    import torch
+    a = _Latent(q, cache, rank, cu_q, cu_q_dev, k_lens, scale, page_table, k_starts)
+    if token_ids.dim() != 2:
+        raise ValueError("token_ids must be [Tq, width]")
+    width = token_ids.shape[1]
+    _like(token_ids, "token_ids", (a.Tq, width), torch.int32, a.device)
+    with _OnDevice(q, stream) as s:
+        out, lse = a.outputs(q, out, lse, want_lse)
+        if workspace is None:
+            nb = int(lib().kpool_attend_latent_selected_workspace_bytes(a.Tq, width, a.H, a.R, a.P))
+            workspace = torch.empty(nb, dtype=torch.uint8, device=a.device) if nb else None
+        rc = lib().kpool_attend_latent_selected(*a.keys, _at(token_ids), width, *a.cu, _at(workspace),
+                                                _bytes(workspace, a.device), _at(out), _at(lse), s)
+    _check(rc, "kpool_attend_latent_selected")
     return out, lse
 
 
