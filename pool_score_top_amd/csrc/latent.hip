@@ -154,37 +154,25 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     before = __builtin_amdgcn_readfirstlane(scratch[5]), seq = __builtin_amdgcn_readfirstlane(scratch[6]);
   }
 
-  // fragments' addresses: a wave's 16 keys of a tile, and its columns, blocks of 16 from wave * CB on
-  uint32_t krow[4], kpe[2], vcol[C::CB];
+  // Addresses are kept as few registers and made where they are used (one instruction, (a ^ b) + c):
+  // fragments of a wave's 16 keys, whose step of 32 is ^ (step << 6) in the latent part; of its columns,
+  // whose block of 16 is ^ (block << 5)
+  uint32_t krow, kpe, vcol;
   {
-    Frag16<128> f;
-    f.init(lds0 + wave * 16 * 256, lane);
-    Frag16<64> fp;
-    fp.init(lds0 + NB * C::BLOCKB + wave * 16 * 128, lane);
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) krow[ks] = f.row[ks];
-    kpe[0] = fp.row[0], kpe[1] = fp.row[1];
     const int r = lane & 15, key = 4 * group + (r >> 2);
-    const uint32_t cb = key * 256 + ((((r & 3) >> 1) ^ Keys16<128>::swz(key)) << 4) + (r & 1) * 8;
-#pragma unroll
-    for (int c = 0; c < C::CB; ++c) {
-      const int at = wave * C::CB + c;
-      vcol[c] = lds0 + (at >> 3) * C::BLOCKB + (cb ^ ((at & 7) << 5));
-      opaque(vcol[c]);
-    }
+    krow = (wave * 16 + r) * 256 + ((group ^ Keys16<128>::swz(r)) << 4);
+    kpe = (wave * 16 + r) * 128 + ((group ^ Keys16<64>::swz(r)) << 4);
+    vcol = key * 256 + ((((r & 3) >> 1) ^ Keys16<128>::swz(key)) << 4) + (r & 1) * 8;
+    opaque(krow), opaque(kpe), opaque(vcol);
   }
-  // loads: of the latent part 4 NB a wave, 4 rows each; of the positional one 2 a wave, 8 rows each
-  uint32_t lcol[4], pcol;  // bytes
-  const int lblock = wave * NB / 4;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int chunk = lblock * 16 + ((lane & 15) ^ Keys16<128>::swz(i * 4 + group));
-    lcol[i] = min(chunk, a.R / 8 - 1) * 16;
-  }
-  pcol = (a.R + (a.P ? min((lane & 7) ^ Keys16<64>::swz(lane >> 3), a.P / 8 - 1) * 8 : -8)) * 2;
-  // the wave's loads of a tile, LOADS of them, in steps of two: step i's rows are read from the list
-  // one step ahead of their use
+  // Loads: of the latent part 4 NB a wave, 4 rows each; of the positional one 2 a wave, 8 rows each; in
+  // steps of two, whose rows are read from the list one step ahead of their use.  A lane's chunk of its
+  // row is lchunk ^ swz(4 i) (i the load's place in 16 rows), its last where the row ends before it.
   constexpr int LOADS = 4 * NB + 2;
+  const uint32_t last_chunk = a.R / 8 - 1;
+  uint32_t lchunk = wave * NB / 4 * 16 + ((lane & 15) ^ Keys16<128>::swz(group)),
+           pcol = (a.R + (a.P ? min((lane & 7) ^ Keys16<64>::swz(lane >> 3), a.P / 8 - 1) * 8 : -8)) * 2;
+  opaque(lchunk), opaque(pcol);
   struct Tile {
     uint32_t rows, pe_rows, to, pe_to;  // LDS: the lane's places in the list, where the loads go
   };
@@ -196,22 +184,23 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     opaque(x.rows), opaque(x.pe_rows), opaque_uniform(x.to), opaque_uniform(x.pe_to);
     return x;
   };
-  auto read_rows = [&](const Tile &x, int i, int64_t (&at)[2]) {
+  auto read_rows = [&](const Tile &x, int i, uint64_t (&at)[2]) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int n = 2 * i + u;
-      at[u] = *(KPOOL_LDS const int64_t *)(uintptr_t)(n < 4 * NB ? x.rows + n * 32 : x.pe_rows + (n - 4 * NB) * 64);
+      at[u] = *(KPOOL_LDS const uint64_t *)(uintptr_t)(n < 4 * NB ? x.rows + n * 32 : x.pe_rows + (n - 4 * NB) * 64);
     }
   };
-  auto load_rows = [&](const Tile &x, int i, const int64_t (&at)[2]) {
+  auto load_rows = [&](const Tile &x, int i, const uint64_t (&at)[2]) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int n = 2 * i + u;
-      if (n < 4 * NB) load_lds_16((const char *)a.cache + at[u] + lcol[n & 3], x.to + n * 1024);
-      else load_lds_16((const char *)a.cache + at[u] + pcol, x.pe_to + (n - 4 * NB) * 1024);
+      uint32_t off = pcol;
+      if (n < 4 * NB) off = min(lchunk ^ (uint32_t)Keys16<128>::swz(n % 4 * 4), last_chunk) * 16;
+      load_lds_16((const void *)(at[u] + off), n < 4 * NB ? x.to + n * 1024 : x.pe_to + (n - 4 * NB) * 1024);
     }
   };
-  int64_t *list = reinterpret_cast<int64_t *>(lds + C::OFFS);
+  uint64_t *list = reinterpret_cast<uint64_t *>(lds + C::OFFS);  // the rows' addresses
   int *places = reinterpret_cast<int *>(lds + C::POS);
   float *top_of = reinterpret_cast<float *>(lds + C::TOP);  // [4][BQ]
   int *count = reinterpret_cast<int *>(lds + C::COUNT);
@@ -260,7 +249,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     for (int block = e_lo; block < e_hi; block += kLatentBlock) {
       // the block's keys that exist, in order: offsets of their rows, and their places
       const int end = min(e_hi, block + kLatentBlock);
-      int64_t off[2];
+      uint64_t off[2];
       int place[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -278,7 +267,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
           if (start >= 0 && start + p < a.nrows) row = start + p;
         }
         place[i] = row >= 0 ? p : -1;
-        off[i] = row * a.cs * 2;
+        off[i] = (uint64_t)(a.cache + row * a.cs);
       }
       uint64_t there[2];
 #pragma unroll
@@ -306,7 +295,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
 
       if (ntile > 0) {
         const Tile x = tile_at(0, 0);
-        int64_t at[2][2];
+        uint64_t at[2][2];
         read_rows(x, 0, at[0]);
 #pragma unroll
         for (int i = 0; i < LOADS / 2; ++i) {
@@ -321,14 +310,13 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         barrier_only();
         const bool more = j + 1 < ntile;
         const Tile next = tile_at(more ? j + 1 : j, (j + 1) & 1);
-        int64_t at[2][2];
+        uint64_t at[2][2];
         read_rows(next, 0, at[0]);
         // S.  Fragments of keys are read a few ahead of the products that need them.
-        uint32_t kr[6];
-#pragma unroll
-        for (int i = 0; i < 6; ++i) kr[i] = (i < 4 ? krow[i & 3] : kpe[i & 1]) + buf;
+        const uint32_t tile0 = lds0 + buf;
         auto read_key = [&](int ks) {
-          return ks < NB * 4 ? lds_read(kr[ks & 3] + (ks >> 2) * C::BLOCKB) : lds_read(kr[4 + ks - NB * 4]);
+          return ks < NB * 4 ? lds_read((krow ^ ((ks & 3) << 6)) + (tile0 + (ks >> 2) * C::BLOCKB))
+                             : lds_read((kpe ^ ((ks & 1) << 6)) + (tile0 + NB * C::BLOCKB));
         };
         // (and so are the loads of the next tile issued beside them)
         constexpr int AHEAD = 4;
@@ -403,11 +391,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         __builtin_amdgcn_s_waitcnt(0xC07F);
         barrier_only();
         // O
-        uint32_t vr[C::CB];
-#pragma unroll
-        for (int c = 0; c < C::CB; ++c) vr[c] = vcol[c] + buf;
-        auto read_value = [&](int i) {  // columns i % CB of keys 32 (i / CB) ..
-          const uint32_t at = vr[i % C::CB] + i / C::CB * 32 * 256;
+        auto read_value = [&](int i) {  // columns i % CB of the wave's, keys 32 (i / CB) ..
+          const int c = wave * C::CB + i % C::CB;
+          const uint32_t at = (vcol ^ ((c & 7) << 5)) + (tile0 + (c >> 3) * C::BLOCKB + i / C::CB * 32 * 256);
           return lds_read_cols(at, at + 16 * 256);
         };
         bf16x8 v[2 * C::CB], p[RB];
@@ -480,37 +466,44 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
   }
 }
 
-// Joins the parts of the units that lie across shares: o = sum_s e^(lse_s - lse) o_s, 8 rows of the
-// unit that a share begins a workgroup.
+// Joins the parts of the units that lie across shares, o = sum_s e^(lse_s - lse) o_s: a workgroup for a
+// row of the unit that a share begins.  256 / (R / 4) groups of threads take the parts in turn, each
+// thread 4 columns, and add up in order.
 __global__ __launch_bounds__(256) void latent_join_kernel(LatentArgs a, int BQ) {
-  const int per_unit = BQ / 8, share = blockIdx.x / per_unit, r0 = blockIdx.x % per_unit * 8;
+  __shared__ float lse_of[kMostShares], weight[kMostShares];
+  __shared__ f32x4 sums[256];
+  const int share = blockIdx.x / BQ, r = blockIdx.x - share * BQ, tid = threadIdx.x;
   const LatentCut cut = a.cut[share];
-  if (cut.end == 0) return;
-  int last = share;  // the share in which the unit ends
-  while (last + 1 < cut.shares && share_start(cut.total, cut.shares, last + 1) < cut.end) ++last;
+  if (cut.end == 0 || r >= cut.nrows) return;
   const float none = -__builtin_inff();
-  const int per = a.R / 4;
-  for (int e = threadIdx.x; e < 8 * per; e += 256) {
-    const int r = r0 + e / per, d = e % per * 4;
-    if (r >= cut.nrows) break;
-    float m = none, total = 0.0f;
-    f32x4 o = {};
-    auto slot = [&](int s) { return (int64_t)(2 * s + (s == share)) * BQ + r; };
-#pragma unroll 4
-    for (int s = share; s <= last; ++s) m = fmaxf(m, a.part_lse[slot(s)]);
-    const float shift = m > none ? m : 0.0f;
-#pragma unroll 4
-    for (int s = share; s <= last; ++s) {
-      const float w = exp2f_fast((a.part_lse[slot(s)] - shift) * kLog2e);
-      o += w * *reinterpret_cast<const f32x4 *>(a.part_o + slot(s) * a.R + d);
-      total += w;
-    }
-    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    const int64_t row = cut.row0 + r;
-    *reinterpret_cast<uint2 *>(a.o + row * a.R + d) =
-        make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
-    if (d == 0 && a.lse) a.lse[row] = total == 0.0f ? none : shift + log2f(total) * kLn2;
+  // part i is share `share` + i's; the unit's end lies in the last of them
+  const int s = share + tid;
+  const bool mine = tid == 0 || (s < cut.shares && share_start(cut.total, cut.shares, s) < cut.end);
+  auto slot = [&](int i) { return (int64_t)(2 * (share + i) + (i == 0)) * BQ + r; };
+  lse_of[tid] = mine ? a.part_lse[slot(tid)] : none;
+  const int parts = __syncthreads_count(mine);
+  float m = none;
+  for (int i = 0; i < parts; ++i) m = fmaxf(m, lse_of[i]);
+  const float shift = m > none ? m : 0.0f;
+  if (mine) weight[tid] = exp2f_fast((lse_of[tid] - shift) * kLog2e);
+  __syncthreads();
+  float total = 0.0f;
+  for (int i = 0; i < parts; ++i) total += weight[i];
+  const int per = a.R / 4, groups = 256 / per, g = tid / per, d = (tid - g * per) * 4;
+  f32x4 o = {};
+  if (g < groups) {
+#pragma unroll 8
+    for (int i = g; i < parts; i += groups) o += weight[i] * *reinterpret_cast<const f32x4 *>(a.part_o + slot(i) * a.R + d);
   }
+  sums[tid] = o;
+  __syncthreads();
+  if (g > 0) return;
+  for (int i = 1; i < groups; ++i) o += sums[i * per + tid];
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  const int64_t row = cut.row0 + r;
+  *reinterpret_cast<uint2 *>(a.o + row * a.R + d) =
+      make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+  if (tid == 0 && a.lse) a.lse[row] = total == 0.0f ? none : shift + log2f(total) * kLn2;
 }
 
 template <int NB, int RB, bool LIST>
@@ -519,7 +512,7 @@ hipError_t launch_latent_t(const LatentArgs &a, hipStream_t st) {
   hipLaunchKernelGGL((latent_kernel<NB, RB, LIST>), dim3(a.shares), dim3(256), C::LDS, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.shares == 1) return e;
-  hipLaunchKernelGGL(latent_join_kernel, dim3(a.shares * (C::BQ / 8)), dim3(256), 0, st, a, C::BQ);
+  hipLaunchKernelGGL(latent_join_kernel, dim3(a.shares * C::BQ), dim3(256), 0, st, a, C::BQ);
   return hipGetLastError();
 }
 
