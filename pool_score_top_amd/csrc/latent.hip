@@ -31,13 +31,14 @@
 namespace kpool {
 namespace {
 
-constexpr int kLatentKeys = 64, kLatentBlock = 512;
+constexpr int kLatentKeys = 64;
 
 struct LatentArgs {
   const uint16_t *q, *cache;
   int64_t qs, cs, nrows;  // elements between tokens, between cache rows; cache rows
   const int32_t *table, *starts, *lens, *cu_q, *ids;
   int per_seq, page, npages, max_len;
+  bool by_place;  // lists: ordered by place in the sequence
   int nseq, H, R, P, width;
   float scale_log2;
   int shares, hblocks, units;  // most shares; lists: units of a token, of the call
@@ -59,16 +60,23 @@ __device__ inline int share_start(int total, int n, int share) {
   return each * share + (total - each * n) * share / n;
 }
 
-template <int NB, int RB>
+template <int NB, int RB, bool LIST>
 struct Latent {
   static constexpr int BK = kLatentKeys, BQ = 16 * RB;
+  // waves by groups of rows and of keys for S: a wave's blocks of 16 rows and of 16 keys
+  static constexpr int RG = RB == 4 ? 2 : 1, KG = 4 / RG, RW = RB / RG, KW = 4 / KG;
   static constexpr int KS = NB * 4 + 2;             // contraction steps of 32: the latent part, then the positional
   static constexpr int CB = NB * 2;                 // 16-column blocks of a wave
   static constexpr int BLOCKB = BK * 256;           // bytes of 128 columns of a tile
   static constexpr int TILE = NB * BLOCKB + BK * 128;
-  static constexpr int PBUF = 2 * TILE, OFFS = PBUF + BQ * BK * 2, POS = OFFS + kLatentBlock * 8,
-                       TOP = POS + kLatentBlock * 4, COUNT = TOP + 4 * BQ * 4, LDS = COUNT + 64;
-  static_assert(LDS <= 163840, "LDS of a CU");
+  static constexpr int EACH = LIST ? 8 : 4, BLOCK = EACH * 256, GROUPS = 16;
+  // P; the rows of a block's keys, and, whole keys, their places.  What is used between tiles only
+  // lies in the tiles (a block's counts, the queries on their way to registers) or in P (exchanges of
+  // maxima and sums), and a tile's four flags where the first keys of the list were, which are loaded.
+  static constexpr int P = 2 * TILE, ROWS = P + BQ * BK * 2, PLACES = ROWS + BLOCK * 4,
+                       LDS = PLACES + (LIST ? 0 : BLOCK * 4);
+  static constexpr int QROW = KS * 64 + 16;  // bytes of a row of queries in LDS (16 rows over all banks)
+  static_assert(LDS <= 163840 && BQ * QROW <= 2 * TILE && GROUPS * 512 <= 2 * TILE && 4 * BQ * 4 <= BQ * BK * 2, "LDS");
 };
 
 // n tokens of a sequence, at most what the caller said and what its pages hold
@@ -85,6 +93,9 @@ __device__ inline int seq_tiles(const LatentArgs &a, int s, int BQ) {
 
 // Keeps the compiler from looking through a value that is the same in all lanes.
 __device__ inline void opaque_uniform(uint32_t &x) { asm volatile("" : "+s"(x)); }
+
+// Moves a fragment to accumulation registers, from where matrix instructions take it as it is.
+__device__ inline void to_accumulation(bf16x8 &x) { asm volatile("" : "+a"(x)); }
 
 // inclusive sum over the workgroup's 256 threads; scratch: 4 values of LDS.  All threads call it.
 __device__ inline int scan_256(int x, int *scratch) {
@@ -103,7 +114,7 @@ __device__ inline int scan_256(int x, int *scratch) {
 
 template <int NB, int RB, bool LIST>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void latent_kernel(LatentArgs a) {
-  using C = Latent<NB, RB>;
+  using C = Latent<NB, RB, LIST>;
   constexpr int BK = C::BK, BQ = C::BQ, TILE = C::TILE;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   const int lane = threadIdx.x & 63;
@@ -126,8 +137,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     }
   }
   total = __builtin_amdgcn_readfirstlane(total);
-  if (threadIdx.x == 0 && a.cut) a.cut[blockIdx.x].end = 0;
-  const int n = min(a.shares, total), share = blockIdx.x;
+  // (workgroups go to the 8 XCDs in turn: those of one take neighbouring shares)
+  const int n = min(a.shares, total), share = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+  if (threadIdx.x == 0 && a.cut && share < a.shares) a.cut[share].end = 0;
   if (share >= n) return;
   int pos = share_start(total, n, share);
   const int hi = share_start(total, n, share + 1);
@@ -157,53 +169,38 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
   // Addresses are kept as few registers and made where they are used (one instruction, (a ^ b) + c):
   // fragments of a wave's 16 keys, whose step of 32 is ^ (step << 6) in the latent part; of its columns,
   // whose block of 16 is ^ (block << 5)
+  const int key0 = wave / C::RG * 16 * C::KW, wrow = wave % C::RG * 16 * C::RW;  // of the wave's part of S
   uint32_t krow, kpe, vcol;
   {
     const int r = lane & 15, key = 4 * group + (r >> 2);
-    krow = (wave * 16 + r) * 256 + ((group ^ Keys16<128>::swz(r)) << 4);
-    kpe = (wave * 16 + r) * 128 + ((group ^ Keys16<64>::swz(r)) << 4);
+    krow = (key0 + r) * 256 + ((group ^ Keys16<128>::swz(r)) << 4);
+    kpe = (key0 + r) * 128 + ((group ^ Keys16<64>::swz(r)) << 4);
     vcol = key * 256 + ((((r & 3) >> 1) ^ Keys16<128>::swz(key)) << 4) + (r & 1) * 8;
     opaque(krow), opaque(kpe), opaque(vcol);
   }
-  // Loads: of the latent part 4 NB a wave, 4 rows each; of the positional one 2 a wave, 8 rows each; in
-  // steps of two, whose rows are read from the list one step ahead of their use.  A lane's chunk of its
-  // row is lchunk ^ swz(4 i) (i the load's place in 16 rows), its last where the row ends before it.
+  // Loads: of the latent part 4 NB a wave, 4 rows each; of the positional one 2 a wave, 8 rows each.  A
+  // lane's chunk of its row is lchunk ^ swz(4 i) (i the load's place in 16 rows), its last where the row
+  // ends before it.
   constexpr int LOADS = 4 * NB + 2;
-  const uint32_t last_chunk = a.R / 8 - 1;
+  const uint32_t last_chunk = a.R / 8 - 1, pitch = (uint32_t)a.cs * 2;
   uint32_t lchunk = wave * NB / 4 * 16 + ((lane & 15) ^ Keys16<128>::swz(group)),
            pcol = (a.R + (a.P ? min((lane & 7) ^ Keys16<64>::swz(lane >> 3), a.P / 8 - 1) * 8 : -8)) * 2;
-  opaque(lchunk), opaque(pcol);
-  struct Tile {
-    uint32_t rows, pe_rows, to, pe_to;  // LDS: the lane's places in the list, where the loads go
-  };
-  auto tile_at = [&](int tile, int buf) {
-    Tile x;
-    const uint32_t offs = lds0 + C::OFFS + tile * BK * 8;
-    x.rows = offs + (wave * 4 * NB % 16 * 4 + group) * 8, x.pe_rows = offs + (wave * 16 + (lane >> 3)) * 8;
-    x.to = lds0 + buf * TILE + wave * 4 * NB * 1024, x.pe_to = lds0 + buf * TILE + NB * C::BLOCKB + wave * 2048;
-    opaque(x.rows), opaque(x.pe_rows), opaque_uniform(x.to), opaque_uniform(x.pe_to);
-    return x;
-  };
-  auto read_rows = [&](const Tile &x, int i, uint64_t (&at)[2]) {
+  uint32_t rows_at = lds0 + C::ROWS + (wave * 4 * NB % 16 * 4 + group) * 4, pe_rows_at = lds0 + C::ROWS + (wave * 16 + (lane >> 3)) * 4;
+  opaque(lchunk), opaque(pcol), opaque(rows_at), opaque(pe_rows_at);
+  auto read_rows = [&](int tile, uint32_t (&at)[LOADS]) {
+    const uint32_t r = rows_at + tile * BK * 4, pe = pe_rows_at + tile * BK * 4;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int n = 2 * i + u;
-      at[u] = *(KPOOL_LDS const uint64_t *)(uintptr_t)(n < 4 * NB ? x.rows + n * 32 : x.pe_rows + (n - 4 * NB) * 64);
-    }
+    for (int n = 0; n < LOADS; ++n)
+      at[n] = *(KPOOL_LDS const uint32_t *)(uintptr_t)(n < 4 * NB ? r + n * 16 : pe + (n - 4 * NB) * 32);
   };
-  auto load_rows = [&](const Tile &x, int i, const uint64_t (&at)[2]) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int n = 2 * i + u;
-      uint32_t off = pcol;
-      if (n < 4 * NB) off = min(lchunk ^ (uint32_t)Keys16<128>::swz(n % 4 * 4), last_chunk) * 16;
-      load_lds_16((const void *)(at[u] + off), n < 4 * NB ? x.to + n * 1024 : x.pe_to + (n - 4 * NB) * 1024);
-    }
+  auto load_row = [&](int n, uint32_t at, uint32_t to) {  // to: the tile's buffer
+    uint32_t off = pcol;
+    if (n < 4 * NB) off = min(lchunk ^ (uint32_t)Keys16<128>::swz(n % 4 * 4), last_chunk) * 16;
+    load_lds_16((const char *)a.cache + (uint64_t)at * pitch + off,
+                to + (n < 4 * NB ? (wave * 4 * NB + n) * 1024 : NB * C::BLOCKB + (wave * 2 + n - 4 * NB) * 1024));
   };
-  uint64_t *list = reinterpret_cast<uint64_t *>(lds + C::OFFS);  // the rows' addresses
-  int *places = reinterpret_cast<int *>(lds + C::POS);
-  float *top_of = reinterpret_cast<float *>(lds + C::TOP);  // [4][BQ]
-  int *count = reinterpret_cast<int *>(lds + C::COUNT);
+  int *list = reinterpret_cast<int *>(lds + C::ROWS), *places = reinterpret_cast<int *>(lds + C::PLACES);
+  float *exchange = reinterpret_cast<float *>(lds + C::P);  // [4][BQ]
 
   while (pos < hi) {
     const int q_start = a.cu_q[seq], Lq = a.cu_q[seq + 1] - q_start, len = latent_len(a, seq);
@@ -218,202 +215,293 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     const int t0 = n0 / a.H + len - Lq, t1 = (n0 + nrows - 1) / a.H + len - Lq;  // first and last position
     const int e_lo = k0 * BK, e_hi = min(k1 * BK, LIST ? a.width : t1 + 1);
 
-    bf16x8 q[RB][C::KS];
-    int t[RB];
-    int part = group * 8;  // (opaque: what depends on it is not worth a register from one unit to the next)
-    asm volatile("" : "+v"(part));
+    // A block's keys.  place: of a thread's entries; found: what the page table (or the starts) say of them.
+    int place[C::EACH], found[C::EACH];
+    auto look_up = [&](int block) {
+      const int end = min(e_hi, block + C::BLOCK);
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-      const int r = rb * 16 + col;
-      const int at = (n0 + r) / a.H;
-      const uint16_t *src = a.q + (int64_t)(q_start + at) * a.qs + (n0 + r - at * a.H) * (a.R + a.P);
-      t[rb] = at + len - Lq;
+      for (int i = 0; i < C::EACH; ++i) {
+        const int e = block + threadIdx.x * C::EACH + i;
+        place[i] = -1;
+        if (e < end) place[i] = LIST ? a.ids[((int64_t)q_start + tok) * a.width + e] : e;
+      }
+#pragma unroll
+      for (int i = 0; i < C::EACH; ++i) {
+        if (place[i] > t1) place[i] = -1;
+        found[i] = -1;
+        if (place[i] >= 0) found[i] = a.table ? a.table[(int64_t)seq * a.per_seq + place[i] / a.page] : a.starts[seq];
+      }
+    };
+    // queries to LDS (behind the first tile), whole rows at a time, and from there to registers
+    __syncthreads();
+    {
+      constexpr int CHUNKS = C::KS * 4, THREADS = 256 / BQ, BATCH = (CHUNKS + THREADS - 1) / THREADS;  // of a row
+      uint32_t tid = threadIdx.x;  // (opaque: what depends on it is not worth a register from one unit to the next)
+      opaque(tid);
+      const int r = tid / THREADS, c0 = tid % THREADS, at = (n0 + r) / a.H;
+      const int latent = r < nrows ? a.R / 8 : 0, pe = r < nrows ? NB * 16 + a.P / 8 : 0;  // ends of its parts
+      const uint16_t *src = a.q + (int64_t)(q_start + at) * a.qs + (n0 + r - at * a.H) * (a.R + a.P) + c0 * 8;
+      uint4 z[BATCH];
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u) {
+        const int chunk = c0 + u * THREADS;
+        z[u] = make_uint4(0, 0, 0, 0);
+        if (chunk < NB * 16 ? chunk < latent : chunk < pe)
+          z[u] = *reinterpret_cast<const uint4 *>(src + u * THREADS * 8 + (chunk < NB * 16 ? 0 : a.R - NB * 128));
+      }
+      look_up(e_lo);
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u)
+        if (CHUNKS % THREADS == 0 || c0 + u * THREADS < CHUNKS)
+          *reinterpret_cast<uint4 *>(lds + TILE + r * C::QROW + (c0 + u * THREADS) * 16) = z[u];
+    }
+    __syncthreads();
+    bf16x8 q[C::RW][C::KS];
+    int t[C::RW];
+#pragma unroll
+    for (int rb = 0; rb < C::RW; ++rb) {
+      const int r = wrow + rb * 16 + col;
+      t[rb] = LIST ? 0 : (n0 + r) / a.H + len - Lq;
 #pragma unroll
       for (int ks = 0; ks < C::KS; ++ks) {
-        const int d = (ks < NB * 4 ? ks : ks - NB * 4) * 32 + part, most = ks < NB * 4 ? a.R : a.P;
-        uint4 z = make_uint4(0, 0, 0, 0);
-        if (r < nrows && d < most) z = *reinterpret_cast<const uint4 *>(src + (ks < NB * 4 ? 0 : a.R) + d);
-        q[rb][ks] = __builtin_bit_cast(bf16x8, z);
+        q[rb][ks] = lds_read(lds0 + TILE + r * C::QROW + ks * 64 + group * 16);
+        to_accumulation(q[rb][ks]);
       }
     }
     f32x4 o[C::CB][RB];
-    float m[RB], l[RB];
+    float m[RB], l[C::RW];  // the maxima of all rows, the wave's part of its rows' sums
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
-      m[rb] = -__builtin_inff(), l[rb] = 0.0f;
+      m[rb] = -__builtin_inff();
 #pragma unroll
       for (int c = 0; c < C::CB; ++c) o[c][rb] = f32x4{};
     }
-    wait_loads();
+#pragma unroll
+    for (int rb = 0; rb < C::RW; ++rb) l[rb] = 0.0f;
+    // m of the wave's row block rb (its group is the same for the wave)
+    auto own = [&](int rb) {
+      const float first = m[rb], other = m[RB - C::RW + rb];
+      return wrow == 0 ? first : other;
+    };
+    // group of a token in the order of a block: by the top 4 bits of its place, or one for all
+    const int shift = LIST && a.by_place ? max(0, 28 - __clz(max(len - 1, 1))) : 31;
+    const int ngroups = LIST && a.by_place ? C::GROUPS : 1;
 
-    for (int block = e_lo; block < e_hi; block += kLatentBlock) {
-      // the block's keys that exist, in order: offsets of their rows, and their places
-      const int end = min(e_hi, block + kLatentBlock);
-      uint64_t off[2];
-      int place[2];
+    for (int block = e_lo; block < e_hi; block += C::BLOCK) {
+      // the block's keys that exist: their rows (and places) in LDS by group, thread and place in the
+      // list.  Each thread counts its own, the counts are summed, each takes places from its starts on.
+      if (block > e_lo) look_up(block);
+      int row[C::EACH];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int e = block + i * 256 + threadIdx.x;
-        int p = -1;
-        if (e < end) p = LIST ? a.ids[((int64_t)q_start + tok) * a.width + e] : e;
-        if (p > t1) p = -1;
-        int64_t row = -1;
-        if (p >= 0 && a.table) {
-          const int pg = p / a.page;
-          const int id = a.table[(int64_t)seq * a.per_seq + pg];
-          if (id >= 0 && id < a.npages) row = (int64_t)id * a.page + (p - pg * a.page);
-        } else if (p >= 0) {
-          const int64_t start = a.starts[seq];
-          if (start >= 0 && start + p < a.nrows) row = start + p;
+      for (int i = 0; i < C::EACH; ++i) {
+        const int p = place[i], id = found[i];
+        row[i] = -1;
+        if (a.table) {
+          if (id >= 0 && id < a.npages) row[i] = id * a.page + p % a.page;
+        } else if (id >= 0 && (int64_t)id + p < a.nrows) {
+          row[i] = id + p;
         }
-        place[i] = row >= 0 ? p : -1;
-        off[i] = (uint64_t)(a.cache + row * a.cs);
       }
-      uint64_t there[2];
+      __syncthreads();  // (nobody reads the last block's list or tiles, or the queries, any more)
+      uint16_t *mine = reinterpret_cast<uint16_t *>(lds) + threadIdx.x;  // [ngroups][256]
+      for (int g = 0; g < ngroups; ++g) mine[g * 256] = 0;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) there[i] = __ballot(place[i] >= 0);
-      __syncthreads();  // (nobody reads the last block's list or tiles any more)
-      if (lane == 0) count[wave] = __popcll(there[0]), count[4 + wave] = __popcll(there[1]);
+      for (int i = 0; i < C::EACH; ++i)
+        if (row[i] >= 0) ++mine[(place[i] >> shift) * 256];
       __syncthreads();
-      int present = 0;
+      uint16_t *run = reinterpret_cast<uint16_t *>(lds) + threadIdx.x * 16;  // 16 threads' counts of a group
+      int sum = 0;
+      if ((int)threadIdx.x < ngroups * 16)
+        for (int i = 0; i < 16; ++i) {
+          const int c = run[i];
+          run[i] = (uint16_t)sum;
+          sum += c;
+        }
+      int *scratch = reinterpret_cast<int *>(lds + C::GROUPS * 512);
+      const int upto = scan_256(sum, scratch);
+      if (threadIdx.x == 255) scratch[4] = upto;
+      if ((int)threadIdx.x < ngroups * 16)
+        for (int i = 0; i < 16; ++i) run[i] += (uint16_t)(upto - sum);
+      __syncthreads();
+      const int present = __builtin_amdgcn_readfirstlane(scratch[4]);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          if (w == wave && place[i] >= 0) {
-            const int to = present + __popcll(there[i] & ((uint64_t(1) << lane) - 1));
-            list[to] = off[i], places[to] = place[i];
-          }
-          present += count[i * 4 + w];
+      for (int i = 0; i < C::EACH; ++i)
+        if (row[i] >= 0) {
+          const int to = mine[(place[i] >> shift) * 256]++;
+          list[to] = row[i];
+          if (!LIST) places[to] = place[i];
         }
       __syncthreads();
       const int ntile = (present + BK - 1) / BK;
       // (the last tile's absent keys read its first one and count for nothing)
-      if ((int)threadIdx.x < ntile * BK - present)
-        list[present + threadIdx.x] = list[(ntile - 1) * BK];
+      if ((int)threadIdx.x < ntile * BK - present) list[present + threadIdx.x] = list[(ntile - 1) * BK];
       __syncthreads();
 
+      uint32_t at[LOADS];
       if (ntile > 0) {
-        const Tile x = tile_at(0, 0);
-        uint64_t at[2][2];
-        read_rows(x, 0, at[0]);
+        read_rows(0, at);
 #pragma unroll
-        for (int i = 0; i < LOADS / 2; ++i) {
-          if (i + 1 < LOADS / 2) read_rows(x, i + 1, at[(i + 1) & 1]);
-          load_rows(x, i, at[i & 1]);
-        }
+        for (int n = 0; n < LOADS; ++n) load_row(n, at[n], lds0);
       }
       for (int j = 0; j < ntile; ++j) {
-        const uint32_t buf = (j & 1) * TILE;
-        f32x4 s[RB];
+        const uint32_t tile0 = lds0 + (j & 1) * TILE;
+        const bool more = j + 1 < ntile;
+        read_rows(more ? j + 1 : j, at);
+        // the wave's part of tile j has landed; behind the barrier everyone's has, and everyone is done with
+        // the buffer that tile j + 1 goes to
         __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0), lgkmcnt(0)
         barrier_only();
-        const bool more = j + 1 < ntile;
-        const Tile next = tile_at(more ? j + 1 : j, (j + 1) & 1);
-        uint64_t at[2][2];
-        read_rows(next, 0, at[0]);
-        // S.  Fragments of keys are read a few ahead of the products that need them.
-        const uint32_t tile0 = lds0 + buf;
-        auto read_key = [&](int ks) {
-          return ks < NB * 4 ? lds_read((krow ^ ((ks & 3) << 6)) + (tile0 + (ks >> 2) * C::BLOCKB))
-                             : lds_read((kpe ^ ((ks & 1) << 6)) + (tile0 + NB * C::BLOCKB));
+        uint32_t to = lds0 + ((j + 1) & 1) * TILE;
+        opaque_uniform(to);
+        // S, a block of keys after the other.  Fragments of keys are read a few ahead of the products that
+        // need them, the next tile's loads go out beside them, and P of a block is found beside the
+        // products of the next one: with the maximum so far.  A score far above that is rare: the waves
+        // say so, and only then find the tile's maximum together and begin again.
+        f32x4 s[C::KW][C::RW];
+        float p[C::RW][4], part[C::RW], top[C::RW], shift[C::RW];
+#pragma unroll
+        for (int rb = 0; rb < C::RW; ++rb) part[rb] = 0.0f, top[rb] = -__builtin_inff();
+        auto shifts = [&] {
+#pragma unroll
+          for (int rb = 0; rb < C::RW; ++rb) {
+            const float most = own(rb);
+            shift[rb] = most > -__builtin_inff() ? most : 0.0f;
+          }
         };
-        // (and so are the loads of the next tile issued beside them)
-        constexpr int AHEAD = 4;
-        static_assert(C::KS == LOADS, "two loads for two steps");
-        bf16x8 k[C::KS];
+        shifts();
+        const int last = LIST ? 0 : places[min(present, j * BK + BK) - 1];
+        const bool masked = j * BK + BK > present || (!LIST && last > t0);
+        auto mask = [&](int kb) {  // what a row does not see
+          if (!masked) return;
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) s[rb] = f32x4{};
+          for (int i = 0; i < 4; ++i) {
+            const int key = j * BK + key0 + kb * 16 + 4 * group + i;
+            const bool absent = key >= present;
+            const int place = absent || LIST ? 0 : places[key];
 #pragma unroll
-        for (int ks = 0; ks < AHEAD; ++ks) k[ks] = read_key(ks);
+            for (int rb = 0; rb < C::RW; ++rb)
+              if (absent || (!LIST && place > t[rb])) s[kb][rb][i] = -__builtin_inff();
+          }
+        };
+        auto weight = [&](int kb, int rb, int i) { p[rb][i] = exp2f_fast(fmaf(s[kb][rb][i], a.scale_log2, -shift[rb])); };
+        auto put = [&](int kb, int rb) {
+          top[rb] = fmaxf(fmaxf(fmaxf(top[rb], s[kb][rb][0]), fmaxf(s[kb][rb][1], s[kb][rb][2])), s[kb][rb][3]);
+          part[rb] += (p[rb][0] + p[rb][1]) + (p[rb][2] + p[rb][3]);
+          // row r: 16-byte chunks, each with a lane group's 8 keys of a contraction of 32 in the order of
+          // lds_read_cols
+          const int r = wrow + rb * 16 + col, b16 = key0 / 16 + kb, chunk = (b16 >> 1) * 4 + group;
+          const uint32_t at = lds0 + C::P + r * 128 + ((chunk ^ (r & 7)) << 4) + (b16 & 1) * 8;
+          typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+          *(KPOOL_LDS u32x2 *)(uintptr_t)at = u32x2{pack_bf16(p[rb][0], p[rb][1]), pack_bf16(p[rb][2], p[rb][3])};
+        };
+        auto weights = [&](int kb) {
 #pragma unroll
-        for (int ks = 0; ks < C::KS; ks += 2) {
+          for (int rb = 0; rb < C::RW; ++rb) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) weight(kb, rb, i);
+            put(kb, rb);
+          }
+        };
+        auto read_key = [&](int n) {  // block n / KS, step n % KS
+          const int ks = n % C::KS, kb = n / C::KS;
+          return ks < NB * 4 ? lds_read((krow ^ ((ks & 3) << 6)) + (tile0 + (ks >> 2) * C::BLOCKB + kb * 16 * 256))
+                             : lds_read((kpe ^ ((ks & 1) << 6)) + (tile0 + NB * C::BLOCKB + kb * 16 * 128));
+        };
+        constexpr int STEPS = C::KS * C::KW, AHEAD = 4;
+        static_assert(C::KS == LOADS, "a load for every step of a block");
+        bf16x8 k[STEPS];
+#pragma unroll
+        for (int n = 0; n < AHEAD; ++n) k[n] = read_key(n);
+#pragma unroll
+        for (int n = 0; n < STEPS; ++n) {
+          const int ks = n % C::KS, kb = n / C::KS;
           __builtin_amdgcn_sched_barrier(0);
-          if (ks + 2 < LOADS) read_rows(next, ks / 2 + 1, at[(ks / 2 + 1) & 1]);
-          if (more) load_rows(next, ks / 2, at[(ks / 2) & 1]);
+          if (n % C::KW == 0 && more) load_row(n / C::KW, at[n / C::KW], to);
+          if (n + AHEAD < STEPS) k[n + AHEAD] = read_key(n + AHEAD);
+          if (ks == 0)
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
-            if (ks + AHEAD + u < C::KS) k[ks + AHEAD + u] = read_key(ks + AHEAD + u);
+            for (int rb = 0; rb < C::RW; ++rb) s[kb][rb] = f32x4{};
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb) s[rb] = mfma(k[ks + u], q[rb][ks + u], s[rb]);
+          for (int rb = 0; rb < C::RW; ++rb) s[kb][rb] = mfma(k[n], q[rb][ks], s[kb][rb]);
+          static_assert(4 * C::RW + 1 < C::KS, "a value a step, from step 1 on");
+          if (kb > 0 && ks == 1) mask(kb - 1);
+          if (kb > 0 && ks >= 1 && ks < 1 + 4 * C::RW) weight(kb - 1, (ks - 1) / 4, (ks - 1) % 4);
+          if (kb > 0 && ks >= 5 && (ks - 5) % 4 == 0 && (ks - 5) / 4 < C::RW) put(kb - 1, (ks - 5) / 4);
         }
         __builtin_amdgcn_sched_barrier(0);
-        // what a row does not see
-        const int key = j * BK + wave * 16 + 4 * group;
-        const int last = places[min(present, j * BK + BK) - 1];
-        if (j * BK + BK > present || (!LIST && last > t0)) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool absent = key + i >= present;
-            const int p = absent || LIST ? 0 : places[key + i];
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb)
-              if (absent || (!LIST && p > t[rb])) s[rb][i] = -__builtin_inff();
-          }
-        }
-        // the tile's maximum of a row
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-          const Pair x = row_pair(fmaxf(fmaxf(s[rb][0], s[rb][1]), fmaxf(s[rb][2], s[rb][3])));
-          float y = fmaxf(x.a, x.b);
-          y = fmaxf(y, other_half(y));
-          if (lane < 16) top_of[wave * BQ + rb * 16 + col] = y;
-        }
-        __builtin_amdgcn_s_waitcnt(0xC07F);
-        barrier_only();
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-          const float *x = top_of + rb * 16 + col;
-          const float top = fmaxf(fmaxf(x[0], x[BQ]), fmaxf(x[2 * BQ], x[3 * BQ])) * a.scale_log2;
-          if (__any(top > m[rb] + 8.0f)) {  // (the same in every wave)
-            const float up = fmaxf(top, m[rb]);
-            const float f = up > m[rb] ? exp2f_fast(m[rb] - up) : 1.0f;
-            m[rb] = up;
-            l[rb] *= f;
-#pragma unroll
-            for (int c = 0; c < C::CB; ++c) o[c][rb] *= f;
-          }
-          const float shift = m[rb] > -__builtin_inff() ? m[rb] : 0.0f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            s[rb][i] = exp2f_fast(fmaf(s[rb][i], a.scale_log2, -shift));
-            l[rb] += s[rb][i];
-          }
-          // P of row rb * 16 + col: 16-byte chunks, each with a lane group's 8 keys of a contraction of
-          // 32 in the order of lds_read_cols
-          const int r = rb * 16 + col, chunk = (wave >> 1) * 4 + group;
-          const uint32_t at = lds0 + C::PBUF + r * 128 + ((chunk ^ (r & 7)) << 4) + (wave & 1) * 8;
-          typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-          *(KPOOL_LDS u32x2 *)(uintptr_t)at = u32x2{pack_bf16(s[rb][0], s[rb][1]), pack_bf16(s[rb][2], s[rb][3])};
-        }
-        __builtin_amdgcn_s_waitcnt(0xC07F);
-        barrier_only();
-        // O
+        // the first columns of values do not wait for P
         auto read_value = [&](int i) {  // columns i % CB of the wave's, keys 32 (i / CB) ..
           const int c = wave * C::CB + i % C::CB;
           const uint32_t at = (vcol ^ ((c & 7) << 5)) + (tile0 + (c >> 3) * C::BLOCKB + i / C::CB * 32 * 256);
           return lds_read_cols(at, at + 16 * 256);
         };
-        bf16x8 v[2 * C::CB], p[RB];
+        constexpr int VALUES = 2 * C::CB, VAHEAD = VALUES < 6 ? VALUES : 6;
+        bf16x8 v[VALUES], pf[2][RB];
+        mask(C::KW - 1);
+        weights(C::KW - 1);
+        bool over = false;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = read_value(i);
+        for (int rb = 0; rb < C::RW; ++rb) over |= top[rb] * a.scale_log2 > own(rb) + 8.0f;  // (m = -inf: any visible key)
+        const bool any_over = __any(over);
+        if (lane == 0) list[wave] = any_over;
+        wait_reads();
+        barrier_only();
+        const int4 flags = *reinterpret_cast<const int4 *>(list);
 #pragma unroll
-        for (int i = 0; i < 2 * C::CB; ++i) {
-          if (i % 2 == 0) {
-            __builtin_amdgcn_sched_barrier(0);
-            if (i + 4 < 2 * C::CB) v[i + 4] = read_value(i + 4), v[i + 5] = read_value(i + 5);
+        for (int i = 0; i < VAHEAD; ++i) v[i] = read_value(i);
+        if (__builtin_amdgcn_readfirstlane(flags.x | flags.y | flags.z | flags.w)) {
+          // (the maxima go where P is, which is written anew)
+#pragma unroll
+          for (int rb = 0; rb < C::RW; ++rb) {
+            const Pair x = row_pair(top[rb]);
+            float y = fmaxf(x.a, x.b);
+            y = fmaxf(y, other_half(y));
+            if (lane < 16) exchange[wave / C::RG * BQ + wrow + rb * 16 + col] = y;
           }
-          if (i % C::CB == 0) {
+          wait_reads();
+          barrier_only();
 #pragma unroll
-            for (int rb = 0; rb < RB; ++rb) {
-              const int r = rb * 16 + col;
-              p[rb] = lds_read(lds0 + C::PBUF + r * 128 + (((i / C::CB * 4 + group) ^ (r & 7)) << 4));
+          for (int rb = 0; rb < RB; ++rb) {
+            float most = exchange[rb * 16 + col];
+#pragma unroll
+            for (int g = 1; g < C::KG; ++g) most = fmaxf(most, exchange[g * BQ + rb * 16 + col]);
+            most *= a.scale_log2;
+            if (most > m[rb] + 8.0f) {  // (the same in every wave)
+              const float f = exp2f_fast(m[rb] - most);  // m = -inf gives 0
+              m[rb] = most;
+#pragma unroll
+              for (int b = 0; b < C::RW; ++b)
+                if (wrow + b * 16 == rb * 16) l[b] *= f;
+#pragma unroll
+              for (int c = 0; c < C::CB; ++c) o[c][rb] *= f;
             }
           }
+          wait_reads();
+          barrier_only();
+          shifts();
 #pragma unroll
-          for (int rb = 0; rb < RB; ++rb) o[i % C::CB][rb] = mfma(v[i], p[rb], o[i % C::CB][rb]);
+          for (int rb = 0; rb < C::RW; ++rb) part[rb] = 0.0f;
+#pragma unroll
+          for (int kb = 0; kb < C::KW; ++kb) weights(kb);
+          wait_reads();
+          barrier_only();
+        }
+#pragma unroll
+        for (int rb = 0; rb < C::RW; ++rb) l[rb] += part[rb];
+        // O
+#pragma unroll
+        for (int kc = 0; kc < 2; ++kc)
+#pragma unroll
+          for (int rb = 0; rb < RB; ++rb) {
+            const int r = rb * 16 + col;
+            pf[kc][rb] = lds_read(lds0 + C::P + r * 128 + (((kc * 4 + group) ^ (r & 7)) << 4));
+          }
+#pragma unroll
+        for (int i = 0; i < VALUES; ++i) {
+          __builtin_amdgcn_sched_barrier(0);
+          if (i + VAHEAD < VALUES) v[i + VAHEAD] = read_value(i + VAHEAD);
+#pragma unroll
+          for (int rb = 0; rb < RB; ++rb) o[i % C::CB][rb] = mfma(v[i], pf[i / C::CB][rb], o[i % C::CB][rb]);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -422,11 +510,11 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     // l of a row over the lane groups and waves
     __syncthreads();
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
+    for (int rb = 0; rb < C::RW; ++rb) {
       const Pair x = row_pair(l[rb]);
       float y = x.a + x.b;
       y += other_half(y);
-      if (lane < 16) top_of[wave * BQ + rb * 16 + col] = y;
+      if (lane < 16) exchange[wave / C::RG * BQ + wrow + rb * 16 + col] = y;
     }
     __syncthreads();
     const bool whole = k1 - k0 == kt;
@@ -434,23 +522,30 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
       const int r = rb * 16 + col;
-      if (r >= nrows) continue;
-      const float *x = top_of + r;
-      const float sum = (x[0] + x[BQ]) + (x[2 * BQ] + x[3 * BQ]);
+      float sum = exchange[r];
+#pragma unroll
+      for (int g = 1; g < C::KG; ++g) sum += exchange[g * BQ + r];
       // (0 where the row saw nothing; NaN goes through)
       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
       const float lse = sum == 0.0f ? -__builtin_inff() : (m[rb] + log2f(sum)) * kLn2;
 #pragma unroll
-      for (int c = 0; c < C::CB; ++c) {
-        const int d = (wave * C::CB + c) * 16 + group * 4;
-        if (d >= a.R) continue;
-        const f32x4 y = o[c][rb] * inv;
-        if (whole)
-          *reinterpret_cast<uint2 *>(a.o + (row0 + r) * a.R + d) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
-        else
-          *reinterpret_cast<f32x4 *>(a.part_o + ((int64_t)slot * BQ + r) * a.R + d) = y;
+      for (int c = 0; c < C::CB; c += 2) {
+        const int d = (wave * C::CB + c) * 16;
+        const f32x4 y0 = o[c][rb] * inv, y1 = o[c + 1][rb] * inv;
+        if (whole) {
+          // lane groups exchange halves: groups 0 and 2 take 8 columns each of the first block, 1 and 3 of
+          // the second
+          const auto x = __builtin_amdgcn_permlane16_swap(pack_bf16(y0[0], y0[1]), pack_bf16(y1[0], y1[1]), false, false);
+          const auto z = __builtin_amdgcn_permlane16_swap(pack_bf16(y0[2], y0[3]), pack_bf16(y1[2], y1[3]), false, false);
+          const int to = d + (group & 1) * 16 + (group >> 1) * 8;
+          if (r < nrows && to < a.R) *reinterpret_cast<uint4 *>(a.o + (row0 + r) * a.R + to) = make_uint4(x[0], z[0], x[1], z[1]);
+        } else if (r < nrows) {
+          float *to = a.part_o + ((int64_t)slot * BQ + r) * a.R + d + group * 4;
+          if (d + group * 4 < a.R) *reinterpret_cast<f32x4 *>(to) = y0;
+          if (d + 16 + group * 4 < a.R) *reinterpret_cast<f32x4 *>(to + 16) = y1;
+        }
       }
-      if (wave == 0 && group == 0) {
+      if (wave == 0 && group == 0 && r < nrows) {
         if (!whole) a.part_lse[(int64_t)slot * BQ + r] = lse;
         else if (a.lse) a.lse[row0 + r] = lse;
       }
@@ -508,8 +603,8 @@ __global__ __launch_bounds__(256) void latent_join_kernel(LatentArgs a, int BQ) 
 
 template <int NB, int RB, bool LIST>
 hipError_t launch_latent_t(const LatentArgs &a, hipStream_t st) {
-  using C = Latent<NB, RB>;
-  hipLaunchKernelGGL((latent_kernel<NB, RB, LIST>), dim3(a.shares), dim3(256), C::LDS, st, a);
+  using C = Latent<NB, RB, LIST>;
+  hipLaunchKernelGGL((latent_kernel<NB, RB, LIST>), dim3((a.shares + 7) / 8 * 8), dim3(256), C::LDS, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.shares == 1) return e;
   hipLaunchKernelGGL(latent_join_kernel, dim3(a.shares * C::BQ), dim3(256), 0, st, a, C::BQ);
@@ -569,6 +664,7 @@ hipError_t launch_latent(const LatentCall &c, const LatentPlan &p, void *workspa
   a.nseq = c.nseq, a.H = c.H, a.R = c.R, a.P = c.P, a.width = c.width;
   a.scale_log2 = c.scale * kLog2e;
   a.shares = p.shares, a.units = (int)p.units, a.hblocks = (c.H + 16 * p.rb - 1) / (16 * p.rb);
+  a.by_place = c.ids && p.units >= kMostShares;
   a.o = c.o, a.lse = c.lse;
   if (p.shares > 1) {
     a.cut = (LatentCut *)workspace;
