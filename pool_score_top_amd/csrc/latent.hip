@@ -26,6 +26,8 @@
 // the lengths, which are on the device (a captured decoding step replays while its lengths grow), so each
 // workgroup finds its share itself.  A unit (rows of one tile) that lies across shares leaves a
 // part each in fp32; a second kernel joins them in order.
+#include <type_traits>
+
 #include "attend_tile.h"
 
 namespace kpool {
@@ -193,11 +195,13 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     for (int n = 0; n < LOADS; ++n)
       at[n] = *(KPOOL_LDS const uint32_t *)(uintptr_t)(n < 4 * NB ? r + n * 16 : pe + (n - 4 * NB) * 32);
   };
-  auto load_row = [&](int n, uint32_t at, uint32_t to) {  // to: the tile's buffer
+  auto address = [&](int n, uint32_t row) {
     uint32_t off = pcol;
     if (n < 4 * NB) off = min(lchunk ^ (uint32_t)Keys16<128>::swz(n % 4 * 4), last_chunk) * 16;
-    load_lds_16((const char *)a.cache + (uint64_t)at * pitch + off,
-                to + (n < 4 * NB ? (wave * 4 * NB + n) * 1024 : NB * C::BLOCKB + (wave * 2 + n - 4 * NB) * 1024));
+    return (const char *)a.cache + (uint64_t)row * pitch + off;
+  };
+  auto load_row = [&](int n, const char *from, uint32_t to) {  // to: the tile's buffer
+    load_lds_16(from, to + (n < 4 * NB ? (wave * 4 * NB + n) * 1024 : NB * C::BLOCKB + (wave * 2 + n - 4 * NB) * 1024));
   };
   int *list = reinterpret_cast<int *>(lds + C::ROWS), *places = reinterpret_cast<int *>(lds + C::PLACES);
   float *exchange = reinterpret_cast<float *>(lds + C::P);  // [4][BQ]
@@ -341,7 +345,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
       if (ntile > 0) {
         read_rows(0, at);
 #pragma unroll
-        for (int n = 0; n < LOADS; ++n) load_row(n, at[n], lds0);
+        for (int n = 0; n < LOADS; ++n) load_row(n, address(n, at[n]), lds0);
       }
       for (int j = 0; j < ntile; ++j) {
         const uint32_t tile0 = lds0 + (j & 1) * TILE;
@@ -409,26 +413,43 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         };
         constexpr int STEPS = C::KS * C::KW, AHEAD = 4;
         static_assert(C::KS == LOADS, "a load for every step of a block");
-        bf16x8 k[STEPS];
+        auto scores = [&](auto loads) {
+          bf16x8 k[STEPS];
 #pragma unroll
-        for (int n = 0; n < AHEAD; ++n) k[n] = read_key(n);
+          for (int n = 0; n < AHEAD; ++n) k[n] = read_key(n);
+          // (a matrix instruction takes 16 cycles, of which 12 are left for others: more than one or two
+          // between it and the next would hold that up)
+          const char *from = nullptr;
 #pragma unroll
-        for (int n = 0; n < STEPS; ++n) {
-          const int ks = n % C::KS, kb = n / C::KS;
+          for (int n = 0; n < STEPS; ++n) {
+            const int ks = n % C::KS, kb = n / C::KS;
+            const bool weighs = kb > 0 && ks >= 1 && ks < 1 + 4 * C::RW;
+            const int wr = (ks - 1) / 4, wi = (ks - 1) % 4;
+            float x = 0.0f;
+#pragma unroll
+            for (int rb = 0; rb < C::RW; ++rb) {
+              __builtin_amdgcn_sched_barrier(0);
+              s[kb][rb] = mfma(k[n], q[rb][ks], ks == 0 ? f32x4{} : s[kb][rb]);
+              __builtin_amdgcn_sched_barrier(0);
+              if (rb == 0) {
+                if (kb > 0 && ks == 1) mask(kb - 1);
+                if (decltype(loads)::value && n % C::KW == 0) from = address(n / C::KW, at[n / C::KW]);
+                if (weighs) x = fmaf(s[kb - 1][wr][wi], a.scale_log2, -shift[wr]);
+                if (C::RW > 1) __builtin_amdgcn_sched_barrier(0);
+              }
+              if (rb == C::RW - 1) {
+                if (decltype(loads)::value && n % C::KW == C::KW - 1) load_row(n / C::KW, from, to);
+                if (n + AHEAD < STEPS) k[n + AHEAD] = read_key(n + AHEAD);
+                if (weighs) p[wr][wi] = exp2f_fast(x);
+                static_assert(4 * C::RW + 1 < C::KS, "a value a step, from step 1 on");
+                if (kb > 0 && ks >= 5 && (ks - 5) % 4 == 0 && (ks - 5) / 4 < C::RW) put(kb - 1, (ks - 5) / 4);
+              }
+            }
+          }
           __builtin_amdgcn_sched_barrier(0);
-          if (n % C::KW == 0 && more) load_row(n / C::KW, at[n / C::KW], to);
-          if (n + AHEAD < STEPS) k[n + AHEAD] = read_key(n + AHEAD);
-          if (ks == 0)
-#pragma unroll
-            for (int rb = 0; rb < C::RW; ++rb) s[kb][rb] = f32x4{};
-#pragma unroll
-          for (int rb = 0; rb < C::RW; ++rb) s[kb][rb] = mfma(k[n], q[rb][ks], s[kb][rb]);
-          static_assert(4 * C::RW + 1 < C::KS, "a value a step, from step 1 on");
-          if (kb > 0 && ks == 1) mask(kb - 1);
-          if (kb > 0 && ks >= 1 && ks < 1 + 4 * C::RW) weight(kb - 1, (ks - 1) / 4, (ks - 1) % 4);
-          if (kb > 0 && ks >= 5 && (ks - 5) % 4 == 0 && (ks - 5) / 4 < C::RW) put(kb - 1, (ks - 5) / 4);
-        }
-        __builtin_amdgcn_sched_barrier(0);
+        };
+        if (more) scores(std::true_type{});
+        else scores(std::false_type{});
         // the first columns of values do not wait for P
         auto read_value = [&](int i) {  // columns i % CB of the wave's, keys 32 (i / CB) ..
           const int c = wave * C::CB + i % C::CB;
@@ -437,6 +458,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         };
         constexpr int VALUES = 2 * C::CB, VAHEAD = VALUES < 6 ? VALUES : 6;
         bf16x8 v[VALUES], pf[2][RB];
+#pragma unroll
+        for (int i = 0; i < VAHEAD; ++i) v[i] = read_value(i);
+        __builtin_amdgcn_sched_barrier(0);
         mask(C::KW - 1);
         weights(C::KW - 1);
         bool over = false;
@@ -447,8 +471,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         wait_reads();
         barrier_only();
         const int4 flags = *reinterpret_cast<const int4 *>(list);
+        auto read_p = [&](int kc, int rb) {
+          const int r = rb * 16 + col;
+          pf[kc][rb] = lds_read(lds0 + C::P + r * 128 + (((kc * 4 + group) ^ (r & 7)) << 4));
+        };
 #pragma unroll
-        for (int i = 0; i < VAHEAD; ++i) v[i] = read_value(i);
+        for (int rb = 0; rb < RB; ++rb) read_p(0, rb);
         if (__builtin_amdgcn_readfirstlane(flags.x | flags.y | flags.z | flags.w)) {
           // (the maxima go where P is, which is written anew)
 #pragma unroll
@@ -485,23 +513,22 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
           for (int kb = 0; kb < C::KW; ++kb) weights(kb);
           wait_reads();
           barrier_only();
+#pragma unroll
+          for (int rb = 0; rb < RB; ++rb) read_p(0, rb);
         }
 #pragma unroll
         for (int rb = 0; rb < C::RW; ++rb) l[rb] += part[rb];
         // O
 #pragma unroll
-        for (int kc = 0; kc < 2; ++kc)
+        for (int i = 0; i < VALUES; ++i) {
 #pragma unroll
           for (int rb = 0; rb < RB; ++rb) {
-            const int r = rb * 16 + col;
-            pf[kc][rb] = lds_read(lds0 + C::P + r * 128 + (((kc * 4 + group) ^ (r & 7)) << 4));
+            __builtin_amdgcn_sched_barrier(0);
+            o[i % C::CB][rb] = mfma(v[i], pf[i / C::CB][rb], o[i % C::CB][rb]);
+            __builtin_amdgcn_sched_barrier(0);
+            if (rb == 0 && i + VAHEAD < VALUES) v[i + VAHEAD] = read_value(i + VAHEAD);
+            if (i == 1) read_p(1, rb);
           }
-#pragma unroll
-        for (int i = 0; i < VALUES; ++i) {
-          __builtin_amdgcn_sched_barrier(0);
-          if (i + VAHEAD < VALUES) v[i + VAHEAD] = read_value(i + VAHEAD);
-#pragma unroll
-          for (int rb = 0; rb < RB; ++rb) o[i % C::CB][rb] = mfma(v[i], pf[i / C::CB][rb], o[i % C::CB][rb]);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
