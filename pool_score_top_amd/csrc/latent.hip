@@ -40,7 +40,6 @@ struct LatentArgs {
   int64_t qs, cs, nrows;  // elements between tokens, between cache rows; cache rows
   const int32_t *table, *starts, *lens, *cu_q, *ids;
   int per_seq, page, npages, max_len;
-  bool by_place;  // lists: ordered by place in the sequence
   int nseq, H, R, P, width;
   float scale_log2;
   int shares, hblocks, units;  // most shares; lists: units of a token, of the call
@@ -71,14 +70,14 @@ struct Latent {
   static constexpr int CB = NB * 2;                 // 16-column blocks of a wave
   static constexpr int BLOCKB = BK * 256;           // bytes of 128 columns of a tile
   static constexpr int TILE = NB * BLOCKB + BK * 128;
-  static constexpr int EACH = LIST ? 8 : 4, BLOCK = EACH * 256, GROUPS = 16;
+  static constexpr int EACH = LIST ? 8 : 4, BLOCK = EACH * 256;
   // P; the rows of a block's keys, and, whole keys, their places.  What is used between tiles only
-  // lies in the tiles (a block's counts, the queries on their way to registers) or in P (exchanges of
+  // lies in the tiles (counts, the queries on their way to registers) or in P (exchanges of
   // maxima and sums), and a tile's four flags where the first keys of the list were, which are loaded.
   static constexpr int P = 2 * TILE, ROWS = P + BQ * BK * 2, PLACES = ROWS + BLOCK * 4,
                        LDS = PLACES + (LIST ? 0 : BLOCK * 4);
   static constexpr int QROW = KS * 64 + 16;  // bytes of a row of queries in LDS (16 rows over all banks)
-  static_assert(LDS <= 163840 && BQ * QROW <= 2 * TILE && GROUPS * 512 <= 2 * TILE && 4 * BQ * 4 <= BQ * BK * 2, "LDS");
+  static_assert(LDS <= 163840 && BQ * QROW <= 2 * TILE && 4 * BQ * 4 <= BQ * BK * 2, "LDS");
 };
 
 // n tokens of a sequence, at most what the caller said and what its pages hold
@@ -125,17 +124,18 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
   const uint32_t lds0 = lds_offset(lds);
 
   // this workgroup's share of all tiles: [pos, hi), from sequence `seq` on, whose tiles begin at `before`
-  int total = 0, before, seq;
+  int total = 0, before, seq, mine = 0, upto = 0;  // (upto: tiles up to and with the thread's sequence, mine of them its own)
   const int list_tiles = LIST ? tiles_of(a.width) : 0;
   int *scratch = reinterpret_cast<int *>(lds);
   if (LIST) {
     total = a.units * list_tiles;
   } else {
     for (int base = 0; base < a.nseq; base += 256) {
-      const int x = scan_256(seq_tiles(a, base + threadIdx.x, BQ), scratch);
-      if (threadIdx.x == 255) scratch[4] = x;
+      mine = seq_tiles(a, base + threadIdx.x, BQ);
+      upto = total + scan_256(mine, scratch);
+      if (threadIdx.x == 255) scratch[4] = upto;
       __syncthreads();
-      total += scratch[4];
+      total = scratch[4];
     }
   }
   total = __builtin_amdgcn_readfirstlane(total);
@@ -156,12 +156,13 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     }
     before = a.cu_q[seq] * a.hblocks * list_tiles;
   } else {
-    int run = 0;
-    for (int base = 0; base < a.nseq; base += 256) {
-      const int mine = seq_tiles(a, base + threadIdx.x, BQ);
-      const int x = run + scan_256(mine, scratch);
-      if (x - mine <= pos && pos < x) scratch[5] = x - mine, scratch[6] = base + threadIdx.x;
-      if (threadIdx.x == 255) scratch[4] = x;
+    for (int base = 0, run = 0; base < a.nseq; base += 256) {
+      if (a.nseq > 256) {  // (otherwise they are as they were)
+        mine = seq_tiles(a, base + threadIdx.x, BQ);
+        upto = run + scan_256(mine, scratch);
+        if (threadIdx.x == 255) scratch[4] = upto;
+      }
+      if (upto - mine <= pos && pos < upto) scratch[5] = upto - mine, scratch[6] = base + threadIdx.x;
       __syncthreads();
       run = scratch[4];
     }
@@ -287,13 +288,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
       const float first = m[rb], other = m[RB - C::RW + rb];
       return wrow == 0 ? first : other;
     };
-    // group of a token in the order of a block: by the top 4 bits of its place, or one for all
-    const int shift = LIST && a.by_place ? max(0, 28 - __clz(max(len - 1, 1))) : 31;
-    const int ngroups = LIST && a.by_place ? C::GROUPS : 1;
 
     for (int block = e_lo; block < e_hi; block += C::BLOCK) {
-      // the block's keys that exist: their rows (and places) in LDS by group, thread and place in the
-      // list.  Each thread counts its own, the counts are summed, each takes places from its starts on.
+      // the block's keys that exist, in order: their rows (and places) in LDS
       if (block > e_lo) look_up(block);
       int row[C::EACH];
 #pragma unroll
@@ -307,33 +304,20 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         }
       }
       __syncthreads();  // (nobody reads the last block's list or tiles, or the queries, any more)
-      uint16_t *mine = reinterpret_cast<uint16_t *>(lds) + threadIdx.x;  // [ngroups][256]
-      for (int g = 0; g < ngroups; ++g) mine[g * 256] = 0;
-#pragma unroll
-      for (int i = 0; i < C::EACH; ++i)
-        if (row[i] >= 0) ++mine[(place[i] >> shift) * 256];
-      __syncthreads();
-      uint16_t *run = reinterpret_cast<uint16_t *>(lds) + threadIdx.x * 16;  // 16 threads' counts of a group
       int sum = 0;
-      if ((int)threadIdx.x < ngroups * 16)
-        for (int i = 0; i < 16; ++i) {
-          const int c = run[i];
-          run[i] = (uint16_t)sum;
-          sum += c;
-        }
-      int *scratch = reinterpret_cast<int *>(lds + C::GROUPS * 512);
+#pragma unroll
+      for (int i = 0; i < C::EACH; ++i) sum += row[i] >= 0;
       const int upto = scan_256(sum, scratch);
       if (threadIdx.x == 255) scratch[4] = upto;
-      if ((int)threadIdx.x < ngroups * 16)
-        for (int i = 0; i < 16; ++i) run[i] += (uint16_t)(upto - sum);
+      int to = upto - sum;
       __syncthreads();
       const int present = __builtin_amdgcn_readfirstlane(scratch[4]);
 #pragma unroll
       for (int i = 0; i < C::EACH; ++i)
         if (row[i] >= 0) {
-          const int to = mine[(place[i] >> shift) * 256]++;
           list[to] = row[i];
           if (!LIST) places[to] = place[i];
+          ++to;
         }
       __syncthreads();
       const int ntile = (present + BK - 1) / BK;
@@ -691,7 +675,6 @@ hipError_t launch_latent(const LatentCall &c, const LatentPlan &p, void *workspa
   a.nseq = c.nseq, a.H = c.H, a.R = c.R, a.P = c.P, a.width = c.width;
   a.scale_log2 = c.scale * kLog2e;
   a.shares = p.shares, a.units = (int)p.units, a.hblocks = (c.H + 16 * p.rb - 1) / (16 * p.rb);
-  a.by_place = c.ids && p.units >= kMostShares;
   a.o = c.o, a.lse = c.lse;
   if (p.shares > 1) {
     a.cut = (LatentCut *)workspace;
