@@ -311,6 +311,49 @@ int kpool_attend_selected(const uint16_t *q, int64_t q_stride, const uint16_t *k
                           int32_t Hkv, int32_t D, float scale, void *workspace,
                           size_t workspace_bytes, uint16_t *o, float *lse, void *stream);
 
+/* Latent attention with its keys and values expanded for each head - prompts and training (Atlas
+ * inference docs, glm5next_dsa/tp.rs: the shard plan's q_b_proj, kv_b_proj and kv_a_proj_with_mqa):
+ * kpool_attend with keys that have a positional part besides, P values a token that all heads share,
+ *   s[i,h,j] = scale * (<q[i,h,:D], k[j,g,:]> + <q[i,h,D:], k_pe[j,:]>)
+ *   o[i,h,:] = sum_j softmax_j(s) v[j,g,:]        lse[i,h] = log sum_j exp(s)
+ *   q        bf16, token row i at q + i * q_stride elements, its heads [Hq, D + P] contiguous
+ *   k, v     bf16, head g of token j at k + j * k_stride + g * k_head_stride (v likewise): heads may lie
+ *            side by side with the values, as one projection gives them
+ *   k_pe     bf16, token j's at k_pe + j * pe_stride
+ *   o        bf16 [Tq, Hq, D] contiguous;  lse NULLABLE fp32 [Tq, Hq]
+ * cu_q, cu_k, scale, the workspace and what holds for rows, sums, bits and overlaps are kpool_attend's.
+ * One kernel for all numbers of rows: new tokens over a cache take kpool_attend_latent.
+ * Sizes: D a multiple of 8 up to 128, P one from 8 to 64; Hq a multiple of Hkv; strides multiples of 8 up to
+ * 2^24, q's from Hq * (D + P), k's and v's from (Hkv - 1) * their head stride + D, head strides from D,
+ * pe_stride from P; q, k, k_pe, v, o and the workspace 16-byte aligned. */
+size_t kpool_attend_expanded_workspace_bytes(const int32_t *cu_q_host, const int32_t *cu_k_host,
+                                             int32_t nseq, int32_t Hq, int32_t Hkv, int32_t D, int32_t P);
+int kpool_attend_expanded(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                          int64_t k_head_stride, const uint16_t *k_pe, int64_t pe_stride,
+                          const uint16_t *v, int64_t v_stride, int64_t v_head_stride,
+                          const int32_t *cu_q_host, const int32_t *cu_q_dev, const int32_t *cu_k_host,
+                          const int32_t *cu_k_dev, int32_t nseq, int32_t Hq, int32_t Hkv, int32_t D,
+                          int32_t P, float scale, void *workspace, size_t workspace_bytes, uint16_t *o,
+                          float *lse, void *stream);
+
+/* Its gradients, by kpool_attend_backward's formulas: dq [Tq, Hq, D + P], dk and dv [Tk, Hkv, D] and
+ *   dk_pe[j] = scale * sum_h sum_i dS[i,h,j] q[i,h,D:]        [Tk, P]
+ * summed over all query heads in fp32; all bf16, contiguous, overwritten (0 for a row that sees nothing and a
+ * key that no row sees).  d_o and o bf16 [Tq, Hq, D] and lse fp32 [Tq, Hq] contiguous; the other arguments
+ * are the forward call's, and what holds for kpool_attend_backward holds here. */
+size_t kpool_attend_expanded_backward_workspace_bytes(const int32_t *cu_q_host, const int32_t *cu_k_host,
+                                                      int32_t nseq, int32_t Hq, int32_t Hkv, int32_t D,
+                                                      int32_t P);
+int kpool_attend_expanded_backward(const uint16_t *d_o, const uint16_t *q, int64_t q_stride,
+                                   const uint16_t *k, int64_t k_stride, int64_t k_head_stride,
+                                   const uint16_t *k_pe, int64_t pe_stride, const uint16_t *v,
+                                   int64_t v_stride, int64_t v_head_stride, const uint16_t *o,
+                                   const float *lse, const int32_t *cu_q_host, const int32_t *cu_q_dev,
+                                   const int32_t *cu_k_host, const int32_t *cu_k_dev, int32_t nseq,
+                                   int32_t Hq, int32_t Hkv, int32_t D, int32_t P, float scale,
+                                   void *workspace, size_t workspace_bytes, uint16_t *dq, uint16_t *dk,
+                                   uint16_t *dk_pe, uint16_t *dv, void *stream);
+
 /* Latent attention over a cache - the absorbed form (Atlas inference docs, glm5next_dsa/tp.rs: the
  * shard plan's kv_a_proj_with_mqa and kv_b_proj): one row of R + P values a token is the key of every
  * head, its first R values are the value.  For token row i of sequence s and head h

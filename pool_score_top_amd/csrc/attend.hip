@@ -46,14 +46,20 @@ struct AttendArgs {
   float *part_o, *part_lse;  // [nsplit][Tq * Hq][D], [nsplit][Tq * Hq]
   int64_t rows;              // Tq * Hq
   TileTable table;
+  // expanded latent attention: the keys' positional part, the heads' strides, a query head's values
+  const uint16_t *pe;
+  int64_t pes, kh, vh;
+  int P, QD;
 };
 
-// One wave's 32 query rows: fragments, running softmax and output.
-template <int DP>
+// One wave's 32 query rows: fragments, running softmax and output.  PP: values of the keys' and queries'
+// positional part, which has no values beside it (0 for none).
+template <int DP, int PP = 0>
 struct Rows {
   using S = Keys<DP>;
+  static constexpr int PS = PP / 16;  // contraction steps over it
   static constexpr int ROWS = 32, VALUES = 16;  // of a fragment of o: its rows, a lane's values
-  bf16x8 q[S::KS];
+  bf16x8 q[S::KS + PS];
   f32x16 o[S::DT];
   float m, l;  // base 2; l is this lane half's part
 
@@ -64,8 +70,15 @@ struct Rows {
   // the row's sum over its lanes
   __device__ inline float sum() const { return l + other_half(l); }
 
-  // row: this lane's query (l % 32), null for none
-  __device__ inline void init(const uint16_t *row, int D, int lane) {
+  // row: this lane's query (l % 32), null for none; P: its positional values, behind the D others
+  __device__ inline void init(const uint16_t *row, int D, int lane, int P = 0) {
+#pragma unroll
+    for (int ks = 0; ks < PS; ++ks) {
+      const int d = ks * 16 + (lane >> 5) * 8;
+      uint4 z = make_uint4(0, 0, 0, 0);
+      if (row && d < P) z = *reinterpret_cast<const uint4 *>(row + D + d);
+      q[S::KS + ks] = __builtin_bit_cast(bf16x8, z);
+    }
 #pragma unroll
     for (int ks = 0; ks < S::KS; ++ks) {
       const int d = ks * 16 + (lane >> 5) * 8;
@@ -167,6 +180,34 @@ struct Rows {
 #pragma unroll
       for (int dt = 0; dt < S::DT; ++dt) o[dt] = mfma(vr[kc][dt], w, o[dt]);
     }
+  }
+
+  // The same with the positional part, whose tile lies at sp past the addresses of `fp`.  Its products come
+  // first, and the keys' fragments are read beside them.
+  template <int BK, class F>
+  __device__ inline void add(const Frag<DP> &f, const Frag<PP> &fp, uint32_t sk, uint32_t sp, uint32_t sv, float c,
+                             int lane, bool masked, F &&visible) {
+    f32x16 s[BK / 32];
+    bf16x8 pr[BK / 32][PS];
+#pragma unroll
+    for (int sub = 0; sub < BK / 32; ++sub)
+#pragma unroll
+      for (int ks = 0; ks < PS; ++ks) pr[sub][ks] = fp.rows(sp + sub * 32 * Keys<PP>::ROWB, ks);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int sub = 0; sub < BK / 32; ++sub) {
+      bf16x8 kr[S::KS];
+#pragma unroll
+      for (int ks = 0; ks < S::KS; ++ks) kr[ks] = f.rows(sk + sub * 32 * S::ROWB, ks);
+      f32x16 t = {};
+#pragma unroll
+      for (int ks = 0; ks < PS; ++ks) t = mfma(pr[sub][ks], q[S::KS + ks], t);
+#pragma unroll
+      for (int ks = 0; ks < S::KS; ++ks) t = mfma(kr[ks], q[ks], t);
+      s[sub] = t;
+    }
+    weights(s, c, lane, masked, visible);
+    values(f, sv, s);
   }
 
   template <int BK, class F>
@@ -314,10 +355,12 @@ __device__ inline void write_row(const AttendArgs &a, bool live, int64_t row, bo
 // to their starts and ends, beside which a CU has nothing else to run.
 // Head dims above 64 run as 128: the blocks past D multiply zeros (8192 tokens, 16 heads over 2: D
 // = 64 192 us, 80 258, 96 263, 128 272).
-template <int DP, int NW>
+// With the positional part of expanded latent attention (PP = 64): its tile of 8 KiB stands behind the
+// values'.
+template <int DP, int NW, int PP>
 __global__ __launch_bounds__(NW * 64) void attend_tile_kernel(AttendArgs a) {
   using S = Keys<DP>;
-  constexpr int BK = 64, BQ = NW * 32, TILE = BK * S::ROWB;
+  constexpr int BK = 64, BQ = NW * 32, TILE = BK * S::ROWB, BUFB = 2 * TILE + BK * PP * 2;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -332,8 +375,8 @@ __global__ __launch_bounds__(NW * 64) void attend_tile_kernel(AttendArgs a) {
   const int t1 = (at.n0 + nrows - 1) / G + at.Lk - at.Lq;  // the last row's position
   const int k_lo = split * a.chunk, k_hi = (int)min64(t1 + 1, (int64_t)k_lo + a.chunk);
   if (split > 0 && k_lo >= k_hi) return;  // (the join does not read this part)
-  const uint16_t *kb = (const uint16_t *)uniform_ptr(a.k + (int64_t)at.k_start * a.ks + (int64_t)kvh * a.D);
-  const uint16_t *vb = (const uint16_t *)uniform_ptr(a.v + (int64_t)at.k_start * a.vs + (int64_t)kvh * a.D);
+  const uint16_t *kb = (const uint16_t *)uniform_ptr(a.k + (int64_t)at.k_start * a.ks + (int64_t)kvh * (PP ? a.kh : a.D));
+  const uint16_t *vb = (const uint16_t *)uniform_ptr(a.v + (int64_t)at.k_start * a.vs + (int64_t)kvh * (PP ? a.vh : a.D));
 
   const int n = at.n0 + wave * 32 + (lane & 31);
   const bool live = wave * 32 + (lane & 31) < nrows;
@@ -344,19 +387,29 @@ __global__ __launch_bounds__(NW * 64) void attend_tile_kernel(AttendArgs a) {
   const int wave_rows = min(32, nrows - wave * 32);
   const int w0 = (at.n0 + wave * 32) / G + at.Lk - at.Lq;
   const int w1 = wave_rows > 0 ? (at.n0 + wave * 32 + wave_rows - 1) / G + at.Lk - at.Lq : -1;
-  Rows<DP> r;
-  r.init(live ? a.q + ((int64_t)at.q_start + tok) * a.qs + (int64_t)head * a.D : nullptr, a.D, lane);
+  Rows<DP, PP> r;
+  r.init(live ? a.q + ((int64_t)at.q_start + tok) * a.qs + (int64_t)head * (PP ? a.QD : a.D) : nullptr, a.D, lane, a.P);
 
   const uint32_t lds0 = lds_offset(lds);
   Frag<DP> f;
   f.init(lds0, lane);
   KeyLoader<DP, BK, NW> keys;
   keys.init(wave, lane, a.D);
+  constexpr int PW = PP ? PP : 64;
+  Frag<PW> fp;
+  KeyLoader<PW, BK, NW> pes;
+  const uint16_t *pb = nullptr;
+  if constexpr (PP > 0) {
+    fp.init(lds0, lane);
+    pes.init(wave, lane, a.P);
+    pb = (const uint16_t *)uniform_ptr(a.pe + (int64_t)at.k_start * a.pes);
+  }
   const int ntile = k_hi > k_lo ? (k_hi - k_lo + BK - 1) / BK : 0;
   auto load = [&](int tile, int buf) {
     const int k0 = k_lo + tile * BK;
-    keys.load(kb + (int64_t)k0 * a.ks, a.ks, at.Lk - 1 - k0, lds0 + buf * 2 * TILE);
-    keys.load(vb + (int64_t)k0 * a.vs, a.vs, at.Lk - 1 - k0, lds0 + buf * 2 * TILE + TILE);
+    keys.load(kb + (int64_t)k0 * a.ks, a.ks, at.Lk - 1 - k0, lds0 + buf * BUFB);
+    keys.load(vb + (int64_t)k0 * a.vs, a.vs, at.Lk - 1 - k0, lds0 + buf * BUFB + TILE);
+    if constexpr (PP > 0) pes.load(pb + (int64_t)k0 * a.pes, a.pes, at.Lk - 1 - k0, lds0 + buf * BUFB + 2 * TILE);
   };
   auto step = [&](int j, auto buf_c) {
     constexpr int BUF = decltype(buf_c)::value;
@@ -366,9 +419,14 @@ __global__ __launch_bounds__(NW * 64) void attend_tile_kernel(AttendArgs a) {
     barrier_only();
     if (j + 1 < ntile) load(j + 1, BUF ^ 1);
     const int k0 = k_lo + j * BK;
-    if (k0 <= w1)  // (the whole wave; not where it sees none of the tile, or has no rows)
-      r.template add<BK>(f, BUF * 2 * TILE, BUF * 2 * TILE + TILE, a.scale_log2, lane, k0 + BK - 1 > w0,
-                         [&](int sub, int i) { return k0 + sub * 32 + i <= t; });
+    const auto visible = [&](int sub, int i) { return k0 + sub * 32 + i <= t; };
+    if (k0 <= w1) {  // (the whole wave; not where it sees none of the tile, or has no rows)
+      if constexpr (PP > 0)
+        r.template add<BK>(f, fp, BUF * BUFB, BUF * BUFB + 2 * TILE, BUF * BUFB + TILE, a.scale_log2, lane,
+                           k0 + BK - 1 > w0, visible);
+      else
+        r.template add<BK>(f, BUF * BUFB, BUF * BUFB + TILE, a.scale_log2, lane, k0 + BK - 1 > w0, visible);
+    }
   };
   wait_loads();
   if (ntile > 0) load(0, 0);
@@ -804,11 +862,22 @@ hipError_t launch_attend_t(const AttendPlan &p, const AttendArgs &a, hipStream_t
     hipLaunchKernelGGL(attend_rows_kernel<DP>, dim3(grid), dim3(256), lds, st, a);
   } else {
     constexpr size_t lds = 4 * 64 * DP * 2;
-    hipLaunchKernelGGL((attend_tile_kernel<DP, kTileWaves>), dim3(grid), dim3(kTileWaves * 64), lds, st, a);
+    hipLaunchKernelGGL((attend_tile_kernel<DP, kTileWaves, 0>), dim3(grid), dim3(kTileWaves * 64), lds, st, a);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.nsplit == 1) return e;
   if (few) return launch_join(a, st);
+  hipLaunchKernelGGL(attend_tile_join_kernel, dim3((unsigned)(a.ntiles * a.Hkv * 8)), dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
+template <int DP>
+hipError_t launch_expanded_t(const AttendArgs &a, hipStream_t st) {
+  constexpr size_t lds = 2 * 64 * (2 * DP + 64) * 2;
+  hipLaunchKernelGGL((attend_tile_kernel<DP, kTileWaves, 64>), dim3((unsigned)(a.ntiles * a.nsplit * a.Hkv)),
+                     dim3(kTileWaves * 64), lds, st, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.nsplit == 1) return e;
   hipLaunchKernelGGL(attend_tile_join_kernel, dim3((unsigned)(a.ntiles * a.Hkv * 8)), dim3(256), 0, st, a);
   return hipGetLastError();
 }
@@ -868,7 +937,7 @@ int64_t attend_threads(const AttendPlan &p, int Hq, int Hkv) {
   return std::max(units * kTileWaves * 64, join);
 }
 
-AttendPlan plan_attend(const int32_t *cu_q, const int32_t *cu_k, int nseq, int Hq, int Hkv) {
+AttendPlan plan_attend(const int32_t *cu_q, const int32_t *cu_k, int nseq, int Hq, int Hkv, bool tiles) {
   const int64_t G = Hq / Hkv;
   int64_t most_rows = 0, most_keys = 0;
   for (int s = 0; s < nseq; ++s) {
@@ -879,7 +948,8 @@ AttendPlan plan_attend(const int32_t *cu_q, const int32_t *cu_k, int nseq, int H
   // 32 virtual rows fill one wave's tile; from there on sharing key tiles among waves is as good
   // (us by the rows kernel and the tile kernel, D = 128, 4 key heads: 8 sequences of 8192 keys, 32
   // rows 27 35, 64 rows 43 38, 128 rows 56 48; one of 16384 keys, 32 rows 24 24, 64 rows 26 25)
-  p.form = most_rows <= 32 ? AttendPlan::kRows : AttendPlan::kTiles;
+  // (expanded latent attention has the tile kernel alone: its single tokens take the absorbed form)
+  p.form = most_rows <= 32 && !tiles ? AttendPlan::kRows : AttendPlan::kTiles;
   const int BQ = p.form == AttendPlan::kRows ? 32 : kTileWaves * 32;
   p.ntiles = tile_start(cu_q[nseq], nseq, (int)G, BQ);
   // workgroups, and the keys that all of them walk, without a split
@@ -923,6 +993,13 @@ AttendPlan plan_list(int64_t Tq, int nseq, int width, int Hq, int Hkv) {
 hipError_t launch_attend(const AttendCall &c, const AttendPlan &p, void *workspace, hipStream_t st) {
   const AttendArgs a = make_args(c, p, workspace);
   return c.D <= 64 ? launch_attend_t<64>(p, a, st) : launch_attend_t<128>(p, a, st);
+}
+
+hipError_t launch_attend_expanded(const AttendCall &c, const ExpandedKeys &x, const AttendPlan &p, void *workspace,
+                                  hipStream_t st) {
+  AttendArgs a = make_args(c, p, workspace);
+  a.pe = x.k_pe, a.pes = x.pe_stride, a.kh = x.k_head, a.vh = x.v_head, a.P = x.P, a.QD = c.D + x.P;
+  return c.D <= 64 ? launch_expanded_t<64>(a, st) : launch_expanded_t<128>(a, st);
 }
 
 hipError_t launch_attend_list(const AttendCall &c, const AttendPlan &p, const int32_t *ids, int width,

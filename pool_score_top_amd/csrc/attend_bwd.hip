@@ -40,6 +40,13 @@ struct BwdArgs {
   uint16_t *dq, *dk, *dv;
   float *part;          // fp32 parts, used by one kernel and its sum at a time
   TileTable table;      // of keys, or of query rows
+  // expanded latent attention: as AttendArgs has it; the keys' positional gradient by key heads in fp32,
+  // [Hkv][Tk][P], and their sum
+  const uint16_t *pe;
+  int64_t pes, kh, vh;
+  int P, QD;
+  float *pe_part;
+  uint16_t *dpe;
 };
 
 // Writes a lane's column of a transposed result x^T [DP, 32]: row `row` of out (bf16, D
@@ -62,6 +69,42 @@ __device__ inline void write_cols(const f32x16 (&x)[DP / 32], float mul, uint16_
             make_uint2(pack_bf16(x[dt][i] * mul, x[dt][i + 1] * mul),
                        pack_bf16(x[dt][i + 2] * mul, x[dt][i + 3] * mul));
     }
+}
+
+// The same for the DT blocks from column `col` on of rows of `width` columns, `end` of them in this part.
+template <int DT>
+__device__ inline void write_part(const f32x16 *x, float mul, uint16_t *out, float *part, int64_t row, int width, int col,
+                                  int end, int lane) {
+  const int h = lane >> 5;
+#pragma unroll
+  for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const int d = dt * 32 + 2 * i + 4 * h;
+      if (d >= end) continue;
+      const int64_t at = row * width + col + d;
+      if (part)
+        *reinterpret_cast<float4 *>(part + at) =
+            make_float4(x[dt][i] * mul, x[dt][i + 1] * mul, x[dt][i + 2] * mul, x[dt][i + 3] * mul);
+      else
+        *reinterpret_cast<uint2 *>(out + at) =
+            make_uint2(pack_bf16(x[dt][i] * mul, x[dt][i + 1] * mul), pack_bf16(x[dt][i + 2] * mul, x[dt][i + 3] * mul));
+    }
+}
+
+// A lane's fragments of a row of PP values in LDS rather than in registers, for itself to read again:
+// 4 KiB a wave.
+template <int PP>
+__device__ inline uint32_t stash(uint32_t lds0, const uint16_t *row, int P, int lane) {
+  const uint32_t at = lds0 + Keys<PP>::row_base(lane);
+#pragma unroll
+  for (int ks = 0; ks < PP / 16; ++ks) {
+    const int d = ks * 16 + (lane >> 5) * 8;
+    uint4 z = make_uint4(0, 0, 0, 0);
+    if (row && d < P) z = *reinterpret_cast<const uint4 *>(row + d);
+    *(KPOOL_LDS bf16x8 *)(uintptr_t)(at ^ (ks << 5)) = __builtin_bit_cast(bf16x8, z);
+  }
+  return at;
 }
 
 template <int DP>
@@ -88,14 +131,17 @@ __device__ inline void load_frag(bf16x8 (&f)[DP / 16], const uint16_t *row, int 
 // parts of at most the CUs' average the CUs had work 66% of the time (the same tokens as at dQ's
 // kernel: 330 us; by shares 254 and 13 to join, 210 GFLOP at 0.83 PFLOP/s; CUs busy 85% of the
 // time, the matrix pipe 45% of that).
-template <int DP>
+// PP = 64: with the positional part of expanded latent attention, whose 32 rows lie behind the others in
+// rows as wide as theirs, so that they share their lanes' addresses.
+template <int DP, int PP = 0>
 struct BwdKeys {
   static constexpr int BR = 32, NG = 4, KEYS = NG * 32;
-  static constexpr int TILE = BR * Keys<DP>::ROWB, BUFB = 2 * TILE;
+  static constexpr int TILE = BR * Keys<DP>::ROWB, BUFB = (PP ? 3 : 2) * TILE;
   static constexpr int AHEAD = 2, NBUF = 4;
   static constexpr int STAT = NBUF * BUFB, STATB = 256;   // lse and delta of the buffers
   static constexpr int PBUF = 32 * 32 * 4, P = STAT + NBUF * STATB;
-  static constexpr int LDS = P + 2 * NG * PBUF;
+  static constexpr int KEYS_PE = P + 2 * NG * PBUF;  // the keys' positional parts
+  static constexpr int LDS = KEYS_PE + KEYS * PP * 2;
 };
 
 // The first row of the first 32 virtual rows in which one sees a key of the tile from n0 on.
@@ -104,14 +150,15 @@ __host__ __device__ inline int64_t first_row(int64_t nvirt, int64_t Lk, int64_t 
   return min64(nvirt, (off > 0 ? off : 0) * G) / 32 * 32;
 }
 
-template <int DP>
+template <int DP, int PP>
 __global__ __launch_bounds__(512) void bwd_keys_kernel(BwdArgs a, Shares shares) {
   using S = Keys<DP>;
-  using C = BwdKeys<DP>;
+  using C = BwdKeys<DP, PP>;
   constexpr int BR = C::BR, TILE = C::TILE, BUFB = C::BUFB, NW = 8;
   constexpr int REGIONS = 2 * BR / S::REGION_ROWS;  // q's, then do's
   constexpr int PER = REGIONS / NW;                 // loads a wave
   static_assert(REGIONS % NW == 0, "whole loads a wave");
+  constexpr int PS = PP / 16, PT = PP / 32;  // the positional part's steps and blocks
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -121,6 +168,7 @@ __global__ __launch_bounds__(512) void bwd_keys_kernel(BwdArgs a, Shares shares)
   const uint32_t lds0 = lds_offset(lds);
   Frag<DP> f;
   f.init(lds0, lane);
+  const int q_width = PP ? a.QD : a.D;  // of a query head
   uint32_t st0 = lds0 + C::STAT + (lane >> 5) * 16 + (second ? 128 : 0);
   uint32_t pb = lds0 + C::P + group * C::PBUF + lane * 16;
   opaque(st0), opaque(pb);
@@ -153,11 +201,19 @@ __global__ __launch_bounds__(512) void bwd_keys_kernel(BwdArgs a, Shares shares)
     barrier_only();  // (everyone is done with the last unit's tiles)
 
     bf16x8 kv[S::KS];  // the first wave's keys, the second's values
+    uint32_t kp = 0;  // (and the first's positional ones)
     {
       const uint16_t *row = second ? a.v + ((int64_t)k_start + key) * a.vs : a.k + ((int64_t)k_start + key) * a.ks;
-      load_frag<DP>(kv, live ? row + (int64_t)kvh * a.D : nullptr, a.D, lane);
+      if constexpr (PP > 0) row += (int64_t)kvh * (second ? a.vh : a.kh);
+      else row += (int64_t)kvh * a.D;
+      load_frag<DP>(kv, live ? row : nullptr, a.D, lane);
+      if constexpr (PP > 0)
+        if (!second)
+          kp = stash<PP>(lds0 + C::KEYS_PE + group * 32 * PP * 2, live ? a.pe + ((int64_t)k_start + key) * a.pes : nullptr,
+                         a.P, lane);
     }
     f32x16 sum[S::DT];  // dV^T of the first, dK^T of the second
+    f32x16 sum_pe[PT + 1];  // (and its positional part)
   #pragma unroll
     for (int dt = 0; dt < S::DT; ++dt)
   #pragma unroll
@@ -174,15 +230,27 @@ __global__ __launch_bounds__(512) void bwd_keys_kernel(BwdArgs a, Shares shares)
     int64_t move[PER], move_over[PER];  // 32 virtual rows on, without and with a new token
   #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      move[i] = step_tok * pitch_of(i) + step_g * a.D;
-      move_over[i] = move[i] + pitch_of(i) - (int64_t)G * a.D;
+      const int width = wave + i * NW >= REGIONS / 2 ? a.D : q_width;
+      move[i] = step_tok * pitch_of(i) + step_g * width;
+      move_over[i] = move[i] + pitch_of(i) - (int64_t)G * width;
     }
     auto address = [&](int i, int n) {  // of the lane's 16 bytes of virtual row n
       const int row = row_of(i);
       const int chunk = min((lane & (DP / 8 - 1)) ^ S::swz(row), a.D / 8 - 1);
       const uint16_t *p = wave + i * NW >= REGIONS / 2 ? a.d_o : a.q;
       const int tok = n / G;
-      return p + (q_start + tok) * pitch_of(i) + (int64_t)(kvh * G + n - tok * G) * a.D + chunk * 8;
+      const int width = wave + i * NW >= REGIONS / 2 ? a.D : q_width;
+      return p + (q_start + tok) * pitch_of(i) + (int64_t)(kvh * G + n - tok * G) * width + chunk * 8;
+    };
+    // the positional part's load goes with the wave's first one, of the same row (a wave whose loads are
+    // all do's repeats one of them, so that all waves' loads count the same)
+    int pe_off = 0;
+    if (PP && wave < REGIONS / 2) {
+      const int chunk = (lane & (DP / 8 - 1)) ^ S::swz(row_of(0));
+      pe_off = a.D + (min(chunk, a.P / 8 - 1) - min(chunk, a.D / 8 - 1)) * 8;
+    }
+    auto load_pe = [&](const uint16_t *first, int buf) {
+      load_lds_16(first + pe_off, lds0 + buf * BUFB + (wave < REGIONS / 2 ? 2 * TILE : 0) + wave * 1024);
     };
   #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -195,6 +263,7 @@ __global__ __launch_bounds__(512) void bwd_keys_kernel(BwdArgs a, Shares shares)
       const uint32_t to = lds0 + buf * BUFB + wave * 1024;
       const int n0 = n_lo + tile * BR;
       if (n0 + BR <= nvirt) {
+        if constexpr (PP > 0) load_pe(src[0], buf);
   #pragma unroll
         for (int i = 0; i < PER; ++i) {
           load_lds_16(src[i], to + i * NW * 1024);
@@ -207,6 +276,7 @@ __global__ __launch_bounds__(512) void bwd_keys_kernel(BwdArgs a, Shares shares)
   #pragma unroll
         for (int i = 0; i < PER; ++i)
           load_lds_16(address(i, min(n0 + row_of(i), nvirt - 1)), to + i * NW * 1024);
+        if constexpr (PP > 0) load_pe(address(0, min(n0 + row_of(0), nvirt - 1)), buf);
       }
       // (every wave loads the statistics, the same to the same place: its loads then count alike)
       load_lds_4(stat + min(n0 + (lane & 31), nvirt - 1), lds0 + C::STAT + buf * C::STATB);
@@ -225,6 +295,11 @@ __global__ __launch_bounds__(512) void bwd_keys_kernel(BwdArgs a, Shares shares)
       for (int ks = 0; ks < S::KS; ++ks) t = mfma(r[ks], kv[ks], t);
       return t;
     };
+    auto positional = [&](uint32_t buf, f32x16 t) {  // what the first wave's product has besides
+  #pragma unroll
+      for (int ks = 0; ks < PS; ++ks) t = mfma(f.rows(buf, ks), lds_read(kp ^ (ks << 5)), t);
+      return t;
+    };
     auto columns = [&](uint32_t buf, int c, bf16x8 (&w)[S::DT]) {
   #pragma unroll
       for (int dt = 0; dt < S::DT; ++dt) w[dt] = f.cols(buf + c * 16 * S::ROWB, dt);
@@ -232,6 +307,10 @@ __global__ __launch_bounds__(512) void bwd_keys_kernel(BwdArgs a, Shares shares)
     auto gather = [&](const bf16x8 (&w)[S::DT], const bf16x8 &x) {
   #pragma unroll
       for (int dt = 0; dt < S::DT; ++dt) sum[dt] = mfma(w[dt], x, sum[dt]);
+    };
+    auto gather_positional = [&](uint32_t buf, int c, const bf16x8 &x) {
+  #pragma unroll
+      for (int dt = 0; dt < PT; ++dt) sum_pe[dt] = mfma(f.cols(buf + c * 16 * S::ROWB, dt), x, sum_pe[dt]);
     };
     wait_loads();
   #pragma unroll
@@ -242,6 +321,8 @@ __global__ __launch_bounds__(512) void bwd_keys_kernel(BwdArgs a, Shares shares)
       // nobody reads the buffer of tile j - 2 any more, where tile j + 2 goes
       static_assert(C::AHEAD == 2 && C::NBUF == 4 && (PER == 1 || PER == 2), "one tile's loads stay out");
       if (j + 1 >= ntile) __builtin_amdgcn_s_waitcnt(0x0070);    // vmcnt(0), lgkmcnt(0)
+      else if (PP && PER == 2) __builtin_amdgcn_s_waitcnt(0x0074);  // vmcnt(4)
+      else if (PP) __builtin_amdgcn_s_waitcnt(0x0073);           // vmcnt(3)
       else if (PER == 2) __builtin_amdgcn_s_waitcnt(0x0073);     // vmcnt(3)
       else __builtin_amdgcn_s_waitcnt(0x0072);                   // vmcnt(2)
       barrier_only();
@@ -256,6 +337,7 @@ __global__ __launch_bounds__(512) void bwd_keys_kernel(BwdArgs a, Shares shares)
       const int n0 = n_lo + j * BR;
       f32x4 lse[4];
       f32x16 p = product(BUF * BUFB, lse, st0 + BUF * C::STATB);
+      if constexpr (PP > 0) p = positional(BUF * BUFB + 2 * TILE, p);
       bf16x8 w0[S::DT], w1[S::DT];
       columns(BUF * BUFB + TILE, 0, w0);
       __builtin_amdgcn_sched_barrier(0);
@@ -281,9 +363,30 @@ __global__ __launch_bounds__(512) void bwd_keys_kernel(BwdArgs a, Shares shares)
       constexpr int BUF = (decltype(buf)::value + 3) & 3;
       enter(j);
       f32x4 delta[4], p[4];
+      auto read_p = [&] {
   #pragma unroll
-      for (int b = 0; b < 4; ++b)
-        p[b] = *(KPOOL_LDS const f32x4 *)(uintptr_t)(pb + (BUF & 1) * C::NG * C::PBUF + b * 1024);
+        for (int b = 0; b < 4; ++b)
+          p[b] = *(KPOOL_LDS const f32x4 *)(uintptr_t)(pb + (BUF & 1) * C::NG * C::PBUF + b * 1024);
+      };
+      if constexpr (PP > 0) {
+        // (P once the product's fragments are used up: beside them it would not fit the registers)
+        f32x16 ds = product(BUF * BUFB + TILE, delta, st0 + BUF * C::STATB);
+        __builtin_amdgcn_sched_barrier(0);
+        read_p();
+        bf16x8 w[S::DT];
+        columns(BUF * BUFB, 0, w);
+        __builtin_amdgcn_sched_barrier(0);
+  #pragma unroll
+        for (int i = 0; i < 16; ++i) ds[i] = p[i / 4][i % 4] * (ds[i] - delta[i / 4][i % 4]);
+        const bf16x8 x0 = as_operand(ds, 0), x1 = as_operand(ds, 1);
+        gather(w, x0);
+        gather_positional(BUF * BUFB + 2 * TILE, 0, x0);
+        columns(BUF * BUFB, 1, w);
+        gather(w, x1);
+        gather_positional(BUF * BUFB + 2 * TILE, 1, x1);
+        return;
+      }
+      read_p();
       f32x16 ds = product(BUF * BUFB + TILE, delta, st0 + BUF * C::STATB);
       bf16x8 w0[S::DT], w1[S::DT];
       columns(BUF * BUFB, 0, w0);
@@ -313,14 +416,34 @@ __global__ __launch_bounds__(512) void bwd_keys_kernel(BwdArgs a, Shares shares)
       steps(skip, ntile, first_wave);
       enter(ntile);
     } else {
+  #pragma unroll
+      for (int dt = 0; dt < PT; ++dt)
+  #pragma unroll
+        for (int i = 0; i < 16; ++i) sum_pe[dt][i] = 0.0f;
       for (int j = 0; j <= skip; ++j) enter(j);
       steps(skip + 1, ntile + 1, second_wave);
+      if constexpr (PP > 0) {
+        // (a part's rows are D + P wide; a whole unit's positional columns go to their head's sums)
+        const bool whole = ntile == nsteps;
+        float *part = a.part + ((2 * span.share + (step0 == 0)) * 2 + 1) * (int64_t)(C::KEYS * q_width);
+        if (live)
+          write_part<PT>(sum_pe, a.scale, nullptr, whole ? a.pe_part : part,
+                         whole ? kvh * a.Tk + k_start + key : group * 32 + (lane & 31), whole ? a.P : q_width,
+                         whole ? 0 : a.D, a.P, lane);
+      }
     }
     const bool whole = ntile == nsteps;
-    float *part = a.part + ((2 * span.share + (step0 == 0)) * 2 + second) * (int64_t)(C::KEYS * a.D);
-    if (live)
-      write_cols<DP>(sum, second ? a.scale : 1.0f, second ? a.dk : a.dv, whole ? nullptr : part,
-                     whole ? ((int64_t)k_start + key) * a.Hkv + kvh : group * 32 + (lane & 31), a.D, lane);
+    if constexpr (PP == 0) {
+      float *part = a.part + ((2 * span.share + (step0 == 0)) * 2 + second) * (int64_t)(C::KEYS * a.D);
+      if (live)
+        write_cols<DP>(sum, second ? a.scale : 1.0f, second ? a.dk : a.dv, whole ? nullptr : part,
+                       whole ? ((int64_t)k_start + key) * a.Hkv + kvh : group * 32 + (lane & 31), a.D, lane);
+    } else if (live) {
+      float *part = a.part + ((2 * span.share + (step0 == 0)) * 2 + second) * (int64_t)(C::KEYS * q_width);
+      write_part<S::DT>(sum, second ? a.scale : 1.0f, second ? a.dk : a.dv, whole ? nullptr : part,
+                        whole ? ((int64_t)k_start + key) * a.Hkv + kvh : group * 32 + (lane & 31),
+                        whole ? a.D : q_width, 0, a.D, lane);
+    }
   }
 }
 
@@ -366,16 +489,59 @@ __global__ __launch_bounds__(256) void bwd_keys_sum_kernel(BwdArgs a, Shares sha
 //   512, 2048      1.12  1.45  89    576
 constexpr int kFewKeys = 512, kFineKeys = 1024;
 
+// The same with rows of D + P columns, whose positional ones go to their head's sums.
+__global__ __launch_bounds__(256) void bwd_expanded_sum_kernel(BwdArgs a, Shares shares) {
+  constexpr int KEYS = 128;
+  const int share = blockIdx.x >> 4, key0 = (blockIdx.x & 15) * 8, lane = threadIdx.x & 63;
+  int u, end;
+  if (!begins_cut(shares, share, lane, u, end)) return;
+  const int kvh = u % a.Hkv;
+  const TileAt at = find_tile(a.table, a.cu_k, a.cu_q, a.nseq, 1, KEYS, u / a.Hkv, a.ktiles, lane);
+  const int per = (a.D + a.QD) / 4, per_v = a.D / 4;  // of a key: dv, then dk and its positional part
+  const int64_t pitch = (int64_t)KEYS * a.QD;
+  for (int e = threadIdx.x; e < 8 * per; e += 256) {
+    const int r = key0 + e / per, c = e % per, which = c >= per_v, d = (c - which * per_v) * 4;
+    if (at.n0 + r >= at.Lq) continue;
+    const float *part = a.part + which * pitch + r * a.QD + d;
+    float4 t = *reinterpret_cast<const float4 *>(part + (2 * share + 1) * 2 * pitch);
+#pragma unroll 4
+    for (int s = share + 1; s < end; ++s) {
+      const float4 x = *reinterpret_cast<const float4 *>(part + 2 * s * 2 * pitch);
+      t.x += x.x, t.y += x.y, t.z += x.z, t.w += x.w;
+    }
+    const int64_t token = (int64_t)at.q_start + at.n0 + r;
+    if (d >= a.D)
+      *reinterpret_cast<float4 *>(a.pe_part + (kvh * a.Tk + token) * a.P + d - a.D) = t;
+    else
+      *reinterpret_cast<uint2 *>((which ? a.dk : a.dv) + (token * a.Hkv + kvh) * a.D + d) =
+          make_uint2(pack_bf16(t.x, t.y), pack_bf16(t.z, t.w));
+  }
+}
+
+// The positional gradient: the key heads' sums, in order.
+__global__ __launch_bounds__(256) void bwd_positional_kernel(BwdArgs a) {
+  const int64_t n = a.Tk * a.P, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+  for (int h = 0; h < a.Hkv; ++h) {
+    const float4 x = *reinterpret_cast<const float4 *>(a.pe_part + h * n + i);
+    t.x += x.x, t.y += x.y, t.z += x.z, t.w += x.w;
+  }
+  *reinterpret_cast<uint2 *>(a.dpe + i) = make_uint2(pack_bf16(t.x, t.y), pack_bf16(t.z, t.w));
+}
+
 // dQ: NW waves of 32 virtual rows; key tiles of 64 pass through LDS, as in the forward pass.
 // 8192 packed tokens (4096, 2777, 1000, 319), 16 heads over 4 of 128: 157 GFLOP in 193 us, 0.81
 // PFLOP/s.  CUs are busy 75% of the time, the matrix pipe 54% of that: within a wave a half tile's
 // exponentials wait for its products and the next half's products for them (the scheduling
 // barriers keep the phases apart), and all waves wait for a whole tile's loads together.  Cutting
 // the longest tiles to the CUs' average leaves the time as it is.
-template <int DP, int NW>
+template <int DP, int NW, int PP>
 __global__ __launch_bounds__(NW * 64) void bwd_rows_kernel(BwdArgs a) {
   using S = Keys<DP>;
-  constexpr int BK = 64, BQ = NW * 32, TILE = BK * S::ROWB;
+  constexpr int BK = 64, BQ = NW * 32, TILE = BK * S::ROWB, BUFB = 2 * TILE + BK * PP * 2;
+  constexpr int PS = PP / 16, PT = PP / 32, PW = PP ? PP : 64;  // the positional part's steps, blocks, width
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -391,8 +557,8 @@ __global__ __launch_bounds__(NW * 64) void bwd_rows_kernel(BwdArgs a) {
   const bool whole = t1 < a.qchunk;  // (the only part, which writes dQ itself)
   const int k_lo = split * a.qchunk, k_hi = (int)min64(t1 + 1, (int64_t)k_lo + a.qchunk);
   if (split > 0 && k_lo >= k_hi) return;  // (the sum does not read this part)
-  const uint16_t *kb = (const uint16_t *)uniform_ptr(a.k + (int64_t)at.k_start * a.ks + (int64_t)kvh * a.D);
-  const uint16_t *vb = (const uint16_t *)uniform_ptr(a.v + (int64_t)at.k_start * a.vs + (int64_t)kvh * a.D);
+  const uint16_t *kb = (const uint16_t *)uniform_ptr(a.k + (int64_t)at.k_start * a.ks + (int64_t)kvh * (PP ? a.kh : a.D));
+  const uint16_t *vb = (const uint16_t *)uniform_ptr(a.v + (int64_t)at.k_start * a.vs + (int64_t)kvh * (PP ? a.vh : a.D));
   const int n = at.n0 + wave * 32 + (lane & 31);
   const bool live = wave * 32 + (lane & 31) < nrows;
   const int tok = n / G, head = kvh * G + (n - tok * G);
@@ -402,7 +568,11 @@ __global__ __launch_bounds__(NW * 64) void bwd_rows_kernel(BwdArgs a) {
   const int w1 = wave_rows > 0 ? (at.n0 + wave * 32 + wave_rows - 1) / G + at.Lk - at.Lq : -1;
   const int64_t row = ((int64_t)at.q_start + tok) * a.Hq + head;
   bf16x8 qf[S::KS], dof[S::KS];
-  load_frag<DP>(qf, live ? a.q + ((int64_t)at.q_start + tok) * a.qs + (int64_t)head * a.D : nullptr, a.D, lane);
+  const uint16_t *q_row = a.q + ((int64_t)at.q_start + tok) * a.qs + (int64_t)head * (PP ? a.QD : a.D);
+  load_frag<DP>(qf, live ? q_row : nullptr, a.D, lane);
+  uint32_t qp = 0;
+  if constexpr (PP > 0)
+    qp = stash<PP>(lds_offset(lds) + 2 * BUFB + wave * 32 * Keys<PP>::ROWB, live ? q_row + a.D : nullptr, a.P, lane);
   load_frag<DP>(dof, live ? a.d_o + row * a.D : nullptr, a.D, lane);
   // the rows' lse and delta, which dK's and dV's kernel reads
   const int64_t stat = (int64_t)kvh * a.Tq * G + (int64_t)at.q_start * G + n;
@@ -418,9 +588,9 @@ __global__ __launch_bounds__(NW * 64) void bwd_rows_kernel(BwdArgs a) {
       for (int i = 0; i < 8; ++i) delta = fmaf((float)of[ks][i], (float)dof[ks][i], delta);
     delta += other_half(delta);
   }
-  f32x16 dq[S::DT];
+  f32x16 dq[S::DT + PT];
 #pragma unroll
-  for (int dt = 0; dt < S::DT; ++dt)
+  for (int dt = 0; dt < S::DT + PT; ++dt)
 #pragma unroll
     for (int i = 0; i < 16; ++i) dq[dt][i] = 0.0f;
 
@@ -429,13 +599,50 @@ __global__ __launch_bounds__(NW * 64) void bwd_rows_kernel(BwdArgs a) {
   f.init(lds0, lane);
   KeyLoader<DP, BK, NW> keys;
   keys.init(wave, lane, a.D);
+  Frag<PW> fp;
+  KeyLoader<PW, BK, NW> pes;
+  const uint16_t *pb = nullptr;
+  if constexpr (PP > 0) {
+    fp.init(lds0, lane);
+    pes.init(wave, lane, a.P);
+    pb = (const uint16_t *)uniform_ptr(a.pe + (int64_t)at.k_start * a.pes);
+  }
   const int ntile = k_hi > k_lo ? (k_hi - k_lo + BK - 1) / BK : 0;
   auto load = [&](int k0, int buf) {
-    keys.load(kb + (int64_t)k0 * a.ks, a.ks, at.Lk - 1 - k0, lds0 + buf * 2 * TILE);
-    keys.load(vb + (int64_t)k0 * a.vs, a.vs, at.Lk - 1 - k0, lds0 + buf * 2 * TILE + TILE);
+    keys.load(kb + (int64_t)k0 * a.ks, a.ks, at.Lk - 1 - k0, lds0 + buf * BUFB);
+    keys.load(vb + (int64_t)k0 * a.vs, a.vs, at.Lk - 1 - k0, lds0 + buf * BUFB + TILE);
+    if constexpr (PP > 0) pes.load(pb + (int64_t)k0 * a.pes, a.pes, at.Lk - 1 - k0, lds0 + buf * BUFB + 2 * TILE);
   };
   // S and dP of 32 keys
-  auto half_tile = [&](uint32_t sk, uint32_t sv, f32x16 &s, f32x16 &dp) {
+  auto half_tile = [&](uint32_t sk, uint32_t sv, uint32_t sp, f32x16 &s, f32x16 &dp) {
+    if constexpr (PP > 0) {  // (a few fragments ahead: more would not fit the registers)
+      constexpr int N = 2 * PS + 2 * S::KS, AHEAD = 4;
+      auto read = [&](int n) {  // fragments in the order of their use: positional pairs, keys, values
+        return n < 2 * PS ? (n & 1 ? lds_read(qp ^ (n / 2 << 5)) : fp.rows(sp, n / 2))
+                          : n < 2 * PS + S::KS ? f.rows(sk, n - 2 * PS) : f.rows(sv, n - 2 * PS - S::KS);
+      };
+      bf16x8 r[N];
+#pragma unroll
+      for (int n = 0; n < AHEAD; ++n) r[n] = read(n);
+      s = f32x16{}, dp = f32x16{};
+#pragma unroll
+      for (int n = 0; n < N; n += 2) {
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (n + AHEAD + u < N) r[n + AHEAD + u] = read(n + AHEAD + u);
+        if (n < 2 * PS) s = mfma(r[n], r[n + 1], s);
+        else
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int ks = n + u - 2 * PS;
+            if (ks < S::KS) s = mfma(r[n + u], qf[ks < S::KS ? ks : 0], s);
+            else dp = mfma(r[n + u], dof[ks < S::KS ? 0 : ks - S::KS], dp);
+          }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      return;
+    }
     // (the reads of a phase go out together, ahead of what needs them)
     bf16x8 kr[S::KS], vr[S::KS];
 #pragma unroll
@@ -475,9 +682,9 @@ __global__ __launch_bounds__(NW * 64) void bwd_rows_kernel(BwdArgs a) {
       if (k0 > w1) continue;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const uint32_t sk = (j & 1) * 2 * TILE + half * 32 * S::ROWB;
+        const uint32_t sk = (j & 1) * BUFB + half * 32 * S::ROWB;
         f32x16 s, dp;
-        half_tile(sk, sk + TILE, s, dp);
+        half_tile(sk, sk + TILE, (j & 1) * BUFB + 2 * TILE + half * 32 * Keys<PW>::ROWB, s, dp);
         to_weights(s, k0 + half * 32, k0 + BK - 1 > w0);
 #pragma unroll
         for (int i = 0; i < 16; ++i) sum = fmaf(s[i], dp[i], sum);
@@ -495,10 +702,27 @@ __global__ __launch_bounds__(NW * 64) void bwd_rows_kernel(BwdArgs a) {
     if (k0 > w1) return;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      constexpr uint32_t SK = BUF * 2 * TILE, SV = SK + TILE;
-      const uint32_t down = half * 32 * S::ROWB;
+      constexpr uint32_t SK = BUF * BUFB, SV = SK + TILE, SP = SK + 2 * TILE;
+      const uint32_t down = half * 32 * S::ROWB, pe_down = half * 32 * Keys<PW>::ROWB;
       f32x16 s, dp;
-      half_tile(SK + down, SV + down, s, dp);
+      half_tile(SK + down, SV + down, SP + pe_down, s, dp);
+      if constexpr (PP > 0) {
+        to_weights(s, k0 + half * 32, k0 + BK - 1 > w0);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] *= dp[i] - delta;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const bf16x8 ds = as_operand(s, c), rest = as_operand_rest(s, c, ds);
+#pragma unroll
+          for (int dt = 0; dt < S::DT + PT; ++dt) {
+            const bf16x8 w = dt < S::DT ? f.cols(SK + down + c * 16 * S::ROWB, dt < S::DT ? dt : 0)
+                                        : fp.cols(SP + pe_down + c * 16 * Keys<PW>::ROWB, dt < S::DT ? 0 : dt - S::DT);
+            dq[dt] = mfma(w, ds, dq[dt]);
+            if (t1 < kFineKeys) dq[dt] = mfma(w, rest, dq[dt]);
+          }
+        }
+        continue;
+      }
       bf16x8 w[2][S::DT];
 #pragma unroll
       for (int c = 0; c < 2; ++c)
@@ -526,14 +750,20 @@ __global__ __launch_bounds__(NW * 64) void bwd_rows_kernel(BwdArgs a) {
     if (j + 1 < ntile) step(j + 1, std::integral_constant<int, 1>{});
   }
   if (!live) return;
-  float *part = whole ? nullptr : a.part + (int64_t)split * a.Tq * a.Hq * a.D;
-  write_cols<DP>(dq, a.scale, a.dq, part, row, a.D, lane);
+  if constexpr (PP > 0) {
+    float *part = whole ? nullptr : a.part + (int64_t)split * a.Tq * a.Hq * a.QD;
+    write_part<S::DT>(dq, a.scale, a.dq, part, row, a.QD, 0, a.D, lane);
+    write_part<PT>(dq + S::DT, a.scale, a.dq, part, row, a.QD, a.D, a.P, lane);
+  } else {
+    float *part = whole ? nullptr : a.part + (int64_t)split * a.Tq * a.Hq * a.D;
+    write_cols<DP>(dq, a.scale, a.dq, part, row, a.D, lane);
+  }
 }
 
 constexpr int kBwdWaves = 8;
 
 // Adds dQ's parts, in order, of the tiles that have more than one; 8 workgroups a tile.
-__global__ __launch_bounds__(256) void bwd_rows_sum_kernel(BwdArgs a) {
+__global__ __launch_bounds__(256) void bwd_rows_sum_kernel(BwdArgs a, int width) {
   constexpr int BQ = kBwdWaves * 32, ROWS = BQ / 8;
   const int row0 = (blockIdx.x & 7) * ROWS, lane = threadIdx.x & 63, G = a.Hq / a.Hkv;
   const int unit = blockIdx.x >> 3, kvh = unit % a.Hkv;
@@ -542,12 +772,12 @@ __global__ __launch_bounds__(256) void bwd_rows_sum_kernel(BwdArgs a) {
   const int nrows = min(BQ, at.Lq * G - at.n0);
   const int parts = ((at.n0 + nrows - 1) / G + at.Lk - at.Lq) / a.qchunk + 1;
   if (parts <= 1) return;
-  const int per = a.D / 4;
-  const int64_t pitch = a.Tq * a.Hq * a.D;
+  const int per = width / 4;
+  const int64_t pitch = a.Tq * a.Hq * width;
   for (int e = threadIdx.x; e < ROWS * per; e += 256) {
     const int n = at.n0 + row0 + e / per;
     if (n >= at.Lq * G) break;
-    const int64_t to = (((int64_t)at.q_start + n / G) * a.Hq + kvh * G + n % G) * a.D + e % per * 4;
+    const int64_t to = (((int64_t)at.q_start + n / G) * a.Hq + kvh * G + n % G) * width + e % per * 4;
     float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
     for (int s = 0; s < parts; ++s) {
@@ -570,35 +800,42 @@ UnitCost rows_cost(int64_t lq, int64_t lk, int64_t n0, int64_t G) {
   return {2 + (t1 < kFewKeys ? steps * 2 / 3 : 0), steps};
 }
 
-template <int DP>
+template <int DP, int PP>
 hipError_t launch_bwd_t(const AttendCall &c, const BwdPlan &p, BwdArgs a, hipStream_t st) {
+  using C = BwdKeys<DP, PP>;
   hipError_t e = hipSuccess;
   const int G = a.Hq / a.Hkv;
   if (a.Tq > 0) {
     a.qtiles = make_table(a.table, c.cu_q_host, c.cu_k_host, a.nseq, a.Hq / a.Hkv, kBwdWaves * 32, true);
-    const size_t lds = 4 * 64 * DP * 2;
-    hipLaunchKernelGGL((bwd_rows_kernel<DP, kBwdWaves>), dim3((unsigned)(a.qtiles * a.qsplit * a.Hkv)),
+    const size_t lds = 2 * 64 * (2 * DP + PP) * 2 + kBwdWaves * 32 * PP * 2;
+    hipLaunchKernelGGL((bwd_rows_kernel<DP, kBwdWaves, PP>), dim3((unsigned)(a.qtiles * a.qsplit * a.Hkv)),
                        dim3(kBwdWaves * 64), lds, st, a);
     e = hipGetLastError();
     if (e == hipSuccess && a.qsplit > 1) {
-      hipLaunchKernelGGL(bwd_rows_sum_kernel, dim3((unsigned)(a.qtiles * a.Hkv * 8)), dim3(256), 0, st, a);
+      hipLaunchKernelGGL(bwd_rows_sum_kernel, dim3((unsigned)(a.qtiles * a.Hkv * 8)), dim3(256), 0, st, a,
+                         a.D + a.P);
       e = hipGetLastError();
     }
     if (e != hipSuccess) return e;
   }
   // (behind dQ's kernel, which lays lse and delta out for it)
   if (a.Tk > 0) {
-    a.ktiles = make_table(a.table, c.cu_k_host, c.cu_q_host, a.nseq, 1, BwdKeys<DP>::KEYS, false);
+    a.ktiles = make_table(a.table, c.cu_k_host, c.cu_q_host, a.nseq, 1, C::KEYS, false);
     Shares shares;
     const bool cut = make_shares(shares, p.kshares, p.kcost, a.Hkv, a.table, c.cu_k_host, c.cu_q_host, a.nseq, 1,
-                                 BwdKeys<DP>::KEYS, a.ktiles, [&](int64_t lk, int64_t lq, int64_t n0) {
+                                 C::KEYS, a.ktiles, [&](int64_t lk, int64_t lq, int64_t n0) {
                                    return keys_cost(lk, lq, n0, G);
                                  });
     const unsigned grid = (unsigned)(shares.n ? shares.n : a.ktiles * a.Hkv);
-    hipLaunchKernelGGL(bwd_keys_kernel<DP>, dim3(grid), dim3(512), BwdKeys<DP>::LDS, st, a, shares);
+    hipLaunchKernelGGL((bwd_keys_kernel<DP, PP>), dim3(grid), dim3(512), C::LDS, st, a, shares);
     e = hipGetLastError();
     if (e == hipSuccess && cut) {
-      hipLaunchKernelGGL(bwd_keys_sum_kernel, dim3(grid * 16), dim3(256), 0, st, a, shares);
+      if (PP) hipLaunchKernelGGL(bwd_expanded_sum_kernel, dim3(grid * 16), dim3(256), 0, st, a, shares);
+      else hipLaunchKernelGGL(bwd_keys_sum_kernel, dim3(grid * 16), dim3(256), 0, st, a, shares);
+      e = hipGetLastError();
+    }
+    if (e == hipSuccess && PP) {
+      hipLaunchKernelGGL(bwd_positional_kernel, dim3((unsigned)((a.Tk * a.P / 4 + 255) / 256)), dim3(256), 0, st, a);
       e = hipGetLastError();
     }
   }
@@ -625,11 +862,11 @@ BwdPlan plan_attend_bwd(const int32_t *cu_q, const int32_t *cu_k, int nseq, int 
   return p;
 }
 
-size_t attend_bwd_workspace(const BwdPlan &p, int64_t Tq, int64_t Tk, int Hq, int Hkv, int D) {
-  const int64_t stat = up_to(Tq * Hq * 8, 16);
-  const int64_t kpart = (int64_t)p.kshares * 4 * 128 * D * 4;                 // dK and dV, two slots a share
-  const int64_t qpart = p.qsplit > 1 ? (int64_t)p.qsplit * Tq * Hq * D * 4 : 0;
-  return (size_t)(stat + (kpart > qpart ? kpart : qpart));
+size_t attend_bwd_workspace(const BwdPlan &p, int64_t Tq, int64_t Tk, int Hq, int Hkv, int D, int P) {
+  const int64_t stat = up_to(Tq * Hq * 8, 16), width = D + P;
+  const int64_t kpart = (int64_t)p.kshares * 4 * 128 * width * 4;             // dK and dV, two slots a share
+  const int64_t qpart = p.qsplit > 1 ? (int64_t)p.qsplit * Tq * Hq * width * 4 : 0;
+  return (size_t)(stat + Tk * Hkv * P * 4 + (kpart > qpart ? kpart : qpart));
 }
 
 int64_t attend_bwd_threads(const BwdPlan &p, int Hkv) {
@@ -637,8 +874,10 @@ int64_t attend_bwd_threads(const BwdPlan &p, int Hkv) {
   return std::max({p.ktiles * Hkv * 512, p.qtiles * p.qsplit * Hkv * kBwdWaves * 64, sum});
 }
 
-hipError_t launch_attend_bwd(const AttendCall &c, const uint16_t *d_o, const BwdPlan &p, void *workspace,
-                             uint16_t *dq, uint16_t *dk, uint16_t *dv, hipStream_t st) {
+namespace {
+
+BwdArgs make_bwd_args(const AttendCall &c, const uint16_t *d_o, const BwdPlan &p, void *workspace, uint16_t *dq,
+                      uint16_t *dk, uint16_t *dv) {
   BwdArgs a{};
   a.q = c.q, a.k = c.k, a.v = c.v, a.d_o = d_o, a.o = c.o, a.lse = c.lse;
   a.qs = c.q_stride, a.ks = c.k_stride, a.vs = c.v_stride;
@@ -650,7 +889,25 @@ hipError_t launch_attend_bwd(const AttendCall &c, const uint16_t *d_o, const Bwd
   a.part = (float *)((char *)workspace + up_to(c.Tq * c.Hq * 8, 16));
   a.qsplit = p.qsplit, a.qchunk = p.qchunk;
   a.dq = dq, a.dk = dk, a.dv = dv;
-  return c.D <= 64 ? launch_bwd_t<64>(c, p, a, st) : launch_bwd_t<128>(c, p, a, st);
+  return a;
+}
+
+}  // namespace
+
+hipError_t launch_attend_bwd(const AttendCall &c, const uint16_t *d_o, const BwdPlan &p, void *workspace,
+                             uint16_t *dq, uint16_t *dk, uint16_t *dv, hipStream_t st) {
+  const BwdArgs a = make_bwd_args(c, d_o, p, workspace, dq, dk, dv);
+  return c.D <= 64 ? launch_bwd_t<64, 0>(c, p, a, st) : launch_bwd_t<128, 0>(c, p, a, st);
+}
+
+hipError_t launch_expanded_bwd(const AttendCall &c, const ExpandedKeys &x, const uint16_t *d_o, const BwdPlan &p,
+                               void *workspace, uint16_t *dq, uint16_t *dk, uint16_t *dk_pe, uint16_t *dv,
+                               hipStream_t st) {
+  BwdArgs a = make_bwd_args(c, d_o, p, workspace, dq, dk, dv);
+  a.pe = x.k_pe, a.pes = x.pe_stride, a.kh = x.k_head, a.vh = x.v_head, a.P = x.P, a.QD = c.D + x.P;
+  a.pe_part = a.part, a.part += c.Tk * c.Hkv * x.P;
+  a.dpe = dk_pe;
+  return c.D <= 64 ? launch_bwd_t<64, 64>(c, p, a, st) : launch_bwd_t<128, 64>(c, p, a, st);
 }
 
 }  // namespace kpool

@@ -89,6 +89,12 @@ int check_heads(const char *fn, int32_t Hq, int32_t Hkv, int32_t D) {
   return KPOOL_OK;
 }
 
+int check_positional(const char *fn, int32_t P) {
+  if (P < 8 || P % 8) return fail(KPOOL_EINVAL, "%s: P must be a positive multiple of 8 (got %d)", fn, P);
+  if (P > 64) return fail(KPOOL_EUNSUPPORTED, "%s: P up to 64 is compiled in (got %d)", fn, P);
+  return KPOOL_OK;
+}
+
 int check_lengths(const char *fn, const int32_t *cu_q, const int32_t *cu_k, int32_t nseq, int32_t G) {
   int rc = check_cu(cu_q, nseq, fn);
   if (!rc) rc = check_cu(cu_k, nseq, fn);
@@ -99,15 +105,20 @@ int check_lengths(const char *fn, const int32_t *cu_q, const int32_t *cu_k, int3
   return KPOOL_OK;
 }
 
-// Fills in Tq and Tk.  Tq = 0 needs no pointers.
-int check_attend(const char *fn, kpool::AttendCall &c, const int32_t *cu_q_host, const int32_t *cu_k_host) {
+// Fills in Tq and Tk.  Tq = 0 needs no pointers.  x: the positional part of expanded latent attention.
+int check_attend(const char *fn, kpool::AttendCall &c, const int32_t *cu_q_host, const int32_t *cu_k_host,
+                 const kpool::ExpandedKeys &x) {
   int rc = check_heads(fn, c.Hq, c.Hkv, c.D);
   if (!rc) rc = check_lengths(fn, cu_q_host, cu_k_host, c.nseq, c.Hq / c.Hkv);
   if (rc) return rc;
   if (!(c.scale > 0.0f) || !isfinite(c.scale)) return fail(KPOOL_EINVAL, "%s: scale must be finite and > 0", fn);
-  const struct { int64_t stride, least; } st[3] = {{c.q_stride, (int64_t)c.Hq * c.D},
-                                                   {c.k_stride, (int64_t)c.Hkv * c.D},
-                                                   {c.v_stride, (int64_t)c.Hkv * c.D}};
+  for (const int64_t head : {x.k_head, x.v_head})
+    if (head < c.D || head % 8 || head > (1 << 24))
+      return fail(KPOOL_EINVAL, "%s: a head stride must be a multiple of 8 in [%d, 2^24] (got %lld)", fn, c.D, (long long)head);
+  const struct { int64_t stride, least; } st[4] = {{c.q_stride, (int64_t)c.Hq * (c.D + x.P)},
+                                                   {c.k_stride, (c.Hkv - 1) * x.k_head + c.D},
+                                                   {c.v_stride, (c.Hkv - 1) * x.v_head + c.D},
+                                                   {x.pe_stride, x.P}};
   for (const auto &x : st)
     if (x.stride < x.least || x.stride % 8 || x.stride > (1 << 24))
       return fail(KPOOL_EINVAL, "%s: a token stride must be a multiple of 8 in [%lld, 2^24] (got %lld)", fn,
@@ -125,15 +136,44 @@ int check_attend(const char *fn, kpool::AttendCall &c, const int32_t *cu_q_host,
   return KPOOL_OK;
 }
 
+// (a call without a positional part: its heads are contiguous)
+int check_attend(const char *fn, kpool::AttendCall &c, const int32_t *cu_q_host, const int32_t *cu_k_host) {
+  return check_attend(fn, c, cu_q_host, cu_k_host, {nullptr, 0, c.D, c.D, 0});
+}
+
+int check_expanded(const char *fn, kpool::AttendCall &c, const int32_t *cu_q_host, const int32_t *cu_k_host,
+                   const kpool::ExpandedKeys &x) {
+  int rc = check_positional(fn, x.P);
+  if (!rc) rc = check_attend(fn, c, cu_q_host, cu_k_host, x);
+  if (rc) return rc;
+  if (c.Tk > 0 && !x.k_pe && c.Tq > 0) return fail(KPOOL_EINVAL, "%s: null pointer", fn);
+  if (!aligned16(x.k_pe)) return fail(KPOOL_EINVAL, "%s: k_pe must be 16-byte aligned", fn);
+  return KPOOL_OK;
+}
+
 Operand q_of(const kpool::AttendCall &c) { return {"q", c.q, (int64_t)c.Hq * c.D * 2, c.Tq, c.q_stride * 2}; }
 Operand k_of(const kpool::AttendCall &c) { return {"k", c.k, (int64_t)c.Hkv * c.D * 2, c.Tk, c.k_stride * 2}; }
 Operand v_of(const kpool::AttendCall &c) { return {"v", c.v, (int64_t)c.Hkv * c.D * 2, c.Tk, c.v_stride * 2}; }
 Operand cu_q_of(const kpool::AttendCall &c) { return {"cu_q", c.cu_q, ((int64_t)c.nseq + 1) * 4}; }
 Operand cu_k_of(const kpool::AttendCall &c) { return {"cu_k", c.cu_k, ((int64_t)c.nseq + 1) * 4}; }
 
+// Operands of the expanded form (a token's heads with what lies between them, which others may be in).
+Operand expanded_q(const kpool::AttendCall &c, const kpool::ExpandedKeys &x) {
+  return {"q", c.q, (int64_t)c.Hq * (c.D + x.P) * 2, c.Tq, c.q_stride * 2};
+}
+Operand expanded_k(const kpool::AttendCall &c, const kpool::ExpandedKeys &x) {
+  return {"k", c.k, ((c.Hkv - 1) * x.k_head + c.D) * 2, c.Tk, c.k_stride * 2};
+}
+Operand expanded_v(const kpool::AttendCall &c, const kpool::ExpandedKeys &x) {
+  return {"v", c.v, ((c.Hkv - 1) * x.v_head + c.D) * 2, c.Tk, c.v_stride * 2};
+}
+Operand expanded_pe(const kpool::AttendCall &c, const kpool::ExpandedKeys &x) {
+  return {"k_pe", x.k_pe, x.P * 2, c.Tk, x.pe_stride * 2};
+}
+
 // The forward calls' plan, workspace and outputs; ids: the lists, if there are any.
 int check_attend_plan(const char *fn, const kpool::AttendCall &c, const kpool::AttendPlan &p, const void *workspace,
-                      size_t workspace_bytes, const Operand &ids) {
+                      size_t workspace_bytes, const Operand &ids, const kpool::ExpandedKeys *x = nullptr) {
   if (kpool::attend_threads(p, c.Hq, c.Hkv) >= kLaunchThreads)
     return fail(KPOOL_EUNSUPPORTED, "%s: too many query rows or sequences for one launch", fn);
   const size_t need = kpool::attend_workspace(p, c.Tq * c.Hq, c.D);
@@ -143,7 +183,8 @@ int check_attend_plan(const char *fn, const kpool::AttendCall &c, const kpool::A
   if (need && !aligned16(workspace)) return fail(KPOOL_EINVAL, "%s: workspace must be 16-byte aligned", fn);
   const int64_t rows = c.Tq * c.Hq;
   return check_apart(fn, {{"o", c.o, rows * c.D * 2}, {"lse", c.lse, rows * 4}, {"workspace", workspace, (int64_t)need}},
-                     {q_of(c), k_of(c), v_of(c), cu_q_of(c), cu_k_of(c), ids});
+                     {x ? expanded_q(c, *x) : q_of(c), x ? expanded_k(c, *x) : k_of(c), x ? expanded_v(c, *x) : v_of(c),
+                      x ? expanded_pe(c, *x) : Operand{}, cu_q_of(c), cu_k_of(c), ids});
 }
 
 int check_latent_sizes(const char *fn, int32_t H, int32_t R, int32_t P) {
@@ -328,6 +369,93 @@ int kpool_attend_selected(const uint16_t *q, int64_t q_stride, const uint16_t *k
   hipStream_t st = (hipStream_t)stream;
   hipError_t e = timed_layer(kAttend, st, [&] {
     return kpool::launch_attend_list(c, p, token_ids, width, workspace, st);
+  });
+  if (e != hipSuccess) return hip_fail(fn, e);
+  return ok();
+}
+
+size_t kpool_attend_expanded_workspace_bytes(const int32_t *cu_q_host, const int32_t *cu_k_host,
+                                             int32_t nseq, int32_t Hq, int32_t Hkv, int32_t D, int32_t P) {
+  const char *fn = "kpool_attend_expanded_workspace_bytes";
+  if (check_heads(fn, Hq, Hkv, D) || check_positional(fn, P) || check_lengths(fn, cu_q_host, cu_k_host, nseq, Hq / Hkv))
+    return 0;
+  ok();
+  return kpool::attend_workspace(kpool::plan_attend(cu_q_host, cu_k_host, nseq, Hq, Hkv, true),
+                                 (int64_t)cu_q_host[nseq] * Hq, D);
+}
+
+int kpool_attend_expanded(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                          int64_t k_head_stride, const uint16_t *k_pe, int64_t pe_stride,
+                          const uint16_t *v, int64_t v_stride, int64_t v_head_stride,
+                          const int32_t *cu_q_host, const int32_t *cu_q_dev, const int32_t *cu_k_host,
+                          const int32_t *cu_k_dev, int32_t nseq, int32_t Hq, int32_t Hkv, int32_t D,
+                          int32_t P, float scale, void *workspace, size_t workspace_bytes, uint16_t *o,
+                          float *lse, void *stream) {
+  const char *fn = "kpool_attend_expanded";
+  kpool::AttendCall c{q, k, v, q_stride, k_stride, v_stride, cu_q_dev, cu_k_dev, cu_q_host,
+                      cu_k_host, nseq, Hq, Hkv, D,
+                      0, 0, scale, o, lse};
+  const kpool::ExpandedKeys x{k_pe, pe_stride, k_head_stride, v_head_stride, P};
+  int rc = check_expanded(fn, c, cu_q_host, cu_k_host, x);
+  if (rc || c.Tq == 0) return rc;
+  const kpool::AttendPlan p = kpool::plan_attend(cu_q_host, cu_k_host, nseq, Hq, Hkv, true);
+  rc = check_attend_plan(fn, c, p, workspace, workspace_bytes, {}, &x);
+  if (rc) return rc;
+  hipStream_t st = (hipStream_t)stream;
+  hipError_t e = timed_layer(kAttend, st, [&] { return kpool::launch_attend_expanded(c, x, p, workspace, st); });
+  if (e != hipSuccess) return hip_fail(fn, e);
+  return ok();
+}
+
+size_t kpool_attend_expanded_backward_workspace_bytes(const int32_t *cu_q_host, const int32_t *cu_k_host,
+                                                      int32_t nseq, int32_t Hq, int32_t Hkv, int32_t D,
+                                                      int32_t P) {
+  const char *fn = "kpool_attend_expanded_backward_workspace_bytes";
+  if (check_heads(fn, Hq, Hkv, D) || check_positional(fn, P) || check_lengths(fn, cu_q_host, cu_k_host, nseq, Hq / Hkv))
+    return 0;
+  ok();
+  return kpool::attend_bwd_workspace(kpool::plan_attend_bwd(cu_q_host, cu_k_host, nseq, Hq, Hkv),
+                                     cu_q_host[nseq], cu_k_host[nseq], Hq, Hkv, D, P);
+}
+
+int kpool_attend_expanded_backward(const uint16_t *d_o, const uint16_t *q, int64_t q_stride,
+                                   const uint16_t *k, int64_t k_stride, int64_t k_head_stride,
+                                   const uint16_t *k_pe, int64_t pe_stride, const uint16_t *v,
+                                   int64_t v_stride, int64_t v_head_stride, const uint16_t *o,
+                                   const float *lse, const int32_t *cu_q_host, const int32_t *cu_q_dev,
+                                   const int32_t *cu_k_host, const int32_t *cu_k_dev, int32_t nseq,
+                                   int32_t Hq, int32_t Hkv, int32_t D, int32_t P, float scale,
+                                   void *workspace, size_t workspace_bytes, uint16_t *dq, uint16_t *dk,
+                                   uint16_t *dk_pe, uint16_t *dv, void *stream) {
+  const char *fn = "kpool_attend_expanded_backward";
+  kpool::AttendCall c{q, k, v, q_stride, k_stride, v_stride, cu_q_dev, cu_k_dev, cu_q_host,
+                      cu_k_host, nseq, Hq, Hkv, D,
+                      0, 0, scale, const_cast<uint16_t *>(o), const_cast<float *>(lse)};
+  const kpool::ExpandedKeys x{k_pe, pe_stride, k_head_stride, v_head_stride, P};
+  int rc = check_expanded(fn, c, cu_q_host, cu_k_host, x);
+  if (rc) return rc;
+  if (c.Tq == 0 && c.Tk == 0) return ok();
+  if (!cu_q_dev || !cu_k_dev || (c.Tq > 0 && (!d_o || !lse || !dq)) || (c.Tk > 0 && (!k || !k_pe || !v || !dk || !dk_pe || !dv)))
+    return fail(KPOOL_EINVAL, "%s: null pointer", fn);
+  if (!aligned16(k) || !aligned16(v) || !aligned16(d_o) || !aligned16(dq) || !aligned16(dk) || !aligned16(dk_pe) || !aligned16(dv))
+    return fail(KPOOL_EINVAL, "%s: k, v, d_o, dq, dk, dk_pe and dv must be 16-byte aligned", fn);
+  const kpool::BwdPlan p = kpool::plan_attend_bwd(cu_q_host, cu_k_host, nseq, Hq, Hkv);
+  if (kpool::attend_bwd_threads(p, Hkv) >= kLaunchThreads || c.Tk * P / 4 >= kLaunchThreads - 256)
+    return fail(KPOOL_EUNSUPPORTED, "%s: too many rows or sequences for one launch", fn);
+  const size_t need = kpool::attend_bwd_workspace(p, c.Tq, c.Tk, Hq, Hkv, D, P);
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(KPOOL_EWORKSPACE, "%s: needs %zu bytes of workspace, got %zu", fn, need,
+                workspace ? workspace_bytes : (size_t)0);
+  if (!aligned16(workspace)) return fail(KPOOL_EINVAL, "%s: workspace must be 16-byte aligned", fn);
+  const int64_t obytes = c.Tq * Hq * D * 2, kbytes = c.Tk * Hkv * D * 2, lbytes = c.Tq * Hq * 4;
+  rc = check_apart(fn, {{"dq", dq, c.Tq * Hq * (D + P) * 2}, {"dk", dk, kbytes}, {"dk_pe", dk_pe, c.Tk * P * 2},
+                        {"dv", dv, kbytes}, {"workspace", workspace, (int64_t)need}},
+                   {expanded_q(c, x), expanded_k(c, x), expanded_v(c, x), expanded_pe(c, x), cu_q_of(c), cu_k_of(c),
+                    {"d_o", d_o, obytes}, {"o", o, obytes}, {"lse", lse, lbytes}});
+  if (rc) return rc;
+  hipStream_t st = (hipStream_t)stream;
+  hipError_t e = timed_layer(kAttend, st, [&] {
+    return kpool::launch_expanded_bwd(c, x, d_o, p, workspace, dq, dk, dk_pe, dv, st);
   });
   if (e != hipSuccess) return hip_fail(fn, e);
   return ok();

@@ -65,11 +65,20 @@ struct AttendPlan {
   bool by_place;   // lists: ordered by place in the sequence first
   bool wave_rows;  // lists: a wave a row instead of four
 };
-AttendPlan plan_attend(const int32_t *cu_q, const int32_t *cu_k, int nseq, int Hq, int Hkv);
+AttendPlan plan_attend(const int32_t *cu_q, const int32_t *cu_k, int nseq, int Hq, int Hkv, bool tiles = false);
 AttendPlan plan_list(int64_t Tq, int nseq, int width, int Hq, int Hkv);
 size_t attend_workspace(const AttendPlan &p, int64_t rows, int D);
 int64_t attend_threads(const AttendPlan &p, int Hq, int Hkv);  // of its largest launch, or more
 hipError_t launch_attend(const AttendCall &c, const AttendPlan &p, void *workspace, hipStream_t st);
+// Expanded latent attention: a call's keys have a positional part besides, [Tk, P], shared by the heads,
+// and queries D + P values a head; the keys' and values' heads lie k_head and v_head elements apart.
+struct ExpandedKeys {
+  const uint16_t *k_pe;
+  int64_t pe_stride, k_head, v_head;
+  int32_t P;
+};
+hipError_t launch_attend_expanded(const AttendCall &c, const ExpandedKeys &x, const AttendPlan &p, void *workspace,
+                                  hipStream_t st);
 hipError_t launch_attend_list(const AttendCall &c, const AttendPlan &p, const int32_t *ids, int width,
                               void *workspace, hipStream_t st);
 
@@ -81,10 +90,14 @@ struct BwdPlan {
   int qsplit, qchunk;      // parts of the keys (dQ)
 };
 BwdPlan plan_attend_bwd(const int32_t *cu_q, const int32_t *cu_k, int nseq, int Hq, int Hkv);
-size_t attend_bwd_workspace(const BwdPlan &p, int64_t Tq, int64_t Tk, int Hq, int Hkv, int D);
+size_t attend_bwd_workspace(const BwdPlan &p, int64_t Tq, int64_t Tk, int Hq, int Hkv, int D, int P = 0);
 int64_t attend_bwd_threads(const BwdPlan &p, int Hkv);  // of its largest launch, or more
 hipError_t launch_attend_bwd(const AttendCall &c, const uint16_t *d_o, const BwdPlan &p, void *workspace,
                              uint16_t *dq, uint16_t *dk, uint16_t *dv, hipStream_t st);
+
+hipError_t launch_expanded_bwd(const AttendCall &c, const ExpandedKeys &x, const uint16_t *d_o, const BwdPlan &p,
+                               void *workspace, uint16_t *dq, uint16_t *dk, uint16_t *dk_pe, uint16_t *dv,
+                               hipStream_t st);
 
 // Latent attention over a cache of one row a token (latent.hip).  ids: [Tq, width] lists, or null.
 struct LatentCall {

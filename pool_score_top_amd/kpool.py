@@ -70,6 +70,12 @@ def lib():
         "kpool_layer_norm_backward_workspace_bytes": (sz, [i64, i32]),
         "kpool_layer_norm_backward": (ctypes.c_int, [vp, vp, i64, vp, vp, vp, i64, i32, i32, vp, sz,
                                                      vp, vp, vp, vp]),
+        "kpool_attend_expanded_workspace_bytes": (sz, [vp, vp, i32, i32, i32, i32, i32]),
+        "kpool_attend_expanded": (ctypes.c_int, [vp, i64, vp, i64, i64, vp, i64, vp, i64, i64, vp, vp, vp, vp, i32, i32,
+                                                 i32, i32, i32, f32, vp, sz, vp, vp, vp]),
+        "kpool_attend_expanded_backward_workspace_bytes": (sz, [vp, vp, i32, i32, i32, i32, i32]),
+        "kpool_attend_expanded_backward": (ctypes.c_int, [vp, vp, i64, vp, i64, i64, vp, i64, vp, i64, i64, vp, vp, vp, vp,
+                                                          vp, vp, i32, i32, i32, i32, i32, f32, vp, sz, vp, vp, vp, vp, vp]),
         "kpool_attend_latent_workspace_bytes": (sz, [vp, i32, i32, i32, i32, i32]),
         "kpool_attend_latent": (ctypes.c_int, [vp, i64, vp, i64, i64, vp, i32, i32, vp, vp, i32, vp, vp, i32, i32, i32,
                                                i32, f32, vp, sz, vp, vp, vp]),
@@ -537,6 +543,124 @@ def attend_selected(q, k, v, token_ids, cu_q, cu_q_dev, cu_k=None, cu_k_dev=None
                                          _bytes(ws, q.device), _at(out), _at(lse), s)
     _check(rc, "kpool_attend_selected")
     return out, lse
+
+
+def _spaced_heads(t, name, device, codes):
+    """t as packed tokens [T, H, D] of bf16 with any token and head stride: (T, H, D, stride, head stride)."""
+    if t.dim() != 3 or not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a device tensor [T, heads, D] on {device}")
+    if t.dtype not in codes:
+        raise ValueError(f"{name} must be bfloat16 (or int16 bit patterns)")
+    T, H, D = t.shape
+    s0, s1, s2 = t.stride()
+    if s2 != 1 and D > 1:
+        raise ValueError(f"the values of a head of {name} must be contiguous")
+    s1 = s1 if H > 1 else D
+    return T, H, D, s0 if T > 1 else (H - 1) * s1 + D, s1
+
+
+class _Expanded:
+    """The arguments that the expanded form's calls share, checked."""
+
+    def __init__(self, q, k, k_pe, v, cu_q, cu_q_dev, cu_k, cu_k_dev, scale):
+        import torch
+        codes = (torch.bfloat16, torch.int16)
+        self.device = device = q.device
+        tq, self.Hq, width, qs = _heads(q, "q", device, codes)
+        tk, self.Hkv, self.D, ks, kh = _spaced_heads(k, "k", device, codes)
+        tv, hv, dv, vs, vh = _spaced_heads(v, "v", device, codes)
+        if k_pe.dim() != 2:
+            raise ValueError("k_pe must be [T, P]")
+        tp, _, self.P, ps, _ = _spaced_heads(k_pe[:, None], "k_pe", device, codes)
+        if hv != self.Hkv or dv != self.D or width != self.D + self.P:
+            raise ValueError("k and v must agree in their heads and D, and q have D + P values a head")
+        self.cu_q, q_dev, self.cu_k, k_dev = _cu_pair(cu_q, cu_q_dev, cu_k, cu_k_dev, device)
+        q_ptr = _host_address(self.cu_q)
+        k_ptr = q_ptr if self.cu_k is self.cu_q else _host_address(self.cu_k)
+        self.Tq, self.Tk = int(self.cu_q[-1]), int(self.cu_k[-1])
+        if tq < self.Tq or min(tk, tv, tp) < self.Tk:
+            raise ValueError("q, k, k_pe or v has fewer tokens than its cumulative lengths say")
+        nseq = len(self.cu_q) - 1
+        scale = float(np.float32(1.0) / np.sqrt(np.float32(width))) if scale is None else scale
+        self.lens = (q_ptr, k_ptr, nseq, self.Hq, self.Hkv, self.D, self.P)
+        self.rows = (q.data_ptr(), qs, k.data_ptr(), ks, kh, k_pe.data_ptr(), ps, v.data_ptr(), vs, vh)
+        self.cu = (q_ptr, q_dev.data_ptr(), k_ptr, k_dev.data_ptr(), nseq, self.Hq, self.Hkv, self.D, self.P, scale)
+
+
+def _expanded_bytes(fn, cu_q, cu_k, Hq, Hkv, D, P):
+    cu_q, qp = _host_i32(cu_q)
+    cu_k, kp = _host_i32(cu_k)
+    if cu_q.ndim != 1 or cu_k.shape != cu_q.shape:
+        raise ValueError("cu_q and cu_k must be 1-dimensional with nseq + 1 entries each")
+    return _latent_bytes(fn, qp, kp, len(cu_q) - 1, Hq, Hkv, D, P)
+
+
+def attend_expanded_workspace_bytes(cu_q, cu_k, Hq: int, Hkv: int, D: int, P: int) -> int:
+    """Workspace of attend_expanded for these sequences (0 where it needs none)."""
+    return _expanded_bytes("kpool_attend_expanded_workspace_bytes", cu_q, cu_k, Hq, Hkv, D, P)
+
+
+def attend_expanded(q, k, k_pe, v, cu_q, cu_q_dev, cu_k=None, cu_k_dev=None, scale: float | None = None, out=None,
+                    want_lse: bool = False, lse=None, workspace=None, stream=None):
+    """Latent attention with expanded keys and values, as attend: (o, lse or None).
+
+    q bf16 [Tq, Hq, D + P]; k and v bf16 [Tk, Hkv, D] of any token and head stride (the two halves of one
+    projection's heads, say); k_pe bf16 [Tk, P], the keys' positional part, which all heads share.  scale
+    is 1 / sqrt(D + P) by default; the rest is attend's.  attend_expanded_backward has its gradients; new
+    tokens over a cache take attend_latent."""
+    import torch
+    _refuse_graph("attend_expanded", q, k, k_pe, v)
+    a = _Expanded(q, k, k_pe, v, cu_q, cu_q_dev, cu_k, cu_k_dev, scale)
+    with _OnDevice(q, stream) as s:
+        shape = (a.Tq, a.Hq, a.D)
+        if out is None:
+            out = torch.empty(shape, dtype=q.dtype, device=a.device)
+        else:
+            _like(out, "out", shape, q.dtype, a.device)
+        if lse is not None:
+            _like(lse, "lse", shape[:2], torch.float32, a.device)
+        elif want_lse:
+            lse = torch.empty(shape[:2], dtype=torch.float32, device=a.device)
+        if workspace is None:
+            nb = int(lib().kpool_attend_expanded_workspace_bytes(*a.lens))
+            workspace = torch.empty(nb, dtype=torch.uint8, device=a.device) if nb else None
+        rc = lib().kpool_attend_expanded(*a.rows, *a.cu, _at(workspace), _bytes(workspace, a.device), _at(out), _at(lse), s)
+    _check(rc, "kpool_attend_expanded")
+    return out, lse
+
+
+def attend_expanded_backward_workspace_bytes(cu_q, cu_k, Hq: int, Hkv: int, D: int, P: int) -> int:
+    """Workspace of attend_expanded_backward for these sequences."""
+    return _expanded_bytes("kpool_attend_expanded_backward_workspace_bytes", cu_q, cu_k, Hq, Hkv, D, P)
+
+
+def attend_expanded_backward(d_o, q, k, k_pe, v, o, lse, cu_q, cu_q_dev, cu_k=None, cu_k_dev=None,
+                             scale: float | None = None, workspace=None, dq=None, dk=None, dk_pe=None, dv=None, stream=None):
+    """Gradients (dq, dk, dk_pe, dv) of attend_expanded: d_o is the gradient of o [Tq, Hq, D]; o and lse are
+    what attend_expanded returned (want_lse=True); the rest are its arguments.  dq is [Tq, Hq, D + P], dk and
+    dv [Tk, Hkv, D], dk_pe [Tk, P], in bf16."""
+    import torch
+    a = _Expanded(q, k, k_pe, v, cu_q, cu_q_dev, cu_k, cu_k_dev, scale)
+    rows, keys = (a.Tq, a.Hq, a.D), (a.Tk, a.Hkv, a.D)
+    _like(d_o, "d_o", rows, q.dtype, q.device)
+    _like(o, "o", rows, q.dtype, q.device)
+    _like(lse, "lse", rows[:2], torch.float32, q.device)
+    with _OnDevice(q, stream) as s:
+        out = []
+        for t, name, shape in ((dq, "dq", (a.Tq, a.Hq, a.D + a.P)), (dk, "dk", keys), (dk_pe, "dk_pe", (a.Tk, a.P)),
+                               (dv, "dv", keys)):
+            if t is None:
+                t = torch.empty(shape, dtype=q.dtype, device=q.device)
+            else:
+                _like(t, name, shape, q.dtype, q.device)
+            out.append(t)
+        if workspace is None:
+            nb = int(lib().kpool_attend_expanded_backward_workspace_bytes(*a.lens))
+            workspace = torch.empty(nb, dtype=torch.uint8, device=a.device) if nb else None
+        rc = lib().kpool_attend_expanded_backward(_at(d_o), *a.rows, _at(o), _at(lse), *a.cu, _at(workspace),
+                                                  _bytes(workspace, q.device), *(_at(t) for t in out), s)
+    _check(rc, "kpool_attend_expanded_backward")
+    return tuple(out)
 
 
 class _Latent:
