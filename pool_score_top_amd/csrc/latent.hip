@@ -61,23 +61,30 @@ __device__ inline int share_start(int total, int n, int share) {
   return each * share + (total - each * n) * share / n;
 }
 
-template <int NB, int RB, bool LIST>
+// A workgroup's tiles and LDS, NB blocks of 128 columns wide (R padded), for BQ rows.
+template <int NB, int ROWS, bool LIST>
 struct Latent {
-  static constexpr int BK = kLatentKeys, BQ = 16 * RB;
-  // waves by groups of rows and of keys for S: a wave's blocks of 16 rows and of 16 keys
-  static constexpr int RG = RB == 4 ? 2 : 1, KG = 4 / RG, RW = RB / RG, KW = 4 / KG;
-  static constexpr int KS = NB * 4 + 2;             // contraction steps of 32: the latent part, then the positional
-  static constexpr int CB = NB * 2;                 // 16-column blocks of a wave
+  static constexpr int BK = kLatentKeys, BQ = ROWS;
   static constexpr int BLOCKB = BK * 256;           // bytes of 128 columns of a tile
-  static constexpr int TILE = NB * BLOCKB + BK * 128;
+  static constexpr int PE = NB * BLOCKB;            // where the positional part lies in it
+  static constexpr int TILE = PE + BK * 128;
+  static constexpr int LOADS = 4 * NB + 2;          // a wave's loads of a tile
   static constexpr int EACH = LIST ? 8 : 4, BLOCK = EACH * 256;
   // P; the rows of a block's keys, and, whole keys, their places.  What is used between tiles only
   // lies in the tiles (counts, the queries on their way to registers) or in P (exchanges of
   // maxima and sums), and a tile's four flags where the first keys of the list were, which are loaded.
-  static constexpr int P = 2 * TILE, ROWS = P + BQ * BK * 2, PLACES = ROWS + BLOCK * 4,
+  static constexpr int P = 2 * TILE, KEYS = P + BQ * BK * 2, PLACES = KEYS + BLOCK * 4,
                        LDS = PLACES + (LIST ? 0 : BLOCK * 4);
-  static constexpr int QROW = KS * 64 + 16;  // bytes of a row of queries in LDS (16 rows over all banks)
-  static_assert(LDS <= 163840 && BQ * QROW <= 2 * TILE && 4 * BQ * 4 <= BQ * BK * 2, "LDS");
+  static constexpr int CHUNKS = NB * 16 + 8;    // of 16 bytes in a row of queries
+  static constexpr int QROW = CHUNKS * 16 + 16;  // its bytes in LDS (16 rows over all banks)
+  static_assert(LDS <= 163840 && BQ * QROW <= TILE + BQ * BK * 2 && 4 * BQ * 4 <= BQ * BK * 2, "LDS");
+};
+
+// What a wave knows of a tile in LDS
+struct TileKeys {
+  uint32_t at;        // its first byte
+  int first, present;  // number of its first key in the block, keys of the block
+  bool masked;         // whether some row does not see some key
 };
 
 // n tokens of a sequence, at most what the caller said and what its pages hold
@@ -113,14 +120,409 @@ __device__ inline int scan_256(int x, int *scratch) {
   return x;
 }
 
+// Up to 32 rows, by products of 16 rows: wave w has keys 16 w .. 16 w + 15 of a tile and all RB blocks
+// of rows for S, columns w R / 4 .. and all rows for O.
+template <int NB, int RB, bool LIST>
+struct Latent16 {
+  using C = Latent<NB, 16 * RB, LIST>;
+  using S = Keys16<128>;
+  using SP = Keys16<64>;
+  static constexpr int KS = NB * 4 + 2;  // contraction steps of 32: the latent part, then the positional
+  static constexpr int CB = NB * 2;      // 16-column blocks of a wave
+  static constexpr int VALUES = 2 * CB, AHEAD = VALUES < 6 ? VALUES : 6;
+  int wave, lane, col, group;
+  // addresses are kept as few registers and made where they are used: (a ^ b) + c is one instruction
+  uint32_t krow, kpe, vcol;
+  bf16x8 q[RB][KS];
+  f32x4 o[CB][RB], s[RB];
+  float m[RB], l[RB], part[RB], top[RB];
+  int t[RB];  // positions of the lane's rows (whole keys)
+  bf16x8 v[VALUES], p[2][RB];
+
+  __device__ inline void init(int wave_, int lane_) {
+    wave = wave_, lane = lane_, col = lane & 15, group = lane >> 4;
+    const int key = 4 * group + (col >> 2);
+    krow = (wave * 16 + col) * 256 + ((group ^ S::swz(col)) << 4);
+    kpe = (wave * 16 + col) * 128 + ((group ^ SP::swz(col)) << 4);
+    vcol = key * 256 + ((((col & 3) >> 1) ^ S::swz(key)) << 4) + (col & 1) * 8;
+    opaque(krow), opaque(kpe), opaque(vcol);
+  }
+  // position(r): the token position of row r
+  template <class F>
+  __device__ inline void begin(uint32_t queries, F &&position) {
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      const int r = rb * 16 + col;
+      t[rb] = LIST ? 0 : position(r);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        q[rb][ks] = lds_read(queries + r * C::QROW + ks * 64 + group * 16);
+        to_accumulation(q[rb][ks]);
+      }
+      m[rb] = -__builtin_inff(), l[rb] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < CB; ++c) o[c][rb] = f32x4{};
+    }
+  }
+  __device__ inline bf16x8 key(const TileKeys &k, int ks) const {
+    return ks < NB * 4 ? lds_read((krow ^ ((ks & 3) << 6)) + (k.at + (ks >> 2) * C::BLOCKB))
+                       : lds_read((kpe ^ ((ks & 1) << 6)) + (k.at + C::PE));
+  }
+  __device__ inline bf16x8 value(const TileKeys &k, int i) const {  // columns i % CB of the wave's, keys 32 (i / CB) ..
+    const int c = wave * CB + i % CB;
+    const uint32_t at = (vcol ^ ((c & 7) << 5)) + (k.at + (c >> 3) * C::BLOCKB + i / CB * 32 * 256);
+    return lds_read_cols(at, at + 16 * 256);
+  }
+  // S.  Keys are read a few steps ahead; the next tile's loads go out beside the products, a load's
+  // address and the load itself apart (a product takes 16 cycles, of which 12 are left for others).
+  template <class L>
+  __device__ inline void scores(const TileKeys &k, L &&loads) {
+    constexpr int KAHEAD = 4;
+    bf16x8 kr[KS];
+#pragma unroll
+    for (int n = 0; n < KAHEAD; ++n) kr[n] = key(k, n);
+#pragma unroll
+    for (int n = 0; n < KS; ++n) {
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) {
+        __builtin_amdgcn_sched_barrier(0);
+        s[rb] = mfma(kr[n], q[rb][n], n == 0 ? f32x4{} : s[rb]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (rb == 0) loads.address(n);
+        if (rb == 0 && RB > 1) __builtin_amdgcn_sched_barrier(0);
+        if (rb == RB - 1) {
+          loads.issue(n);
+          if (n + KAHEAD < KS) kr[n + KAHEAD] = key(k, n + KAHEAD);
+        }
+      }
+    }
+    static_assert(KS == C::LOADS, "a load a step");
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  __device__ inline void mask(const TileKeys &k, const int *places) {
+    if (!k.masked) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = k.first + wave * 16 + 4 * group + i;
+      const bool absent = n >= k.present;
+      const int place = absent || LIST ? 0 : places[n];
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb)
+        if (absent || (!LIST && place > t[rb])) s[rb][i] = -__builtin_inff();
+    }
+  }
+  // P to LDS, with the maxima so far
+  __device__ inline void weights(uint32_t to, float c) {
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      const float shift = m[rb] > -__builtin_inff() ? m[rb] : 0.0f;
+      float x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = exp2f_fast(fmaf(s[rb][i], c, -shift));
+      part[rb] = (x[0] + x[1]) + (x[2] + x[3]);
+      // row r: 16-byte chunks, each with a lane group's 8 keys of a contraction of 32 in the order of
+      // lds_read_cols
+      const int r = rb * 16 + col, chunk = (wave >> 1) * 4 + group;
+      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+      *(KPOOL_LDS u32x2 *)(uintptr_t)(to + r * 128 + ((chunk ^ (r & 7)) << 4) + (wave & 1) * 8) =
+          u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+    }
+  }
+  // whether a score lies far above its row's maximum so far (m = -inf: any visible key)
+  __device__ inline bool over(float c) {
+    bool far = false;
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      top[rb] = fmaxf(fmaxf(s[rb][0], s[rb][1]), fmaxf(s[rb][2], s[rb][3]));
+      far |= top[rb] * c > m[rb] + 8.0f;
+    }
+    return far;
+  }
+  // a value of each row, found over the lanes that share it, to the exchange [4][BQ]
+  template <class F>
+  __device__ inline void give(float *exchange, const float (&x)[RB], F &&join) const {
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      const Pair y = row_pair(x[rb]);
+      const float z = join(y.a, y.b), all = join(z, other_half(z));
+      if (lane < 16) exchange[wave * C::BQ + rb * 16 + col] = all;
+    }
+  }
+  __device__ inline void give_top(float *exchange) const {
+    give(exchange, top, [](float a, float b) { return fmaxf(a, b); });
+  }
+  __device__ inline void raise(const float *exchange, float c) {
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      const float *x = exchange + rb * 16 + col;
+      const float most = fmaxf(fmaxf(x[0], x[C::BQ]), fmaxf(x[2 * C::BQ], x[3 * C::BQ])) * c;
+      if (most > m[rb] + 8.0f) {  // (the same in every wave)
+        const float f = exp2f_fast(m[rb] - most);  // m = -inf gives 0
+        m[rb] = most, l[rb] *= f;
+#pragma unroll
+        for (int b = 0; b < CB; ++b) o[b][rb] *= f;
+      }
+    }
+  }
+  __device__ inline void read_values(const TileKeys &k) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) v[i] = value(k, i);
+  }
+  __device__ inline void read_p(uint32_t from, int kc) {
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      const int r = rb * 16 + col;
+      p[kc][rb] = lds_read(from + r * 128 + (((kc * 4 + group) ^ (r & 7)) << 4));
+    }
+  }
+  __device__ inline void first_p(uint32_t from) { read_p(from, 0); }
+  // O, once read_values and first_p have begun
+  __device__ inline void values(const TileKeys &k, uint32_t p_at) {
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) l[rb] += part[rb];
+#pragma unroll
+    for (int i = 0; i < VALUES; ++i) {
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) {
+        __builtin_amdgcn_sched_barrier(0);
+        o[i % CB][rb] = mfma(v[i], p[i / CB][rb], o[i % CB][rb]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (rb == 0 && i + AHEAD < VALUES) v[i + AHEAD] = value(k, i + AHEAD);
+      }
+      if (i == 1) read_p(p_at, 1);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  __device__ inline void give_sum(float *exchange) const {
+    give(exchange, l, [](float a, float b) { return a + b; });
+  }
+  // out(r, lse) for the rows, then to8(r, column, 8 values packed) or to4(r, column, 4 values)
+  template <class L, class F8, class F4>
+  __device__ inline void finish(const float *exchange, bool whole, L &&out, F8 &&to8, F4 &&to4) const {
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      const int r = rb * 16 + col;
+      const float *x = exchange + r;
+      const float sum = (x[0] + x[C::BQ]) + (x[2 * C::BQ] + x[3 * C::BQ]);
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      if (wave == 0 && group == 0) out(r, m[rb], sum);
+#pragma unroll
+      for (int c = 0; c < CB; c += 2) {
+        const int d = (wave * CB + c) * 16;
+        const f32x4 y0 = o[c][rb] * inv, y1 = o[c + 1][rb] * inv;
+        if (whole) {
+          // lane groups exchange halves: groups 0 and 2 take 8 columns each of the first block, 1 and 3 of
+          // the second
+          const auto a = __builtin_amdgcn_permlane16_swap(pack_bf16(y0[0], y0[1]), pack_bf16(y1[0], y1[1]), false, false);
+          const auto b = __builtin_amdgcn_permlane16_swap(pack_bf16(y0[2], y0[3]), pack_bf16(y1[2], y1[3]), false, false);
+          to8(r, d + (group & 1) * 16 + (group >> 1) * 8, make_uint4(a[0], b[0], a[1], b[1]));
+        } else {
+          to4(r, d + group * 4, y0);
+          to4(r, d + 16 + group * 4, y1);
+        }
+      }
+    }
+  }
+};
+
+// 64 rows, by products of 32 rows, half as many instructions for the same work: wave w has 32 keys (w / 2)
+// and 32 rows (w % 2) for S, columns w R / 4 .. and all rows for O.  Queries of 64 rows for 16 keys a
+// wave would read each key once instead of twice, but take 288 registers beside O's 128: they spill.
+template <int NB, bool LIST>
+struct Latent32 {
+  using C = Latent<NB, 64, LIST>;
+  using S = Keys<128>;
+  using SP = Keys<64>;
+  static constexpr int KS = NB * 8 + 4;  // contraction steps of 16
+  static constexpr int CB = NB;          // 32-column blocks of a wave
+  static constexpr int VALUES = 4 * CB, AHEAD = VALUES < 6 ? VALUES : 6;
+  int wave, lane, col, half, rows0, keys0;
+  uint32_t krow, kpe, vcol0, vcol1;
+  bf16x8 q[KS];
+  f32x16 o[CB][2], s;
+  float m[2], l, part, top;  // m: of rows l % 32 and 32 + l % 32; the others of the wave's own row
+  int t;
+  bf16x8 v[VALUES], p[4][2];
+
+  __device__ inline void init(int wave_, int lane_) {
+    wave = wave_, lane = lane_, col = lane & 31, half = lane >> 5;
+    rows0 = (wave & 1) * 32, keys0 = (wave >> 1) * 32;
+    krow = keys0 * 256 + S::row_base(lane), kpe = keys0 * 128 + SP::row_base(lane);
+    vcol0 = S::col_base(lane, 0), vcol1 = S::col_base(lane, 1);
+    opaque(krow), opaque(kpe), opaque(vcol0), opaque(vcol1);
+  }
+  template <class F>
+  __device__ inline void begin(uint32_t queries, F &&position) {
+    t = LIST ? 0 : position(rows0 + col);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      q[ks] = lds_read(queries + (rows0 + col) * C::QROW + ks * 32 + half * 16);
+      to_accumulation(q[ks]);
+    }
+    l = 0.0f;
+#pragma unroll
+    for (int rb = 0; rb < 2; ++rb) {
+      m[rb] = -__builtin_inff();
+#pragma unroll
+      for (int c = 0; c < CB; ++c) o[c][rb] = f32x16{};
+    }
+  }
+  __device__ inline float own() const {
+    const float first = m[0], second = m[1];
+    return rows0 ? second : first;
+  }
+  __device__ inline bf16x8 key(const TileKeys &k, int ks) const {
+    return ks < NB * 8 ? lds_read((krow ^ ((ks & 7) << 5)) + (k.at + (ks >> 3) * C::BLOCKB))
+                       : lds_read((kpe ^ ((ks & 3) << 5)) + (k.at + C::PE));
+  }
+  __device__ inline bf16x8 value(const TileKeys &k, int i) const {  // columns i % CB of the wave's, keys 16 (i / CB) ..
+    const int c = wave * CB + i % CB;
+    const uint32_t to = k.at + (c >> 2) * C::BLOCKB + i / CB * 16 * 256;
+    return lds_read_cols((vcol0 ^ ((c & 3) << 6)) + to, (vcol1 ^ ((c & 3) << 6)) + to);
+  }
+  // (two sums in turn: a product's result is not there yet when the next one starts)
+  template <class L>
+  __device__ inline void scores(const TileKeys &k, L &&loads) {
+    constexpr int KAHEAD = 4;
+    bf16x8 kr[KS];
+    f32x16 x[2];
+#pragma unroll
+    for (int n = 0; n < KAHEAD; ++n) kr[n] = key(k, n);
+#pragma unroll
+    for (int n = 0; n < KS; ++n) {
+      __builtin_amdgcn_sched_barrier(0);
+      x[n & 1] = mfma(kr[n], q[n], n < 2 ? f32x16{} : x[n & 1]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (n + KAHEAD < KS) kr[n + KAHEAD] = key(k, n + KAHEAD);
+      if (n & 1) loads.issue(n / 2);
+      else loads.address(n / 2);
+    }
+    static_assert(KS == 2 * C::LOADS, "a load for two steps");
+    __builtin_amdgcn_sched_barrier(0);
+    s = x[0] + x[1];
+  }
+  __device__ inline void mask(const TileKeys &k, const int *places) {
+    if (!k.masked) return;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int n = k.first + keys0 + 8 * (i / 4) + 4 * half + i % 4;
+      const bool absent = n >= k.present;
+      if (absent || (!LIST && places[absent ? 0 : n] > t)) s[i] = -__builtin_inff();
+    }
+  }
+  __device__ inline void weights(uint32_t to, float c) {
+    const float most = own(), shift = most > -__builtin_inff() ? most : 0.0f;
+    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    f32x16 x;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      x[i] = exp2f_fast(fmaf(s[i], c, -shift));
+      sum[i % 4] += x[i];
+    }
+    part = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    // 16-byte chunks of row r, each with a lane half's 8 keys of 16
+    const int r = rows0 + col;
+#pragma unroll
+    for (int kc = 0; kc < 2; ++kc)
+      *(KPOOL_LDS bf16x8 *)(uintptr_t)(to + r * 128 + (((keys0 / 8 + kc * 2 + half) ^ (r & 7)) << 4)) = as_operand(x, kc);
+  }
+  __device__ inline bool over(float c) {
+    top = s[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+    return top * c > own() + 8.0f;
+  }
+  __device__ inline void give_top(float *exchange) const {
+    const float x = fmaxf(top, other_half(top));
+    if (lane < 32) exchange[(wave >> 1) * 64 + rows0 + col] = x;
+  }
+  __device__ inline void raise(const float *exchange, float c) {
+#pragma unroll
+    for (int rb = 0; rb < 2; ++rb) {
+      const float most = fmaxf(exchange[rb * 32 + col], exchange[64 + rb * 32 + col]) * c;
+      if (most > m[rb] + 8.0f) {  // (the same in every wave)
+        const float f = exp2f_fast(m[rb] - most);  // m = -inf gives 0
+        m[rb] = most;
+        if (rows0 == rb * 32) l *= f;
+#pragma unroll
+        for (int b = 0; b < CB; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[b][rb][i] *= f;
+      }
+    }
+  }
+  __device__ inline void read_values(const TileKeys &k) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) v[i] = value(k, i);
+  }
+  __device__ inline void read_p(uint32_t from, int kc) {
+#pragma unroll
+    for (int rb = 0; rb < 2; ++rb) {
+      const int r = rb * 32 + col;
+      p[kc][rb] = lds_read(from + r * 128 + (((kc * 2 + half) ^ (r & 7)) << 4));
+    }
+  }
+  __device__ inline void first_p(uint32_t from) { read_p(from, 0), read_p(from, 1); }
+  __device__ inline void values(const TileKeys &k, uint32_t p_at) {
+    l += part;
+#pragma unroll
+    for (int i = 0; i < VALUES; ++i) {
+#pragma unroll
+      for (int rb = 0; rb < 2; ++rb) {
+        __builtin_amdgcn_sched_barrier(0);
+        o[i % CB][rb] = mfma(v[i], p[i / CB][rb], o[i % CB][rb]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (rb == 0 && i + AHEAD < VALUES) v[i + AHEAD] = value(k, i + AHEAD);
+        if (rb == 1 && i < 2) read_p(p_at, 2 + i);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  __device__ inline void give_sum(float *exchange) const {
+    const float x = l + other_half(l);
+    if (lane < 32) exchange[(wave >> 1) * 64 + rows0 + col] = x;
+  }
+  template <class L, class F8, class F4>
+  __device__ inline void finish(const float *exchange, bool whole, L &&out, F8 &&to8, F4 &&to4) const {
+#pragma unroll
+    for (int rb = 0; rb < 2; ++rb) {
+      const int r = rb * 32 + col;
+      const float sum = exchange[r] + exchange[64 + r];
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      if (wave == 0 && half == 0) out(r, m[rb], sum);
+#pragma unroll
+      for (int c = 0; c < CB; ++c)
+#pragma unroll
+        for (int i = 0; i < 16; i += 8) {
+          const int d = (wave * CB + c) * 32 + 2 * i;
+          f32x4 y0, y1;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) y0[u] = o[c][rb][i + u] * inv, y1[u] = o[c][rb][i + 4 + u] * inv;
+          if (whole) {
+            // the halves exchange: the first takes 8 columns of the first 8, the second those of the next
+            const auto a = __builtin_amdgcn_permlane32_swap(pack_bf16(y0[0], y0[1]), pack_bf16(y1[0], y1[1]), false, false);
+            const auto b = __builtin_amdgcn_permlane32_swap(pack_bf16(y0[2], y0[3]), pack_bf16(y1[2], y1[3]), false, false);
+            to8(r, d + half * 8, make_uint4(a[0], b[0], a[1], b[1]));
+          } else {
+            to4(r, d + half * 4, y0);
+            to4(r, d + 8 + half * 4, y1);
+          }
+        }
+    }
+  }
+};
+
+template <int NB, int RB, bool LIST>
+using LatentRows = std::conditional_t<RB == 4, Latent32<NB, LIST>, Latent16<NB, RB == 4 ? 1 : RB, LIST>>;
+
 template <int NB, int RB, bool LIST>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void latent_kernel(LatentArgs a) {
-  using C = Latent<NB, RB, LIST>;
+  using R = LatentRows<NB, RB, LIST>;
+  using C = typename R::C;
   constexpr int BK = C::BK, BQ = C::BQ, TILE = C::TILE;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int col = lane & 15, group = lane >> 4;
   const uint32_t lds0 = lds_offset(lds);
 
   // this workgroup's share of all tiles: [pos, hi), from sequence `seq` on, whose tiles begin at `before`
@@ -169,27 +571,18 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     before = __builtin_amdgcn_readfirstlane(scratch[5]), seq = __builtin_amdgcn_readfirstlane(scratch[6]);
   }
 
-  // Addresses are kept as few registers and made where they are used (one instruction, (a ^ b) + c):
-  // fragments of a wave's 16 keys, whose step of 32 is ^ (step << 6) in the latent part; of its columns,
-  // whose block of 16 is ^ (block << 5)
-  const int key0 = wave / C::RG * 16 * C::KW, wrow = wave % C::RG * 16 * C::RW;  // of the wave's part of S
-  uint32_t krow, kpe, vcol;
-  {
-    const int r = lane & 15, key = 4 * group + (r >> 2);
-    krow = (key0 + r) * 256 + ((group ^ Keys16<128>::swz(r)) << 4);
-    kpe = (key0 + r) * 128 + ((group ^ Keys16<64>::swz(r)) << 4);
-    vcol = key * 256 + ((((r & 3) >> 1) ^ Keys16<128>::swz(key)) << 4) + (r & 1) * 8;
-    opaque(krow), opaque(kpe), opaque(vcol);
-  }
+  R r;
+  r.init(wave, lane);
   // Loads: of the latent part 4 NB a wave, 4 rows each; of the positional one 2 a wave, 8 rows each.  A
-  // lane's chunk of its row is lchunk ^ swz(4 i) (i the load's place in 16 rows), its last where the row
-  // ends before it.
-  constexpr int LOADS = 4 * NB + 2;
-  const uint32_t last_chunk = a.R / 8 - 1, pitch = (uint32_t)a.cs * 2;
-  uint32_t lchunk = wave * NB / 4 * 16 + ((lane & 15) ^ Keys16<128>::swz(group)),
-           pcol = (a.R + (a.P ? min((lane & 7) ^ Keys16<64>::swz(lane >> 3), a.P / 8 - 1) * 8 : -8)) * 2;
-  uint32_t rows_at = lds0 + C::ROWS + (wave * 4 * NB % 16 * 4 + group) * 4, pe_rows_at = lds0 + C::ROWS + (wave * 16 + (lane >> 3)) * 4;
-  opaque(lchunk), opaque(pcol), opaque(rows_at), opaque(pe_rows_at);
+  // lane's chunk of its row is chunk ^ swz(4 i) (i the load's place in 16 rows; 8 i), its last where the
+  // row ends before it.
+  constexpr int LOADS = C::LOADS;
+  const uint32_t last_chunk = a.R / 8 - 1, last_pe = max(a.P / 8 - 1, 0), pitch = (uint32_t)a.cs * 2;
+  const uint32_t pe_at = (a.P ? a.R : 0) * 2;
+  uint32_t chunk = wave * NB / 4 * 16 + ((lane & 15) ^ R::S::swz(lane >> 4)), pe_chunk = (lane & 7) ^ R::SP::swz(lane >> 3);
+  uint32_t rows_at = lds0 + C::KEYS + (wave * 4 * NB % 16 * 4 + (lane >> 4)) * 4,
+           pe_rows_at = lds0 + C::KEYS + (wave * 16 + (lane >> 3)) * 4;
+  opaque(chunk), opaque(pe_chunk), opaque(rows_at), opaque(pe_rows_at);
   auto read_rows = [&](int tile, uint32_t (&at)[LOADS]) {
     const uint32_t r = rows_at + tile * BK * 4, pe = pe_rows_at + tile * BK * 4;
 #pragma unroll
@@ -197,14 +590,14 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
       at[n] = *(KPOOL_LDS const uint32_t *)(uintptr_t)(n < 4 * NB ? r + n * 16 : pe + (n - 4 * NB) * 32);
   };
   auto address = [&](int n, uint32_t row) {
-    uint32_t off = pcol;
-    if (n < 4 * NB) off = min(lchunk ^ (uint32_t)Keys16<128>::swz(n % 4 * 4), last_chunk) * 16;
+    const uint32_t off = n < 4 * NB ? min(chunk ^ (uint32_t)R::S::swz(n % 4 * 4), last_chunk) * 16
+                                    : min(pe_chunk ^ (uint32_t)R::SP::swz((n & 1) * 8), last_pe) * 16 + pe_at;
     return (const char *)a.cache + (uint64_t)row * pitch + off;
   };
   auto load_row = [&](int n, const char *from, uint32_t to) {  // to: the tile's buffer
-    load_lds_16(from, to + (n < 4 * NB ? (wave * 4 * NB + n) * 1024 : NB * C::BLOCKB + (wave * 2 + n - 4 * NB) * 1024));
+    load_lds_16(from, to + (n < 4 * NB ? (wave * 4 * NB + n) * 1024 : C::PE + (wave * 2 + n - 4 * NB) * 1024));
   };
-  int *list = reinterpret_cast<int *>(lds + C::ROWS), *places = reinterpret_cast<int *>(lds + C::PLACES);
+  int *list = reinterpret_cast<int *>(lds + C::KEYS), *places = reinterpret_cast<int *>(lds + C::PLACES);
   float *exchange = reinterpret_cast<float *>(lds + C::P);  // [4][BQ]
 
   while (pos < hi) {
@@ -240,12 +633,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     // queries to LDS (behind the first tile), whole rows at a time, and from there to registers
     __syncthreads();
     {
-      constexpr int CHUNKS = C::KS * 4, THREADS = 256 / BQ, BATCH = (CHUNKS + THREADS - 1) / THREADS;  // of a row
+      constexpr int CHUNKS = C::CHUNKS, THREADS = 256 / BQ, BATCH = (CHUNKS + THREADS - 1) / THREADS;  // of a row
       uint32_t tid = threadIdx.x;  // (opaque: what depends on it is not worth a register from one unit to the next)
       opaque(tid);
-      const int r = tid / THREADS, c0 = tid % THREADS, at = (n0 + r) / a.H;
-      const int latent = r < nrows ? a.R / 8 : 0, pe = r < nrows ? NB * 16 + a.P / 8 : 0;  // ends of its parts
-      const uint16_t *src = a.q + (int64_t)(q_start + at) * a.qs + (n0 + r - at * a.H) * (a.R + a.P) + c0 * 8;
+      const int row = tid / THREADS, c0 = tid % THREADS, at = (n0 + row) / a.H;
+      const int latent = row < nrows ? a.R / 8 : 0, pe = row < nrows ? NB * 16 + a.P / 8 : 0;  // ends of its parts
+      const uint16_t *src = a.q + (int64_t)(q_start + at) * a.qs + (n0 + row - at * a.H) * (a.R + a.P) + c0 * 8;
       uint4 z[BATCH];
 #pragma unroll
       for (int u = 0; u < BATCH; ++u) {
@@ -258,36 +651,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
 #pragma unroll
       for (int u = 0; u < BATCH; ++u)
         if (CHUNKS % THREADS == 0 || c0 + u * THREADS < CHUNKS)
-          *reinterpret_cast<uint4 *>(lds + TILE + r * C::QROW + (c0 + u * THREADS) * 16) = z[u];
+          *reinterpret_cast<uint4 *>(lds + TILE + row * C::QROW + (c0 + u * THREADS) * 16) = z[u];
     }
     __syncthreads();
-    bf16x8 q[C::RW][C::KS];
-    int t[C::RW];
-#pragma unroll
-    for (int rb = 0; rb < C::RW; ++rb) {
-      const int r = wrow + rb * 16 + col;
-      t[rb] = LIST ? 0 : (n0 + r) / a.H + len - Lq;
-#pragma unroll
-      for (int ks = 0; ks < C::KS; ++ks) {
-        q[rb][ks] = lds_read(lds0 + TILE + r * C::QROW + ks * 64 + group * 16);
-        to_accumulation(q[rb][ks]);
-      }
-    }
-    f32x4 o[C::CB][RB];
-    float m[RB], l[C::RW];  // the maxima of all rows, the wave's part of its rows' sums
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-      m[rb] = -__builtin_inff();
-#pragma unroll
-      for (int c = 0; c < C::CB; ++c) o[c][rb] = f32x4{};
-    }
-#pragma unroll
-    for (int rb = 0; rb < C::RW; ++rb) l[rb] = 0.0f;
-    // m of the wave's row block rb (its group is the same for the wave)
-    auto own = [&](int rb) {
-      const float first = m[rb], other = m[RB - C::RW + rb];
-      return wrow == 0 ? first : other;
-    };
+    r.begin(lds0 + TILE, [&](int row) { return (n0 + row) / a.H + len - Lq; });
 
     for (int block = e_lo; block < e_hi; block += C::BLOCK) {
       // the block's keys that exist, in order: their rows (and places) in LDS
@@ -331,8 +698,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
 #pragma unroll
         for (int n = 0; n < LOADS; ++n) load_row(n, address(n, at[n]), lds0);
       }
+      const uint32_t p_at = lds0 + C::P;
       for (int j = 0; j < ntile; ++j) {
-        const uint32_t tile0 = lds0 + (j & 1) * TILE;
         const bool more = j + 1 < ntile;
         read_rows(more ? j + 1 : j, at);
         // the wave's part of tile j has landed; behind the barrier everyone's has, and everyone is done with
@@ -341,226 +708,76 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         barrier_only();
         uint32_t to = lds0 + ((j + 1) & 1) * TILE;
         opaque_uniform(to);
-        // S, a block of keys after the other.  Fragments of keys are read a few ahead of the products that
-        // need them, the next tile's loads go out beside them, and P of a block is found beside the
-        // products of the next one: with the maximum so far.  A score far above that is rare: the waves
-        // say so, and only then find the tile's maximum together and begin again.
-        f32x4 s[C::KW][C::RW];
-        float p[C::RW][4], part[C::RW], top[C::RW], shift[C::RW];
-#pragma unroll
-        for (int rb = 0; rb < C::RW; ++rb) part[rb] = 0.0f, top[rb] = -__builtin_inff();
-        auto shifts = [&] {
-#pragma unroll
-          for (int rb = 0; rb < C::RW; ++rb) {
-            const float most = own(rb);
-            shift[rb] = most > -__builtin_inff() ? most : 0.0f;
-          }
-        };
-        shifts();
         const int last = LIST ? 0 : places[min(present, j * BK + BK) - 1];
-        const bool masked = j * BK + BK > present || (!LIST && last > t0);
-        auto mask = [&](int kb) {  // what a row does not see
-          if (!masked) return;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int key = j * BK + key0 + kb * 16 + 4 * group + i;
-            const bool absent = key >= present;
-            const int place = absent || LIST ? 0 : places[key];
-#pragma unroll
-            for (int rb = 0; rb < C::RW; ++rb)
-              if (absent || (!LIST && place > t[rb])) s[kb][rb][i] = -__builtin_inff();
-          }
+        const TileKeys k{lds0 + (j & 1) * TILE, j * BK, present, j * BK + BK > present || (!LIST && last > t0)};
+        struct Loads {  // the next tile's
+          decltype(address) &make;
+          decltype(load_row) &send;
+          const uint32_t (&at)[LOADS];
+          uint32_t to;
+          const char *from;
+          __device__ inline void address(int n) { from = make(n, at[n]); }
+          __device__ inline void issue(int n) { send(n, from, to); }
         };
-        auto weight = [&](int kb, int rb, int i) { p[rb][i] = exp2f_fast(fmaf(s[kb][rb][i], a.scale_log2, -shift[rb])); };
-        auto put = [&](int kb, int rb) {
-          top[rb] = fmaxf(fmaxf(fmaxf(top[rb], s[kb][rb][0]), fmaxf(s[kb][rb][1], s[kb][rb][2])), s[kb][rb][3]);
-          part[rb] += (p[rb][0] + p[rb][1]) + (p[rb][2] + p[rb][3]);
-          // row r: 16-byte chunks, each with a lane group's 8 keys of a contraction of 32 in the order of
-          // lds_read_cols
-          const int r = wrow + rb * 16 + col, b16 = key0 / 16 + kb, chunk = (b16 >> 1) * 4 + group;
-          const uint32_t at = lds0 + C::P + r * 128 + ((chunk ^ (r & 7)) << 4) + (b16 & 1) * 8;
-          typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-          *(KPOOL_LDS u32x2 *)(uintptr_t)at = u32x2{pack_bf16(p[rb][0], p[rb][1]), pack_bf16(p[rb][2], p[rb][3])};
+        struct NoLoads {
+          __device__ inline void address(int) {}
+          __device__ inline void issue(int) {}
         };
-        auto weights = [&](int kb) {
-#pragma unroll
-          for (int rb = 0; rb < C::RW; ++rb) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) weight(kb, rb, i);
-            put(kb, rb);
-          }
-        };
-        auto read_key = [&](int n) {  // block n / KS, step n % KS
-          const int ks = n % C::KS, kb = n / C::KS;
-          return ks < NB * 4 ? lds_read((krow ^ ((ks & 3) << 6)) + (tile0 + (ks >> 2) * C::BLOCKB + kb * 16 * 256))
-                             : lds_read((kpe ^ ((ks & 1) << 6)) + (tile0 + NB * C::BLOCKB + kb * 16 * 128));
-        };
-        constexpr int STEPS = C::KS * C::KW, AHEAD = 4;
-        static_assert(C::KS == LOADS, "a load for every step of a block");
-        auto scores = [&](auto loads) {
-          bf16x8 k[STEPS];
-#pragma unroll
-          for (int n = 0; n < AHEAD; ++n) k[n] = read_key(n);
-          // (a matrix instruction takes 16 cycles, of which 12 are left for others: more than one or two
-          // between it and the next would hold that up)
-          const char *from = nullptr;
-#pragma unroll
-          for (int n = 0; n < STEPS; ++n) {
-            const int ks = n % C::KS, kb = n / C::KS;
-            const bool weighs = kb > 0 && ks >= 1 && ks < 1 + 4 * C::RW;
-            const int wr = (ks - 1) / 4, wi = (ks - 1) % 4;
-            float x = 0.0f;
-#pragma unroll
-            for (int rb = 0; rb < C::RW; ++rb) {
-              __builtin_amdgcn_sched_barrier(0);
-              s[kb][rb] = mfma(k[n], q[rb][ks], ks == 0 ? f32x4{} : s[kb][rb]);
-              __builtin_amdgcn_sched_barrier(0);
-              if (rb == 0) {
-                if (kb > 0 && ks == 1) mask(kb - 1);
-                if (decltype(loads)::value && n % C::KW == 0) from = address(n / C::KW, at[n / C::KW]);
-                if (weighs) x = fmaf(s[kb - 1][wr][wi], a.scale_log2, -shift[wr]);
-                if (C::RW > 1) __builtin_amdgcn_sched_barrier(0);
-              }
-              if (rb == C::RW - 1) {
-                if (decltype(loads)::value && n % C::KW == C::KW - 1) load_row(n / C::KW, from, to);
-                if (n + AHEAD < STEPS) k[n + AHEAD] = read_key(n + AHEAD);
-                if (weighs) p[wr][wi] = exp2f_fast(x);
-                static_assert(4 * C::RW + 1 < C::KS, "a value a step, from step 1 on");
-                if (kb > 0 && ks >= 5 && (ks - 5) % 4 == 0 && (ks - 5) / 4 < C::RW) put(kb - 1, (ks - 5) / 4);
-              }
-            }
-          }
-          __builtin_amdgcn_sched_barrier(0);
-        };
-        if (more) scores(std::true_type{});
-        else scores(std::false_type{});
+        if (more) r.scores(k, Loads{address, load_row, at, to, nullptr});
+        else r.scores(k, NoLoads{});
         // the first columns of values do not wait for P
-        auto read_value = [&](int i) {  // columns i % CB of the wave's, keys 32 (i / CB) ..
-          const int c = wave * C::CB + i % C::CB;
-          const uint32_t at = (vcol ^ ((c & 7) << 5)) + (tile0 + (c >> 3) * C::BLOCKB + i / C::CB * 32 * 256);
-          return lds_read_cols(at, at + 16 * 256);
-        };
-        constexpr int VALUES = 2 * C::CB, VAHEAD = VALUES < 6 ? VALUES : 6;
-        bf16x8 v[VALUES], pf[2][RB];
-#pragma unroll
-        for (int i = 0; i < VAHEAD; ++i) v[i] = read_value(i);
+        r.read_values(k);
         __builtin_amdgcn_sched_barrier(0);
-        mask(C::KW - 1);
-        weights(C::KW - 1);
-        bool over = false;
-#pragma unroll
-        for (int rb = 0; rb < C::RW; ++rb) over |= top[rb] * a.scale_log2 > own(rb) + 8.0f;  // (m = -inf: any visible key)
-        const bool any_over = __any(over);
+        // P, with the maximum so far.  A score far above it is rare: the waves say so, and only then find
+        // the tile's maximum together and begin again.
+        r.mask(k, places);
+        const bool any_over = __any(r.over(a.scale_log2));
         if (lane == 0) list[wave] = any_over;
+        r.weights(p_at, a.scale_log2);
         wait_reads();
         barrier_only();
         const int4 flags = *reinterpret_cast<const int4 *>(list);
-        auto read_p = [&](int kc, int rb) {
-          const int r = rb * 16 + col;
-          pf[kc][rb] = lds_read(lds0 + C::P + r * 128 + (((kc * 4 + group) ^ (r & 7)) << 4));
-        };
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) read_p(0, rb);
+        r.first_p(p_at);
         if (__builtin_amdgcn_readfirstlane(flags.x | flags.y | flags.z | flags.w)) {
           // (the maxima go where P is, which is written anew)
-#pragma unroll
-          for (int rb = 0; rb < C::RW; ++rb) {
-            const Pair x = row_pair(top[rb]);
-            float y = fmaxf(x.a, x.b);
-            y = fmaxf(y, other_half(y));
-            if (lane < 16) exchange[wave / C::RG * BQ + wrow + rb * 16 + col] = y;
-          }
           wait_reads();
           barrier_only();
-#pragma unroll
-          for (int rb = 0; rb < RB; ++rb) {
-            float most = exchange[rb * 16 + col];
-#pragma unroll
-            for (int g = 1; g < C::KG; ++g) most = fmaxf(most, exchange[g * BQ + rb * 16 + col]);
-            most *= a.scale_log2;
-            if (most > m[rb] + 8.0f) {  // (the same in every wave)
-              const float f = exp2f_fast(m[rb] - most);  // m = -inf gives 0
-              m[rb] = most;
-#pragma unroll
-              for (int b = 0; b < C::RW; ++b)
-                if (wrow + b * 16 == rb * 16) l[b] *= f;
-#pragma unroll
-              for (int c = 0; c < C::CB; ++c) o[c][rb] *= f;
-            }
-          }
+          r.give_top(exchange);
           wait_reads();
           barrier_only();
-          shifts();
-#pragma unroll
-          for (int rb = 0; rb < C::RW; ++rb) part[rb] = 0.0f;
-#pragma unroll
-          for (int kb = 0; kb < C::KW; ++kb) weights(kb);
+          r.raise(exchange, a.scale_log2);
           wait_reads();
           barrier_only();
-#pragma unroll
-          for (int rb = 0; rb < RB; ++rb) read_p(0, rb);
+          r.weights(p_at, a.scale_log2);
+          wait_reads();
+          barrier_only();
+          r.first_p(p_at);
         }
-#pragma unroll
-        for (int rb = 0; rb < C::RW; ++rb) l[rb] += part[rb];
-        // O
-#pragma unroll
-        for (int i = 0; i < VALUES; ++i) {
-#pragma unroll
-          for (int rb = 0; rb < RB; ++rb) {
-            __builtin_amdgcn_sched_barrier(0);
-            o[i % C::CB][rb] = mfma(v[i], pf[i / C::CB][rb], o[i % C::CB][rb]);
-            __builtin_amdgcn_sched_barrier(0);
-            if (rb == 0 && i + VAHEAD < VALUES) v[i + VAHEAD] = read_value(i + VAHEAD);
-            if (i == 1) read_p(1, rb);
-          }
-        }
-        __builtin_amdgcn_sched_barrier(0);
+        r.values(k, p_at);
       }
     }
 
-    // l of a row over the lane groups and waves
+    // l of a row over the lanes and waves
     __syncthreads();
-#pragma unroll
-    for (int rb = 0; rb < C::RW; ++rb) {
-      const Pair x = row_pair(l[rb]);
-      float y = x.a + x.b;
-      y += other_half(y);
-      if (lane < 16) exchange[wave / C::RG * BQ + wrow + rb * 16 + col] = y;
-    }
+    r.give_sum(exchange);
     __syncthreads();
     const bool whole = k1 - k0 == kt;
     const int slot = 2 * share + (k0 == 0);
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-      const int r = rb * 16 + col;
-      float sum = exchange[r];
-#pragma unroll
-      for (int g = 1; g < C::KG; ++g) sum += exchange[g * BQ + r];
-      // (0 where the row saw nothing; NaN goes through)
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-      const float lse = sum == 0.0f ? -__builtin_inff() : (m[rb] + log2f(sum)) * kLn2;
-#pragma unroll
-      for (int c = 0; c < C::CB; c += 2) {
-        const int d = (wave * C::CB + c) * 16;
-        const f32x4 y0 = o[c][rb] * inv, y1 = o[c + 1][rb] * inv;
-        if (whole) {
-          // lane groups exchange halves: groups 0 and 2 take 8 columns each of the first block, 1 and 3 of
-          // the second
-          const auto x = __builtin_amdgcn_permlane16_swap(pack_bf16(y0[0], y0[1]), pack_bf16(y1[0], y1[1]), false, false);
-          const auto z = __builtin_amdgcn_permlane16_swap(pack_bf16(y0[2], y0[3]), pack_bf16(y1[2], y1[3]), false, false);
-          const int to = d + (group & 1) * 16 + (group >> 1) * 8;
-          if (r < nrows && to < a.R) *reinterpret_cast<uint4 *>(a.o + (row0 + r) * a.R + to) = make_uint4(x[0], z[0], x[1], z[1]);
-        } else if (r < nrows) {
-          float *to = a.part_o + ((int64_t)slot * BQ + r) * a.R + d + group * 4;
-          if (d + group * 4 < a.R) *reinterpret_cast<f32x4 *>(to) = y0;
-          if (d + 16 + group * 4 < a.R) *reinterpret_cast<f32x4 *>(to + 16) = y1;
-        }
-      }
-      if (wave == 0 && group == 0 && r < nrows) {
-        if (!whole) a.part_lse[(int64_t)slot * BQ + r] = lse;
-        else if (a.lse) a.lse[row0 + r] = lse;
-      }
-    }
+    r.finish(
+        exchange, whole,
+        [&](int row, float m, float sum) {
+          if (row >= nrows) return;
+          // (0 where the row saw nothing; NaN goes through)
+          const float lse = sum == 0.0f ? -__builtin_inff() : (m + log2f(sum)) * kLn2;
+          if (!whole) a.part_lse[(int64_t)slot * BQ + row] = lse;
+          else if (a.lse) a.lse[row0 + row] = lse;
+        },
+        [&](int row, int d, uint4 x) {
+          if (row < nrows && d < a.R) *reinterpret_cast<uint4 *>(a.o + (row0 + row) * a.R + d) = x;
+        },
+        [&](int row, int d, f32x4 x) {
+          if (row < nrows && d < a.R) *reinterpret_cast<f32x4 *>(a.part_o + ((int64_t)slot * BQ + row) * a.R + d) = x;
+        });
     if (!whole && k0 == 0 && threadIdx.x == 0)
       a.cut[share] = {row0, before + (unit + 1) * kt, total, n, nrows};
     pos += k1 - k0;
@@ -614,7 +831,7 @@ __global__ __launch_bounds__(256) void latent_join_kernel(LatentArgs a, int BQ) 
 
 template <int NB, int RB, bool LIST>
 hipError_t launch_latent_t(const LatentArgs &a, hipStream_t st) {
-  using C = Latent<NB, RB, LIST>;
+  using C = typename LatentRows<NB, RB, LIST>::C;
   hipLaunchKernelGGL((latent_kernel<NB, RB, LIST>), dim3((a.shares + 7) / 8 * 8), dim3(256), C::LDS, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.shares == 1) return e;
