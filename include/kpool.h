@@ -385,7 +385,7 @@ int kpool_attend_expanded_backward(const uint16_t *d_o, const uint16_t *q, int64
  * Sizes: R a multiple of 8 up to 512; P a multiple of 8 up to 64, or 0; strides multiples of 8 (q's from
  * H * (R + P) to 2^24, the cache's from R + P to 2^24); q, cache, o and the workspace 16-byte aligned; at
  * most 2^31 - 1 cache rows and tokens in pages_per_seq pages, max_len at most 2^31 - 256; tiles (16
- * to 64 rows of a sequence by 64 tokens) of all sequences below 2^31.
+ * to 64 rows of a sequence by 64 tokens) of all sequences below 2^28.
  *   workspace  kpool_attend_latent(_selected)_workspace_bytes(the same sizes) bytes (may be 0: then it is
  *            not read); scratch.  It does not depend on what k_lens holds. */
 size_t kpool_attend_latent_workspace_bytes(const int32_t *cu_q_host, int32_t nseq, int32_t max_len,

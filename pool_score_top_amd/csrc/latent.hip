@@ -55,7 +55,25 @@ struct LatentCut {
   int32_t end, total, shares, nrows;  // (end 0: none)
 };
 
-// The first of n equal shares' tiles.
+// Shares are of the units' costs: a unit costs its tiles and, where shares are of several tiles, `fixed` more
+// for its start and end (rows of queries in, outputs out, no products meanwhile; about 4 tiles' time).
+// A cut that would leave a part of fewer than `least` tiles moves to the unit's start or end.
+constexpr int kUnitCost = 4;
+struct LatentCosts {
+  int fixed, least, total, shares;
+  __device__ inline LatentCosts(int tiles, int units, int most) {
+    shares = min(most, tiles);
+    fixed = tiles >= 4 * shares ? kUnitCost : 0, least = fixed ? 4 : 1;
+    total = tiles + fixed * units;
+  }
+  // the tiles before position x of a unit of kt tiles that starts at `start`
+  __device__ inline int cut(int x, int start, int kt) const {
+    const int t = x - start - fixed;
+    return t < least ? 0 : t > kt - least ? kt : t;
+  }
+};
+
+// Where the share begins.
 __device__ inline int share_start(int total, int n, int share) {
   const int each = total / n;
   return each * share + (total - each * n) * share / n;
@@ -93,10 +111,11 @@ __device__ inline int latent_len(const LatentArgs &a, int s) {
   return a.table ? (int)min64(len, (int64_t)a.per_seq * a.page) : len;
 }
 __device__ inline int tiles_of(int keys) { return max(1, (keys + kLatentKeys - 1) / kLatentKeys); }
-__device__ inline int seq_tiles(const LatentArgs &a, int s, int BQ) {
+// a sequence's units (high 32 bits) and tiles
+__device__ inline int64_t seq_work(const LatentArgs &a, int s, int BQ) {
   if (s >= a.nseq) return 0;
-  const int64_t rows = (int64_t)(a.cu_q[s + 1] - a.cu_q[s]) * a.H;
-  return (int)((rows + BQ - 1) / BQ) * tiles_of(latent_len(a, s));
+  const int units = ((a.cu_q[s + 1] - a.cu_q[s]) * a.H + BQ - 1) / BQ;
+  return (int64_t)units << 32 | (int64_t)units * tiles_of(latent_len(a, s));
 }
 
 // Keeps the compiler from looking through a value that is the same in all lanes.
@@ -106,11 +125,12 @@ __device__ inline void opaque_uniform(uint32_t &x) { asm volatile("" : "+s"(x));
 __device__ inline void to_accumulation(bf16x8 &x) { asm volatile("" : "+a"(x)); }
 
 // inclusive sum over the workgroup's 256 threads; scratch: 4 values of LDS.  All threads call it.
-__device__ inline int scan_256(int x, int *scratch) {
+template <class T>
+__device__ inline T scan_256(T x, T *scratch) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int up = __shfl_up(x, d);
+    const T up = __shfl_up(x, d);
     if (lane >= d) x += up;
   }
   __syncthreads();
@@ -129,7 +149,7 @@ struct Latent16 {
   using SP = Keys16<64>;
   static constexpr int KS = NB * 4 + 2;  // contraction steps of 32: the latent part, then the positional
   static constexpr int CB = NB * 2;      // 16-column blocks of a wave
-  static constexpr int VALUES = 2 * CB, AHEAD = VALUES < 6 ? VALUES : 6;
+  static constexpr int VALUES = 2 * CB, AHEAD = VALUES < 4 ? VALUES : 4;
   int wave, lane, col, group;
   // addresses are kept as few registers and made where they are used: (a ^ b) + c is one instruction
   uint32_t krow, kpe, vcol;
@@ -335,7 +355,7 @@ struct Latent32 {
   using SP = Keys<64>;
   static constexpr int KS = NB * 8 + 4;  // contraction steps of 16
   static constexpr int CB = NB;          // 32-column blocks of a wave
-  static constexpr int VALUES = 4 * CB, AHEAD = VALUES < 6 ? VALUES : 6;
+  static constexpr int VALUES = 4 * CB, AHEAD = VALUES < 4 ? VALUES : 4;
   int wave, lane, col, half, rows0, keys0;
   uint32_t krow, kpe, vcol0, vcol1;
   bf16x8 q[KS];
@@ -525,30 +545,32 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t lds0 = lds_offset(lds);
 
-  // this workgroup's share of all tiles: [pos, hi), from sequence `seq` on, whose tiles begin at `before`
-  int total = 0, before, seq, mine = 0, upto = 0;  // (upto: tiles up to and with the thread's sequence, mine of them its own)
+  // this workgroup's share of all units' costs: [pos, hi), from sequence `seq` on, whose units begin at `before`
+  int before, seq, tiles, units_all;
+  int64_t mine = 0, upto = 0;  // work of the thread's sequence, and up to its end
   const int list_tiles = LIST ? tiles_of(a.width) : 0;
-  int *scratch = reinterpret_cast<int *>(lds);
+  int64_t *scratch = reinterpret_cast<int64_t *>(lds);
   if (LIST) {
-    total = a.units * list_tiles;
+    tiles = a.units * list_tiles, units_all = a.units;
   } else {
+    int64_t all = 0;
     for (int base = 0; base < a.nseq; base += 256) {
-      mine = seq_tiles(a, base + threadIdx.x, BQ);
-      upto = total + scan_256(mine, scratch);
+      mine = seq_work(a, base + threadIdx.x, BQ);
+      upto = all + scan_256(mine, scratch);
       if (threadIdx.x == 255) scratch[4] = upto;
       __syncthreads();
-      total = scratch[4];
+      all = scratch[4];
     }
+    tiles = __builtin_amdgcn_readfirstlane((int)all), units_all = __builtin_amdgcn_readfirstlane((int)(all >> 32));
   }
-  total = __builtin_amdgcn_readfirstlane(total);
+  const LatentCosts costs(tiles, units_all, a.shares);
   // (workgroups go to the 8 XCDs in turn: those of one take neighbouring shares)
-  const int n = min(a.shares, total), share = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+  const int share = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
   if (threadIdx.x == 0 && a.cut && share < a.shares) a.cut[share].end = 0;
-  if (share >= n) return;
-  int pos = share_start(total, n, share);
-  const int hi = share_start(total, n, share + 1);
+  if (share >= costs.shares) return;
+  const int pos = share_start(costs.total, costs.shares, share), hi = share_start(costs.total, costs.shares, share + 1);
   if (LIST) {
-    const int token = pos / list_tiles / a.hblocks;
+    const int token = pos / (list_tiles + costs.fixed) / a.hblocks;
     int step = a.nseq;  // (the sequence of a token: the last that starts at or before it)
     seq = 0;
     while (step > 1) {
@@ -556,19 +578,21 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
       if (a.cu_q[seq + half] <= token) seq += half;
       step -= half;
     }
-    before = a.cu_q[seq] * a.hblocks * list_tiles;
+    before = a.cu_q[seq] * a.hblocks * (list_tiles + costs.fixed);
   } else {
-    for (int base = 0, run = 0; base < a.nseq; base += 256) {
+    auto cost = [&](int64_t work) { return (int)work + costs.fixed * (int)(work >> 32); };
+    int64_t run = 0;
+    for (int base = 0; base < a.nseq; base += 256) {
       if (a.nseq > 256) {  // (otherwise they are as they were)
-        mine = seq_tiles(a, base + threadIdx.x, BQ);
+        mine = seq_work(a, base + threadIdx.x, BQ);
         upto = run + scan_256(mine, scratch);
         if (threadIdx.x == 255) scratch[4] = upto;
       }
-      if (upto - mine <= pos && pos < upto) scratch[5] = upto - mine, scratch[6] = base + threadIdx.x;
+      if (cost(upto - mine) <= pos && pos < cost(upto)) scratch[5] = cost(upto - mine), scratch[6] = base + threadIdx.x;
       __syncthreads();
       run = scratch[4];
     }
-    before = __builtin_amdgcn_readfirstlane(scratch[5]), seq = __builtin_amdgcn_readfirstlane(scratch[6]);
+    before = __builtin_amdgcn_readfirstlane((int)scratch[5]), seq = __builtin_amdgcn_readfirstlane((int)scratch[6]);
   }
 
   R r;
@@ -577,12 +601,18 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
   // lane's chunk of its row is chunk ^ swz(4 i) (i the load's place in 16 rows; 8 i), its last where the
   // row ends before it.
   constexpr int LOADS = C::LOADS;
-  const uint32_t last_chunk = a.R / 8 - 1, last_pe = max(a.P / 8 - 1, 0), pitch = (uint32_t)a.cs * 2;
-  const uint32_t pe_at = (a.P ? a.R : 0) * 2;
-  uint32_t chunk = wave * NB / 4 * 16 + ((lane & 15) ^ R::S::swz(lane >> 4)), pe_chunk = (lane & 7) ^ R::SP::swz(lane >> 3);
+  const uint32_t pitch = (uint32_t)a.cs * 2;
+  const uint16_t *from[4], *pe_from[2];  // the lane's places in row 0
+  {
+    const int chunk = wave * NB / 4 * 16 + ((lane & 15) ^ R::S::swz(lane >> 4)), pe = (lane & 7) ^ R::SP::swz(lane >> 3);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) from[i] = a.cache + min(chunk ^ R::S::swz(4 * i), a.R / 8 - 1) * 8;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) pe_from[i] = a.cache + (a.P ? a.R + min(pe ^ R::SP::swz(8 * i), a.P / 8 - 1) * 8 : 0);
+  }
   uint32_t rows_at = lds0 + C::KEYS + (wave * 4 * NB % 16 * 4 + (lane >> 4)) * 4,
            pe_rows_at = lds0 + C::KEYS + (wave * 16 + (lane >> 3)) * 4;
-  opaque(chunk), opaque(pe_chunk), opaque(rows_at), opaque(pe_rows_at);
+  opaque(rows_at), opaque(pe_rows_at);
   auto read_rows = [&](int tile, uint32_t (&at)[LOADS]) {
     const uint32_t r = rows_at + tile * BK * 4, pe = pe_rows_at + tile * BK * 4;
 #pragma unroll
@@ -590,9 +620,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
       at[n] = *(KPOOL_LDS const uint32_t *)(uintptr_t)(n < 4 * NB ? r + n * 16 : pe + (n - 4 * NB) * 32);
   };
   auto address = [&](int n, uint32_t row) {
-    const uint32_t off = n < 4 * NB ? min(chunk ^ (uint32_t)R::S::swz(n % 4 * 4), last_chunk) * 16
-                                    : min(pe_chunk ^ (uint32_t)R::SP::swz((n & 1) * 8), last_pe) * 16 + pe_at;
-    return (const char *)a.cache + (uint64_t)row * pitch + off;
+    return (const char *)(n < 4 * NB ? from[n % 4] : pe_from[n % 2]) + (uint64_t)row * pitch;
   };
   auto load_row = [&](int n, const char *from, uint32_t to) {  // to: the tile's buffer
     load_lds_16(from, to + (n < 4 * NB ? (wave * 4 * NB + n) * 1024 : C::PE + (wave * 2 + n - 4 * NB) * 1024));
@@ -600,11 +628,24 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
   int *list = reinterpret_cast<int *>(lds + C::KEYS), *places = reinterpret_cast<int *>(lds + C::PLACES);
   float *exchange = reinterpret_cast<float *>(lds + C::P);  // [4][BQ]
 
-  while (pos < hi) {
+  int unit = -1;  // of the sequence
+  for (;;) {
     const int q_start = a.cu_q[seq], Lq = a.cu_q[seq + 1] - q_start, len = latent_len(a, seq);
-    const int kt = LIST ? list_tiles : tiles_of(len);
+    const int kt = LIST ? list_tiles : tiles_of(len), cost = kt + costs.fixed;
     const int units = LIST ? Lq * a.hblocks : (Lq * a.H + BQ - 1) / BQ;
-    const int unit = (pos - before) / kt, k0 = pos - before - unit * kt, k1 = min(kt, k0 + hi - pos);
+    if (unit < 0) unit = max(pos - before, 0) / cost;
+    if (unit >= units) {  // (no rows, or no more)
+      before += units * cost, ++seq, unit = 0;
+      continue;
+    }
+    const int start = before + unit * cost;
+    if (start >= hi) break;
+    const int k0 = costs.cut(pos, start, kt), k1 = costs.cut(hi, start, kt);
+    if (k0 >= k1) {
+      if (start + cost >= costs.total) break;
+      ++unit;
+      continue;
+    }
     // rows n0 .. n0 + nrows - 1 of the sequence's Lq * H
     const int tok = LIST ? unit / a.hblocks : 0, first = LIST ? (unit - tok * a.hblocks) * BQ : 0;
     const int n0 = LIST ? tok * a.H + first : unit * BQ;
@@ -674,11 +715,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
       int sum = 0;
 #pragma unroll
       for (int i = 0; i < C::EACH; ++i) sum += row[i] >= 0;
-      const int upto = scan_256(sum, scratch);
-      if (threadIdx.x == 255) scratch[4] = upto;
+      int *counts = reinterpret_cast<int *>(lds);
+      const int upto = scan_256(sum, counts);
+      if (threadIdx.x == 255) counts[4] = upto;
       int to = upto - sum;
       __syncthreads();
-      const int present = __builtin_amdgcn_readfirstlane(scratch[4]);
+      const int present = __builtin_amdgcn_readfirstlane(counts[4]);
 #pragma unroll
       for (int i = 0; i < C::EACH; ++i)
         if (row[i] >= 0) {
@@ -779,13 +821,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
           if (row < nrows && d < a.R) *reinterpret_cast<f32x4 *>(a.part_o + ((int64_t)slot * BQ + row) * a.R + d) = x;
         });
     if (!whole && k0 == 0 && threadIdx.x == 0)
-      a.cut[share] = {row0, before + (unit + 1) * kt, total, n, nrows};
-    pos += k1 - k0;
-    if (pos == before + units * kt) {
-      before = pos;
-      do ++seq;
-      while (seq < a.nseq && a.cu_q[seq + 1] == a.cu_q[seq]);
-    }
+      a.cut[share] = {row0, start + costs.fixed + kt - costs.least + 1, costs.total, costs.shares, nrows};
+    if (start + cost >= costs.total) break;
+    ++unit;
   }
 }
 

@@ -228,7 +228,7 @@ int run_latent(const char *fn, kpool::LatentCall &c, const kpool::LatentPlan &p,
     return fail(KPOOL_EINVAL, "%s: need page_size >= 1, pages_per_seq >= 0 and fewer than 2^31 tokens of both (%d, %d)", fn,
                 c.page_size, c.pages_per_seq);
   if (Tq == 0) return ok();
-  if (p.tiles > 0x7FFFFFFF || p.units > 0x7FFFFFFF) return fail(KPOOL_EUNSUPPORTED, "%s: too many query rows for one launch", fn);
+  if (p.tiles >= 1 << 28) return fail(KPOOL_EUNSUPPORTED, "%s: too many query rows for one launch", fn);
   if (!c.q || !c.o || !c.cu_q || !c.k_lens || (!c.page_table && !c.k_starts) || (c.cache_rows > 0 && !c.cache))
     return fail(KPOOL_EINVAL, "%s: null pointer", fn);
   if (!aligned16(c.q) || !aligned16(c.cache) || !aligned16(c.o))
