@@ -790,9 +790,16 @@ __global__ __launch_bounds__(256) void bwd_rows_sum_kernel(BwdArgs a, int width)
 
 // Costs of a tile of keys and of a tile of rows (which may have to find delta first, two of its
 // three products), and the steps that a share has at least.
+// A unit of dK's and dV's kernel costs 4 steps besides its own, with the positional part 12: its first
+// tiles and its sums, half as wide again, pass while nothing else runs on the CU, and where every head has
+// its own keys there are many short units.  (Lengths 4096, 2001, 511 and 1, 16 heads of 128 + 64, forward and
+// backward: 730 us with 4, 677 with 8, 642 with 12, 648 with 16.  Parts of 16 steps where those 12 are counted
+// cut units that are better left whole: 300 and 77 tokens, 8 heads of 64 + 32, 54.3 us, with 24 50.6, which
+// 32 and 48 leave as it is.)
 constexpr int kKeysShare = 16, kRowsShare = 6;
-UnitCost keys_cost(int64_t lk, int64_t lq, int64_t n0, int64_t G) {
-  return {4, (lq * G - first_row(lq * G, lk, lq, n0, G) + 31) / 32};
+constexpr int kUnitCost = 4, kExpandedCost = 12, kExpandedShare = 24;
+UnitCost keys_cost(int64_t lk, int64_t lq, int64_t n0, int64_t G, bool expanded) {
+  return {expanded ? kExpandedCost : kUnitCost, (lq * G - first_row(lq * G, lk, lq, n0, G) + 31) / 32};
 }
 UnitCost rows_cost(int64_t lq, int64_t lk, int64_t n0, int64_t G) {
   const int64_t last = std::min<int64_t>(lq * G, n0 + kBwdWaves * 32) - 1, t1 = last / G + lk - lq;
@@ -824,7 +831,7 @@ hipError_t launch_bwd_t(const AttendCall &c, const BwdPlan &p, BwdArgs a, hipStr
     Shares shares;
     const bool cut = make_shares(shares, p.kshares, p.kcost, a.Hkv, a.table, c.cu_k_host, c.cu_q_host, a.nseq, 1,
                                  C::KEYS, a.ktiles, [&](int64_t lk, int64_t lq, int64_t n0) {
-                                   return keys_cost(lk, lq, n0, G);
+                                   return keys_cost(lk, lq, n0, G, PP > 0);
                                  });
     const unsigned grid = (unsigned)(shares.n ? shares.n : a.ktiles * a.Hkv);
     hipLaunchKernelGGL((bwd_keys_kernel<DP, PP>), dim3(grid), dim3(512), C::LDS, st, a, shares);
@@ -846,7 +853,7 @@ int64_t up_to(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
 }  // namespace
 
-BwdPlan plan_attend_bwd(const int32_t *cu_q, const int32_t *cu_k, int nseq, int Hq, int Hkv) {
+BwdPlan plan_attend_bwd(const int32_t *cu_q, const int32_t *cu_k, int nseq, int Hq, int Hkv, bool expanded) {
   const int G = Hq / Hkv;
   BwdPlan p;
   p.ktiles = tile_start(cu_k[nseq], nseq, 1, 128);
@@ -854,10 +861,10 @@ BwdPlan plan_attend_bwd(const int32_t *cu_q, const int32_t *cu_k, int nseq, int 
   TotalCost qcost;
   for (int s = 0; s < nseq; ++s) {
     const int64_t lq = cu_q[s + 1] - cu_q[s], lk = cu_k[s + 1] - cu_k[s];
-    for (int64_t n0 = 0; n0 < lk; n0 += 128) p.kcost.add(keys_cost(lk, lq, n0, G), Hkv);
+    for (int64_t n0 = 0; n0 < lk; n0 += 128) p.kcost.add(keys_cost(lk, lq, n0, G, expanded), Hkv);
     for (int64_t n0 = 0; n0 < lq * G; n0 += kBwdWaves * 32) qcost.add(rows_cost(lq, lk, n0, G), Hkv);
   }
-  p.kshares = share_count(p.kcost, kKeysShare);
+  p.kshares = share_count(p.kcost, expanded ? kExpandedShare : kKeysShare);
   plan_parts(qcost, kRowsShare, &p.qsplit, &p.qchunk);
   return p;
 }

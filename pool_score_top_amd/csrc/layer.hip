@@ -414,7 +414,7 @@ size_t kpool_attend_expanded_backward_workspace_bytes(const int32_t *cu_q_host, 
   if (check_heads(fn, Hq, Hkv, D) || check_positional(fn, P) || check_lengths(fn, cu_q_host, cu_k_host, nseq, Hq / Hkv))
     return 0;
   ok();
-  return kpool::attend_bwd_workspace(kpool::plan_attend_bwd(cu_q_host, cu_k_host, nseq, Hq, Hkv),
+  return kpool::attend_bwd_workspace(kpool::plan_attend_bwd(cu_q_host, cu_k_host, nseq, Hq, Hkv, true),
                                      cu_q_host[nseq], cu_k_host[nseq], Hq, Hkv, D, P);
 }
 
@@ -439,7 +439,7 @@ int kpool_attend_expanded_backward(const uint16_t *d_o, const uint16_t *q, int64
     return fail(KPOOL_EINVAL, "%s: null pointer", fn);
   if (!aligned16(k) || !aligned16(v) || !aligned16(d_o) || !aligned16(dq) || !aligned16(dk) || !aligned16(dk_pe) || !aligned16(dv))
     return fail(KPOOL_EINVAL, "%s: k, v, d_o, dq, dk, dk_pe and dv must be 16-byte aligned", fn);
-  const kpool::BwdPlan p = kpool::plan_attend_bwd(cu_q_host, cu_k_host, nseq, Hq, Hkv);
+  const kpool::BwdPlan p = kpool::plan_attend_bwd(cu_q_host, cu_k_host, nseq, Hq, Hkv, true);
   if (kpool::attend_bwd_threads(p, Hkv) >= kLaunchThreads || c.Tk * P / 4 >= kLaunchThreads - 256)
     return fail(KPOOL_EUNSUPPORTED, "%s: too many rows or sequences for one launch", fn);
   const size_t need = kpool::attend_bwd_workspace(p, c.Tq, c.Tk, Hq, Hkv, D, P);

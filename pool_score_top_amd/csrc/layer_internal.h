@@ -89,7 +89,8 @@ struct BwdPlan {
   int kshares;             // its equal shares (0: a workgroup per tile and key head)
   int qsplit, qchunk;      // parts of the keys (dQ)
 };
-BwdPlan plan_attend_bwd(const int32_t *cu_q, const int32_t *cu_k, int nseq, int Hq, int Hkv);
+BwdPlan plan_attend_bwd(const int32_t *cu_q, const int32_t *cu_k, int nseq, int Hq, int Hkv,
+                        bool expanded = false);
 size_t attend_bwd_workspace(const BwdPlan &p, int64_t Tq, int64_t Tk, int Hq, int Hkv, int D, int P = 0);
 int64_t attend_bwd_threads(const BwdPlan &p, int Hkv);  // of its largest launch, or more
 hipError_t launch_attend_bwd(const AttendCall &c, const uint16_t *d_o, const BwdPlan &p, void *workspace,
