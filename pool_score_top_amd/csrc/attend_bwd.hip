@@ -567,33 +567,6 @@ __global__ __launch_bounds__(NW * 64) void bwd_rows_kernel(BwdArgs a) {
   const int w0 = (at.n0 + wave * 32) / G + at.Lk - at.Lq;
   const int w1 = wave_rows > 0 ? (at.n0 + wave * 32 + wave_rows - 1) / G + at.Lk - at.Lq : -1;
   const int64_t row = ((int64_t)at.q_start + tok) * a.Hq + head;
-  bf16x8 qf[S::KS], dof[S::KS];
-  const uint16_t *q_row = a.q + ((int64_t)at.q_start + tok) * a.qs + (int64_t)head * (PP ? a.QD : a.D);
-  load_frag<DP>(qf, live ? q_row : nullptr, a.D, lane);
-  uint32_t qp = 0;
-  if constexpr (PP > 0)
-    qp = stash<PP>(lds_offset(lds) + 2 * BUFB + wave * 32 * Keys<PP>::ROWB, live ? q_row + a.D : nullptr, a.P, lane);
-  load_frag<DP>(dof, live ? a.d_o + row * a.D : nullptr, a.D, lane);
-  // the rows' lse and delta, which dK's and dV's kernel reads
-  const int64_t stat = (int64_t)kvh * a.Tq * G + (int64_t)at.q_start * G + n;
-  const float none = -__builtin_inff(), given = live ? a.lse[row] : none;
-  const float lse = given != none ? given * kLog2e : -none;
-  float delta = 0.0f;
-  if (t1 >= kFewKeys) {
-    bf16x8 of[S::KS];
-    load_frag<DP>(of, live ? a.o + row * a.D : nullptr, a.D, lane);
-#pragma unroll
-    for (int ks = 0; ks < S::KS; ++ks)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) delta = fmaf((float)of[ks][i], (float)dof[ks][i], delta);
-    delta += other_half(delta);
-  }
-  f32x16 dq[S::DT + PT];
-#pragma unroll
-  for (int dt = 0; dt < S::DT + PT; ++dt)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) dq[dt][i] = 0.0f;
-
   const uint32_t lds0 = lds_offset(lds);
   Frag<DP> f;
   f.init(lds0, lane);
@@ -613,6 +586,36 @@ __global__ __launch_bounds__(NW * 64) void bwd_rows_kernel(BwdArgs a) {
     keys.load(vb + (int64_t)k0 * a.vs, a.vs, at.Lk - 1 - k0, lds0 + buf * BUFB + TILE);
     if constexpr (PP > 0) pes.load(pb + (int64_t)k0 * a.pes, a.pes, at.Lk - 1 - k0, lds0 + buf * BUFB + 2 * TILE);
   };
+  // (the first tile is on its way while the rows' own values are)
+  const bool few = t1 < kFewKeys;
+  if (!few && ntile > 0) load(k_lo, 0);
+  bf16x8 qf[S::KS], dof[S::KS];
+  const uint16_t *q_row = a.q + ((int64_t)at.q_start + tok) * a.qs + (int64_t)head * (PP ? a.QD : a.D);
+  load_frag<DP>(qf, live ? q_row : nullptr, a.D, lane);
+  uint32_t qp = 0;
+  if constexpr (PP > 0)
+    qp = stash<PP>(lds_offset(lds) + 2 * BUFB + wave * 32 * Keys<PP>::ROWB, live ? q_row + a.D : nullptr, a.P, lane);
+  load_frag<DP>(dof, live ? a.d_o + row * a.D : nullptr, a.D, lane);
+  // the rows' lse and delta, which dK's and dV's kernel reads
+  const int64_t stat = (int64_t)kvh * a.Tq * G + (int64_t)at.q_start * G + n;
+  const float none = -__builtin_inff(), given = live ? a.lse[row] : none;
+  const float lse = given != none ? given * kLog2e : -none;
+  float delta = 0.0f;
+  if (!few) {
+    bf16x8 of[S::KS];
+    load_frag<DP>(of, live ? a.o + row * a.D : nullptr, a.D, lane);
+#pragma unroll
+    for (int ks = 0; ks < S::KS; ++ks)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) delta = fmaf((float)of[ks][i], (float)dof[ks][i], delta);
+    delta += other_half(delta);
+  }
+  f32x16 dq[S::DT + PT];
+#pragma unroll
+  for (int dt = 0; dt < S::DT + PT; ++dt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) dq[dt][i] = 0.0f;
+
   // S and dP of 32 keys
   auto half_tile = [&](uint32_t sk, uint32_t sv, uint32_t sp, f32x16 &s, f32x16 &dp) {
     if constexpr (PP > 0) {  // (a few fragments ahead: more would not fit the registers)
@@ -670,7 +673,7 @@ __global__ __launch_bounds__(NW * 64) void bwd_rows_kernel(BwdArgs a) {
     if (j + 1 < ntile) load(k_first + (j + 1) * BK, buf ^ 1);
   };
   wait_loads();
-  if (t1 < kFewKeys) {
+  if (few) {
     // delta from P and dP themselves: o was rounded to bf16, and where a few keys share the
     // weight that error reaches dS at the size of dS's own rounding
     const int n_all = t1 >= 0 ? t1 / BK + 1 : 0;
@@ -693,6 +696,7 @@ __global__ __launch_bounds__(NW * 64) void bwd_rows_kernel(BwdArgs a) {
     delta = sum + other_half(sum);
     __builtin_amdgcn_s_waitcnt(0x0070);
     barrier_only();
+    if (ntile > 0) load(k_lo, 0);
   }
   if (split == 0 && live && lane < 32) a.lse2[stat] = lse, a.delta[stat] = delta;
   auto step = [&](int j, auto buf_c) {
@@ -744,7 +748,6 @@ __global__ __launch_bounds__(NW * 64) void bwd_rows_kernel(BwdArgs a) {
       }
     }
   };
-  if (ntile > 0) load(k_lo, 0);
   for (int j = 0; j < ntile; j += 2) {
     step(j, std::integral_constant<int, 0>{});
     if (j + 1 < ntile) step(j + 1, std::integral_constant<int, 1>{});
