@@ -84,36 +84,38 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(RotaryArgs a, in
     const int64_t head = (int64_t)(head0 + h) * a.D;
     const T *x = (const T *)a.x + (row0 + r) * a.xs + head;
     T *y = (T *)a.y + (row0 + r) * a.ys + head;
-    if ((int)unit < a.turned) {
-      const float2 *t = turn + r * a.pairs;
-      const int at = a.begin + unit * step;
-      if constexpr (NEAR) {
-        const Vec v = *(const Vec *)(x + at);
-        Vec w;
+    const int c = (int)unit - a.turned;  // (from 0 on: copied)
+    const float2 *t = turn + r * a.pairs + unit * (NEAR ? V / 2 : V);
+    int at = c < a.before ? c * V : a.begin + 2 * a.pairs + (c - a.before) * V;
+    if constexpr (NEAR) {
+      // (one load for turned and copied units alike: a wave holds both, and would wait for two in turn; 8192
+      // rows of 16 heads of 192, 64 of them turned, both ways: 62.8 us, so 47.7)
+      if (c < 0) at = a.begin + (int)unit * V;
+      Vec v = *(const Vec *)(x + at);
+      if (c < 0) {
 #pragma unroll
         for (int i = 0; i < V; i += 2) {
-          const float2 cs = t[unit * (V / 2) + i / 2];
+          const float2 cs = t[i / 2];
           const float p = to_float(v.v[i]), q = to_float(v.v[i + 1]);
-          from_float(w.v[i], p * cs.x - q * cs.y);
-          from_float(w.v[i + 1], p * cs.y + q * cs.x);
+          from_float(v.v[i], p * cs.x - q * cs.y);
+          from_float(v.v[i + 1], p * cs.y + q * cs.x);
         }
-        *(Vec *)(y + at) = w;
-      } else {
-        const Vec v0 = *(const Vec *)(x + at), v1 = *(const Vec *)(x + at + apart);
-        Vec w0, w1;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float2 cs = t[unit * V + i];
-          const float p = to_float(v0.v[i]), q = to_float(v1.v[i]);
-          from_float(w0.v[i], p * cs.x - q * cs.y);
-          from_float(w1.v[i], p * cs.y + q * cs.x);
-        }
-        *(Vec *)(y + at) = w0;
-        *(Vec *)(y + at + apart) = w1;
       }
+      *(Vec *)(y + at) = v;
+    } else if (c < 0) {
+      at = a.begin + (int)unit * step;
+      const Vec v0 = *(const Vec *)(x + at), v1 = *(const Vec *)(x + at + apart);
+      Vec w0, w1;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float2 cs = t[i];
+        const float p = to_float(v0.v[i]), q = to_float(v1.v[i]);
+        from_float(w0.v[i], p * cs.x - q * cs.y);
+        from_float(w1.v[i], p * cs.y + q * cs.x);
+      }
+      *(Vec *)(y + at) = w0;
+      *(Vec *)(y + at + apart) = w1;
     } else {
-      const int c = (int)unit - a.turned;
-      const int at = c < a.before ? c * V : a.begin + 2 * a.pairs + (c - a.before) * V;
       *(Vec *)(y + at) = *(const Vec *)(x + at);
     }
   }
@@ -127,12 +129,15 @@ hipError_t launch_rotary_v(RotaryArgs a, bool interleaved, bool in_place, int64_
   a.before = a.begin / V;
   const int copied = in_place ? 0 : (a.D - 2 * a.pairs) / V;
   const int units_head = a.turned + copied;
-  // heads of a workgroup, evened out over the workgroups of a row; then rows, up to 16 units a thread
-  int nheads = std::max(1, std::min(a.heads, 8192 / units_head));
+  // heads of a workgroup, evened out over the workgroups of a row, then rows: 4 units a thread.  (8192 rows of 16
+  // heads of 192, 64 of them turned, both ways, and 32768 rows of 32 heads of 128: 16 units a thread 45.5 and
+  // 115 us, 8 43.0 and 110, 4 40.3 and 99.1, 2 40.7 and 97.4, 1 50.0 and 109.)
+  constexpr int kUnits = 4 * kRotaryThreads;
+  const int nheads = std::max(1, std::min(a.heads, kUnits / units_head));
   a.hblocks = (a.heads + nheads - 1) / nheads;
   a.nheads = (a.heads + a.hblocks - 1) / a.hblocks;
   const int units_row = a.nheads * units_head;
-  a.nrows = std::max(1, std::min({64, 4096 / units_row, kRotaryAngles / a.pairs}));
+  a.nrows = std::max(1, std::min({64, kUnits / units_row, kRotaryAngles / a.pairs}));
   a.units_row = divide_by(units_row), a.units_head = divide_by(units_head);
   const int64_t blocks = (a.rows + a.nrows - 1) / a.nrows * a.hblocks;
   if (threads) {
