@@ -69,7 +69,7 @@ struct LatentCosts {
   // the tiles before position x of a unit of kt tiles that starts at `start`
   __device__ inline int cut(int x, int start, int kt) const {
     const int t = x - start - fixed;
-    return t < least ? 0 : t > kt - least ? kt : t;
+    return t > kt - least ? kt : t < least ? 0 : t;  // (its end before its start: a unit may be shorter than `least`)
   }
 };
 

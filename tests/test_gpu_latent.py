@@ -64,6 +64,23 @@ def test_long_caches(H):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("H", [16, 40, 64])
+@pytest.mark.parametrize("few", [1, 7])
+def test_short_units_beside_long_ones(H, few):
+    """Shares of several tiles each, and units of fewer tiles than a part of one may have."""
+    short = [1, 64, 65, 130, 200, 257, 300, 0, 500]
+    run([1] * (2 * len(short) + 2), [40000] + short + [60001] + short, H, 64, 16, 64, 20 + few)
+    run([few] * 6, [30000, 130, few, 400, 90000, 65], H, 64, 16, 64, 30)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H", [16, 64])
+@pytest.mark.parametrize("width", [1, 128, 200, 256, 300, 500])
+def test_short_lists_of_many_rows(H, width):
+    run([1100, 0, 33], [1200, 5, 700], H, 64, 16, 64, width, width)
+
+
+@pytest.mark.gpu
 def test_many_sequences():
     """More than a workgroup's threads."""
     g = np.random.default_rng(1)
