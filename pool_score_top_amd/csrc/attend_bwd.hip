@@ -132,7 +132,10 @@ __device__ inline void load_frag(bf16x8 (&f)[DP / 16], const uint16_t *row, int 
 // kernel: 330 us; by shares 254 and 13 to join, 210 GFLOP at 0.83 PFLOP/s; CUs busy 85% of the
 // time, the matrix pipe 45% of that).
 // PP = 64: with the positional part of expanded latent attention, whose 32 rows lie behind the others in
-// rows as wide as theirs, so that they share their lanes' addresses.
+// rows as wide as theirs, so that they share their lanes' addresses.  Its products go to both waves, 4 a tile
+// each: the first reads the keys' part from LDS (its registers are full), the second sums the gradient.
+// 4096, 2001, 511 and 1 tokens, 16 heads of 128 + 64, 215 GFLOP: 262 us and 19 to join, 0.8 PFLOP/s; a step
+// takes 2210 cycles, 1280 of them products of the SIMD's two waves, a unit 22 thousand cycles besides its steps.
 template <int DP, int PP = 0>
 struct BwdKeys {
   static constexpr int BR = 32, NG = 4, KEYS = NG * 32;
@@ -518,7 +521,8 @@ __global__ __launch_bounds__(256) void bwd_expanded_sum_kernel(BwdArgs a, Shares
   }
 }
 
-// The positional gradient: the key heads' sums, in order.
+// The positional gradient, of a row that all key heads share: their sums, each head's in fp32 by the kernel
+// above or by dK's, added in the heads' order.  (6609 tokens, 16 heads: 27 MB in 5.5 us.)
 __global__ __launch_bounds__(256) void bwd_positional_kernel(BwdArgs a) {
   const int64_t n = a.Tk * a.P, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (i >= n) return;
@@ -537,6 +541,10 @@ __global__ __launch_bounds__(256) void bwd_positional_kernel(BwdArgs a) {
 // exponentials wait for its products and the next half's products for them (the scheduling
 // barriers keep the phases apart), and all waves wait for a whole tile's loads together.  Cutting
 // the longest tiles to the CUs' average leaves the time as it is.
+// With the positional part (PP = 64) the rows' share of it lies in LDS, each lane's for itself, as the registers
+// are full, and fragments are read four ahead of their products.  4096, 2001, 511 and 1 tokens, 16 heads of
+// 128 + 64: 172 GFLOP in 231 us, 0.75 PFLOP/s; a step of 64 keys takes 6700 cycles, 4100 of them products.
+// With one of a SIMD's two waves ahead of the other (s_setprio), or with the rows read through LDS, the same.
 template <int DP, int NW, int PP>
 __global__ __launch_bounds__(NW * 64) void bwd_rows_kernel(BwdArgs a) {
   using S = Keys<DP>;

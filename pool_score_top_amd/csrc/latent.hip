@@ -8,24 +8,35 @@
 // tokens are what a row attends to.
 //
 // All heads share one key, so the heads of a sequence's new tokens form one axis of Lq * H rows
-// (row n: head n % H of token n / H).  A workgroup takes up to 64 of them (16 RB) and walks key tiles
-// of 64 through LDS, each read once from memory and used twice, as keys and, transposed, as values.
-//   S^T = C Q^T: wave w multiplies keys 16 w .. 16 w + 15 of the tile with all rows, whose
-//     fragments stay in registers (R + P = 576 and 64 rows: 288 a lane);
-//   the running maximum is common to the four waves (one exchange a tile), P goes through LDS in
-//     bf16, each wave sums its own keys' share of l;
-//   O^T = C^T P^T: wave w keeps columns w R / 4 .. of all rows (128 registers a lane).
-// So a key tile passes from LDS to registers 1 + 8 / 9 times, whatever the rows.  Statistics as in
-// attend.hip: fp32, base 2, the maximum followed when it rises by more than 8; P rounded to bf16 for
-// its product, l from the unrounded values.
+// (row n: head n % H of token n / H).  A workgroup of 4 waves, one a CU, takes up to 64 of them and walks
+// key tiles of 64 through two LDS buffers (72 KiB each at R + P = 576), each read once from memory and used
+// twice, as keys and, transposed, as values:
+//   S^T = C Q^T, the queries in registers, which lie in the accumulation half of the file;
+//   P to LDS in bf16, where all waves read it back;
+//   O^T = C^T P^T: wave w keeps columns w R / 4 .. of all rows (128 registers a lane at 64 rows).
+// Statistics as in attend.hip: fp32, base 2.  The maximum is followed only when a score lies more than 8
+// (a factor of 256) above it: the waves vote on that through flags in LDS, and exchange maxima only then.  P is
+// rounded to bf16 for its product (as the keys that it meets are), l is summed from the unrounded values.
 //
-// Keys lie anywhere (pages, lists): a block of 512 of them is first turned into a list of row offsets
-// in LDS, without those that do not exist, and tiles are gathered by it.
+// Keys lie anywhere (pages, lists): a block of 1024 (lists: 2048) of them is first turned into a list of
+// rows in LDS, without those that do not exist, and tiles are gathered by it.  The next tile's loads
+// go out one by one between the matrix instructions of S.
 //
-// Work goes by equal shares of all the tiles, one share a CU.  Where the shares begin depends on
+// Work goes by equal shares of all the units' costs, one share a CU.  Where the shares begin depends on
 // the lengths, which are on the device (a captured decoding step replays while its lengths grow), so each
 // workgroup finds its share itself.  A unit (rows of one tile) that lies across shares leaves a
 // part each in fp32; a second kernel joins them in order.
+//
+// What bounds it, at R + P = 512 + 64 (captured calls, both kernels):
+//   few rows: memory.  16 requests of one token, 205k cached tokens, 16 heads: 62.5 us; the first kernel
+//     takes 44 (236 MB, 5.4 TB/s, as much as a copy moves), the join 7;
+//   many rows: the matrix instructions and what they wait for within a tile, as there is one wave a
+//     SIMD: S 1600 cycles of 4200 (1152 of products), softmax and its exchange 700, O 1530 (1024), the
+//     tile's arrival 310.  8 requests of 2 tokens, 128 heads, 117k tokens: 102 us (93 and 11; 65 GFLOP; CUs busy
+//     79% of the time, the matrix pipe 36% of that): a unit's start and end take 22k cycles besides, 5 tiles' time;
+//   lists of many rows: the listed rows' way from beyond the L2, which holds 12% of them.  1024 rows of 2048
+//     tokens, 64 heads: 356 us, 2.4 GB at 7 TB/s (CUs busy 94%, the pipe 42% of that);
+//   a token or two: latencies.  One token over 1003, 16 heads: 16.3 us (11 and 4).
 #include <type_traits>
 
 #include "attend_tile.h"
@@ -56,7 +67,10 @@ struct LatentCut {
 };
 
 // Shares are of the units' costs: a unit costs its tiles and, where shares are of several tiles, `fixed` more
-// for its start and end (rows of queries in, outputs out, no products meanwhile; about 4 tiles' time).
+// for its start and end (rows of queries in, outputs out, no products meanwhile).  With tiles alone a share of
+// many short units took up to twice its time: 8 requests of 2 tokens, 128 heads, us of the first kernel by tiles
+// 118, by cost 93; 16 requests, 16 heads, 49.6 and 43.7 (whole calls: cost 3 62.6 and 103, 4 62.5 and 102, 6 64.1
+// and 101).  Where shares are of fewer tiles, a unit has a share and more to itself either way.
 // A cut that would leave a part of fewer than `least` tiles moves to the unit's start or end.
 constexpr int kUnitCost = 4;
 struct LatentCosts {
@@ -345,7 +359,8 @@ struct Latent16 {
   }
 };
 
-// 64 rows, by products of 32 rows, half as many instructions for the same work: wave w has 32 keys (w / 2)
+// 64 rows, by products of 32 rows, half as many instructions for the same work (8 requests of 2 tokens, 128
+// heads, 123 us by products of 16 rows, 118 so): wave w has 32 keys (w / 2)
 // and 32 rows (w % 2) for S, columns w R / 4 .. and all rows for O.  Queries of 64 rows for 16 keys a
 // wave would read each key once instead of twice, but take 288 registers beside O's 128: they spill.
 template <int NB, bool LIST>
@@ -828,7 +843,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
 }
 
 // Joins the parts of the units that lie across shares, o = sum_s e^(lse_s - lse) o_s: a workgroup for a
-// row of the unit that a share begins.  256 / (R / 4) groups of threads take the parts in turn, each
+// row of the unit that a share begins (8 tokens of 2048 selected ones, 64 heads: 65 us with a workgroup for all
+// of its rows, 10 so; 4 us, a chain of latencies, at the least).  256 / (R / 4) groups of threads take the parts in turn, each
 // thread 4 columns, and add up in order.
 __global__ __launch_bounds__(256) void latent_join_kernel(LatentArgs a, int BQ) {
   __shared__ float lse_of[kMostShares], weight[kMostShares];
@@ -892,9 +908,9 @@ static_assert(sizeof(LatentCut) <= 32, "parts stay aligned");
 LatentPlan shares_of(LatentPlan p, int64_t units, int64_t keys) {
   p.units = units;
   p.tiles = units * std::max<int64_t>(1, (keys + kLatentKeys - 1) / kLatentKeys);
-  // A share for each tile, of 64 rows for two: a part of theirs costs four tiles' time to begin and to join
-  // (8 tokens of 2048 selected ones, 128 heads, 512 tiles on 256 CUs either way where shares are few: us with
-  // one, two, four tiles: 35, 32, 34; one request of 1003 tokens, 16 rows: 16.3, 18.0, 21.8).
+  // A share for each tile, of 64 rows for two, as their parts cost four tiles' time to begin and to join.
+  // (us with one, two and four tiles a share: 8 tokens of 2048 selected ones, 64 heads, 35, 32, 34; one token
+  // over 1003, 16 heads, 16.3, 18.0, 21.8.)
   const int64_t shares = p.rb == 4 ? (p.tiles + 1) / 2 : p.tiles;
   p.shares = (int)std::min<int64_t>(kMostShares, std::max<int64_t>(1, shares));
   return p;
@@ -902,7 +918,9 @@ LatentPlan shares_of(LatentPlan p, int64_t units, int64_t keys) {
 
 }  // namespace
 
-// 16-row blocks: as many as the rows that share keys fill.
+// Units of 16, 32 or 64 rows: as many as share keys and no more.  (us with 16, 32 and 64 rows, 8 requests of
+// one token over 64k cached tokens in all, and 256 rows of 1024 selected tokens: 16 heads 37, 41, - and 51, 54,
+// -; 32 heads 46, 43, 50 and 89, 54, 62; 64 heads -, 51, 55 and -, 95, 67; 128 heads -, 66, 60 and -, 173, 114.)
 LatentPlan plan_latent(const int32_t *cu_q, int nseq, int H, int64_t max_len) {
   int64_t most = 0, units = 0;
   for (int s = 0; s < nseq; ++s) most = std::max<int64_t>(most, (int64_t)(cu_q[s + 1] - cu_q[s]) * H);
