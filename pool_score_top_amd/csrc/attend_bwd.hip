@@ -809,7 +809,7 @@ __global__ __launch_bounds__(256) void bwd_rows_sum_kernel(BwdArgs a, int width)
 // 32 and 48 leave as it is.)
 constexpr int kKeysShare = 16, kRowsShare = 6;
 constexpr int kUnitCost = 4, kExpandedCost = 12, kExpandedShare = 24;
-UnitCost keys_cost(int64_t lk, int64_t lq, int64_t n0, int64_t G, bool expanded) {
+UnitCost keys_cost(int64_t lk, int64_t lq, int64_t n0, int64_t G, bool expanded = false) {
   return {expanded ? kExpandedCost : kUnitCost, (lq * G - first_row(lq * G, lk, lq, n0, G) + 31) / 32};
 }
 UnitCost rows_cost(int64_t lq, int64_t lk, int64_t n0, int64_t G) {

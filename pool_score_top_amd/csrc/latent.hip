@@ -75,20 +75,20 @@ struct LatentCut {
 constexpr int kUnitCost = 4;
 struct LatentCosts {
   int fixed, least, total, shares;
-  __device__ inline LatentCosts(int tiles, int units, int most) {
-    shares = min(most, tiles);
+  __host__ __device__ inline LatentCosts(int tiles, int units, int most) {
+    shares = most < tiles ? most : tiles;
     fixed = tiles >= 4 * shares ? kUnitCost : 0, least = fixed ? 4 : 1;
     total = tiles + fixed * units;
   }
   // the tiles before position x of a unit of kt tiles that starts at `start`
-  __device__ inline int cut(int x, int start, int kt) const {
+  __host__ __device__ inline int cut(int x, int start, int kt) const {
     const int t = x - start - fixed;
     return t > kt - least ? kt : t < least ? 0 : t;  // (its end before its start: a unit may be shorter than `least`)
   }
 };
 
 // Where the share begins.
-__device__ inline int share_start(int total, int n, int share) {
+__host__ __device__ inline int share_start(int total, int n, int share) {
   const int each = total / n;
   return each * share + (total - each * n) * share / n;
 }
