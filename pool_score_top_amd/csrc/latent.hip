@@ -907,7 +907,8 @@ static_assert(sizeof(LatentCut) <= 32, "parts stay aligned");
 
 LatentPlan shares_of(LatentPlan p, int64_t units, int64_t keys) {
   p.units = units;
-  p.tiles = units * std::max<int64_t>(1, (keys + kLatentKeys - 1) / kLatentKeys);
+  // (more units than a call may have tiles are refused as they are: their product may not fit 64 bits)
+  p.tiles = units < (1 << 28) ? units * std::max<int64_t>(1, (keys + kLatentKeys - 1) / kLatentKeys) : units;
   // A share for each tile, of 64 rows for two, as their parts cost four tiles' time to begin and to join.
   // (us with one, two and four tiles a share: 8 tokens of 2048 selected ones, 64 heads, 35, 32, 34; one token
   // over 1003, 16 heads, 16.3, 18.0, 21.8.)

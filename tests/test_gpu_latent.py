@@ -380,6 +380,13 @@ def test_refuses_lengths_and_lists():
     assert _call(cu=(0, 0), q=None, o=None, lens=None, cud=None, ws=None) == 0
 
 
+def test_refuses_products_past_64_bits():
+    """Rows and list entries, each within its own bound, whose tiles a 64-bit product would wrap to few or negative."""
+    cu = np.arange(65537, dtype=np.int64) * 32000
+    assert _call(True, cu=cu, H=65536, R=8, P=0, width=1 << 30) == -2
+    assert _call(cu=cu, H=65536, R=8, P=0, max_len=0x7FFFFF00) == -2
+
+
 @pytest.mark.parametrize("selected", [False, True])
 @pytest.mark.parametrize("out", ["o", "lse", "ws"])
 @pytest.mark.parametrize("over", ["q", "cache", "table", "starts", "lens", "cud", "ids", "lse", "ws", "o"])
