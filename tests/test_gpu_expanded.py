@@ -62,6 +62,14 @@ def test_many_sequences():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D,P", [(64, 32), (128, 64)])
+def test_short_units_beside_long_ones(D, P):
+    """Shares of keys' units that are cut, and units of a step or two between them."""
+    lens = [1300, 5, 130, 1, 64, 300, 1, 129, 40, 257]
+    run(lens, lens, 16, 16, D, P, 17)
+
+
+@pytest.mark.gpu
 def test_strided_tokens():
     run([200, 31], [200, 90], 8, 8, 128, 64, 8, pad=24)
 
@@ -132,6 +140,34 @@ def test_same_bits_other_stream_workspace_and_outputs():
     bits = [t.view(torch.int16) for t in x]
     o2, none = K.attend_expanded(*bits, *cu)
     assert none is None and torch.equal(o2, o.view(torch.int16))
+
+
+@pytest.mark.gpu
+def test_calls_of_two_threads_at_once():
+    import threading
+    jobs = []
+    for seed, D, P in ((18, 128, 64), (19, 64, 24)):
+        x, cu, o, lse, d_o = run([700, 40], [700, 300], 4, 4, D, P, seed)
+        jobs.append(lambda stream=None, x=x, cu=cu, o=o, lse=lse, d=d_o: [
+            *K.attend_expanded(*x, *cu, want_lse=True, stream=stream),
+            *K.attend_expanded_backward(d, *x, o, lse, *cu, stream=stream)])
+    alone = [job() for job in jobs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(job, want):
+        stream = torch.cuda.Stream()
+        for _ in range(10):
+            got = job(stream)
+            stream.synchronize()
+            wrong.extend(i for i, (a, b) in enumerate(zip(got, want)) if not torch.equal(a, b))
+
+    threads = [threading.Thread(target=work, args=pair) for pair in zip(jobs, alone)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
 
 
 @pytest.mark.gpu
