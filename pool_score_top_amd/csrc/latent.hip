@@ -93,6 +93,18 @@ __host__ __device__ inline int share_start(int total, int n, int share) {
   return each * share + (total - each * n) * share / n;
 }
 
+// The keys [lo, hi) by blocks, counted by what is left of them: the last block may end past 2^31, so no number
+// past hi is formed.
+struct KeyBlocks {
+  int hi, left;
+  __host__ __device__ inline KeyBlocks(int lo, int hi_) : hi(hi_), left(hi_ - lo) {}
+  __host__ __device__ inline bool any() const { return left > 0; }
+  __host__ __device__ inline int at() const { return hi - left; }  // the block's first key
+  // key i of the block, -1 where there is none
+  __host__ __device__ inline int key(int i) const { return i < left ? hi - left + i : -1; }
+  __host__ __device__ inline void next(int size) { left -= size; }  // (below 0 behind the last, by less than size)
+};
+
 // A workgroup's tiles and LDS, NB blocks of 128 columns wide (R padded), for BQ rows.
 template <int NB, int ROWS, bool LIST>
 struct Latent {
@@ -667,17 +679,17 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     const int nrows = LIST ? min(BQ, a.H - first) : min(BQ, Lq * a.H - n0);
     const int64_t row0 = (int64_t)q_start * a.H + n0;
     const int t0 = n0 / a.H + len - Lq, t1 = (n0 + nrows - 1) / a.H + len - Lq;  // first and last position
-    const int e_lo = k0 * BK, e_hi = min(k1 * BK, LIST ? a.width : t1 + 1);
+    const int e_lo = k0 * BK;
+    KeyBlocks blocks(e_lo, min(k1 * BK, LIST ? a.width : t1 + 1));
 
     // A block's keys.  place: of a thread's entries; found: what the page table (or the starts) say of them.
     int place[C::EACH], found[C::EACH];
-    auto look_up = [&](int block) {
-      const int end = min(e_hi, block + C::BLOCK);
+    auto look_up = [&](const KeyBlocks &blocks) {
 #pragma unroll
       for (int i = 0; i < C::EACH; ++i) {
-        const int e = block + threadIdx.x * C::EACH + i;
+        const int e = blocks.key((int)threadIdx.x * C::EACH + i);
         place[i] = -1;
-        if (e < end) place[i] = LIST ? a.ids[((int64_t)q_start + tok) * a.width + e] : e;
+        if (e >= 0) place[i] = LIST ? a.ids[((int64_t)q_start + tok) * a.width + e] : e;
       }
 #pragma unroll
       for (int i = 0; i < C::EACH; ++i) {
@@ -703,7 +715,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         if (chunk < NB * 16 ? chunk < latent : chunk < pe)
           z[u] = *reinterpret_cast<const uint4 *>(src + u * THREADS * 8 + (chunk < NB * 16 ? 0 : a.R - NB * 128));
       }
-      look_up(e_lo);
+      look_up(blocks);
 #pragma unroll
       for (int u = 0; u < BATCH; ++u)
         if (CHUNKS % THREADS == 0 || c0 + u * THREADS < CHUNKS)
@@ -712,9 +724,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     __syncthreads();
     r.begin(lds0 + TILE, [&](int row) { return (n0 + row) / a.H + len - Lq; });
 
-    for (int block = e_lo; block < e_hi; block += C::BLOCK) {
+    for (; blocks.any(); blocks.next(C::BLOCK)) {
       // the block's keys that exist, in order: their rows (and places) in LDS
-      if (block > e_lo) look_up(block);
+      if (blocks.at() > e_lo) look_up(blocks);
       int row[C::EACH];
 #pragma unroll
       for (int i = 0; i < C::EACH; ++i) {
