@@ -906,12 +906,14 @@ hipError_t launch_latent_t(const LatentArgs &a, hipStream_t st) {
 }
 
 template <int NB, int RB>
-hipError_t launch_latent_l(const LatentArgs &a, hipStream_t st) {
-  return a.ids ? launch_latent_t<NB, RB, true>(a, st) : launch_latent_t<NB, RB, false>(a, st);
+hipError_t launch_latent_l(bool list, const LatentArgs &a, hipStream_t st) {
+  return list ? launch_latent_t<NB, RB, true>(a, st) : launch_latent_t<NB, RB, false>(a, st);
 }
 template <int NB>
-hipError_t launch_latent_r(int rb, const LatentArgs &a, hipStream_t st) {
-  return rb == 1 ? launch_latent_l<NB, 1>(a, st) : rb == 2 ? launch_latent_l<NB, 2>(a, st) : launch_latent_l<NB, 4>(a, st);
+hipError_t launch_latent_r(int rb, bool list, const LatentArgs &a, hipStream_t st) {
+  return rb == 1   ? launch_latent_l<NB, 1>(list, a, st)
+         : rb == 2 ? launch_latent_l<NB, 2>(list, a, st)
+                   : launch_latent_l<NB, 4>(list, a, st);
 }
 
 int64_t cut_bytes(int shares) { return (int64_t)shares * 32; }
@@ -971,7 +973,7 @@ hipError_t launch_latent(const LatentCall &c, const LatentPlan &p, void *workspa
     a.part_o = (float *)((char *)workspace + cut_bytes(p.shares));
     a.part_lse = a.part_o + (int64_t)2 * p.shares * 16 * p.rb * c.R;
   }
-  return c.R <= 256 ? launch_latent_r<2>(p.rb, a, st) : launch_latent_r<4>(p.rb, a, st);
+  return c.R <= 256 ? launch_latent_r<2>(p.rb, c.list, a, st) : launch_latent_r<4>(p.rb, c.list, a, st);
 }
 
 }  // namespace kpool

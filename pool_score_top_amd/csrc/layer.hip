@@ -483,7 +483,7 @@ int kpool_attend_latent(const uint16_t *q, int64_t q_stride, const uint16_t *cac
   if (!rc) rc = check_max_len(fn, max_len);
   if (rc) return rc;
   kpool::LatentCall c{q, cache, q_stride, cache_stride, cache_rows, page_table, k_starts, k_lens,
-                      pages_per_seq, page_size, max_len, cu_q_dev, nullptr, 0, nseq, H, R, P, scale, o, lse};
+                      pages_per_seq, page_size, max_len, cu_q_dev, nullptr, 0, nseq, H, R, P, scale, o, lse, false};
   return run_latent(fn, c, kpool::plan_latent(cu_q_host, nseq, H, max_len), cu_q_host[nseq], workspace,
                     workspace_bytes, stream);
 }
@@ -514,12 +514,11 @@ int kpool_attend_latent_selected(const uint16_t *q, int64_t q_stride, const uint
   if (width < 0 || width > (1 << 30)) return fail(KPOOL_EINVAL, "%s: width must be in [0, 2^30] (got %d)", fn, width);
   const int64_t Tq = cu_q_host[nseq];
   if (Tq > 0 && width > 0 && !token_ids) return fail(KPOOL_EINVAL, "%s: null pointer", fn);
-  // (a list of no entries is the same as no tokens)
+  // (lists of no entries run as the others do, by the plan that their workspace was asked for with)
   kpool::LatentCall c{q, cache, q_stride, cache_stride, cache_rows, page_table, k_starts, k_lens, pages_per_seq,
-                      page_size, width ? 0x7FFFFFFF : 0, cu_q_dev, width ? token_ids : nullptr, width, nseq, H, R, P, scale,
-                      o, lse};
-  return run_latent(fn, c, width ? kpool::plan_latent_list(Tq, H, width) : kpool::plan_latent(cu_q_host, nseq, H, 0), Tq,
-                    workspace, workspace_bytes, stream);
+                      page_size, 0x7FFFFFFF, cu_q_dev, width ? token_ids : nullptr, width, nseq, H, R, P, scale,
+                      o, lse, true};
+  return run_latent(fn, c, kpool::plan_latent_list(Tq, H, width), Tq, workspace, workspace_bytes, stream);
 }
 
 int kpool_layer_norm(const void *x, int64_t x_stride, const float *weight, const float *bias,

@@ -100,7 +100,8 @@ hipError_t launch_expanded_bwd(const AttendCall &c, const ExpandedKeys &x, const
                                void *workspace, uint16_t *dq, uint16_t *dk, uint16_t *dk_pe, uint16_t *dv,
                                hipStream_t st);
 
-// Latent attention over a cache of one row a token (latent.hip).  ids: [Tq, width] lists, or null.
+// Latent attention over a cache of one row a token (latent.hip).  ids: [Tq, width] lists, null where their
+// width is 0; list: whether the rows have lists, of any width.
 struct LatentCall {
   const uint16_t *q, *cache;
   int64_t q_stride, cache_stride, cache_rows;        // strides in elements
@@ -111,6 +112,7 @@ struct LatentCall {
   float scale;
   uint16_t *o;
   float *lse;
+  bool list;
 };
 struct LatentPlan {
   int rb;         // rows of a workgroup, by 16

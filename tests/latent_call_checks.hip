@@ -1,5 +1,6 @@
 // Calls of the latent attention on the CPU, as the kernel and the entry points see them: the keys that a
-// share walks, block by block.  Nothing here launches a kernel.
+// share walks, block by block; the parts that shares leave, within the workspace that the call's plan asks
+// for, whatever the lengths on the device.  Nothing here launches a kernel.
 #include "../pool_score_top_amd/csrc/latent.hip"
 
 #include <cstdio>
@@ -64,6 +65,56 @@ static void walk_shares(const std::vector<int> &lens, int heads, int most) {
   }
 }
 
+// The parts of a call by the shares that the device finds: each in a slot of its own, within the workspace.
+// `units` tiles of rows with kt[u] key tiles.
+static void parts(const LatentPlan &p, int R, const std::vector<int> &kt) {
+  int64_t tiles = 0;
+  for (int k : kt) tiles += k;
+  CHECK((int64_t)kt.size() == p.units && tiles <= p.tiles && p.shares >= 1 && p.shares <= kMostShares);
+  if (kt.empty()) return;
+  const LatentCosts costs((int)tiles, (int)kt.size(), p.shares);
+  CHECK(costs.shares >= 1 && costs.shares <= p.shares);
+  const int BQ = 16 * p.rb;
+  const int64_t most = (int64_t)latent_workspace(p, R);
+  std::vector<char> used(2 * p.shares);
+  int64_t at = 0;
+  size_t u = 0;
+  for (int s = 0; s < costs.shares; ++s) {
+    const int pos = share_start(costs.total, costs.shares, s), hi = share_start(costs.total, costs.shares, s + 1);
+    while (at + kt[u] + costs.fixed <= pos) at += kt[u++] + costs.fixed;
+    int64_t start = at;
+    for (size_t v = u; v < kt.size() && start < hi; start += kt[v++] + costs.fixed) {
+      const int k0 = costs.cut(pos, (int)start, kt[v]), k1 = costs.cut(hi, (int)start, kt[v]);
+      if (k0 >= k1 || k1 - k0 == kt[v]) continue;
+      CHECK(p.shares > 1);  // (one share leaves no parts)
+      const int64_t slot = 2 * s + (k0 == 0);
+      CHECK(slot < 2 * p.shares && !used[slot]);
+      used[slot] = 1;
+      const int64_t part_o = cut_bytes(p.shares), part_lse = part_o + (int64_t)2 * p.shares * BQ * R * 4;
+      CHECK(part_o + (slot + 1) * BQ * R * 4 <= part_lse && part_lse + (slot + 1) * BQ * 4 <= most);
+    }
+  }
+  CHECK(p.shares == 1 || (int64_t)p.shares * (int64_t)sizeof(LatentCut) <= cut_bytes(p.shares));
+}
+
+static void random_call(Rng &r) {
+  const int H = 1 + (int)r.upto(r.upto(1) ? 20 : 150), R = 8 * (1 + (int)r.upto(63));
+  const int nseq = 1 + (int)r.upto(r.upto(2) ? 8 : 400), most = (int)r.upto(r.upto(1) ? 300 : 60000);
+  std::vector<int32_t> cu{0};
+  for (int s = 0; s < nseq; ++s) cu.push_back(cu.back() + (int)(r.upto(9) ? r.upto(3) : r.upto(200)));
+  const LatentPlan whole = plan_latent(cu.data(), nseq, H, most);
+  std::vector<int> kt;
+  for (int s = 0; s < nseq; ++s) {
+    const int units = (int)(((int64_t)(cu[s + 1] - cu[s]) * H + 16 * whole.rb - 1) / (16 * whole.rb));
+    kt.insert(kt.end(), units, std::max(1, (int)(((r.upto(1) ? r.upto(most) : most) + 63) / 64)));
+  }
+  parts(whole, R, kt);
+  const int width = (int)(r.upto(2) ? r.upto(3000) : r.upto(2));  // (0 among them)
+  const LatentPlan lists = plan_latent_list(cu.back(), H, width);
+  const int64_t units = (int64_t)cu.back() * ((H + 16 * lists.rb - 1) / (16 * lists.rb));
+  parts(lists, R, std::vector<int>(units, std::max(1, (width + 63) / 64)));
+}
+
 int main(int argc, char **argv) {
   const int n = argc > 1 ? std::atoi(argv[1]) : 1000;
   Rng r{std::mt19937_64(7)};
@@ -79,6 +130,7 @@ int main(int argc, char **argv) {
   for (g_case = 0; g_case < n; ++g_case) {
     const int64_t lo = r.upto(kLongest / 64) * 64;
     walk((int)lo, (int)std::min<int64_t>(kLongest, lo + r.upto(300000)), r.upto(1) ? 1024 : 2048);
+    random_call(r);
     if (g_case % 100) continue;
     std::vector<int> lens;
     const int64_t most = r.upto(2) ? kLongest - r.upto(5000) : 1 + r.upto(1000000);

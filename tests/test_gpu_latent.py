@@ -113,6 +113,24 @@ def test_selected_rows_without_tokens():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("q_lens,H,R,P", [([5, 0, 1, 1, 1], 16, 64, 8), ([5] + [1] * 8, 8, 64, 8), ([33] + [1] * 600, 1, 64, 8),
+                                          ([1024], 16, 512, 64), ([2] * 300, 40, 256, 0)])
+def test_lists_without_entries(q_lens, H, R, P):
+    """Widths of 0 over many rows and sequences: o = 0 and lse = -inf in the workspace that the query names."""
+    q, cache, where, _ = make(q_lens, [7] * len(q_lens), H, R, P, 16, 25)
+    cu, dev = cu_of(q_lens)
+    T = sum(q_lens)
+    ids = torch.zeros(T, 0, dtype=torch.int32, device="cuda")
+    nb = K.attend_latent_selected_workspace_bytes(T, 0, H, R, P)
+    ws = torch.full((max(nb, 1) + 64,), 255, dtype=torch.uint8, device="cuda")
+    for workspace in (None, ws[:nb] if nb else None):
+        big, lse = torch.full((T + 2, H, R), 3.0, dtype=BF16, device="cuda"), torch.full((T, H), 3.0, device="cuda")
+        K.attend_latent_selected(q, cache, R, ids, cu, dev, lens_of([7] * len(q_lens)), 0.1, out=big[:T], lse=lse,
+                                 workspace=workspace, **where)
+        assert (big[:T] == 0).all() and (big[T:] == 3.0).all() and (lse == -math.inf).all() and (ws[nb:] == 255).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("width", [None, 500])
 def test_whole_lists_equal_whole_keys_in_64_bits(width):
     """Every token listed in order, beside the whole form: both within the bounds of the same values."""
