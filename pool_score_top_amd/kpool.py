@@ -360,6 +360,13 @@ def _like(t, name, shape, dtype, device):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}")
 
 
+def _int32(**numbers):
+    """Numbers for 32-bit arguments, of which ctypes would pass the low bits alone."""
+    for name, x in numbers.items():
+        if not -2 ** 31 <= x < 2 ** 31:
+            raise ValueError(f"{name} must fit 32 bits (got {x})")
+
+
 def _refuse_graph(fn, *tensors):
     """Results are plain tensors: where autograd would record the call, its gradients would be lost
     without a word."""
@@ -588,6 +595,7 @@ class _Expanded:
 
 
 def _expanded_bytes(fn, cu_q, cu_k, Hq, Hkv, D, P):
+    _int32(Hq=Hq, Hkv=Hkv, D=D, P=P)
     cu_q, qp = _host_i32(cu_q)
     cu_k, kp = _host_i32(cu_k)
     if cu_q.ndim != 1 or cu_k.shape != cu_q.shape:
@@ -733,6 +741,7 @@ def _latent_bytes(fn, *args):
 
 def attend_latent_workspace_bytes(cu_q, max_len: int, H: int, R: int, P: int) -> int:
     """Workspace of attend_latent for these sizes (0 where it needs none)."""
+    _int32(max_len=max_len, H=H, R=R, P=P)
     cu_q, qp = _host_i32(cu_q)
     return _latent_bytes("kpool_attend_latent_workspace_bytes", qp, len(cu_q) - 1, max_len, H, R, P)
 
@@ -749,6 +758,7 @@ def attend_latent(q, cache, rank: int, cu_q, cu_q_dev, k_lens, max_len: int, sca
     anew at each replay.  o is bf16 [Tq, H, R].  Serving only: there is no backward pass, and tensors
     that require gradients are refused where autograd would record the call."""
     _refuse_graph("attend_latent", q, cache)
+    _int32(max_len=max_len)
     a = _Latent(q, cache, rank, cu_q, cu_q_dev, k_lens, scale, page_table, k_starts)
     with _OnDevice(q, stream) as s:
         out, lse = a.outputs(q, out, lse, want_lse)
@@ -764,6 +774,7 @@ def attend_latent(q, cache, rank: int, cu_q, cu_q_dev, k_lens, max_len: int, sca
 
 def attend_latent_selected_workspace_bytes(Tq: int, width: int, H: int, R: int, P: int) -> int:
     """Workspace of attend_latent_selected for these sizes (0 where it needs none)."""
+    _int32(Tq=Tq, width=width, H=H, R=R, P=P)
     return _latent_bytes("kpool_attend_latent_selected_workspace_bytes", Tq, width, H, R, P)
 
 
@@ -895,6 +906,7 @@ def rotary_frequencies(pairs: int, base: float = 10000.0, scale: float = 1.0, tr
 
 def _rotary(fn, x, positions, freqs, begin, interleaved, factor, out, stream, inverse):
     import torch
+    _int32(begin=begin)
     dtype, device = x.dtype, x.device
     shape = x.shape
     if len(shape) == 2:

@@ -52,3 +52,28 @@ def test_calls_take_the_workspace_they_ask_for():
             q_lens[0] = 1
         _takes_what_it_says(q_lens, int(g.integers(1, 140)), 8 * int(g.integers(1, 65)), 8 * int(g.integers(0, 9)),
                             int(g.integers(0, 30000)), int(g.integers(0, 3000)) * int(g.integers(0, 2)))
+
+
+@pytest.mark.parametrize("far", [2 ** 32 + 64, 2 ** 31, -2 ** 31 - 1, 2 ** 40])
+def test_numbers_past_32_bits_are_refused(far):
+    """ctypes passes the low 32 bits of a number: 2^32 + 64 would be 64."""
+    import torch
+    sizes = dict(max_len=640, H=16, R=512, P=64)
+    for name in sizes:
+        with pytest.raises(ValueError, match="32 bits"):
+            K.attend_latent_workspace_bytes([0, 1], **{**sizes, name: far})
+    sizes = dict(Tq=5, width=64, H=16, R=512, P=64)
+    for name in sizes:
+        with pytest.raises(ValueError, match="32 bits"):
+            K.attend_latent_selected_workspace_bytes(**{**sizes, name: far})
+    sizes = dict(Hq=16, Hkv=16, D=128, P=64)
+    for fn in (K.attend_expanded_workspace_bytes, K.attend_expanded_backward_workspace_bytes):
+        for name in sizes:
+            with pytest.raises(ValueError, match="32 bits"):
+                fn([0, 5], [0, 5], **{**sizes, name: far})
+    q, cu = torch.zeros(1, 2, 16), np.array([0, 1], dtype=np.int32)
+    with pytest.raises(ValueError, match="32 bits"):
+        K.attend_latent(q, torch.zeros(4, 16), 8, cu, torch.from_numpy(cu), torch.ones(1), far, 0.1)
+    for fn in (K.rotary, K.rotary_backward):
+        with pytest.raises(ValueError, match="32 bits"):
+            fn(q, torch.zeros(1), torch.zeros(4), begin=far)
