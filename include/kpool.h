@@ -154,6 +154,7 @@ int64_t kpool_chunk_rows(int32_t max_pools, size_t workspace_bytes, uint32_t fla
  *   q        bf16 [T, H, D]    index queries
  *   kp       bf16 [P_tot, D]   pooled keys from kpool_pool_keys
  *   w        fp32 [T, H]       per-row head weights (any sign)
+ *            (of q and w the rows [q_lo, q_hi) are read and no others)
  *   scale    > 0, usually 1/sqrt(D)
  *   budget   pools kept per row, 1..2048 (index_topk / kpool; 2048 for the per-token
  *            indexer, kpool = 1)

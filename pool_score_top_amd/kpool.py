@@ -224,6 +224,13 @@ def score_topk(q, kp, w, cu_seqlens, cu_seqlens_dev, kpool: int, budget: int, q_
 
     overlap=True passes KPOOL_FLAG_OVERLAP (two chunk buffers on two streams); a
     workspace allocated here then holds two chunk buffers, otherwise one."""
+    return _score_topk(q, 0, kp, w, cu_seqlens, cu_seqlens_dev, kpool, budget, q_lo, q_hi, scale, workspace, pool_ids,
+                       scores_out, want_scores, overlap, stream, tail)
+
+
+def _score_topk(q, first, kp, w, cu_seqlens, cu_seqlens_dev, kpool, budget, q_lo, q_hi, scale, workspace, pool_ids,
+                scores_out, want_scores, overlap, stream, tail):
+    """score_topk where q holds the batch's rows from `first` <= q_lo on (the library reads the rows [q_lo, q_hi) alone)."""
     import torch
     _need(q, "q", 2)
     _need(kp, "kp", 2)
@@ -246,7 +253,8 @@ def score_topk(q, kp, w, cu_seqlens, cu_seqlens_dev, kpool: int, budget: int, q_
         if workspace is None:
             nb = workspace_bytes(q_lo, q_hi, max_pools, 2 if overlap else 1)
             workspace = torch.empty(max(nb, 16), dtype=torch.uint8, device=q.device)
-    rc = lib().kpool_score_topk(_p(q), _p(kp), _p(w), cup, _p(cu_seqlens_dev), nseq, H, D, kpool,
+    q_at = q.data_ptr() - first * H * D * q.element_size()  # (where row 0 would be)
+    rc = lib().kpool_score_topk(ctypes.c_void_p(q_at), _p(kp), _p(w), cup, _p(cu_seqlens_dev), nseq, H, D, kpool,
                                 ctypes.c_float(scale), q_lo, q_hi, budget, _p(workspace),
                                 workspace.numel() * workspace.element_size(),
                                 (KPOOL_FLAG_OVERLAP if overlap else 0) | _tail(tail), _p(pool_ids),
@@ -1052,7 +1060,7 @@ class Selector:
         if rotary is not None:
             local = np.arange(self.T, dtype=np.int32) - np.repeat(self.cu[:-1], np.diff(self.cu))
             self.positions = torch.from_numpy(local.astype(np.int32)).to(device)
-            self.q_turned = torch.empty((self.T, H, D), dtype=torch.int16, device=device)
+            self.q_turned = torch.empty((rows, H, D), dtype=torch.int16, device=device)  # (the range's rows)
             self.k_turned = torch.empty((self.T, D), dtype=torch.int16, device=device)
 
     @property
@@ -1087,8 +1095,10 @@ class Selector:
             g = None if g is None else g[:self.T]
             with torch.no_grad():  # (ids have no gradients)
                 k = layer_norm(k[:self.T], weight, bias, eps, out=self.k_normed.view(k.dtype), stream=stream)[0]
+        first = 0
         if self.rotary is not None:
             q, k = self._turn(q, k, stream)
+            first = self.q_lo
             g = None if g is None else g[:self.T]
         if g is not None:
             pool_keys_gated(k, g, ape, self.cu, self.cu_dev, self.cu_pools_dev, self.kpool,
@@ -1096,9 +1106,9 @@ class Selector:
         else:
             pool_keys(k, self.cu, self.cu_dev, self.cu_pools_dev, self.kpool, out=self.kp,
                       stream=stream, tail=self.tail)
-        score_topk(q, self.kp, w, self.cu, self.cu_dev, self.kpool, self.budget, self.q_lo, self.q_hi,
-                   scale=self.scale, workspace=self.workspace, pool_ids=self.pool_ids,
-                   scores_out=scores_out, overlap=overlap, stream=stream, tail=self.tail)
+        _score_topk(q, first, self.kp, w, self.cu, self.cu_dev, self.kpool, self.budget, self.q_lo, self.q_hi,
+                    scale=self.scale, workspace=self.workspace, pool_ids=self.pool_ids, scores_out=scores_out,
+                    want_scores=False, overlap=overlap, stream=stream, tail=self.tail)
         expand(self.pool_ids, self.cu, self.cu_dev, self.kpool, self.budget, self.q_lo, self.q_hi,
                out=self.token_ids, stream=stream, tail=self.tail)
         return {"kp": self.kp, "pool_ids": self.pool_ids, "token_ids": self.token_ids}
@@ -1106,13 +1116,13 @@ class Selector:
     def _turn(self, q, k, stream):
         """Index queries (the rows' own) and keys at their positions, in the selector's buffers."""
         import torch
-        if q.shape != self.q_turned.shape or q.element_size() != 2 or k.dim() != 2 or k.shape[0] < self.T:
+        if q.shape != (self.T, self.H, self.D) or q.element_size() != 2 or k.dim() != 2 or k.shape[0] < self.T:
             raise ValueError(f"need q [{self.T}, {self.H}, {self.D}] and k with {self.T} rows in bfloat16 (or int16)")
         freqs, begin, interleaved, factor = self.rotary
         how = dict(begin=begin, interleaved=interleaved, factor=factor, stream=stream)
         rows = slice(self.q_lo, self.q_hi)
         with torch.no_grad():  # (ids have no gradients)
-            rotary(q[rows], self.positions[rows], freqs, out=self.q_turned[rows].view(q.dtype), **how)
+            rotary(q[rows], self.positions[rows], freqs, out=self.q_turned.view(q.dtype), **how)
             rotary(k[:self.T], self.positions, freqs, out=self.k_turned.view(k.dtype), **how)
         return self.q_turned, self.k_turned
 

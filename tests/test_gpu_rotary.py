@@ -262,3 +262,29 @@ def test_refuses_tensors_of_other_shapes():
                 lambda: K.rotary(x[0, 0], pos, f), lambda: K.rotary(x, pos, f.cpu())):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_selector_of_a_range_holds_the_queries_of_its_rows():
+    cu = np.array([0, 700, 701, 701, 1500], dtype=np.int32)
+    freqs, factor = K.rotary_frequencies(32, device="cpu")
+    for q_lo, q_hi, rows in ((200, 210, 10), (1490, None, 10), (0, None, 1500), (700, 700, 0)):
+        sel = K.Selector(cu, 4, 64, 32, 128, device="cpu", q_lo=q_lo, q_hi=q_hi, rotary=(freqs, 0, False, factor))
+        assert sel.q_turned.shape == (rows, 32, 128) and sel.k_turned.shape == (1500, 128)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("q_lo,q_hi", [(0, 3), (699, 705), (1490, 1500), (1499, 1500), (700, 700)])
+def test_selector_of_few_rows_equals_the_whole(q_lo, q_hi):
+    """Ids of a range of rows against those of all rows; the range's buffers hold no others."""
+    cu = np.array([0, 700, 701, 701, 1500], dtype=np.int32)
+    wl = synth.workload("sq4096", T=1500, kpool=4, budget=64)
+    r = synth.host_inputs(wl, 5)
+    q, k, w = (torch.from_numpy(r[n].view(np.int16) if r[n].dtype == np.uint16 else r[n]).cuda() for n in ("q", "k", "w"))
+    freqs, factor = freqs_of(32, 40.0)
+    make_sel = lambda **kw: K.Selector(cu, 4, 64, 32, 128, rotary=(freqs, 64, True, factor), **kw)
+    whole = make_sel().run(q, k, w)
+    few = make_sel(q_lo=q_lo, q_hi=q_hi)
+    for _ in range(2):
+        out = few.run(q, k, w)
+        assert torch.equal(out["pool_ids"], whole["pool_ids"][q_lo:q_hi])
+        assert torch.equal(out["token_ids"], whole["token_ids"][q_lo:q_hi])
