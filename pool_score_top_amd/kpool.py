@@ -721,7 +721,9 @@ class _Latent:
         if stride[-1] != 1 and width > 1:
             raise ValueError("the values of a row of the cache must be contiguous")
         self.cu_ptr = _host_address(cu)
-        self.keys = (q.data_ptr(), qs, cache.data_ptr() if rows else None, row_stride, rows, _at(page_table), per_seq, page,
+        # (a table of no pages has no address, but is one: nothing is read behind the address given for it)
+        table = k_lens.data_ptr() if page_table is not None and per_seq == 0 else _at(page_table)
+        self.keys = (q.data_ptr(), qs, cache.data_ptr() if rows else None, row_stride, rows, table, per_seq, page,
                      _at(k_starts), k_lens.data_ptr())
         self.cu = (self.cu_ptr, cu_q_dev.data_ptr(), self.nseq, self.H, self.R, self.P, scale)
 

@@ -212,6 +212,24 @@ def test_lengths_are_cut_and_negative_ones_are_none():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("width", [None, 30])
+def test_tables_and_caches_of_nothing(width):
+    """A page table without columns, a cache without pages or rows: no tokens, o = 0 and lse = -inf."""
+    q, cache, where, rows = make([2, 1], [40, 20], 16, 64, 8, 16, 26)
+    cu, dev = cu_of([2, 1])
+    ids = None if width is None else lists([2, 1], [40, 20], width, 27, "wild")
+    none = torch.empty(2, 0, dtype=torch.int32, device="cuda")
+    start = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for c, kw in ((cache, dict(page_table=none)), (cache[:0], dict(page_table=none)), (cache[:0], where),
+                  (cache.flatten(0, 1)[:0], dict(k_starts=start))):
+        if width is None:
+            o, lse = K.attend_latent(q, c, 64, cu, dev, lens_of([40, 20]), 40, 0.1, want_lse=True, **kw)
+        else:
+            o, lse = K.attend_latent_selected(q, c, 64, ids, cu, dev, lens_of([40, 20]), 0.1, want_lse=True, **kw)
+        assert (o == 0).all() and (lse == -math.inf).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("width", [None, 600])
 def test_same_bits_other_stream_workspace_and_outputs(width):
     q_lens, k_lens, R = [1, 2], [9000, 500], 512
