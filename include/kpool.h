@@ -368,7 +368,8 @@ int kpool_attend_expanded_backward(const uint16_t *d_o, const uint16_t *q, int64
  *   cache    bf16, row r at cache + r * cache_stride elements, cache_rows of them
  *   page_table  int32 [nseq, pages_per_seq] device: token j of sequence s is the cache's row
  *            page_table[s, j / page_size] * page_size + j % page_size; or NULL:
- *   k_starts int32 [nseq] device: token j is row k_starts[s] + j (not read with a page table)
+ *   k_starts int32 [nseq] device: token j is row k_starts[s] + j (not read with a page table); a negative
+ *            start stands for no tokens at all
  *   k_lens   int32 [nseq] device: the sequence's tokens, those of its queries among them; its queries
  *            are the LAST of them: with Lq queries, query n sits at position t = k_lens[s] - Lq + n.
  *            Lengths, page table and starts are read when the call runs on the device: a captured

@@ -357,8 +357,10 @@ __device__ inline void write_row(const AttendArgs &a, bool live, int64_t row, bo
 // = 64 192 us, 80 258, 96 263, 128 272).
 // With the positional part of expanded latent attention (PP = 64): its tile of 8 KiB stands behind the
 // values', so that the heads' keys are not written out with it beside each.  8192 tokens, 16 heads of 128 + 64:
-// 344 GFLOP in 347 us, 0.99 PFLOP/s (CUs busy 81% of the time, the pipe 57% of that); 4096, 2001, 511 and 1
-// tokens 137 us, 67% and 49%, as the longest tiles' 64 steps stand against 43 a CU on average.
+// 344 GFLOP in 347 to 366 us by box, 0.94 to 0.99 PFLOP/s (CUs busy 81% of the time, the pipe 57% of that); 4096,
+// 2001, 511 and 1 tokens 143 us, 67% and 49%, as the longest tiles' 64 steps stand against 43 a CU on average.
+// Every P runs as 64, its blocks past P multiplying zeros: 8192 tokens with 64, 32 and 8 of them 362, 354 and
+// 348 us; 96 + 40, as 128 + 64, 345.
 template <int DP, int NW, int PP>
 __global__ __launch_bounds__(NW * 64) void attend_tile_kernel(AttendArgs a) {
   using S = Keys<DP>;

@@ -134,8 +134,9 @@ __device__ inline void load_frag(bf16x8 (&f)[DP / 16], const uint16_t *row, int 
 // PP = 64: with the positional part of expanded latent attention, whose 32 rows lie behind the others in
 // rows as wide as theirs, so that they share their lanes' addresses.  Its products go to both waves, 4 a tile
 // each: the first reads the keys' part from LDS (its registers are full), the second sums the gradient.
-// 4096, 2001, 511 and 1 tokens, 16 heads of 128 + 64, 215 GFLOP: 262 us and 19 to join, 0.8 PFLOP/s; a step
-// takes 2210 cycles, 1280 of them products of the SIMD's two waves, a unit 22 thousand cycles besides its steps.
+// 4096, 2001, 511 and 1 tokens, 16 heads of 128 + 64, 215 GFLOP: 274 us (the median of 40 calls, the least 262) and
+// 19 to join, 0.78 PFLOP/s; a step takes 2210 cycles, 1280 of them products of the SIMD's two waves, a unit 22
+// thousand cycles besides its steps, ten steps' time in which the pipe stands idle.
 template <int DP, int PP = 0>
 struct BwdKeys {
   static constexpr int BR = 32, NG = 4, KEYS = NG * 32;
@@ -543,7 +544,8 @@ __global__ __launch_bounds__(256) void bwd_positional_kernel(BwdArgs a) {
 // the longest tiles to the CUs' average leaves the time as it is.
 // With the positional part (PP = 64) the rows' share of it lies in LDS, each lane's for itself, as the registers
 // are full, and fragments are read four ahead of their products.  4096, 2001, 511 and 1 tokens, 16 heads of
-// 128 + 64: 172 GFLOP in 231 us, 0.75 PFLOP/s; a step of 64 keys takes 6700 cycles, 4100 of them products.
+// 128 + 64: 172 GFLOP in 239 us (the least 231), 0.72 PFLOP/s; a step of 64 keys takes 6700 cycles, 4100 of them
+// products.
 // With one of a SIMD's two waves ahead of the other (s_setprio), or with the rows read through LDS, the same.
 template <int DP, int NW, int PP>
 __global__ __launch_bounds__(NW * 64) void bwd_rows_kernel(BwdArgs a) {
@@ -806,7 +808,7 @@ __global__ __launch_bounds__(256) void bwd_rows_sum_kernel(BwdArgs a, int width)
 // its own keys there are many short units.  (Lengths 4096, 2001, 511 and 1, 16 heads of 128 + 64, forward and
 // backward: 730 us with 4, 677 with 8, 642 with 12, 648 with 16.  Parts of 16 steps where those 12 are counted
 // cut units that are better left whole: 300 and 77 tokens, 8 heads of 64 + 32, 54.3 us, with 24 50.6, which
-// 32 and 48 leave as it is.)
+// 32 and 48 leave as it is.  Each was set by that one batch; others were not measured for them.)
 constexpr int kKeysShare = 16, kRowsShare = 6;
 constexpr int kUnitCost = 4, kExpandedCost = 12, kExpandedShare = 24;
 UnitCost keys_cost(int64_t lk, int64_t lq, int64_t n0, int64_t G, bool expanded = false) {

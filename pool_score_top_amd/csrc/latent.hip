@@ -29,14 +29,17 @@
 //
 // What bounds it, at R + P = 512 + 64 (captured calls, both kernels):
 //   few rows: memory.  16 requests of one token, 205k cached tokens, 16 heads: 62.5 us; the first kernel
-//     takes 44 (236 MB, 5.4 TB/s, as much as a copy moves), the join 7;
+//     takes 44 (236 MB, 5.4 TB/s, as a copy of 268 MB does), the join 7;
 //   many rows: the matrix instructions and what they wait for within a tile, as there is one wave a
 //     SIMD: S 1600 cycles of 4200 (1152 of products), softmax and its exchange 700, O 1530 (1024), the
-//     tile's arrival 310.  8 requests of 2 tokens, 128 heads, 117k tokens: 102 us (93 and 11; 65 GFLOP; CUs busy
+//     tile's arrival 310.  8 requests of 2 tokens, 128 heads, 117k tokens: 106 us (99 and 12; 65 GFLOP; CUs busy
 //     79% of the time, the matrix pipe 36% of that): a unit's start and end take 22k cycles besides, 5 tiles' time;
 //   lists of many rows: the listed rows' way from beyond the L2, which holds 12% of them.  1024 rows of 2048
-//     tokens, 64 heads: 356 us, 2.4 GB at 7 TB/s (CUs busy 94%, the pipe 42% of that);
-//   a token or two: latencies.  One token over 1003, 16 heads: 16.3 us (11 and 4).
+//     tokens, 64 heads: 358 us, 2.4 GB at 7 TB/s (CUs busy 94%, the pipe 42% of that);
+//   a token or two: latencies.  One token over 1003, 16 heads: 17 us (11 and 4);
+//   chunks of a prompt: 512 tokens behind 8192, 16 heads 177 us (0.85 PFLOP/s), 128 heads 1176 us (1.03).  A unit
+//     counts the tiles of its whole sequence, also of keys behind its rows: 2048 tokens of a new prompt, 16
+//     heads, 153 us (0.48), which the expanded form is for.
 #include <type_traits>
 
 #include "attend_tile.h"
@@ -70,7 +73,8 @@ struct LatentCut {
 // for its start and end (rows of queries in, outputs out, no products meanwhile).  With tiles alone a share of
 // many short units took up to twice its time: 8 requests of 2 tokens, 128 heads, us of the first kernel by tiles
 // 118, by cost 93; 16 requests, 16 heads, 49.6 and 43.7 (whole calls: cost 3 62.6 and 103, 4 62.5 and 102, 6 64.1
-// and 101).  Where shares are of fewer tiles, a unit has a share and more to itself either way.
+// and 101; no other batches were measured for it).  Where shares are of fewer tiles, a unit has a share and more
+// to itself either way.
 // A cut that would leave a part of fewer than `least` tiles moves to the unit's start or end.
 constexpr int kUnitCost = 4;
 struct LatentCosts {
@@ -923,7 +927,9 @@ LatentPlan shares_of(LatentPlan p, int64_t units, int64_t keys) {
   p.units = units;
   // (more units than a call may have tiles are refused as they are: their product may not fit 64 bits)
   p.tiles = units < (1 << 28) ? units * std::max<int64_t>(1, (keys + kLatentKeys - 1) / kLatentKeys) : units;
-  // A share for each tile, of 64 rows for two, as their parts cost four tiles' time to begin and to join.
+  // A share for each tile, of 64 rows for two, as their parts cost four tiles' time to begin and to join.  (By
+  // the most tiles that max_len allows: a call whose lengths on the device are shorter has up to a share a tile
+  // of its own.  8 requests of 2 tokens over 500, 128 heads, 31.7 us with max_len 500, 35.2 with 524288.)
   // (us with one, two and four tiles a share: 8 tokens of 2048 selected ones, 64 heads, 35, 32, 34; one token
   // over 1003, 16 heads, 16.3, 18.0, 21.8.)
   const int64_t shares = p.rb == 4 ? (p.tiles + 1) / 2 : p.tiles;
@@ -936,6 +942,8 @@ LatentPlan shares_of(LatentPlan p, int64_t units, int64_t keys) {
 // Units of 16, 32 or 64 rows: as many as share keys and no more.  (us with 16, 32 and 64 rows, 8 requests of
 // one token over 64k cached tokens in all, and 256 rows of 1024 selected tokens: 16 heads 37, 41, - and 51, 54,
 // -; 32 heads 46, 43, 50 and 89, 54, 62; 64 heads -, 51, 55 and -, 95, 67; 128 heads -, 66, 60 and -, 173, 114.)
+// A batch takes the units of its longest sequence throughout: of 16 requests over 205k tokens, 16 heads, 62.5 us,
+// one of 4 tokens instead of one makes it 68 to 69, one of 64 over 300 68.
 LatentPlan plan_latent(const int32_t *cu_q, int nseq, int H, int64_t max_len) {
   int64_t most = 0, units = 0;
   for (int s = 0; s < nseq; ++s) most = std::max<int64_t>(most, (int64_t)(cu_q[s + 1] - cu_q[s]) * H);

@@ -13,10 +13,13 @@
 // those of its rows once and keeps cosine and sine, times factor, in LDS.
 //
 // HBM-bound: 6 flops a rotated value against 2 to 8 bytes.  32768 rows of 32 heads of 128 in bf16, half of each
-// turned: 97.6 us, 5.5 TB/s (a copy of 2 GiB moves 5.0); 8192 rows of 16 heads of 192, 64 of them turned, both
-// ways: 42.8 us, 4.7 TB/s; 8 rows of 32 heads: 8.3 us, which is the host's call (the kernel takes 3.5).  A thread turns vectors of V elements, the
-// widest up to 16 bytes that divides every offset: a vector of each half, or, where pairs are
-// neighbours, one vector of whole pairs.
+// turned: 97.5 us, 5.5 TB/s (a copy of as many bytes 99 us, 5.4; last-level cache holds part of both, a copy of
+// 2 GiB moves 4.8 to 5.0); 16 heads of 128 in fp32 97; 8192 rows of 16 heads of 192, 64 of them turned, both
+// ways: 42.8 us, 4.7 TB/s; 8 rows of 32 heads: 8.3 us, which is the host's call (the kernel takes 3.5).
+// A thread turns vectors of V elements, the widest up to 16 bytes that divides every offset: a vector of
+// each half, or, where pairs are neighbours, one vector of whole pairs.  The copied part goes by the same width, so
+// that what no vector divides is slow throughout.  The first shape with rows a few elements further apart: 8
+// more 104 us, 4 more 123, 2 more 194, 5 more 296; with 9 pairs 327; in fp32 with 5 more 176.
 #include <algorithm>
 
 #include "layer_internal.h"
