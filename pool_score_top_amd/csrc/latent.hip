@@ -29,10 +29,10 @@
 //
 // What bounds it, at R + P = 512 + 64 (captured calls, both kernels):
 //   few rows: memory.  16 requests of one token, 205k cached tokens, 16 heads: 62.5 us; the first kernel
-//     takes 44 (236 MB, 5.4 TB/s, as a copy of 268 MB does), the join 7;
+//     takes 45 (236 MB, 5.3 TB/s, as a copy of 268 MB does), the join 7;
 //   many rows: the matrix instructions and what they wait for within a tile, as there is one wave a
 //     SIMD: S 1600 cycles of 4200 (1152 of products), softmax and its exchange 700, O 1530 (1024), the
-//     tile's arrival 310.  8 requests of 2 tokens, 128 heads, 117k tokens: 106 us (99 and 12; 65 GFLOP; CUs busy
+//     tile's arrival 310.  8 requests of 2 tokens, 128 heads, 117k tokens: 106 us (100 and 11; 65 GFLOP; CUs busy
 //     79% of the time, the matrix pipe 36% of that): a unit's start and end take 22k cycles besides, 5 tiles' time;
 //   lists of many rows: the listed rows' way from beyond the L2, which holds 12% of them.  1024 rows of 2048
 //     tokens, 64 heads: 358 us, 2.4 GB at 7 TB/s (CUs busy 94%, the pipe 42% of that);

@@ -621,9 +621,9 @@ def attend_expanded(q, k, k_pe, v, cu_q, cu_q_dev, cu_k=None, cu_k_dev=None, sca
                     want_lse: bool = False, lse=None, workspace=None, stream=None):
     """Latent attention with expanded keys and values, as attend: (o, lse or None).
 
-    q bf16 [Tq, Hq, D + P]; k and v bf16 [Tk, Hkv, D], a token's heads side by side at any stride (the two halves
-    of one projection's heads, say; keys stored head by head are refused); strides are multiples of 8; k_pe bf16 [Tk, P], the keys' positional part, which all heads share.  scale
-    is 1 / sqrt(D + P) by default; the rest is attend's.  attend_expanded_backward has its gradients; new
+    q bf16 [Tq, Hq, D + P]; k and v bf16 [Tk, Hkv, D], a token's heads side by side (the two halves of one
+    projection's heads, say; keys stored head by head are refused); k_pe bf16 [Tk, P], the keys' positional
+    part, which all heads share; strides are multiples of 8.  scale is 1 / sqrt(D + P) by default; the rest is attend's.  attend_expanded_backward has its gradients; new
     tokens over a cache take attend_latent."""
     import torch
     _refuse_graph("attend_expanded", q, k, k_pe, v)
@@ -763,11 +763,12 @@ def attend_latent(q, cache, rank: int, cu_q, cu_q_dev, k_lens, max_len: int, sca
 
     q bf16 [Tq, H, R + P] (any token stride), R being rank; the cache holds one row of R + P values a
     token, which is every head's key and whose first R are the value: [pages, page_size, R + P] with
-    page_table int32 [nseq, pages], the pages of the cache one behind another (a slice of interleaved ones is
-    refused), or [rows, R + P] with k_starts int32 [nseq], the sequences' first rows.  k_lens int32 [nseq], on the device: each sequence's tokens, of which its queries (cu_q,
-    host and device) are the last, at most max_len.  A captured call reads lengths, pages and starts
-    anew at each replay.  o is bf16 [Tq, H, R].  Serving only: there is no backward pass, and tensors
-    that require gradients are refused where autograd would record the call."""
+    page_table int32 [nseq, pages], the cache's pages one behind another (a slice of interleaved ones is
+    refused), or [rows, R + P] with k_starts int32 [nseq], the sequences' first rows.  k_lens int32
+    [nseq], on the device: each sequence's tokens, of which its queries (cu_q, host and device) are the
+    last, at most max_len.  A captured call reads lengths, pages and starts anew at each replay.  o is
+    bf16 [Tq, H, R].  Serving only: there is no backward pass, and tensors that require gradients are
+    refused where autograd would record the call."""
     _refuse_graph("attend_latent", q, cache)
     _int32(max_len=max_len)
     a = _Latent(q, cache, rank, cu_q, cu_q_dev, k_lens, scale, page_table, k_starts)

@@ -288,3 +288,18 @@ def test_selector_of_few_rows_equals_the_whole(q_lo, q_hi):
         out = few.run(q, k, w)
         assert torch.equal(out["pool_ids"], whole["pool_ids"][q_lo:q_hi])
         assert torch.equal(out["token_ids"], whole["token_ids"][q_lo:q_hi])
+
+
+@pytest.mark.gpu
+def test_queries_and_weights_outside_the_range_are_not_read():
+    cu = np.array([0, 700, 701, 701, 1500], dtype=np.int32)
+    r = synth.host_inputs(synth.workload("sq4096", T=1500, kpool=4, budget=64), 6)
+    q, k, w = (torch.from_numpy(r[n].view(np.int16) if r[n].dtype == np.uint16 else r[n]).cuda() for n in ("q", "k", "w"))
+    whole = K.Selector(cu, 4, 64, 32, 128).run(q, k, w)["token_ids"]
+    for lo, hi in ((0, 3), (690, 705), (1499, 1500)):
+        outside = torch.ones(1500, dtype=torch.bool, device="cuda")
+        outside[lo:hi] = False
+        q2, w2 = q.clone(), w.clone()
+        q2.view(BF16)[outside], w2[outside] = float("nan"), float("nan")
+        out = K.Selector(cu, 4, 64, 32, 128, q_lo=lo, q_hi=hi).run(q2, k, w2)
+        assert torch.equal(out["token_ids"], whole[lo:hi])
